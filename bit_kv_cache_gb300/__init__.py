@@ -30,7 +30,8 @@ EXPORTS = ("kvq_status_str", "kvq_config_check", "kvq_buffer_bytes", "kvq_quant_
            "kvq_paged_bytes", "kvq_paged_init",
            "kvq_paged_prefill", "kvq_paged_append", "kvq_paged_flush_plan", "kvq_paged_flush",
            "kvq_paged_release", "kvq_paged_workspace_bytes", "kvq_paged_decode_attn",
-           "kvq_paged_read_status")
+           "kvq_paged_read_status", "kvq_paged_plan", "kvq_paged_chunk_workspace_bytes",
+           "kvq_paged_chunk_attn", "kvq_paged_extend", "kvq_qk_norm_rope")
 PAGED_MAX_B = 512
 
 
@@ -64,13 +65,26 @@ class Paged(ctypes.Structure):
                                                "lens_host", "status")]
 
 
+class ChunkDesc(ctypes.Structure):
+    """kvq_chunk"""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("cu", "slot", "pos", "desc", "host")] + \
+               [(n, ctypes.c_int64) for n in ("max_tokens", "n_tokens")]
+
+
+class QkConfig(ctypes.Structure):
+    """kvq_qk_config"""
+    _fields_ = [(n, ctypes.c_int32) for n in ("H_q", "H_kv", "D", "rotary_dim", "halves", "rotate")] + \
+               [(n, ctypes.c_float) for n in ("eps", "rope_base")] + \
+               [(n, ctypes.c_int64) for n in ("q_stride", "k_stride")]
+
+
 def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     if not os.path.exists(path):
         raise ImportError("libkvq.so not built (%s); run: python bit_kv_cache_gb300/build.py" % path)
     L = ctypes.CDLL(path)
     P, I, I64, Sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t
     CP, KP, PP = ctypes.POINTER(Config), ctypes.POINTER(Cache), ctypes.POINTER(Paged)
-    IP = ctypes.POINTER(I)
+    IP, HP = ctypes.POINTER(I), ctypes.POINTER(ChunkDesc)
     sig = {
         "kvq_status_str": ([I], ctypes.c_char_p),
         "kvq_config_check": ([CP], I),
@@ -99,6 +113,11 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "kvq_paged_workspace_bytes": ([CP], Sz),
         "kvq_paged_decode_attn": ([CP, PP, P, P, P, Sz, P], I),
         "kvq_paged_read_status": ([PP, P, ctypes.POINTER(ctypes.c_int32), P], I),
+        "kvq_paged_plan": ([CP, PP, P, P, I64, HP, P], I),
+        "kvq_paged_chunk_workspace_bytes": ([CP], Sz),
+        "kvq_paged_chunk_attn": ([CP, PP, HP, P, I64, P, I64, P, I64, P, P, Sz, P], I),
+        "kvq_paged_extend": ([CP, PP, HP, P, I64, P, I64, P], I),
+        "kvq_qk_norm_rope": ([ctypes.POINTER(QkConfig), P, P, P, P, P, I64, P, P, P], I),
     }
     for name, (args, res) in sig.items():
         f = getattr(L, name)
@@ -128,6 +147,94 @@ def make_config(B, H_q, H_kv, D, G, bits, S=0, R=None, n_boost=0, mode="kivi", m
     m = {"kivi": KVQ_MODE_KIVI, "kitty": KVQ_MODE_KITTY, "nvfp4": KVQ_MODE_NVFP4}[mode]
     return Config(B, H_q, H_kv, D, G, bits, S, G if R is None else R, n_boost, m, v_bits or 0, max_T,
                   1 if rope_base else 0, float(rope_base or 0.0))
+
+
+def _stream_of(device):
+    """The current stream of a device, which must be the current device."""
+    import torch
+    if torch.cuda.current_device() != device.index:
+        raise ValueError("the tensors are on %s, which is not the current device" % device)
+    return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+
+
+def _rows(t, heads, D, n, device, what):
+    """(pointer, row stride) of token-major rows [>= n][heads][D], float16, heads adjacent."""
+    import torch
+    if t.device != device or t.dtype != torch.float16:
+        raise ValueError("%s must be a float16 tensor on %s" % (what, device))
+    if t.dim() != 3 or t.shape[0] < n or t.shape[1] != heads or t.shape[2] != D:
+        raise ValueError("%s has shape %s, expected at least [%d, %d, %d]" % (what, tuple(t.shape), n, heads, D))
+    if (D > 1 and t.stride(2) != 1) or (heads > 1 and t.stride(1) != D):
+        raise ValueError("%s must hold each token's heads contiguously" % what)
+    return ctypes.c_void_p(t.data_ptr()), (t.stride(0) if t.shape[0] > 1 else heads * D)
+
+
+def qk_norm_rope(q, k=None, w_q=None, w_k=None, pos=None, eps=1e-6, rope_base=10000.0, rotary_dim=None,
+                 halves=False, rotate_q=True, rotate_k=True, out=None):
+    """RMS norm of every query and key head and the rotary position embedding in one pass
+    (kvq_qk_norm_rope).
+
+    q: float16 [n, H_q, D]; k: float16 [n, H_kv, D] or None; rows may be strided (views of a
+    fused projection).  w_q, w_k: float16 [D], or None for no norm.  pos: int32 [n] on the
+    device.  rotary_dim: the first channels, which rotate (all of them by default); halves:
+    pairs (j, j + rotary_dim/2) instead of (2j, 2j+1).  rotate_q, rotate_k: a cache that
+    stores keys before RoPE takes rotate_k=False.  out: (q_out, k_out), contiguous; an
+    output may be its own contiguous input.  Returns (q_out, k_out)."""
+    import torch
+    n, H_q, D = q.shape
+    dev = q.device
+    H_kv = 0 if k is None else k.shape[1]
+    qp, qs = _rows(q, H_q, D, n, dev, "q")
+    kp, ks = (None, 0) if k is None else _rows(k, H_kv, D, n, dev, "k")
+    if k is not None and k.shape[0] != n:
+        raise ValueError("q and k have %d and %d rows" % (n, k.shape[0]))
+    if pos is None or pos.device != dev or pos.dtype != torch.int32 or pos.shape != (n,) or not pos.is_contiguous():
+        raise ValueError("pos must be a contiguous int32 tensor [%d] on %s" % (n, dev))
+    for w, what in ((w_q, "w_q"), (w_k, "w_k")):
+        if w is not None and (w.device != dev or w.dtype != torch.float16 or w.shape != (D,) or not w.is_contiguous()):
+            raise ValueError("%s must be a contiguous float16 tensor [%d] on %s" % (what, D, dev))
+    if out is None:
+        out = (torch.empty((n, H_q, D), dtype=torch.float16, device=dev),
+               None if k is None else torch.empty((n, H_kv, D), dtype=torch.float16, device=dev))
+    q_out, k_out = out
+    for y, H, what in ((q_out, H_q, "q_out"), (k_out, H_kv, "k_out")):
+        if (y is None) != (what == "k_out" and k is None):
+            raise ValueError("%s is %s" % (what, "missing" if y is None else "given without k"))
+        if y is not None and (y.device != dev or y.dtype != torch.float16 or y.shape != (n, H, D) or not y.is_contiguous()):
+            raise ValueError("%s must be a contiguous float16 tensor [%d, %d, %d] on %s" % (what, n, H, D, dev))
+    c = QkConfig(H_q, H_kv, D, D if rotary_dim is None else rotary_dim, int(bool(halves)),
+                 int(bool(rotate_q)) + 2 * int(bool(rotate_k)), eps, rope_base, qs, ks)
+    ptr = lambda t: None if t is None else ctypes.c_void_p(t.data_ptr())  # noqa: E731
+    _check(lib.kvq_qk_norm_rope(ctypes.byref(c), qp, kp, ptr(w_q), ptr(w_k), ptr(pos), n, ptr(q_out), ptr(k_out),
+                                _stream_of(dev)), "kvq_qk_norm_rope")
+    return q_out, k_out
+
+
+class KVQChunk:
+    """The buffers of a plan (kvq_chunk) and of the attention that reads it: slot maps
+    ``cu`` [B + 1], ``slot`` and ``pos`` [max_tokens] (int32, on the device).  Made by
+    KVQPagedCache.new_chunk.  Every cache of the same configuration and lengths may use it;
+    two attention calls that may overlap need a chunk each."""
+
+    def __init__(self, cfg, max_tokens, device):
+        import torch
+        i32 = dict(dtype=torch.int32, device=device)
+        self.cu = torch.zeros(cfg.B + 1, **i32)
+        self.slot = torch.zeros(max_tokens, **i32)
+        self.pos = torch.zeros(max_tokens, **i32)
+        self.desc = torch.zeros((cfg.B, 8), **i32)
+        self.host = (ctypes.c_int32 * (8 * cfg.B))()
+        self.ws = torch.empty(lib.kvq_paged_chunk_workspace_bytes(ctypes.byref(cfg)), dtype=torch.uint8, device=device)
+        self.B = cfg.B
+        pad = torch.zeros(4, **i32) if max_tokens == 0 else None  # an empty tensor has no address
+        self._pad = pad
+        self.c = ChunkDesc(self.cu.data_ptr(), (self.slot if pad is None else pad).data_ptr(),
+                           (self.pos if pad is None else pad).data_ptr(), self.desc.data_ptr(),
+                           ctypes.cast(self.host, ctypes.c_void_p), max_tokens, 0)
+
+    @property
+    def n_tokens(self) -> int:
+        return self.c.n_tokens
 
 
 class KVQCache:
@@ -365,6 +472,7 @@ class KVQPagedCache:
         self.p.lens_host = ctypes.cast(self.lens_host, ctypes.c_void_p)
         self.p.status = self.status.data_ptr()
         self.ws = torch.zeros(lib.kvq_paged_workspace_bytes(cp), dtype=torch.uint8, device=self.device)
+        self.caller_pages = False                     # plan() was given pages of the caller's
         self.free = list(range(n_pages - 1, -1, -1))  # pop() hands out the lowest id first
         self.pages = [[] for _ in range(B)]           # physical pages of each slot, logical order
         _check(lib.kvq_paged_init(cp, ctypes.byref(self.p), KVQCache._stream()), "paged init")
@@ -378,6 +486,8 @@ class KVQPagedCache:
 
     def _map(self, b, n):
         """Maps the next n logical pages of slot b to free physical pages."""
+        if self.caller_pages:
+            raise KvqError(-1, "the caller maps this cache's pages")
         if len(self.free) < n:
             raise KvqError(-3, "page pool exhausted")
         j0 = len(self.pages[b])
@@ -395,7 +505,7 @@ class KVQPagedCache:
         if self.lens_host[4 * b + 3]:
             raise KvqError(-1, "prefill of an occupied slot")
         ns = min(cfg.S, L0)
-        self._map(b, (L0 - ns) // cfg.G)
+        self._map(b, max(0, (L0 - ns) // cfg.G - len(self.pages[b])))
         _check(lib.kvq_paged_prefill(ctypes.byref(self.cfg), ctypes.byref(self.p), b, ctypes.c_void_p(k.data_ptr()),
                                      ctypes.c_void_p(v.data_ptr()), L0, KVQCache._stream()), "paged prefill")
 
@@ -415,7 +525,7 @@ class KVQPagedCache:
                "flush plan")
         out = list(seqs[: n.value])
         for b in out:
-            self._map(b, cfg.R // cfg.G)
+            self._map(b, max(0, (self.lens_host[4 * b + 1] + cfg.R) // cfg.G - len(self.pages[b])))
         nf = ctypes.c_int(0)
         _check(lib.kvq_paged_flush(ctypes.byref(self.cfg), ctypes.byref(self.p), ctypes.byref(nf),
                                    KVQCache._stream()), "paged flush")
@@ -426,6 +536,122 @@ class KVQPagedCache:
         self.pages[b] = []
         _check(lib.kvq_paged_release(ctypes.byref(self.cfg), ctypes.byref(self.p), b, KVQCache._stream()),
                "paged release")
+
+    def clear(self, unmap=True):
+        """Empties every slot.  unmap=False: the pages stay mapped to their slots, which
+        refill them."""
+        _check(lib.kvq_paged_init(ctypes.byref(self.cfg), ctypes.byref(self.p), _stream_of(self.table.device)),
+               "paged init")
+        if unmap:
+            for b in range(self.cfg.B - 1, -1, -1):
+                self.free.extend(reversed(self.pages[b]))
+                self.pages[b] = []
+
+    # -- chunks of new tokens ------------------------------------------------- #
+    def new_chunk(self, max_tokens) -> KVQChunk:
+        """Buffers for plans of up to max_tokens new tokens."""
+        return KVQChunk(self.cfg, max_tokens, self.table.device)
+
+    def plan(self, n_new, chunk=None, pages=None) -> KVQChunk:
+        """Plans n_new[b] new tokens for every slot (kvq_paged_plan): slot maps, positions,
+        and the page-table rows of the pages that extend() will pack.  n_new: B integers, or
+        an int32 CPU tensor.  pages: int32 device tensor of physical pages that the caller
+        hands out, in the order slots need them; by default they come from the cache's own
+        free list."""
+        torch, cfg = self.torch, self.cfg
+        if isinstance(n_new, torch.Tensor):
+            if n_new.device.type != "cpu" or n_new.dtype != torch.int32 or n_new.shape != (cfg.B,) or not n_new.is_contiguous():
+                raise ValueError("n_new must be a contiguous int32 CPU tensor [%d]" % cfg.B)
+            np_ = ctypes.c_void_p(n_new.data_ptr())
+        else:
+            n_new = [int(x) for x in n_new]
+            if len(n_new) != cfg.B or any(not 0 <= x < 1 << 31 for x in n_new):
+                raise ValueError("n_new must hold %d counts" % cfg.B)
+            np_ = (ctypes.c_int32 * cfg.B)(*n_new)
+        if chunk is None:
+            chunk = self.new_chunk(int(sum(n_new)))
+        if chunk.B != cfg.B or chunk.cu.device != self.table.device:
+            raise ValueError("the chunk belongs to another configuration")
+        if pages is None:
+            pages = self._plan_pages(n_new.tolist() if isinstance(n_new, torch.Tensor) else n_new)
+        elif pages.device != self.table.device or pages.dtype != torch.int32 or pages.dim() != 1 or not pages.is_contiguous():
+            raise ValueError("pages must be a contiguous int32 tensor on %s" % self.table.device)
+        else:
+            self.caller_pages = True
+        _check(lib.kvq_paged_plan(ctypes.byref(cfg), ctypes.byref(self.p), np_,
+                                  None if pages is None else ctypes.c_void_p(pages.data_ptr()),
+                                  0 if pages is None else pages.numel(), ctypes.byref(chunk.c),
+                                  _stream_of(self.table.device)), "kvq_paged_plan")
+        return chunk
+
+    def _plan_pages(self, n_new):
+        """Physical pages of a plan, from the free list: logical pages [T/G, ...) of each
+        slot that packs, as a device tensor (None: no slot packs)."""
+        cfg = self.cfg
+        todo = []
+        for b, n in enumerate(n_new):
+            ns, T, nr, on = self.lens_host[4 * b: 4 * b + 4]
+            if n <= 0:
+                continue
+            if not on:
+                ns = T = nr = 0
+            pk = (nr + n - min(n, cfg.S - ns)) // cfg.R * cfg.R
+            if pk and T + pk <= cfg.max_T:  # a longer one is refused by the library
+                todo.append((b, T // cfg.G, (T + pk) // cfg.G))
+        if not todo:
+            return None
+        if self.caller_pages:
+            raise KvqError(-1, "the caller maps this cache's pages")
+        if sum(max(0, hi - len(self.pages[b])) for b, lo, hi in todo) > len(self.free):
+            raise KvqError(-3, "page pool exhausted")
+        ids = []
+        for b, lo, hi in todo:
+            while len(self.pages[b]) < hi:
+                self.pages[b].append(self.free.pop())
+            ids += self.pages[b][lo:hi]
+        t = self.torch.tensor(ids, dtype=self.torch.int32).pin_memory()
+        return t.to(self.table.device, non_blocking=True)
+
+    def chunk_attn(self, chunk, q, k_new, v_new, out=None):
+        """Attention of the planned chunk's tokens over the cached tokens and, causally, the
+        chunk (kvq_paged_chunk_attn).  q: float16 [n, H_q, D], k_new, v_new: float16
+        [n, H_kv, D], n >= chunk.n_tokens, token-major rows that may be strided; rows behind
+        chunk.n_tokens are left alone.  The cache is not changed."""
+        torch, cfg, dev, n = self.torch, self.cfg, self.table.device, chunk.n_tokens
+        qp, qs = _rows(q, cfg.H_q, cfg.D, n, dev, "q")
+        kp, ks = _rows(k_new, cfg.H_kv, cfg.D, n, dev, "k_new")
+        vp, vs = _rows(v_new, cfg.H_kv, cfg.D, n, dev, "v_new")
+        if out is None:
+            out = (torch.empty if q.shape[0] == n else torch.zeros)(q.shape, dtype=torch.float16, device=dev)
+        op, os_ = _rows(out, cfg.H_q, cfg.D, n, dev, "out")
+        if os_ != cfg.H_q * cfg.D:
+            raise ValueError("out must be contiguous")
+        _check(lib.kvq_paged_chunk_attn(ctypes.byref(cfg), ctypes.byref(self.p), ctypes.byref(chunk.c), qp, qs, kp, ks,
+                                        vp, vs, op, ctypes.c_void_p(chunk.ws.data_ptr()), chunk.ws.numel(),
+                                        _stream_of(dev)), "kvq_paged_chunk_attn")
+        return out
+
+    def extend(self, chunk, k_new, v_new):
+        """The planned chunk's tokens enter the cache (kvq_paged_extend)."""
+        cfg, dev = self.cfg, self.table.device
+        kp, ks = _rows(k_new, cfg.H_kv, cfg.D, chunk.n_tokens, dev, "k_new")
+        vp, vs = _rows(v_new, cfg.H_kv, cfg.D, chunk.n_tokens, dev, "v_new")
+        _check(lib.kvq_paged_extend(ctypes.byref(cfg), ctypes.byref(self.p), ctypes.byref(chunk.c), kp, ks, vp, vs,
+                                    _stream_of(dev)), "kvq_paged_extend")
+
+    def chunk_step(self, n_new, q, k, v, w_q=None, w_k=None, eps=1e-6, rope_base=10000.0, rotary_dim=None,
+                   halves=False, chunk=None, out=None):
+        """One step of n_new[b] new tokens per slot: plan, norm and rotation of q and k at
+        their positions, attention, and the tokens' entry into the cache.  q: float16
+        [n, H_q, D], k, v: float16 [n, H_kv, D], n = sum(n_new).  Returns (out, chunk)."""
+        chunk = self.plan(n_new, chunk)
+        n = chunk.n_tokens
+        if n == 0:
+            return q.new_empty(q.shape) if out is None else out, chunk
+        q, k = qk_norm_rope(q[:n], k[:n], w_q, w_k, chunk.pos[:n], eps, rope_base, rotary_dim, halves)
+        out = self.chunk_attn(chunk, q, k, v, out)
+        self.extend(chunk, k, v)
+        return out, chunk
 
     def decode_attn(self, q, out=None):
         cfg = self.cfg

@@ -1,0 +1,798 @@
+// kvq_chunk.cu -- chunks of new tokens over the paged cache: the C ABI of
+// kvq_paged_plan, kvq_paged_chunk_attn, kvq_paged_extend and kvq_qk_norm_rope, and the
+// kernels of all but the attention (kvq_chunk_attn.cu).
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+#include <string.h>
+
+#include <algorithm>
+#include <cmath>
+#include <type_traits>
+
+#include "kvq.h"
+#include "kvq_chunk.h"
+#include "kvq_host.h"
+#include "kvq_quantizer.cuh"
+
+using namespace kvq;
+using namespace kvq::host;
+
+namespace kvq {
+
+// ------------------------------------------------------------------------------
+// Plan.  Every CTA scans the slots (one thread each: rows and pages before the slot) and
+// writes its share of the rows and page-table entries; CTA 0 also the per-slot arrays.
+// ------------------------------------------------------------------------------
+constexpr int kPlanThreads = 512;
+static_assert(kPlanThreads >= KVQ_PAGED_MAX_B, "one thread per slot");
+
+// The slot holding index i: the first one whose end (exclusive prefix of the next) is above i.
+__device__ __forceinline__ int find_slot(const int *start, int B, int i) {
+    int lo = 0, hi = B - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (start[mid + 1] > i) hi = mid;
+        else lo = mid + 1;
+    }
+    return lo;
+}
+
+__global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constant__ PlanParams p) {
+    __shared__ int s_row[kPlanThreads + 1], s_page[kPlanThreads + 1], s_pos[kPlanThreads], s_lp[kPlanThreads];
+    __shared__ int2 s_warp[kPlanThreads / 32];
+    const int b = threadIdx.x, lane = b & 31, w = b >> 5;
+    int4 ln = make_int4(0, 0, 0, 0);
+    int n = 0, to_sink = 0, pk = 0;
+    if (b < p.B) {
+        ln = reinterpret_cast<const int4 *>(p.lens)[b];
+        if (!ln.w) ln = make_int4(0, 0, 0, 0);
+        n = p.n_new[b];
+        to_sink = min(n, p.S - ln.x);
+        pk = n ? (ln.z + n - to_sink) / p.R * p.R : 0;
+    }
+    // inclusive scans of (rows, pages) over the warp, then over the warps
+    int r = n, g = pk / p.G;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int a = __shfl_up_sync(0xffffffffu, r, o), c = __shfl_up_sync(0xffffffffu, g, o);
+        if (lane >= o) {
+            r += a;
+            g += c;
+        }
+    }
+    if (lane == 31) s_warp[w] = make_int2(r, g);
+    __syncthreads();
+    for (int i = 0; i < w; i++) {
+        r += s_warp[i].x;
+        g += s_warp[i].y;
+    }
+    s_row[b + 1] = r;
+    s_page[b + 1] = g;
+    s_pos[b] = ln.x + ln.y + ln.z;
+    s_lp[b] = ln.y / p.G;
+    if (b == 0) s_row[0] = s_page[0] = 0;
+    __syncthreads();
+    if (blockIdx.x == 0 && b < p.B) {
+        p.cu[b] = r - n;
+        if (b == p.B - 1) p.cu[p.B] = r;
+        int4 *d = reinterpret_cast<int4 *>(p.desc) + 2 * b;
+        d[0] = make_int4(ln.x, ln.y, ln.z, n);
+        d[1] = make_int4(r - n, to_sink, pk, s_page[b]);
+    }
+    const int stride = gridDim.x * kPlanThreads, t0 = blockIdx.x * kPlanThreads + threadIdx.x;
+    // four rows per thread; a group of four that stays in one slot (most do) costs one search
+    for (int64_t i = 4 * (int64_t)t0; i < p.n_tokens; i += 4 * (int64_t)stride) {
+        int sl = find_slot(s_row, p.B, (int)i);
+        int s4[4], q4[4];
+#pragma unroll
+        for (int k = 0; k < 4; k++) {
+            const int x = (int)i + k;
+            while (sl < p.B - 1 && s_row[sl + 1] <= x) sl++;
+            s4[k] = sl;
+            q4[k] = s_pos[sl] + x - s_row[sl];
+        }
+        if (i + 4 <= p.n_tokens) {
+            *reinterpret_cast<int4 *>(p.slot + i) = make_int4(s4[0], s4[1], s4[2], s4[3]);
+            *reinterpret_cast<int4 *>(p.pos + i) = make_int4(q4[0], q4[1], q4[2], q4[3]);
+        } else {
+#pragma unroll
+            for (int k = 0; k < 4; k++)
+                if (i + k < p.n_tokens) {
+                    p.slot[i + k] = s4[k];
+                    p.pos[i + k] = q4[k];
+                }
+        }
+    }
+    if (!p.new_pages) return;
+    const int pages = s_page[p.B];
+    for (int i = t0; i < pages; i += stride) {
+        const int sl = find_slot(s_page, p.B, i);
+        p.table[(size_t)sl * p.table_stride + s_lp[sl] + i - s_page[sl]] = p.new_pages[i];
+    }
+}
+
+cudaError_t launch_plan(const PlanParams &p, cudaStream_t st) {
+    const int64_t per = 4 * kPlanThreads;
+    const int grid = (int)std::max<int64_t>(1, std::min<int64_t>(64, (p.n_tokens + per - 1) / per));
+    plan_kernel<<<grid, kPlanThreads, 0, st>>>(p);
+    return cudaGetLastError();
+}
+
+// ------------------------------------------------------------------------------
+// Extend.  The tokens that a slot packs are the stream [residual | chunk behind the sink];
+// page j of the call holds its tokens j G .. j G + G - 1.  One CTA per (page, head, keys or
+// 128 value tokens) gathers its rows from the two places and quantizes them as the prefill
+// kernels do (kvq_quantizer.cuh), so codes and scales are theirs bit for bit.
+// ------------------------------------------------------------------------------
+struct PageJob {
+    ChunkSlot s;
+    int b;
+    int64_t page;          // physical page
+    int t0;                // first stream token
+};
+
+// The slot of page i of the call: the number of slots whose pages all come before it.
+__device__ __forceinline__ PageJob find_page(const ExtendParams &p, int i) {
+    const int4 *d = reinterpret_cast<const int4 *>(p.desc);
+    int b = 0;
+    for (int k = 0; k < p.B; k += blockDim.x) {
+        const int c = k + threadIdx.x;
+        bool before = false;
+        if (c < p.B) {
+            const int4 x = d[2 * c + 1];
+            before = x.w + x.z / p.G <= i;
+        }
+        b += __syncthreads_count(before);
+    }
+    b = min(b, p.B - 1);
+    const int4 x = d[2 * b], y = d[2 * b + 1];
+    PageJob j;
+    j.s = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+    j.b = b;
+    const int k = i - y.w;
+    j.t0 = k * p.G;
+    j.page = p.ptab[(size_t)b * p.ptab_stride + x.y / p.G + k];
+    if (j.page < 0 || j.page >= p.n_pages) {
+        if (threadIdx.x == 0) report(p.status, KVQ_DEV_BAD_STATE);
+        j.page = 0;
+    }
+    return j;
+}
+
+__device__ __forceinline__ const uint16_t *stream_row(const ExtendParams &p, const PageJob &j, const uint16_t *res,
+                                                      const uint16_t *src, int64_t stride, int h, int t) {
+    return t < j.s.nr ? res + (((size_t)j.b * p.H_kv + h) * p.R + t) * 128
+                      : src + (int64_t)(j.s.cu + j.s.to_sink + t - j.s.nr) * stride + h * 128;
+}
+
+// Keys of one page: TPW tokens per warp, lane l holds channels 4 l .. 4 l + 3 of them.
+template <int BITS, int TPW>
+__device__ __forceinline__ void extend_keys(const ExtendParams &p, const PageJob &jb, int h, unsigned char *smem) {
+    constexpr int D = 128, FPI = 32 / BITS, NWR = TPW / FPI, MAXI = (1 << BITS) - 1;
+    uint16_t(*s_lo)[D] = reinterpret_cast<uint16_t(*)[D]>(smem);
+    uint16_t(*s_hi)[D] = s_lo + 8;
+    float *s_mn = reinterpret_cast<float *>(smem + 16 * D * 2), *s_inv = s_mn + D;
+    uint32_t *s_meta = reinterpret_cast<uint32_t *>(s_inv + D);
+    const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
+    uint2 x[TPW];
+#pragma unroll
+    for (int j = 0; j < TPW; j++)
+        x[j] = __ldg(reinterpret_cast<const uint2 *>(stream_row(p, jb, p.k_res, p.k_new, p.k_stride, h, jb.t0 + w * TPW + j)) + lane);
+    __half2 lo0 = *reinterpret_cast<const __half2 *>(&x[0].x), hi0 = lo0;
+    __half2 lo1 = *reinterpret_cast<const __half2 *>(&x[0].y), hi1 = lo1;
+#pragma unroll
+    for (int j = 1; j < TPW; j++) {
+        const __half2 a = *reinterpret_cast<const __half2 *>(&x[j].x), c = *reinterpret_cast<const __half2 *>(&x[j].y);
+        lo0 = __hmin2(lo0, a);
+        hi0 = __hmax2(hi0, a);
+        lo1 = __hmin2(lo1, c);
+        hi1 = __hmax2(hi1, c);
+    }
+    reinterpret_cast<uint2 *>(&s_lo[w][0])[lane] =
+        make_uint2(*reinterpret_cast<uint32_t *>(&lo0), *reinterpret_cast<uint32_t *>(&lo1));
+    reinterpret_cast<uint2 *>(&s_hi[w][0])[lane] =
+        make_uint2(*reinterpret_cast<uint32_t *>(&hi0), *reinterpret_cast<uint32_t *>(&hi1));
+    __syncthreads();
+    const int64_t page = jb.page * p.H_kv + h;
+    if (tid < D) {
+        float mn = h2f(s_lo[0][tid]), mx = h2f(s_hi[0][tid]);
+#pragma unroll
+        for (int ww = 1; ww < 8; ww++) {
+            mn = fminf(mn, h2f(s_lo[ww][tid]));
+            mx = fmaxf(mx, h2f(s_hi[ww][tid]));
+        }
+        const GroupQ g = make_group(mn, mx, MAXI);
+        s_mn[tid] = g.mn;
+        s_inv[tid] = g.inv;
+        const uint32_t m = (uint32_t)g.s16 | ((uint32_t)g.mn16 << 16);
+        s_meta[tid] = m;
+        reinterpret_cast<uint32_t *>(p.k_meta + (size_t)page * D * 2)[tid] = m;
+    }
+    __syncthreads();
+    const float4 mn4 = reinterpret_cast<const float4 *>(s_mn)[lane], in4 = reinterpret_cast<const float4 *>(s_inv)[lane];
+    const uint64_t mn01 = pk2(mn4.x, mn4.y), mn23 = pk2(mn4.z, mn4.w);
+    const uint64_t in01 = pk2(in4.x, in4.y), in23 = pk2(in4.z, in4.w);
+    constexpr uint32_t lim = kMagicBits + MAXI;
+    const int64_t row0 = page * (8 * TPW / FPI) + w * NWR;
+#pragma unroll
+    for (int r = 0; r < NWR; r++) {
+        uint32_t wd[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+        for (int k = 0; k < FPI; k++) {
+            const uint2 v = x[r * FPI + k];
+            uint32_t a0, a1, a2, a3;
+            float em = 0.f;
+            qbits2(v.x, mn01, in01, lim, a0, a1, em);
+            qbits2(v.y, mn23, in23, lim, a2, a3, em);
+            if (em > kTieMargin) {
+                const uint4 e = exact_codes4(v, reinterpret_cast<const uint4 *>(s_meta)[lane], MAXI);
+                a0 = kMagicBits + e.x;
+                a1 = kMagicBits + e.y;
+                a2 = kMagicBits + e.z;
+                a3 = kMagicBits + e.w;
+            }
+            const uint32_t m = 1u << (BITS * k);
+            wd[0] += a0 * m;
+            wd[1] += a1 * m;
+            wd[2] += a2 * m;
+            wd[3] += a3 * m;
+        }
+        const uint32_t off = magic_sum(BITS, FPI);
+        *reinterpret_cast<uint4 *>(p.k_codes + (size_t)(row0 + r) * D + kword_pos(4 * lane, w * NWR + r)) =
+            make_uint4(wd[0] - off, wd[1] - off, wd[2] - off, wd[3] - off);
+    }
+}
+
+// 128 value tokens of one page (block vb of it): 16 tokens per warp, lane (tq, c) holds
+// tokens 8 g + tq and of each the 8-channel chunks c, c + 4, c + 8, c + 12.
+template <int BITS>
+__device__ __forceinline__ void extend_values(const ExtendParams &p, const PageJob &jb, int h, int vb, unsigned char *smem) {
+    constexpr int D = 128, FPI = 32 / BITS, NWORD = D / FPI;
+    uint32_t(*s_codes)[128] = reinterpret_cast<uint32_t(*)[128]>(smem);
+    uint32_t *s_meta = reinterpret_cast<uint32_t *>(smem + NWORD * 512);
+    const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31, tq = lane >> 2, c = lane & 3;
+    uint4 x[2][4];
+#pragma unroll
+    for (int g = 0; g < 2; g++) {
+        const uint4 *row = reinterpret_cast<const uint4 *>(
+            stream_row(p, jb, p.v_res, p.v_new, p.v_stride, h, jb.t0 + vb * 128 + 16 * w + 8 * g + tq));
+#pragma unroll
+        for (int i = 0; i < 4; i++) x[g][i] = __ldg(row + c + 4 * i);
+    }
+    constexpr uint32_t lim = kMagicBits + (1u << BITS) - 1;
+#pragma unroll
+    for (int g = 0; g < 2; g++) {
+        const int tt = 16 * w + 8 * g + tq;
+        __half2 lo = *reinterpret_cast<const __half2 *>(&x[g][0].x), hi = lo;
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+#pragma unroll
+            for (int k = (i == 0 ? 1 : 0); k < 4; k++) {
+                const uint32_t wk = (&x[g][i].x)[k];
+                const __half2 v = *reinterpret_cast<const __half2 *>(&wk);
+                lo = __hmin2(lo, v);
+                hi = __hmax2(hi, v);
+            }
+        float a = fminf(__low2float(lo), __high2float(lo)), b = fmaxf(__low2float(hi), __high2float(hi));
+#pragma unroll
+        for (int o = 1; o < 4; o <<= 1) {
+            a = fminf(a, __shfl_xor_sync(0xffffffffu, a, o));
+            b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, o));
+        }
+        const GroupQ gr = make_group(a, b, (1 << BITS) - 1);
+        if (c == 0) s_meta[tt] = (uint32_t)gr.s16 | ((uint32_t)gr.mn16 << 16);
+        const uint64_t mn2 = pk2(gr.mn, gr.mn), inv2 = pk2(gr.inv, gr.inv);
+#pragma unroll
+        for (int i = 0; i < 4; i++) {  // chunk c + 4 i: channels 8 (c + 4 i) .. + 7
+            constexpr int NP = BITS == 8 ? 2 : 1, PER = 8 / NP;  // words of a chunk, codes in each
+            uint32_t part[NP];
+            float emax = 0.f;
+#pragma unroll
+            for (int n = 0; n < NP; n++) {
+                part[n] = 0;
+#pragma unroll
+                for (int k = 0; k < PER / 2; k++) {
+                    uint32_t c0, c1;
+                    qbits2((&x[g][i].x)[n * (PER / 2) + k], mn2, inv2, lim, c0, c1, emax);
+                    part[n] += c0 * (1u << (BITS * (2 * k)));
+                    part[n] += c1 * (1u << (BITS * (2 * k + 1)));
+                }
+                part[n] -= magic_sum(BITS, PER);
+            }
+            if (emax > kTieMargin) {  // near a half-integer in this chunk: the exact path
+#pragma unroll
+                for (int n = 0; n < NP; n++) {
+                    part[n] = 0;
+#pragma unroll
+                    for (int k = 0; k < PER / 2; k++) {
+                        const float2 f = unpack_half2((&x[g][i].x)[n * (PER / 2) + k]);
+                        part[n] |= quant_code(f.x, gr) << (BITS * (2 * k));
+                        part[n] |= quant_code(f.y, gr) << (BITS * (2 * k + 1));
+                    }
+                }
+            }
+            if (BITS == 2) {  // 16 channels per word: chunks 2m (lane c even) and 2m + 1
+                const uint32_t nb = __shfl_xor_sync(0xffffffffu, part[0], 1);
+                if ((c & 1) == 0) s_codes[(c + 4 * i) >> 1][tt] = part[0] | (nb << 16);
+            } else {
+#pragma unroll
+                for (int n = 0; n < NP; n++) s_codes[NP * (c + 4 * i) + n][tt] = part[n];
+            }
+        }
+    }
+    __syncthreads();
+    const int64_t page = jb.page * p.H_kv + h;
+    const int TV = p.TV;
+    for (int i = tid; i < NWORD * 32; i += 256) {
+        const int m = i >> 5, tt = vb * 128 + 4 * (i & 31), tile = tt / TV, j = tt - tile * TV;
+        *reinterpret_cast<uint4 *>(p.v_codes + (size_t)page * NWORD * p.G + ((size_t)tile * NWORD + m) * TV + vword_pos(j, m, TV)) =
+            *reinterpret_cast<const uint4 *>(&s_codes[m][4 * (i & 31)]);
+    }
+    if (tid < 32)
+        reinterpret_cast<uint4 *>(reinterpret_cast<uint32_t *>(p.v_meta) + (size_t)page * p.G + vb * 128)[tid] =
+            *reinterpret_cast<const uint4 *>(&s_meta[4 * tid]);
+}
+
+// G = 8 TPW tokens per page.
+template <int TPW>
+__global__ void __launch_bounds__(256, TPW == 16 ? 4 : 2) extend_pack_kernel(const ExtendParams p, int kbits, int vbits) {
+    __shared__ __align__(16) unsigned char smem[32 * 512 + 512];
+    const int h = blockIdx.y;
+    const PageJob jb = find_page(p, blockIdx.x);
+    if (blockIdx.z == 0) {
+        if (kbits == 2) extend_keys<2, TPW>(p, jb, h, smem);
+        else if (kbits == 4) extend_keys<4, TPW>(p, jb, h, smem);
+        else extend_keys<8, TPW>(p, jb, h, smem);
+    } else {
+        const int vb = blockIdx.z - 1;
+        if (vbits == 2) extend_values<2>(p, jb, h, vb, smem);
+        else if (vbits == 4) extend_values<4>(p, jb, h, vb, smem);
+        else extend_values<8>(p, jb, h, vb, smem);
+    }
+}
+
+// The rows that stay fp16: CTA (b, head and side, slice) copies slot b's new sink rows and
+// its residual's new rows; the first CTA of a slot commits the lengths.  Runs after the
+// pack kernel, which reads the old residual rows that this overwrites.
+constexpr int kTailSlices = 4;
+__global__ void __launch_bounds__(256) extend_tail_kernel(const ExtendParams p) {
+    const int b = blockIdx.x, h = blockIdx.y >> 1, side = blockIdx.y & 1;
+    const int4 *d = reinterpret_cast<const int4 *>(p.desc);
+    const int4 x = d[2 * b];
+    if (!x.w) return;
+    const int4 y = d[2 * b + 1];
+    const int to_sink = y.y, pk = y.z, tot = x.z + x.w - to_sink, lo = pk ? 0 : x.z, hi = tot - pk;
+    const int64_t stride = side ? p.v_stride : p.k_stride;
+    const uint16_t *src = (side ? p.v_new : p.k_new) + h * 128;
+    const size_t u = (size_t)b * p.H_kv + h;
+    uint16_t *sink = side ? p.v_sink : p.k_sink, *res = side ? p.v_res : p.k_res;
+    const int n = to_sink + hi - lo, c = threadIdx.x & 15;
+    for (int i = blockIdx.z * 16 + (threadIdx.x >> 4); i < n; i += kTailSlices * 16) {
+        // chunk token and destination row; residual rows come from the chunk alone, since a
+        // slot that packs nothing keeps its old rows and one that packs takes all of them
+        const int r = i - to_sink + lo;
+        const int tok = i < to_sink ? i : to_sink + pk + r - x.z;
+        uint16_t *dst = i < to_sink ? sink + (u * p.S + x.x + i) * 128 : res + (u * p.R + r) * 128;
+        reinterpret_cast<uint4 *>(dst)[c] = __ldg(reinterpret_cast<const uint4 *>(src + (int64_t)(y.x + tok) * stride) + c);
+    }
+    if (blockIdx.y == 0 && blockIdx.z == 0 && threadIdx.x == 0)
+        reinterpret_cast<int4 *>(p.lens)[b] = make_int4(x.x + to_sink, x.y + pk, hi, 1);
+}
+
+cudaError_t launch_extend(const ExtendParams &p, int kbits, int vbits, cudaStream_t st) {
+    if (p.n_pack > 0) {
+        const dim3 grid((unsigned)p.n_pack, (unsigned)p.H_kv, (unsigned)(1 + p.G / 128));
+        if (p.G == 128) extend_pack_kernel<16><<<grid, 256, 0, st>>>(p, kbits, vbits);
+        else if (p.G == 256) extend_pack_kernel<32><<<grid, 256, 0, st>>>(p, kbits, vbits);
+        else return cudaErrorInvalidValue;
+        const cudaError_t e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+    }
+    extend_tail_kernel<<<dim3((unsigned)p.B, (unsigned)(2 * p.H_kv), kTailSlices), 256, 0, st>>>(p);
+    return cudaGetLastError();
+}
+
+// ------------------------------------------------------------------------------
+// Norm and rotation of new queries and keys.  A warp holds one head's row (D / 32
+// consecutive channels per lane), a CTA a token's heads; the token's sines and cosines are
+// formed once per CTA.  An angle pos * base^(-2j/n) is reduced in 64-bit fixed point:
+// pos * turn[j] mod 2^64 is the exact fraction of a turn, whose upper 32 bits go to
+// sincospif.
+// ------------------------------------------------------------------------------
+template <int D>
+__global__ void __launch_bounds__(256) qk_kernel(const __grid_constant__ QkParams p, int heads) {
+    constexpr int E = D / 32;
+    using Vec = typename std::conditional<E == 2, uint32_t, typename std::conditional<E == 4, uint2, uint4>::type>::type;
+    __shared__ float2 s_cs[D / 2];
+    const int64_t i = blockIdx.x;
+    const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, half = p.rotary >> 1;
+    if (tid < half) {
+        const uint64_t a = (uint64_t)(int64_t)p.pos[i] * p.turn[tid];
+        float s, c;
+        sincospif((float)(int32_t)(a >> 32) * 0x1p-31f, &s, &c);
+        s_cs[tid] = make_float2(c, s);
+    }
+    __syncthreads();
+    const int H = p.H_q + p.H_kv, h1 = min(H, (int)(blockIdx.y + 1) * heads);
+    for (int h = blockIdx.y * heads + w; h < h1; h += 8) {
+        const bool key = h >= p.H_q;
+        const uint16_t *src = key ? p.k + i * p.k_stride + (h - p.H_q) * D : p.q + i * p.q_stride + h * D;
+        uint16_t *dst = key ? p.k_out + (i * p.H_kv + h - p.H_q) * D : p.q_out + (i * p.H_q + h) * D;
+        const uint16_t *wt = key ? p.w_k : p.w_q;
+        Vec v = reinterpret_cast<const Vec *>(src)[lane];
+        float x[E];
+#pragma unroll
+        for (int e = 0; e < E; e += 2) {
+            const float2 f = unpack_half2(reinterpret_cast<const uint32_t *>(&v)[e / 2]);
+            x[e] = f.x;
+            x[e + 1] = f.y;
+        }
+        if (wt) {
+            float ss = 0.f;
+#pragma unroll
+            for (int e = 0; e < E; e++) ss += x[e] * x[e];
+#pragma unroll
+            for (int o = 16; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+            const float r = rsqrtf(ss * (1.0f / D) + p.eps);
+            const Vec wv = reinterpret_cast<const Vec *>(wt)[lane];
+#pragma unroll
+            for (int e = 0; e < E; e += 2) {
+                const float2 f = unpack_half2(reinterpret_cast<const uint32_t *>(&wv)[e / 2]);
+                x[e] = x[e] * r * f.x;
+                x[e + 1] = x[e + 1] * r * f.y;
+            }
+        }
+        if (p.rotate & (key ? 2 : 1)) {
+            const int c0 = lane * E;
+            if (!p.halves) {
+                if (c0 < p.rotary)
+#pragma unroll
+                    for (int e = 0; e < E; e += 2) {
+                        const float2 cs = s_cs[(c0 + e) >> 1];
+                        const float a = x[e], b = x[e + 1];
+                        x[e] = a * cs.x - b * cs.y;
+                        x[e + 1] = a * cs.y + b * cs.x;
+                    }
+            } else {
+                const int hl = half / E;  // lanes of the first half (half is a multiple of E)
+                const int other = lane < hl ? lane + hl : lane < 2 * hl ? lane - hl : lane;
+                const int j0 = lane < hl ? c0 : c0 - half;
+#pragma unroll
+                for (int e = 0; e < E; e++) {
+                    const float o = __shfl_sync(0xffffffffu, x[e], other);
+                    if (lane < 2 * hl) {
+                        const float2 cs = s_cs[j0 + e];
+                        x[e] = lane < hl ? x[e] * cs.x - o * cs.y : o * cs.y + x[e] * cs.x;
+                    }
+                }
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < E; e += 2) reinterpret_cast<uint32_t *>(&v)[e / 2] = pack_half2(x[e], x[e + 1]);
+        reinterpret_cast<Vec *>(dst)[lane] = v;
+    }
+}
+
+cudaError_t launch_qk(const QkParams &p, int D, cudaStream_t st) {
+    const int H = p.H_q + p.H_kv;
+    // few tokens: their heads go to several CTAs, eight at least each
+    int y = 1;
+    while (p.n * y < 2 * num_sms() && (H + y - 1) / y > 8) y++;
+    const int heads = (H + y - 1) / y;
+    const dim3 grid((unsigned)p.n, (unsigned)((H + heads - 1) / heads));
+    if (D == 64) qk_kernel<64><<<grid, 256, 0, st>>>(p, heads);
+    else if (D == 128) qk_kernel<128><<<grid, 256, 0, st>>>(p, heads);
+    else qk_kernel<256><<<grid, 256, 0, st>>>(p, heads);
+    return cudaGetLastError();
+}
+
+}  // namespace kvq
+
+// ------------------------------------------------------------------------------
+// C ABI
+// ------------------------------------------------------------------------------
+namespace {
+
+bool capturing(cudaStream_t st) {
+    cudaStreamCaptureStatus s = cudaStreamCaptureStatusNone;
+    if (cudaStreamIsCapturing(st, &s) != cudaSuccess) {
+        cudaGetLastError();  // a legacy-stream query that a global capture forbids
+        return true;
+    }
+    return s != cudaStreamCaptureStatusNone;
+}
+
+int check_chunk(const kvq_config *c, const kvq_chunk *ch) {
+    if (!ch || !ch->host || ch->max_tokens < 0) return KVQ_ERR_INVALID_ARG;
+    const void *need[] = {ch->cu, ch->slot, ch->pos, ch->desc};
+    for (const void *p : need)
+        if (!p || !aligned16(p)) return KVQ_ERR_INVALID_ARG;
+    (void)c;
+    return KVQ_OK;
+}
+
+ChunkSlot *slots_of(const kvq_chunk *ch) { return reinterpret_cast<ChunkSlot *>(ch->host); }
+
+// Whether the cache's host lengths are those that the plan was made for.
+bool plan_holds(const kvq_config *c, const kvq_paged *pc, const kvq_chunk *ch) {
+    const ChunkSlot *s = slots_of(ch);
+    int64_t rows = 0;
+    for (int b = 0; b < c->B; b++) {
+        const int32_t *l = pc->lens_host + 4 * b;
+        const bool on = l[3] != 0;
+        if (s[b].ns != (on ? l[0] : 0) || s[b].T != (on ? l[1] : 0) || s[b].nr != (on ? l[2] : 0)) return false;
+        if (s[b].n_new < 0 || s[b].cu != rows) return false;
+        // what the plan derived, for this configuration
+        const int to_sink = std::min(s[b].n_new, c->S - s[b].ns);
+        const int64_t pk = s[b].n_new ? ((int64_t)s[b].nr + s[b].n_new - to_sink) / c->R * c->R : 0;
+        if (s[b].to_sink != to_sink || s[b].pk != pk || s[b].T + pk > c->max_T) return false;
+        rows += s[b].n_new;
+    }
+    return rows == ch->n_tokens;
+}
+
+bool rows_ok(const uint16_t *p, int64_t stride, int64_t heads, int64_t D) {
+    return p && aligned16(p) && stride >= heads * D && stride % 8 == 0;
+}
+
+bool overlap(const void *a, size_t na, const void *b, size_t nb) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y + nb && y < x + na;
+}
+
+// CTAs of the attention and its partials: two ranges' ends per CTA, 256 rows each.
+int chunk_ctas() { return 2 * num_sms(); }
+constexpr int kWsRows = 256;
+struct ChunkWs {
+    size_t ml, o, total;
+};
+ChunkWs chunk_ws() {
+    ChunkWs w;
+    const size_t slots = (size_t)2 * num_sms() * kWsRows;  // per CTA: 2 x 256 rows, or 4 x 128 ...
+    w.ml = 0;
+    w.o = (slots * sizeof(float2) + 255) / 256 * 256;
+    w.total = w.o + slots * 128 * sizeof(float);
+    return w;
+}
+
+}  // namespace
+
+extern "C" {
+
+int kvq_paged_plan(const kvq_config *c, kvq_paged *pc, const int32_t *n_new, const int32_t *new_pages,
+                   int64_t n_new_pages, kvq_chunk *ch, void *stream) {
+    int e = check_paged(c, pc);
+    if (e) return e;
+    if ((e = check_chunk(c, ch))) return e;
+    if (!n_new || n_new_pages < 0 || (reinterpret_cast<uintptr_t>(new_pages) & 3u)) return KVQ_ERR_INVALID_ARG;
+    int64_t rows = 0, pages = 0;
+    for (int b = 0; b < c->B; b++) {
+        const int32_t *l = pc->lens_host + 4 * b;
+        if (n_new[b] < 0) return KVQ_ERR_INVALID_ARG;
+        const int64_t ns = l[3] ? l[0] : 0, T = l[3] ? l[1] : 0, nr = l[3] ? l[2] : 0;
+        const int64_t to_sink = std::min<int64_t>(n_new[b], c->S - ns);
+        const int64_t pk = n_new[b] ? (nr + n_new[b] - to_sink) / c->R * c->R : 0;
+        if (T + pk > c->max_T || ns + T + nr + n_new[b] > INT32_MAX) return KVQ_ERR_CAPACITY;
+        rows += n_new[b];
+        pages += pk / c->G;
+    }
+    if (rows > ch->max_tokens || rows > INT32_MAX - 4096) return KVQ_ERR_CAPACITY;
+    if (new_pages && pages > n_new_pages) return KVQ_ERR_CAPACITY;
+    cudaStream_t st = (cudaStream_t)stream;
+    if (capturing(st)) return KVQ_ERR_UNSUPPORTED;
+    PlanParams p;
+    p.cu = ch->cu;
+    p.slot = ch->slot;
+    p.pos = ch->pos;
+    p.desc = ch->desc;
+    p.table = const_cast<int32_t *>(pc->page_table);
+    p.lens = pc->lens;
+    p.new_pages = new_pages;
+    p.B = c->B;
+    p.S = c->S;
+    p.R = c->R;
+    p.G = c->G;
+    p.table_stride = (int)(c->max_T / c->G);
+    p.n_tokens = (int)rows;
+    memcpy(p.n_new, n_new, (size_t)c->B * 4);
+    if (launch_plan(p, st) != cudaSuccess) return KVQ_ERR_CUDA;
+    int cu = 0, pg = 0;
+    for (int b = 0; b < c->B; b++) {
+        const int32_t *l = pc->lens_host + 4 * b;
+        ChunkSlot &s = slots_of(ch)[b];
+        s.ns = l[3] ? l[0] : 0;
+        s.T = l[3] ? l[1] : 0;
+        s.nr = l[3] ? l[2] : 0;
+        s.n_new = n_new[b];
+        s.cu = cu;
+        s.to_sink = std::min(n_new[b], c->S - s.ns);
+        s.pk = n_new[b] ? (s.nr + n_new[b] - s.to_sink) / c->R * c->R : 0;
+        s.page0 = pg;
+        cu += n_new[b];
+        pg += s.pk / c->G;
+    }
+    ch->n_tokens = rows;
+    return KVQ_OK;
+}
+
+size_t kvq_paged_chunk_workspace_bytes(const kvq_config *c) {
+    return paged_cfg_check(c) == KVQ_OK ? chunk_ws().total : 0;
+}
+
+int kvq_paged_chunk_attn(const kvq_config *c, const kvq_paged *pc, const kvq_chunk *ch, const uint16_t *q,
+                         int64_t q_stride, const uint16_t *kn, int64_t k_stride, const uint16_t *vn, int64_t v_stride,
+                         uint16_t *out, void *ws, size_t ws_bytes, void *stream) {
+    int e = check_paged(c, pc);
+    if (e) return e;
+    if ((e = check_chunk(c, ch))) return e;
+    if (!plan_holds(c, pc, ch)) return KVQ_ERR_INVALID_ARG;
+    if (ch->n_tokens == 0) return KVQ_OK;
+    if (!rows_ok(q, q_stride, c->H_q, c->D) || !rows_ok(kn, k_stride, c->H_kv, c->D) ||
+        !rows_ok(vn, v_stride, c->H_kv, c->D) || !out || !aligned16(out))
+        return KVQ_ERR_INVALID_ARG;
+    const ChunkWs wl = chunk_ws();
+    if (!ws || !aligned16(ws) || ws_bytes < wl.total) return KVQ_ERR_WORKSPACE;
+    ChunkAttnParams p;
+    memset(&p, 0, sizeof(p));
+    p.desc = ch->desc;
+    p.ptab = pc->page_table;
+    p.k_codes = pc->k_codes;
+    p.v_codes = pc->v_codes;
+    p.k_meta = pc->k_meta;
+    p.v_meta = pc->v_meta;
+    p.k_sink = pc->k_sink;
+    p.v_sink = pc->v_sink;
+    p.k_res = pc->k_res;
+    p.v_res = pc->v_res;
+    p.q = q;
+    p.k_new = kn;
+    p.v_new = vn;
+    p.out = out;
+    p.part_ml = reinterpret_cast<float2 *>(static_cast<char *>(ws) + wl.ml);
+    p.part_o = reinterpret_cast<float *>(static_cast<char *>(ws) + wl.o);
+    p.status = pc->status;
+    p.q_stride = q_stride;
+    p.k_stride = k_stride;
+    p.v_stride = v_stride;
+    p.n_pages = pc->n_pages;
+    p.B = c->B;
+    p.H_kv = c->H_kv;
+    p.g = c->H_q / c->H_kv;
+    p.G = c->G;
+    p.kbits = c->bits;
+    p.vbits = vbits_of(c);
+    p.S = c->S;
+    p.R = c->R;
+    p.ptab_stride = (int)(c->max_T / c->G);
+    const int rows = 64;
+    int64_t n = 0;
+    for (int b = 0; b < c->B; b++) {
+        const ChunkSlot &s = slots_of(ch)[b];
+        p.item0[b] = (int32_t)n;
+        int64_t per = 0;
+        const int64_t nt = cdiv((int64_t)s.n_new * p.g, rows);
+        for (int64_t t = 0; t < nt; t++) per += chunk_tiles(s, (int)t, rows, p.g);
+        n += per * p.H_kv;
+        if (n >= (1LL << 30)) return KVQ_ERR_UNSUPPORTED;
+    }
+    for (int b = c->B; b <= KVQ_PAGED_MAX_B; b++) p.item0[b] = (int32_t)n;
+    p.n_items = (int)n;
+    p.C = (int)std::min<int64_t>(n, chunk_ctas());
+    return status_of(launch_chunk_attn(p, rows, (cudaStream_t)stream));
+}
+
+int kvq_paged_extend(const kvq_config *c, kvq_paged *pc, const kvq_chunk *ch, const uint16_t *kn, int64_t k_stride,
+                     const uint16_t *vn, int64_t v_stride, void *stream) {
+    int e = check_paged(c, pc);
+    if (e) return e;
+    if ((e = check_chunk(c, ch))) return e;
+    if (!plan_holds(c, pc, ch)) return KVQ_ERR_INVALID_ARG;
+    if (ch->n_tokens == 0) return KVQ_OK;
+    if (!rows_ok(kn, k_stride, c->H_kv, c->D) || !rows_ok(vn, v_stride, c->H_kv, c->D)) return KVQ_ERR_INVALID_ARG;
+    cudaStream_t st = (cudaStream_t)stream;
+    if (capturing(st)) return KVQ_ERR_UNSUPPORTED;
+    ExtendParams p;
+    memset(&p, 0, sizeof(p));
+    p.desc = ch->desc;
+    p.lens = pc->lens;
+    p.status = pc->status;
+    p.k_new = kn;
+    p.v_new = vn;
+    p.k_stride = k_stride;
+    p.v_stride = v_stride;
+    p.k_sink = pc->k_sink;
+    p.v_sink = pc->v_sink;
+    p.k_res = pc->k_res;
+    p.v_res = pc->v_res;
+    p.k_codes = pc->k_codes;
+    p.v_codes = pc->v_codes;
+    p.k_meta = pc->k_meta;
+    p.v_meta = pc->v_meta;
+    p.ptab = pc->page_table;
+    p.n_pages = pc->n_pages;
+    p.B = c->B;
+    p.H_kv = c->H_kv;
+    p.G = c->G;
+    p.S = c->S;
+    p.R = c->R;
+    p.TV = vtile_of(c);
+    p.ptab_stride = (int)(c->max_T / c->G);
+    for (int b = 0; b < c->B; b++) p.n_pack += slots_of(ch)[b].pk / c->G;
+    if (p.n_pack > 0 && pc->n_pages < 1) return KVQ_ERR_CAPACITY;
+    if (launch_extend(p, c->bits, vbits_of(c), st) != cudaSuccess) return KVQ_ERR_CUDA;
+    for (int b = 0; b < c->B; b++) {
+        const ChunkSlot &s = slots_of(ch)[b];
+        if (!s.n_new) continue;
+        int32_t *l = pc->lens_host + 4 * b;
+        l[0] = s.ns + s.to_sink;
+        l[1] = s.T + s.pk;
+        l[2] = s.nr + s.n_new - s.to_sink - s.pk;
+        l[3] = 1;
+    }
+    return KVQ_OK;
+}
+
+int kvq_qk_norm_rope(const kvq_qk_config *c, const uint16_t *q, const uint16_t *k, const uint16_t *w_q,
+                     const uint16_t *w_k, const int32_t *pos, int64_t n, uint16_t *q_out, uint16_t *k_out,
+                     void *stream) {
+    if (!c || c->H_q < 0 || c->H_kv < 0 || c->H_q + (int64_t)c->H_kv < 1 || c->H_q > 65535 || c->H_kv > 65535 || n < 0)
+        return KVQ_ERR_INVALID_ARG;
+    if (c->D != 64 && c->D != 128 && c->D != 256) return KVQ_ERR_UNSUPPORTED;
+    if (c->rotary_dim < 0 || c->rotary_dim > c->D || (c->halves & ~1) || (c->rotate & ~3)) return KVQ_ERR_INVALID_ARG;
+    if (c->rotary_dim % 16) return KVQ_ERR_UNSUPPORTED;
+    if (!(c->eps >= 0.f) || !std::isfinite(c->eps) || !(c->rope_base >= 0.f) || !std::isfinite(c->rope_base))
+        return KVQ_ERR_INVALID_ARG;
+    if (n == 0) return KVQ_OK;
+    if (n > INT32_MAX) return KVQ_ERR_UNSUPPORTED;
+    if (!pos || (reinterpret_cast<uintptr_t>(pos) & 3u)) return KVQ_ERR_INVALID_ARG;
+    struct Side {
+        const uint16_t *x, *w;
+        uint16_t *y;
+        int64_t stride, H;
+    } side[2] = {{q, w_q, q_out, c->q_stride, c->H_q}, {k, w_k, k_out, c->k_stride, c->H_kv}};
+    for (const Side &s : side) {
+        if (!s.H) continue;
+        if (!rows_ok(s.x, s.stride, s.H, c->D) || !s.y || !aligned16(s.y) || (s.w && !aligned16(s.w)))
+            return KVQ_ERR_INVALID_ARG;
+    }
+    for (int a = 0; a < 2; a++) {
+        if (!side[a].H) continue;
+        const size_t ny = (size_t)n * side[a].H * c->D * 2;
+        if (side[1 - a].H && a == 0 && overlap(side[0].y, ny, side[1].y, (size_t)n * side[1].H * c->D * 2))
+            return KVQ_ERR_INVALID_ARG;
+        for (int b = 0; b < 2; b++) {
+            if (!side[b].H) continue;
+            const size_t nx = ((size_t)(n - 1) * side[b].stride + side[b].H * c->D) * 2;
+            const bool own = a == b && side[a].y == side[a].x && (side[a].stride == side[a].H * c->D || n == 1);
+            if (!own && overlap(side[a].y, ny, side[b].x, nx)) return KVQ_ERR_INVALID_ARG;
+        }
+    }
+    QkParams p;
+    memset(&p, 0, sizeof(p));
+    p.q = q;
+    p.k = k;
+    p.w_q = w_q;
+    p.w_k = w_k;
+    p.pos = pos;
+    p.q_out = q_out;
+    p.k_out = k_out;
+    p.n = n;
+    p.q_stride = c->q_stride;
+    p.k_stride = c->k_stride;
+    p.H_q = c->H_q;
+    p.H_kv = c->H_kv;
+    p.rotary = c->rotary_dim;
+    p.halves = c->halves;
+    p.rotate = c->rotary_dim ? c->rotate : 0;
+    p.eps = c->eps;
+    const long double base = c->rope_base > 0.f ? (long double)c->rope_base : 10000.0L;
+    for (int j = 0; j < c->rotary_dim / 2; j++) {
+        const long double turn = powl(base, -2.0L * j / c->rotary_dim) / 6.283185307179586476925286766559L;
+        p.turn[j] = (uint64_t)ldexpl(turn - floorl(turn), 64);
+    }
+    return status_of(launch_qk(p, c->D, (cudaStream_t)stream));
+}
+
+}  // extern "C"

@@ -1,0 +1,89 @@
+// kvq_chunk.h -- parameter blocks and launchers of the chunk operators of the paged cache
+// (kvq_chunk.cu, kvq_chunk_attn.cu); not part of the public ABI.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "kvq.h"
+
+namespace kvq {
+
+// One slot of a plan (kvq_chunk.desc).
+struct ChunkSlot {
+    int ns, T, nr, n_new;                // lengths before the chunk, new tokens
+    int cu, to_sink, pk, page0;          // first row, tokens to the sink, tokens to pack, pages before
+};
+
+struct PlanParams {
+    int32_t *cu, *slot, *pos, *desc, *table;
+    const int32_t *lens, *new_pages;
+    int B, S, R, G, table_stride;
+    int n_tokens;
+    int32_t n_new[KVQ_PAGED_MAX_B];
+};
+
+struct ExtendParams {
+    const int32_t *desc;
+    int32_t *lens, *status;
+    const uint16_t *k_new, *v_new;
+    int64_t k_stride, v_stride;
+    uint16_t *k_sink, *v_sink, *k_res, *v_res;
+    int32_t *k_codes, *v_codes;
+    uint16_t *k_meta, *v_meta;
+    const int32_t *ptab;
+    int64_t n_pages;
+    int B, H_kv, G, S, R, TV, ptab_stride;
+    int n_pack;                          // pages to pack, over all slots
+};
+
+struct QkParams {
+    const uint16_t *q, *k, *w_q, *w_k;
+    const int32_t *pos;
+    uint16_t *q_out, *k_out;
+    int64_t n, q_stride, k_stride;
+    int H_q, H_kv, rotary, halves, rotate;
+    float eps;
+    uint64_t turn[128];                  // base^(-2j/rotary) / (2 pi) in units of 2^-64 turns
+};
+
+// Chunk attention.  A unit is (slot, key head, tile of `rows` query rows): row r of a slot
+// is its new token r / g under query head r % g of the key head's group.  Its items are
+// key tiles of 128 tokens: the packed ones, then the fp16 tokens [sink | residual | chunk]
+// up to the tile's last query token.  The items of all units, slot-major, then by head and
+// row tile, are cut into C equal ranges, one per CTA.  A unit inside one range is finished
+// there; of one that is cut, each range leaves fp32 partials, and the combine kernel joins
+// them in range order.
+struct ChunkAttnParams {
+    const int32_t *desc;
+    const int32_t *ptab;
+    const int32_t *k_codes, *v_codes;
+    const uint16_t *k_meta, *v_meta;
+    const uint16_t *k_sink, *v_sink, *k_res, *v_res;
+    const uint16_t *q, *k_new, *v_new;
+    uint16_t *out;
+    float *part_o;                       // [2 C][rows][128]
+    float2 *part_ml;                     // [2 C][rows] (max, sum)
+    int32_t *status;
+    int64_t q_stride, k_stride, v_stride, n_pages;
+    int B, H_kv, g, G, kbits, vbits, S, R, ptab_stride;
+    int n_items, C;
+    int32_t item0[KVQ_PAGED_MAX_B + 1];  // first item of each slot
+};
+
+cudaError_t launch_plan(const PlanParams &p, cudaStream_t st);
+cudaError_t launch_extend(const ExtendParams &p, int kbits, int vbits, cudaStream_t st);
+cudaError_t launch_qk(const QkParams &p, int D, cudaStream_t st);
+// rows: query rows per unit (chunk_attn_rows); p.item0, n_items and C follow from it.
+cudaError_t launch_chunk_attn(const ChunkAttnParams &p, int rows, cudaStream_t st);
+
+constexpr int kChunkKeys = 128;          // tokens per key tile
+
+// Key tiles of row tile t of a slot (rows query rows per tile, g per token).
+__host__ __device__ inline int chunk_tiles(const ChunkSlot &s, int t, int rows, int g) {
+    const int last = ((t + 1) * rows - 1) / g + 1;                 // new tokens up to the tile's last
+    const int seen = s.ns + s.nr + (last < s.n_new ? last : s.n_new);
+    return s.T / kChunkKeys + (seen + kChunkKeys - 1) / kChunkKeys;
+}
+
+}  // namespace kvq

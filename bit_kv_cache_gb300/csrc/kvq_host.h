@@ -67,6 +67,11 @@ size_t decode_ws_counter_end(const kvq_config *c);
 int decode_attn_status(const kvq_config *c, const kvq_cache *k, const uint16_t *q, uint16_t *out, void *ws,
                        size_t ws_bytes, void *stream, int32_t *status_word);
 
+// Checks of a paged cache shared by the paged ABI (defined in kvq_paged.cu): the
+// configuration, and the configuration with the cache's pointers and host lengths.
+int paged_cfg_check(const kvq_config *c);
+int check_paged(const kvq_config *c, const kvq_paged *pc);
+
 inline bool fast_supported(const kvq_config *c) {
     const int tok = 256 / c->bits;  // a tile holds 8 key word rows
     if (nvfp4(c) && (c->rope || c->D != 128 || c->H_q / c->H_kv > 4 || c->G % 64 || (c->G & (c->G - 1))))

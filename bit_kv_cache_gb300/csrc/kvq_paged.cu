@@ -21,6 +21,41 @@
 using namespace kvq;
 using namespace kvq::host;
 
+namespace kvq {
+namespace host {
+
+int paged_cfg_check(const kvq_config *c) {
+    const int e = kvq_config_check(c);
+    if (e) return e;
+    if (kitty(c) || c->rope || !fast_supported(c) || c->B > KVQ_PAGED_MAX_B) return KVQ_ERR_UNSUPPORTED;
+    if (c->max_T / c->G < 1) return KVQ_ERR_INVALID_ARG;
+    return KVQ_OK;
+}
+
+int check_paged(const kvq_config *c, const kvq_paged *pc) {
+    int e = paged_cfg_check(c);
+    if (e) return e;
+    if (!pc || !pc->lens_host) return KVQ_ERR_INVALID_ARG;
+    const void *need[] = {pc->k_codes, pc->k_meta, pc->v_codes, pc->v_meta, pc->page_table,
+                          pc->k_res, pc->v_res, pc->lens};
+    for (const void *p : need)
+        if (!p || !aligned16(p)) return KVQ_ERR_INVALID_ARG;
+    if (c->S > 0 && (!pc->k_sink || !pc->v_sink || !aligned16(pc->k_sink) || !aligned16(pc->v_sink)))
+        return KVQ_ERR_INVALID_ARG;
+    if (pc->n_pages < 0 || pc->n_pages > (int64_t)INT32_MAX) return KVQ_ERR_INVALID_ARG;
+    for (int b = 0; b < c->B; b++) {
+        const int32_t *l = pc->lens_host + 4 * b;
+        if (l[3] != 0 && l[3] != 1) return KVQ_ERR_INVALID_ARG;
+        if (!l[3]) continue;
+        if (l[0] < 0 || l[0] > c->S || l[1] < 0 || l[1] % c->G || l[1] > c->max_T || l[2] < 0 || l[2] > c->R)
+            return KVQ_ERR_INVALID_ARG;
+    }
+    return KVQ_OK;
+}
+
+}  // namespace host
+}  // namespace kvq
+
 namespace {
 
 // Per-sequence slot ids a paged decode may need (the CTAs of both pools touching one
@@ -48,36 +83,7 @@ PagedWs paged_ws_layout(const kvq_config *c) {
     return w;
 }
 
-int paged_cfg_check(const kvq_config *c) {
-    const int e = kvq_config_check(c);
-    if (e) return e;
-    if (kitty(c) || c->rope || !fast_supported(c) || c->B > KVQ_PAGED_MAX_B) return KVQ_ERR_UNSUPPORTED;
-    if (c->max_T / c->G < 1) return KVQ_ERR_INVALID_ARG;
-    return KVQ_OK;
-}
-
 int64_t max_pages(const kvq_config *c) { return c->max_T / c->G; }
-
-int check_paged(const kvq_config *c, const kvq_paged *pc) {
-    int e = paged_cfg_check(c);
-    if (e) return e;
-    if (!pc || !pc->lens_host) return KVQ_ERR_INVALID_ARG;
-    const void *need[] = {pc->k_codes, pc->k_meta, pc->v_codes, pc->v_meta, pc->page_table,
-                          pc->k_res, pc->v_res, pc->lens};
-    for (const void *p : need)
-        if (!p || !aligned16(p)) return KVQ_ERR_INVALID_ARG;
-    if (c->S > 0 && (!pc->k_sink || !pc->v_sink || !aligned16(pc->k_sink) || !aligned16(pc->v_sink)))
-        return KVQ_ERR_INVALID_ARG;
-    if (pc->n_pages < 0 || pc->n_pages > (int64_t)INT32_MAX) return KVQ_ERR_INVALID_ARG;
-    for (int b = 0; b < c->B; b++) {
-        const int32_t *l = pc->lens_host + 4 * b;
-        if (l[3] != 0 && l[3] != 1) return KVQ_ERR_INVALID_ARG;
-        if (!l[3]) continue;
-        if (l[0] < 0 || l[0] > c->S || l[1] < 0 || l[1] % c->G || l[1] > c->max_T || l[2] < 0 || l[2] > c->R)
-            return KVQ_ERR_INVALID_ARG;
-    }
-    return KVQ_OK;
-}
 
 PageMap page_map(const kvq_config *c, const kvq_paged *pc) {
     PageMap m;

@@ -430,6 +430,104 @@ int kvq_paged_decode_attn(const kvq_config *cfg, const kvq_paged *pc, const uint
 /* As kvq_read_status, for the workspace status word and pc->status. */
 int kvq_paged_read_status(const kvq_paged *pc, void *ws, int32_t *dev_status, void *stream);
 
+/* ---------------------------------------------------------------------------------
+ * Chunks of new tokens over the paged cache.  A serving step adds n_new[b] >= 0 tokens
+ * to every batch slot b: the next chunk of a prompt, drafted tokens to verify, or one
+ * token each.  The order of a step is
+ *   kvq_paged_plan        slot maps, positions and block-table rows (once per step; any
+ *                         number of caches of the same configuration and lengths, such
+ *                         as the layers of a model, may use one plan)
+ *   kvq_qk_norm_rope      norm and rotation of the new queries and keys
+ *   kvq_paged_chunk_attn  every new token attends to its slot's cached tokens and to the
+ *                         chunk's tokens up to itself
+ *   kvq_paged_extend      the new tokens enter the cache
+ * The chunk's rows are token-major: slot 0's tokens, then slot 1's, ...; row i of a
+ * tensor of H heads starts `stride` elements after row i - 1 (stride >= H * D, a multiple
+ * of 8), its heads D elements apart, so that the rows of a fused projection can be passed
+ * in place.
+ *
+ * kvq_chunk: caller-owned buffers of a plan.
+ *   cu    int32 [B + 1]          (device) first row of each slot; cu[B] = n_tokens
+ *   slot  int32 [max_tokens]     (device) batch slot of each row
+ *   pos   int32 [max_tokens]     (device) position of each row's token in its sequence
+ *   desc  int32 [B][8]           (device) {n_sink, T, n_res, n_new, cu, tokens to the
+ *                                sink, tokens to pack, pages of the slots before}: lengths
+ *                                before the chunk
+ *   host  int32 [B][8]           (host)   the same
+ * n_tokens is set by kvq_paged_plan.  slot and pos keep their values behind n_tokens.
+ * --------------------------------------------------------------------------------- */
+typedef struct {
+    int32_t *cu, *slot, *pos, *desc;
+    int32_t *host;
+    int64_t max_tokens, n_tokens;
+} kvq_chunk;
+
+/* Plans a chunk of n_new[b] (host int32 [B]) tokens for each slot.  A slot that is not
+ * active starts an empty sequence; one with n_new[b] = 0 stays as it is.  Extending slot b
+ * fills its sink first; of the residual's tokens followed by the rest of the chunk, whole
+ * groups of R are packed and the others form the new residual -- the state that n_new[b]
+ * times append and flush would leave.  The pages it packs are logical pages [T_b / G, ...)
+ * of the slot; if new_pages (device int32 [n_new_pages]) is given, their page-table rows
+ * are written from it, slot after slot in order; if it is NULL the caller maps them.
+ * Host data is read before the call returns.  KVQ_ERR_CAPACITY if the tokens exceed
+ * max_tokens, a slot exceeds max_T, or new_pages is too short; nothing is enqueued then.
+ * KVQ_ERR_UNSUPPORTED while `stream` is capturing (a replay would not advance the host
+ * lengths). */
+int kvq_paged_plan(const kvq_config *cfg, kvq_paged *pc, const int32_t *n_new, const int32_t *new_pages,
+                   int64_t n_new_pages, kvq_chunk *chunk, void *stream);
+
+/* Workspace bytes of kvq_paged_chunk_attn (0 for an unsupported cfg).  It needs no
+ * initialization, and calls that may overlap need one each. */
+size_t kvq_paged_chunk_workspace_bytes(const kvq_config *cfg);
+
+/* Attention of the chunk's tokens: for row i of slot b (its j-th new token, query head h)
+ *   out[i][h] = softmax_t( q[i][h] . K_t / sqrt(D) ) . V_t
+ * over the slot's cached tokens (sink, packed pages, residual) and its new tokens 0 .. j.
+ * q: device fp16 rows of H_q heads; k_new, v_new: rows of H_kv heads; out: device fp16
+ * [n_tokens][H_q][D], contiguous.  Rows of the tensors behind n_tokens are neither read
+ * nor written.  The cache is not changed.  Operands are fp16 (dequantized keys and values
+ * and softmax weights are rounded to it once), sums and softmax statistics fp32.
+ * KVQ_ERR_INVALID_ARG if the cache's lengths are not those of the plan. */
+int kvq_paged_chunk_attn(const kvq_config *cfg, const kvq_paged *pc, const kvq_chunk *chunk, const uint16_t *q,
+                         int64_t q_stride, const uint16_t *k_new, int64_t k_stride, const uint16_t *v_new,
+                         int64_t v_stride, uint16_t *out, void *ws, size_t ws_bytes, void *stream);
+
+/* The chunk's tokens enter the cache (see kvq_paged_plan): sink and residual rows are
+ * copied, whole groups quantized into the mapped pages with the codes and scales that
+ * kvq_paged_flush gives, and the lengths advance (host lengths at enqueue time).  Rows of
+ * the fp16 buffers behind the new lengths keep their values.  k_new, v_new as for
+ * kvq_paged_chunk_attn.  KVQ_ERR_INVALID_ARG if the cache's lengths are not those of the
+ * plan (so a plan extends a cache once); KVQ_ERR_UNSUPPORTED while `stream` is capturing. */
+int kvq_paged_extend(const kvq_config *cfg, kvq_paged *pc, const kvq_chunk *chunk, const uint16_t *k_new,
+                     int64_t k_stride, const uint16_t *v_new, int64_t v_stride, void *stream);
+
+/* Norm and rotation of new queries and keys.
+ *   H_q, H_kv, D   : heads and head dim (D 64, 128 or 256; either head count may be 0)
+ *   rotary_dim     : channels that rotate, the first ones of a head: a multiple of 16,
+ *                    0 <= rotary_dim <= D
+ *   halves         : 0: channel pairs (2j, 2j+1), as the keys of a pre-RoPE cache are
+ *                    paired; 1: pairs (j, j + rotary_dim/2)
+ *   rotate         : bit 0: rotate the queries, bit 1: rotate the keys (3: both; 1 for a
+ *                    cache that stores keys before RoPE)
+ *   eps, rope_base : of the norm; of the angles pos * rope_base^(-2j/rotary_dim)
+ *                    (10000 if 0)
+ *   q_stride, k_stride : elements between input rows                                   */
+typedef struct {
+    int32_t H_q, H_kv, D, rotary_dim, halves, rotate;
+    float eps, rope_base;
+    int64_t q_stride, k_stride;
+} kvq_qk_config;
+
+/* y = x / sqrt(mean(x^2) + eps) * w over each head's D channels (skipped where the weight
+ * pointer is NULL), then the rotation by pos[i], in fp32 with one rounding to fp16; angles
+ * are exact to 2^-31 turns at any position.  q, k: device fp16 rows (strides above); w_q,
+ * w_k: device fp16 [D] or NULL; pos: device int32 [n]; q_out, k_out: device fp16
+ * [n][H][D], contiguous.  An output may be its own input if that is contiguous; any other
+ * overlap of an output with an input or the other output is KVQ_ERR_INVALID_ARG. */
+int kvq_qk_norm_rope(const kvq_qk_config *c, const uint16_t *q, const uint16_t *k, const uint16_t *w_q,
+                     const uint16_t *w_k, const int32_t *pos, int64_t n, uint16_t *q_out, uint16_t *k_out,
+                     void *stream);
+
 /* Synchronizes `stream`, then returns in *dev_status the OR of the error bits the
  * kernels wrote into the workspace status word and into cache->status (if cache is
  * not NULL and its status pointer is set), and clears both.  KVQ_ERR_DEVICE if any
