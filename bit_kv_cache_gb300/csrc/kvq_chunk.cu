@@ -542,15 +542,13 @@ bool overlap(const void *a, size_t na, const void *b, size_t nb) {
     return x < y + nb && y < x + na;
 }
 
-// CTAs of the attention and its partials: two ranges' ends per CTA, 256 rows each.
-int chunk_ctas() { return 2 * num_sms(); }
-constexpr int kWsRows = 256;
+// Partials of the attention: two segments' ends per CTA.
 struct ChunkWs {
     size_t ml, o, total;
 };
 ChunkWs chunk_ws() {
     ChunkWs w;
-    const size_t slots = (size_t)2 * num_sms() * kWsRows;  // per CTA: 2 x 256 rows, or 4 x 128 ...
+    const size_t slots = (size_t)2 * num_sms() * kWideRows;  // rows: 2 x 256 per SM (narrow: 2 x 2 x 64)
     w.ml = 0;
     w.o = (slots * sizeof(float2) + 255) / 256 * 256;
     w.total = w.o + slots * 128 * sizeof(float);
@@ -666,21 +664,32 @@ int kvq_paged_chunk_attn(const kvq_config *c, const kvq_paged *pc, const kvq_chu
     p.S = c->S;
     p.R = c->R;
     p.ptab_stride = (int)(c->max_T / c->G);
-    const int rows = 64;
-    int64_t n = 0;
-    for (int b = 0; b < c->B; b++) {
-        const ChunkSlot &s = slots_of(ch)[b];
-        p.item0[b] = (int32_t)n;
-        int64_t per = 0;
-        const int64_t nt = cdiv((int64_t)s.n_new * p.g, rows);
-        for (int64_t t = 0; t < nt; t++) per += chunk_tiles(s, (int)t, rows, p.g);
-        n += per * p.H_kv;
-        if (n >= (1LL << 30)) return KVQ_ERR_UNSUPPORTED;
+    // slots of few query rows per key head and slots of many take a kernel each
+    ChunkAttnParams part[2];
+    for (int wide = 0; wide < 2; wide++) {
+        ChunkAttnParams &a = part[wide];
+        a = p;
+        const int rows = wide ? kWideRows : kNarrowRows;
+        int64_t n = 0;
+        for (int b = 0; b < c->B; b++) {
+            const ChunkSlot &s = slots_of(ch)[b];
+            a.item0[b] = (int32_t)n;
+            const int64_t r = (int64_t)s.n_new * p.g, nt = cdiv(r, rows);
+            if ((r > kNarrowRows) != (wide != 0)) continue;
+            int64_t per = 0;
+            for (int64_t t = 0; t < nt; t++) per += chunk_tiles(s, (int)t, rows, p.g);
+            n += per * p.H_kv;
+            if (n >= (1LL << 30)) return KVQ_ERR_UNSUPPORTED;
+        }
+        for (int b = c->B; b <= KVQ_PAGED_MAX_B; b++) a.item0[b] = (int32_t)n;
+        a.n_items = (int)n;
+        a.C = (int)std::min<int64_t>(n, wide ? num_sms() : 2 * num_sms());
     }
-    for (int b = c->B; b <= KVQ_PAGED_MAX_B; b++) p.item0[b] = (int32_t)n;
-    p.n_items = (int)n;
-    p.C = (int)std::min<int64_t>(n, chunk_ctas());
-    return status_of(launch_chunk_attn(p, rows, (cudaStream_t)stream));
+    for (int wide = 1; wide >= 0; wide--)
+        if (part[wide].n_items &&
+            launch_chunk_attn(part[wide], wide ? kWideRows : kNarrowRows, (cudaStream_t)stream) != cudaSuccess)
+            return KVQ_ERR_CUDA;
+    return KVQ_OK;
 }
 
 int kvq_paged_extend(const kvq_config *c, kvq_paged *pc, const kvq_chunk *ch, const uint16_t *kn, int64_t k_stride,

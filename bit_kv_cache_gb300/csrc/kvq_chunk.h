@@ -74,8 +74,10 @@ struct ChunkAttnParams {
 cudaError_t launch_plan(const PlanParams &p, cudaStream_t st);
 cudaError_t launch_extend(const ExtendParams &p, int kbits, int vbits, cudaStream_t st);
 cudaError_t launch_qk(const QkParams &p, int D, cudaStream_t st);
-// rows: query rows per unit (chunk_attn_rows); p.item0, n_items and C follow from it.
+// rows: query rows per unit, kNarrowRows or kWideRows; p.item0, n_items and C follow from it.
 cudaError_t launch_chunk_attn(const ChunkAttnParams &p, int rows, cudaStream_t st);
+cudaError_t launch_chunk_wide(const ChunkAttnParams &p, cudaStream_t st);
+constexpr int kNarrowRows = 64, kWideRows = 256;
 
 constexpr int kChunkKeys = 128;          // tokens per key tile
 
