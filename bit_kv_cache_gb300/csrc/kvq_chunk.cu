@@ -797,10 +797,11 @@ int kvq_qk_norm_rope(const kvq_qk_config *c, const uint16_t *q, const uint16_t *
     p.rotate = c->rotary_dim ? c->rotate : 0;
     p.eps = c->eps;
     const long double base = c->rope_base > 0.f ? (long double)c->rope_base : 10000.0L;
-    for (int j = 0; j < c->rotary_dim / 2; j++) {
-        const long double turn = powl(base, -2.0L * j / c->rotary_dim) / 6.283185307179586476925286766559L;
-        p.turn[j] = (uint64_t)ldexpl(turn - floorl(turn), 64);
-    }
+    // one power, then products: a call's host time is a fraction of that of a power per pair,
+    // and each product adds half a step of a long double (2^-64 or less) at most
+    const long double step = c->rotary_dim ? powl(base, -2.0L / c->rotary_dim) : 0.0L;
+    long double turn = 0.159154943091895335768883763372514362L;  // 1 / (2 pi)
+    for (int j = 0; j < c->rotary_dim / 2; j++, turn *= step) p.turn[j] = (uint64_t)ldexpl(turn - floorl(turn), 64);
     return status_of(launch_qk(p, c->D, (cudaStream_t)stream));
 }
 

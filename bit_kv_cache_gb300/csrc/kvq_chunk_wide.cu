@@ -1,14 +1,14 @@
 // kvq_chunk_wide.cu -- chunk attention for many query rows per slot: 256 rows per unit on
 // the 5th-generation tensor cores.
 //
-// One CTA per SM, sixteen warps in four groups of four:
+// One CTA per SM, five groups of four warps:
 //   groups 0, 1  softmax of query tile m = 0, 1 (128 rows each, a thread per row): reads
 //                the scores S_m from tensor memory, keeps the row's running maximum and sum
 //                in registers, writes the weights P_m over S_m as fp16, rescales O_m when
 //                the maximum has grown by more than 2^8;
-//   group 2      makes the key and value tiles: packed pages arrive by bulk copies and are
-//                dequantized into fp16 tiles in shared memory, fp16 rows are gathered;
-//   warp 12      issues the products S_m = Q_m K^T and O_m += P_m V.
+//   groups 2, 3  make the key and the value tiles: packed pages arrive by bulk copies and
+//                are dequantized into fp16 tiles in shared memory, fp16 rows are gathered;
+//   warp 16      issues the products S_m = Q_m K^T and O_m += P_m V.
 // The two query tiles alternate on the tensor core: while one's scores are in softmax, the
 // other's products run; a key tile is dequantized once for both.  Tensor memory holds S_0,
 // S_1, O_0, O_1 (128 columns each).
@@ -23,7 +23,7 @@ namespace kvq {
 
 namespace {
 
-constexpr int kRows = 256, kThreads = 512;
+constexpr int kRows = 256, kThreads = 640, kMulThread = 512;
 constexpr int kTileBytes = kChunkKeys * kD * 2;          // an fp16 key or value tile: 32 KB
 constexpr int kRing = 2;                                 // tiles of each kind
 constexpr int kRawBytes = 2 * (16384 + 512);             // packed tiles: codes and (scale, min)
@@ -34,8 +34,9 @@ constexpr float kScale = kLog2e * 0.08838834764831845f;  // log2(e) / sqrt(128)
 // Weights are 2^(s - m + kUp): the running maximum may lag by kLag, so they stay below
 // 2^(kUp + kLag) < 65504, and small ones keep kUp more bits above fp16's smallest step.
 constexpr float kUp = 6.f, kLag = 8.f;
-constexpr int kRegsSoftmax = 168, kRegsOther = 88;
-static_assert(256 * kRegsSoftmax + 256 * kRegsOther <= 65536 && kThreads * 128 == 65536, "register split");
+// registers of a thread after the split; 96 at launch, times 640 threads
+constexpr int kRegsSoftmax = 144, kRegsTiles = 72, kRegsMul = 48;
+static_assert(256 * kRegsSoftmax + 256 * kRegsTiles + 128 * kRegsMul <= kThreads * 96, "register split");
 
 struct Bars {
     uint64_t q_full, q_empty, k_full[kRing], k_empty[kRing], v_full[kRing], v_empty[kRing];
@@ -70,104 +71,71 @@ __device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
     asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
     return r;
 }
-// Two codes in place (bits sh .. sh + BITS - 1 of each half) -> code * scale + min.  With
-// the exponent of 1024 above them the halves are 1024 + code 2^sh; one fused step makes the
-// exact code of it, another the value, rounded once.
-template <int SH, uint32_t MASK>
-__device__ __forceinline__ uint32_t deq2(uint32_t w, uint32_t s2, uint32_t m2) {
-    const uint32_t v = (w & (MASK << SH)) | 0x64006400u;
-    constexpr uint32_t mul = (uint32_t)(0x3c00 - (SH << 10)) * 0x10001u;            // 2^-SH
-    constexpr uint32_t sub = (uint32_t)(0xe400 - (SH << 10)) * 0x10001u;            // -1024 2^-SH
-    return hfma2(hfma2(v, mul, sub), s2, m2);
-}
-// The codes of one word as half2 pairs (j, j + n/2), n = 32 / BITS codes.
+// A code's bits under the exponent of 1024 make 1024 + code 2^sh; one fused step makes the
+// exact code of it, another code * scale + min, rounded once.
+// A packed tile becomes an fp16 operand whose rows run along the packed direction (keys: a
+// row per token, channels contiguous; values: a row per channel, tokens contiguous).  A job
+// is one word row m and eight neighbouring columns: words w of two columns are split into
+// halves (the codes of the rows' first and second half, in pairs of columns), so that every
+// row is four half2, one 16-byte store.  wd: the eight words; s2, m2: (scale, min) of the
+// column pairs; dst: row 0 of the job at its 16-byte chunk, which row r xors with r mod 8.
 template <int BITS>
-__device__ __forceinline__ void deq_word(uint32_t w, uint32_t s2, uint32_t m2, uint32_t *h) {
-    if (BITS == 2) {
-        h[0] = deq2<0, 0x00030003u>(w, s2, m2);
-        h[1] = deq2<2, 0x00030003u>(w, s2, m2);
-        h[2] = deq2<4, 0x00030003u>(w, s2, m2);
-        h[3] = deq2<6, 0x00030003u>(w, s2, m2);
-        h[4] = deq2<8, 0x00030003u>(w, s2, m2);
-        w >>= 10;
-        h[5] = deq2<0, 0x00030003u>(w, s2, m2);
-        h[6] = deq2<2, 0x00030003u>(w, s2, m2);
-        h[7] = deq2<4, 0x00030003u>(w, s2, m2);
-    } else if (BITS == 4) {
-        h[0] = deq2<0, 0x000f000fu>(w, s2, m2);
-        h[1] = deq2<4, 0x000f000fu>(w, s2, m2);
-        w >>= 8;
-        h[2] = deq2<0, 0x000f000fu>(w, s2, m2);
-        h[3] = deq2<4, 0x000f000fu>(w, s2, m2);
-    } else {
-        h[0] = deq2<0, 0x00ff00ffu>(w, s2, m2);
-        w >>= 8;
-        h[1] = deq2<0, 0x00ff00ffu>(w, s2, m2);
-    }
-}
-// Position of token t within a packed tile: the pairs (j, j + n/2) of a key word side by side.
-__device__ __forceinline__ int token_at(int pos, int kbits) {  // its inverse
-    const int n = 32 / kbits, i = pos & (n - 1);
-    return (pos & ~(n - 1)) + (i >> 1) + (n >> 1) * (i & 1);
-}
-
-// Keys: thread d dequantizes channel d.  Tile: rows are channels, tokens contiguous (two
-// blocks of 64 tokens), so that a word's tokens are one or two 16-byte stores.
-template <int BITS>
-__device__ __forceinline__ void make_keys(const unsigned char *raw, unsigned char *tile, int d) {
-    const uint32_t *cw = reinterpret_cast<const uint32_t *>(raw);
-    const uint32_t sm = cw[512 * BITS + d];
-    const uint32_t s2 = prmt(sm, sm, 0x1010), m2 = prmt(sm, sm, 0x3232);
-    unsigned char *row = tile + d * 128;
-    constexpr int NR = 4 * BITS;  // word rows of a tile
-#pragma unroll 8
-    for (int r = 0; r < NR; r += (BITS == 8 ? 2 : 1)) {
-        uint32_t h[8];
-        deq_word<BITS>(cw[r * kD + (d ^ ((r & 7) << 2))], s2, m2, h);
-        if (BITS == 2) {
-            unsigned char *b = row + (r >> 2) * 16384;
-            const int c = 2 * (r & 3);
-            *reinterpret_cast<uint4 *>(b + ((c ^ (d & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
-            *reinterpret_cast<uint4 *>(b + (((c + 1) ^ (d & 7)) << 4)) = make_uint4(h[4], h[5], h[6], h[7]);
-        } else if (BITS == 4) {
-            *reinterpret_cast<uint4 *>(row + (r >> 3) * 16384 + (((r & 7) ^ (d & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
-        } else {
-            deq_word<BITS>(cw[(r + 1) * kD + (d ^ (((r + 1) & 7) << 2))], s2, m2, h + 2);
-            *reinterpret_cast<uint4 *>(row + (r >> 4) * 16384 + ((((r >> 1) & 7) ^ (d & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+__device__ __forceinline__ void deq_job(const uint32_t (&wd)[8], const uint32_t (&s2)[4], const uint32_t (&m2)[4], uint32_t dst) {
+    constexpr int N = 32 / BITS;                       // rows
+    constexpr uint32_t MASK = ((1u << BITS) - 1u) * 0x10001u;
+    constexpr int FIT = BITS == 2 ? 5 : BITS == 4 ? 2 : 1;  // codes of a half below bit 10
+#pragma unroll
+    for (int hf = 0; hf < 2; hf++) {
+        uint32_t x[4];
+#pragma unroll
+        for (int c = 0; c < 4; c++) x[c] = prmt(wd[2 * c], wd[2 * c + 1], hf ? 0x7632 : 0x5410);
+#pragma unroll
+        for (int j = 0; j < N / 2; j++) {
+            uint32_t y[4];
+#pragma unroll
+            for (int c = 0; c < 4; c++) {
+                if (j > 0 && j % FIT == 0) x[c] >>= FIT * BITS;
+                const uint32_t v = (x[c] & (MASK << (j % FIT * BITS))) | 0x64006400u;
+                const uint32_t mul = (uint32_t)(0x3c00 - ((j % FIT * BITS) << 10)) * 0x10001u;  // 2^-sh
+                const uint32_t sub = (uint32_t)(0xe400 - ((j % FIT * BITS) << 10)) * 0x10001u;  // -1024 2^-sh
+                y[c] = hfma2(hfma2(v, mul, sub), s2[c], m2[c]);
+            }
+            const int r = hf * (N / 2) + j;
+            const uint32_t at = (dst ^ ((r & 7) << 4)) + r * 128;
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3]) : "memory");
         }
     }
 }
 
-// Values: thread p dequantizes the token at position p.  Tile: rows are token positions,
-// channels contiguous (two blocks of 64 channels), in their natural order.
+__device__ __forceinline__ void lds128(uint32_t *r, uint32_t addr) {
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
+}
+
+// raw: codes [4 BITS word rows][128 columns] (values: tiles of TV columns, [rows][TV] each),
+// then 128 (scale, min).  Thread t takes columns 8 (t mod 16) .. + 7 of word rows t / 16 + 8 i.
 template <int BITS>
-__device__ __forceinline__ void make_values(const unsigned char *raw, unsigned char *tile, int p, int kbits) {
-    const uint32_t *cw = reinterpret_cast<const uint32_t *>(raw);
-    const int t = token_at(p, kbits), TV = 256 / kbits, j = t & (TV - 1);
-    constexpr int NR = 4 * BITS;  // word rows of a token
-    const uint32_t sm = cw[512 * BITS + t];
-    const uint32_t s2 = prmt(sm, sm, 0x1010), m2 = prmt(sm, sm, 0x3232);
-    cw += (t - j) * NR;           // value tile of the token: [NR][TV]
-    unsigned char *row = tile + p * 128;
-#pragma unroll 8
-    for (int m = 0; m < NR; m += (BITS == 8 ? 2 : 1)) {
-        uint32_t h[8];
-        deq_word<BITS>(cw[m * TV + (j ^ ((m & 7) << 2))], s2, m2, h);
-        if (BITS == 2) {
-            unsigned char *b = row + (m >> 2) * 16384;
-            const int c = 2 * (m & 3);
-            *reinterpret_cast<uint4 *>(b + ((c ^ (p & 7)) << 4)) = make_uint4(prmt(h[0], h[1], 0x5410), prmt(h[2], h[3], 0x5410),
-                                                                            prmt(h[4], h[5], 0x5410), prmt(h[6], h[7], 0x5410));
-            *reinterpret_cast<uint4 *>(b + (((c + 1) ^ (p & 7)) << 4)) = make_uint4(
-                prmt(h[0], h[1], 0x7632), prmt(h[2], h[3], 0x7632), prmt(h[4], h[5], 0x7632), prmt(h[6], h[7], 0x7632));
-        } else if (BITS == 4) {
-            *reinterpret_cast<uint4 *>(row + (m >> 3) * 16384 + (((m & 7) ^ (p & 7)) << 4)) =
-                make_uint4(prmt(h[0], h[1], 0x5410), prmt(h[2], h[3], 0x5410), prmt(h[0], h[1], 0x7632), prmt(h[2], h[3], 0x7632));
-        } else {
-            deq_word<BITS>(cw[(m + 1) * TV + (j ^ (((m + 1) & 7) << 2))], s2, m2, h + 2);
-            *reinterpret_cast<uint4 *>(row + (m >> 4) * 16384 + ((((m >> 1) & 7) ^ (p & 7)) << 4)) =
-                make_uint4(prmt(h[0], h[1], 0x5410), prmt(h[0], h[1], 0x7632), prmt(h[2], h[3], 0x5410), prmt(h[2], h[3], 0x7632));
-        }
+__device__ __forceinline__ void make_tile(uint32_t raw, uint32_t tile, int t, int TV) {
+    const int c0 = 8 * (t & 15), m0 = t >> 4;
+    constexpr int N = 32 / BITS, NR = 4 * BITS;
+    uint32_t mt[8], s2[4], m2[4];
+    lds128(mt, raw + 4 * (512 * BITS + c0));
+    lds128(mt + 4, raw + 4 * (512 * BITS + c0) + 16);
+#pragma unroll
+    for (int c = 0; c < 4; c++) {
+        s2[c] = prmt(mt[2 * c], mt[2 * c + 1], 0x5410);
+        m2[c] = prmt(mt[2 * c], mt[2 * c + 1], 0x7632);
+    }
+    const int j = c0 & (TV - 1);
+    const uint32_t src = raw + 4 * ((c0 - j) * NR);
+#pragma unroll
+    for (int i = 0; i < NR / 8; i++) {
+        const int m = m0 + 8 * i;
+        uint32_t wd[8];  // the row's 16-byte chunks are permuted by xor with m mod 8
+        lds128(wd, src + 4 * (m * TV + (j ^ ((m & 7) << 2))));
+        lds128(wd + 4, src + 4 * (m * TV + ((j + 4) ^ ((m & 7) << 2))));
+        // row N m; N is a multiple of 4: for 8-bit codes an odd word row starts inside an atom
+        const uint32_t row = tile + (c0 >> 6) * 16384 + m * N * 128 + ((((c0 >> 3) & 7) ^ ((m * N) & 7)) << 4);
+        deq_job<BITS>(wd, s2, m2, row);
     }
 }
 
@@ -196,33 +164,31 @@ __device__ __forceinline__ bool make_tail(const ChunkAttnParams &p, const Seg &s
     return bad;
 }
 
-// ---------------------------------------------------------------- group 2: tiles ------
+// ---------------------------------------------------------------- groups 2, 3: tiles --
+template <bool VALUE>
 __device__ __forceinline__ void produce(const ChunkAttnParams &p, unsigned char *sm, Bars *bar, int begin, int end) {
-    const int tid = threadIdx.x & 127;
-    const int kraw = 2048 * p.kbits + 512, vraw = 2048 * p.vbits + 512;
+    const int tid = threadIdx.x & 127, bits = VALUE ? p.vbits : p.kbits;
+    const int kraw = 2048 * p.kbits + 512, vraw = 2048 * p.vbits + 512, size = VALUE ? vraw : kraw;
     const uint32_t slots = min(kMaxRaw, kRawBytes / (kraw + vraw));
-    unsigned char *raw_k = sm + kOffRaw, *raw_v = raw_k + slots * kraw;
-    uint32_t nk = 0, nv = 0;              // tiles made
-    uint32_t ck = 0, cv = 0, ik = 0, iv = 0;  // packed tiles consumed, copies issued (of keys, values)
-    uint32_t nq = 0;
-    // the copies of packed tile kt (thread 0)
-    auto copy_k = [&](const Seg &s, int kt) {
+    unsigned char *raw = sm + kOffRaw + (VALUE ? slots * kraw : 0);
+    unsigned char *ring = sm + (VALUE ? kOffV : kOffK);
+    uint64_t *arrived = VALUE ? bar->rawv : bar->rawk, *read = VALUE ? bar->readv : bar->readk;
+    uint64_t *full = VALUE ? bar->v_full : bar->k_full, *empty = VALUE ? bar->v_empty : bar->k_empty;
+    const int32_t *codes = VALUE ? p.v_codes : p.k_codes;
+    const uint16_t *meta = VALUE ? p.v_meta : p.k_meta;
+    uint32_t n = 0, c = 0, i = 0, nq = 0;  // tiles made, packed tiles read, copies issued, query tiles
+    // thread 0: the copies of packed tile kt, once the slot's last tile has been read
+    auto copy = [&](const Seg &s, int kt) {
+        const uint32_t sl = i % slots;
+        if (i >= slots && !wait_or_stop(&read[sl], (i / slots - 1) & 1, &bar->stop, p.status)) return false;
         const int64_t page = page_of(p, s.it, kt);
-        const int t0 = kt * kChunkKeys & (p.G - 1), sl = ik % slots;
-        unsigned char *dst = raw_k + sl * kraw;
-        mbar_arrive_expect_tx(&bar->rawk[sl], kraw);
-        bulk_g2s(dst, p.k_codes + ((size_t)page * p.G + t0) * (kD * p.kbits / 32), 2048 * p.kbits, &bar->rawk[sl]);
-        bulk_g2s(dst + 2048 * p.kbits, p.k_meta + (size_t)page * kD * 2, 512, &bar->rawk[sl]);
-        ik++;
-    };
-    auto copy_v = [&](const Seg &s, int kt) {
-        const int64_t page = page_of(p, s.it, kt);
-        const int t0 = kt * kChunkKeys & (p.G - 1), sl = iv % slots;
-        unsigned char *dst = raw_v + sl * vraw;
-        mbar_arrive_expect_tx(&bar->rawv[sl], vraw);
-        bulk_g2s(dst, p.v_codes + ((size_t)page * p.G + t0) * (kD * p.vbits / 32), 2048 * p.vbits, &bar->rawv[sl]);
-        bulk_g2s(dst + 2048 * p.vbits, p.v_meta + ((size_t)page * p.G + t0) * 2, 512, &bar->rawv[sl]);
-        iv++;
+        const int t0 = kt * kChunkKeys & (p.G - 1);
+        unsigned char *dst = raw + sl * size;
+        mbar_arrive_expect_tx(&arrived[sl], size);
+        bulk_g2s(dst, codes + ((size_t)page * p.G + t0) * (kD * bits / 32), 2048 * bits, &arrived[sl]);
+        bulk_g2s(dst + 2048 * bits, meta + (VALUE ? ((size_t)page * p.G + t0) * 2 : (size_t)page * kD * 2), 512, &arrived[sl]);
+        i++;
+        return true;
     };
     auto run = [&]() {
         int seg = 0;
@@ -230,107 +196,84 @@ __device__ __forceinline__ void produce(const ChunkAttnParams &p, unsigned char 
             const Seg s = next_seg(p, at, end);
             const int npk = min(s.k1, s.np);
             if (tid == 0)
-                for (int kt = s.k0; kt < min(npk, s.k0 + (int)slots); kt++) {
-                    // the slots' last readers were in the segment before
-                    if (ik >= slots && !wait_or_stop(&bar->readk[ik % slots], (ik / slots - 1) & 1, &bar->stop, p.status)) return;
-                    copy_k(s, kt);
-                    if (iv >= slots && !wait_or_stop(&bar->readv[iv % slots], (iv / slots - 1) & 1, &bar->stop, p.status)) return;
-                    copy_v(s, kt);
-                }
-            // queries: 128-row tiles, rows of tokens' heads; rows behind the last one repeat it
-            if (!wait_or_stop(&bar->q_empty, (nq & 1) ^ 1, &bar->stop, p.status)) return;
-            nq++;
-            {
-                const int c = tid & 15, rows = s.valid > 128 ? 256 : 128;
+                for (int kt = s.k0; kt < min(npk, s.k0 + (int)slots); kt++)
+                    if (!copy(s, kt)) return;
+            if (VALUE) {
+                // queries: 128-row tiles, rows of tokens' heads; rows behind the last one repeat it
+                if (!wait_or_stop(&bar->q_empty, (nq & 1) ^ 1, &bar->stop, p.status)) return;
+                nq++;
+                const int ch = tid & 15, rows = s.valid > 128 ? 256 : 128;
 #pragma unroll 4
                 for (int r = tid >> 4; r < rows; r += 8) {
                     const int x = s.it.t * kRows + min(r, s.valid - 1);
                     const uint4 a = __ldg(reinterpret_cast<const uint4 *>(p.q + (int64_t)(s.it.s.cu + x / p.g) * p.q_stride +
-                                                                          (s.it.h * p.g + x % p.g) * kD) + c);
-                    *reinterpret_cast<uint4 *>(sm + kOffQ + (r >> 7) * kTileBytes + (c >> 3) * 16384 + (r & 127) * 128 +
-                                               (((c & 7) ^ (r & 7)) << 4)) = a;
+                                                                          (s.it.h * p.g + x % p.g) * kD) + ch);
+                    *reinterpret_cast<uint4 *>(sm + kOffQ + (r >> 7) * kTileBytes + (ch >> 3) * 16384 + (r & 127) * 128 +
+                                               (((ch & 7) ^ (r & 7)) << 4)) = a;
                 }
                 fence_proxy_async();
                 mbar_arrive(&bar->q_full);
             }
             for (int kt = s.k0; kt < s.k1; kt++) {
-                const int ks = nk % kRing, vs = nv % kRing;
-                unsigned char *kt_ = sm + kOffK + ks * kTileBytes, *vt_ = sm + kOffV + vs * kTileBytes;
-                if (!wait_or_stop(&bar->k_empty[ks], ((nk / kRing) & 1) ^ 1, &bar->stop, p.status)) return;
-                nk++;
+                const uint32_t st = n % kRing;
+                unsigned char *tile = ring + st * kTileBytes;
+                if (!wait_or_stop(&empty[st], ((n / kRing) & 1) ^ 1, &bar->stop, p.status)) return;
+                n++;
                 if (kt < s.np) {
-                    const int sl = ck % slots;
-                    if (!wait_or_stop(&bar->rawk[sl], (ck / slots) & 1, &bar->stop, p.status)) return;
-                    ck++;
-                    const unsigned char *raw = raw_k + sl * kraw;
-                    if (p.kbits == 2) make_keys<2>(raw, kt_, tid);
-                    else if (p.kbits == 4) make_keys<4>(raw, kt_, tid);
-                    else make_keys<8>(raw, kt_, tid);
+                    const uint32_t sl = c % slots;
+                    if (!wait_or_stop(&arrived[sl], (c / slots) & 1, &bar->stop, p.status)) return;
+                    c++;
+                    const uint32_t src = smem_u32(raw + sl * size), dst = smem_u32(tile);
+                    const int TV = VALUE ? 256 / p.kbits : kChunkKeys;
+                    if (bits == 2) make_tile<2>(src, dst, tid, TV);
+                    else if (bits == 4) make_tile<4>(src, dst, tid, TV);
+                    else make_tile<8>(src, dst, tid, TV);
+                    fence_proxy_async();
+                    mbar_arrive(&full[st]);
+                    mbar_arrive(&read[sl]);
+                    if (tid == 0 && kt + (int)slots < npk && !copy(s, kt + (int)slots)) return;
                 } else {
-                    make_tail(p, s, (kt - s.np) * kChunkKeys, false, kt_, tid);
-                }
-                fence_proxy_async();
-                mbar_arrive(&bar->k_full[ks]);
-                if (kt < s.np) {
-                    const int sl = (ck - 1) % slots;
-                    mbar_arrive(&bar->readk[sl]);
-                    if (tid == 0 && kt + (int)slots < npk) {  // the next copy into this slot
-                        if (!wait_or_stop(&bar->readk[sl], ((ck - 1) / slots) & 1, &bar->stop, p.status)) return;
-                        copy_k(s, kt + (int)slots);
+                    if (make_tail(p, s, (kt - s.np) * kChunkKeys, VALUE, tile, tid)) {
+                        // infinite and NaN values enter the product as 0 (0 weights of rows that may
+                        // not see them would spread them) and are added to their rows at the end
+                        *(volatile int *)&bar->odd[seg & 3] = seg + 1;
                     }
-                }
-                if (!wait_or_stop(&bar->v_empty[vs], ((nv / kRing) & 1) ^ 1, &bar->stop, p.status)) return;
-                nv++;
-                if (kt < s.np) {
-                    const int sl = cv % slots;
-                    if (!wait_or_stop(&bar->rawv[sl], (cv / slots) & 1, &bar->stop, p.status)) return;
-                    cv++;
-                    const unsigned char *raw = raw_v + sl * vraw;
-                    if (p.vbits == 2) make_values<2>(raw, vt_, tid, p.kbits);
-                    else if (p.vbits == 4) make_values<4>(raw, vt_, tid, p.kbits);
-                    else make_values<8>(raw, vt_, tid, p.kbits);
-                } else if (make_tail(p, s, (kt - s.np) * kChunkKeys, true, vt_, tid)) {
-                    // infinite and NaN values enter the product as 0 (0 weights of rows that may
-                    // not see them would spread them) and are added to their rows at the end
-                    *(volatile int *)&bar->odd[seg & 3] = seg + 1;
-                }
-                fence_proxy_async();
-                mbar_arrive(&bar->v_full[vs]);
-                if (kt < s.np) {
-                    const int sl = (cv - 1) % slots;
-                    mbar_arrive(&bar->readv[sl]);
-                    if (tid == 0 && kt + (int)slots < npk) {  // the next copy into this slot
-                        if (!wait_or_stop(&bar->readv[sl], ((cv - 1) / slots) & 1, &bar->stop, p.status)) return;
-                        copy_v(s, kt + (int)slots);
-                    }
+                    fence_proxy_async();
+                    mbar_arrive(&full[st]);
                 }
             }
             at = s.first + s.k1;
         }
     };
     run();
-    if (tid == 0) {  // copies still in flight after an early end
-        for (; ck < ik; ck++) mbar_wait(&bar->rawk[ck % slots], (ck / slots) & 1, p.status);
-        for (; cv < iv; cv++) mbar_wait(&bar->rawv[cv % slots], (cv / slots) & 1, p.status);
-    }
+    if (tid == 0)  // copies still in flight after an early end
+        for (; c < i; c++) mbar_wait(&arrived[c % slots], (c / slots) & 1, p.status);
 }
 
-// ---------------------------------------------------------------- warp 12: products ---
+// ---------------------------------------------------------------- warp 16: products ---
 __device__ __forceinline__ void multiply(const ChunkAttnParams &p, unsigned char *sm, Bars *bar, uint32_t tm, int begin, int end) {
     const uint32_t base = smem_u32(sm);
     uint32_t nk = 0, nv = 0, nq = 0, np_[2] = {0, 0};
-    auto scores = [&](int m, int ks, bool packed) {
-        const uint64_t a0 = smem_desc(base + kOffQ + m * kTileBytes, 16, 1024);
-        const uint32_t kb = base + kOffK + ks * kTileBytes;
-        const uint64_t b0 = packed ? smem_desc(kb, 16384, 1024) : smem_desc(kb, 16, 1024);
-        const uint32_t id = packed ? f16_idesc(128, 128, true) : f16_idesc(128, 128, false);
+    // Rows along M and N (keys: tokens, packed values: channels): 16 of the contracted
+    // dimension are 32 bytes of a row; fp16 value rows run along the tokens: 16 are two atoms.
+    auto scores = [&](int m, int ks) {
+        const uint64_t a0 = smem_desc(base + kOffQ + m * kTileBytes, 16, 1024), b0 = smem_desc(base + kOffK + ks * kTileBytes, 16, 1024);
 #pragma unroll
-        for (int k = 0; k < 8; k++) {  // 16 channels each
-            const uint64_t a = a0 + (((k >> 2) * 16384 + (k & 3) * 32) >> 4);
-            const uint64_t b = b0 + (packed ? (k * 2048) >> 4 : ((k >> 2) * 16384 + (k & 3) * 32) >> 4);
-            mma_ss(tm + m * 128, a, b, id, k > 0);
+        for (int k = 0; k < 8; k++) {
+            const uint32_t off = ((k >> 2) * 16384 + (k & 3) * 32) >> 4;
+            mma_ss(tm + m * 128, a0 + off, b0 + off, f16_idesc(128, 128, false), k > 0);
         }
         tc_commit(&bar->s_full[m]);
+    };
+    auto weigh = [&](int m, int vs, bool packed, bool acc) {
+        const uint32_t vb = base + kOffV + vs * kTileBytes;
+        const uint64_t b0 = packed ? smem_desc(vb, 16, 1024) : smem_desc(vb, 16384, 1024);
+        const uint32_t id = packed ? f16_idesc(128, 128, false) : f16_idesc(128, 128, true);
+#pragma unroll
+        for (int k = 0; k < 8; k++) {
+            const uint32_t off = (packed ? (k >> 2) * 16384 + (k & 3) * 32 : k * 2048) >> 4;
+            mma_ts(tm + 256 + m * 128, tm + m * 128 + 8 * k, b0 + off, id, acc || k > 0);
+        }
     };
     auto run = [&]() {
         for (int at = begin; at < end;) {
@@ -340,7 +283,7 @@ __device__ __forceinline__ void multiply(const ChunkAttnParams &p, unsigned char
             nq++;
             if (!wait_or_stop(&bar->k_full[nk % kRing], (nk / kRing) & 1, &bar->stop, p.status)) return;
             tc_fence_after();
-            for (int m = 0; m < M; m++) scores(m, nk % kRing, s.k0 < s.np);
+            for (int m = 0; m < M; m++) scores(m, nk % kRing);
             tc_commit(&bar->k_empty[nk % kRing]);
             nk++;
             if (n == 1) tc_commit(&bar->q_empty);
@@ -351,16 +294,13 @@ __device__ __forceinline__ void multiply(const ChunkAttnParams &p, unsigned char
                     if (!wait_or_stop(&bar->p_full[m], np_[m] & 1, &bar->stop, p.status)) return;
                     np_[m]++;
                     tc_fence_after();
-                    const uint64_t b0 = smem_desc(base + kOffV + vs * kTileBytes, 16384, 1024);
-#pragma unroll
-                    for (int k = 0; k < 8; k++)  // 16 tokens each
-                        mma_ts(tm + 256 + m * 128, tm + m * 128 + 8 * k, b0 + ((k * 2048) >> 4), f16_idesc(128, 128, true), j > 0 || k > 0);
+                    weigh(m, vs, s.k0 + j < s.np, j > 0);
                     if (j + 1 < n) {
                         if (m == 0) {
                             if (!wait_or_stop(&bar->k_full[nk % kRing], (nk / kRing) & 1, &bar->stop, p.status)) return;
                             tc_fence_after();
                         }
-                        scores(m, nk % kRing, s.k0 + j + 1 < s.np);
+                        scores(m, nk % kRing);
                     } else {
                         tc_commit(&bar->o_full[m]);
                     }
@@ -382,6 +322,42 @@ __device__ __forceinline__ void multiply(const ChunkAttnParams &p, unsigned char
 }
 
 // ---------------------------------------------------------------- groups 0, 1 ---------
+// Scores of 32 keys: those from the n-th on are not seen.
+__device__ __forceinline__ void mask_keys(uint32_t *x, int n) {
+    if (n < 32) {
+#pragma unroll
+        for (int c = 0; c < 32; c++)
+            if (c >= n) x[c] = 0xff800000u;
+    }
+}
+__device__ __forceinline__ float max64(const float *f) {
+    float t[8];
+#pragma unroll
+    for (int e = 0; e < 8; e++) t[e] = f[e];
+#pragma unroll
+    for (int c = 8; c < 64; c += 8)
+#pragma unroll
+        for (int e = 0; e < 8; e++) t[e] = fmaxf(t[e], f[c + e]);
+    return fmaxf(fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])), fmaxf(fmaxf(t[4], t[5]), fmaxf(t[6], t[7])));
+}
+// Weights 2^(s scale + off) of 32 scores, as 16 half2 in place; their sums to l0 and l1.
+__device__ __forceinline__ void weights32(uint32_t *x, float off, uint64_t &l0, uint64_t &l1) {
+    const uint64_t sc2 = pair_of(kScale, kScale), of2 = pair_of(off, off);
+    const float *f = reinterpret_cast<const float *>(x);
+#pragma unroll
+    for (int c = 0; c < 32; c += 4) {
+        float2 a = of_pair(fma_pair(pair_of(f[c], f[c + 1]), sc2, of2)), b = of_pair(fma_pair(pair_of(f[c + 2], f[c + 3]), sc2, of2));
+        a.x = ex2(a.x);
+        a.y = ex2(a.y);
+        b.x = ex2(b.x);
+        b.y = ex2(b.y);
+        l0 = add_pair(l0, pair_of(a.x, a.y));
+        l1 = add_pair(l1, pair_of(b.x, b.y));
+        x[c >> 1] = pack_half2(a.x, a.y);
+        x[(c >> 1) + 1] = pack_half2(b.x, b.y);
+    }
+}
+
 __device__ __forceinline__ void softmax(const ChunkAttnParams &p, Bars *bar, uint32_t tm, int m, int begin, int end) {
     const int lane = threadIdx.x & 31, row = 128 * m + (threadIdx.x & 127);
     const uint32_t lanes = (uint32_t)(threadIdx.x & 96) << 16;
@@ -400,30 +376,22 @@ __device__ __forceinline__ void softmax(const ChunkAttnParams &p, Bars *bar, uin
             if (!warp_wait_or_stop(&bar->s_full[m], ns & 1, &bar->stop, p.status)) return;
             ns++;
             tc_fence_after();
-            uint32_t x[128];
+            // maximum over the row; the first half stays in registers, the second is read again
+            const int y = kt >= s.np ? lim - (kt - s.np) * kChunkKeys : kChunkKeys;  // keys it may see
+            uint32_t x[64];
+            float cand = -INFINITY;
 #pragma unroll
-            for (int c = 0; c < 4; c++) tmem_ld32(x + 32 * c, ts + 32 * c);
-            tmem_wait_ld();
+            for (int hf = 1; hf >= 0; hf--) {
+                tmem_ld32(x, ts + 64 * hf);
+                tmem_ld32(x + 32, ts + 64 * hf + 32);
+                tmem_wait_ld();
 #pragma unroll
-            for (int c = 0; c < 8; c++) tmem_tie16(x + 16 * c);
-            float *f = reinterpret_cast<float *>(x);
-            if (kt >= s.np) {
-                const int y = lim - (kt - s.np) * kChunkKeys;
-                if (y < kChunkKeys) {
-#pragma unroll
-                    for (int c = 0; c < 128; c++)
-                        if (c >= y) f[c] = -INFINITY;
-                }
+                for (int c = 0; c < 4; c++) tmem_tie16(x + 16 * c);
+                mask_keys(x, y - 64 * hf);
+                mask_keys(x + 32, y - 64 * hf - 32);
+                cand = fmaxf(cand, max64(reinterpret_cast<const float *>(x)));
             }
-            float t0 = fmaxf(f[0], f[1]), t1 = fmaxf(f[2], f[3]), t2 = fmaxf(f[4], f[5]), t3 = fmaxf(f[6], f[7]);
-#pragma unroll
-            for (int c = 8; c < 128; c += 8) {
-                t0 = fmaxf(t0, fmaxf(f[c], f[c + 1]));
-                t1 = fmaxf(t1, fmaxf(f[c + 2], f[c + 3]));
-                t2 = fmaxf(t2, fmaxf(f[c + 4], f[c + 5]));
-                t3 = fmaxf(t3, fmaxf(f[c + 6], f[c + 7]));
-            }
-            const float cand = fmaxf(fmaxf(t0, t1), fmaxf(t2, t3)) * kScale;
+            cand *= kScale;
             // S is complete, so the product before it, the last to write O, is too
             const bool grow = cand > mx + kLag || (mx == -INFINITY && cand > -INFINITY);
             if (__any_sync(0xffffffffu, grow)) {
@@ -444,17 +412,27 @@ __device__ __forceinline__ void softmax(const ChunkAttnParams &p, Bars *bar, uin
                 }
             }
             const float off = kUp - (mx == -INFINITY ? 0.f : mx);
-            float l0 = 0.f, l1 = 0.f;
-#pragma unroll
-            for (int c = 0; c < 128; c += 2) {
-                const float a = ex2(fmaf(f[c], kScale, off)), b = ex2(fmaf(f[c + 1], kScale, off));
-                l0 += a;
-                l1 += b;
-                x[c >> 1] = pack_half2(a, b);
-            }
-            l += l0 + l1;
-            tmem_st32(ts, x);
-            tmem_st32(ts + 32, x + 32);
+            uint64_t l0 = 0, l1 = 0;
+            uint32_t z[32];
+            tmem_ld32(z, ts + 64);
+            weights32(x, off, l0, l1);
+            tmem_st16(ts, x);
+            weights32(x + 32, off, l0, l1);
+            tmem_st16(ts + 16, x + 32);
+            tmem_ld32(x, ts + 96);
+            tmem_wait_ld();
+            tmem_tie16(z);
+            tmem_tie16(z + 16);
+            tmem_tie16(x);
+            tmem_tie16(x + 16);
+            mask_keys(z, y - 64);
+            mask_keys(x, y - 96);
+            weights32(z, off, l0, l1);
+            tmem_st16(ts + 32, z);
+            weights32(x, off, l0, l1);
+            tmem_st16(ts + 48, x);
+            const float2 ls = of_pair(add_pair(l0, l1));
+            l += ls.x + ls.y;
             tmem_wait_st();
             tc_fence_before();
             mbar_arrive(&bar->p_full[m]);
@@ -535,7 +513,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_wide_kernel(const __grid_co
         for (int i = 0; i < 4; i++) bar->odd[i] = 0;
         fence_barrier_init();
     }
-    if (w == 12) tmem_alloc(&bar->tmem);
+    if (w == 16) tmem_alloc(&bar->tmem);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -544,16 +522,19 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_wide_kernel(const __grid_co
     if (w < 8) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
         softmax(p, bar, tm, w >> 2, begin, end);
+    } else if (w < 16) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsTiles));
+        if (w < 12) produce<false>(p, sm, bar, begin, end);
+        else produce<true>(p, sm, bar, begin, end);
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
-        if (w < 12) produce(p, sm, bar, begin, end);
-        else if (threadIdx.x == 384) multiply(p, sm, bar, tm, begin, end);
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsMul));
+        if (threadIdx.x == kMulThread) multiply(p, sm, bar, tm, begin, end);
     }
     __syncwarp();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (w == 12) tmem_free(tm);
+    if (w == 16) tmem_free(tm);
 }
 
 }  // namespace
