@@ -23,7 +23,7 @@ namespace kvq {
 
 namespace {
 
-constexpr int kRows = 256, kThreads = 640, kMulThread = 512;
+constexpr int kRows = 256, kThreads = 640;
 constexpr int kTileBytes = kChunkKeys * kD * 2;          // an fp16 key or value tile: 32 KB
 constexpr int kRing = 2;                                 // tiles of each kind
 constexpr int kRawBytes = 2 * (16384 + 512);             // packed tiles: codes and (scale, min)
@@ -84,7 +84,7 @@ __device__ __forceinline__ void deq_job(const uint32_t (&wd)[8], const uint32_t 
     constexpr int N = 32 / BITS;                       // rows
     constexpr uint32_t MASK = ((1u << BITS) - 1u) * 0x10001u;
     constexpr int FIT = BITS == 2 ? 5 : BITS == 4 ? 2 : 1;  // codes of a half below bit 10
-#pragma unroll
+#pragma unroll 1
     for (int hf = 0; hf < 2; hf++) {
         uint32_t x[4];
 #pragma unroll
@@ -100,10 +100,10 @@ __device__ __forceinline__ void deq_job(const uint32_t (&wd)[8], const uint32_t 
                 const uint32_t sub = (uint32_t)(0xe400 - ((j % FIT * BITS) << 10)) * 0x10001u;  // -1024 2^-sh
                 y[c] = hfma2(hfma2(v, mul, sub), s2[c], m2[c]);
             }
-            const int r = hf * (N / 2) + j;
-            const uint32_t at = (dst ^ ((r & 7) << 4)) + r * 128;
+            const uint32_t at = (dst ^ ((j & 7) << 4)) + j * 128;
             asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3]) : "memory");
         }
+        dst = (dst ^ ((N / 2 & 7) << 4)) + N / 2 * 128;  // the rows of the second half
     }
 }
 
@@ -127,7 +127,7 @@ __device__ __forceinline__ void make_tile(uint32_t raw, uint32_t tile, int t, in
     }
     const int j = c0 & (TV - 1);
     const uint32_t src = raw + 4 * ((c0 - j) * NR);
-#pragma unroll
+#pragma unroll 1
     for (int i = 0; i < NR / 8; i++) {
         const int m = m0 + 8 * i;
         uint32_t wd[8];  // the row's 16-byte chunks are permuted by xor with m mod 8
@@ -165,17 +165,18 @@ __device__ __forceinline__ bool make_tail(const ChunkAttnParams &p, const Seg &s
 }
 
 // ---------------------------------------------------------------- groups 2, 3: tiles --
-template <bool VALUE>
-__device__ __forceinline__ void produce(const ChunkAttnParams &p, unsigned char *sm, Bars *bar, int begin, int end) {
-    const int tid = threadIdx.x & 127, bits = VALUE ? p.vbits : p.kbits;
-    const int kraw = 2048 * p.kbits + 512, vraw = 2048 * p.vbits + 512, size = VALUE ? vraw : kraw;
+// Both groups run the same code (the kernel is as fast as its hot code is small: five roles
+// share an SM's instruction cache).
+__device__ __forceinline__ void produce(const ChunkAttnParams &p, unsigned char *sm, Bars *bar, bool value, int begin, int end) {
+    const int tid = threadIdx.x & 127, bits = value ? p.vbits : p.kbits;
+    const int kraw = 2048 * p.kbits + 512, vraw = 2048 * p.vbits + 512, size = value ? vraw : kraw;
     const uint32_t slots = min(kMaxRaw, kRawBytes / (kraw + vraw));
-    unsigned char *raw = sm + kOffRaw + (VALUE ? slots * kraw : 0);
-    unsigned char *ring = sm + (VALUE ? kOffV : kOffK);
-    uint64_t *arrived = VALUE ? bar->rawv : bar->rawk, *read = VALUE ? bar->readv : bar->readk;
-    uint64_t *full = VALUE ? bar->v_full : bar->k_full, *empty = VALUE ? bar->v_empty : bar->k_empty;
-    const int32_t *codes = VALUE ? p.v_codes : p.k_codes;
-    const uint16_t *meta = VALUE ? p.v_meta : p.k_meta;
+    unsigned char *raw = sm + kOffRaw + (value ? slots * kraw : 0);
+    unsigned char *ring = sm + (value ? kOffV : kOffK);
+    uint64_t *arrived = value ? bar->rawv : bar->rawk, *read = value ? bar->readv : bar->readk;
+    uint64_t *full = value ? bar->v_full : bar->k_full, *empty = value ? bar->v_empty : bar->k_empty;
+    const int32_t *codes = value ? p.v_codes : p.k_codes;
+    const uint16_t *meta = value ? p.v_meta : p.k_meta;
     uint32_t n = 0, c = 0, i = 0, nq = 0;  // tiles made, packed tiles read, copies issued, query tiles
     // thread 0: the copies of packed tile kt, once the slot's last tile has been read
     auto copy = [&](const Seg &s, int kt) {
@@ -186,7 +187,7 @@ __device__ __forceinline__ void produce(const ChunkAttnParams &p, unsigned char 
         unsigned char *dst = raw + sl * size;
         mbar_arrive_expect_tx(&arrived[sl], size);
         bulk_g2s(dst, codes + ((size_t)page * p.G + t0) * (kD * bits / 32), 2048 * bits, &arrived[sl]);
-        bulk_g2s(dst + 2048 * bits, meta + (VALUE ? ((size_t)page * p.G + t0) * 2 : (size_t)page * kD * 2), 512, &arrived[sl]);
+        bulk_g2s(dst + 2048 * bits, meta + (value ? ((size_t)page * p.G + t0) * 2 : (size_t)page * kD * 2), 512, &arrived[sl]);
         i++;
         return true;
     };
@@ -198,7 +199,7 @@ __device__ __forceinline__ void produce(const ChunkAttnParams &p, unsigned char 
             if (tid == 0)
                 for (int kt = s.k0; kt < min(npk, s.k0 + (int)slots); kt++)
                     if (!copy(s, kt)) return;
-            if (VALUE) {
+            if (value) {
                 // queries: 128-row tiles, rows of tokens' heads; rows behind the last one repeat it
                 if (!wait_or_stop(&bar->q_empty, (nq & 1) ^ 1, &bar->stop, p.status)) return;
                 nq++;
@@ -224,7 +225,7 @@ __device__ __forceinline__ void produce(const ChunkAttnParams &p, unsigned char 
                     if (!wait_or_stop(&arrived[sl], (c / slots) & 1, &bar->stop, p.status)) return;
                     c++;
                     const uint32_t src = smem_u32(raw + sl * size), dst = smem_u32(tile);
-                    const int TV = VALUE ? 256 / p.kbits : kChunkKeys;
+                    const int TV = value ? 256 / p.kbits : kChunkKeys;
                     if (bits == 2) make_tile<2>(src, dst, tid, TV);
                     else if (bits == 4) make_tile<4>(src, dst, tid, TV);
                     else make_tile<8>(src, dst, tid, TV);
@@ -233,7 +234,7 @@ __device__ __forceinline__ void produce(const ChunkAttnParams &p, unsigned char 
                     mbar_arrive(&read[sl]);
                     if (tid == 0 && kt + (int)slots < npk && !copy(s, kt + (int)slots)) return;
                 } else {
-                    if (make_tail(p, s, (kt - s.np) * kChunkKeys, VALUE, tile, tid)) {
+                    if (make_tail(p, s, (kt - s.np) * kChunkKeys, value, tile, tid)) {
                         // infinite and NaN values enter the product as 0 (0 weights of rows that may
                         // not see them would spread them) and are added to their rows at the end
                         *(volatile int *)&bar->odd[seg & 3] = seg + 1;
@@ -252,7 +253,7 @@ __device__ __forceinline__ void produce(const ChunkAttnParams &p, unsigned char 
 
 // ---------------------------------------------------------------- warp 16: products ---
 __device__ __forceinline__ void multiply(const ChunkAttnParams &p, unsigned char *sm, Bars *bar, uint32_t tm, int begin, int end) {
-    const uint32_t base = smem_u32(sm);
+    const uint32_t base = smem_u32(sm), lead = elect_lane();
     uint32_t nk = 0, nv = 0, nq = 0, np_[2] = {0, 0};
     // Rows along M and N (keys: tokens, packed values: channels): 16 of the contracted
     // dimension are 32 bytes of a row; fp16 value rows run along the tokens: 16 are two atoms.
@@ -261,9 +262,9 @@ __device__ __forceinline__ void multiply(const ChunkAttnParams &p, unsigned char
 #pragma unroll
         for (int k = 0; k < 8; k++) {
             const uint32_t off = ((k >> 2) * 16384 + (k & 3) * 32) >> 4;
-            mma_ss(tm + m * 128, a0 + off, b0 + off, f16_idesc(128, 128, false), k > 0);
+            mma_ss(tm + m * 128, a0 + off, b0 + off, f16_idesc(128, 128, false), k > 0, lead);
         }
-        tc_commit(&bar->s_full[m]);
+        tc_commit(&bar->s_full[m], lead);
     };
     auto weigh = [&](int m, int vs, bool packed, bool acc) {
         const uint32_t vb = base + kOffV + vs * kTileBytes;
@@ -272,80 +273,85 @@ __device__ __forceinline__ void multiply(const ChunkAttnParams &p, unsigned char
 #pragma unroll
         for (int k = 0; k < 8; k++) {
             const uint32_t off = (packed ? (k >> 2) * 16384 + (k & 3) * 32 : k * 2048) >> 4;
-            mma_ts(tm + 256 + m * 128, tm + m * 128 + 8 * k, b0 + off, id, acc || k > 0);
+            mma_ts(tm + 256 + m * 128, tm + m * 128 + 8 * k, b0 + off, id, acc || k > 0, lead);
         }
     };
     auto run = [&]() {
         for (int at = begin; at < end;) {
             const Seg s = next_seg(p, at, end);
             const int n = s.k1 - s.k0, M = s.valid > 128 ? 2 : 1;
-            if (!wait_or_stop(&bar->q_full, nq & 1, &bar->stop, p.status)) return;
+            if (!warp_wait_or_stop(&bar->q_full, nq & 1, &bar->stop, p.status)) return;
             nq++;
-            if (!wait_or_stop(&bar->k_full[nk % kRing], (nk / kRing) & 1, &bar->stop, p.status)) return;
+            if (!warp_wait_or_stop(&bar->k_full[nk % kRing], (nk / kRing) & 1, &bar->stop, p.status)) return;
             tc_fence_after();
             for (int m = 0; m < M; m++) scores(m, nk % kRing);
-            tc_commit(&bar->k_empty[nk % kRing]);
+            tc_commit(&bar->k_empty[nk % kRing], lead);
             nk++;
-            if (n == 1) tc_commit(&bar->q_empty);
+            if (n == 1) tc_commit(&bar->q_empty, lead);
             for (int j = 0; j < n; j++) {
                 const int vs = nv % kRing;
-                if (!wait_or_stop(&bar->v_full[vs], (nv / kRing) & 1, &bar->stop, p.status)) return;
+                if (!warp_wait_or_stop(&bar->v_full[vs], (nv / kRing) & 1, &bar->stop, p.status)) return;
                 for (int m = 0; m < M; m++) {
-                    if (!wait_or_stop(&bar->p_full[m], np_[m] & 1, &bar->stop, p.status)) return;
+                    if (!warp_wait_or_stop(&bar->p_full[m], np_[m] & 1, &bar->stop, p.status)) return;
                     np_[m]++;
                     tc_fence_after();
                     weigh(m, vs, s.k0 + j < s.np, j > 0);
+                    if (m == M - 1) tc_commit(&bar->v_empty[vs], lead);
                     if (j + 1 < n) {
                         if (m == 0) {
-                            if (!wait_or_stop(&bar->k_full[nk % kRing], (nk / kRing) & 1, &bar->stop, p.status)) return;
+                            if (!warp_wait_or_stop(&bar->k_full[nk % kRing], (nk / kRing) & 1, &bar->stop, p.status)) return;
                             tc_fence_after();
                         }
                         scores(m, nk % kRing);
                     } else {
-                        tc_commit(&bar->o_full[m]);
+                        tc_commit(&bar->o_full[m], lead);
                     }
                 }
-                tc_commit(&bar->v_empty[vs]);
                 nv++;
                 if (j + 1 < n) {
-                    tc_commit(&bar->k_empty[nk % kRing]);
+                    tc_commit(&bar->k_empty[nk % kRing], lead);
                     nk++;
-                    if (j + 2 == n) tc_commit(&bar->q_empty);
+                    if (j + 2 == n) tc_commit(&bar->q_empty, lead);
                 }
             }
             at = s.first + s.k1;
         }
     };
     run();
-    tc_commit(&bar->drain);  // every product has ended before the tensor memory is freed
+    tc_commit(&bar->drain, lead);  // every product has ended before the tensor memory is freed
     mbar_wait(&bar->drain, 0, p.status);
 }
 
 // ---------------------------------------------------------------- groups 0, 1 ---------
-// Scores of 32 keys: those from the n-th on are not seen.
-__device__ __forceinline__ void mask_keys(uint32_t *x, int n) {
-    if (n < 32) {
+// Scores of 64 keys: those from the n-th on are not seen.
+__device__ __forceinline__ void mask64(uint32_t *x, int n) {
 #pragma unroll
-        for (int c = 0; c < 32; c++)
-            if (c >= n) x[c] = 0xff800000u;
-    }
+    for (int c = 0; c < 64; c++)
+        if (c >= n) x[c] = 0xff800000u;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
 }
 __device__ __forceinline__ float max64(const float *f) {
     float t[8];
 #pragma unroll
     for (int e = 0; e < 8; e++) t[e] = f[e];
 #pragma unroll
-    for (int c = 8; c < 64; c += 8)
+    for (int c = 8; c < 56; c += 16)
 #pragma unroll
-        for (int e = 0; e < 8; e++) t[e] = fmaxf(t[e], f[c + e]);
-    return fmaxf(fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])), fmaxf(fmaxf(t[4], t[5]), fmaxf(t[6], t[7])));
+        for (int e = 0; e < 8; e++) t[e] = max3(t[e], f[c + 2 * e], f[c + 2 * e + 1]);
+#pragma unroll
+    for (int e = 0; e < 8; e++) t[e] = fmaxf(t[e], f[56 + e]);
+    return fmaxf(max3(t[0], t[1], t[2]), max3(max3(t[3], t[4], t[5]), t[6], t[7]));
 }
-// Weights 2^(s scale + off) of 32 scores, as 16 half2 in place; their sums to l0 and l1.
-__device__ __forceinline__ void weights32(uint32_t *x, float off, uint64_t &l0, uint64_t &l1) {
+// Weights 2^(s scale + off) of 64 scores, as 32 half2 in place; their sums to l0 and l1.
+__device__ __forceinline__ void weights64(uint32_t *x, float off, uint64_t &l0, uint64_t &l1) {
     const uint64_t sc2 = pair_of(kScale, kScale), of2 = pair_of(off, off);
     const float *f = reinterpret_cast<const float *>(x);
 #pragma unroll
-    for (int c = 0; c < 32; c += 4) {
+    for (int c = 0; c < 64; c += 4) {
         float2 a = of_pair(fma_pair(pair_of(f[c], f[c + 1]), sc2, of2)), b = of_pair(fma_pair(pair_of(f[c + 2], f[c + 3]), sc2, of2));
         a.x = ex2(a.x);
         a.y = ex2(a.y);
@@ -376,19 +382,19 @@ __device__ __forceinline__ void softmax(const ChunkAttnParams &p, Bars *bar, uin
             if (!warp_wait_or_stop(&bar->s_full[m], ns & 1, &bar->stop, p.status)) return;
             ns++;
             tc_fence_after();
-            // maximum over the row; the first half stays in registers, the second is read again
+            // the maximum over the row, then the weights: 64 scores at a time, read twice, which
+            // keeps registers and code small
             const int y = kt >= s.np ? lim - (kt - s.np) * kChunkKeys : kChunkKeys;  // keys it may see
             uint32_t x[64];
             float cand = -INFINITY;
-#pragma unroll
-            for (int hf = 1; hf >= 0; hf--) {
+#pragma unroll 1
+            for (int hf = 0; hf < 2; hf++) {
                 tmem_ld32(x, ts + 64 * hf);
                 tmem_ld32(x + 32, ts + 64 * hf + 32);
                 tmem_wait_ld();
 #pragma unroll
                 for (int c = 0; c < 4; c++) tmem_tie16(x + 16 * c);
-                mask_keys(x, y - 64 * hf);
-                mask_keys(x + 32, y - 64 * hf - 32);
+                if (y < kChunkKeys) mask64(x, y - 64 * hf);
                 cand = fmaxf(cand, max64(reinterpret_cast<const float *>(x)));
             }
             cand *= kScale;
@@ -413,24 +419,17 @@ __device__ __forceinline__ void softmax(const ChunkAttnParams &p, Bars *bar, uin
             }
             const float off = kUp - (mx == -INFINITY ? 0.f : mx);
             uint64_t l0 = 0, l1 = 0;
-            uint32_t z[32];
-            tmem_ld32(z, ts + 64);
-            weights32(x, off, l0, l1);
-            tmem_st16(ts, x);
-            weights32(x + 32, off, l0, l1);
-            tmem_st16(ts + 16, x + 32);
-            tmem_ld32(x, ts + 96);
-            tmem_wait_ld();
-            tmem_tie16(z);
-            tmem_tie16(z + 16);
-            tmem_tie16(x);
-            tmem_tie16(x + 16);
-            mask_keys(z, y - 64);
-            mask_keys(x, y - 96);
-            weights32(z, off, l0, l1);
-            tmem_st16(ts + 32, z);
-            weights32(x, off, l0, l1);
-            tmem_st16(ts + 48, x);
+#pragma unroll 1
+            for (int hf = 0; hf < 2; hf++) {
+                tmem_ld32(x, ts + 64 * hf);
+                tmem_ld32(x + 32, ts + 64 * hf + 32);
+                tmem_wait_ld();
+#pragma unroll
+                for (int c = 0; c < 4; c++) tmem_tie16(x + 16 * c);
+                if (y < kChunkKeys) mask64(x, y - 64 * hf);
+                weights64(x, off, l0, l1);
+                tmem_st32(ts + 32 * hf, x);  // over scores that have been read
+            }
             const float2 ls = of_pair(add_pair(l0, l1));
             l += ls.x + ls.y;
             tmem_wait_st();
@@ -487,7 +486,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_wide_kernel(const __grid_co
     extern __shared__ unsigned char smem_raw[];
     unsigned char *sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     Bars *bar = reinterpret_cast<Bars *>(sm + kOffBar);
-    const int w = threadIdx.x >> 5;
+    const int w = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
     if (threadIdx.x == 0) {
         mbar_init(&bar->q_full, 128);
         mbar_init(&bar->q_empty, 1);
@@ -524,11 +523,10 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_wide_kernel(const __grid_co
         softmax(p, bar, tm, w >> 2, begin, end);
     } else if (w < 16) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsTiles));
-        if (w < 12) produce<false>(p, sm, bar, begin, end);
-        else produce<true>(p, sm, bar, begin, end);
+        produce(p, sm, bar, w >= 12, begin, end);
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsMul));
-        if (threadIdx.x == kMulThread) multiply(p, sm, bar, tm, begin, end);
+        if (w == 16) multiply(p, sm, bar, tm, begin, end);
     }
     __syncwarp();
     tc_fence_before();
