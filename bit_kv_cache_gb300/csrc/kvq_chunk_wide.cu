@@ -9,9 +9,9 @@
 //   groups 2, 3  make the key and the value tiles: packed pages arrive by bulk copies and
 //                are dequantized into fp16 tiles in shared memory, fp16 rows are gathered;
 //   warp 16      issues the products S_m = Q_m K^T and O_m += P_m V.
-// The two query tiles alternate on the tensor core: while one's scores are in softmax, the
-// other's products run; a key tile is dequantized once for both.  Tensor memory holds S_0,
-// S_1, O_0, O_1 (128 columns each).
+// A step is half a key tile (64 keys).  S_m has two buffers of 64 columns, so that the scores
+// of the next step are made while the softmax of this one runs; a key tile is dequantized
+// once for both query tiles.  Tensor memory: S_0, S_1, O_0, O_1, 128 columns each.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -40,7 +40,8 @@ static_assert(256 * kRegsSoftmax + 256 * kRegsTiles + 128 * kRegsMul <= kThreads
 
 struct Bars {
     uint64_t q_full, q_empty, k_full[kRing], k_empty[kRing], v_full[kRing], v_empty[kRing];
-    uint64_t s_full[2], p_full[2], o_full[2], drain;
+    uint64_t s_full[2][2], p_full[2][2];              // of query tile m, step parity h
+    uint64_t pv_done[2], drain;
     uint64_t rawk[kMaxRaw], rawv[kMaxRaw];            // packed tile arrived
     uint64_t readk[kMaxRaw], readv[kMaxRaw];          // packed tile read by all producers
     uint32_t tmem;
@@ -53,7 +54,7 @@ static_assert(kSmemBytes <= 232448, "shared memory");
 // Segment: the items of one unit inside the CTA's range.
 struct Seg {
     Item it;
-    int k0, k1, np, valid, first;
+    int k0, k1, np, valid, first, steps;
 };
 __device__ __forceinline__ Seg next_seg(const ChunkAttnParams &p, int at, int end) {
     Seg s;
@@ -63,6 +64,10 @@ __device__ __forceinline__ Seg next_seg(const ChunkAttnParams &p, int at, int en
     s.np = s.it.s.T / kChunkKeys;
     s.valid = min(kRows, s.it.s.n_new * p.g - s.it.t * kRows);
     s.first = s.it.first;
+    // the unit's last key tile may end in its first half
+    const int last = min(s.it.s.n_new, ((s.it.t + 1) * kRows - 1) / p.g + 1);
+    const int seen = s.it.s.ns + s.it.s.nr + last - (s.it.n - s.np - 1) * kChunkKeys;
+    s.steps = 2 * (s.k1 - s.k0) - (s.k1 == s.it.n && seen <= 64 ? 1 : 0);
     return s;
 }
 
@@ -254,64 +259,71 @@ __device__ __forceinline__ void produce(const ChunkAttnParams &p, unsigned char 
 // ---------------------------------------------------------------- warp 16: products ---
 __device__ __forceinline__ void multiply(const ChunkAttnParams &p, unsigned char *sm, Bars *bar, uint32_t tm, int begin, int end) {
     const uint32_t base = smem_u32(sm), lead = elect_lane();
-    uint32_t nk = 0, nv = 0, nq = 0, np_[2] = {0, 0};
+    uint32_t nk = 0, nv = 0, nq = 0, np_[2][2] = {{0, 0}, {0, 0}}, npv[2] = {0, 0};
     // Rows along M and N (keys: tokens, packed values: channels): 16 of the contracted
     // dimension are 32 bytes of a row; fp16 value rows run along the tokens: 16 are two atoms.
-    auto scores = [&](int m, int ks) {
-        const uint64_t a0 = smem_desc(base + kOffQ + m * kTileBytes, 16, 1024), b0 = smem_desc(base + kOffK + ks * kTileBytes, 16, 1024);
+    auto scores = [&](int m, int h, int ks) {
+        const uint64_t a0 = smem_desc(base + kOffQ + m * kTileBytes, 16, 1024);
+        const uint64_t b0 = smem_desc(base + kOffK + ks * kTileBytes + h * 8192, 16, 1024);
 #pragma unroll
         for (int k = 0; k < 8; k++) {
             const uint32_t off = ((k >> 2) * 16384 + (k & 3) * 32) >> 4;
-            mma_ss(tm + m * 128, a0 + off, b0 + off, f16_idesc(128, 128, false), k > 0, lead);
+            mma_ss(tm + m * 128 + h * 64, a0 + off, b0 + off, f16_idesc(128, 64, false), k > 0, lead);
         }
-        tc_commit(&bar->s_full[m], lead);
+        tc_commit(&bar->s_full[m][h], lead);
     };
-    auto weigh = [&](int m, int vs, bool packed, bool acc) {
+    auto weigh = [&](int m, int h, int vs, bool packed, bool acc) {
         const uint32_t vb = base + kOffV + vs * kTileBytes;
-        const uint64_t b0 = packed ? smem_desc(vb, 16, 1024) : smem_desc(vb, 16384, 1024);
+        const uint64_t b0 = packed ? smem_desc(vb + h * 16384, 16, 1024) : smem_desc(vb + h * 8192, 16384, 1024);
         const uint32_t id = packed ? f16_idesc(128, 128, false) : f16_idesc(128, 128, true);
 #pragma unroll
-        for (int k = 0; k < 8; k++) {
-            const uint32_t off = (packed ? (k >> 2) * 16384 + (k & 3) * 32 : k * 2048) >> 4;
-            mma_ts(tm + 256 + m * 128, tm + m * 128 + 8 * k, b0 + off, id, acc || k > 0, lead);
-        }
+        for (int k = 0; k < 4; k++)
+            mma_ts(tm + 256 + m * 128, tm + m * 128 + h * 64 + 8 * k, b0 + ((packed ? k * 32 : k * 2048) >> 4), id, acc || k > 0, lead);
+        tc_commit(&bar->pv_done[m], lead);
     };
     auto run = [&]() {
         for (int at = begin; at < end;) {
             const Seg s = next_seg(p, at, end);
-            const int n = s.k1 - s.k0, M = s.valid > 128 ? 2 : 1;
+            const int M = s.valid > 128 ? 2 : 1;
             if (!warp_wait_or_stop(&bar->q_full, nq & 1, &bar->stop, p.status)) return;
             nq++;
             if (!warp_wait_or_stop(&bar->k_full[nk % kRing], (nk / kRing) & 1, &bar->stop, p.status)) return;
             tc_fence_after();
-            for (int m = 0; m < M; m++) scores(m, nk % kRing);
-            tc_commit(&bar->k_empty[nk % kRing], lead);
-            nk++;
-            if (n == 1) tc_commit(&bar->q_empty, lead);
-            for (int j = 0; j < n; j++) {
-                const int vs = nv % kRing;
-                if (!warp_wait_or_stop(&bar->v_full[vs], (nv / kRing) & 1, &bar->stop, p.status)) return;
-                for (int m = 0; m < M; m++) {
-                    if (!warp_wait_or_stop(&bar->p_full[m], np_[m] & 1, &bar->stop, p.status)) return;
-                    np_[m]++;
-                    tc_fence_after();
-                    weigh(m, vs, s.k0 + j < s.np, j > 0);
-                    if (m == M - 1) tc_commit(&bar->v_empty[vs], lead);
-                    if (j + 1 < n) {
-                        if (m == 0) {
-                            if (!warp_wait_or_stop(&bar->k_full[nk % kRing], (nk / kRing) & 1, &bar->stop, p.status)) return;
+            for (int m = 0; m < M; m++) scores(m, 0, nk % kRing);
+            if (s.steps == 1) tc_commit(&bar->q_empty, lead);
+            for (int i = 0; i < s.steps; i++) {
+                const int h = i & 1, vs = nv % kRing;
+                const bool next = i + 1 < s.steps;
+                if (next) {
+                    // the next scores of both query tiles, before any wait for weights: once the
+                    // products of the step before this one have read the weights in their buffers
+                    // (the other query tile's products run meanwhile)
+                    if (h == 1) {
+                        if (!warp_wait_or_stop(&bar->k_full[nk % kRing], (nk / kRing) & 1, &bar->stop, p.status)) return;
+                        tc_fence_after();
+                    }
+                    for (int m = 0; m < M; m++) {
+                        if (i > 0) {
+                            if (!warp_wait_or_stop(&bar->pv_done[m], (npv[m] - 1) & 1, &bar->stop, p.status)) return;
                             tc_fence_after();
                         }
-                        scores(m, nk % kRing);
-                    } else {
-                        tc_commit(&bar->o_full[m], lead);
+                        scores(m, h ^ 1, nk % kRing);
                     }
                 }
-                nv++;
-                if (j + 1 < n) {
-                    tc_commit(&bar->k_empty[nk % kRing], lead);
-                    nk++;
-                    if (j + 2 == n) tc_commit(&bar->q_empty, lead);
+                if (h == 0) tc_commit(&bar->k_empty[nk % kRing], lead);
+                if (i + 2 == s.steps) tc_commit(&bar->q_empty, lead);
+                if (h == 0 && !warp_wait_or_stop(&bar->v_full[vs], (nv / kRing) & 1, &bar->stop, p.status)) return;
+                for (int m = 0; m < M; m++) {
+                    if (!warp_wait_or_stop(&bar->p_full[m][h], np_[m][h] & 1, &bar->stop, p.status)) return;
+                    np_[m][h]++;
+                    tc_fence_after();
+                    weigh(m, h, vs, s.k0 + (i >> 1) < s.np, i > 0);
+                    npv[m]++;
+                }
+                if (h == 0) nk++;
+                if (h == 1 || !next) {
+                    tc_commit(&bar->v_empty[vs], lead);
+                    nv++;
                 }
             }
             at = s.first + s.k1;
@@ -368,7 +380,7 @@ __device__ __forceinline__ void softmax(const ChunkAttnParams &p, Bars *bar, uin
     const int lane = threadIdx.x & 31, row = 128 * m + (threadIdx.x & 127);
     const uint32_t lanes = (uint32_t)(threadIdx.x & 96) << 16;
     const uint32_t ts = tm + lanes + m * 128, to = tm + lanes + 256 + m * 128;
-    uint32_t ns = 0, no = 0;
+    uint32_t ns[2] = {0, 0}, npv = 0;  // scores taken of each buffer, weights given
     int seg = 0;
     for (int at = begin; at < end; seg++) {
         const Seg s = next_seg(p, at, end);
@@ -378,33 +390,29 @@ __device__ __forceinline__ void softmax(const ChunkAttnParams &p, Bars *bar, uin
         const int r = s.it.t * kRows + min(row, s.valid - 1);
         const int lim = s.it.s.ns + s.it.s.nr + r / p.g + 1;  // fp16 tokens this row may see
         float mx = -INFINITY, l = 0.f;
-        for (int kt = s.k0; kt < s.k1; kt++) {
-            if (!warp_wait_or_stop(&bar->s_full[m], ns & 1, &bar->stop, p.status)) return;
-            ns++;
+        for (int i = 0; i < s.steps; i++) {
+            const int h = i & 1, kt = s.k0 + (i >> 1);
+            if (!warp_wait_or_stop(&bar->s_full[m][h], ns[h] & 1, &bar->stop, p.status)) return;
+            ns[h]++;
             tc_fence_after();
-            // the maximum over the row, then the weights: 64 scores at a time, read twice, which
-            // keeps registers and code small
-            const int y = kt >= s.np ? lim - (kt - s.np) * kChunkKeys : kChunkKeys;  // keys it may see
             uint32_t x[64];
-            float cand = -INFINITY;
-#pragma unroll 1
-            for (int hf = 0; hf < 2; hf++) {
-                tmem_ld32(x, ts + 64 * hf);
-                tmem_ld32(x + 32, ts + 64 * hf + 32);
-                tmem_wait_ld();
+            tmem_ld32(x, ts + 64 * h);
+            tmem_ld32(x + 32, ts + 64 * h + 32);
+            tmem_wait_ld();
 #pragma unroll
-                for (int c = 0; c < 4; c++) tmem_tie16(x + 16 * c);
-                if (y < kChunkKeys) mask64(x, y - 64 * hf);
-                cand = fmaxf(cand, max64(reinterpret_cast<const float *>(x)));
-            }
-            cand *= kScale;
-            // S is complete, so the product before it, the last to write O, is too
+            for (int c = 0; c < 4; c++) tmem_tie16(x + 16 * c);
+            const int y = kt >= s.np ? lim - (kt - s.np) * kChunkKeys - 64 * h : 64;  // keys it may see
+            if (y < 64) mask64(x, y);
+            const float cand = max64(reinterpret_cast<const float *>(x)) * kScale;
             const bool grow = cand > mx + kLag || (mx == -INFINITY && cand > -INFINITY);
             if (__any_sync(0xffffffffu, grow)) {
                 const float corr = grow ? ex2(mx - cand) : 1.f;
                 if (grow) mx = cand;
                 l *= corr;
-                if (kt > s.k0) {
+                if (i > 0) {
+                    // the step before was the last to write O
+                    if (!warp_wait_or_stop(&bar->pv_done[m], (npv - 1) & 1, &bar->stop, p.status)) return;
+                    tc_fence_after();
 #pragma unroll 1
                     for (int c = 0; c < 8; c++) {
                         uint32_t o[16];
@@ -419,25 +427,18 @@ __device__ __forceinline__ void softmax(const ChunkAttnParams &p, Bars *bar, uin
             }
             const float off = kUp - (mx == -INFINITY ? 0.f : mx);
             uint64_t l0 = 0, l1 = 0;
-#pragma unroll 1
-            for (int hf = 0; hf < 2; hf++) {
-                tmem_ld32(x, ts + 64 * hf);
-                tmem_ld32(x + 32, ts + 64 * hf + 32);
-                tmem_wait_ld();
-#pragma unroll
-                for (int c = 0; c < 4; c++) tmem_tie16(x + 16 * c);
-                if (y < kChunkKeys) mask64(x, y - 64 * hf);
-                weights64(x, off, l0, l1);
-                tmem_st32(ts + 32 * hf, x);  // over scores that have been read
-            }
+            weights64(x, off, l0, l1);
+            tmem_st32(ts + 64 * h, x);  // over the scores
             const float2 ls = of_pair(add_pair(l0, l1));
             l += ls.x + ls.y;
             tmem_wait_st();
             tc_fence_before();
-            mbar_arrive(&bar->p_full[m]);
+            mbar_arrive(&bar->p_full[m][h]);
+            npv++;
         }
-        if (!warp_wait_or_stop(&bar->o_full[m], no & 1, &bar->stop, p.status)) return;
-        no++;
+        // the last scores followed all products but two (a wait names a phase by its parity)
+        if (s.steps > 1 && !warp_wait_or_stop(&bar->pv_done[m], (npv - 2) & 1, &bar->stop, p.status)) return;
+        if (!warp_wait_or_stop(&bar->pv_done[m], (npv - 1) & 1, &bar->stop, p.status)) return;
         tc_fence_after();
         const bool whole = s.k0 == 0 && s.k1 == s.it.n;
         const bool odd = *(volatile int *)&bar->odd[seg & 3] == seg + 1;
@@ -497,9 +498,11 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_wide_kernel(const __grid_co
             mbar_init(&bar->v_empty[i], 1);
         }
         for (int i = 0; i < 2; i++) {
-            mbar_init(&bar->s_full[i], 1);
-            mbar_init(&bar->p_full[i], 128);
-            mbar_init(&bar->o_full[i], 1);
+            mbar_init(&bar->pv_done[i], 1);
+            for (int h = 0; h < 2; h++) {
+                mbar_init(&bar->s_full[i][h], 1);
+                mbar_init(&bar->p_full[i][h], 128);
+            }
         }
         mbar_init(&bar->drain, 1);
         for (int i = 0; i < kMaxRaw; i++) {
