@@ -20,7 +20,7 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libkvq.so")
 SOURCES = ["kvq_api.cu", "kvq_quant.cu", "kvq_decode.cu", "kvq_noalloc.cu", "kvq_paged.cu",
            "kvq_decode_paged.cu", "kvq_decode_rope.cu", "kvq_decode_nvfp4.cu", "kvq_selftest.cu",
-           "kvq_chunk.cu", "kvq_chunk_attn.cu", "kvq_chunk_wide.cu"]
+           "kvq_chunk.cu", "kvq_chunk_attn.cu", "kvq_chunk_combine.cu"]
 HEADERS = ["kvq_device.cuh", "kvq_internal.h", "kvq_decode_fast.cuh", "kvq_host.h",
            "kvq_decode.cuh", "kvq_quantizer.cuh", "kvq_chunk.h",
            "kvq_chunk_attn.cuh", "kvq_tcgen05.cuh"]

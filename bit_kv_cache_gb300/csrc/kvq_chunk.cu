@@ -548,7 +548,7 @@ struct ChunkWs {
 };
 ChunkWs chunk_ws() {
     ChunkWs w;
-    const size_t slots = (size_t)2 * num_sms() * kWideRows;  // rows: 2 x 256 per SM (narrow: 2 x 2 x 64)
+    const size_t slots = (size_t)2 * num_sms() * kWideRows;  // rows
     w.ml = 0;
     w.o = (slots * sizeof(float2) + 255) / 256 * 256;
     w.total = w.o + slots * 128 * sizeof(float);
@@ -664,32 +664,22 @@ int kvq_paged_chunk_attn(const kvq_config *c, const kvq_paged *pc, const kvq_chu
     p.S = c->S;
     p.R = c->R;
     p.ptab_stride = (int)(c->max_T / c->G);
-    // slots of few query rows per key head and slots of many take a kernel each
-    ChunkAttnParams part[2];
-    for (int wide = 0; wide < 2; wide++) {
-        ChunkAttnParams &a = part[wide];
-        a = p;
-        const int rows = wide ? kWideRows : kNarrowRows;
-        int64_t n = 0;
-        for (int b = 0; b < c->B; b++) {
-            const ChunkSlot &s = slots_of(ch)[b];
-            a.item0[b] = (int32_t)n;
-            const int64_t r = (int64_t)s.n_new * p.g, nt = cdiv(r, rows);
-            if ((r > kNarrowRows) != (wide != 0)) continue;
-            int64_t per = 0;
-            for (int64_t t = 0; t < nt; t++) per += chunk_tiles(s, (int)t, rows, p.g);
-            n += per * p.H_kv;
-            if (n >= (1LL << 30)) return KVQ_ERR_UNSUPPORTED;
-        }
-        for (int b = c->B; b <= KVQ_PAGED_MAX_B; b++) a.item0[b] = (int32_t)n;
-        a.n_items = (int)n;
-        a.C = (int)std::min<int64_t>(n, wide ? num_sms() : 2 * num_sms());
+    int64_t cost = 0, items = 0;
+    for (int b = 0; b < c->B; b++) {
+        const ChunkSlot &s = slots_of(ch)[b];
+        p.cost0[b] = (int32_t)cost;
+        const bool narrow = chunk_narrow(s.n_new, p.g);
+        const int rows = narrow ? kNarrowRows : kWideRows;
+        int64_t per = 0;
+        for (int64_t t = 0; t * rows < (int64_t)s.n_new * p.g; t++) per += chunk_tiles(s, (int)t, rows, p.g);
+        items += per * p.H_kv;
+        cost += per * p.H_kv * (narrow ? kNarrowCost : kWideCost);
+        if (cost >= (1LL << 30)) return KVQ_ERR_UNSUPPORTED;
     }
-    for (int wide = 1; wide >= 0; wide--)
-        if (part[wide].n_items &&
-            launch_chunk_attn(part[wide], wide ? kWideRows : kNarrowRows, (cudaStream_t)stream) != cudaSuccess)
-            return KVQ_ERR_CUDA;
-    return KVQ_OK;
+    for (int b = c->B; b <= KVQ_PAGED_MAX_B; b++) p.cost0[b] = (int32_t)cost;
+    p.cost = (int)cost;
+    p.C = (int)std::min<int64_t>(items, num_sms());
+    return status_of(launch_chunk_attn(p, (cudaStream_t)stream));
 }
 
 int kvq_paged_extend(const kvq_config *c, kvq_paged *pc, const kvq_chunk *ch, const uint16_t *kn, int64_t k_stride,

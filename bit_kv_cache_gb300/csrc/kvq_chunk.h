@@ -47,13 +47,14 @@ struct QkParams {
     uint64_t turn[128];                  // base^(-2j/rotary) / (2 pi) in units of 2^-64 turns
 };
 
-// Chunk attention.  A unit is (slot, key head, tile of `rows` query rows): row r of a slot
-// is its new token r / g under query head r % g of the key head's group.  Its items are
-// key tiles of 128 tokens: the packed ones, then the fp16 tokens [sink | residual | chunk]
-// up to the tile's last query token.  The items of all units, slot-major, then by head and
-// row tile, are cut into C equal ranges, one per CTA.  A unit inside one range is finished
-// there; of one that is cut, each range leaves fp32 partials, and the combine kernel joins
-// them in range order.
+// Chunk attention.  A unit is (slot, key head, tile of query rows): row r of a slot is its
+// new token r / g under query head r % g of the key head's group.  Its items are key tiles
+// of 128 tokens: the packed ones, then the fp16 tokens [sink | residual | chunk] up to the
+// row tile's last query token.  A slot of at most kNarrowRows rows is one narrow unit per
+// head, whose items cost a third of a wide unit's (kWideRows rows); positions count cost.
+// The items of all units, slot-major, then by head and row tile, are cut into C ranges of
+// equal cost, one per CTA.  A unit inside one range is finished there; of one that is cut,
+// each range leaves fp32 partials, and the combine kernel joins them in range order.
 struct ChunkAttnParams {
     const int32_t *desc;
     const int32_t *ptab;
@@ -62,23 +63,22 @@ struct ChunkAttnParams {
     const uint16_t *k_sink, *v_sink, *k_res, *v_res;
     const uint16_t *q, *k_new, *v_new;
     uint16_t *out;
-    float *part_o;                       // [2 C][rows][128]
-    float2 *part_ml;                     // [2 C][rows] (max, sum)
+    float *part_o;                       // [2 C][kWideRows][128]
+    float2 *part_ml;                     // [2 C][kWideRows] (max, sum)
     int32_t *status;
     int64_t q_stride, k_stride, v_stride, n_pages;
     int B, H_kv, g, G, kbits, vbits, S, R, ptab_stride;
-    int n_items, C;
-    int32_t item0[KVQ_PAGED_MAX_B + 1];  // first item of each slot
+    int cost, C;                         // of all items; ranges
+    int32_t cost0[KVQ_PAGED_MAX_B + 1];  // position of each slot's first item
 };
 
 cudaError_t launch_plan(const PlanParams &p, cudaStream_t st);
 cudaError_t launch_extend(const ExtendParams &p, int kbits, int vbits, cudaStream_t st);
 cudaError_t launch_qk(const QkParams &p, int D, cudaStream_t st);
-// rows: query rows per unit, kNarrowRows or kWideRows; p.item0, n_items and C follow from it.
-cudaError_t launch_chunk_attn(const ChunkAttnParams &p, int rows, cudaStream_t st);
-cudaError_t launch_chunk_wide(const ChunkAttnParams &p, cudaStream_t st);
-constexpr int kNarrowRows = 64, kWideRows = 256;
+cudaError_t launch_chunk_attn(const ChunkAttnParams &p, cudaStream_t st);
 
+constexpr int kNarrowRows = 128, kWideRows = 256, kNarrowCost = 1, kWideCost = 3;
+__host__ __device__ inline bool chunk_narrow(int n_new, int g) { return (int64_t)n_new * g <= kNarrowRows; }
 constexpr int kChunkKeys = 128;          // tokens per key tile
 
 // Key tiles of row tile t of a slot (rows query rows per tile, g per token).

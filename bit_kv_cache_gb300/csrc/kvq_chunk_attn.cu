@@ -1,269 +1,663 @@
-// kvq_chunk_attn.cu -- attention of a chunk of new tokens over the paged low-bit cache.
+// kvq_chunk_attn.cu -- the chunk attention kernel: softmax(q K^T) V of a unit's query rows
+// over a range of its key tiles, on the 5th-generation tensor cores.
 //
 // For query row r of a unit (see ChunkAttnParams) and key t of its slot,
 //   s_t = q . (code_t * scale + min) / sqrt(D),   out = sum_t softmax(s)_t v_t,
-// in one pass over the keys with a running maximum and sum per row.  A CTA takes a range
-// of the items of all units; each item is a tile of 128 keys, dequantized once into shared
-// memory as fp16 (one rounding of code * scale + min) and used by all of the unit's rows.
+// in one pass over the keys with a running maximum and sum per row.  Dequantized keys and
+// values are rounded once to fp16, softmax weights too; sums are fp32.
+//
+// One CTA per SM, five groups of four warps:
+//   groups 0, 1  softmax, a thread per row of 128: reads the scores S_m from tensor memory,
+//                keeps the row's running maximum and sum in registers, writes the weights
+//                P_m over S_m as fp16, rescales O_m when the maximum has grown by more than
+//                2^8;
+//   groups 2, 3  make the key and the value tiles: packed pages arrive by bulk copies and
+//                are dequantized into fp16 tiles in shared memory, fp16 rows are gathered;
+//   group 4      warps 16 + m issue the products S_m = Q K^T, warps 18 + m O_m += P_m V: each
+//                waits for its own operands while the others keep the tensor core busy (one
+//                warp for all four was the bottleneck: a wait costs it about 200 cycles).
+// In a wide unit (256 rows) m names the query tile: a key tile is dequantized once for both.
+// In a narrow one (at most 128 rows) m is the parity of the key tile: the two groups keep
+// softmax states of their own, joined at the end.
+// A step is half a key tile (64 keys).  S_m has two buffers of 64 columns, so that the scores
+// of the next step are made while the softmax of this one runs.  Tensor memory: S_0, S_1,
+// O_0, O_1, 128 columns each.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
 #include "kvq_chunk_attn.cuh"
+#include "kvq_tcgen05.cuh"
 
 namespace kvq {
 
 namespace {
 
-// ------------------------------------------------------------------------------
-// 64 query rows per CTA, 16 per warp; mma.sync on fp16 tiles in shared memory.
-// ------------------------------------------------------------------------------
-constexpr int kRows = 64, kPitch = kD + 8;  // halves per shared-memory row: ldmatrix without bank conflicts
+constexpr int kRows = kWideRows, kThreads = 640;
+constexpr int kTileBytes = kChunkKeys * kD * 2;          // an fp16 key or value tile: 32 KB
+constexpr int kRing = 2;                                 // tiles of each kind
+constexpr int kRawBytes = 2 * (16384 + 512);             // packed tiles: codes and (scale, min)
+constexpr int kMaxRaw = 4;
+constexpr int kOffQ = 0, kOffK = 2 * kTileBytes, kOffV = kOffK + kRing * kTileBytes, kOffRaw = kOffV + kRing * kTileBytes,
+              kOffBar = kOffRaw + kRawBytes;
+constexpr float kScale = kLog2e * 0.08838834764831845f;  // log2(e) / sqrt(128)
+// Weights are 2^(s - m + kUp): the running maximum may lag by kLag, so they stay below
+// 2^(kUp + kLag) < 65504, and small ones keep kUp more bits above fp16's smallest step.
+constexpr float kUp = 6.f, kLag = 8.f;
+// registers of a thread after the split; 96 at launch, times 640 threads
+constexpr int kRegsSoftmax = 120, kRegsTiles = 72, kRegsMul = 96;
+static_assert(256 * kRegsSoftmax + 256 * kRegsTiles + 128 * kRegsMul <= kThreads * 96, "register split");
 
-__global__ void __launch_bounds__(128) chunk_attn_kernel(const __grid_constant__ ChunkAttnParams p) {
-    extern __shared__ __align__(16) uint16_t smem[];
-    uint16_t *ks = smem, *vs = smem + kChunkKeys * kPitch;
-    __shared__ int s_odd;                     // the tile holds values that are not finite
-    const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
-    const float scale = kLog2e * 0.08838834764831845f;  // log2(e) / sqrt(128)
-    const int begin = range_begin(blockIdx.x, p.n_items, p.C), end = range_begin(blockIdx.x + 1, p.n_items, p.C);
-    for (int at = begin; at < end;) {
-        const Item it = find_item(p, at, kRows);
-        const int k0 = at - it.first, k1 = min(it.n, end - it.first);
-        const int valid = min(kRows, it.s.n_new * p.g - it.t * kRows);
-        const int np = it.s.T / kChunkKeys, ntail = it.s.ns + it.s.nr + it.s.n_new;
-        int row[2], lim[2];                   // this thread's rows; fp16 tokens each may see
+struct Bars {
+    uint64_t q_full, q_empty, k_full[kRing], k_empty[kRing], v_full[kRing], v_empty[kRing];
+    uint64_t s_full[2][2], p_full[2][2];              // of query tile m, step parity h
+    // (a wait names a phase by its parity, so no barrier may run two phases ahead of a waiter)
+    uint64_t pv_done[2][2], drain;
+    uint64_t o1_full, o1_free;                        // narrow units: O_1 and its sums are final, have been read
+    float2 state1[128];                               // (max, sum) of O_1's rows
+    uint64_t rawk[kMaxRaw], rawv[kMaxRaw];            // packed tile arrived
+    uint64_t readk[kMaxRaw], readv[kMaxRaw];          // packed tile read by all producers
+    uint32_t tmem;
+    int stop;
+    int odd[4];              // segment (+ 1) whose tail values are not all finite, by segment mod 4
+};
+constexpr int kSmemBytes = kOffBar + (int)sizeof(Bars);
+static_assert(kSmemBytes <= 232448, "shared memory");
+
+// Segment: the items of one unit inside the CTA's range; its end, and its steps.
+struct Seg {
+    Item it;
+    int k0, k1, np, valid, end, steps;
+    bool narrow;
+};
+__device__ __forceinline__ Seg next_seg(const ChunkAttnParams &p, int at, int end) {
+    Seg s;
+    s.it = find_item(p, at);
+    s.narrow = s.it.rows == kNarrowRows;
+    s.k0 = (at - s.it.first) / s.it.w;
+    s.k1 = min(s.it.n, (end - s.it.first) / s.it.w);
+    s.end = s.it.first + s.k1 * s.it.w;
+    s.np = s.it.s.T / kChunkKeys;
+    s.valid = min(s.it.rows, s.it.s.n_new * p.g - s.it.t * s.it.rows);
+    // a wide unit's last key tile may end in its first half
+    const int last = min(s.it.s.n_new, ((s.it.t + 1) * s.it.rows - 1) / p.g + 1);
+    const int seen = s.it.s.ns + s.it.s.nr + last - (s.it.n - s.np - 1) * kChunkKeys;
+    s.steps = 2 * (s.k1 - s.k0) - (!s.narrow && s.k1 == s.it.n && seen <= 64 ? 1 : 0);
+    return s;
+}
+
+__device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
+    uint32_t r;
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+    return r;
+}
+// A code's bits under the exponent of 1024 make 1024 + code 2^sh; one fused step makes the
+// exact code of it, another code * scale + min, rounded once.
+// A packed tile becomes an fp16 operand whose rows run along the packed direction (keys: a
+// row per token, channels contiguous; values: a row per channel, tokens contiguous).  A job
+// is one word row m and eight neighbouring columns: words w of two columns are split into
+// halves (the codes of the rows' first and second half, in pairs of columns), so that every
+// row is four half2, one 16-byte store.  wd: the eight words; s2, m2: (scale, min) of the
+// column pairs; dst: row 0 of the job at its 16-byte chunk, which row r xors with r mod 8.
+template <int BITS>
+__device__ __forceinline__ void deq_job(const uint32_t (&wd)[8], const uint32_t (&s2)[4], const uint32_t (&m2)[4], uint32_t dst) {
+    constexpr int N = 32 / BITS;                       // rows
+    constexpr uint32_t MASK = ((1u << BITS) - 1u) * 0x10001u;
+    constexpr int FIT = BITS == 2 ? 5 : BITS == 4 ? 2 : 1;  // codes of a half below bit 10
+#pragma unroll 1
+    for (int hf = 0; hf < 2; hf++) {
+        uint32_t x[4];
 #pragma unroll
-        for (int i = 0; i < 2; i++) {
-            row[i] = 16 * w + (lane >> 2) + 8 * i;
-            const int r = it.t * kRows + min(row[i], valid - 1);
-            lim[i] = it.s.ns + it.s.nr + r / p.g + 1;
-        }
-        uint32_t qf[8][4];
+        for (int c = 0; c < 4; c++) x[c] = prmt(wd[2 * c], wd[2 * c + 1], hf ? 0x7632 : 0x5410);
 #pragma unroll
-        for (int i = 0; i < 2; i++) {
-            const int r = it.t * kRows + min(row[i], valid - 1);
-            const uint16_t *src = p.q + (int64_t)(it.s.cu + r / p.g) * p.q_stride + (it.h * p.g + r % p.g) * kD + 2 * (lane & 3);
+        for (int j = 0; j < N / 2; j++) {
+            uint32_t y[4];
 #pragma unroll
-            for (int k = 0; k < 8; k++) {
-                qf[k][i] = *reinterpret_cast<const uint32_t *>(src + 16 * k);
-                qf[k][2 + i] = *reinterpret_cast<const uint32_t *>(src + 16 * k + 8);
+            for (int c = 0; c < 4; c++) {
+                if (j > 0 && j % FIT == 0) x[c] >>= FIT * BITS;
+                const uint32_t v = (x[c] & (MASK << (j % FIT * BITS))) | 0x64006400u;
+                const uint32_t mul = (uint32_t)(0x3c00 - ((j % FIT * BITS) << 10)) * 0x10001u;  // 2^-sh
+                const uint32_t sub = (uint32_t)(0xe400 - ((j % FIT * BITS) << 10)) * 0x10001u;  // -1024 2^-sh
+                y[c] = hfma2(hfma2(v, mul, sub), s2[c], m2[c]);
             }
+            const uint32_t at = (dst ^ ((j & 7) << 4)) + j * 128;
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3]) : "memory");
         }
-        float o[16][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-#pragma unroll
-        for (int n = 0; n < 16; n++)
-#pragma unroll
-            for (int e = 0; e < 4; e++) o[n][e] = 0.f;
-        bool odd = false;
-        for (int kt = k0; kt < k1; kt++) {
-            __syncthreads();
-            if (kt < np) {
-                const int64_t page = page_of(p, it, kt);
-                const int t0 = kt * kChunkKeys % p.G;
-                const int fk = 32 / p.kbits, fv = 32 / p.vbits, TV = 256 / p.kbits;
-                {  // keys: thread = channel
-                    const int32_t *src = p.k_codes + ((size_t)page * p.G + t0) / fk * kD;
-                    const float2 sm = unpack_half2(reinterpret_cast<const uint32_t *>(p.k_meta)[(size_t)page * kD + tid]);
-                    for (int r = 0; r < kChunkKeys / fk; r++) {
-                        uint32_t wd = (uint32_t)src[(size_t)r * kD + kword_pos(tid, t0 / fk + r)];
-                        for (int j = 0; j < fk; j++, wd >>= p.kbits)
-                            ks[(r * fk + j) * kPitch + tid] =
-                                __half_as_ushort(__float2half_rn(fmaf((float)(wd & ((1u << p.kbits) - 1)), sm.x, sm.y)));
-                    }
-                }
-                {  // values: thread = token
-                    const int tt = t0 + tid, j0 = tt % TV;
-                    const int32_t *src = p.v_codes + (size_t)page * p.G * (kD / fv) + (size_t)(tt / TV) * (kD / fv) * TV;
-                    const float2 sm = unpack_half2(reinterpret_cast<const uint32_t *>(p.v_meta)[(size_t)page * p.G + tt]);
-                    for (int r = 0; r < kD / fv; r++) {
-                        uint32_t wd = (uint32_t)src[r * TV + vword_pos(j0, r, TV)];
-                        for (int j = 0; j < fv; j++, wd >>= p.vbits)
-                            vs[tid * kPitch + r * fv + j] =
-                                __half_as_ushort(__float2half_rn(fmaf((float)(wd & ((1u << p.vbits) - 1)), sm.x, sm.y)));
-                    }
-                }
-                __syncthreads();
-            } else {
-                if (tid == 0) s_odd = 0;
-                __syncthreads();
-                bool bad = false;
-                for (int i = tid; i < kChunkKeys * 16; i += 128) {
-                    const int x = (kt - np) * kChunkKeys + (i >> 4), c = i & 15;
-                    uint4 a = make_uint4(0, 0, 0, 0), b = a;
-                    if (x < ntail) {
-                        a = reinterpret_cast<const uint4 *>(tail_row(p, it, x, false))[c];
-                        b = reinterpret_cast<const uint4 *>(tail_row(p, it, x, true))[c];
-                        // a value that is not finite would reach rows that may not see it (0 * inf):
-                        // it enters the product as 0 and is added to its rows at the end
-                        uint32_t *v = reinterpret_cast<uint32_t *>(&b);
-#pragma unroll
-                        for (int e = 0; e < 4; e++) {
-                            if ((v[e] & 0x7c00u) == 0x7c00u) v[e] &= 0xffff0000u, bad = true;
-                            if ((v[e] & 0x7c000000u) == 0x7c000000u) v[e] &= 0xffffu, bad = true;
-                        }
-                    }
-                    *reinterpret_cast<uint4 *>(ks + (i >> 4) * kPitch + 8 * c) = a;
-                    *reinterpret_cast<uint4 *>(vs + (i >> 4) * kPitch + 8 * c) = b;
-                }
-                if (bad) s_odd = 1;
-                __syncthreads();
-                odd |= s_odd != 0;
-            }
-            // s = q k^T: 16 rows x 128 keys
-            float s[16][4];
-#pragma unroll
-            for (int n = 0; n < 16; n++)
-#pragma unroll
-                for (int e = 0; e < 4; e++) s[n][e] = 0.f;
-#pragma unroll
-            for (int n = 0; n < 16; n++)
-#pragma unroll
-                for (int k = 0; k < 8; k += 2) {
-                    uint32_t b[4];
-                    ldmatrix_x4(b, smem_u32(ks + (8 * n + (lane & 7)) * kPitch + 16 * k + 8 * (lane >> 3)));
-                    mma_16816(s[n], qf[k][0], qf[k][1], qf[k][2], qf[k][3], b[0], b[1]);
-                    mma_16816(s[n], qf[k + 1][0], qf[k + 1][1], qf[k + 1][2], qf[k + 1][3], b[2], b[3]);
-                }
-            if (kt >= np) {
-                const int x0 = (kt - np) * kChunkKeys + 2 * (lane & 3);
-#pragma unroll
-                for (int n = 0; n < 16; n++)
-#pragma unroll
-                    for (int e = 0; e < 4; e++)
-                        if (x0 + 8 * n + (e & 1) >= lim[e >> 1]) s[n][e] = -INFINITY;
-            }
-#pragma unroll
-            for (int i = 0; i < 2; i++) {
-                float mx = -INFINITY;
-#pragma unroll
-                for (int n = 0; n < 16; n++) mx = fmaxf(mx, fmaxf(s[n][2 * i], s[n][2 * i + 1]));
-                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-                const float mn = fmaxf(m[i], mx * scale);
-                const float base = mn == -INFINITY ? 0.f : mn;  // a row that sees nothing yet keeps sum 0
-                const float corr = exp2f(m[i] - base);
-                m[i] = mn;
-                float sum = 0.f;
-#pragma unroll
-                for (int n = 0; n < 16; n++)
-#pragma unroll
-                    for (int e = 2 * i; e < 2 * i + 2; e++) {
-                        s[n][e] = exp2f(fmaf(s[n][e], scale, -base));
-                        sum += s[n][e];
-                    }
-                l[i] = l[i] * corr + sum;
-#pragma unroll
-                for (int n = 0; n < 16; n++) {
-                    o[n][2 * i] *= corr;
-                    o[n][2 * i + 1] *= corr;
-                }
-            }
-#pragma unroll
-            for (int k = 0; k < 8; k++) {
-                const uint32_t a0 = pack_half2(s[2 * k][0], s[2 * k][1]), a1 = pack_half2(s[2 * k][2], s[2 * k][3]);
-                const uint32_t a2 = pack_half2(s[2 * k + 1][0], s[2 * k + 1][1]), a3 = pack_half2(s[2 * k + 1][2], s[2 * k + 1][3]);
-#pragma unroll
-                for (int n = 0; n < 16; n += 2) {
-                    uint32_t b[4];
-                    ldmatrix_x4_trans(b, smem_u32(vs + (16 * k + (lane & 15)) * kPitch + 8 * n + 8 * (lane >> 4)));
-                    mma_16816(o[n], a0, a1, a2, a3, b[0], b[1]);
-                    mma_16816(o[n + 1], a0, a1, a2, a3, b[2], b[3]);
-                }
-            }
-        }
-        const bool whole = k0 == 0 && k1 == it.n;
-#pragma unroll
-        for (int i = 0; i < 2; i++) {
-            l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
-            l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
-        }
-        if (odd) {  // values that are not finite, in the tail tiles of this range
-            for (int i = 0; i < 2; i++)
-                for (int x = max(0, k0 - np) * kChunkKeys; x < min(lim[i], (k1 - np) * kChunkKeys); x++) {
-                    const uint16_t *v = tail_row(p, it, x, true);
-#pragma unroll
-                    for (int n = 0; n < 16; n++)
-#pragma unroll
-                        for (int e = 0; e < 2; e++) {
-                            const float f = h2f(v[8 * n + 2 * (lane & 3) + e]);
-                            if (!isfinite(f)) o[n][2 * i + e] += f;
-                        }
-                }
-        }
-        // the range's first segment has slot 2 c, its last one (a unit that goes on) 2 c + 1
-        const size_t slot = 2 * (size_t)blockIdx.x + (k0 == 0 && at != begin ? 1 : 0);
-#pragma unroll
-        for (int i = 0; i < 2; i++) {
-            if (row[i] >= valid) continue;
-            if (whole) {
-                const float inv = 1.0f / l[i];
-                const int r = it.t * kRows + row[i];
-                uint16_t *dst = p.out + ((int64_t)(it.s.cu + r / p.g) * p.H_kv * p.g + it.h * p.g + r % p.g) * kD + 2 * (lane & 3);
-#pragma unroll
-                for (int n = 0; n < 16; n++)
-                    *reinterpret_cast<uint32_t *>(dst + 8 * n) = pack_half2(o[n][2 * i] * inv, o[n][2 * i + 1] * inv);
-            } else {
-                if ((lane & 3) == 0) p.part_ml[slot * kRows + row[i]] = make_float2(m[i], l[i]);
-                float *dst = p.part_o + (slot * kRows + row[i]) * kD + 2 * (lane & 3);
-#pragma unroll
-                for (int n = 0; n < 16; n++) *reinterpret_cast<float2 *>(dst + 8 * n) = make_float2(o[n][2 * i], o[n][2 * i + 1]);
-            }
-        }
-        at = it.first + k1;
+        dst = (dst ^ ((N / 2 & 7) << 4)) + N / 2 * 128;  // the rows of the second half
     }
 }
 
-// Joins the partials of the unit that boundary x between two ranges cuts, if it is the
-// unit's first: 8 rows per CTA, a warp each.  Ranges are joined in order, so the result
-// does not depend on timing.
-__global__ void __launch_bounds__(256) chunk_combine_kernel(const __grid_constant__ ChunkAttnParams p, int rows) {
-    const int c0 = blockIdx.x, cut = range_begin(c0 + 1, p.n_items, p.C), begin = range_begin(c0, p.n_items, p.C);
-    const Item it = find_item(p, cut, rows);
-    if (it.first == cut || (it.first < begin)) return;  // not cut here, or cut before
-    const int c1 = range_of(it.first + it.n - 1, p.n_items, p.C);
-    const int row = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-    if (row >= min(rows, it.s.n_new * p.g - it.t * rows)) return;
-    const size_t s0 = 2 * (size_t)c0 + (it.first == begin ? 0 : 1);
-    float m = -INFINITY;
-    for (int c = c0; c <= c1; c++) m = fmaxf(m, p.part_ml[(c == c0 ? s0 : 2 * (size_t)c) * rows + row].x);
-    float l = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int c = c0; c <= c1; c++) {
-        const size_t s = (c == c0 ? s0 : 2 * (size_t)c) * rows + row;
-        const float2 ml = p.part_ml[s];
-        const float wgt = ml.x == -INFINITY && m != -INFINITY ? 0.f : exp2f(ml.x - m);
-        const float4 v = reinterpret_cast<const float4 *>(p.part_o + s * kD)[lane];
-        l += wgt * ml.y;
-        o.x += wgt * v.x;
-        o.y += wgt * v.y;
-        o.z += wgt * v.z;
-        o.w += wgt * v.w;
+__device__ __forceinline__ void lds128(uint32_t *r, uint32_t addr) {
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
+}
+
+// raw: codes [4 BITS word rows][128 columns] (values: tiles of TV columns, [rows][TV] each),
+// then 128 (scale, min).  Thread t takes columns 8 (t mod 16) .. + 7 of word rows t / 16 + 8 i.
+template <int BITS>
+__device__ __forceinline__ void make_tile(uint32_t raw, uint32_t tile, int t, int TV) {
+    const int c0 = 8 * (t & 15), m0 = t >> 4;
+    constexpr int N = 32 / BITS, NR = 4 * BITS;
+    uint32_t mt[8], s2[4], m2[4];
+    lds128(mt, raw + 4 * (512 * BITS + c0));
+    lds128(mt + 4, raw + 4 * (512 * BITS + c0) + 16);
+#pragma unroll
+    for (int c = 0; c < 4; c++) {
+        s2[c] = prmt(mt[2 * c], mt[2 * c + 1], 0x5410);
+        m2[c] = prmt(mt[2 * c], mt[2 * c + 1], 0x7632);
     }
-    const float inv = 1.0f / l;
-    const int r = it.t * rows + row;
-    uint16_t *dst = p.out + ((int64_t)(it.s.cu + r / p.g) * p.H_kv * p.g + it.h * p.g + r % p.g) * kD;
-    reinterpret_cast<uint2 *>(dst)[lane] = make_uint2(pack_half2(o.x * inv, o.y * inv), pack_half2(o.z * inv, o.w * inv));
+    const int j = c0 & (TV - 1);
+    const uint32_t src = raw + 4 * ((c0 - j) * NR);
+#pragma unroll 1
+    for (int i = 0; i < NR / 8; i++) {
+        const int m = m0 + 8 * i;
+        uint32_t wd[8];  // the row's 16-byte chunks are permuted by xor with m mod 8
+        lds128(wd, src + 4 * (m * TV + (j ^ ((m & 7) << 2))));
+        lds128(wd + 4, src + 4 * (m * TV + ((j + 4) ^ ((m & 7) << 2))));
+        // row N m; N is a multiple of 4: for 8-bit codes an odd word row starts inside an atom
+        const uint32_t row = tile + (c0 >> 6) * 16384 + m * N * 128 + ((((c0 >> 3) & 7) ^ ((m * N) & 7)) << 4);
+        deq_job<BITS>(wd, s2, m2, row);
+    }
+}
+
+// fp16 rows x0 .. x0 + 127 of [sink | residual | chunk]: row = token, 16-byte chunk c of a
+// row at block c / 8, position c ^ row within it (the layout of both tail operands: key
+// rows run along the tokens, value rows along the channels).  True if a value is not finite.
+__device__ __forceinline__ bool make_tail(const ChunkAttnParams &p, const Seg &s, int x0, bool value, unsigned char *tile, int tid) {
+    const int ntail = s.it.s.ns + s.it.s.nr + s.it.s.n_new, c = tid & 15;
+    bool bad = false;
+#pragma unroll 4
+    for (int r = tid >> 4; r < kChunkKeys; r += 8) {
+        uint4 a = make_uint4(0, 0, 0, 0);
+        if (x0 + r < ntail) {
+            a = __ldg(reinterpret_cast<const uint4 *>(tail_row(p, s.it, x0 + r, value)) + c);
+            if (value) {
+                uint32_t *v = reinterpret_cast<uint32_t *>(&a);
+#pragma unroll
+                for (int e = 0; e < 4; e++) {
+                    if ((v[e] & 0x7c00u) == 0x7c00u) v[e] &= 0xffff0000u, bad = true;
+                    if ((v[e] & 0x7c000000u) == 0x7c000000u) v[e] &= 0xffffu, bad = true;
+                }
+            }
+        }
+        *reinterpret_cast<uint4 *>(tile + (c >> 3) * 16384 + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = a;
+    }
+    return bad;
+}
+
+// ---------------------------------------------------------------- groups 2, 3: tiles --
+// Both groups run the same code (the kernel is as fast as its hot code is small: five roles
+// share an SM's instruction cache).
+__device__ __forceinline__ void produce(const ChunkAttnParams &p, unsigned char *sm, Bars *bar, bool value, int begin, int end) {
+    const int tid = threadIdx.x & 127, bits = value ? p.vbits : p.kbits;
+    const int kraw = 2048 * p.kbits + 512, vraw = 2048 * p.vbits + 512, size = value ? vraw : kraw;
+    const int slots = min(kMaxRaw, kRawBytes / (kraw + vraw));
+    unsigned char *raw = sm + kOffRaw + (value ? slots * kraw : 0);
+    unsigned char *ring = sm + (value ? kOffV : kOffK);
+    uint64_t *arrived = value ? bar->rawv : bar->rawk, *read = value ? bar->readv : bar->readk;
+    uint64_t *full = value ? bar->v_full : bar->k_full, *empty = value ? bar->v_empty : bar->k_empty;
+    const int32_t *codes = value ? p.v_codes : p.k_codes;
+    const uint16_t *meta = value ? p.v_meta : p.k_meta;
+    // a position in a ring of barriers: slot, and the parity of its next completion
+    struct Ring {
+        int i;
+        uint32_t parity;
+        __device__ __forceinline__ void next(int n) {
+            if (++i == n) i = 0, parity ^= 1;
+        }
+    };
+    Ring tile = {0, 1}, src = {0, 0}, cp = {0, 1};  // tiles made (their slots' release), packed tiles read, copies
+    int ahead = 0, seg = 0;                         // copies issued and not read (thread 0)
+    uint32_t nq = 1;
+    // thread 0: the copies of packed tile kt, once the slot's last tile has been read
+    auto copy = [&](const Seg &s, int kt) {
+        await(&read[cp.i], cp.parity, &bar->stop, p.status);
+        if (*(volatile int *)&bar->stop) return;
+        const int64_t page = page_of(p, s.it, kt);
+        const int t0 = kt * kChunkKeys & (p.G - 1);
+        unsigned char *dst = raw + cp.i * size;
+        mbar_arrive_expect_tx(&arrived[cp.i], size);
+        bulk_g2s(dst, codes + ((size_t)page * p.G + t0) * (kD * bits / 32), 2048 * bits, &arrived[cp.i]);
+        bulk_g2s(dst + 2048 * bits, meta + (value ? ((size_t)page * p.G + t0) * 2 : (size_t)page * kD * 2), 512, &arrived[cp.i]);
+        cp.next(slots);
+        ahead++;
+    };
+    for (int at = begin; at < end; seg++) {
+        const Seg s = next_seg(p, at, end);
+        at = s.end;
+        const int npk = min(s.k1, s.np);
+        if (tid == 0)
+            for (int kt = s.k0; kt < min(npk, s.k0 + slots); kt++) copy(s, kt);
+        if (value) {
+            // queries: 128-row tiles, rows of tokens' heads; rows behind the last one repeat it
+            await(&bar->q_empty, nq & 1, &bar->stop, p.status);
+            nq++;
+            const int ch = tid & 15, rows = (s.valid + 31) & ~31;  // whole warps of the softmax
+#pragma unroll 4
+            for (int r = tid >> 4; r < rows; r += 8) {
+                const int x = s.it.t * s.it.rows + min(r, s.valid - 1);
+                const uint4 a = __ldg(reinterpret_cast<const uint4 *>(p.q + (int64_t)(s.it.s.cu + x / p.g) * p.q_stride +
+                                                                      (s.it.h * p.g + x % p.g) * kD) + ch);
+                *reinterpret_cast<uint4 *>(sm + kOffQ + (r >> 7) * kTileBytes + (ch >> 3) * 16384 + (r & 127) * 128 +
+                                           (((ch & 7) ^ (r & 7)) << 4)) = a;
+            }
+            fence_proxy_async();
+            mbar_arrive(&bar->q_full);
+        }
+        for (int kt = s.k0; kt < s.k1; kt++) {
+            unsigned char *dst = ring + tile.i * kTileBytes;
+            await(&empty[tile.i], tile.parity, &bar->stop, p.status);
+            if (kt < s.np) {
+                await(&arrived[src.i], src.parity, &bar->stop, p.status);
+                const uint32_t from = smem_u32(raw + src.i * size), to = smem_u32(dst);
+                const int TV = value ? 256 / p.kbits : kChunkKeys;
+                if (bits == 2) make_tile<2>(from, to, tid, TV);
+                else if (bits == 4) make_tile<4>(from, to, tid, TV);
+                else make_tile<8>(from, to, tid, TV);
+                fence_proxy_async();
+                mbar_arrive(&full[tile.i]);
+                mbar_arrive(&read[src.i]);
+                src.next(slots);
+                ahead--;
+                if (tid == 0 && kt + slots < npk) copy(s, kt + slots);
+            } else {
+                if (make_tail(p, s, (kt - s.np) * kChunkKeys, value, dst, tid)) {
+                    // infinite and NaN values enter the product as 0 (0 weights of rows that may
+                    // not see them would spread them) and are added to their rows at the end
+                    *(volatile int *)&bar->odd[seg & 3] = seg + 1;
+                }
+                fence_proxy_async();
+                mbar_arrive(&full[tile.i]);
+            }
+            tile.next(kRing);
+        }
+    }
+    if (tid == 0)  // copies still in flight after an early end
+        for (; ahead > 0; ahead--, src.next(slots)) mbar_wait(&arrived[src.i], src.parity, p.status);
+}
+
+// ---------------------------------------------------------------- group 4: products ---
+// Rows along M and N (keys: tokens, packed values: channels): 16 of the contracted dimension
+// are 32 bytes of a row; fp16 value rows run along the tokens: 16 are two atoms.
+
+// Warp 16 + m: the scores S_m.  A buffer's next scores go over its old weights, once the
+// product that reads those has ended.
+__device__ __forceinline__ void issue_scores(const ChunkAttnParams &p, unsigned char *sm, Bars *bar, uint32_t tm, int m, int begin, int end) {
+    const uint32_t base = smem_u32(sm), lead = (threadIdx.x & 31) == 0;
+    uint32_t n = 0, nq = 0;       // key tiles, query tiles
+    uint32_t ph = 0, any = 0;     // per buffer h: parity of the products awaited, whether there was one
+    auto wait = [&](uint64_t *b, uint32_t parity) { warp_await(b, parity & 1, &bar->stop, p.status); };
+    auto ready = [&](int h) {     // buffer h may be written
+        if ((any >> h) & 1) wait(&bar->pv_done[m][h], ph >> h);
+        ph ^= ((any >> h) & 1) << h;
+        any |= 1u << h;
+    };
+    auto scores = [&](int q, int h, uint32_t slot, uint32_t idesc) {
+        tc_fence_after();
+        const uint64_t a0 = smem_desc(base + kOffQ + q * kTileBytes, 16, 1024);
+        const uint64_t b0 = smem_desc(base + kOffK + slot * kTileBytes + h * 8192, 16, 1024);
+#pragma unroll
+        for (int k = 0; k < 8; k++) {
+            const uint32_t off = ((k >> 2) * 16384 + (k & 3) * 32) >> 4;
+            mma_ss(tm + m * 128 + h * 64, a0 + off, b0 + off, idesc, k > 0, lead);
+        }
+        tc_commit(&bar->s_full[m][h], lead);
+    };
+    for (int at = begin; at < end;) {
+        const Seg s = next_seg(p, at, end);
+        at = s.end;
+        wait(&bar->q_full, nq);
+        nq++;
+        const int tiles = s.k1 - s.k0;
+        for (int j = 0; j < tiles; j++) {
+            const uint32_t slot = n % kRing;
+            wait(&bar->k_full[slot], n / kRing);
+            n++;
+            if (s.narrow ? (j & 1) == m : 128 * m < s.valid) {
+                if (s.narrow) {
+                    ready(0);
+                    ready(1);
+                    scores(0, 0, slot, f16_idesc(128, 128, false));  // both buffers
+                    tc_commit(&bar->s_full[m][1], lead);
+                } else {
+#pragma unroll 1
+                    for (int h = 0; h < 2 && 2 * j + h < s.steps; h++) {
+                        ready(h);
+                        scores(m, h, slot, f16_idesc(128, 64, false));
+                    }
+                }
+                tc_commit(&bar->k_empty[slot], lead);
+            } else if (lead) {
+                mbar_arrive(&bar->k_empty[slot]);
+            }
+            __syncwarp();
+        }
+        tc_commit(&bar->q_empty, lead);
+    }
+}
+
+// Warp 18 + m: the products O_m += P_m V.
+__device__ __forceinline__ void issue_values(const ChunkAttnParams &p, unsigned char *sm, Bars *bar, uint32_t tm, int m, int begin, int end) {
+    const uint32_t base = smem_u32(sm), lead = (threadIdx.x & 31) == 0;
+    uint32_t n = 0, ph = 0;       // value tiles; per buffer h: parity of the weights awaited
+    auto wait = [&](uint64_t *b, uint32_t parity) { warp_await(b, parity & 1, &bar->stop, p.status); };
+    for (int at = begin; at < end;) {
+        const Seg s = next_seg(p, at, end);
+        at = s.end;
+        const int tiles = s.k1 - s.k0, steps = s.narrow ? 2 * tiles : s.steps;
+        bool acc = false;
+        for (int j = 0; j < tiles; j++) {
+            const uint32_t slot = n % kRing, vb = base + kOffV + slot * kTileBytes;
+            wait(&bar->v_full[slot], n / kRing);
+            n++;
+            if (s.narrow ? (j & 1) == m : 128 * m < s.valid) {
+                const bool packed = s.k0 + j < s.np;
+                const uint32_t id = packed ? f16_idesc(128, 128, false) : f16_idesc(128, 128, true);
+                const uint64_t b0 = packed ? smem_desc(vb, 16, 1024) : smem_desc(vb, 16384, 1024);
+                const uint32_t step = (packed ? 32 : 2048) >> 4, half = (packed ? 16384 : 8192) >> 4;
+#pragma unroll 1
+                for (int h = 0; h < 2 && 2 * j + h < steps; h++) {
+                    wait(&bar->p_full[m][h], ph >> h);
+                    ph ^= 1u << h;
+                    tc_fence_after();
+#pragma unroll
+                    for (int k = 0; k < 4; k++)
+                        mma_ts(tm + 256 + m * 128, tm + m * 128 + h * 64 + 8 * k, b0 + (h * half + k * step), id, acc || k > 0, lead);
+                    acc = true;
+                    tc_commit(&bar->pv_done[m][h], lead);
+                }
+                tc_commit(&bar->v_empty[slot], lead);
+            } else if (lead) {
+                mbar_arrive(&bar->v_empty[slot]);
+            }
+            __syncwarp();
+        }
+    }
+}
+
+// ---------------------------------------------------------------- groups 0, 1 ---------
+// Scores of 64 keys: those from the n-th on are not seen.
+__device__ __forceinline__ void mask64(uint32_t *x, int n) {
+#pragma unroll
+    for (int c = 0; c < 64; c++)
+        if (c >= n) x[c] = 0xff800000u;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+__device__ __forceinline__ float max64(const float *f) {
+    float t[8];
+#pragma unroll
+    for (int e = 0; e < 8; e++) t[e] = f[e];
+#pragma unroll
+    for (int c = 8; c < 56; c += 16)
+#pragma unroll
+        for (int e = 0; e < 8; e++) t[e] = max3(t[e], f[c + 2 * e], f[c + 2 * e + 1]);
+#pragma unroll
+    for (int e = 0; e < 8; e++) t[e] = fmaxf(t[e], f[56 + e]);
+    return fmaxf(max3(t[0], t[1], t[2]), max3(max3(t[3], t[4], t[5]), t[6], t[7]));
+}
+// Weights 2^(s scale + off) of 64 scores, as 32 half2 in place; returns their sum.
+__device__ __forceinline__ float weights64(uint32_t *x, float off) {
+    uint64_t l0 = 0, l1 = 0;
+    const uint64_t sc2 = pair_of(kScale, kScale), of2 = pair_of(off, off);
+    const float *f = reinterpret_cast<const float *>(x);
+#pragma unroll
+    for (int c = 0; c < 64; c += 4) {
+        float2 a = of_pair(fma_pair(pair_of(f[c], f[c + 1]), sc2, of2)), b = of_pair(fma_pair(pair_of(f[c + 2], f[c + 3]), sc2, of2));
+        a.x = ex2(a.x);
+        a.y = ex2(a.y);
+        b.x = ex2(b.x);
+        b.y = ex2(b.y);
+        l0 = add_pair(l0, pair_of(a.x, a.y));
+        l1 = add_pair(l1, pair_of(b.x, b.y));
+        x[c >> 1] = pack_half2(a.x, a.y);
+        x[(c >> 1) + 1] = pack_half2(b.x, b.y);
+    }
+    const float2 ls = of_pair(add_pair(l0, l1));
+    return ls.x + ls.y;
+}
+
+// Parities of a softmax group's barriers and the row's state.
+struct RowState {
+    uint32_t ns, given, no1;  // per buffer h: parity of the weights given, any given; narrow units joined
+    float mx, l;
+};
+
+// The scores of step buffer h as weights' arguments, those of unseen keys as -inf.
+__device__ __forceinline__ void load_scores(uint32_t (&x)[64], uint32_t ts, int y) {
+    tmem_ld32(x, ts);
+    tmem_ld32(x + 32, ts + 32);
+    tmem_wait_ld();
+#pragma unroll
+    for (int c = 0; c < 4; c++) tmem_tie16(x + 16 * c);
+    if (y < 64) mask64(x, y);
+}
+
+// The steps of one segment for query tile or key parity m; narrow units: every second key
+// tile.  ts, to: tensor memory of S_m and O_m; lim: fp16 tokens the row may see; any: whether
+// the warp has rows at all.  The weights are formed with the maximum of the steps before,
+// which lets them overlap the search for this step's; the rare step that raises it by more
+// than 2^kLag forms them again.
+template <bool NARROW>
+__device__ __forceinline__ void softmax_steps(const ChunkAttnParams &p, Bars *bar, const Seg &s, RowState &st, uint32_t ts, uint32_t to,
+                                              int m, int lim, bool any) {
+    const int steps = NARROW ? 2 * ((s.k1 - s.k0 - m + 1) >> 1) : s.steps;
+    float mx = -INFINITY, l = 0.f;
+    for (int i = 0; i < steps; i++) {
+        const int h = i & 1, kt = s.k0 + (NARROW ? 2 * (i >> 1) + m : i >> 1);
+        warp_await(&bar->s_full[m][h], (st.ns >> h) & 1, &bar->stop, p.status);
+        if (any) {
+            tc_fence_after();
+            const int y = kt >= s.np ? lim - (kt - s.np) * kChunkKeys - 64 * h : 64;  // keys it may see
+            uint32_t x[64];
+            load_scores(x, ts + 64 * h, y);
+            const float cand = max64(reinterpret_cast<const float *>(x)) * kScale;
+            float off = kUp - (mx == -INFINITY ? 0.f : mx), add = weights64(x, off);
+            const bool grow = cand > mx + kLag || (mx == -INFINITY && cand > -INFINITY);
+            if (__any_sync(0xffffffffu, grow)) {
+                const float corr = grow ? ex2(mx - cand) : 1.f;
+                if (grow) mx = cand;
+                l *= corr;
+                if (i > 0) {
+                    // the step before was the last to write O
+                    warp_await(&bar->pv_done[m][h ^ 1], (~st.ns >> (h ^ 1)) & 1, &bar->stop, p.status);
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int c = 0; c < 8; c++) {
+                        tmem_ld16(x, to + 16 * c);
+                        tmem_wait_ld();
+                        tmem_tie16(x);
+#pragma unroll
+                        for (int e = 0; e < 16; e++) x[e] = __float_as_uint(__uint_as_float(x[e]) * corr);
+                        tmem_st16(to + 16 * c, x);
+                    }
+                }
+                load_scores(x, ts + 64 * h, y);
+                off = kUp - (mx == -INFINITY ? 0.f : mx);
+                add = weights64(x, off);
+            }
+            tmem_st32(ts + 64 * h, x);  // over the scores
+            l += add;
+            tmem_wait_st();
+        }
+        // a segment's first weights let their product overwrite O_1: once it has been read
+        if (m == 1 && i == 0 && st.no1 > 0) warp_await(&bar->o1_free, (st.no1 - 1) & 1, &bar->stop, p.status);
+        tc_fence_before();
+        mbar_arrive(&bar->p_full[m][h]);
+        st.ns ^= 1u << h;
+        st.given |= 1u << h;
+    }
+    st.mx = mx;
+    st.l = l;
+}
+
+__device__ __forceinline__ void softmax(const ChunkAttnParams &p, Bars *bar, uint32_t tm, int m, int begin, int end) {
+    const int lane_row = threadIdx.x & 127;
+    const uint32_t lanes = (uint32_t)(threadIdx.x & 96) << 16;
+    const uint32_t ts = tm + lanes + m * 128, to = tm + lanes + 256 + m * 128;
+    RowState st = {0, 0, 0, 0.f, 0.f};
+    int seg = 0;
+    for (int at = begin; at < end; seg++) {
+        const Seg s = next_seg(p, at, end);
+        const bool last_first = s.k0 == 0 && at != begin;
+        const int base = s.narrow ? 0 : 128 * m, row = base + lane_row;
+        at = s.end;
+        const int n = s.k1 - s.k0;
+        if (base >= s.valid || (s.narrow && m >= n)) continue;
+        const bool any = base + (lane_row & 96) < s.valid;
+        const int r = s.it.t * s.it.rows + min(row, s.valid - 1);
+        const int lim = s.it.s.ns + s.it.s.nr + r / p.g + 1;
+        const bool join = s.narrow && n > 1;
+        if (s.narrow) softmax_steps<true>(p, bar, s, st, ts, to, m, lim, any);
+        else softmax_steps<false>(p, bar, s, st, ts, to, m, lim, any);
+        float mx = st.mx, l = st.l;
+        for (int h = 0; h < 2; h++)  // the last products
+            if ((st.given >> h) & 1) warp_await(&bar->pv_done[m][h], (~st.ns >> h) & 1, &bar->stop, p.status);
+        tc_fence_after();
+        float a0 = 1.f, a1 = 0.f;
+        if (join) {
+            st.no1++;
+            if (m == 1) {
+                bar->state1[lane_row] = make_float2(mx, l);
+                tc_fence_before();
+                mbar_arrive(&bar->o1_full);
+                continue;
+            }
+            warp_await(&bar->o1_full, (st.no1 - 1) & 1, &bar->stop, p.status);
+            tc_fence_after();
+            const float2 other = bar->state1[lane_row];
+            const float mn = fmaxf(mx, other.x);
+            a0 = mx == mn ? 1.f : ex2(mx - mn);
+            a1 = other.x == mn ? 1.f : ex2(other.x - mn);
+            mx = mn;
+            l = a0 * l + a1 * other.y;
+        }
+        const bool whole = s.k0 == 0 && s.k1 == s.it.n;
+        const bool odd = *(volatile int *)&bar->odd[seg & 3] == seg + 1;
+        const float inv = 1.f / l;
+        // the range's first segment has slot 2 c, its last one (a unit that goes on) 2 c + 1
+        const size_t slot = (2 * (size_t)blockIdx.x + (last_first ? 1 : 0)) * kRows + row;
+        uint16_t *dst = p.out + ((int64_t)(s.it.s.cu + r / p.g) * p.H_kv * p.g + s.it.h * p.g + r % p.g) * kD;
+        if (any) {
+            if (!whole && row < s.valid) p.part_ml[slot] = make_float2(mx, l);
+#pragma unroll 1
+            for (int c = 0; c < 8; c++) {
+                uint32_t o[16];
+                float *f = reinterpret_cast<float *>(o);
+                tmem_ld16(o, to + 16 * c);
+                tmem_wait_ld();
+                tmem_tie16(o);
+                if (join) {
+                    uint32_t o1[16];
+                    tmem_ld16(o1, to + 128 + 16 * c);
+                    tmem_wait_ld();
+                    tmem_tie16(o1);
+#pragma unroll
+                    for (int e = 0; e < 16; e++) f[e] = a0 * f[e] + a1 * __uint_as_float(o1[e]);
+                }
+                if (odd)
+                    for (int x = max(0, s.k0 - s.np) * kChunkKeys; x < min(lim, (s.k1 - s.np) * kChunkKeys); x++) {
+                        const uint16_t *v = tail_row(p, s.it, x, true) + 16 * c;
+#pragma unroll
+                        for (int e = 0; e < 16; e++) {
+                            const float y = h2f(v[e]);
+                            if (!isfinite(y)) f[e] += y;
+                        }
+                    }
+                if (row < s.valid) {
+                    if (whole) {
+                        uint4 y[2];
+                        uint32_t *w = reinterpret_cast<uint32_t *>(y);
+#pragma unroll
+                        for (int e = 0; e < 8; e++) w[e] = pack_half2(f[2 * e] * inv, f[2 * e + 1] * inv);
+                        reinterpret_cast<uint4 *>(dst)[2 * c] = y[0];
+                        reinterpret_cast<uint4 *>(dst)[2 * c + 1] = y[1];
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 4; e++)
+                            reinterpret_cast<float4 *>(p.part_o + slot * kD)[4 * c + e] =
+                                make_float4(f[4 * e], f[4 * e + 1], f[4 * e + 2], f[4 * e + 3]);
+                    }
+                }
+                __syncwarp();
+            }
+        }
+        tc_fence_before();
+        if (join) mbar_arrive(&bar->o1_free);
+    }
+}
+
+__global__ void __launch_bounds__(kThreads, 1) chunk_attn_kernel(const __grid_constant__ ChunkAttnParams p) {
+    extern __shared__ __align__(1024) unsigned char sm[];  // swizzle atoms are 1024 bytes
+    Bars *bar = reinterpret_cast<Bars *>(sm + kOffBar);
+    const int w = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
+    if (threadIdx.x == 0) {
+        mbar_init(&bar->q_full, 128);
+        mbar_init(&bar->q_empty, 2);
+        for (int i = 0; i < kRing; i++) {
+            mbar_init(&bar->k_full[i], 128);
+            mbar_init(&bar->k_empty[i], 2);
+            mbar_init(&bar->v_full[i], 128);
+            mbar_init(&bar->v_empty[i], 2);
+        }
+        for (int i = 0; i < 2; i++) {
+            mbar_init(i ? &bar->o1_free : &bar->o1_full, 128);
+            for (int h = 0; h < 2; h++) {
+                mbar_init(&bar->s_full[i][h], 1);
+                mbar_init(&bar->p_full[i][h], 128);
+                mbar_init(&bar->pv_done[i][h], 1);
+            }
+        }
+        mbar_init(&bar->drain, 4);
+        for (int i = 0; i < kMaxRaw; i++) {
+            mbar_init(&bar->rawk[i], 1);
+            mbar_init(&bar->rawv[i], 1);
+            mbar_init(&bar->readk[i], 128);
+            mbar_init(&bar->readv[i], 128);
+        }
+        bar->stop = 0;
+        for (int i = 0; i < 4; i++) bar->odd[i] = 0;
+        fence_barrier_init();
+    }
+    if (w == 16) tmem_alloc(&bar->tmem);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tm = bar->tmem;
+    const int begin = range_begin(p, blockIdx.x), end = range_begin(p, blockIdx.x + 1);
+    if (w < 8) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+        softmax(p, bar, tm, w >> 2, begin, end);
+    } else if (w < 16) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsTiles));
+        produce(p, sm, bar, w >= 12, begin, end);
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsMul));
+        if (w < 18) issue_scores(p, sm, bar, tm, w & 1, begin, end);
+        else issue_values(p, sm, bar, tm, w & 1, begin, end);
+        __syncwarp();
+        tc_commit(&bar->drain, (threadIdx.x & 31) == 0);
+        mbar_wait(&bar->drain, 0, p.status);  // every product has ended before the tensor memory is freed
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (w == 16) tmem_free(tm);
 }
 
 }  // namespace
 
-cudaError_t launch_chunk_attn(const ChunkAttnParams &p, int rows, cudaStream_t st) {
-    cudaError_t e;
-    if (rows == kWideRows) {
-        if ((e = launch_chunk_wide(p, st)) != cudaSuccess) return e;
-    } else {
-        const int smem = 2 * kChunkKeys * kPitch * 2;
-        e = cudaFuncSetAttribute(chunk_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-        if (e != cudaSuccess) return e;
-        chunk_attn_kernel<<<p.C, 128, smem, st>>>(p);
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    }
-    if (p.C > 1) {
-        chunk_combine_kernel<<<dim3((unsigned)(p.C - 1), (unsigned)(rows / 8)), 256, 0, st>>>(p, rows);
-        e = cudaGetLastError();
-    }
-    return e;
+cudaError_t launch_chunk_combine(const ChunkAttnParams &p, cudaStream_t st);
+
+cudaError_t launch_chunk_attn(const ChunkAttnParams &p, cudaStream_t st) {
+    cudaError_t e = cudaFuncSetAttribute(chunk_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+    if (e != cudaSuccess) return e;
+    chunk_attn_kernel<<<p.C, kThreads, kSmemBytes, st>>>(p);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    return launch_chunk_combine(p, st);
 }
 
 }  // namespace kvq

@@ -14,11 +14,12 @@ namespace kvq {
 constexpr int kD = 128;
 constexpr float kLog2e = 1.4426950408889634f;
 
-// Where an item lies: slot, key head, row tile, key tile, and the unit's item range.
+// Where a position lies: slot, key head, row tile; the unit's first position and number of
+// items, the cost of each, and its query rows.
 struct Item {
     ChunkSlot s;
     int b, h, t;
-    int first, n;          // first item of the unit, its number of items
+    int first, n, w, rows;
 };
 
 __device__ __forceinline__ ChunkSlot load_slot(const int32_t *desc, int b) {
@@ -27,41 +28,44 @@ __device__ __forceinline__ ChunkSlot load_slot(const int32_t *desc, int b) {
     return {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
 }
 
-__device__ __forceinline__ Item find_item(const ChunkAttnParams &p, int it, int rows) {
+__device__ __forceinline__ int slot_of(const ChunkAttnParams &p, int pos) {
     int lo = 0, hi = p.B - 1;
     while (lo < hi) {
         const int mid = (lo + hi) >> 1;
-        if (p.item0[mid + 1] > it) hi = mid;
+        if (p.cost0[mid + 1] > pos) hi = mid;
         else lo = mid + 1;
     }
+    return lo;
+}
+
+__device__ __forceinline__ Item find_item(const ChunkAttnParams &p, int pos) {
     Item r;
-    r.b = lo;
-    r.s = load_slot(p.desc, lo);
-    const int per = (p.item0[lo + 1] - p.item0[lo]) / p.H_kv;  // items of one head
-    int x = it - p.item0[lo];
+    r.b = slot_of(p, pos);
+    r.s = load_slot(p.desc, r.b);
+    const bool narrow = chunk_narrow(r.s.n_new, p.g);
+    r.rows = narrow ? kNarrowRows : kWideRows;
+    r.w = narrow ? kNarrowCost : kWideCost;
+    const int per = (p.cost0[r.b + 1] - p.cost0[r.b]) / p.H_kv;  // cost of one head
+    int x = pos - p.cost0[r.b];
     r.h = x / per;
-    x -= r.h * per;
+    x = (x - r.h * per) / r.w;
     int t = 0, a = 0;
     for (;; t++) {
-        const int n = chunk_tiles(r.s, t, rows, p.g);
-        if (x < a + n) {
-            r.n = n;
-            break;
-        }
-        a += n;
+        r.n = chunk_tiles(r.s, t, r.rows, p.g);
+        if (x < a + r.n) break;
+        a += r.n;
     }
     r.t = t;
-    r.first = p.item0[lo] + r.h * per + a;
+    r.first = p.cost0[r.b] + r.h * per + a * r.w;
     return r;
 }
 
-// CTA whose range holds item x: ranges [c N / C, (c + 1) N / C).
-__host__ __device__ __forceinline__ int range_begin(int c, int N, int C) { return (int)((int64_t)c * N / C); }
-__device__ __forceinline__ int range_of(int x, int N, int C) {
-    int c = (int)(((int64_t)x * C) / N);
-    while (c + 1 < C && range_begin(c + 1, N, C) <= x) c++;
-    while (range_begin(c, N, C) > x) c--;
-    return c;
+// First position of range c: an item starts there.
+__device__ __forceinline__ int range_begin(const ChunkAttnParams &p, int c) {
+    const int pos = (int)((int64_t)c * p.cost / p.C);
+    if (pos >= p.cost) return p.cost;
+    const int b = slot_of(p, pos), w = chunk_narrow(p.desc[8 * b + 3], p.g) ? kNarrowCost : kWideCost;
+    return p.cost0[b] + (pos - p.cost0[b] + w - 1) / w * w;
 }
 
 // Row of fp16 token x of [sink | residual | chunk].

@@ -9,25 +9,27 @@
 
 namespace kvq {
 
-// Waits for phase `parity` of bar.  Gives up, with a status bit, after kWaitLimitCycles, or
-// once another warp has given up (*stop); the caller then leaves its loop.
-__device__ __forceinline__ bool wait_or_stop(uint64_t *bar, uint32_t parity, volatile int *stop, int32_t *status) {
-    if (mbar_try_wait(bar, parity)) return true;
+// Waits for phase `parity` of bar.  After kWaitLimitCycles it gives up: it sets a status bit
+// and *stop, with which every later wait of the CTA returns at once, so that the kernel runs
+// to its end (with wrong results).  The common case, a phase that is already complete, is a
+// few instructions: a warp that only passes data on competes for issue slots with warps that
+// compute, and every instruction it needs delays all of them.
+__device__ __forceinline__ void await(uint64_t *bar, uint32_t parity, volatile int *stop, int32_t *status) {
+    if (mbar_try_wait(bar, parity)) return;
     const long long t0 = clock64();
     while (!mbar_try_wait(bar, parity)) {
-        if (*stop) return false;
+        if (*stop) return;
         if (clock64() - t0 > kWaitLimitCycles) {
             report(status, 1 /*KVQ_DEV_TIMEOUT*/);
             *stop = 1;
-            return false;
         }
     }
-    return true;
 }
 
 // The same for a whole warp, which stays together.
-__device__ __forceinline__ bool warp_wait_or_stop(uint64_t *bar, uint32_t parity, volatile int *stop, int32_t *status) {
-    return __all_sync(0xffffffffu, wait_or_stop(bar, parity, stop, status));
+__device__ __forceinline__ void warp_await(uint64_t *bar, uint32_t parity, volatile int *stop, int32_t *status) {
+    await(bar, parity, stop, status);
+    __syncwarp();
 }
 
 // 2^x (hardware approximation, relative error below 2^-22; results below 2^-126 are 0).
@@ -72,12 +74,7 @@ __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence:
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
 // Products are issued by a warp that stays together, so that descriptors are computed once
-// for the warp; `lead` (1 in one lane, elect_lane) names the lane whose instruction it is.
-__device__ __forceinline__ uint32_t elect_lane() {
-    uint32_t r;
-    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
-    return r;
-}
+// for the warp; `lead` (1 in one lane, 0 in the others) names the lane whose instruction it is.
 
 // One arrival on bar once every matrix product this thread has issued is complete.
 __device__ __forceinline__ void tc_commit(uint64_t *bar, uint32_t lead) {
