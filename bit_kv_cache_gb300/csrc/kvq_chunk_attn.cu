@@ -8,9 +8,8 @@
 //
 // One CTA per SM, five groups of four warps:
 //   groups 0, 1  softmax, a thread per row of 128: reads the scores S_m from tensor memory,
-//                keeps the row's running maximum and sum in registers, writes the weights
-//                P_m over S_m as fp16, rescales O_m when the maximum has grown by more than
-//                2^8;
+//                keeps a reference near the row's running maximum and the sum in registers,
+//                writes the weights P_m over S_m as fp16, rescales O_m when the reference moves;
 //   groups 2, 3  make the key and the value tiles: packed pages arrive by bulk copies and
 //                are dequantized into fp16 tiles in shared memory, fp16 rows are gathered;
 //   group 4      warps 16 + m issue the products S_m = Q K^T, warps 18 + m O_m += P_m V: each
@@ -41,9 +40,10 @@ constexpr int kMaxRaw = 4;
 constexpr int kOffQ = 0, kOffK = 2 * kTileBytes, kOffV = kOffK + kRing * kTileBytes, kOffRaw = kOffV + kRing * kTileBytes,
               kOffBar = kOffRaw + kRawBytes;
 constexpr float kScale = kLog2e * 0.08838834764831845f;  // log2(e) / sqrt(128)
-// Weights are 2^(s - m + kUp): the running maximum may lag by kLag, so they stay below
-// 2^(kUp + kLag) < 65504, and small ones keep kUp more bits above fp16's smallest step.
-constexpr float kUp = 6.f, kLag = 8.f;
+// Weights are 2^(s - m + kUp) with a reference m that may lag behind the maximum while 64
+// weights sum to kMostSum at most, below fp16's 65504; kUp more bits keep small weights
+// above fp16's smallest step.
+constexpr float kUp = 6.f, kMostSum = 16384.f;
 // registers of a thread after the split; 96 at launch, times 640 threads
 constexpr int kRegsSoftmax = 120, kRegsTiles = 72, kRegsMul = 96;
 static_assert(256 * kRegsSoftmax + 256 * kRegsTiles + 128 * kRegsMul <= kThreads * 96, "register split");
@@ -437,9 +437,9 @@ __device__ __forceinline__ void load_scores(uint32_t (&x)[64], uint32_t ts, int 
 
 // The steps of one segment for query tile or key parity m; narrow units: every second key
 // tile.  ts, to: tensor memory of S_m and O_m; lim: fp16 tokens the row may see; any: whether
-// the warp has rows at all.  The weights are formed with the maximum of the steps before,
-// which lets them overlap the search for this step's; the rare step that raises it by more
-// than 2^kLag forms them again.
+// the warp has rows at all.  The weights are formed with a reference mx that some earlier
+// step's maximum gave: their sum tells whether one of them is above 2^(kUp + kLag), and only
+// then the maximum is looked for and the weights are formed again.
 template <bool NARROW>
 __device__ __forceinline__ void softmax_steps(const ChunkAttnParams &p, Bars *bar, const Seg &s, RowState &st, uint32_t ts, uint32_t to,
                                               int m, int lim, bool any) {
@@ -453,10 +453,11 @@ __device__ __forceinline__ void softmax_steps(const ChunkAttnParams &p, Bars *ba
             const int y = kt >= s.np ? lim - (kt - s.np) * kChunkKeys - 64 * h : 64;  // keys it may see
             uint32_t x[64];
             load_scores(x, ts + 64 * h, y);
-            const float cand = max64(reinterpret_cast<const float *>(x)) * kScale;
-            float off = kUp - (mx == -INFINITY ? 0.f : mx), add = weights64(x, off);
-            const bool grow = cand > mx + kLag || (mx == -INFINITY && cand > -INFINITY);
-            if (__any_sync(0xffffffffu, grow)) {
+            float add = weights64(x, kUp - mx);                  // infinite or NaN without a reference
+            if (__any_sync(0xffffffffu, !(add <= kMostSum))) {
+                load_scores(x, ts + 64 * h, y);
+                const float cand = max64(reinterpret_cast<const float *>(x)) * kScale;
+                const bool grow = cand > mx;
                 const float corr = grow ? ex2(mx - cand) : 1.f;
                 if (grow) mx = cand;
                 l *= corr;
@@ -474,9 +475,8 @@ __device__ __forceinline__ void softmax_steps(const ChunkAttnParams &p, Bars *ba
                         tmem_st16(to + 16 * c, x);
                     }
                 }
-                load_scores(x, ts + 64 * h, y);
-                off = kUp - (mx == -INFINITY ? 0.f : mx);
-                add = weights64(x, off);
+                if (i > 0) load_scores(x, ts + 64 * h, y);
+                add = weights64(x, kUp - (mx == -INFINITY ? 0.f : mx));
             }
             tmem_st32(ts + 64 * h, x);  // over the scores
             l += add;
