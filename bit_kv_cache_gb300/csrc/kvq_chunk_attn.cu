@@ -209,10 +209,10 @@ __device__ __forceinline__ void produce(const ChunkAttnParams &p, unsigned char 
     int ahead = 0, seg = 0;                         // copies issued and not read (thread 0)
     uint32_t nq = 1;
     // thread 0: the copies of packed tile kt, once the slot's last tile has been read
-    auto copy = [&](const Seg &s, int kt) {
+    auto copy = [&](const Seg &s, int kt, int32_t entry) {
         await(&read[cp.i], cp.parity, &bar->stop, p.status);
         if (*(volatile int *)&bar->stop) return;
-        const int64_t page = page_of(p, s.it, kt);
+        const int64_t page = page_index(p, s.it, entry);
         const int t0 = kt * kChunkKeys & (p.G - 1);
         unsigned char *dst = raw + cp.i * size;
         mbar_arrive_expect_tx(&arrived[cp.i], size);
@@ -221,12 +221,26 @@ __device__ __forceinline__ void produce(const ChunkAttnParams &p, unsigned char 
         cp.next(slots);
         ahead++;
     };
+    // A tile's copy goes to the slot of the tile `slots` before it.  With two slots or more it
+    // is issued a tile later than it could be, when that slot's readers are long done, and its
+    // page-table entry is read a tile before: thread 0 then waits for neither.
+    const int lag = slots > 1 ? 1 : 0, lead = slots - lag;
     for (int at = begin; at < end; seg++) {
         const Seg s = next_seg(p, at, end);
         at = s.end;
         const int npk = min(s.k1, s.np);
-        if (tid == 0)
-            for (int kt = s.k0; kt < min(npk, s.k0 + slots); kt++) copy(s, kt);
+        int32_t entry = 0;
+        if (tid == 0 && s.k0 < npk) {
+            int32_t first[kMaxRaw + 1];
+#pragma unroll
+            for (int i = 0; i <= kMaxRaw; i++) first[i] = page_entry(p, s.it, min(s.k0 + i, npk - 1));
+#pragma unroll
+            for (int i = 0; i < kMaxRaw; i++)
+                if (i < lead && s.k0 + i < npk) copy(s, s.k0 + i, first[i]);
+#pragma unroll
+            for (int i = 0; i <= kMaxRaw; i++)
+                if (i == lead) entry = first[i];
+        }
         if (value) {
             // queries: 128-row tiles, rows of tokens' heads; rows behind the last one repeat it
             await(&bar->q_empty, nq & 1, &bar->stop, p.status);
@@ -258,7 +272,10 @@ __device__ __forceinline__ void produce(const ChunkAttnParams &p, unsigned char 
                 mbar_arrive(&read[src.i]);
                 src.next(slots);
                 ahead--;
-                if (tid == 0 && kt + slots < npk) copy(s, kt + slots);
+                if (tid == 0 && kt + lead < npk) {
+                    copy(s, kt + lead, entry);
+                    entry = page_entry(p, s.it, min(kt + lead + 1, npk - 1));
+                }
             } else {
                 if (make_tail(p, s, (kt - s.np) * kChunkKeys, value, dst, tid)) {
                     // infinite and NaN values enter the product as 0 (0 weights of rows that may

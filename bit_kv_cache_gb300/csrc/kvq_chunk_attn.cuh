@@ -79,13 +79,16 @@ __device__ __forceinline__ const uint16_t *tail_row(const ChunkAttnParams &p, co
                  : p.k_new + (int64_t)(it.s.cu + x) * p.k_stride + it.h * kD;
 }
 
-__device__ __forceinline__ int64_t page_of(const ChunkAttnParams &p, const Item &it, int tile) {
-    int64_t e = p.ptab[(size_t)it.b * p.ptab_stride + (int64_t)tile * kChunkKeys / p.G];
-    if (e < 0 || e >= p.n_pages) {
+// The page-table entry of a key tile, and the page index it stands for.
+__device__ __forceinline__ int32_t page_entry(const ChunkAttnParams &p, const Item &it, int tile) {
+    return p.ptab[(size_t)it.b * p.ptab_stride + (int64_t)tile * kChunkKeys / p.G];
+}
+__device__ __forceinline__ int64_t page_index(const ChunkAttnParams &p, const Item &it, int32_t entry) {
+    if (entry < 0 || entry >= p.n_pages) {
         report(p.status, KVQ_DEV_BAD_STATE);
-        e = 0;
+        entry = 0;
     }
-    return e * p.H_kv + it.h;
+    return (int64_t)entry * p.H_kv + it.h;
 }
 
 }  // namespace kvq
