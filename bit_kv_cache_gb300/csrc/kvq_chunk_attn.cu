@@ -32,7 +32,7 @@ namespace kvq {
 
 namespace {
 
-constexpr int kRows = kWideRows, kThreads = 640;
+constexpr int kRows = kWideRows, kThreads = 768;
 constexpr int kTileBytes = kChunkKeys * kD * 2;          // an fp16 key or value tile: 32 KB
 constexpr int kRing = 2;                                 // tiles of each kind
 constexpr int kRawBytes = 2 * (16384 + 512);             // packed tiles: codes and (scale, min)
@@ -44,9 +44,9 @@ constexpr float kScale = kLog2e * 0.08838834764831845f;  // log2(e) / sqrt(128)
 // weights sum to kMostSum at most, below fp16's 65504; kUp more bits keep small weights
 // above fp16's smallest step.
 constexpr float kUp = 6.f, kMostSum = 16384.f;
-// registers of a thread after the split; 96 at launch, times 640 threads
-constexpr int kRegsSoftmax = 120, kRegsTiles = 72, kRegsMul = 96;
-static_assert(256 * kRegsSoftmax + 256 * kRegsTiles + 128 * kRegsMul <= kThreads * 96, "register split");
+// registers of a thread after the split; 80 at launch, times 768 threads
+constexpr int kRegsSoftmax = 120, kRegsTiles = 72, kRegsOther = 48;
+static_assert(256 * kRegsSoftmax + 256 * kRegsTiles + 256 * kRegsOther <= kThreads * 80, "register split");
 
 struct Bars {
     uint64_t q_full, q_empty, k_full[kRing], k_empty[kRing], v_full[kRing], v_empty[kRing];
@@ -184,63 +184,81 @@ __device__ __forceinline__ bool make_tail(const ChunkAttnParams &p, const Seg &s
     return bad;
 }
 
-// ---------------------------------------------------------------- groups 2, 3: tiles --
-// Both groups run the same code (the kernel is as fast as its hot code is small: five roles
-// share an SM's instruction cache).
-__device__ __forceinline__ void produce(const ChunkAttnParams &p, unsigned char *sm, Bars *bar, bool value, int begin, int end) {
-    const int tid = threadIdx.x & 127, bits = value ? p.vbits : p.kbits;
-    const int kraw = 2048 * p.kbits + 512, vraw = 2048 * p.vbits + 512, size = value ? vraw : kraw;
-    const int slots = min(kMaxRaw, kRawBytes / (kraw + vraw));
-    unsigned char *raw = sm + kOffRaw + (value ? slots * kraw : 0);
-    unsigned char *ring = sm + (value ? kOffV : kOffK);
+// A position in a ring of barriers: slot, and the parity of its next completion.
+struct Ring {
+    int i;
+    uint32_t parity;
+    __device__ __forceinline__ void next(int n) {
+        if (++i == n) i = 0, parity ^= 1;
+    }
+};
+
+// Shared memory of the packed tiles of one side.
+struct Raw {
+    int slots, size, off;
+    __device__ __forceinline__ Raw(const ChunkAttnParams &p, bool value) {
+        const int kraw = 2048 * p.kbits + 512, vraw = 2048 * p.vbits + 512;
+        slots = min(kMaxRaw, kRawBytes / (kraw + vraw));
+        size = value ? vraw : kraw;
+        off = kOffRaw + (value ? slots * kraw : 0);
+    }
+};
+
+// ---------------------------------------------------------------- warps 20, 21: copies --
+// One lane brings the packed tiles of the keys (values) into their ring, as far ahead as it
+// has slots.  The page-table entry of a tile is read before the copy of the tile before it
+// is waited for.
+__device__ __forceinline__ void bring(const ChunkAttnParams &p, unsigned char *sm, Bars *bar, bool value, int begin, int end) {
+    const Raw raw(p, value);
+    const int bits = value ? p.vbits : p.kbits;
     uint64_t *arrived = value ? bar->rawv : bar->rawk, *read = value ? bar->readv : bar->readk;
-    uint64_t *full = value ? bar->v_full : bar->k_full, *empty = value ? bar->v_empty : bar->k_empty;
     const int32_t *codes = value ? p.v_codes : p.k_codes;
     const uint16_t *meta = value ? p.v_meta : p.k_meta;
-    // a position in a ring of barriers: slot, and the parity of its next completion
-    struct Ring {
-        int i;
-        uint32_t parity;
-        __device__ __forceinline__ void next(int n) {
-            if (++i == n) i = 0, parity ^= 1;
-        }
-    };
-    Ring tile = {0, 1}, src = {0, 0}, cp = {0, 1};  // tiles made (their slots' release), packed tiles read, copies
-    int ahead = 0, seg = 0;                         // copies issued and not read (thread 0)
-    uint32_t nq = 1;
-    // thread 0: the copies of packed tile kt, once the slot's last tile has been read
-    auto copy = [&](const Seg &s, int kt, int32_t entry) {
-        await(&read[cp.i], cp.parity, &bar->stop, p.status);
-        if (*(volatile int *)&bar->stop) return;
-        const int64_t page = page_index(p, s.it, entry);
-        const int t0 = kt * kChunkKeys & (p.G - 1);
-        unsigned char *dst = raw + cp.i * size;
-        mbar_arrive_expect_tx(&arrived[cp.i], size);
-        bulk_g2s(dst, codes + ((size_t)page * p.G + t0) * (kD * bits / 32), 2048 * bits, &arrived[cp.i]);
-        bulk_g2s(dst + 2048 * bits, meta + (value ? ((size_t)page * p.G + t0) * 2 : (size_t)page * kD * 2), 512, &arrived[cp.i]);
-        cp.next(slots);
-        ahead++;
-    };
-    // A tile's copy goes to the slot of the tile `slots` before it.  With two slots or more it
-    // is issued a tile later than it could be, when that slot's readers are long done, and its
-    // page-table entry is read a tile before: thread 0 then waits for neither.
-    const int lag = slots > 1 ? 1 : 0, lead = slots - lag;
-    for (int at = begin; at < end; seg++) {
+    const int gshift = p.G == kChunkKeys ? 0 : 1;  // key tiles per page: 1 or 2
+    Ring cp = {0, 1};
+    uint32_t n = 0;
+    for (int at = begin; at < end;) {
         const Seg s = next_seg(p, at, end);
         at = s.end;
         const int npk = min(s.k1, s.np);
-        int32_t entry = 0;
-        if (tid == 0 && s.k0 < npk) {
-            int32_t first[kMaxRaw + 1];
-#pragma unroll
-            for (int i = 0; i <= kMaxRaw; i++) first[i] = page_entry(p, s.it, min(s.k0 + i, npk - 1));
-#pragma unroll
-            for (int i = 0; i < kMaxRaw; i++)
-                if (i < lead && s.k0 + i < npk) copy(s, s.k0 + i, first[i]);
-#pragma unroll
-            for (int i = 0; i <= kMaxRaw; i++)
-                if (i == lead) entry = first[i];
+        const int32_t *row = p.ptab + (size_t)s.it.b * p.ptab_stride;
+        if (s.k0 >= npk) continue;
+        int32_t entry = row[s.k0 >> gshift];
+        for (int kt = s.k0; kt < npk; kt++) {
+            const int32_t ahead = row[min(kt + 1, npk - 1) >> gshift];
+            await(&read[cp.i], cp.parity, &bar->stop, p.status);
+            if (*(volatile int *)&bar->stop) break;
+            const int64_t page = page_index(p, s.it, entry);
+            const int t0 = kt * kChunkKeys & (p.G - 1);
+            unsigned char *dst = sm + raw.off + cp.i * raw.size;
+            mbar_arrive_expect_tx(&arrived[cp.i], raw.size);
+            bulk_g2s(dst, codes + ((size_t)page * p.G + t0) * (kD * bits / 32), 2048 * bits, &arrived[cp.i]);
+            bulk_g2s(dst + 2048 * bits, meta + (value ? ((size_t)page * p.G + t0) * 2 : (size_t)page * kD * 2), 512, &arrived[cp.i]);
+            cp.next(raw.slots);
+            n++;
+            entry = ahead;
         }
+    }
+    // the last copies land before the block ends, whether they are awaited there or not
+    for (uint32_t k = n > (uint32_t)raw.slots ? n - raw.slots : 0; k < n; k++)
+        mbar_wait(&arrived[k % raw.slots], (k / raw.slots) & 1, p.status);
+}
+
+// ---------------------------------------------------------------- groups 2, 3: tiles --
+// Both groups run the same code (the kernel is as fast as its hot code is small: six roles
+// share an SM's instruction cache).
+__device__ __forceinline__ void produce(const ChunkAttnParams &p, unsigned char *sm, Bars *bar, bool value, int begin, int end) {
+    const int tid = threadIdx.x & 127, bits = value ? p.vbits : p.kbits, TV = value ? 256 / p.kbits : kChunkKeys;
+    const Raw raw(p, value);
+    unsigned char *ring = sm + (value ? kOffV : kOffK);
+    uint64_t *arrived = value ? bar->rawv : bar->rawk, *read = value ? bar->readv : bar->readk;
+    uint64_t *full = value ? bar->v_full : bar->k_full, *empty = value ? bar->v_empty : bar->k_empty;
+    Ring tile = {0, 1}, src = {0, 0};  // tiles made (their slots' release), packed tiles
+    uint32_t nq = 1;
+    int seg = 0;
+    for (int at = begin; at < end; seg++) {
+        const Seg s = next_seg(p, at, end);
+        at = s.end;
         if (value) {
             // queries: 128-row tiles, rows of tokens' heads; rows behind the last one repeat it
             await(&bar->q_empty, nq & 1, &bar->stop, p.status);
@@ -259,37 +277,28 @@ __device__ __forceinline__ void produce(const ChunkAttnParams &p, unsigned char 
         }
         for (int kt = s.k0; kt < s.k1; kt++) {
             unsigned char *dst = ring + tile.i * kTileBytes;
-            await(&empty[tile.i], tile.parity, &bar->stop, p.status);
             if (kt < s.np) {
                 await(&arrived[src.i], src.parity, &bar->stop, p.status);
-                const uint32_t from = smem_u32(raw + src.i * size), to = smem_u32(dst);
-                const int TV = value ? 256 / p.kbits : kChunkKeys;
+                await(&empty[tile.i], tile.parity, &bar->stop, p.status);
+                const uint32_t from = smem_u32(sm + raw.off + src.i * raw.size), to = smem_u32(dst);
                 if (bits == 2) make_tile<2>(from, to, tid, TV);
                 else if (bits == 4) make_tile<4>(from, to, tid, TV);
                 else make_tile<8>(from, to, tid, TV);
-                fence_proxy_async();
-                mbar_arrive(&full[tile.i]);
                 mbar_arrive(&read[src.i]);
-                src.next(slots);
-                ahead--;
-                if (tid == 0 && kt + lead < npk) {
-                    copy(s, kt + lead, entry);
-                    entry = page_entry(p, s.it, min(kt + lead + 1, npk - 1));
-                }
+                src.next(raw.slots);
             } else {
+                await(&empty[tile.i], tile.parity, &bar->stop, p.status);
                 if (make_tail(p, s, (kt - s.np) * kChunkKeys, value, dst, tid)) {
                     // infinite and NaN values enter the product as 0 (0 weights of rows that may
                     // not see them would spread them) and are added to their rows at the end
                     *(volatile int *)&bar->odd[seg & 3] = seg + 1;
                 }
-                fence_proxy_async();
-                mbar_arrive(&full[tile.i]);
             }
+            fence_proxy_async();
+            mbar_arrive(&full[tile.i]);
             tile.next(kRing);
         }
     }
-    if (tid == 0)  // copies still in flight after an early end
-        for (; ahead > 0; ahead--, src.next(slots)) mbar_wait(&arrived[src.i], src.parity, p.status);
 }
 
 // ---------------------------------------------------------------- group 4: products ---
@@ -651,12 +660,16 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attn_kernel(const __grid_co
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsTiles));
         produce(p, sm, bar, w >= 12, begin, end);
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsMul));
-        if (w < 18) issue_scores(p, sm, bar, tm, w & 1, begin, end);
-        else issue_values(p, sm, bar, tm, w & 1, begin, end);
-        __syncwarp();
-        tc_commit(&bar->drain, (threadIdx.x & 31) == 0);
-        mbar_wait(&bar->drain, 0, p.status);  // every product has ended before the tensor memory is freed
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
+        if (w < 20) {
+            if (w < 18) issue_scores(p, sm, bar, tm, w & 1, begin, end);
+            else issue_values(p, sm, bar, tm, w & 1, begin, end);
+            __syncwarp();
+            tc_commit(&bar->drain, (threadIdx.x & 31) == 0);
+            mbar_wait(&bar->drain, 0, p.status);  // every product has ended before the tensor memory is freed
+        } else if (w < 22 && (threadIdx.x & 31) == 0) {
+            bring(p, sm, bar, w == 21, begin, end);
+        }
     }
     __syncwarp();
     tc_fence_before();
