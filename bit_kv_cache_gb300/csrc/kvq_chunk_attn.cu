@@ -17,7 +17,10 @@
 //                warp for all four was the bottleneck: a wait costs it about 200 cycles).
 // In a wide unit (256 rows) m names the query tile: a key tile is dequantized once for both.
 // In a narrow one (at most 128 rows) m is the parity of the key tile: the two groups keep
-// softmax states of their own, joined at the end.
+// softmax states of their own, joined at the end.  With at most 64 (32) rows the query tile
+// holds them twice (four times), and each copy's softmax takes half (a quarter) of a tile's
+// keys: the tensor core's rows cost nothing, and a step of the softmax, which is what such a
+// unit waits for, is as much shorter.
 // A step is half a key tile (64 keys).  S_m has two buffers of 64 columns, so that the scores
 // of the next step are made while the softmax of this one runs.  Tensor memory: S_0, S_1,
 // O_0, O_1, 128 columns each.
@@ -67,7 +70,7 @@ static_assert(kSmemBytes <= 232448, "shared memory");
 // Segment: the items of one unit inside the CTA's range; its end, and its steps.
 struct Seg {
     Item it;
-    int k0, k1, np, valid, end, steps;
+    int k0, k1, np, valid, end, steps, rep;  // rep: copies of a narrow unit's rows in its query tile
     bool narrow;
 };
 __device__ __forceinline__ Seg next_seg(const ChunkAttnParams &p, int at, int end) {
@@ -79,6 +82,7 @@ __device__ __forceinline__ Seg next_seg(const ChunkAttnParams &p, int at, int en
     s.end = s.it.first + s.k1 * s.it.w;
     s.np = s.it.s.T / kChunkKeys;
     s.valid = min(s.it.rows, s.it.s.n_new * p.g - s.it.t * s.it.rows);
+    s.rep = !s.narrow || s.valid > 64 ? 1 : s.valid > 32 ? 2 : 4;
     // a wide unit's last key tile may end in its first half
     const int last = min(s.it.s.n_new, ((s.it.t + 1) * s.it.rows - 1) / p.g + 1);
     const int seen = s.it.s.ns + s.it.s.nr + last - (s.it.n - s.np - 1) * kChunkKeys;
@@ -263,10 +267,11 @@ __device__ __forceinline__ void produce(const ChunkAttnParams &p, unsigned char 
             // queries: 128-row tiles, rows of tokens' heads; rows behind the last one repeat it
             await(&bar->q_empty, nq & 1, &bar->stop, p.status);
             nq++;
-            const int ch = tid & 15, rows = (s.valid + 31) & ~31;  // whole warps of the softmax
+            const int ch = tid & 15, rows = s.rep > 1 ? 128 : (s.valid + 31) & ~31;  // whole warps of the softmax
+            const int copy = s.rep > 1 ? 128 / s.rep - 1 : kRows - 1;
 #pragma unroll 4
             for (int r = tid >> 4; r < rows; r += 8) {
-                const int x = s.it.t * s.it.rows + min(r, s.valid - 1);
+                const int x = s.it.t * s.it.rows + min(r & copy, s.valid - 1);
                 const uint4 a = __ldg(reinterpret_cast<const uint4 *>(p.q + (int64_t)(s.it.s.cu + x / p.g) * p.q_stride +
                                                                       (s.it.h * p.g + x % p.g) * kD) + ch);
                 *reinterpret_cast<uint4 *>(sm + kOffQ + (r >> 7) * kTileBytes + (ch >> 3) * 16384 + (r & 127) * 128 +
@@ -401,10 +406,11 @@ __device__ __forceinline__ void issue_values(const ChunkAttnParams &p, unsigned 
 }
 
 // ---------------------------------------------------------------- groups 0, 1 ---------
-// Scores of 64 keys: those from the n-th on are not seen.
-__device__ __forceinline__ void mask64(uint32_t *x, int n) {
+// Scores of N keys: those from the n-th on are not seen.
+template <int N>
+__device__ __forceinline__ void mask_keys(uint32_t *x, int n) {
 #pragma unroll
-    for (int c = 0; c < 64; c++)
+    for (int c = 0; c < N; c++)
         if (c >= n) x[c] = 0xff800000u;
 }
 __device__ __forceinline__ float max3(float a, float b, float c) {
@@ -412,25 +418,27 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
     return d;
 }
-__device__ __forceinline__ float max64(const float *f) {
+template <int N>
+__device__ __forceinline__ float max_of(const float *f) {
     float t[8];
 #pragma unroll
     for (int e = 0; e < 8; e++) t[e] = f[e];
 #pragma unroll
-    for (int c = 8; c < 56; c += 16)
+    for (int c = 8; c + 16 <= N; c += 16)
 #pragma unroll
         for (int e = 0; e < 8; e++) t[e] = max3(t[e], f[c + 2 * e], f[c + 2 * e + 1]);
 #pragma unroll
-    for (int e = 0; e < 8; e++) t[e] = fmaxf(t[e], f[56 + e]);
+    for (int e = 0; e < 8; e++) t[e] = fmaxf(t[e], f[N - 8 + e]);
     return fmaxf(max3(t[0], t[1], t[2]), max3(max3(t[3], t[4], t[5]), t[6], t[7]));
 }
-// Weights 2^(s scale + off) of 64 scores, as 32 half2 in place; returns their sum.
-__device__ __forceinline__ float weights64(uint32_t *x, float off) {
+// Weights 2^(s scale + off) of N scores, as N / 2 half2 in place; returns their sum.
+template <int N>
+__device__ __forceinline__ float weights(uint32_t *x, float off) {
     uint64_t l0 = 0, l1 = 0;
     const uint64_t sc2 = pair_of(kScale, kScale), of2 = pair_of(off, off);
     const float *f = reinterpret_cast<const float *>(x);
 #pragma unroll
-    for (int c = 0; c < 64; c += 4) {
+    for (int c = 0; c < N; c += 4) {
         float2 a = of_pair(fma_pair(pair_of(f[c], f[c + 1]), sc2, of2)), b = of_pair(fma_pair(pair_of(f[c + 2], f[c + 3]), sc2, of2));
         a.x = ex2(a.x);
         a.y = ex2(a.y);
@@ -451,14 +459,15 @@ struct RowState {
     float mx, l;
 };
 
-// The scores of step buffer h as weights' arguments, those of unseen keys as -inf.
-__device__ __forceinline__ void load_scores(uint32_t (&x)[64], uint32_t ts, int y) {
-    tmem_ld32(x, ts);
-    tmem_ld32(x + 32, ts + 32);
+// N scores from column ts on, those of unseen keys (from the y-th on) as -inf.
+template <int N>
+__device__ __forceinline__ void load_scores(uint32_t *x, uint32_t ts, int y) {
+#pragma unroll
+    for (int c = 0; c < N; c += 32) tmem_ld32(x + c, ts + c);
     tmem_wait_ld();
 #pragma unroll
-    for (int c = 0; c < 4; c++) tmem_tie16(x + 16 * c);
-    if (y < 64) mask64(x, y);
+    for (int c = 0; c < N; c += 16) tmem_tie16(x + c);
+    if (y < N) mask_keys<N>(x, y);
 }
 
 // The steps of one segment for query tile or key parity m; narrow units: every second key
@@ -478,11 +487,11 @@ __device__ __forceinline__ void softmax_steps(const ChunkAttnParams &p, Bars *ba
             tc_fence_after();
             const int y = kt >= s.np ? lim - (kt - s.np) * kChunkKeys - 64 * h : 64;  // keys it may see
             uint32_t x[64];
-            load_scores(x, ts + 64 * h, y);
-            float add = weights64(x, kUp - mx);                  // infinite or NaN without a reference
+            load_scores<64>(x, ts + 64 * h, y);
+            float add = weights<64>(x, kUp - mx);                  // infinite or NaN without a reference
             if (__any_sync(0xffffffffu, !(add <= kMostSum))) {
-                load_scores(x, ts + 64 * h, y);
-                const float cand = max64(reinterpret_cast<const float *>(x)) * kScale;
+                load_scores<64>(x, ts + 64 * h, y);
+                const float cand = max_of<64>(reinterpret_cast<const float *>(x)) * kScale;
                 const bool grow = cand > mx;
                 const float corr = grow ? ex2(mx - cand) : 1.f;
                 if (grow) mx = cand;
@@ -501,8 +510,8 @@ __device__ __forceinline__ void softmax_steps(const ChunkAttnParams &p, Bars *ba
                         tmem_st16(to + 16 * c, x);
                     }
                 }
-                if (i > 0) load_scores(x, ts + 64 * h, y);
-                add = weights64(x, kUp - (mx == -INFINITY ? 0.f : mx));
+                if (i > 0) load_scores<64>(x, ts + 64 * h, y);
+                add = weights<64>(x, kUp - (mx == -INFINITY ? 0.f : mx));
             }
             tmem_st32(ts + 64 * h, x);  // over the scores
             l += add;
@@ -519,6 +528,114 @@ __device__ __forceinline__ void softmax_steps(const ChunkAttnParams &p, Bars *ba
     st.l = l;
 }
 
+// The key tiles of one segment of a narrow unit that holds its rows REP times: the thread's
+// copy takes keys KEYS c .. of every tile, the other keys' weights in its lane are 0.
+template <int REP>
+__device__ __forceinline__ void softmax_tiles(const ChunkAttnParams &p, Bars *bar, const Seg &s, RowState &st, uint32_t ts, uint32_t to,
+                                              int m, int lim, int c) {
+    constexpr int KEYS = 128 / REP;
+    float mx = -INFINITY, l = 0.f;
+    for (int kt = s.k0 + m; kt < s.k1; kt += 2) {
+        warp_await(&bar->s_full[m][0], st.ns & 1, &bar->stop, p.status);
+        warp_await(&bar->s_full[m][1], (st.ns >> 1) & 1, &bar->stop, p.status);
+        tc_fence_after();
+        const int y = kt >= s.np ? lim - (kt - s.np) * kChunkKeys - KEYS * c : KEYS;  // keys it may see
+        uint32_t x[KEYS];
+        load_scores<KEYS>(x, ts + KEYS * c, y);
+        float add = weights<KEYS>(x, kUp - mx);                  // infinite or NaN without a reference
+        if (__any_sync(0xffffffffu, !(add <= kMostSum))) {
+            load_scores<KEYS>(x, ts + KEYS * c, y);
+            const float cand = max_of<KEYS>(reinterpret_cast<const float *>(x)) * kScale;
+            const bool grow = cand > mx;
+            const float corr = grow ? ex2(mx - cand) : 1.f;
+            if (grow) mx = cand;
+            l *= corr;
+            if (kt > s.k0 + m) {  // the products before these scores have ended
+#pragma unroll 1
+                for (int e0 = 0; e0 < 128; e0 += 16) {
+                    tmem_ld16(x, to + e0);
+                    tmem_wait_ld();
+                    tmem_tie16(x);
+#pragma unroll
+                    for (int e = 0; e < 16; e++) x[e] = __float_as_uint(__uint_as_float(x[e]) * corr);
+                    tmem_st16(to + e0, x);
+                }
+                load_scores<KEYS>(x, ts + KEYS * c, y);
+            }
+            add = weights<KEYS>(x, kUp - (mx == -INFINITY ? 0.f : mx));
+        }
+        l += add;
+        // weights of keys 64 h .. at columns 64 h .., two to a column
+        uint32_t zero[16];
+#pragma unroll
+        for (int e = 0; e < 16; e++) zero[e] = 0;
+#pragma unroll
+        for (int q = 0; q < 4; q++) {
+            const uint32_t at = ts + 64 * (q >> 1) + 16 * (q & 1);
+            if (q / (4 / REP) == c) tmem_st16(at, x + (q % (4 / REP)) * 16);
+            else tmem_st16(at, zero);
+        }
+        tmem_wait_st();
+        if (m == 1 && kt == s.k0 + m && st.no1 > 0) warp_await(&bar->o1_free, (st.no1 - 1) & 1, &bar->stop, p.status);
+        tc_fence_before();
+        mbar_arrive(&bar->p_full[m][0]);
+        mbar_arrive(&bar->p_full[m][1]);
+        st.ns ^= 3;
+        st.given = 3;
+    }
+    st.mx = mx;
+    st.l = l;
+}
+
+// Joins the copies of a narrow unit's rows, which lie in the partial rows 128 .. 255 of
+// `slot` (written by this group before the barrier): a row's result goes to its output row,
+// or to its partial row.
+__device__ __forceinline__ void join_copies(const ChunkAttnParams &p, const Seg &s, size_t slot, bool whole, bool odd) {
+    asm volatile("bar.sync 1, 128;" ::: "memory");  // no thread of the group leaves before this
+    const int t = threadIdx.x & 127, row = t / s.rep, part = t - row * s.rep, R = 128 / s.rep, n = 32 / s.rep;
+    if (row >= s.valid) return;
+    const float2 *ml = p.part_ml + slot + 128 + row;
+    float mx = -INFINITY, l = 0.f, a[4];
+    for (int k = 0; k < s.rep; k++) mx = fmaxf(mx, ml[k * R].x);
+#pragma unroll
+    for (int k = 0; k < 4; k++) {
+        const float2 v = k < s.rep ? ml[k * R] : make_float2(-INFINITY, 0.f);
+        a[k] = k < s.rep && v.x == mx ? 1.f : ex2(v.x - mx);
+        if (k < s.rep) l += a[k] * v.y;
+    }
+    const int r = s.it.t * s.it.rows + row;
+    uint16_t *dst = p.out + ((int64_t)(s.it.s.cu + r / p.g) * p.H_kv * p.g + s.it.h * p.g + r % p.g) * kD;
+    const float4 *src = reinterpret_cast<const float4 *>(p.part_o + (slot + 128 + row) * kD);
+    const float inv = 1.f / l;
+    for (int i = part * n; i < part * n + n; i++) {
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int k = 0; k < 4; k++)
+            if (k < s.rep) {
+                const float4 v = src[(size_t)k * R * (kD / 4) + i];
+                o.x += a[k] * v.x;
+                o.y += a[k] * v.y;
+                o.z += a[k] * v.z;
+                o.w += a[k] * v.w;
+            }
+        if (odd) {
+            const int lim = s.it.s.ns + s.it.s.nr + r / p.g + 1;
+            for (int x = max(0, s.k0 - s.np) * kChunkKeys; x < min(lim, (s.k1 - s.np) * kChunkKeys); x++) {
+                const uint16_t *v = tail_row(p, s.it, x, true) + 4 * i;
+                float *f = &o.x;
+#pragma unroll
+                for (int e = 0; e < 4; e++) {
+                    const float y = h2f(v[e]);
+                    if (!isfinite(y)) f[e] += y;
+                }
+            }
+        }
+        if (whole) reinterpret_cast<uint2 *>(dst)[i] = make_uint2(pack_half2(o.x * inv, o.y * inv), pack_half2(o.z * inv, o.w * inv));
+        else reinterpret_cast<float4 *>(p.part_o + (slot + row) * kD)[i] = o;
+    }
+    if (!whole && part == 0) p.part_ml[slot + row] = make_float2(mx, l);
+}
+
 __device__ __forceinline__ void softmax(const ChunkAttnParams &p, Bars *bar, uint32_t tm, int m, int begin, int end) {
     const int lane_row = threadIdx.x & 127;
     const uint32_t lanes = (uint32_t)(threadIdx.x & 96) << 16;
@@ -528,15 +645,17 @@ __device__ __forceinline__ void softmax(const ChunkAttnParams &p, Bars *bar, uin
     for (int at = begin; at < end; seg++) {
         const Seg s = next_seg(p, at, end);
         const bool last_first = s.k0 == 0 && at != begin;
-        const int base = s.narrow ? 0 : 128 * m, row = base + lane_row;
+        const int base = s.narrow ? 0 : 128 * m, row = s.rep > 1 ? lane_row & (128 / s.rep - 1) : base + lane_row;
         at = s.end;
         const int n = s.k1 - s.k0;
         if (base >= s.valid || (s.narrow && m >= n)) continue;
-        const bool any = base + (lane_row & 96) < s.valid;
+        const bool any = s.rep > 1 || base + (lane_row & 96) < s.valid;
         const int r = s.it.t * s.it.rows + min(row, s.valid - 1);
         const int lim = s.it.s.ns + s.it.s.nr + r / p.g + 1;
         const bool join = s.narrow && n > 1;
-        if (s.narrow) softmax_steps<true>(p, bar, s, st, ts, to, m, lim, any);
+        if (s.rep == 4) softmax_tiles<4>(p, bar, s, st, ts, to, m, lim, lane_row >> 5);
+        else if (s.rep == 2) softmax_tiles<2>(p, bar, s, st, ts, to, m, lim, lane_row >> 6);
+        else if (s.narrow) softmax_steps<true>(p, bar, s, st, ts, to, m, lim, any);
         else softmax_steps<false>(p, bar, s, st, ts, to, m, lim, any);
         float mx = st.mx, l = st.l;
         for (int h = 0; h < 2; h++)  // the last products
@@ -564,10 +683,12 @@ __device__ __forceinline__ void softmax(const ChunkAttnParams &p, Bars *bar, uin
         const bool odd = *(volatile int *)&bar->odd[seg & 3] == seg + 1;
         const float inv = 1.f / l;
         // the range's first segment has slot 2 c, its last one (a unit that goes on) 2 c + 1
-        const size_t slot = (2 * (size_t)blockIdx.x + (last_first ? 1 : 0)) * kRows + row;
+        const size_t slot0 = (2 * (size_t)blockIdx.x + (last_first ? 1 : 0)) * kRows;
+        const bool direct = whole && s.rep == 1, mine = s.rep > 1 || row < s.valid;
+        const size_t slot = slot0 + (s.rep > 1 ? 128 + lane_row : row);
         uint16_t *dst = p.out + ((int64_t)(s.it.s.cu + r / p.g) * p.H_kv * p.g + s.it.h * p.g + r % p.g) * kD;
         if (any) {
-            if (!whole && row < s.valid) p.part_ml[slot] = make_float2(mx, l);
+            if (!direct && mine) p.part_ml[slot] = make_float2(mx, l);
 #pragma unroll 1
             for (int c = 0; c < 8; c++) {
                 uint32_t o[16];
@@ -583,7 +704,7 @@ __device__ __forceinline__ void softmax(const ChunkAttnParams &p, Bars *bar, uin
 #pragma unroll
                     for (int e = 0; e < 16; e++) f[e] = a0 * f[e] + a1 * __uint_as_float(o1[e]);
                 }
-                if (odd)
+                if (odd && s.rep == 1)
                     for (int x = max(0, s.k0 - s.np) * kChunkKeys; x < min(lim, (s.k1 - s.np) * kChunkKeys); x++) {
                         const uint16_t *v = tail_row(p, s.it, x, true) + 16 * c;
 #pragma unroll
@@ -592,8 +713,8 @@ __device__ __forceinline__ void softmax(const ChunkAttnParams &p, Bars *bar, uin
                             if (!isfinite(y)) f[e] += y;
                         }
                     }
-                if (row < s.valid) {
-                    if (whole) {
+                if (mine) {
+                    if (direct) {
                         uint4 y[2];
                         uint32_t *w = reinterpret_cast<uint32_t *>(y);
 #pragma unroll
@@ -612,6 +733,7 @@ __device__ __forceinline__ void softmax(const ChunkAttnParams &p, Bars *bar, uin
         }
         tc_fence_before();
         if (join) mbar_arrive(&bar->o1_free);
+        if (s.rep > 1) join_copies(p, s, slot0, whole, odd);
     }
 }
 
