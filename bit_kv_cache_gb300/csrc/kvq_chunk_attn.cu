@@ -6,13 +6,14 @@
 // in one pass over the keys with a running maximum and sum per row.  Dequantized keys and
 // values are rounded once to fp16, softmax weights too; sums are fp32.
 //
-// One CTA per SM, five groups of four warps:
+// One CTA per SM, eight groups of four warps:
 //   groups 0, 1  softmax, a thread per row of 128: reads the scores S_m from tensor memory,
 //                keeps a reference near the row's running maximum and the sum in registers,
 //                writes the weights P_m over S_m as fp16, rescales O_m when the reference moves;
-//   groups 2, 3  make the key and the value tiles: packed pages arrive by bulk copies and
-//                are dequantized into fp16 tiles in shared memory, fp16 rows are gathered;
-//   group 4      warps 16 + m issue the products S_m = Q K^T, warps 18 + m O_m += P_m V: each
+//   groups 2-5   make the key tiles (2, 3) and the value tiles (4, 5), every second one each:
+//                packed pages arrive by bulk copies and are dequantized into fp16 tiles in
+//                shared memory, fp16 rows are gathered;
+//   groups 6, 7  warps 24 + m issue the products S_m = Q K^T, warps 26 + m O_m += P_m V: each
 //                waits for its own operands while the others keep the tensor core busy (one
 //                warp for all four was the bottleneck: a wait costs it about 200 cycles).
 // In a wide unit (256 rows) m names the query tile: a key tile is dequantized once for both.
@@ -35,10 +36,10 @@ namespace kvq {
 
 namespace {
 
-constexpr int kRows = kWideRows, kThreads = 768;
+constexpr int kRows = kWideRows, kThreads = 1024;
 constexpr int kTileBytes = kChunkKeys * kD * 2;          // an fp16 key or value tile: 32 KB
 constexpr int kRing = 2;                                 // tiles of each kind
-constexpr int kRawBytes = 2 * (16384 + 512);             // packed tiles: codes and (scale, min)
+constexpr int kRawBytes = 4 * (8192 + 512);              // packed tiles: codes and (scale, min)
 constexpr int kMaxRaw = 4;
 constexpr int kOffQ = 0, kOffK = 2 * kTileBytes, kOffV = kOffK + kRing * kTileBytes, kOffRaw = kOffV + kRing * kTileBytes,
               kOffBar = kOffRaw + kRawBytes;
@@ -47,9 +48,9 @@ constexpr float kScale = kLog2e * 0.08838834764831845f;  // log2(e) / sqrt(128)
 // weights sum to kMostSum at most, below fp16's 65504; kUp more bits keep small weights
 // above fp16's smallest step.
 constexpr float kUp = 6.f, kMostSum = 16384.f;
-// registers of a thread after the split; 80 at launch, times 768 threads
-constexpr int kRegsSoftmax = 120, kRegsTiles = 72, kRegsOther = 48;
-static_assert(256 * kRegsSoftmax + 256 * kRegsTiles + 256 * kRegsOther <= kThreads * 80, "register split");
+// registers of a thread after the split; 64 at launch, times 1024 threads
+constexpr int kRegsSoftmax = 112, kRegsTiles = 48, kRegsOther = 48;
+static_assert(256 * kRegsSoftmax + 512 * kRegsTiles + 256 * kRegsOther <= kThreads * 64, "register split");
 
 struct Bars {
     uint64_t q_full, q_empty, k_full[kRing], k_empty[kRing], v_full[kRing], v_empty[kRing];
@@ -57,8 +58,7 @@ struct Bars {
     // (a wait names a phase by its parity, so no barrier may run two phases ahead of a waiter)
     uint64_t pv_done[2][2], drain;
     uint64_t o1_full, o1_free;                        // narrow units: O_1 and its sums are final, have been read
-    float2 state1[128];                               // (max, sum) of O_1's rows
-    uint64_t rawk[kMaxRaw], rawv[kMaxRaw];            // packed tile arrived
+    uint64_t rawk[2][kMaxRaw], rawv[2][kMaxRaw];      // packed tile arrived, by the tile's parity
     uint64_t readk[kMaxRaw], readv[kMaxRaw];          // packed tile read by all producers
     uint32_t tmem;
     int stop;
@@ -208,23 +208,25 @@ struct Raw {
     }
 };
 
-// ---------------------------------------------------------------- warps 20, 21: copies --
+// ---------------------------------------------------------------- warps 28, 29: copies --
 // One lane brings the packed tiles of the keys (values) into their ring, as far ahead as it
 // has slots.  The page-table entry of a tile is read before the copy of the tile before it
 // is waited for.
 __device__ __forceinline__ void bring(const ChunkAttnParams &p, unsigned char *sm, Bars *bar, bool value, int begin, int end) {
     const Raw raw(p, value);
     const int bits = value ? p.vbits : p.kbits;
-    uint64_t *arrived = value ? bar->rawv : bar->rawk, *read = value ? bar->readv : bar->readk;
+    uint64_t(*arrived)[kMaxRaw] = value ? bar->rawv : bar->rawk, *read = value ? bar->readv : bar->readk;
     const int32_t *codes = value ? p.v_codes : p.k_codes;
     const uint16_t *meta = value ? p.v_meta : p.k_meta;
     const int gshift = p.G == kChunkKeys ? 0 : 1;  // key tiles per page: 1 or 2
     Ring cp = {0, 1};
-    uint32_t n = 0;
+    int n = 0;                 // tiles of the segments before
+    uint32_t used = 0, parity = 0;  // per barrier (bit kMaxRaw par + slot): whether and how often used
     for (int at = begin; at < end;) {
         const Seg s = next_seg(p, at, end);
         at = s.end;
-        const int npk = min(s.k1, s.np);
+        const int npk = min(s.k1, s.np), n0 = n - s.k0;
+        n += s.k1 - s.k0;
         const int32_t *row = p.ptab + (size_t)s.it.b * p.ptab_stride;
         if (s.k0 >= npk) continue;
         int32_t entry = row[s.k0 >> gshift];
@@ -235,35 +237,38 @@ __device__ __forceinline__ void bring(const ChunkAttnParams &p, unsigned char *s
             const int64_t page = page_index(p, s.it, entry);
             const int t0 = kt * kChunkKeys & (p.G - 1);
             unsigned char *dst = sm + raw.off + cp.i * raw.size;
-            mbar_arrive_expect_tx(&arrived[cp.i], raw.size);
-            bulk_g2s(dst, codes + ((size_t)page * p.G + t0) * (kD * bits / 32), 2048 * bits, &arrived[cp.i]);
-            bulk_g2s(dst + 2048 * bits, meta + (value ? ((size_t)page * p.G + t0) * 2 : (size_t)page * kD * 2), 512, &arrived[cp.i]);
+            const int par = (n0 + kt) & 1, bit = 1 << (kMaxRaw * par + cp.i);
+            uint64_t *b = &arrived[par][cp.i];
+            mbar_arrive_expect_tx(b, raw.size);
+            bulk_g2s(dst, codes + ((size_t)page * p.G + t0) * (kD * bits / 32), 2048 * bits, b);
+            bulk_g2s(dst + 2048 * bits, meta + (value ? ((size_t)page * p.G + t0) * 2 : (size_t)page * kD * 2), 512, b);
             cp.next(raw.slots);
-            n++;
+            used |= bit;
+            parity ^= bit;
             entry = ahead;
         }
     }
     // the last copies land before the block ends, whether they are awaited there or not
-    for (uint32_t k = n > (uint32_t)raw.slots ? n - raw.slots : 0; k < n; k++)
-        mbar_wait(&arrived[k % raw.slots], (k / raw.slots) & 1, p.status);
+    for (int i = 0; i < 2 * kMaxRaw; i++)
+        if ((used >> i) & 1) mbar_wait(&arrived[i / kMaxRaw][i % kMaxRaw], ~(parity >> i) & 1, p.status);
 }
 
-// ---------------------------------------------------------------- groups 2, 3: tiles --
-// Both groups run the same code (the kernel is as fast as its hot code is small: six roles
+// ---------------------------------------------------------------- groups 2-5: tiles ---
+// All four run the same code (the kernel is as fast as its hot code is small: six roles
 // share an SM's instruction cache).
-__device__ __forceinline__ void produce(const ChunkAttnParams &p, unsigned char *sm, Bars *bar, bool value, int begin, int end) {
+__device__ __forceinline__ void produce(const ChunkAttnParams &p, unsigned char *sm, Bars *bar, bool value, int par, int begin, int end) {
     const int tid = threadIdx.x & 127, bits = value ? p.vbits : p.kbits, TV = value ? 256 / p.kbits : kChunkKeys;
     const Raw raw(p, value);
-    unsigned char *ring = sm + (value ? kOffV : kOffK);
-    uint64_t *arrived = value ? bar->rawv : bar->rawk, *read = value ? bar->readv : bar->readk;
-    uint64_t *full = value ? bar->v_full : bar->k_full, *empty = value ? bar->v_empty : bar->k_empty;
-    Ring tile = {0, 1}, src = {0, 0};  // tiles made (their slots' release), packed tiles
-    uint32_t nq = 1;
-    int seg = 0;
+    unsigned char *dst = sm + (value ? kOffV : kOffK) + par * kTileBytes;
+    uint64_t *arrived = (value ? bar->rawv : bar->rawk)[par], *read = value ? bar->readv : bar->readk;
+    uint64_t *full = (value ? bar->v_full : bar->k_full) + par, *empty = (value ? bar->v_empty : bar->k_empty) + par;
+    int slot = 0;              // of the next packed tile, of either parity
+    uint32_t landed = 0, free = 1, nq = 1;  // parities: of the slots' arrivals, of the tile's release
+    int seg = 0, n = 0;        // n: tiles of the segments before
     for (int at = begin; at < end; seg++) {
         const Seg s = next_seg(p, at, end);
         at = s.end;
-        if (value) {
+        if (value && par == 0) {
             // queries: 128-row tiles, rows of tokens' heads; rows behind the last one repeat it
             await(&bar->q_empty, nq & 1, &bar->stop, p.status);
             nq++;
@@ -281,18 +286,22 @@ __device__ __forceinline__ void produce(const ChunkAttnParams &p, unsigned char 
             mbar_arrive(&bar->q_full);
         }
         for (int kt = s.k0; kt < s.k1; kt++) {
-            unsigned char *dst = ring + tile.i * kTileBytes;
+            if (((n + kt - s.k0) & 1) != par) {
+                if (kt < s.np && ++slot == raw.slots) slot = 0;
+                continue;
+            }
             if (kt < s.np) {
-                await(&arrived[src.i], src.parity, &bar->stop, p.status);
-                await(&empty[tile.i], tile.parity, &bar->stop, p.status);
-                const uint32_t from = smem_u32(sm + raw.off + src.i * raw.size), to = smem_u32(dst);
+                await(&arrived[slot], (landed >> slot) & 1, &bar->stop, p.status);
+                landed ^= 1u << slot;
+                await(empty, free, &bar->stop, p.status);
+                const uint32_t from = smem_u32(sm + raw.off + slot * raw.size), to = smem_u32(dst);
                 if (bits == 2) make_tile<2>(from, to, tid, TV);
                 else if (bits == 4) make_tile<4>(from, to, tid, TV);
                 else make_tile<8>(from, to, tid, TV);
-                mbar_arrive(&read[src.i]);
-                src.next(raw.slots);
+                mbar_arrive(&read[slot]);
+                if (++slot == raw.slots) slot = 0;
             } else {
-                await(&empty[tile.i], tile.parity, &bar->stop, p.status);
+                await(empty, free, &bar->stop, p.status);
                 if (make_tail(p, s, (kt - s.np) * kChunkKeys, value, dst, tid)) {
                     // infinite and NaN values enter the product as 0 (0 weights of rows that may
                     // not see them would spread them) and are added to their rows at the end
@@ -300,17 +309,18 @@ __device__ __forceinline__ void produce(const ChunkAttnParams &p, unsigned char 
                 }
             }
             fence_proxy_async();
-            mbar_arrive(&full[tile.i]);
-            tile.next(kRing);
+            mbar_arrive(full);
+            free ^= 1;
         }
+        n += s.k1 - s.k0;
     }
 }
 
-// ---------------------------------------------------------------- group 4: products ---
+// ---------------------------------------------------------------- group 6: products ---
 // Rows along M and N (keys: tokens, packed values: channels): 16 of the contracted dimension
 // are 32 bytes of a row; fp16 value rows run along the tokens: 16 are two atoms.
 
-// Warp 16 + m: the scores S_m.  A buffer's next scores go over its old weights, once the
+// Warp 24 + m: the scores S_m.  A buffer's next scores go over its old weights, once the
 // product that reads those has ended.
 __device__ __forceinline__ void issue_scores(const ChunkAttnParams &p, unsigned char *sm, Bars *bar, uint32_t tm, int m, int begin, int end) {
     const uint32_t base = smem_u32(sm), lead = (threadIdx.x & 31) == 0;
@@ -366,7 +376,7 @@ __device__ __forceinline__ void issue_scores(const ChunkAttnParams &p, unsigned 
     }
 }
 
-// Warp 18 + m: the products O_m += P_m V.
+// Warp 26 + m: the products O_m += P_m V.
 __device__ __forceinline__ void issue_values(const ChunkAttnParams &p, unsigned char *sm, Bars *bar, uint32_t tm, int m, int begin, int end) {
     const uint32_t base = smem_u32(sm), lead = (threadIdx.x & 31) == 0;
     uint32_t n = 0, ph = 0;       // value tiles; per buffer h: parity of the weights awaited
@@ -662,17 +672,20 @@ __device__ __forceinline__ void softmax(const ChunkAttnParams &p, Bars *bar, uin
             if ((st.given >> h) & 1) warp_await(&bar->pv_done[m][h], (~st.ns >> h) & 1, &bar->stop, p.status);
         tc_fence_after();
         float a0 = 1.f, a1 = 0.f;
-        if (join) {
+        // the range's first segment has slot 2 c, its last one (a unit that goes on) 2 c + 1
+        const size_t slot0 = (2 * (size_t)blockIdx.x + (last_first ? 1 : 0)) * kRows;
+        if (join) {  // O_1's states reach group 0 through the partial rows that its result may go to
+            float2 *state1 = p.part_ml + slot0;
             st.no1++;
             if (m == 1) {
-                bar->state1[lane_row] = make_float2(mx, l);
+                state1[lane_row] = make_float2(mx, l);
                 tc_fence_before();
                 mbar_arrive(&bar->o1_full);
                 continue;
             }
             warp_await(&bar->o1_full, (st.no1 - 1) & 1, &bar->stop, p.status);
             tc_fence_after();
-            const float2 other = bar->state1[lane_row];
+            const float2 other = state1[lane_row];
             const float mn = fmaxf(mx, other.x);
             a0 = mx == mn ? 1.f : ex2(mx - mn);
             a1 = other.x == mn ? 1.f : ex2(other.x - mn);
@@ -682,8 +695,6 @@ __device__ __forceinline__ void softmax(const ChunkAttnParams &p, Bars *bar, uin
         const bool whole = s.k0 == 0 && s.k1 == s.it.n;
         const bool odd = *(volatile int *)&bar->odd[seg & 3] == seg + 1;
         const float inv = 1.f / l;
-        // the range's first segment has slot 2 c, its last one (a unit that goes on) 2 c + 1
-        const size_t slot0 = (2 * (size_t)blockIdx.x + (last_first ? 1 : 0)) * kRows;
         const bool direct = whole && s.rep == 1, mine = s.rep > 1 || row < s.valid;
         const size_t slot = slot0 + (s.rep > 1 ? 128 + lane_row : row);
         uint16_t *dst = p.out + ((int64_t)(s.it.s.cu + r / p.g) * p.H_kv * p.g + s.it.h * p.g + r % p.g) * kD;
@@ -760,8 +771,10 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attn_kernel(const __grid_co
         }
         mbar_init(&bar->drain, 4);
         for (int i = 0; i < kMaxRaw; i++) {
-            mbar_init(&bar->rawk[i], 1);
-            mbar_init(&bar->rawv[i], 1);
+            for (int par = 0; par < 2; par++) {
+                mbar_init(&bar->rawk[par][i], 1);
+                mbar_init(&bar->rawv[par][i], 1);
+            }
             mbar_init(&bar->readk[i], 128);
             mbar_init(&bar->readv[i], 128);
         }
@@ -769,7 +782,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attn_kernel(const __grid_co
         for (int i = 0; i < 4; i++) bar->odd[i] = 0;
         fence_barrier_init();
     }
-    if (w == 16) tmem_alloc(&bar->tmem);
+    if (w == 24) tmem_alloc(&bar->tmem);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -778,26 +791,26 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attn_kernel(const __grid_co
     if (w < 8) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
         softmax(p, bar, tm, w >> 2, begin, end);
-    } else if (w < 16) {
+    } else if (w < 24) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsTiles));
-        produce(p, sm, bar, w >= 12, begin, end);
+        produce(p, sm, bar, w >= 16, (w >> 2) & 1, begin, end);
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
-        if (w < 20) {
-            if (w < 18) issue_scores(p, sm, bar, tm, w & 1, begin, end);
+        if (w < 28) {
+            if (w < 26) issue_scores(p, sm, bar, tm, w & 1, begin, end);
             else issue_values(p, sm, bar, tm, w & 1, begin, end);
             __syncwarp();
             tc_commit(&bar->drain, (threadIdx.x & 31) == 0);
             mbar_wait(&bar->drain, 0, p.status);  // every product has ended before the tensor memory is freed
-        } else if (w < 22 && (threadIdx.x & 31) == 0) {
-            bring(p, sm, bar, w == 21, begin, end);
+        } else if (w < 30 && (threadIdx.x & 31) == 0) {
+            bring(p, sm, bar, w == 29, begin, end);
         }
     }
     __syncwarp();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (w == 16) tmem_free(tm);
+    if (w == 24) tmem_free(tm);
 }
 
 }  // namespace
