@@ -548,7 +548,7 @@ struct ChunkWs {
 };
 ChunkWs chunk_ws() {
     ChunkWs w;
-    const size_t slots = (size_t)2 * num_sms() * kWideRows;  // rows
+    const size_t slots = (size_t)2 * std::min(num_sms(), kMaxRanges) * kWideRows;  // rows
     w.ml = 0;
     w.o = (slots * sizeof(float2) + 255) / 256 * 256;
     w.total = w.o + slots * 128 * sizeof(float);
@@ -671,14 +671,19 @@ int kvq_paged_chunk_attn(const kvq_config *c, const kvq_paged *pc, const kvq_chu
         const bool narrow = chunk_narrow(s.n_new, p.g);
         const int rows = narrow ? kNarrowRows : kWideRows;
         int64_t per = 0;
-        for (int64_t t = 0; t * rows < (int64_t)s.n_new * p.g; t++) per += chunk_tiles(s, (int)t, rows, p.g);
-        items += per * p.H_kv;
+        for (int64_t t = 0; t * rows < (int64_t)s.n_new * p.g; t++) {
+            const int n = chunk_tiles(s, (int)t, rows, p.g);
+            per += n + kUnitItems;
+            items += (int64_t)n * p.H_kv;
+        }
+        if (s.n_new && narrow) p.narrow = std::max(p.narrow, s.n_new * p.g);
+        if (s.n_new && !narrow) p.wide = 1;
         cost += per * p.H_kv * (narrow ? kNarrowCost : kWideCost);
         if (cost >= (1LL << 30)) return KVQ_ERR_UNSUPPORTED;
     }
     for (int b = c->B; b <= KVQ_PAGED_MAX_B; b++) p.cost0[b] = (int32_t)cost;
     p.cost = (int)cost;
-    p.C = (int)std::min<int64_t>(items, num_sms());
+    p.C = (int)std::min<int64_t>(items, std::min(num_sms(), kMaxRanges));
     return status_of(launch_chunk_attn(p, (cudaStream_t)stream));
 }
 

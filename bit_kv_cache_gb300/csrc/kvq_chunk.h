@@ -51,10 +51,12 @@ struct QkParams {
 // new token r / g under query head r % g of the key head's group.  Its items are key tiles
 // of 128 tokens: the packed ones, then the fp16 tokens [sink | residual | chunk] up to the
 // row tile's last query token.  A slot of at most kNarrowRows rows is one narrow unit per
-// head, whose items cost a third of a wide unit's (kWideRows rows); positions count cost.
-// The items of all units, slot-major, then by head and row tile, are cut into C ranges of
-// equal cost, one per CTA.  A unit inside one range is finished there; of one that is cut,
-// each range leaves fp32 partials, and the combine kernel joins them in range order.
+// head, a slot of more consists of wide ones (kWideRows rows).  Positions count cost: an
+// item's (kNarrowCost, kWideCost: 1.5 and 2.0 us measured) and, before a unit's first item,
+// that of kUnitItems more (the start and the end of a unit).  All units, slot-major, then by
+// head and row tile, are cut into C ranges of equal cost, one per CTA.  A unit inside one
+// range is finished there; of one that is cut, each range leaves fp32 partials, and the
+// combine kernels join them in range order.
 struct ChunkAttnParams {
     const int32_t *desc;
     const int32_t *ptab;
@@ -68,8 +70,9 @@ struct ChunkAttnParams {
     int32_t *status;
     int64_t q_stride, k_stride, v_stride, n_pages;
     int B, H_kv, g, G, kbits, vbits, S, R, ptab_stride;
-    int cost, C;                         // of all items; ranges
-    int32_t cost0[KVQ_PAGED_MAX_B + 1];  // position of each slot's first item
+    int cost, C;                         // of all units; ranges
+    int narrow, wide;                    // most rows of a narrow unit (0: there is none), whether there are wide ones
+    int32_t cost0[KVQ_PAGED_MAX_B + 1];  // position of each slot's first unit
 };
 
 cudaError_t launch_plan(const PlanParams &p, cudaStream_t st);
@@ -77,8 +80,29 @@ cudaError_t launch_extend(const ExtendParams &p, int kbits, int vbits, cudaStrea
 cudaError_t launch_qk(const QkParams &p, int D, cudaStream_t st);
 cudaError_t launch_chunk_attn(const ChunkAttnParams &p, cudaStream_t st);
 
-constexpr int kNarrowRows = 128, kWideRows = 256, kNarrowCost = 1, kWideCost = 3;
+constexpr int kNarrowRows = 128, kWideRows = 256, kNarrowCost = 3, kWideCost = 4, kUnitItems = 3, kMaxRanges = 256;
 __host__ __device__ inline bool chunk_narrow(int n_new, int g) { return (int64_t)n_new * g <= kNarrowRows; }
+// Copies of a narrow unit's rows in its query tile.
+__host__ __device__ inline int chunk_copies(int rows) { return rows > 64 ? 1 : rows > 32 ? 2 : 4; }
+
+// Launches a kernel that may start while the kernel before it in the stream drains; it calls
+// griddep_wait before it touches anything that one writes.
+template <typename K, typename... A>
+inline cudaError_t launch_dependent(K kernel, dim3 grid, int threads, int smem, cudaStream_t st, A... args) {
+    cudaLaunchConfig_t lc = {};
+    lc.gridDim = grid;
+    lc.blockDim = dim3((unsigned)threads);
+    lc.dynamicSmemBytes = (size_t)smem;
+    lc.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    lc.attrs = at;
+    lc.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&lc, kernel, args...);
+    return e == cudaSuccess ? cudaGetLastError() : e;
+}
+
 constexpr int kChunkKeys = 128;          // tokens per key tile
 
 // Key tiles of row tile t of a slot (rows query rows per tile, g per token).

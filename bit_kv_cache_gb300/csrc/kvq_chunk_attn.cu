@@ -18,10 +18,11 @@
 //                warp for all four was the bottleneck: a wait costs it about 200 cycles).
 // In a wide unit (256 rows) m names the query tile: a key tile is dequantized once for both.
 // In a narrow one (at most 128 rows) m is the parity of the key tile: the two groups keep
-// softmax states of their own, joined at the end.  With at most 64 (32) rows the query tile
-// holds them twice (four times), and each copy's softmax takes half (a quarter) of a tile's
-// keys: the tensor core's rows cost nothing, and a step of the softmax, which is what such a
-// unit waits for, is as much shorter.
+// softmax states of their own, joined at the end.  With at most 64 (32) rows, a part of a unit
+// that is cut holds them twice (four times) in its query tile, and each copy's softmax takes
+// half (a quarter) of a tile's keys: the tensor core's rows cost nothing, and a step of the
+// softmax, which is what such a unit waits for, is as much shorter.  The combine kernel joins
+// the copies' partials like those of the ranges.
 // A step is half a key tile (64 keys).  S_m has two buffers of 64 columns, so that the scores
 // of the next step are made while the softmax of this one runs.  Tensor memory: S_0, S_1,
 // O_0, O_1, 128 columns each.
@@ -77,12 +78,12 @@ __device__ __forceinline__ Seg next_seg(const ChunkAttnParams &p, int at, int en
     Seg s;
     s.it = find_item(p, at);
     s.narrow = s.it.rows == kNarrowRows;
-    s.k0 = (at - s.it.first) / s.it.w;
-    s.k1 = min(s.it.n, (end - s.it.first) / s.it.w);
-    s.end = s.it.first + s.k1 * s.it.w;
+    s.k0 = s.it.at(at);
+    s.k1 = s.it.at(end);
+    s.end = min(end, s.it.end());
     s.np = s.it.s.T / kChunkKeys;
     s.valid = min(s.it.rows, s.it.s.n_new * p.g - s.it.t * s.it.rows);
-    s.rep = !s.narrow || s.valid > 64 ? 1 : s.valid > 32 ? 2 : 4;
+    s.rep = s.narrow && s.k1 - s.k0 < s.it.n ? chunk_copies(s.valid) : 1;  // partials: each copy leaves its own
     // a wide unit's last key tile may end in its first half
     const int last = min(s.it.s.n_new, ((s.it.t + 1) * s.it.rows - 1) / p.g + 1);
     const int seen = s.it.s.ns + s.it.s.nr + last - (s.it.n - s.np - 1) * kChunkKeys;
@@ -163,28 +164,41 @@ __device__ __forceinline__ void make_tile(uint32_t raw, uint32_t tile, int t, in
     }
 }
 
+// 16 bytes from global to shared memory without registers (zeros if !ok).
+__device__ __forceinline__ void copy16(void *dst, const void *src, bool ok) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(ok ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy16_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
 // fp16 rows x0 .. x0 + 127 of [sink | residual | chunk]: row = token, 16-byte chunk c of a
 // row at block c / 8, position c ^ row within it (the layout of both tail operands: key
-// rows run along the tokens, value rows along the channels).  True if a value is not finite.
+// rows run along the tokens, value rows along the channels).  True if a value is not finite;
+// it is replaced by 0.
 __device__ __forceinline__ bool make_tail(const ChunkAttnParams &p, const Seg &s, int x0, bool value, unsigned char *tile, int tid) {
     const int ntail = s.it.s.ns + s.it.s.nr + s.it.s.n_new, c = tid & 15;
-    bool bad = false;
-#pragma unroll 4
+    unsigned char *col = tile + (c >> 3) * 16384;
+#pragma unroll 1
     for (int r = tid >> 4; r < kChunkKeys; r += 8) {
-        uint4 a = make_uint4(0, 0, 0, 0);
-        if (x0 + r < ntail) {
-            a = __ldg(reinterpret_cast<const uint4 *>(tail_row(p, s.it, x0 + r, value)) + c);
-            if (value) {
-                uint32_t *v = reinterpret_cast<uint32_t *>(&a);
-#pragma unroll
-                for (int e = 0; e < 4; e++) {
-                    if ((v[e] & 0x7c00u) == 0x7c00u) v[e] &= 0xffff0000u, bad = true;
-                    if ((v[e] & 0x7c000000u) == 0x7c000000u) v[e] &= 0xffffu, bad = true;
-                }
-            }
-        }
-        *reinterpret_cast<uint4 *>(tile + (c >> 3) * 16384 + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = a;
+        const int x = min(x0 + r, ntail - 1);
+        copy16(col + r * 128 + (((c & 7) ^ (r & 7)) << 4), tail_row(p, s.it, x, value) + 8 * c, x0 + r < ntail);
     }
+    copy16_wait();
+    bool bad = false;
+    if (value)
+#pragma unroll 1
+        for (int r = tid >> 4; r < kChunkKeys; r += 8) {
+            uint4 *at = reinterpret_cast<uint4 *>(col + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+            uint4 a = *at;
+            uint32_t *v = reinterpret_cast<uint32_t *>(&a);
+            bool here = false;
+#pragma unroll
+            for (int e = 0; e < 4; e++) {
+                if ((v[e] & 0x7c00u) == 0x7c00u) v[e] &= 0xffff0000u, here = true;
+                if ((v[e] & 0x7c000000u) == 0x7c000000u) v[e] &= 0xffffu, here = true;
+            }
+            if (here) *at = a;
+            bad |= here;
+        }
     return bad;
 }
 
@@ -274,14 +288,13 @@ __device__ __forceinline__ void produce(const ChunkAttnParams &p, unsigned char 
             nq++;
             const int ch = tid & 15, rows = s.rep > 1 ? 128 : (s.valid + 31) & ~31;  // whole warps of the softmax
             const int copy = s.rep > 1 ? 128 / s.rep - 1 : kRows - 1;
-#pragma unroll 4
+#pragma unroll 1
             for (int r = tid >> 4; r < rows; r += 8) {
-                const int x = s.it.t * s.it.rows + min(r & copy, s.valid - 1);
-                const uint4 a = __ldg(reinterpret_cast<const uint4 *>(p.q + (int64_t)(s.it.s.cu + x / p.g) * p.q_stride +
-                                                                      (s.it.h * p.g + x % p.g) * kD) + ch);
-                *reinterpret_cast<uint4 *>(sm + kOffQ + (r >> 7) * kTileBytes + (ch >> 3) * 16384 + (r & 127) * 128 +
-                                           (((ch & 7) ^ (r & 7)) << 4)) = a;
+                const int x = s.it.t * s.it.rows + min(r & copy, s.valid - 1), tok = x / p.g;
+                copy16(sm + kOffQ + (r >> 7) * kTileBytes + (ch >> 3) * 16384 + (r & 127) * 128 + (((ch & 7) ^ (r & 7)) << 4),
+                       p.q + (int64_t)(s.it.s.cu + tok) * p.q_stride + (s.it.h * p.g + x - tok * p.g) * kD + 8 * ch, true);
             }
+            copy16_wait();
             fence_proxy_async();
             mbar_arrive(&bar->q_full);
         }
@@ -597,55 +610,6 @@ __device__ __forceinline__ void softmax_tiles(const ChunkAttnParams &p, Bars *ba
     st.l = l;
 }
 
-// Joins the copies of a narrow unit's rows, which lie in the partial rows 128 .. 255 of
-// `slot` (written by this group before the barrier): a row's result goes to its output row,
-// or to its partial row.
-__device__ __forceinline__ void join_copies(const ChunkAttnParams &p, const Seg &s, size_t slot, bool whole, bool odd) {
-    asm volatile("bar.sync 1, 128;" ::: "memory");  // no thread of the group leaves before this
-    const int t = threadIdx.x & 127, row = t / s.rep, part = t - row * s.rep, R = 128 / s.rep, n = 32 / s.rep;
-    if (row >= s.valid) return;
-    const float2 *ml = p.part_ml + slot + 128 + row;
-    float mx = -INFINITY, l = 0.f, a[4];
-    for (int k = 0; k < s.rep; k++) mx = fmaxf(mx, ml[k * R].x);
-#pragma unroll
-    for (int k = 0; k < 4; k++) {
-        const float2 v = k < s.rep ? ml[k * R] : make_float2(-INFINITY, 0.f);
-        a[k] = k < s.rep && v.x == mx ? 1.f : ex2(v.x - mx);
-        if (k < s.rep) l += a[k] * v.y;
-    }
-    const int r = s.it.t * s.it.rows + row;
-    uint16_t *dst = p.out + ((int64_t)(s.it.s.cu + r / p.g) * p.H_kv * p.g + s.it.h * p.g + r % p.g) * kD;
-    const float4 *src = reinterpret_cast<const float4 *>(p.part_o + (slot + 128 + row) * kD);
-    const float inv = 1.f / l;
-    for (int i = part * n; i < part * n + n; i++) {
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int k = 0; k < 4; k++)
-            if (k < s.rep) {
-                const float4 v = src[(size_t)k * R * (kD / 4) + i];
-                o.x += a[k] * v.x;
-                o.y += a[k] * v.y;
-                o.z += a[k] * v.z;
-                o.w += a[k] * v.w;
-            }
-        if (odd) {
-            const int lim = s.it.s.ns + s.it.s.nr + r / p.g + 1;
-            for (int x = max(0, s.k0 - s.np) * kChunkKeys; x < min(lim, (s.k1 - s.np) * kChunkKeys); x++) {
-                const uint16_t *v = tail_row(p, s.it, x, true) + 4 * i;
-                float *f = &o.x;
-#pragma unroll
-                for (int e = 0; e < 4; e++) {
-                    const float y = h2f(v[e]);
-                    if (!isfinite(y)) f[e] += y;
-                }
-            }
-        }
-        if (whole) reinterpret_cast<uint2 *>(dst)[i] = make_uint2(pack_half2(o.x * inv, o.y * inv), pack_half2(o.z * inv, o.w * inv));
-        else reinterpret_cast<float4 *>(p.part_o + (slot + row) * kD)[i] = o;
-    }
-    if (!whole && part == 0) p.part_ml[slot + row] = make_float2(mx, l);
-}
-
 __device__ __forceinline__ void softmax(const ChunkAttnParams &p, Bars *bar, uint32_t tm, int m, int begin, int end) {
     const int lane_row = threadIdx.x & 127;
     const uint32_t lanes = (uint32_t)(threadIdx.x & 96) << 16;
@@ -674,7 +638,7 @@ __device__ __forceinline__ void softmax(const ChunkAttnParams &p, Bars *bar, uin
         float a0 = 1.f, a1 = 0.f;
         // the range's first segment has slot 2 c, its last one (a unit that goes on) 2 c + 1
         const size_t slot0 = (2 * (size_t)blockIdx.x + (last_first ? 1 : 0)) * kRows;
-        if (join) {  // O_1's states reach group 0 through the partial rows that its result may go to
+        if (join) {  // O_1's states reach group 0 through the partial rows that its result goes to
             float2 *state1 = p.part_ml + slot0;
             st.no1++;
             if (m == 1) {
@@ -695,11 +659,11 @@ __device__ __forceinline__ void softmax(const ChunkAttnParams &p, Bars *bar, uin
         const bool whole = s.k0 == 0 && s.k1 == s.it.n;
         const bool odd = *(volatile int *)&bar->odd[seg & 3] == seg + 1;
         const float inv = 1.f / l;
-        const bool direct = whole && s.rep == 1, mine = s.rep > 1 || row < s.valid;
-        const size_t slot = slot0 + (s.rep > 1 ? 128 + lane_row : row);
+        const bool mine = s.rep > 1 || row < s.valid;
+        const size_t slot = slot0 + (s.rep > 1 ? lane_row : row);
         uint16_t *dst = p.out + ((int64_t)(s.it.s.cu + r / p.g) * p.H_kv * p.g + s.it.h * p.g + r % p.g) * kD;
         if (any) {
-            if (!direct && mine) p.part_ml[slot] = make_float2(mx, l);
+            if (!whole && mine) p.part_ml[slot] = make_float2(mx, l);
 #pragma unroll 1
             for (int c = 0; c < 8; c++) {
                 uint32_t o[16];
@@ -715,8 +679,9 @@ __device__ __forceinline__ void softmax(const ChunkAttnParams &p, Bars *bar, uin
 #pragma unroll
                     for (int e = 0; e < 16; e++) f[e] = a0 * f[e] + a1 * __uint_as_float(o1[e]);
                 }
-                if (odd && s.rep == 1)
+                if (odd)
                     for (int x = max(0, s.k0 - s.np) * kChunkKeys; x < min(lim, (s.k1 - s.np) * kChunkKeys); x++) {
+                        if (s.rep > 1 && (x & 127) / (128 / s.rep) != lane_row / (128 / s.rep)) continue;  // another copy's key
                         const uint16_t *v = tail_row(p, s.it, x, true) + 16 * c;
 #pragma unroll
                         for (int e = 0; e < 16; e++) {
@@ -725,7 +690,7 @@ __device__ __forceinline__ void softmax(const ChunkAttnParams &p, Bars *bar, uin
                         }
                     }
                 if (mine) {
-                    if (direct) {
+                    if (whole) {
                         uint4 y[2];
                         uint32_t *w = reinterpret_cast<uint32_t *>(y);
 #pragma unroll
@@ -744,7 +709,6 @@ __device__ __forceinline__ void softmax(const ChunkAttnParams &p, Bars *bar, uin
         }
         tc_fence_before();
         if (join) mbar_arrive(&bar->o1_free);
-        if (s.rep > 1) join_copies(p, s, slot0, whole, odd);
     }
 }
 
@@ -787,6 +751,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attn_kernel(const __grid_co
     __syncthreads();
     tc_fence_after();
     const uint32_t tm = bar->tmem;
+    griddep_wait();
     const int begin = range_begin(p, blockIdx.x), end = range_begin(p, blockIdx.x + 1);
     if (w < 8) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
@@ -820,8 +785,7 @@ cudaError_t launch_chunk_combine(const ChunkAttnParams &p, cudaStream_t st);
 cudaError_t launch_chunk_attn(const ChunkAttnParams &p, cudaStream_t st) {
     cudaError_t e = cudaFuncSetAttribute(chunk_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
     if (e != cudaSuccess) return e;
-    chunk_attn_kernel<<<p.C, kThreads, kSmemBytes, st>>>(p);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    if ((e = launch_dependent(chunk_attn_kernel, dim3((unsigned)p.C), kThreads, kSmemBytes, st, p)) != cudaSuccess) return e;
     return launch_chunk_combine(p, st);
 }
 

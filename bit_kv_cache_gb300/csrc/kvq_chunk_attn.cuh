@@ -14,12 +14,15 @@ namespace kvq {
 constexpr int kD = 128;
 constexpr float kLog2e = 1.4426950408889634f;
 
-// Where a position lies: slot, key head, row tile; the unit's first position and number of
-// items, the cost of each, and its query rows.
+// A unit: slot, key head, row tile; its first position, number of items, the cost of each,
+// query rows.  Item 0 lies at the unit's first position, item j > 0 at first + (kUnitItems + j) w.
 struct Item {
     ChunkSlot s;
     int b, h, t;
     int first, n, w, rows;
+    __device__ __forceinline__ int end() const { return first + (n + kUnitItems) * w; }
+    // the item at a position where one lies, or n at the unit's end or behind it
+    __device__ __forceinline__ int at(int pos) const { return pos >= end() ? n : pos == first ? 0 : (pos - first) / w - kUnitItems; }
 };
 
 __device__ __forceinline__ ChunkSlot load_slot(const int32_t *desc, int b) {
@@ -38,34 +41,44 @@ __device__ __forceinline__ int slot_of(const ChunkAttnParams &p, int pos) {
     return lo;
 }
 
-__device__ __forceinline__ Item find_item(const ChunkAttnParams &p, int pos) {
+// Unit (slot, head, row tile) without its position in the slot's row tiles.
+__device__ __forceinline__ Item make_item(const ChunkAttnParams &p, int b) {
     Item r;
-    r.b = slot_of(p, pos);
-    r.s = load_slot(p.desc, r.b);
+    r.b = b;
+    r.s = load_slot(p.desc, b);
     const bool narrow = chunk_narrow(r.s.n_new, p.g);
     r.rows = narrow ? kNarrowRows : kWideRows;
     r.w = narrow ? kNarrowCost : kWideCost;
-    const int per = (p.cost0[r.b + 1] - p.cost0[r.b]) / p.H_kv;  // cost of one head
-    int x = pos - p.cost0[r.b];
-    r.h = x / per;
-    x = (x - r.h * per) / r.w;
-    int t = 0, a = 0;
-    for (;; t++) {
-        r.n = chunk_tiles(r.s, t, r.rows, p.g);
-        if (x < a + r.n) break;
-        a += r.n;
-    }
-    r.t = t;
-    r.first = p.cost0[r.b] + r.h * per + a * r.w;
     return r;
 }
 
-// First position of range c: an item starts there.
+__device__ __forceinline__ Item find_item(const ChunkAttnParams &p, int pos) {
+    Item r = make_item(p, slot_of(p, pos));
+    const int per = (p.cost0[r.b + 1] - p.cost0[r.b]) / p.H_kv;  // cost of one head
+    int x = pos - p.cost0[r.b];
+    r.h = x / per;
+    x -= r.h * per;
+    int t = 0, a = 0;
+    for (;; t++) {
+        r.n = chunk_tiles(r.s, t, r.rows, p.g);
+        const int c = (r.n + kUnitItems) * r.w;
+        if (x < a + c) break;
+        a += c;
+    }
+    r.t = t;
+    r.first = p.cost0[r.b] + r.h * per + a;
+    return r;
+}
+
+// First position of range c: that of an item.  A unit whose start is no further before the
+// even cut than its own fixed cost starts the range.
 __device__ __forceinline__ int range_begin(const ChunkAttnParams &p, int c) {
     const int pos = (int)((int64_t)c * p.cost / p.C);
     if (pos >= p.cost) return p.cost;
-    const int b = slot_of(p, pos), w = chunk_narrow(p.desc[8 * b + 3], p.g) ? kNarrowCost : kWideCost;
-    return p.cost0[b] + (pos - p.cost0[b] + w - 1) / w * w;
+    const Item it = find_item(p, pos);
+    const int x = (pos - it.first + it.w - 1) / it.w - kUnitItems;  // items before it, rounded up
+    if (x <= 0) return it.first;
+    return it.first + (kUnitItems + x) * it.w;                      // the unit's end if x = n
 }
 
 // Row of fp16 token x of [sink | residual | chunk].
