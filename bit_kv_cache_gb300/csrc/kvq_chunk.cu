@@ -555,6 +555,41 @@ ChunkWs chunk_ws() {
     return w;
 }
 
+// The C ranges: each starts at the item behind its even share of the cost.  A unit whose
+// start is no further before the even cut than its own fixed cost starts the range.
+void chunk_ranges(const kvq_config *c, const ChunkSlot *slots, ChunkAttnParams &p) {
+    int b = 0, t = 0;
+    int64_t head = 0, first = 0;  // start of the current head's units, and of unit t
+    for (int k = 0; k <= p.C; k++) {
+        const int64_t pos = (int64_t)k * p.cost / p.C;
+        if (pos >= p.cost) {
+            p.begin[k] = p.cost;
+            continue;
+        }
+        for (;;) {  // the unit that holds pos
+            while (p.cost0[b + 1] <= pos) head = first = p.cost0[++b], t = 0;
+            const ChunkSlot &s = slots[b];
+            const bool narrow = chunk_narrow(s.n_new, p.g);
+            const int rows = narrow ? kNarrowRows : kWideRows, w = narrow ? kNarrowCost : kWideCost;
+            const int64_t per = (p.cost0[b + 1] - p.cost0[b]) / c->H_kv;
+            if (pos >= head + per) {
+                head += (pos - head) / per * per;
+                first = head;
+                t = 0;
+            }
+            const int64_t end = first + (int64_t)(chunk_tiles(s, t, rows, p.g) + kUnitItems) * w;
+            if (pos >= end) {
+                first = end;
+                t++;
+                continue;
+            }
+            const int64_t x = (pos - first + w - 1) / w - kUnitItems;  // items before it, rounded up
+            p.begin[k] = (int32_t)(x <= 0 ? first : first + (kUnitItems + x) * w);
+            break;
+        }
+    }
+}
+
 }  // namespace
 
 extern "C" {
@@ -684,6 +719,7 @@ int kvq_paged_chunk_attn(const kvq_config *c, const kvq_paged *pc, const kvq_chu
     for (int b = c->B; b <= KVQ_PAGED_MAX_B; b++) p.cost0[b] = (int32_t)cost;
     p.cost = (int)cost;
     p.C = (int)std::min<int64_t>(items, std::min(num_sms(), kMaxRanges));
+    chunk_ranges(c, slots_of(ch), p);
     return status_of(launch_chunk_attn(p, (cudaStream_t)stream));
 }
 

@@ -47,6 +47,8 @@ struct QkParams {
     uint64_t turn[128];                  // base^(-2j/rotary) / (2 pi) in units of 2^-64 turns
 };
 
+constexpr int kNarrowRows = 128, kWideRows = 256, kNarrowCost = 3, kWideCost = 4, kUnitItems = 3, kMaxRanges = 256;
+
 // Chunk attention.  A unit is (slot, key head, tile of query rows): row r of a slot is its
 // new token r / g under query head r % g of the key head's group.  Its items are key tiles
 // of 128 tokens: the packed ones, then the fp16 tokens [sink | residual | chunk] up to the
@@ -73,6 +75,7 @@ struct ChunkAttnParams {
     int cost, C;                         // of all units; ranges
     int narrow, wide;                    // most rows of a narrow unit (0: there is none), whether there are wide ones
     int32_t cost0[KVQ_PAGED_MAX_B + 1];  // position of each slot's first unit
+    int32_t begin[kMaxRanges + 1];       // first position of each range, that of an item; begin[C] = cost
 };
 
 cudaError_t launch_plan(const PlanParams &p, cudaStream_t st);
@@ -80,7 +83,6 @@ cudaError_t launch_extend(const ExtendParams &p, int kbits, int vbits, cudaStrea
 cudaError_t launch_qk(const QkParams &p, int D, cudaStream_t st);
 cudaError_t launch_chunk_attn(const ChunkAttnParams &p, cudaStream_t st);
 
-constexpr int kNarrowRows = 128, kWideRows = 256, kNarrowCost = 3, kWideCost = 4, kUnitItems = 3, kMaxRanges = 256;
 __host__ __device__ inline bool chunk_narrow(int n_new, int g) { return (int64_t)n_new * g <= kNarrowRows; }
 // Copies of a narrow unit's rows in its query tile.
 __host__ __device__ inline int chunk_copies(int rows) { return rows > 64 ? 1 : rows > 32 ? 2 : 4; }

@@ -752,7 +752,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attn_kernel(const __grid_co
     tc_fence_after();
     const uint32_t tm = bar->tmem;
     griddep_wait();
-    const int begin = range_begin(p, blockIdx.x), end = range_begin(p, blockIdx.x + 1);
+    const int begin = p.begin[blockIdx.x], end = p.begin[blockIdx.x + 1];
     if (w < 8) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
         softmax(p, bar, tm, w >> 2, begin, end);

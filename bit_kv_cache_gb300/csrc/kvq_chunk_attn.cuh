@@ -70,17 +70,6 @@ __device__ __forceinline__ Item find_item(const ChunkAttnParams &p, int pos) {
     return r;
 }
 
-// First position of range c: that of an item.  A unit whose start is no further before the
-// even cut than its own fixed cost starts the range.
-__device__ __forceinline__ int range_begin(const ChunkAttnParams &p, int c) {
-    const int pos = (int)((int64_t)c * p.cost / p.C);
-    if (pos >= p.cost) return p.cost;
-    const Item it = find_item(p, pos);
-    const int x = (pos - it.first + it.w - 1) / it.w - kUnitItems;  // items before it, rounded up
-    if (x <= 0) return it.first;
-    return it.first + (kUnitItems + x) * it.w;                      // the unit's end if x = n
-}
-
 // Row of fp16 token x of [sink | residual | chunk].
 __device__ __forceinline__ const uint16_t *tail_row(const ChunkAttnParams &p, const Item &it, int x, bool value) {
     const size_t u = (size_t)it.b * p.H_kv + it.h;

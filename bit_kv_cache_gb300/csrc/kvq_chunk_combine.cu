@@ -37,14 +37,6 @@ __device__ __forceinline__ void store_row(const ChunkAttnParams &p, const Item &
 }
 constexpr Part kNone = {-INFINITY, 0.f, {0.f, 0.f, 0.f, 0.f}};
 
-// Range holding position x.
-__device__ __forceinline__ int range_of(const ChunkAttnParams &p, int x) {
-    int c = min(p.C - 1, (int)((int64_t)x * p.C / p.cost));
-    while (c > 0 && range_begin(p, c) > x) c--;
-    while (c + 1 < p.C && range_begin(p, c + 1) <= x) c++;
-    return c;
-}
-
 static_assert(kMaxRanges <= 256, "a thread per range");
 
 // Narrow units: CTA (head, slot, z) joins rows z, z + gridDim.z, ... of one, its eight warps
@@ -61,10 +53,10 @@ __global__ void __launch_bounds__(256) combine_narrow_kernel(const __grid_consta
     it.t = 0;
     it.n = chunk_tiles(it.s, 0, it.rows, p.g);
     it.first = p.cost0[it.b] + it.h * ((p.cost0[it.b + 1] - p.cost0[it.b]) / p.H_kv);
-    const int rep = chunk_copies(valid), R = 128 / rep, c0 = range_of(p, it.first);
+    const int rep = chunk_copies(valid), R = 128 / rep, last = it.end();
     // the partials' slots: a range's first segment has slot 2 c, one that starts later 2 c + 1
-    const int c = c0 + tid, a = c < p.C ? range_begin(p, c) : p.cost, b = c < p.C ? range_begin(p, c + 1) : p.cost;
-    const bool in = a < it.end() && b > a;
+    const int a = tid < p.C ? p.begin[tid] : p.cost, b = tid < p.C ? p.begin[tid + 1] : p.cost;
+    const bool in = a < last && b > it.first && b > a;
     const unsigned m = __ballot_sync(0xffffffffu, in);
     if (lane == 0) s_n[w] = __popc(m);
     __syncthreads();
@@ -73,7 +65,7 @@ __global__ void __launch_bounds__(256) combine_narrow_kernel(const __grid_consta
         if (i < w) at += s_n[i];
         parts += s_n[i];
     }
-    if (in) s_slot[at] = 2 * c + (c == c0 && a != it.first ? 1 : 0);
+    if (in) s_slot[at] = 2 * tid + (a < it.first ? 1 : 0);
     __syncthreads();
     if (parts == 1) return;  // written by its range
     for (int row = blockIdx.z; row < valid; row += gridDim.z) {
@@ -96,16 +88,16 @@ __global__ void __launch_bounds__(256) combine_narrow_kernel(const __grid_consta
 // inside the unit: 32 rows each, a warp per row.
 __global__ void __launch_bounds__(256) combine_wide_kernel(const __grid_constant__ ChunkAttnParams p) {
     griddep_wait();
-    const int c = blockIdx.x + 1, cut = range_begin(p, c);
+    const int c = blockIdx.x + 1, cut = p.begin[c];
     if (cut >= p.cost) return;
     const Item it = find_item(p, cut);
-    const int begin = range_begin(p, c - 1), lane = threadIdx.x & 31;
+    const int begin = p.begin[c - 1], lane = threadIdx.x & 31;
     if (it.rows != kWideRows || it.first == cut || it.first < begin) return;
     const int valid = min(it.rows, it.s.n_new * p.g - it.t * it.rows), end = it.end();
     for (int row = blockIdx.y * 32 + (threadIdx.x >> 5); row < min(valid, (int)blockIdx.y * 32 + 32); row += 8) {
         Part acc = load_part(p, (2 * (size_t)(c - 1) + (it.first == begin ? 0 : 1)) * kWideRows + row, lane);
         for (int k = c, at = cut; at < end; k++) {
-            const int next = range_begin(p, k + 1);
+            const int next = p.begin[k + 1];
             if (next > at) join(acc, load_part(p, 2 * (size_t)k * kWideRows + row, lane));
             at = next;
         }
