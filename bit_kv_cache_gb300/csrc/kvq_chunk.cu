@@ -43,6 +43,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
     __shared__ int s_row[kPlanThreads + 1], s_page[kPlanThreads + 1], s_pos[kPlanThreads], s_lp[kPlanThreads];
     __shared__ int2 s_warp[kPlanThreads / 32];
     const int b = threadIdx.x, lane = b & 31, w = b >> 5;
+    griddep_wait();
     int4 ln = make_int4(0, 0, 0, 0);
     int n = 0, to_sink = 0, pk = 0;
     if (b < p.B) {
@@ -116,8 +117,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
 cudaError_t launch_plan(const PlanParams &p, cudaStream_t st) {
     const int64_t per = 4 * kPlanThreads;
     const int grid = (int)std::max<int64_t>(1, std::min<int64_t>(64, (p.n_tokens + per - 1) / per));
-    plan_kernel<<<grid, kPlanThreads, 0, st>>>(p);
-    return cudaGetLastError();
+    return launch_dependent(plan_kernel, dim3((unsigned)grid), kPlanThreads, 0, st, p);
 }
 
 // ------------------------------------------------------------------------------
@@ -340,6 +340,7 @@ template <int TPW>
 __global__ void __launch_bounds__(256, TPW == 16 ? 4 : 2) extend_pack_kernel(const ExtendParams p, int kbits, int vbits) {
     __shared__ __align__(16) unsigned char smem[32 * 512 + 512];
     const int h = blockIdx.y;
+    griddep_wait();
     const PageJob jb = find_page(p, blockIdx.x);
     if (blockIdx.z == 0) {
         if (kbits == 2) extend_keys<2, TPW>(p, jb, h, smem);
@@ -359,6 +360,7 @@ __global__ void __launch_bounds__(256, TPW == 16 ? 4 : 2) extend_pack_kernel(con
 constexpr int kTailSlices = 4;
 __global__ void __launch_bounds__(256) extend_tail_kernel(const ExtendParams p) {
     const int b = blockIdx.x, h = blockIdx.y >> 1, side = blockIdx.y & 1;
+    griddep_wait();
     const int4 *d = reinterpret_cast<const int4 *>(p.desc);
     const int4 x = d[2 * b];
     if (!x.w) return;
@@ -384,30 +386,34 @@ __global__ void __launch_bounds__(256) extend_tail_kernel(const ExtendParams p) 
 cudaError_t launch_extend(const ExtendParams &p, int kbits, int vbits, cudaStream_t st) {
     if (p.n_pack > 0) {
         const dim3 grid((unsigned)p.n_pack, (unsigned)p.H_kv, (unsigned)(1 + p.G / 128));
-        if (p.G == 128) extend_pack_kernel<16><<<grid, 256, 0, st>>>(p, kbits, vbits);
-        else if (p.G == 256) extend_pack_kernel<32><<<grid, 256, 0, st>>>(p, kbits, vbits);
-        else return cudaErrorInvalidValue;
-        const cudaError_t e = cudaGetLastError();
+        cudaError_t e = cudaErrorInvalidValue;
+        if (p.G == 128) e = launch_dependent(extend_pack_kernel<16>, grid, 256, 0, st, p, kbits, vbits);
+        else if (p.G == 256) e = launch_dependent(extend_pack_kernel<32>, grid, 256, 0, st, p, kbits, vbits);
         if (e != cudaSuccess) return e;
     }
-    extend_tail_kernel<<<dim3((unsigned)p.B, (unsigned)(2 * p.H_kv), kTailSlices), 256, 0, st>>>(p);
-    return cudaGetLastError();
+    return launch_dependent(extend_tail_kernel, dim3((unsigned)p.B, (unsigned)(2 * p.H_kv), kTailSlices), 256, 0, st, p);
 }
 
 // ------------------------------------------------------------------------------
-// Norm and rotation of new queries and keys.  A warp holds one head's row (D / 32
-// consecutive channels per lane), a CTA a token's heads; the token's sines and cosines are
-// formed once per CTA.  An angle pos * base^(-2j/n) is reduced in 64-bit fixed point:
-// pos * turn[j] mod 2^64 is the exact fraction of a turn, whose upper 32 bits go to
-// sincospif.
+// Norm and rotation of new queries and keys.  D / 8 lanes hold a head's row, 16 bytes each,
+// a CTA a token's heads (or a part of them); a thread's channels are the same in all its
+// rows, so that their weights, sines and cosines are loaded once.  An angle
+// pos * base^(-2j/n) is reduced in 64-bit fixed point: pos * turn[j] mod 2^64 is the exact
+// fraction of a turn, whose upper 32 bits go to sincospif.
 // ------------------------------------------------------------------------------
+constexpr int kQkRows = 3;  // rows of a thread in flight
+
 template <int D>
 __global__ void __launch_bounds__(256) qk_kernel(const __grid_constant__ QkParams p, int heads) {
-    constexpr int E = D / 32;
-    using Vec = typename std::conditional<E == 2, uint32_t, typename std::conditional<E == 4, uint2, uint4>::type>::type;
+    constexpr int L = D / 8, PER = 256 / L;  // lanes per row, rows per pass of the CTA
     __shared__ float2 s_cs[D / 2];
     const int64_t i = blockIdx.x;
-    const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, half = p.rotary >> 1;
+    const int tid = threadIdx.x, l = tid % L, c0 = 8 * l, half = p.rotary >> 1, hl = half / 8;
+    const int h0 = blockIdx.y * heads, h1 = min(p.H_q + p.H_kv, h0 + heads);  // the CTA's heads: queries, then keys
+    // halves: the lane's partner is hl lanes off; interleaved: partners are neighbours
+    const bool second = p.halves && l >= hl;
+    const int off = !p.halves ? 0 : l < hl ? hl : l < 2 * hl ? -hl : 0;
+    griddep_wait();
     if (tid < half) {
         const uint64_t a = (uint64_t)(int64_t)p.pos[i] * p.turn[tid];
         float s, c;
@@ -415,77 +421,97 @@ __global__ void __launch_bounds__(256) qk_kernel(const __grid_constant__ QkParam
         s_cs[tid] = make_float2(c, s);
     }
     __syncthreads();
-    const int H = p.H_q + p.H_kv, h1 = min(H, (int)(blockIdx.y + 1) * heads);
-    for (int h = blockIdx.y * heads + w; h < h1; h += 8) {
-        const bool key = h >= p.H_q;
-        const uint16_t *src = key ? p.k + i * p.k_stride + (h - p.H_q) * D : p.q + i * p.q_stride + h * D;
-        uint16_t *dst = key ? p.k_out + (i * p.H_kv + h - p.H_q) * D : p.q_out + (i * p.H_q + h) * D;
-        const uint16_t *wt = key ? p.w_k : p.w_q;
-        Vec v = reinterpret_cast<const Vec *>(src)[lane];
-        float x[E];
+#pragma unroll 1
+    for (int side = 0; side < 2; side++) {
+        const int lo = side ? max(h0 - p.H_q, 0) : h0, hi = side ? h1 - p.H_q : min(h1, p.H_q);  // heads of this side
+        if (lo >= hi) continue;
+        const uint16_t *src = (side ? p.k + i * p.k_stride : p.q + i * p.q_stride) + c0;
+        uint16_t *dst = (side ? p.k_out + i * p.H_kv * D : p.q_out + i * p.H_q * D) + c0;
+        const uint16_t *wt = side ? p.w_k : p.w_q;
+        uint4 v[kQkRows];
+        const int first = lo + tid / L;
 #pragma unroll
-        for (int e = 0; e < E; e += 2) {
-            const float2 f = unpack_half2(reinterpret_cast<const uint32_t *>(&v)[e / 2]);
-            x[e] = f.x;
-            x[e + 1] = f.y;
-        }
-        if (wt) {
-            float ss = 0.f;
+        for (int r = 0; r < kQkRows; r++)
+            if (first + r * PER < hi) v[r] = __ldcs(reinterpret_cast<const uint4 *>(src + (first + r * PER) * D));
+        // y = f (x a + partner b): the weights are folded into sine and cosine
+        float a[8], b[8];
+        {
+            float w[8], wp[8];
+            if (wt) {
+                const uint4 u = __ldg(reinterpret_cast<const uint4 *>(wt + c0));
+                const uint4 o = __ldg(reinterpret_cast<const uint4 *>(wt + c0 + 8 * off));
 #pragma unroll
-            for (int e = 0; e < E; e++) ss += x[e] * x[e];
-#pragma unroll
-            for (int o = 16; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-            const float r = rsqrtf(ss * (1.0f / D) + p.eps);
-            const Vec wv = reinterpret_cast<const Vec *>(wt)[lane];
-#pragma unroll
-            for (int e = 0; e < E; e += 2) {
-                const float2 f = unpack_half2(reinterpret_cast<const uint32_t *>(&wv)[e / 2]);
-                x[e] = x[e] * r * f.x;
-                x[e + 1] = x[e + 1] * r * f.y;
-            }
-        }
-        if (p.rotate & (key ? 2 : 1)) {
-            const int c0 = lane * E;
-            if (!p.halves) {
-                if (c0 < p.rotary)
-#pragma unroll
-                    for (int e = 0; e < E; e += 2) {
-                        const float2 cs = s_cs[(c0 + e) >> 1];
-                        const float a = x[e], b = x[e + 1];
-                        x[e] = a * cs.x - b * cs.y;
-                        x[e + 1] = a * cs.y + b * cs.x;
-                    }
-            } else {
-                const int hl = half / E;  // lanes of the first half (half is a multiple of E)
-                const int other = lane < hl ? lane + hl : lane < 2 * hl ? lane - hl : lane;
-                const int j0 = lane < hl ? c0 : c0 - half;
-#pragma unroll
-                for (int e = 0; e < E; e++) {
-                    const float o = __shfl_sync(0xffffffffu, x[e], other);
-                    if (lane < 2 * hl) {
-                        const float2 cs = s_cs[j0 + e];
-                        x[e] = lane < hl ? x[e] * cs.x - o * cs.y : o * cs.y + x[e] * cs.x;
-                    }
+                for (int e = 0; e < 4; e++) {
+                    const float2 f = unpack_half2((&u.x)[e]), g = unpack_half2((&o.x)[e]);
+                    w[2 * e] = f.x;
+                    w[2 * e + 1] = f.y;
+                    wp[2 * e] = p.halves ? g.x : f.y;
+                    wp[2 * e + 1] = p.halves ? g.y : f.x;
                 }
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; e++) w[e] = wp[e] = 1.f;
+            }
+            const bool turn = c0 < p.rotary && (p.rotate & (side ? 2 : 1));
+#pragma unroll
+            for (int e = 0; e < 8; e++) {
+                const int j = !p.halves ? (c0 + e) >> 1 : (second ? c0 - half : c0) + e;
+                const float2 cs = turn ? s_cs[j] : make_float2(1.f, 0.f);
+                const bool up = p.halves ? second : (e & 1);  // the pair's second channel
+                a[e] = w[e] * cs.x;
+                b[e] = up ? wp[e] * cs.y : -wp[e] * cs.y;
             }
         }
+        for (int h = first; __any_sync(0xffffffffu, h < hi); h += kQkRows * PER) {
 #pragma unroll
-        for (int e = 0; e < E; e += 2) reinterpret_cast<uint32_t *>(&v)[e / 2] = pack_half2(x[e], x[e + 1]);
-        reinterpret_cast<Vec *>(dst)[lane] = v;
+            for (int r = 0; r < kQkRows; r++) {
+                const int hh = h + r * PER;
+                if (!__any_sync(0xffffffffu, hh < hi)) break;
+                const uint32_t *u = reinterpret_cast<const uint32_t *>(&v[r]);
+                float x[8], y[8];
+#pragma unroll
+                for (int e = 0; e < 4; e++) {
+                    const float2 f = unpack_half2(u[e]);
+                    x[2 * e] = f.x;
+                    x[2 * e + 1] = f.y;
+                }
+                float f = 1.f;
+                if (wt) {
+                    float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+                    for (int e = 0; e < 8; e += 2) {
+                        s0 += x[e] * x[e];
+                        s1 += x[e + 1] * x[e + 1];
+                    }
+                    s0 += s1;
+#pragma unroll
+                    for (int o = L / 2; o; o >>= 1) s0 += __shfl_xor_sync(0xffffffffu, s0, o);
+                    f = rsqrtf(s0 * (1.0f / D) + p.eps);
+                }
+#pragma unroll
+                for (int e = 0; e < 8; e++) {
+                    const float o = p.halves ? __shfl_sync(0xffffffffu, x[e], (tid & 31) + off) : x[e ^ 1];
+                    y[e] = f * (x[e] * a[e] + o * b[e]);
+                }
+                if (hh < hi)
+                    *reinterpret_cast<uint4 *>(dst + hh * D) = make_uint4(pack_half2(y[0], y[1]), pack_half2(y[2], y[3]),
+                                                                         pack_half2(y[4], y[5]), pack_half2(y[6], y[7]));
+                if (hh + kQkRows * PER < hi) v[r] = __ldcs(reinterpret_cast<const uint4 *>(src + (hh + kQkRows * PER) * D));
+            }
+        }
     }
 }
 
 cudaError_t launch_qk(const QkParams &p, int D, cudaStream_t st) {
-    const int H = p.H_q + p.H_kv;
-    // few tokens: their heads go to several CTAs, eight at least each
+    const int H = p.H_q + p.H_kv, pass = 256 / (D / 8);
+    // few tokens: their heads go to several CTAs, one pass of rows at least each
     int y = 1;
-    while (p.n * y < 2 * num_sms() && (H + y - 1) / y > 8) y++;
+    while (p.n * y < 2 * num_sms() && (H + y - 1) / y > pass) y++;
     const int heads = (H + y - 1) / y;
     const dim3 grid((unsigned)p.n, (unsigned)((H + heads - 1) / heads));
-    if (D == 64) qk_kernel<64><<<grid, 256, 0, st>>>(p, heads);
-    else if (D == 128) qk_kernel<128><<<grid, 256, 0, st>>>(p, heads);
-    else qk_kernel<256><<<grid, 256, 0, st>>>(p, heads);
-    return cudaGetLastError();
+    if (D == 64) return launch_dependent(qk_kernel<64>, grid, 256, 0, st, p, heads);
+    if (D == 128) return launch_dependent(qk_kernel<128>, grid, 256, 0, st, p, heads);
+    return launch_dependent(qk_kernel<256>, grid, 256, 0, st, p, heads);
 }
 
 }  // namespace kvq
