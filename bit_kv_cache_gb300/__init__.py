@@ -149,24 +149,29 @@ def make_config(B, H_q, H_kv, D, G, bits, S=0, R=None, n_boost=0, mode="kivi", m
                   1 if rope_base else 0, float(rope_base or 0.0))
 
 
-def _stream_of(device):
-    """The current stream of a device, which must be the current device."""
+def _stream_of(index):
+    """The current stream (cudaStream_t) of a device, which must be the current device."""
     import torch
-    if torch.cuda.current_device() != device.index:
-        raise ValueError("the tensors are on %s, which is not the current device" % device)
-    return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+    if torch._C._cuda_getDevice() != index:
+        raise ValueError("the tensors are on cuda:%d, which is not the current device" % index)
+    return torch._C._cuda_getCurrentRawStream(index)
 
 
 def _rows(t, heads, D, n, device, what):
-    """(pointer, row stride) of token-major rows [>= n][heads][D], float16, heads adjacent."""
-    import torch
-    if t.device != device or t.dtype != torch.float16:
+    """(address, row stride) of token-major rows [>= n][heads][D], float16, heads adjacent."""
+    if t.device != device or t.dtype != _float16():
         raise ValueError("%s must be a float16 tensor on %s" % (what, device))
-    if t.dim() != 3 or t.shape[0] < n or t.shape[1] != heads or t.shape[2] != D:
-        raise ValueError("%s has shape %s, expected at least [%d, %d, %d]" % (what, tuple(t.shape), n, heads, D))
-    if (D > 1 and t.stride(2) != 1) or (heads > 1 and t.stride(1) != D):
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 3 or shape[0] < n or shape[1] != heads or shape[2] != D:
+        raise ValueError("%s has shape %s, expected at least [%d, %d, %d]" % (what, tuple(shape), n, heads, D))
+    if stride[2] != 1 or (heads > 1 and stride[1] != D):
         raise ValueError("%s must hold each token's heads contiguously" % what)
-    return ctypes.c_void_p(t.data_ptr()), (t.stride(0) if t.shape[0] > 1 else heads * D)
+    return t.data_ptr(), (stride[0] if shape[0] > 1 else heads * D)
+
+
+def _float16():
+    import torch
+    return torch.float16
 
 
 def qk_norm_rope(q, k=None, w_q=None, w_k=None, pos=None, eps=1e-6, rope_base=10000.0, rotary_dim=None,
@@ -204,9 +209,9 @@ def qk_norm_rope(q, k=None, w_q=None, w_k=None, pos=None, eps=1e-6, rope_base=10
             raise ValueError("%s must be a contiguous float16 tensor [%d, %d, %d] on %s" % (what, n, H, D, dev))
     c = QkConfig(H_q, H_kv, D, D if rotary_dim is None else rotary_dim, int(bool(halves)),
                  int(bool(rotate_q)) + 2 * int(bool(rotate_k)), eps, rope_base, qs, ks)
-    ptr = lambda t: None if t is None else ctypes.c_void_p(t.data_ptr())  # noqa: E731
-    _check(lib.kvq_qk_norm_rope(ctypes.byref(c), qp, kp, ptr(w_q), ptr(w_k), ptr(pos), n, ptr(q_out), ptr(k_out),
-                                _stream_of(dev)), "kvq_qk_norm_rope")
+    _check(lib.kvq_qk_norm_rope(ctypes.byref(c), qp, kp, None if w_q is None else w_q.data_ptr(),
+                                None if w_k is None else w_k.data_ptr(), pos.data_ptr(), n, q_out.data_ptr(),
+                                None if k_out is None else k_out.data_ptr(), _stream_of(dev.index)), "kvq_qk_norm_rope")
     return q_out, k_out
 
 
@@ -228,9 +233,11 @@ class KVQChunk:
         self.B = cfg.B
         pad = torch.zeros(4, **i32) if max_tokens == 0 else None  # an empty tensor has no address
         self._pad = pad
+        self.ws_ptr, self.ws_bytes = self.ws.data_ptr(), self.ws.numel()
         self.c = ChunkDesc(self.cu.data_ptr(), (self.slot if pad is None else pad).data_ptr(),
                            (self.pos if pad is None else pad).data_ptr(), self.desc.data_ptr(),
                            ctypes.cast(self.host, ctypes.c_void_p), max_tokens, 0)
+        self.ref = ctypes.byref(self.c)
 
     @property
     def n_tokens(self) -> int:
@@ -472,6 +479,8 @@ class KVQPagedCache:
         self.p.lens_host = ctypes.cast(self.lens_host, ctypes.c_void_p)
         self.p.status = self.status.data_ptr()
         self.ws = torch.zeros(lib.kvq_paged_workspace_bytes(cp), dtype=torch.uint8, device=self.device)
+        self._dev = self.table.device                 # with its index
+        self._refs = ctypes.byref(self.cfg), ctypes.byref(self.p)
         self.caller_pages = False                     # plan() was given pages of the caller's
         self.free = list(range(n_pages - 1, -1, -1))  # pop() hands out the lowest id first
         self.pages = [[] for _ in range(B)]           # physical pages of each slot, logical order
@@ -540,7 +549,7 @@ class KVQPagedCache:
     def clear(self, unmap=True):
         """Empties every slot.  unmap=False: the pages stay mapped to their slots, which
         refill them."""
-        _check(lib.kvq_paged_init(ctypes.byref(self.cfg), ctypes.byref(self.p), _stream_of(self.table.device)),
+        _check(lib.kvq_paged_init(*self._refs, _stream_of(self._dev.index)),
                "paged init")
         if unmap:
             for b in range(self.cfg.B - 1, -1, -1):
@@ -550,7 +559,7 @@ class KVQPagedCache:
     # -- chunks of new tokens ------------------------------------------------- #
     def new_chunk(self, max_tokens) -> KVQChunk:
         """Buffers for plans of up to max_tokens new tokens."""
-        return KVQChunk(self.cfg, max_tokens, self.table.device)
+        return KVQChunk(self.cfg, max_tokens, self._dev)
 
     def plan(self, n_new, chunk=None, pages=None) -> KVQChunk:
         """Plans n_new[b] new tokens for every slot (kvq_paged_plan): slot maps, positions,
@@ -562,7 +571,7 @@ class KVQPagedCache:
         if isinstance(n_new, torch.Tensor):
             if n_new.device.type != "cpu" or n_new.dtype != torch.int32 or n_new.shape != (cfg.B,) or not n_new.is_contiguous():
                 raise ValueError("n_new must be a contiguous int32 CPU tensor [%d]" % cfg.B)
-            np_ = ctypes.c_void_p(n_new.data_ptr())
+            np_ = n_new.data_ptr()
         else:
             n_new = [int(x) for x in n_new]
             if len(n_new) != cfg.B or any(not 0 <= x < 1 << 31 for x in n_new):
@@ -570,18 +579,17 @@ class KVQPagedCache:
             np_ = (ctypes.c_int32 * cfg.B)(*n_new)
         if chunk is None:
             chunk = self.new_chunk(int(sum(n_new)))
-        if chunk.B != cfg.B or chunk.cu.device != self.table.device:
+        if chunk.B != cfg.B or chunk.cu.device != self._dev:
             raise ValueError("the chunk belongs to another configuration")
         if pages is None:
             pages = self._plan_pages(n_new.tolist() if isinstance(n_new, torch.Tensor) else n_new)
-        elif pages.device != self.table.device or pages.dtype != torch.int32 or pages.dim() != 1 or not pages.is_contiguous():
-            raise ValueError("pages must be a contiguous int32 tensor on %s" % self.table.device)
+        elif pages.device != self._dev or pages.dtype != torch.int32 or pages.dim() != 1 or not pages.is_contiguous():
+            raise ValueError("pages must be a contiguous int32 tensor on %s" % self._dev)
         else:
             self.caller_pages = True
-        _check(lib.kvq_paged_plan(ctypes.byref(cfg), ctypes.byref(self.p), np_,
-                                  None if pages is None else ctypes.c_void_p(pages.data_ptr()),
-                                  0 if pages is None else pages.numel(), ctypes.byref(chunk.c),
-                                  _stream_of(self.table.device)), "kvq_paged_plan")
+        _check(lib.kvq_paged_plan(*self._refs, np_, None if pages is None else pages.data_ptr(),
+                                  0 if pages is None else pages.numel(), chunk.ref, _stream_of(self._dev.index)),
+               "kvq_paged_plan")
         return chunk
 
     def _plan_pages(self, n_new):
@@ -610,14 +618,14 @@ class KVQPagedCache:
                 self.pages[b].append(self.free.pop())
             ids += self.pages[b][lo:hi]
         t = self.torch.tensor(ids, dtype=self.torch.int32).pin_memory()
-        return t.to(self.table.device, non_blocking=True)
+        return t.to(self._dev, non_blocking=True)
 
     def chunk_attn(self, chunk, q, k_new, v_new, out=None):
         """Attention of the planned chunk's tokens over the cached tokens and, causally, the
         chunk (kvq_paged_chunk_attn).  q: float16 [n, H_q, D], k_new, v_new: float16
         [n, H_kv, D], n >= chunk.n_tokens, token-major rows that may be strided; rows behind
         chunk.n_tokens are left alone.  The cache is not changed."""
-        torch, cfg, dev, n = self.torch, self.cfg, self.table.device, chunk.n_tokens
+        torch, cfg, dev, n = self.torch, self.cfg, self._dev, chunk.n_tokens
         qp, qs = _rows(q, cfg.H_q, cfg.D, n, dev, "q")
         kp, ks = _rows(k_new, cfg.H_kv, cfg.D, n, dev, "k_new")
         vp, vs = _rows(v_new, cfg.H_kv, cfg.D, n, dev, "v_new")
@@ -626,18 +634,16 @@ class KVQPagedCache:
         op, os_ = _rows(out, cfg.H_q, cfg.D, n, dev, "out")
         if os_ != cfg.H_q * cfg.D:
             raise ValueError("out must be contiguous")
-        _check(lib.kvq_paged_chunk_attn(ctypes.byref(cfg), ctypes.byref(self.p), ctypes.byref(chunk.c), qp, qs, kp, ks,
-                                        vp, vs, op, ctypes.c_void_p(chunk.ws.data_ptr()), chunk.ws.numel(),
-                                        _stream_of(dev)), "kvq_paged_chunk_attn")
+        _check(lib.kvq_paged_chunk_attn(*self._refs, chunk.ref, qp, qs, kp, ks, vp, vs, op, chunk.ws_ptr, chunk.ws_bytes,
+                                        _stream_of(dev.index)), "kvq_paged_chunk_attn")
         return out
 
     def extend(self, chunk, k_new, v_new):
         """The planned chunk's tokens enter the cache (kvq_paged_extend)."""
-        cfg, dev = self.cfg, self.table.device
+        cfg, dev = self.cfg, self._dev
         kp, ks = _rows(k_new, cfg.H_kv, cfg.D, chunk.n_tokens, dev, "k_new")
         vp, vs = _rows(v_new, cfg.H_kv, cfg.D, chunk.n_tokens, dev, "v_new")
-        _check(lib.kvq_paged_extend(ctypes.byref(cfg), ctypes.byref(self.p), ctypes.byref(chunk.c), kp, ks, vp, vs,
-                                    _stream_of(dev)), "kvq_paged_extend")
+        _check(lib.kvq_paged_extend(*self._refs, chunk.ref, kp, ks, vp, vs, _stream_of(dev.index)), "kvq_paged_extend")
 
     def chunk_step(self, n_new, q, k, v, w_q=None, w_k=None, eps=1e-6, rope_base=10000.0, rotary_dim=None,
                    halves=False, chunk=None, out=None):

@@ -335,12 +335,49 @@ __device__ __forceinline__ void extend_values(const ExtendParams &p, const PageJ
             *reinterpret_cast<const uint4 *>(&s_meta[4 * tid]);
 }
 
-// G = 8 TPW tokens per page.
+// Rows of a slot that stay fp16: its new sink rows and, from row lo on, its residual's new
+// rows up to hi, which are the chunk's last tokens (a slot that packs nothing keeps its old
+// rows, one that packs takes all of them).  Sixteen threads per row, thread t of n.
+__device__ __forceinline__ void keep_rows(const ExtendParams &p, const int4 &x, const int4 &y, int b, int h, int side, bool sink,
+                                          bool residual, int t, int n) {
+    const int to_sink = sink ? y.y : 0, pk = y.z, lo = pk ? 0 : x.z, hi = residual ? x.z + x.w - y.y - pk : lo;
+    const int64_t stride = side ? p.v_stride : p.k_stride;
+    const uint16_t *src = (side ? p.v_new : p.k_new) + h * 128;
+    const size_t u = (size_t)b * p.H_kv + h;
+    uint16_t *sk = side ? p.v_sink : p.k_sink, *res = side ? p.v_res : p.k_res;
+    const int rows = to_sink + hi - lo, c = t & 15;
+    for (int i = t >> 4; i < rows; i += n >> 4) {
+        const int r = i - to_sink + lo;
+        const int tok = i < to_sink ? i : y.y + pk + r - x.z;
+        uint16_t *dst = i < to_sink ? sk + (u * p.S + x.x + i) * 128 : res + (u * p.R + r) * 128;
+        reinterpret_cast<uint4 *>(dst)[c] = __ldg(reinterpret_cast<const uint4 *>(src + (int64_t)(y.x + tok) * stride) + c);
+    }
+}
+
+// Whether one page holds all old residual rows of a slot, so that the CTA that packs it may
+// overwrite them: then one launch does the whole call.
+__host__ __device__ inline bool extend_once(const ExtendParams &p) { return p.R == p.G && p.G == 128; }
+
+// Slot b's fp16 rows and lengths; slice z of nz.
+__device__ __forceinline__ void extend_slot(const ExtendParams &p, int b, int h, int side, int z, int nz) {
+    const int4 *d = reinterpret_cast<const int4 *>(p.desc);
+    const int4 x = d[2 * b], y = d[2 * b + 1];
+    if (!x.w) return;
+    keep_rows(p, x, y, b, h, side, true, !(extend_once(p) && y.z), z * 256 + threadIdx.x, nz * 256);
+    if (h == 0 && side == 0 && z == 0 && threadIdx.x == 0)
+        reinterpret_cast<int4 *>(p.lens)[b] = make_int4(x.x + y.y, x.y + y.z, x.z + x.w - y.y - y.z, 1);
+}
+
+// Page blockIdx.x of the call (G = 8 TPW tokens), or, behind them, a slot's fp16 rows.
 template <int TPW>
 __global__ void __launch_bounds__(256, TPW == 16 ? 4 : 2) extend_pack_kernel(const ExtendParams p, int kbits, int vbits) {
     __shared__ __align__(16) unsigned char smem[32 * 512 + 512];
     const int h = blockIdx.y;
     griddep_wait();
+    if (blockIdx.x >= p.n_pack) {
+        extend_slot(p, blockIdx.x - p.n_pack, h, blockIdx.z, 0, 1);
+        return;
+    }
     const PageJob jb = find_page(p, blockIdx.x);
     if (blockIdx.z == 0) {
         if (kbits == 2) extend_keys<2, TPW>(p, jb, h, smem);
@@ -352,44 +389,27 @@ __global__ void __launch_bounds__(256, TPW == 16 ? 4 : 2) extend_pack_kernel(con
         else if (vbits == 4) extend_values<4>(p, jb, h, vb, smem);
         else extend_values<8>(p, jb, h, vb, smem);
     }
+    if (extend_once(p) && jb.t0 == 0) {  // every thread has read its rows (a barrier inside the packing)
+        const int4 *d = reinterpret_cast<const int4 *>(p.desc);
+        keep_rows(p, d[2 * jb.b], d[2 * jb.b + 1], jb.b, h, blockIdx.z, false, true, threadIdx.x, 256);
+    }
 }
 
-// The rows that stay fp16: CTA (b, head and side, slice) copies slot b's new sink rows and
-// its residual's new rows; the first CTA of a slot commits the lengths.  Runs after the
-// pack kernel, which reads the old residual rows that this overwrites.
+// Every slot's fp16 rows: after the pages, which read the old residual rows.
 constexpr int kTailSlices = 4;
 __global__ void __launch_bounds__(256) extend_tail_kernel(const ExtendParams p) {
-    const int b = blockIdx.x, h = blockIdx.y >> 1, side = blockIdx.y & 1;
     griddep_wait();
-    const int4 *d = reinterpret_cast<const int4 *>(p.desc);
-    const int4 x = d[2 * b];
-    if (!x.w) return;
-    const int4 y = d[2 * b + 1];
-    const int to_sink = y.y, pk = y.z, tot = x.z + x.w - to_sink, lo = pk ? 0 : x.z, hi = tot - pk;
-    const int64_t stride = side ? p.v_stride : p.k_stride;
-    const uint16_t *src = (side ? p.v_new : p.k_new) + h * 128;
-    const size_t u = (size_t)b * p.H_kv + h;
-    uint16_t *sink = side ? p.v_sink : p.k_sink, *res = side ? p.v_res : p.k_res;
-    const int n = to_sink + hi - lo, c = threadIdx.x & 15;
-    for (int i = blockIdx.z * 16 + (threadIdx.x >> 4); i < n; i += kTailSlices * 16) {
-        // chunk token and destination row; residual rows come from the chunk alone, since a
-        // slot that packs nothing keeps its old rows and one that packs takes all of them
-        const int r = i - to_sink + lo;
-        const int tok = i < to_sink ? i : to_sink + pk + r - x.z;
-        uint16_t *dst = i < to_sink ? sink + (u * p.S + x.x + i) * 128 : res + (u * p.R + r) * 128;
-        reinterpret_cast<uint4 *>(dst)[c] = __ldg(reinterpret_cast<const uint4 *>(src + (int64_t)(y.x + tok) * stride) + c);
-    }
-    if (blockIdx.y == 0 && blockIdx.z == 0 && threadIdx.x == 0)
-        reinterpret_cast<int4 *>(p.lens)[b] = make_int4(x.x + to_sink, x.y + pk, hi, 1);
+    extend_slot(p, blockIdx.x, blockIdx.y >> 1, blockIdx.y & 1, blockIdx.z, kTailSlices);
 }
 
 cudaError_t launch_extend(const ExtendParams &p, int kbits, int vbits, cudaStream_t st) {
+    const bool once = extend_once(p) && p.n_pack > 0;
     if (p.n_pack > 0) {
-        const dim3 grid((unsigned)p.n_pack, (unsigned)p.H_kv, (unsigned)(1 + p.G / 128));
+        const dim3 grid((unsigned)(p.n_pack + (once ? p.B : 0)), (unsigned)p.H_kv, (unsigned)(1 + p.G / 128));
         cudaError_t e = cudaErrorInvalidValue;
         if (p.G == 128) e = launch_dependent(extend_pack_kernel<16>, grid, 256, 0, st, p, kbits, vbits);
         else if (p.G == 256) e = launch_dependent(extend_pack_kernel<32>, grid, 256, 0, st, p, kbits, vbits);
-        if (e != cudaSuccess) return e;
+        if (e != cudaSuccess || once) return e;
     }
     return launch_dependent(extend_tail_kernel, dim3((unsigned)p.B, (unsigned)(2 * p.H_kv), kTailSlices), 256, 0, st, p);
 }
@@ -409,11 +429,20 @@ __global__ void __launch_bounds__(256) qk_kernel(const __grid_constant__ QkParam
     __shared__ float2 s_cs[D / 2];
     const int64_t i = blockIdx.x;
     const int tid = threadIdx.x, l = tid % L, c0 = 8 * l, half = p.rotary >> 1, hl = half / 8;
-    const int h0 = blockIdx.y * heads, h1 = min(p.H_q + p.H_kv, h0 + heads);  // the CTA's heads: queries, then keys
+    // the CTA's heads (queries, then keys) and the thread's first
+    const int h1 = min(p.H_q + p.H_kv, (int)(blockIdx.y + 1) * heads), first = blockIdx.y * heads + tid / L;
     // halves: the lane's partner is hl lanes off; interleaved: partners are neighbours
     const bool second = p.halves && l >= hl;
     const int off = !p.halves ? 0 : l < hl ? hl : l < 2 * hl ? -hl : 0;
     griddep_wait();
+    uint4 v[kQkRows];
+    auto load = [&](int h) {
+        const uint16_t *src = h >= p.H_q ? p.k + i * p.k_stride + (h - p.H_q) * D : p.q + i * p.q_stride + h * D;
+        return __ldcs(reinterpret_cast<const uint4 *>(src + c0));
+    };
+#pragma unroll
+    for (int r = 0; r < kQkRows; r++)
+        if (first + r * PER < h1) v[r] = load(first + r * PER);
     if (tid < half) {
         const uint64_t a = (uint64_t)(int64_t)p.pos[i] * p.turn[tid];
         float s, c;
@@ -421,83 +450,71 @@ __global__ void __launch_bounds__(256) qk_kernel(const __grid_constant__ QkParam
         s_cs[tid] = make_float2(c, s);
     }
     __syncthreads();
-#pragma unroll 1
-    for (int side = 0; side < 2; side++) {
-        const int lo = side ? max(h0 - p.H_q, 0) : h0, hi = side ? h1 - p.H_q : min(h1, p.H_q);  // heads of this side
-        if (lo >= hi) continue;
-        const uint16_t *src = (side ? p.k + i * p.k_stride : p.q + i * p.q_stride) + c0;
-        uint16_t *dst = (side ? p.k_out + i * p.H_kv * D : p.q_out + i * p.H_q * D) + c0;
-        const uint16_t *wt = side ? p.w_k : p.w_q;
-        uint4 v[kQkRows];
-        const int first = lo + tid / L;
+    // y = f (x a + partner b), f the norm's factor: the weights are folded into sine and cosine
+    float a[8], b[8];
+    int side = -1;
+    for (int h = first; __any_sync(0xffffffffu, h < h1); h += kQkRows * PER) {
 #pragma unroll
-        for (int r = 0; r < kQkRows; r++)
-            if (first + r * PER < hi) v[r] = __ldcs(reinterpret_cast<const uint4 *>(src + (first + r * PER) * D));
-        // y = f (x a + partner b): the weights are folded into sine and cosine
-        float a[8], b[8];
-        {
-            float w[8], wp[8];
-            if (wt) {
-                const uint4 u = __ldg(reinterpret_cast<const uint4 *>(wt + c0));
-                const uint4 o = __ldg(reinterpret_cast<const uint4 *>(wt + c0 + 8 * off));
-#pragma unroll
-                for (int e = 0; e < 4; e++) {
-                    const float2 f = unpack_half2((&u.x)[e]), g = unpack_half2((&o.x)[e]);
-                    w[2 * e] = f.x;
-                    w[2 * e + 1] = f.y;
-                    wp[2 * e] = p.halves ? g.x : f.y;
-                    wp[2 * e + 1] = p.halves ? g.y : f.x;
-                }
-            } else {
+        for (int r = 0; r < kQkRows; r++) {
+            const int hh = h + r * PER, key = hh >= p.H_q;
+            if (!__any_sync(0xffffffffu, hh < h1)) break;
+            const uint16_t *wt = key ? p.w_k : p.w_q;
+            if (key != side) {  // once for the queries, once for the keys
+                side = key;
+                float w[8], wp[8];
 #pragma unroll
                 for (int e = 0; e < 8; e++) w[e] = wp[e] = 1.f;
-            }
-            const bool turn = c0 < p.rotary && (p.rotate & (side ? 2 : 1));
-#pragma unroll
-            for (int e = 0; e < 8; e++) {
-                const int j = !p.halves ? (c0 + e) >> 1 : (second ? c0 - half : c0) + e;
-                const float2 cs = turn ? s_cs[j] : make_float2(1.f, 0.f);
-                const bool up = p.halves ? second : (e & 1);  // the pair's second channel
-                a[e] = w[e] * cs.x;
-                b[e] = up ? wp[e] * cs.y : -wp[e] * cs.y;
-            }
-        }
-        for (int h = first; __any_sync(0xffffffffu, h < hi); h += kQkRows * PER) {
-#pragma unroll
-            for (int r = 0; r < kQkRows; r++) {
-                const int hh = h + r * PER;
-                if (!__any_sync(0xffffffffu, hh < hi)) break;
-                const uint32_t *u = reinterpret_cast<const uint32_t *>(&v[r]);
-                float x[8], y[8];
-#pragma unroll
-                for (int e = 0; e < 4; e++) {
-                    const float2 f = unpack_half2(u[e]);
-                    x[2 * e] = f.x;
-                    x[2 * e + 1] = f.y;
-                }
-                float f = 1.f;
                 if (wt) {
-                    float s0 = 0.f, s1 = 0.f;
+                    const uint4 u = __ldg(reinterpret_cast<const uint4 *>(wt + c0));
+                    const uint4 o = __ldg(reinterpret_cast<const uint4 *>(wt + c0 + 8 * off));
 #pragma unroll
-                    for (int e = 0; e < 8; e += 2) {
-                        s0 += x[e] * x[e];
-                        s1 += x[e + 1] * x[e + 1];
+                    for (int e = 0; e < 4; e++) {
+                        const float2 f = unpack_half2((&u.x)[e]), g = unpack_half2((&o.x)[e]);
+                        w[2 * e] = f.x;
+                        w[2 * e + 1] = f.y;
+                        wp[2 * e] = p.halves ? g.x : f.y;
+                        wp[2 * e + 1] = p.halves ? g.y : f.x;
                     }
-                    s0 += s1;
-#pragma unroll
-                    for (int o = L / 2; o; o >>= 1) s0 += __shfl_xor_sync(0xffffffffu, s0, o);
-                    f = rsqrtf(s0 * (1.0f / D) + p.eps);
                 }
+                const bool turn = c0 < p.rotary && (p.rotate & (key ? 2 : 1));
 #pragma unroll
                 for (int e = 0; e < 8; e++) {
-                    const float o = p.halves ? __shfl_sync(0xffffffffu, x[e], (tid & 31) + off) : x[e ^ 1];
-                    y[e] = f * (x[e] * a[e] + o * b[e]);
+                    const int j = !p.halves ? (c0 + e) >> 1 : (second ? c0 - half : c0) + e;
+                    const float2 cs = turn ? s_cs[j] : make_float2(1.f, 0.f);
+                    const bool up = p.halves ? second : (e & 1);  // the pair's second channel
+                    a[e] = w[e] * cs.x;
+                    b[e] = up ? wp[e] * cs.y : -wp[e] * cs.y;
                 }
-                if (hh < hi)
-                    *reinterpret_cast<uint4 *>(dst + hh * D) = make_uint4(pack_half2(y[0], y[1]), pack_half2(y[2], y[3]),
-                                                                         pack_half2(y[4], y[5]), pack_half2(y[6], y[7]));
-                if (hh + kQkRows * PER < hi) v[r] = __ldcs(reinterpret_cast<const uint4 *>(src + (hh + kQkRows * PER) * D));
             }
+            const uint32_t *u = reinterpret_cast<const uint32_t *>(&v[r]);
+            float x[8], y[8];
+#pragma unroll
+            for (int e = 0; e < 4; e++) {
+                const float2 f = unpack_half2(u[e]);
+                x[2 * e] = f.x;
+                x[2 * e + 1] = f.y;
+            }
+            float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+            for (int e = 0; e < 8; e += 2) {
+                s0 += x[e] * x[e];
+                s1 += x[e + 1] * x[e + 1];
+            }
+            s0 += s1;
+#pragma unroll
+            for (int o = L / 2; o; o >>= 1) s0 += __shfl_xor_sync(0xffffffffu, s0, o);
+            const float f = wt ? rsqrtf(s0 * (1.0f / D) + p.eps) : 1.f;
+#pragma unroll
+            for (int e = 0; e < 8; e++) {
+                const float o = p.halves ? __shfl_sync(0xffffffffu, x[e], (tid & 31) + off) : x[e ^ 1];
+                y[e] = f * (x[e] * a[e] + o * b[e]);
+            }
+            if (hh < h1) {
+                uint16_t *dst = key ? p.k_out + (i * p.H_kv + hh - p.H_q) * D : p.q_out + (i * p.H_q + hh) * D;
+                *reinterpret_cast<uint4 *>(dst + c0) = make_uint4(pack_half2(y[0], y[1]), pack_half2(y[2], y[3]),
+                                                                  pack_half2(y[4], y[5]), pack_half2(y[6], y[7]));
+            }
+            if (hh + kQkRows * PER < h1) v[r] = load(hh + kQkRows * PER);
         }
     }
 }
@@ -854,11 +871,17 @@ int kvq_qk_norm_rope(const kvq_qk_config *c, const uint16_t *q, const uint16_t *
     p.rotate = c->rotary_dim ? c->rotate : 0;
     p.eps = c->eps;
     const long double base = c->rope_base > 0.f ? (long double)c->rope_base : 10000.0L;
-    // one power, then products: a call's host time is a fraction of that of a power per pair,
-    // and each product adds half a step of a long double (2^-64 or less) at most
+    // turn[j] = base^(-2j/n) / (2 pi) in 64-bit fixed point: one power, then integer products
+    // (a call's host time is a small part of that of a power per pair), each off by 2^-64 at most
     const long double step = c->rotary_dim ? powl(base, -2.0L / c->rotary_dim) : 0.0L;
-    long double turn = 0.159154943091895335768883763372514362L;  // 1 / (2 pi)
-    for (int j = 0; j < c->rotary_dim / 2; j++, turn *= step) p.turn[j] = (uint64_t)ldexpl(turn - floorl(turn), 64);
+    if (step < 1.0L) {
+        const uint64_t f = (uint64_t)ldexpl(step, 64);
+        uint64_t turn = 0x28be60db9391054aull;  // 2^64 / (2 pi)
+        for (int j = 0; j < c->rotary_dim / 2; j++, turn = (uint64_t)(((unsigned __int128)turn * f) >> 64)) p.turn[j] = turn;
+    } else {
+        long double turn = 0.159154943091895335768883763372514362L;
+        for (int j = 0; j < c->rotary_dim / 2; j++, turn *= step) p.turn[j] = (uint64_t)ldexpl(turn - floorl(turn), 64);
+    }
     return status_of(launch_qk(p, c->D, (cudaStream_t)stream));
 }
 
