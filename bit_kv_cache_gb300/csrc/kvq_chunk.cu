@@ -372,6 +372,7 @@ __device__ __forceinline__ void extend_slot(const ExtendParams &p, int b, int h,
 template <int TPW>
 __global__ void __launch_bounds__(256, TPW == 16 ? 4 : 2) extend_pack_kernel(const ExtendParams p, int kbits, int vbits) {
     __shared__ __align__(16) unsigned char smem[32 * 512 + 512];
+    __shared__ int s_first;  // the slot, if this is its first page
     const int h = blockIdx.y;
     griddep_wait();
     if (blockIdx.x >= p.n_pack) {
@@ -379,6 +380,7 @@ __global__ void __launch_bounds__(256, TPW == 16 ? 4 : 2) extend_pack_kernel(con
         return;
     }
     const PageJob jb = find_page(p, blockIdx.x);
+    if (threadIdx.x == 0) s_first = jb.t0 == 0 ? jb.b : -1;
     if (blockIdx.z == 0) {
         if (kbits == 2) extend_keys<2, TPW>(p, jb, h, smem);
         else if (kbits == 4) extend_keys<4, TPW>(p, jb, h, smem);
@@ -389,9 +391,9 @@ __global__ void __launch_bounds__(256, TPW == 16 ? 4 : 2) extend_pack_kernel(con
         else if (vbits == 4) extend_values<4>(p, jb, h, vb, smem);
         else extend_values<8>(p, jb, h, vb, smem);
     }
-    if (extend_once(p) && jb.t0 == 0) {  // every thread has read its rows (a barrier inside the packing)
-        const int4 *d = reinterpret_cast<const int4 *>(p.desc);
-        keep_rows(p, d[2 * jb.b], d[2 * jb.b + 1], jb.b, h, blockIdx.z, false, true, threadIdx.x, 256);
+    if (TPW == 16 && extend_once(p) && s_first >= 0) {  // every thread has read its rows (a barrier inside the packing)
+        const int4 *d = reinterpret_cast<const int4 *>(p.desc) + 2 * s_first;
+        keep_rows(p, d[0], d[1], s_first, h, blockIdx.z, false, true, threadIdx.x, 256);
     }
 }
 
@@ -415,11 +417,14 @@ cudaError_t launch_extend(const ExtendParams &p, int kbits, int vbits, cudaStrea
 }
 
 // ------------------------------------------------------------------------------
-// Norm and rotation of new queries and keys.  D / 8 lanes hold a head's row, 16 bytes each,
-// a CTA a token's heads (or a part of them); a thread's channels are the same in all its
-// rows, so that their weights, sines and cosines are loaded once.  An angle
-// pos * base^(-2j/n) is reduced in 64-bit fixed point: pos * turn[j] mod 2^64 is the exact
-// fraction of a turn, whose upper 32 bits go to sincospif.
+// Norm and rotation of new queries and keys.  D / 8 lanes hold a head's row, four channel
+// pairs each (both channels of a pair in one thread), a CTA a token's heads or a part of
+// them; a thread's channels are the same in all its rows, so that their weights, sines and
+// cosines are formed once.  An angle pos * base^(-2j/n) is reduced in 64-bit fixed point:
+// pos * turn[j] mod 2^64 is the exact fraction of a turn, whose upper 32 bits go to
+// sincospif.  Bound by instructions, not by memory, until fp32 pairs, folded weights and
+// shuffle-free pairs brought them down (8191 tokens of 32 + 8 heads: 63 us with one row per
+// warp and a shuffle per channel).
 // ------------------------------------------------------------------------------
 constexpr int kQkRows = 3;  // rows of a thread in flight
 
@@ -428,21 +433,23 @@ __global__ void __launch_bounds__(256) qk_kernel(const __grid_constant__ QkParam
     constexpr int L = D / 8, PER = 256 / L;  // lanes per row, rows per pass of the CTA
     __shared__ float2 s_cs[D / 2];
     const int64_t i = blockIdx.x;
-    const int tid = threadIdx.x, l = tid % L, c0 = 8 * l, half = p.rotary >> 1, hl = half / 8;
+    const int tid = threadIdx.x, l = tid % L, half = p.rotary >> 1;
     // the CTA's heads (queries, then keys) and the thread's first
     const int h1 = min(p.H_q + p.H_kv, (int)(blockIdx.y + 1) * heads), first = blockIdx.y * heads + tid / L;
-    // halves: the lane's partner is hl lanes off; interleaved: partners are neighbours
-    const bool second = p.halves && l >= hl;
-    const int off = !p.halves ? 0 : l < hl ? hl : l < 2 * hl ? -hl : 0;
+    // the thread's channels: two pieces of four.  Halves: a piece of the first half and its
+    // partners; interleaved, and behind the rotary channels: neighbours
+    const bool split = p.halves && 4 * l < half;
+    const int c0 = split ? 4 * l : p.halves ? p.rotary + 2 * (4 * l - half) : 8 * l, c1 = split ? c0 + half : c0 + 4;
     griddep_wait();
-    uint4 v[kQkRows];
-    auto load = [&](int h) {
+    uint2 v[kQkRows][2];
+    auto load = [&](uint2 (&r)[2], int h) {
         const uint16_t *src = h >= p.H_q ? p.k + i * p.k_stride + (h - p.H_q) * D : p.q + i * p.q_stride + h * D;
-        return __ldcs(reinterpret_cast<const uint4 *>(src + c0));
+        r[0] = __ldcs(reinterpret_cast<const uint2 *>(src + c0));
+        r[1] = __ldcs(reinterpret_cast<const uint2 *>(src + c1));
     };
 #pragma unroll
     for (int r = 0; r < kQkRows; r++)
-        if (first + r * PER < h1) v[r] = load(first + r * PER);
+        if (first + r * PER < h1) load(v[r], first + r * PER);
     if (tid < half) {
         const uint64_t a = (uint64_t)(int64_t)p.pos[i] * p.turn[tid];
         float s, c;
@@ -450,8 +457,20 @@ __global__ void __launch_bounds__(256) qk_kernel(const __grid_constant__ QkParam
         s_cs[tid] = make_float2(c, s);
     }
     __syncthreads();
-    // y = f (x a + partner b), f the norm's factor: the weights are folded into sine and cosine
-    float a[8], b[8];
+    // first and second channels of the four pairs of eight halves
+    auto pairs = [&](const uint2 (&r)[2], float (&x)[4], float (&y)[4]) {
+        const float2 f0 = unpack_half2(r[0].x), f1 = unpack_half2(r[0].y), f2 = unpack_half2(r[1].x), f3 = unpack_half2(r[1].y);
+        if (p.halves) {
+            x[0] = f0.x, x[1] = f0.y, x[2] = f1.x, x[3] = f1.y;
+            y[0] = f2.x, y[1] = f2.y, y[2] = f3.x, y[3] = f3.y;
+        } else {
+            x[0] = f0.x, x[1] = f1.x, x[2] = f2.x, x[3] = f3.x;
+            y[0] = f0.y, y[1] = f1.y, y[2] = f2.y, y[3] = f3.y;
+        }
+    };
+    // (x, y) -> f (x xx + y xy, x yx + y yy), f the norm's factor: the weights are folded into
+    // sine and cosine
+    uint64_t xx[2], xy[2], yx[2], yy[2];
     int side = -1;
     for (int h = first; __any_sync(0xffffffffu, h < h1); h += kQkRows * PER) {
 #pragma unroll
@@ -461,60 +480,51 @@ __global__ void __launch_bounds__(256) qk_kernel(const __grid_constant__ QkParam
             const uint16_t *wt = key ? p.w_k : p.w_q;
             if (key != side) {  // once for the queries, once for the keys
                 side = key;
-                float w[8], wp[8];
-#pragma unroll
-                for (int e = 0; e < 8; e++) w[e] = wp[e] = 1.f;
+                float w0[4] = {1.f, 1.f, 1.f, 1.f}, w1[4] = {1.f, 1.f, 1.f, 1.f};
                 if (wt) {
-                    const uint4 u = __ldg(reinterpret_cast<const uint4 *>(wt + c0));
-                    const uint4 o = __ldg(reinterpret_cast<const uint4 *>(wt + c0 + 8 * off));
-#pragma unroll
-                    for (int e = 0; e < 4; e++) {
-                        const float2 f = unpack_half2((&u.x)[e]), g = unpack_half2((&o.x)[e]);
-                        w[2 * e] = f.x;
-                        w[2 * e + 1] = f.y;
-                        wp[2 * e] = p.halves ? g.x : f.y;
-                        wp[2 * e + 1] = p.halves ? g.y : f.x;
-                    }
+                    const uint2 u[2] = {__ldg(reinterpret_cast<const uint2 *>(wt + c0)), __ldg(reinterpret_cast<const uint2 *>(wt + c1))};
+                    pairs(u, w0, w1);
                 }
-                const bool turn = c0 < p.rotary && (p.rotate & (key ? 2 : 1));
+                const bool turn = (p.halves ? split : c0 < p.rotary) && (p.rotate & (key ? 2 : 1));
 #pragma unroll
-                for (int e = 0; e < 8; e++) {
-                    const int j = !p.halves ? (c0 + e) >> 1 : (second ? c0 - half : c0) + e;
-                    const float2 cs = turn ? s_cs[j] : make_float2(1.f, 0.f);
-                    const bool up = p.halves ? second : (e & 1);  // the pair's second channel
-                    a[e] = w[e] * cs.x;
-                    b[e] = up ? wp[e] * cs.y : -wp[e] * cs.y;
+                for (int e = 0; e < 2; e++) {
+                    const int j = (p.halves ? c0 : c0 >> 1) + 2 * e;
+                    const float2 c = turn ? s_cs[j] : make_float2(1.f, 0.f), d = turn ? s_cs[j + 1] : make_float2(1.f, 0.f);
+                    xx[e] = pk2(w0[2 * e] * c.x, w0[2 * e + 1] * d.x);
+                    xy[e] = pk2(-w1[2 * e] * c.y, -w1[2 * e + 1] * d.y);
+                    yx[e] = pk2(w0[2 * e] * c.y, w0[2 * e + 1] * d.y);
+                    yy[e] = pk2(w1[2 * e] * c.x, w1[2 * e + 1] * d.x);
                 }
             }
-            const uint32_t *u = reinterpret_cast<const uint32_t *>(&v[r]);
-            float x[8], y[8];
+            float x[4], y[4];
+            pairs(v[r], x, y);
+            const uint64_t X[2] = {pk2(x[0], x[1]), pk2(x[2], x[3])}, Y[2] = {pk2(y[0], y[1]), pk2(y[2], y[3])};
+            const float2 sq = up2(fma_x2(X[0], X[0], fma_x2(X[1], X[1], fma_x2(Y[0], Y[0], mul_x2(Y[1], Y[1])))));
+            float ss = sq.x + sq.y;
 #pragma unroll
-            for (int e = 0; e < 4; e++) {
-                const float2 f = unpack_half2(u[e]);
-                x[2 * e] = f.x;
-                x[2 * e + 1] = f.y;
-            }
-            float s0 = 0.f, s1 = 0.f;
+            for (int o = L / 2; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+            const float f = wt ? rsqrtf(ss * (1.0f / D) + p.eps) : 1.f;
+            const uint64_t f2 = pk2(f, f);
 #pragma unroll
-            for (int e = 0; e < 8; e += 2) {
-                s0 += x[e] * x[e];
-                s1 += x[e + 1] * x[e + 1];
-            }
-            s0 += s1;
-#pragma unroll
-            for (int o = L / 2; o; o >>= 1) s0 += __shfl_xor_sync(0xffffffffu, s0, o);
-            const float f = wt ? rsqrtf(s0 * (1.0f / D) + p.eps) : 1.f;
-#pragma unroll
-            for (int e = 0; e < 8; e++) {
-                const float o = p.halves ? __shfl_sync(0xffffffffu, x[e], (tid & 31) + off) : x[e ^ 1];
-                y[e] = f * (x[e] * a[e] + o * b[e]);
+            for (int e = 0; e < 2; e++) {
+                const float2 a = up2(mul_x2(f2, fma_x2(X[e], xx[e], mul_x2(Y[e], xy[e]))));
+                const float2 b = up2(mul_x2(f2, fma_x2(X[e], yx[e], mul_x2(Y[e], yy[e]))));
+                x[2 * e] = a.x, x[2 * e + 1] = a.y, y[2 * e] = b.x, y[2 * e + 1] = b.y;
             }
             if (hh < h1) {
                 uint16_t *dst = key ? p.k_out + (i * p.H_kv + hh - p.H_q) * D : p.q_out + (i * p.H_q + hh) * D;
-                *reinterpret_cast<uint4 *>(dst + c0) = make_uint4(pack_half2(y[0], y[1]), pack_half2(y[2], y[3]),
-                                                                  pack_half2(y[4], y[5]), pack_half2(y[6], y[7]));
+                uint2 o[2];
+                if (p.halves) {
+                    o[0] = make_uint2(pack_half2(x[0], x[1]), pack_half2(x[2], x[3]));
+                    o[1] = make_uint2(pack_half2(y[0], y[1]), pack_half2(y[2], y[3]));
+                } else {
+                    o[0] = make_uint2(pack_half2(x[0], y[0]), pack_half2(x[1], y[1]));
+                    o[1] = make_uint2(pack_half2(x[2], y[2]), pack_half2(x[3], y[3]));
+                }
+                *reinterpret_cast<uint2 *>(dst + c0) = o[0];
+                *reinterpret_cast<uint2 *>(dst + c1) = o[1];
             }
-            if (hh + kQkRows * PER < h1) v[r] = load(hh + kQkRows * PER);
+            if (hh + kQkRows * PER < h1) load(v[r], hh + kQkRows * PER);
         }
     }
 }

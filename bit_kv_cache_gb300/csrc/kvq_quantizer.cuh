@@ -93,6 +93,12 @@ __device__ __forceinline__ uint64_t add_x2(uint64_t a, uint64_t b) {
     return d;
 }
 
+__device__ __forceinline__ uint64_t fma_x2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+
 // qbits for two elements at once: h is a half2 of two fp16 values whose groups have
 // (min, rcp(scale)) = mn2, inv2.  Returns the two clamped magic-biased codes; em
 // tracks the largest distance to a rounding tie.
