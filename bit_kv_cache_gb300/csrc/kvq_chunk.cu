@@ -418,28 +418,32 @@ cudaError_t launch_extend(const ExtendParams &p, int kbits, int vbits, cudaStrea
 
 // ------------------------------------------------------------------------------
 // Norm and rotation of new queries and keys.  D / 8 lanes hold a head's row, four channel
-// pairs each (both channels of a pair in one thread), a CTA a token's heads or a part of
+// pairs each (both channels of a pair in one thread), a warp a token's heads or a part of
 // them; a thread's channels are the same in all its rows, so that their weights, sines and
 // cosines are formed once.  An angle pos * base^(-2j/n) is reduced in 64-bit fixed point:
 // pos * turn[j] mod 2^64 is the exact fraction of a turn, whose upper 32 bits go to
-// sincospif.  Bound by instructions, not by memory, until fp32 pairs, folded weights and
-// shuffle-free pairs brought them down (8191 tokens of 32 + 8 heads: 63 us with one row per
-// warp and a shuffle per channel).
+// sincospif.  8191 tokens of 32 + 8 heads of 128 channels, 168 MB, take 30 us (5.6 TB/s);
+// bound by instructions before: 63 us with a CTA per token, a row per warp and a shuffle per
+// channel, 45 us with both channels of a pair in one thread and fp32 pairs, 41 us with the
+// weights folded into sine and cosine, 30 us with a warp per token, which forms them once
+// for 20 passes of rows.
 // ------------------------------------------------------------------------------
-constexpr int kQkRows = 3;  // rows of a thread in flight
+constexpr int kQkRows = 4;  // rows of a thread in flight
 
-template <int D>
-__global__ void __launch_bounds__(256) qk_kernel(const __grid_constant__ QkParams p, int heads) {
-    constexpr int L = D / 8, PER = 256 / L;  // lanes per row, rows per pass of the CTA
-    __shared__ float2 s_cs[D / 2];
-    const int64_t i = blockIdx.x;
-    const int tid = threadIdx.x, l = tid % L, half = p.rotary >> 1;
-    // the CTA's heads (queries, then keys) and the thread's first
-    const int h1 = min(p.H_q + p.H_kv, (int)(blockIdx.y + 1) * heads), first = blockIdx.y * heads + tid / L;
+template <int D, bool HALVES>
+__global__ void __launch_bounds__(256) qk_kernel(const __grid_constant__ QkParams p, int heads, int parts) {
+    constexpr int L = D / 8, PER = 32 / L;  // lanes per row, rows per pass of the warp
+    __shared__ float2 s_all[8][D / 2];
+    const int lane = threadIdx.x & 31, l = lane % L, half = p.rotary >> 1;
+    float2 *s_cs = s_all[threadIdx.x >> 5];
+    const int64_t item = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5), i = item / parts;
+    if (i >= p.n) return;
+    // the warp's heads (queries, then keys) and the thread's first
+    const int h0 = (int)(item - i * parts) * heads, h1 = min(p.H_q + p.H_kv, h0 + heads), first = h0 + lane / L;
     // the thread's channels: two pieces of four.  Halves: a piece of the first half and its
     // partners; interleaved, and behind the rotary channels: neighbours
-    const bool split = p.halves && 4 * l < half;
-    const int c0 = split ? 4 * l : p.halves ? p.rotary + 2 * (4 * l - half) : 8 * l, c1 = split ? c0 + half : c0 + 4;
+    const bool split = HALVES && 4 * l < half;
+    const int c0 = split ? 4 * l : HALVES ? p.rotary + 2 * (4 * l - half) : 8 * l, c1 = split ? c0 + half : c0 + 4;
     griddep_wait();
     uint2 v[kQkRows][2];
     auto load = [&](uint2 (&r)[2], int h) {
@@ -450,17 +454,18 @@ __global__ void __launch_bounds__(256) qk_kernel(const __grid_constant__ QkParam
 #pragma unroll
     for (int r = 0; r < kQkRows; r++)
         if (first + r * PER < h1) load(v[r], first + r * PER);
-    if (tid < half) {
-        const uint64_t a = (uint64_t)(int64_t)p.pos[i] * p.turn[tid];
+    const int64_t pos = p.pos[i];
+    for (int j = lane; j < half; j += 32) {
+        const uint64_t a = (uint64_t)pos * p.turn[j];
         float s, c;
         sincospif((float)(int32_t)(a >> 32) * 0x1p-31f, &s, &c);
-        s_cs[tid] = make_float2(c, s);
+        s_cs[j] = make_float2(c, s);
     }
-    __syncthreads();
+    __syncwarp();
     // first and second channels of the four pairs of eight halves
     auto pairs = [&](const uint2 (&r)[2], float (&x)[4], float (&y)[4]) {
         const float2 f0 = unpack_half2(r[0].x), f1 = unpack_half2(r[0].y), f2 = unpack_half2(r[1].x), f3 = unpack_half2(r[1].y);
-        if (p.halves) {
+        if (HALVES) {
             x[0] = f0.x, x[1] = f0.y, x[2] = f1.x, x[3] = f1.y;
             y[0] = f2.x, y[1] = f2.y, y[2] = f3.x, y[3] = f3.y;
         } else {
@@ -485,10 +490,10 @@ __global__ void __launch_bounds__(256) qk_kernel(const __grid_constant__ QkParam
                     const uint2 u[2] = {__ldg(reinterpret_cast<const uint2 *>(wt + c0)), __ldg(reinterpret_cast<const uint2 *>(wt + c1))};
                     pairs(u, w0, w1);
                 }
-                const bool turn = (p.halves ? split : c0 < p.rotary) && (p.rotate & (key ? 2 : 1));
+                const bool turn = (HALVES ? split : c0 < p.rotary) && (p.rotate & (key ? 2 : 1));
 #pragma unroll
                 for (int e = 0; e < 2; e++) {
-                    const int j = (p.halves ? c0 : c0 >> 1) + 2 * e;
+                    const int j = (HALVES ? c0 : c0 >> 1) + 2 * e;
                     const float2 c = turn ? s_cs[j] : make_float2(1.f, 0.f), d = turn ? s_cs[j + 1] : make_float2(1.f, 0.f);
                     xx[e] = pk2(w0[2 * e] * c.x, w0[2 * e + 1] * d.x);
                     xy[e] = pk2(-w1[2 * e] * c.y, -w1[2 * e + 1] * d.y);
@@ -514,7 +519,7 @@ __global__ void __launch_bounds__(256) qk_kernel(const __grid_constant__ QkParam
             if (hh < h1) {
                 uint16_t *dst = key ? p.k_out + (i * p.H_kv + hh - p.H_q) * D : p.q_out + (i * p.H_q + hh) * D;
                 uint2 o[2];
-                if (p.halves) {
+                if (HALVES) {
                     o[0] = make_uint2(pack_half2(x[0], x[1]), pack_half2(x[2], x[3]));
                     o[1] = make_uint2(pack_half2(y[0], y[1]), pack_half2(y[2], y[3]));
                 } else {
@@ -530,15 +535,17 @@ __global__ void __launch_bounds__(256) qk_kernel(const __grid_constant__ QkParam
 }
 
 cudaError_t launch_qk(const QkParams &p, int D, cudaStream_t st) {
-    const int H = p.H_q + p.H_kv, pass = 256 / (D / 8);
-    // few tokens: their heads go to several CTAs, one pass of rows at least each
-    int y = 1;
-    while (p.n * y < 2 * num_sms() && (H + y - 1) / y > pass) y++;
-    const int heads = (H + y - 1) / y;
-    const dim3 grid((unsigned)p.n, (unsigned)((H + heads - 1) / heads));
-    if (D == 64) return launch_dependent(qk_kernel<64>, grid, 256, 0, st, p, heads);
-    if (D == 128) return launch_dependent(qk_kernel<128>, grid, 256, 0, st, p, heads);
-    return launch_dependent(qk_kernel<256>, grid, 256, 0, st, p, heads);
+    const int H = p.H_q + p.H_kv, pass = 32 / (D / 8);
+    // a warp per token; of few tokens the heads go to several warps, one pass of rows at least each
+    int parts = 1;
+    while (p.n * parts < 16 * num_sms() && (H + parts - 1) / parts > pass) parts++;
+    const int heads = (H + parts - 1) / parts;
+    parts = (H + heads - 1) / heads;
+    const dim3 grid((unsigned)((p.n * parts + 7) / 8));
+    auto go = [&](auto kernel) { return launch_dependent(kernel, grid, 256, 0, st, p, heads, parts); };
+    if (D == 64) return p.halves ? go(qk_kernel<64, true>) : go(qk_kernel<64, false>);
+    if (D == 128) return p.halves ? go(qk_kernel<128, true>) : go(qk_kernel<128, false>);
+    return p.halves ? go(qk_kernel<256, true>) : go(qk_kernel<256, false>);
 }
 
 }  // namespace kvq
