@@ -218,8 +218,9 @@ def qk_norm_rope(q, k=None, w_q=None, w_k=None, pos=None, eps=1e-6, rope_base=10
 class KVQChunk:
     """The buffers of a plan (kvq_chunk) and of the attention that reads it: slot maps
     ``cu`` [B + 1], ``slot`` and ``pos`` [max_tokens] (int32, on the device).  Made by
-    KVQPagedCache.new_chunk.  Every cache of the same configuration and lengths may use it;
-    two attention calls that may overlap need a chunk each."""
+    KVQPagedCache.new_chunk.  Every cache of the same configuration and lengths may attend
+    with it; the cache that it was planned on last extends with it.  Two attention calls that
+    may overlap need a chunk each."""
 
     def __init__(self, cfg, max_tokens, device):
         import torch
@@ -231,6 +232,7 @@ class KVQChunk:
         self.host = (ctypes.c_int32 * (8 * cfg.B))()
         self.ws = torch.empty(lib.kvq_paged_chunk_workspace_bytes(ctypes.byref(cfg)), dtype=torch.uint8, device=device)
         self.B = cfg.B
+        self.cache = None  # the cache of the last plan
         pad = torch.zeros(4, **i32) if max_tokens == 0 else None  # an empty tensor has no address
         self._pad = pad
         self.ws_ptr, self.ws_bytes = self.ws.data_ptr(), self.ws.numel()
@@ -590,6 +592,7 @@ class KVQPagedCache:
         _check(lib.kvq_paged_plan(*self._refs, np_, None if pages is None else pages.data_ptr(),
                                   0 if pages is None else pages.numel(), chunk.ref, _stream_of(self._dev.index)),
                "kvq_paged_plan")
+        chunk.cache = self
         return chunk
 
     def _plan_pages(self, n_new):
@@ -639,8 +642,11 @@ class KVQPagedCache:
         return out
 
     def extend(self, chunk, k_new, v_new):
-        """The planned chunk's tokens enter the cache (kvq_paged_extend)."""
+        """The planned chunk's tokens enter the cache (kvq_paged_extend).  The chunk must have
+        been planned on this cache, which maps the pages, unless the caller maps them."""
         cfg, dev = self.cfg, self._dev
+        if chunk.cache is not self and not self.caller_pages:
+            raise KvqError(-1, "the chunk was planned on another cache")
         kp, ks = _rows(k_new, cfg.H_kv, cfg.D, chunk.n_tokens, dev, "k_new")
         vp, vs = _rows(v_new, cfg.H_kv, cfg.D, chunk.n_tokens, dev, "v_new")
         _check(lib.kvq_paged_extend(*self._refs, chunk.ref, kp, ks, vp, vs, _stream_of(dev.index)), "kvq_paged_extend")

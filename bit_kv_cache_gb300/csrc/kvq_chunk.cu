@@ -725,6 +725,12 @@ int kvq_paged_chunk_attn(const kvq_config *c, const kvq_paged *pc, const kvq_chu
     if (!rows_ok(q, q_stride, c->H_q, c->D) || !rows_ok(kn, k_stride, c->H_kv, c->D) ||
         !rows_ok(vn, v_stride, c->H_kv, c->D) || !out || !aligned16(out))
         return KVQ_ERR_INVALID_ARG;
+    // rows are written while others are still read
+    const size_t no = (size_t)ch->n_tokens * c->H_q * c->D * 2;
+    auto span = [&](int64_t stride, int64_t heads) { return ((size_t)(ch->n_tokens - 1) * stride + heads * c->D) * 2; };
+    if (overlap(out, no, q, span(q_stride, c->H_q)) || overlap(out, no, kn, span(k_stride, c->H_kv)) ||
+        overlap(out, no, vn, span(v_stride, c->H_kv)))
+        return KVQ_ERR_INVALID_ARG;
     const ChunkWs wl = chunk_ws();
     if (!ws || !aligned16(ws) || ws_bytes < wl.total) return KVQ_ERR_WORKSPACE;
     ChunkAttnParams p;

@@ -783,8 +783,15 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attn_kernel(const __grid_co
 cudaError_t launch_chunk_combine(const ChunkAttnParams &p, cudaStream_t st);
 
 cudaError_t launch_chunk_attn(const ChunkAttnParams &p, cudaStream_t st) {
-    cudaError_t e = cudaFuncSetAttribute(chunk_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+    static bool ready[64];  // per device
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64 || !ready[dev]) {
+        e = cudaFuncSetAttribute(chunk_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+        if (e != cudaSuccess) return e;
+        if (dev >= 0 && dev < 64) ready[dev] = true;
+    }
     if ((e = launch_dependent(chunk_attn_kernel, dim3((unsigned)p.C), kThreads, kSmemBytes, st, p)) != cudaSuccess) return e;
     return launch_chunk_combine(p, st);
 }

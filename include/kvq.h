@@ -471,6 +471,8 @@ typedef struct {
  * are written from it, slot after slot in order; if it is NULL the caller maps them.
  * Host data is read before the call returns.  KVQ_ERR_CAPACITY if the tokens exceed
  * max_tokens, a slot exceeds max_T, or new_pages is too short; nothing is enqueued then.
+ * A plan may serve other caches of the same configuration and lengths if their page tables
+ * map the pages too.
  * KVQ_ERR_UNSUPPORTED while `stream` is capturing (a replay would not advance the host
  * lengths). */
 int kvq_paged_plan(const kvq_config *cfg, kvq_paged *pc, const int32_t *n_new, const int32_t *new_pages,
@@ -484,9 +486,10 @@ size_t kvq_paged_chunk_workspace_bytes(const kvq_config *cfg);
  *   out[i][h] = softmax_t( q[i][h] . K_t / sqrt(D) ) . V_t
  * over the slot's cached tokens (sink, packed pages, residual) and its new tokens 0 .. j.
  * q: device fp16 rows of H_q heads; k_new, v_new: rows of H_kv heads; out: device fp16
- * [n_tokens][H_q][D], contiguous.  Rows of the tensors behind n_tokens are neither read
- * nor written.  The cache is not changed.  Operands are fp16 (dequantized keys and values
+ * [n_tokens][H_q][D], contiguous, overlapping none of the inputs.  Rows of the tensors
+ * behind n_tokens are neither read nor written.  The cache is not changed.  Operands are fp16 (dequantized keys and values
  * and softmax weights are rounded to it once), sums and softmax statistics fp32.
+ * Infinite and NaN values reach the rows that see them and no others.
  * KVQ_ERR_INVALID_ARG if the cache's lengths are not those of the plan. */
 int kvq_paged_chunk_attn(const kvq_config *cfg, const kvq_paged *pc, const kvq_chunk *chunk, const uint16_t *q,
                          int64_t q_stride, const uint16_t *k_new, int64_t k_stride, const uint16_t *v_new,
@@ -519,8 +522,8 @@ typedef struct {
 } kvq_qk_config;
 
 /* y = x / sqrt(mean(x^2) + eps) * w over each head's D channels (skipped where the weight
- * pointer is NULL), then the rotation by pos[i], in fp32 with one rounding to fp16; angles
- * are exact to 2^-31 turns at any position.  q, k: device fp16 rows (strides above); w_q,
+ * pointer is NULL), then the rotation by pos[i], in fp32 with one rounding to fp16; the
+ * angles are reduced exactly (64-bit fixed point) at any position before the fp32 sine and cosine.  q, k: device fp16 rows (strides above); w_q,
  * w_k: device fp16 [D] or NULL; pos: device int32 [n]; q_out, k_out: device fp16
  * [n][H][D], contiguous.  An output may be its own input if that is contiguous; any other
  * overlap of an output with an input or the other output is KVQ_ERR_INVALID_ARG. */

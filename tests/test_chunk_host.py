@@ -111,6 +111,8 @@ def test_attention_and_extend_refusals(kvq):
             assert call(**kw) == INVALID, kw
     for kw in (dict(q=None), dict(q=0x600002), dict(qs=H_kv * D), dict(out=None), dict(out=0x900004)):
         assert f.attn(**kw) == INVALID, kw
+    for out in (0x600000, 0x600000 + H_q * D * 2 * 6, 0x700000 - 16, 0x800000 + H_kv * D * 2 * 7 - 16):
+        assert f.attn(out=out) == INVALID  # seven rows overlap an input
     assert f.attn(ws=None) == WORKSPACE and f.attn(wsb=64) == WORKSPACE and f.attn(ws=0xA00004) == WORKSPACE
     state = list(f.lens)
     # a plan for other lengths, other counts, another residual size

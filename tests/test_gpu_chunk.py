@@ -316,6 +316,79 @@ def test_plan_goes_stale():
     assert list(c.lens_host) == state
 
 
+def test_plan_of_another_cache():
+    """A plan's slot maps serve a cache of the same lengths; its pages are not that cache's."""
+    import bit_kv_cache_gb300 as kvq
+    a, b = (make_cache(np.random.default_rng(s), [100, 0]) for s in (1, 2))
+    q, k, v = chunk_inputs(np.random.default_rng(3), a, 50)
+    ch = a.plan([40, 10])
+    for c in (a, b):
+        attn_check(c, [40, 10], q, k, v, c.chunk_attn(ch, q, k, v))
+    with pytest.raises(kvq.KvqError):
+        b.extend(ch, k, v)
+    assert b.lengths(0)["n_res"] == 100
+    a.extend(ch, k, v)
+    b.extend(b.plan([40, 10], ch), k, v)
+    assert b.read_status() == 0 and list(a.lens_host) == list(b.lens_host)
+
+
+def test_many_slots():
+    """200 slots of many lengths: units far smaller than a range, empty slots between them."""
+    rng = np.random.default_rng(13)
+    lens = [int(x) for x in rng.integers(0, 500, 200)]
+    new = [int(x) for x in rng.integers(0, 4, 200)]
+    lens[7], new[9], new[199], new[100] = 0, 0, 0, 90
+    c = make_cache(rng, lens, H_q=4, H_kv=1, max_T=1024, spare=16)
+    n = sum(new)
+    q, k, v = chunk_inputs(rng, c, n)
+    ch = c.plan(new)
+    attn_check(c, new, q, k, v, c.chunk_attn(ch, q, k, v))
+    c.extend(ch, k, v)
+    assert [sum(c.lens_host[4 * b: 4 * b + 3]) for b in range(200)] == [x + y for x, y in zip(lens, new)]
+    assert c.read_status() == 0
+
+
+@pytest.mark.parametrize("rows", [1, 8, 9, 16, 17, 32, 33, 63, 64, 65])
+def test_row_counts(rows):
+    """Every form of a unit (copies of its rows, one tile, two), cut into ranges and whole."""
+    rng = np.random.default_rng(rows)
+    c = make_cache(rng, [3000, 120], H_q=4, H_kv=1)
+    new = [rows, rows]
+    q, k, v = chunk_inputs(rng, c, 2 * rows)
+    attn_check(c, new, q, k, v, c.chunk_attn(c.plan(new), q, k, v))
+
+
+def test_out_may_not_overlap():
+    import bit_kv_cache_gb300 as kvq
+    rng = np.random.default_rng(14)
+    c = make_cache(rng, [100])
+    q, k, v = (x.contiguous() for x in chunk_inputs(rng, c, 4))
+    ch = c.plan([4])
+    big = torch.cat([q, q])
+    for x, out in ((q, q), (big[:4], big[3:7])):
+        with pytest.raises(kvq.KvqError) as e:
+            c.chunk_attn(ch, x, k, v, out=out)
+        assert e.value.code == -1
+
+
+def test_two_streams():
+    """Two caches on two streams at once, with a chunk each."""
+    rng = np.random.default_rng(15)
+    cs = [make_cache(np.random.default_rng(i), [2000, 40], max_T=4096) for i in range(2)]
+    io = [chunk_inputs(rng, cs[0], 60) for _ in range(2)]
+    chunks = [c.plan([50, 10]) for c in cs]
+    outs = [torch.zeros(60, 8, 128, dtype=torch.float16, device=DEV) for _ in range(2)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(4):
+        for i in range(2):
+            with torch.cuda.stream(streams[i]):
+                cs[i].chunk_attn(chunks[i], *io[i], out=outs[i])
+    torch.cuda.synchronize()
+    for i in range(2):
+        attn_check(cs[i], [50, 10], *io[i], outs[i])
+
+
 def test_plan_and_extend_refuse_capture():
     import bit_kv_cache_gb300 as kvq
     rng = np.random.default_rng(5)
