@@ -129,8 +129,16 @@ cudaError_t launch_plan(const PlanParams &p, cudaStream_t st) {
 struct PageJob {
     ChunkSlot s;
     int b;
-    int64_t page;          // physical page
+    int entry;             // of the page table; read early, checked and used by page() at the end
     int t0;                // first stream token
+    __device__ __forceinline__ int64_t page(const ExtendParams &p, int h) const {
+        int e = entry;
+        if (e < 0 || e >= p.n_pages) {
+            if (threadIdx.x == 0) report(p.status, KVQ_DEV_BAD_STATE);
+            e = 0;
+        }
+        return (int64_t)e * p.H_kv + h;
+    }
 };
 
 // The slot of page i of the call: the number of slots whose pages all come before it.
@@ -153,11 +161,7 @@ __device__ __forceinline__ PageJob find_page(const ExtendParams &p, int i) {
     j.b = b;
     const int k = i - y.w;
     j.t0 = k * p.G;
-    j.page = p.ptab[(size_t)b * p.ptab_stride + x.y / p.G + k];
-    if (j.page < 0 || j.page >= p.n_pages) {
-        if (threadIdx.x == 0) report(p.status, KVQ_DEV_BAD_STATE);
-        j.page = 0;
-    }
+    j.entry = p.ptab[(size_t)b * p.ptab_stride + x.y / p.G + k];
     return j;
 }
 
@@ -195,7 +199,7 @@ __device__ __forceinline__ void extend_keys(const ExtendParams &p, const PageJob
     reinterpret_cast<uint2 *>(&s_hi[w][0])[lane] =
         make_uint2(*reinterpret_cast<uint32_t *>(&hi0), *reinterpret_cast<uint32_t *>(&hi1));
     __syncthreads();
-    const int64_t page = jb.page * p.H_kv + h;
+    const int64_t page = jb.page(p, h);
     if (tid < D) {
         float mn = h2f(s_lo[0][tid]), mx = h2f(s_hi[0][tid]);
 #pragma unroll
@@ -243,6 +247,22 @@ __device__ __forceinline__ void extend_keys(const ExtendParams &p, const PageJob
         *reinterpret_cast<uint4 *>(p.k_codes + (size_t)(row0 + r) * D + kword_pos(4 * lane, w * NWR + r)) =
             make_uint4(wd[0] - off, wd[1] - off, wd[2] - off, wd[3] - off);
     }
+}
+
+// The exact codes of eight channels of one group (m: its (scale, min)), packed: one word of
+// 2- or 4-bit codes, two of 8-bit ones.  Out of line, as exact_codes4: the unrolled loop
+// around the rare call has to fit the instruction cache.
+static __device__ __noinline__ uint2 exact_codes8(uint4 x, uint32_t m, int bits) {
+    const GroupQ g = group_from_meta(m, (1 << bits) - 1);
+    const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+    uint64_t w = 0;
+#pragma unroll
+    for (int k = 0; k < 4; k++) {
+        const float2 f = unpack_half2(u[k]);
+        w |= (uint64_t)quant_code(f.x, g) << (bits * 2 * k);
+        w |= (uint64_t)quant_code(f.y, g) << (bits * (2 * k + 1));
+    }
+    return make_uint2((uint32_t)w, (uint32_t)(w >> 32));
 }
 
 // 128 value tokens of one page (block vb of it): 16 tokens per warp, lane (tq, c) holds
@@ -302,16 +322,9 @@ __device__ __forceinline__ void extend_values(const ExtendParams &p, const PageJ
                 part[n] -= magic_sum(BITS, PER);
             }
             if (emax > kTieMargin) {  // near a half-integer in this chunk: the exact path
-#pragma unroll
-                for (int n = 0; n < NP; n++) {
-                    part[n] = 0;
-#pragma unroll
-                    for (int k = 0; k < PER / 2; k++) {
-                        const float2 f = unpack_half2((&x[g][i].x)[n * (PER / 2) + k]);
-                        part[n] |= quant_code(f.x, gr) << (BITS * (2 * k));
-                        part[n] |= quant_code(f.y, gr) << (BITS * (2 * k + 1));
-                    }
-                }
+                const uint2 w = exact_codes8(x[g][i], (uint32_t)gr.s16 | ((uint32_t)gr.mn16 << 16), BITS);
+                part[0] = w.x;
+                if (NP == 2) part[NP - 1] = w.y;
             }
             if (BITS == 2) {  // 16 channels per word: chunks 2m (lane c even) and 2m + 1
                 const uint32_t nb = __shfl_xor_sync(0xffffffffu, part[0], 1);
@@ -323,7 +336,7 @@ __device__ __forceinline__ void extend_values(const ExtendParams &p, const PageJ
         }
     }
     __syncthreads();
-    const int64_t page = jb.page * p.H_kv + h;
+    const int64_t page = jb.page(p, h);
     const int TV = p.TV;
     for (int i = tid; i < NWORD * 32; i += 256) {
         const int m = i >> 5, tt = vb * 128 + 4 * (i & 31), tile = tt / TV, j = tt - tile * TV;
