@@ -68,7 +68,7 @@ class Paged(ctypes.Structure):
 class ChunkDesc(ctypes.Structure):
     """kvq_chunk"""
     _fields_ = [(n, ctypes.c_void_p) for n in ("cu", "slot", "pos", "desc", "host")] + \
-               [(n, ctypes.c_int64) for n in ("max_tokens", "n_tokens")]
+               [(n, ctypes.c_int64) for n in ("max_tokens", "n_tokens")] + [("captured", ctypes.c_int32)]
 
 
 class QkConfig(ctypes.Structure):
@@ -220,7 +220,8 @@ class KVQChunk:
     ``cu`` [B + 1], ``slot`` and ``pos`` [max_tokens] (int32, on the device).  Made by
     KVQPagedCache.new_chunk.  Every cache of the same configuration and lengths may attend
     with it; the cache that it was planned on last extends with it.  Two attention calls that
-    may overlap need a chunk each."""
+    may overlap, or captured ones whose replays may, need a chunk each.  A chunk whose
+    attention was captured is not planned again: a replay reads its arrays."""
 
     def __init__(self, cfg, max_tokens, device):
         import torch
@@ -232,13 +233,13 @@ class KVQChunk:
         self.host = (ctypes.c_int32 * (8 * cfg.B))()
         self.ws = torch.empty(lib.kvq_paged_chunk_workspace_bytes(ctypes.byref(cfg)), dtype=torch.uint8, device=device)
         self.B = cfg.B
-        self.cache = None  # the cache of the last plan
+        self.cache, self.mapping = None, 0  # the cache of the last plan, and its state of page mappings
         pad = torch.zeros(4, **i32) if max_tokens == 0 else None  # an empty tensor has no address
         self._pad = pad
         self.ws_ptr, self.ws_bytes = self.ws.data_ptr(), self.ws.numel()
         self.c = ChunkDesc(self.cu.data_ptr(), (self.slot if pad is None else pad).data_ptr(),
                            (self.pos if pad is None else pad).data_ptr(), self.desc.data_ptr(),
-                           ctypes.cast(self.host, ctypes.c_void_p), max_tokens, 0)
+                           ctypes.cast(self.host, ctypes.c_void_p), max_tokens, 0, 0)
         self.ref = ctypes.byref(self.c)
 
     @property
@@ -484,6 +485,7 @@ class KVQPagedCache:
         self._dev = self.table.device                 # with its index
         self._refs = ctypes.byref(self.cfg), ctypes.byref(self.p)
         self.caller_pages = False                     # plan() was given pages of the caller's
+        self.mapping = 0                              # counts the calls that took pages away from slots
         self.free = list(range(n_pages - 1, -1, -1))  # pop() hands out the lowest id first
         self.pages = [[] for _ in range(B)]           # physical pages of each slot, logical order
         _check(lib.kvq_paged_init(cp, ctypes.byref(self.p), KVQCache._stream()), "paged init")
@@ -543,6 +545,7 @@ class KVQPagedCache:
         return out
 
     def release(self, b):
+        self.mapping += len(self.pages[b]) > 0
         self.free.extend(reversed(self.pages[b]))
         self.pages[b] = []
         _check(lib.kvq_paged_release(ctypes.byref(self.cfg), ctypes.byref(self.p), b, KVQCache._stream()),
@@ -554,6 +557,7 @@ class KVQPagedCache:
         _check(lib.kvq_paged_init(*self._refs, _stream_of(self._dev.index)),
                "paged init")
         if unmap:
+            self.mapping += 1
             for b in range(self.cfg.B - 1, -1, -1):
                 self.free.extend(reversed(self.pages[b]))
                 self.pages[b] = []
@@ -583,21 +587,30 @@ class KVQPagedCache:
             chunk = self.new_chunk(int(sum(n_new)))
         if chunk.B != cfg.B or chunk.cu.device != self._dev:
             raise ValueError("the chunk belongs to another configuration")
-        if pages is None:
-            pages = self._plan_pages(n_new.tolist() if isinstance(n_new, torch.Tensor) else n_new)
-        elif pages.device != self._dev or pages.dtype != torch.int32 or pages.dim() != 1 or not pages.is_contiguous():
+        taken = []  # (slot, page) handed out here
+        planned = pages is None
+        if not planned and (pages.device != self._dev or pages.dtype != torch.int32 or pages.dim() != 1 or
+                            not pages.is_contiguous()):
             raise ValueError("pages must be a contiguous int32 tensor on %s" % self._dev)
-        else:
-            self.caller_pages = True
-        _check(lib.kvq_paged_plan(*self._refs, np_, None if pages is None else pages.data_ptr(),
-                                  0 if pages is None else pages.numel(), chunk.ref, _stream_of(self._dev.index)),
-               "kvq_paged_plan")
-        chunk.cache = self
+        try:
+            if planned:
+                pages = self._plan_pages(n_new.tolist() if isinstance(n_new, torch.Tensor) else n_new, taken)
+            _check(lib.kvq_paged_plan(*self._refs, np_, None if pages is None else pages.data_ptr(),
+                                      0 if pages is None else pages.numel(), chunk.ref, _stream_of(self._dev.index)),
+                   "kvq_paged_plan")
+        except Exception:
+            for b, page in reversed(taken):  # their table rows are not written
+                self.pages[b].pop()
+                self.free.append(page)
+            raise
+        self.caller_pages |= not planned
+        chunk.cache, chunk.mapping = self, self.mapping
         return chunk
 
-    def _plan_pages(self, n_new):
+    def _plan_pages(self, n_new, taken):
         """Physical pages of a plan, from the free list: logical pages [T/G, ...) of each
-        slot that packs, as a device tensor (None: no slot packs)."""
+        slot that packs, as a device tensor (None: no slot packs); those that the slot did not
+        have are appended to taken."""
         cfg = self.cfg
         todo = []
         for b, n in enumerate(n_new):
@@ -618,7 +631,8 @@ class KVQPagedCache:
         ids = []
         for b, lo, hi in todo:
             while len(self.pages[b]) < hi:
-                self.pages[b].append(self.free.pop())
+                taken.append((b, self.free.pop()))
+                self.pages[b].append(taken[-1][1])
             ids += self.pages[b][lo:hi]
         t = self.torch.tensor(ids, dtype=self.torch.int32).pin_memory()
         return t.to(self._dev, non_blocking=True)
@@ -647,6 +661,8 @@ class KVQPagedCache:
         cfg, dev = self.cfg, self._dev
         if chunk.cache is not self and not self.caller_pages:
             raise KvqError(-1, "the chunk was planned on another cache")
+        if chunk.mapping != self.mapping and not self.caller_pages:
+            raise KvqError(-1, "pages were released since the plan")
         kp, ks = _rows(k_new, cfg.H_kv, cfg.D, chunk.n_tokens, dev, "k_new")
         vp, vs = _rows(v_new, cfg.H_kv, cfg.D, chunk.n_tokens, dev, "v_new")
         _check(lib.kvq_paged_extend(*self._refs, chunk.ref, kp, ks, vp, vs, _stream_of(dev.index)), "kvq_paged_extend")

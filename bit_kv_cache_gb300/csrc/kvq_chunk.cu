@@ -131,13 +131,13 @@ struct PageJob {
     int b;
     int entry;             // of the page table; read early, checked and used by page() at the end
     int t0;                // first stream token
+    // -1: no page, nothing may be stored
     __device__ __forceinline__ int64_t page(const ExtendParams &p, int h) const {
-        int e = entry;
-        if (e < 0 || e >= p.n_pages) {
+        if (entry < 0 || entry >= p.n_pages) {
             if (threadIdx.x == 0) report(p.status, KVQ_DEV_BAD_STATE);
-            e = 0;
+            return -1;
         }
-        return (int64_t)e * p.H_kv + h;
+        return (int64_t)entry * p.H_kv + h;
     }
 };
 
@@ -200,6 +200,7 @@ __device__ __forceinline__ void extend_keys(const ExtendParams &p, const PageJob
         make_uint2(*reinterpret_cast<uint32_t *>(&hi0), *reinterpret_cast<uint32_t *>(&hi1));
     __syncthreads();
     const int64_t page = jb.page(p, h);
+    if (page < 0) return;
     if (tid < D) {
         float mn = h2f(s_lo[0][tid]), mx = h2f(s_hi[0][tid]);
 #pragma unroll
@@ -337,6 +338,7 @@ __device__ __forceinline__ void extend_values(const ExtendParams &p, const PageJ
     }
     __syncthreads();
     const int64_t page = jb.page(p, h);
+    if (page < 0) return;
     const int TV = p.TV;
     for (int i = tid; i < NWORD * 32; i += 256) {
         const int m = i >> 5, tt = vb * 128 + 4 * (i & 31), tile = tt / TV, j = tt - tile * TV;
@@ -577,12 +579,11 @@ bool capturing(cudaStream_t st) {
     return s != cudaStreamCaptureStatusNone;
 }
 
-int check_chunk(const kvq_config *c, const kvq_chunk *ch) {
+int check_chunk(const kvq_chunk *ch) {
     if (!ch || !ch->host || ch->max_tokens < 0) return KVQ_ERR_INVALID_ARG;
     const void *need[] = {ch->cu, ch->slot, ch->pos, ch->desc};
     for (const void *p : need)
         if (!p || !aligned16(p)) return KVQ_ERR_INVALID_ARG;
-    (void)c;
     return KVQ_OK;
 }
 
@@ -671,7 +672,7 @@ int kvq_paged_plan(const kvq_config *c, kvq_paged *pc, const int32_t *n_new, con
                    int64_t n_new_pages, kvq_chunk *ch, void *stream) {
     int e = check_paged(c, pc);
     if (e) return e;
-    if ((e = check_chunk(c, ch))) return e;
+    if ((e = check_chunk(ch))) return e;
     if (!n_new || n_new_pages < 0 || (reinterpret_cast<uintptr_t>(new_pages) & 3u)) return KVQ_ERR_INVALID_ARG;
     int64_t rows = 0, pages = 0;
     for (int b = 0; b < c->B; b++) {
@@ -687,7 +688,7 @@ int kvq_paged_plan(const kvq_config *c, kvq_paged *pc, const int32_t *n_new, con
     if (rows > ch->max_tokens || rows > INT32_MAX - 4096) return KVQ_ERR_CAPACITY;
     if (new_pages && pages > n_new_pages) return KVQ_ERR_CAPACITY;
     cudaStream_t st = (cudaStream_t)stream;
-    if (capturing(st)) return KVQ_ERR_UNSUPPORTED;
+    if (ch->captured || capturing(st)) return KVQ_ERR_UNSUPPORTED;
     PlanParams p;
     p.cu = ch->cu;
     p.slot = ch->slot;
@@ -727,12 +728,12 @@ size_t kvq_paged_chunk_workspace_bytes(const kvq_config *c) {
     return paged_cfg_check(c) == KVQ_OK ? chunk_ws().total : 0;
 }
 
-int kvq_paged_chunk_attn(const kvq_config *c, const kvq_paged *pc, const kvq_chunk *ch, const uint16_t *q,
+int kvq_paged_chunk_attn(const kvq_config *c, const kvq_paged *pc, kvq_chunk *ch, const uint16_t *q,
                          int64_t q_stride, const uint16_t *kn, int64_t k_stride, const uint16_t *vn, int64_t v_stride,
                          uint16_t *out, void *ws, size_t ws_bytes, void *stream) {
     int e = check_paged(c, pc);
     if (e) return e;
-    if ((e = check_chunk(c, ch))) return e;
+    if ((e = check_chunk(ch))) return e;
     if (!plan_holds(c, pc, ch)) return KVQ_ERR_INVALID_ARG;
     if (ch->n_tokens == 0) return KVQ_OK;
     if (!rows_ok(q, q_stride, c->H_q, c->D) || !rows_ok(kn, k_stride, c->H_kv, c->D) ||
@@ -799,14 +800,16 @@ int kvq_paged_chunk_attn(const kvq_config *c, const kvq_paged *pc, const kvq_chu
     p.cost = (int)cost;
     p.C = (int)std::min<int64_t>(items, std::min(num_sms(), kMaxRanges));
     chunk_ranges(c, slots_of(ch), p);
-    return status_of(launch_chunk_attn(p, (cudaStream_t)stream));
+    if (launch_chunk_attn(p, (cudaStream_t)stream) != cudaSuccess) return KVQ_ERR_CUDA;
+    if (!ch->captured && capturing((cudaStream_t)stream)) ch->captured = 1;
+    return KVQ_OK;
 }
 
 int kvq_paged_extend(const kvq_config *c, kvq_paged *pc, const kvq_chunk *ch, const uint16_t *kn, int64_t k_stride,
                      const uint16_t *vn, int64_t v_stride, void *stream) {
     int e = check_paged(c, pc);
     if (e) return e;
-    if ((e = check_chunk(c, ch))) return e;
+    if ((e = check_chunk(ch))) return e;
     if (!plan_holds(c, pc, ch)) return KVQ_ERR_INVALID_ARG;
     if (ch->n_tokens == 0) return KVQ_OK;
     if (!rows_ok(kn, k_stride, c->H_kv, c->D) || !rows_ok(vn, v_stride, c->H_kv, c->D)) return KVQ_ERR_INVALID_ARG;

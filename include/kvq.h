@@ -455,11 +455,14 @@ int kvq_paged_read_status(const kvq_paged *pc, void *ws, int32_t *dev_status, vo
  *                                before the chunk
  *   host  int32 [B][8]           (host)   the same
  * n_tokens is set by kvq_paged_plan.  slot and pos keep their values behind n_tokens.
+ * captured (0 at first) is set by a kvq_paged_chunk_attn that is captured into a graph: a
+ * replay reads the plan's device arrays, so the chunk is not planned again.
  * --------------------------------------------------------------------------------- */
 typedef struct {
     int32_t *cu, *slot, *pos, *desc;
     int32_t *host;
     int64_t max_tokens, n_tokens;
+    int32_t captured;
 } kvq_chunk;
 
 /* Plans a chunk of n_new[b] (host int32 [B]) tokens for each slot.  A slot that is not
@@ -474,7 +477,7 @@ typedef struct {
  * A plan may serve other caches of the same configuration and lengths if their page tables
  * map the pages too.
  * KVQ_ERR_UNSUPPORTED while `stream` is capturing (a replay would not advance the host
- * lengths). */
+ * lengths), and for a chunk that a captured attention call reads (kvq_chunk.captured). */
 int kvq_paged_plan(const kvq_config *cfg, kvq_paged *pc, const int32_t *n_new, const int32_t *new_pages,
                    int64_t n_new_pages, kvq_chunk *chunk, void *stream);
 
@@ -487,18 +490,21 @@ size_t kvq_paged_chunk_workspace_bytes(const kvq_config *cfg);
  * over the slot's cached tokens (sink, packed pages, residual) and its new tokens 0 .. j.
  * q: device fp16 rows of H_q heads; k_new, v_new: rows of H_kv heads; out: device fp16
  * [n_tokens][H_q][D], contiguous, overlapping none of the inputs.  Rows of the tensors
- * behind n_tokens are neither read nor written.  The cache is not changed.  Operands are fp16 (dequantized keys and values
- * and softmax weights are rounded to it once), sums and softmax statistics fp32.
+ * behind n_tokens are neither read nor written.  The cache is not changed.  Operands are
+ * fp16 (dequantized keys and values and softmax weights are rounded to it once), sums and
+ * softmax statistics fp32.
  * Infinite and NaN values reach the rows that see them and no others.
- * KVQ_ERR_INVALID_ARG if the cache's lengths are not those of the plan. */
-int kvq_paged_chunk_attn(const kvq_config *cfg, const kvq_paged *pc, const kvq_chunk *chunk, const uint16_t *q,
+ * KVQ_ERR_INVALID_ARG if the cache's lengths are not those of the plan.  The call may be
+ * captured: a replay attends over the plan's lengths. */
+int kvq_paged_chunk_attn(const kvq_config *cfg, const kvq_paged *pc, kvq_chunk *chunk, const uint16_t *q,
                          int64_t q_stride, const uint16_t *k_new, int64_t k_stride, const uint16_t *v_new,
                          int64_t v_stride, uint16_t *out, void *ws, size_t ws_bytes, void *stream);
 
 /* The chunk's tokens enter the cache (see kvq_paged_plan): sink and residual rows are
  * copied, whole groups quantized into the mapped pages with the codes and scales that
  * kvq_paged_flush gives, and the lengths advance (host lengths at enqueue time).  Rows of
- * the fp16 buffers behind the new lengths keep their values.  k_new, v_new as for
+ * the fp16 buffers behind the new lengths keep their values.  A group whose page-table
+ * entry is no page is not stored (KVQ_DEV_BAD_STATE).  k_new, v_new as for
  * kvq_paged_chunk_attn.  KVQ_ERR_INVALID_ARG if the cache's lengths are not those of the
  * plan (so a plan extends a cache once); KVQ_ERR_UNSUPPORTED while `stream` is capturing. */
 int kvq_paged_extend(const kvq_config *cfg, kvq_paged *pc, const kvq_chunk *chunk, const uint16_t *k_new,
@@ -523,9 +529,9 @@ typedef struct {
 
 /* y = x / sqrt(mean(x^2) + eps) * w over each head's D channels (skipped where the weight
  * pointer is NULL), then the rotation by pos[i], in fp32 with one rounding to fp16; the
- * angles are reduced exactly (64-bit fixed point) at any position before the fp32 sine and cosine.  q, k: device fp16 rows (strides above); w_q,
- * w_k: device fp16 [D] or NULL; pos: device int32 [n]; q_out, k_out: device fp16
- * [n][H][D], contiguous.  An output may be its own input if that is contiguous; any other
+ * angles are reduced exactly (64-bit fixed point) at any position before the fp32 sine and
+ * cosine.  q, k: device fp16 rows (strides above); w_q, w_k: device fp16 [D] or NULL; pos:
+ * device int32 [n]; q_out, k_out: device fp16 [n][H][D], contiguous.  An output may be its own input if that is contiguous; any other
  * overlap of an output with an input or the other output is KVQ_ERR_INVALID_ARG. */
 int kvq_qk_norm_rope(const kvq_qk_config *c, const uint16_t *q, const uint16_t *k, const uint16_t *w_q,
                      const uint16_t *w_k, const int32_t *pos, int64_t n, uint16_t *q_out, uint16_t *k_out,

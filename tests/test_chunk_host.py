@@ -130,6 +130,14 @@ def test_attention_and_extend_refusals(kvq):
     assert list(f.lens) == state
 
 
+def test_captured_chunk_is_not_planned_again(kvq):
+    f = Fake(kvq, LENS).planned([2, 3, 1, 1])
+    f.ch.captured = 1
+    state = list(f.host)
+    assert f.plan([1, 1, 1, 1]) == UNSUPPORTED
+    assert list(f.host) == state
+
+
 def test_empty_chunk_enqueues_nothing(kvq):
     f = Fake(kvq, LENS).planned([0, 0, 0, 0])
     assert f.attn(q=None) == 0 and f.extend(k=None) == 0

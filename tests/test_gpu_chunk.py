@@ -295,6 +295,77 @@ def test_extend_bad_page_is_reported():
     assert c.read_status() == 2
 
 
+@pytest.mark.parametrize("R", [128, 256])
+@pytest.mark.parametrize("bits", [2, 8])
+def test_extend_bad_page_stores_nothing(R, bits):
+    rng = np.random.default_rng(R)
+    c = make_cache(rng, [100, 0], R=R, bits=bits)
+    n = 2 * R - 100
+    q, k, v = chunk_inputs(rng, c, n)
+    ch = c.plan([n, 0])
+    good = int(c.table[0, 1])
+    c.table[0, 0] = c.n_pages
+    before = {name: c.buf[name].clone() for name in ("k_codes", "k_meta", "v_codes", "v_meta")}
+    c.extend(ch, k, v)
+    assert c.read_status() == 2
+    for name, old in before.items():
+        same = (c.buf[name].view(c.n_pages, -1) == old.view(c.n_pages, -1)).all(1)
+        assert not same[good] and same.sum() == c.n_pages - (2 * R // 128 - 1), name
+
+
+def test_captured_chunk_is_not_planned_again():
+    """A replay reads the plan's arrays."""
+    import bit_kv_cache_gb300 as kvq
+    rng = np.random.default_rng(31)
+    c = make_cache(rng, [300, 40])
+    q, k, v = chunk_inputs(rng, c, 12)
+    ch, other = c.plan([10, 2]), c.plan([10, 2])
+    out = c.chunk_attn(other, q, k, v)
+    got = torch.zeros_like(out)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        c.chunk_attn(ch, q, k, v, out=got)
+    with pytest.raises(kvq.KvqError) as e:
+        c.plan([1, 2], ch)
+    assert e.value.code == -2
+    c.plan([1, 2], other)
+    graph.replay()
+    assert torch.equal(got, out)
+
+
+def test_refused_plan_takes_no_pages():
+    """The pages of a plan that the library refuses go back, so that a later flush maps them."""
+    import bit_kv_cache_gb300 as kvq
+    rng = np.random.default_rng(32)
+    c = make_cache(rng, [127, 0])
+    free = list(c.free)
+    with pytest.raises(kvq.KvqError):
+        c.plan([130, 0], c.new_chunk(8))
+    assert c.free == free and c.pages == [[], []]
+    with pytest.raises(kvq.KvqError):
+        c.plan([1 << 20, 0], c.new_chunk(8), pages=torch.zeros(4, dtype=torch.int32, device=DEV))
+    for _ in range(2):
+        c.append(randn(rng, 2, 2, 128), randn(rng, 2, 2, 128))
+        c.flush()
+    assert c.lengths(0)["T"] == 128 and int(c.table[0, 0]) == free[-1] and c.read_status() == 0
+
+
+def test_extend_after_released_pages():
+    """A plan's pages that went back to the pool are another slot's."""
+    import bit_kv_cache_gb300 as kvq
+    rng = np.random.default_rng(33)
+    c = make_cache(rng, [0, 0])
+    q, k, v = chunk_inputs(rng, c, 130)
+    for give_back in (lambda: c.release(0), c.clear):
+        ch = c.plan([130, 0])
+        give_back()
+        with pytest.raises(kvq.KvqError) as e:
+            c.extend(ch, k, v)
+        assert e.value.code == -1
+    c.extend(c.plan([130, 0], ch), k, v)
+    assert c.lengths(0)["T"] == 128 and c.read_status() == 0
+
+
 def test_plan_goes_stale():
     """A plan holds for the lengths it was made for, and extends a cache once."""
     import bit_kv_cache_gb300 as kvq
@@ -454,8 +525,7 @@ def test_run_together():
         prompt_v.append(v[: new[0]])
         for b in range(3):  # what was cached before is still the front of the cache
             L = kept[b][0].shape[1]
-            T = c.lengths(b)["T"] + c.lengths(b)["n_sink"]
-            same = min(L, T) // 128 * 128 if False else min(L, 4)
+            same = min(L, 4)
             assert np.array_equal(cached_rows(c, b)[0][:, :same], kept[b][0][:, :same])
     # slot 0 holds what a prefill of the same rows holds
     k = torch.cat(prompt_k).transpose(0, 1).contiguous()
