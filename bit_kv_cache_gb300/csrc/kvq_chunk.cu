@@ -629,9 +629,73 @@ ChunkWs chunk_ws() {
     return w;
 }
 
-// The C ranges: each starts at the item behind its even share of the cost.  A unit whose
-// start is no further before the even cut than its own fixed cost starts the range.
-void chunk_ranges(const kvq_config *c, const ChunkSlot *slots, ChunkAttnParams &p) {
+// f(slot, row tile, items, cost of an item) for the units of one head of each slot.
+template <typename F>
+void for_units(const kvq_config *c, const ChunkSlot *slots, int g, F f) {
+    for (int b = 0; b < c->B; b++) {
+        const ChunkSlot &s = slots[b];
+        const bool narrow = chunk_narrow(s.n_new, g);
+        const int rows = narrow ? kNarrowRows : kWideRows, w = narrow ? kNarrowCost : kWideCost;
+        for (int t = 0; (int64_t)t * rows < (int64_t)s.n_new * g; t++) f(b, t, chunk_tiles(s, t, rows, g), w);
+    }
+}
+// Parts of equal length of a unit of n items, each of a cost of at most X, or kPartItems items.
+int unit_parts(int n, int w, int X) {
+    const int m = std::max(kPartItems, X / w - kUnitItems);  // items of a part
+    return (n + m - 1) / m;
+}
+// Few units (at most C): parts of a unit each, if the longest is no longer than a range of
+// even cuts, most of which hold the end of one unit and the start of another.  Units stay
+// whole where that is no longer than parts and the combine kernel.
+bool unit_ranges(const kvq_config *c, const ChunkSlot *slots, int64_t units, ChunkAttnParams &p) {
+    if (units > p.C) return false;
+    int whole = 0;
+    for_units(c, slots, p.g, [&](int, int, int n, int w) { whole = std::max(whole, (n + kUnitItems) * w); });
+    int lo = 0, hi = whole;  // the smallest X whose parts are C at most
+    while (lo < hi) {
+        const int X = (lo + hi) / 2;
+        int64_t parts = 0;
+        for_units(c, slots, p.g, [&](int, int, int n, int w) { parts += (int64_t)c->H_kv * unit_parts(n, w, X); });
+        if (parts <= p.C) hi = X;
+        else lo = X + 1;
+    }
+    int longest = 0;
+    for_units(c, slots, p.g, [&](int, int, int n, int w) {
+        const int parts = unit_parts(n, w, hi);
+        longest = std::max(longest, ((n + parts - 1) / parts + kUnitItems) * w);
+    });
+    const int even = std::max(p.cost / p.C, kPartItems * kNarrowCost) + kUnitItems * kNarrowCost;
+    const bool in_one = whole <= std::min(longest, even) + kCombineCost;
+    if (!in_one && longest > even) return false;
+    const int X = in_one ? whole : hi;
+    int k = 0;
+    for (int b = 0; b < c->B; b++) {
+        const ChunkSlot &s = slots[b];
+        if (s.n_new == 0) continue;
+        const bool narrow = chunk_narrow(s.n_new, p.g);
+        const int rows = narrow ? kNarrowRows : kWideRows, w = narrow ? kNarrowCost : kWideCost;
+        int first = p.cost0[b];
+        for (int h = 0; h < c->H_kv; h++)
+            for (int t = 0; (int64_t)t * rows < (int64_t)s.n_new * p.g; t++) {
+                const int n = chunk_tiles(s, t, rows, p.g), parts = unit_parts(n, w, X);
+                for (int i = 0; i < parts; i++, k++) {
+                    const int x = (int)((int64_t)n * i / parts);
+                    p.begin[k] = i ? first + (kUnitItems + x) * w : first;
+                    p.first[k] = first;
+                    p.tile[k] = t;
+                }
+                if (parts > 1) p.cut = 1;
+                first += (n + kUnitItems) * w;
+            }
+    }
+    p.C = k;
+    p.begin[k] = p.cost;
+    return true;
+}
+
+// Otherwise each of the C ranges starts at the item behind its even share of the cost.  A
+// unit whose start is no further before the even cut than its own fixed cost starts the range.
+void even_ranges(const kvq_config *c, const ChunkSlot *slots, ChunkAttnParams &p) {
     int b = 0, t = 0;
     int64_t head = 0, first = 0;  // start of the current head's units, and of unit t
     for (int k = 0; k <= p.C; k++) {
@@ -651,7 +715,8 @@ void chunk_ranges(const kvq_config *c, const ChunkSlot *slots, ChunkAttnParams &
                 first = head;
                 t = 0;
             }
-            const int64_t end = first + (int64_t)(chunk_tiles(s, t, rows, p.g) + kUnitItems) * w;
+            const int n = chunk_tiles(s, t, rows, p.g);
+            const int64_t end = first + (int64_t)(n + kUnitItems) * w;
             if (pos >= end) {
                 first = end;
                 t++;
@@ -659,6 +724,9 @@ void chunk_ranges(const kvq_config *c, const ChunkSlot *slots, ChunkAttnParams &
             }
             const int64_t x = (pos - first + w - 1) / w - kUnitItems;  // items before it, rounded up
             p.begin[k] = (int32_t)(x <= 0 ? first : first + (kUnitItems + x) * w);
+            p.first[k] = (int32_t)first;
+            p.tile[k] = t;
+            if (x > 0 && x < n) p.cut = 1;
             break;
         }
     }
@@ -779,7 +847,7 @@ int kvq_paged_chunk_attn(const kvq_config *c, const kvq_paged *pc, kvq_chunk *ch
     p.S = c->S;
     p.R = c->R;
     p.ptab_stride = (int)(c->max_T / c->G);
-    int64_t cost = 0, items = 0;
+    int64_t cost = 0, items = 0, units = 0;
     for (int b = 0; b < c->B; b++) {
         const ChunkSlot &s = slots_of(ch)[b];
         p.cost0[b] = (int32_t)cost;
@@ -790,6 +858,7 @@ int kvq_paged_chunk_attn(const kvq_config *c, const kvq_paged *pc, kvq_chunk *ch
             const int n = chunk_tiles(s, (int)t, rows, p.g);
             per += n + kUnitItems;
             items += (int64_t)n * p.H_kv;
+            units += p.H_kv;
         }
         if (s.n_new && narrow) p.narrow = std::max(p.narrow, s.n_new * p.g);
         if (s.n_new && !narrow) p.wide = 1;
@@ -799,7 +868,7 @@ int kvq_paged_chunk_attn(const kvq_config *c, const kvq_paged *pc, kvq_chunk *ch
     for (int b = c->B; b <= KVQ_PAGED_MAX_B; b++) p.cost0[b] = (int32_t)cost;
     p.cost = (int)cost;
     p.C = (int)std::min<int64_t>(items, std::min(num_sms(), kMaxRanges));
-    chunk_ranges(c, slots_of(ch), p);
+    if (!unit_ranges(c, slots_of(ch), units, p)) even_ranges(c, slots_of(ch), p);
     if (launch_chunk_attn(p, (cudaStream_t)stream) != cudaSuccess) return KVQ_ERR_CUDA;
     if (!ch->captured && capturing((cudaStream_t)stream)) ch->captured = 1;
     return KVQ_OK;

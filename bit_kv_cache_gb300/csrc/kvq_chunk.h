@@ -47,14 +47,14 @@ struct QkParams {
     uint64_t turn[128];                  // base^(-2j/rotary) / (2 pi) in units of 2^-64 turns
 };
 
-constexpr int kNarrowRows = 128, kWideRows = 256, kNarrowCost = 3, kWideCost = 4, kUnitItems = 3, kMaxRanges = 256;
+constexpr int kNarrowRows = 128, kWideRows = 256, kNarrowCost = 3, kWideCost = 4, kUnitItems = 5, kCombineCost = 6, kPartItems = 2, kMaxRanges = 256;
 
 // Chunk attention.  A unit is (slot, key head, tile of query rows): row r of a slot is its
 // new token r / g under query head r % g of the key head's group.  Its items are key tiles
 // of 128 tokens: the packed ones, then the fp16 tokens [sink | residual | chunk] up to the
 // row tile's last query token.  A slot of at most kNarrowRows rows is one narrow unit per
 // head, a slot of more consists of wide ones (kWideRows rows).  Positions count cost: an
-// item's (kNarrowCost, kWideCost: 1.5 and 2.0 us measured) and, before a unit's first item,
+// item's (kNarrowCost, kWideCost: a tile took 1.5 and 2.0 us) and, before a unit's first item,
 // that of kUnitItems more (the start and the end of a unit).  All units, slot-major, then by
 // head and row tile, are cut into C ranges of equal cost, one per CTA.  A unit inside one
 // range is finished there; of one that is cut, each range leaves fp32 partials, and the
@@ -72,10 +72,11 @@ struct ChunkAttnParams {
     int32_t *status;
     int64_t q_stride, k_stride, v_stride, n_pages;
     int B, H_kv, g, G, kbits, vbits, S, R, ptab_stride;
-    int cost, C;                         // of all units; ranges
-    int narrow, wide;                    // most rows of a narrow unit (0: there is none), whether there are wide ones
+    int cost, C, cut;                    // of all units; ranges; whether a unit lies in several
+    int narrow, wide;                    // most rows of a narrow unit (0: there is none); whether there are wide units
     int32_t cost0[KVQ_PAGED_MAX_B + 1];  // position of each slot's first unit
     int32_t begin[kMaxRanges + 1];       // first position of each range, that of an item; begin[C] = cost
+    int32_t first[kMaxRanges], tile[kMaxRanges];  // the unit it lies in: first position, row tile
 };
 
 cudaError_t launch_plan(const PlanParams &p, cudaStream_t st);
@@ -87,8 +88,8 @@ __host__ __device__ inline bool chunk_narrow(int n_new, int g) { return (int64_t
 // Copies of a narrow unit's rows in its query tile.
 __host__ __device__ inline int chunk_copies(int rows) { return rows > 64 ? 1 : rows > 32 ? 2 : 4; }
 
-// Launches a kernel that may start while the kernel before it in the stream drains; it calls
-// griddep_wait before it touches anything that one writes.
+// Launches a kernel that may start before the kernel before it in the stream has ended; it
+// calls griddep_wait before it touches anything that one writes.
 template <typename K, typename... A>
 inline cudaError_t launch_dependent(K kernel, dim3 grid, int threads, int smem, cudaStream_t st, A... args) {
     cudaLaunchConfig_t lc = {};

@@ -3,8 +3,22 @@
 //
 // For query row r of a unit (see ChunkAttnParams) and key t of its slot,
 //   s_t = q . (code_t * scale + min) / sqrt(D),   out = sum_t softmax(s)_t v_t,
-// in one pass over the keys with a running maximum and sum per row.  Dequantized keys and
-// values are rounded once to fp16, softmax weights too; sums are fp32.
+// in one pass over the keys with a running maximum and sum per row.  Sums, maxima and the
+// output's accumulators are fp32.  Dequantized keys and values and the softmax weights are
+// rounded once to fp16, the operand type of the products: outputs of unit-variance values are
+// then off by 3.1e-4 to 5.6e-4 of their size (2.1e-4 is the rounding of the output itself).
+// Exact operands would be codes with the scales folded into the other operand, which differ
+// from page to page (keys: another Q tile per page) and would be rounded there instead.
+//
+// What bounds it.  Wide units: the tensor core.  A product with M = 128 reads its operands
+// from shared memory at 128 bytes a cycle: K = 16 takes 48 cycles at N = 64, 64 at N = 128, so
+// a key tile of 256 rows takes 2478 cycles when nothing else runs.  2048 tokens of 32 heads
+// over 32868 cached ones (2-bit; 1137 GFLOP): 864 us, 1.32 PFLOP/s, 0.71 of cuBLAS' burst rate;
+// dequantization and softmax take issue slots (0.5 a cycle and scheduler) and shared memory
+// beside it.  Narrow units: the chain scores - softmax - product of a key tile, whose links
+// wait for warps that share their schedulers with the producers; 2300 cycles a tile, of which
+// products need 1024.  Eight slots of 17K to 56K tokens with 1 to 8 new ones: 147 us, where
+// the packed bytes take 24.
 //
 // One CTA per SM, eight groups of four warps:
 //   groups 0, 1  softmax, a thread per row of 128: reads the scores S_m from tensor memory,
@@ -15,14 +29,18 @@
 //                shared memory, fp16 rows are gathered;
 //   groups 6, 7  warps 24 + m issue the products S_m = Q K^T, warps 26 + m O_m += P_m V: each
 //                waits for its own operands while the others keep the tensor core busy (one
-//                warp for all four was the bottleneck: a wait costs it about 200 cycles).
+//                warp for all four: 1520 us against 1253; a wait that is over costs it about
+//                100 cycles, and up to 3000 when its scheduler's other warps never stall);
+//                warps 28, 29 bring the packed keys and values (issued by the producers
+//                themselves: 1025 us against 990).
 // In a wide unit (256 rows) m names the query tile: a key tile is dequantized once for both.
 // In a narrow one (at most 128 rows) m is the parity of the key tile: the two groups keep
 // softmax states of their own, joined at the end.  With at most 64 (32) rows, a part of a unit
 // that is cut holds them twice (four times) in its query tile, and each copy's softmax takes
 // half (a quarter) of a tile's keys: the tensor core's rows cost nothing, and a step of the
-// softmax, which is what such a unit waits for, is as much shorter.  The combine kernel joins
-// the copies' partials like those of the ranges.
+// softmax, which is what such a unit waits for, is as much shorter (the eight slots above:
+// 171 us against 190 without, when this came in).  The combine kernel joins the copies' partials like those of
+// the ranges.
 // A step is half a key tile (64 keys).  S_m has two buffers of 64 columns, so that the scores
 // of the next step are made while the softmax of this one runs.  Tensor memory: S_0, S_1,
 // O_0, O_1, 128 columns each.
@@ -68,19 +86,29 @@ struct Bars {
 constexpr int kSmemBytes = kOffBar + (int)sizeof(Bars);
 static_assert(kSmemBytes <= 232448, "shared memory");
 
-// Segment: the items of one unit inside the CTA's range; its end, and its steps.
+// Segment: the items of one unit inside the CTA's range; its steps.
 struct Seg {
     Item it;
-    int k0, k1, np, valid, end, steps, rep;  // rep: copies of a narrow unit's rows in its query tile
+    int k0, k1, np, valid, steps, rep;  // rep: copies of a narrow unit's rows in its query tile
     bool narrow;
 };
-__device__ __forceinline__ Seg next_seg(const ChunkAttnParams &p, int at, int end) {
+// A CTA's place in its range.
+struct At {
+    int pos, end, first, tile;  // first, tile: of the unit at pos, or of one before it
+    __device__ __forceinline__ explicit At(const ChunkAttnParams &p)
+        : pos(p.begin[blockIdx.x]), end(p.begin[blockIdx.x + 1]), first(p.first[blockIdx.x]), tile(p.tile[blockIdx.x]) {}
+    __device__ __forceinline__ bool more() const { return pos < end; }
+};
+__device__ __forceinline__ Seg next_seg(const ChunkAttnParams &p, At &c) {
     Seg s;
-    s.it = find_item(p, at);
+    const int at = c.pos, end = c.end;
+    s.it = find_item(p, at, c.first, c.tile);
     s.narrow = s.it.rows == kNarrowRows;
     s.k0 = s.it.at(at);
     s.k1 = s.it.at(end);
-    s.end = min(end, s.it.end());
+    c.pos = min(end, s.it.end());
+    c.first = s.it.end();
+    c.tile = s.it.t + 1;
     s.np = s.it.s.T / kChunkKeys;
     s.valid = min(s.it.rows, s.it.s.n_new * p.g - s.it.t * s.it.rows);
     s.rep = s.narrow && s.k1 - s.k0 < s.it.n ? chunk_copies(s.valid) : 1;  // partials: each copy leaves its own
@@ -226,7 +254,7 @@ struct Raw {
 // One lane brings the packed tiles of the keys (values) into their ring, as far ahead as it
 // has slots.  The page-table entry of a tile is read before the copy of the tile before it
 // is waited for.
-__device__ __forceinline__ void bring(const ChunkAttnParams &p, unsigned char *sm, Bars *bar, bool value, int begin, int end) {
+__device__ __forceinline__ void bring(const ChunkAttnParams &p, unsigned char *sm, Bars *bar, bool value) {
     const Raw raw(p, value);
     const int bits = value ? p.vbits : p.kbits;
     uint64_t(*arrived)[kMaxRaw] = value ? bar->rawv : bar->rawk, *read = value ? bar->readv : bar->readk;
@@ -236,9 +264,8 @@ __device__ __forceinline__ void bring(const ChunkAttnParams &p, unsigned char *s
     Ring cp = {0, 1};
     int n = 0;                 // tiles of the segments before
     uint32_t used = 0, parity = 0;  // per barrier (bit kMaxRaw par + slot): whether and how often used
-    for (int at = begin; at < end;) {
-        const Seg s = next_seg(p, at, end);
-        at = s.end;
+    for (At at(p); at.more();) {
+        const Seg s = next_seg(p, at);
         const int npk = min(s.k1, s.np), n0 = n - s.k0;
         n += s.k1 - s.k0;
         const int32_t *row = p.ptab + (size_t)s.it.b * p.ptab_stride;
@@ -268,9 +295,11 @@ __device__ __forceinline__ void bring(const ChunkAttnParams &p, unsigned char *s
 }
 
 // ---------------------------------------------------------------- groups 2-5: tiles ---
-// All four run the same code (the kernel is as fast as its hot code is small: six roles
-// share an SM's instruction cache).
-__device__ __forceinline__ void produce(const ChunkAttnParams &p, unsigned char *sm, Bars *bar, bool value, int par, int begin, int end) {
+// All four run the same code, and its loops stay rolled: the roles share an SM's instruction
+// cache (unrolled loops: 1672 us against 1107, half of all stalls for want of instructions).
+// Every second tile each: a group that makes every tile of its side waits for the release of
+// the tile before (979 us against 950).
+__device__ __forceinline__ void produce(const ChunkAttnParams &p, unsigned char *sm, Bars *bar, bool value, int par) {
     const int tid = threadIdx.x & 127, bits = value ? p.vbits : p.kbits, TV = value ? 256 / p.kbits : kChunkKeys;
     const Raw raw(p, value);
     unsigned char *dst = sm + (value ? kOffV : kOffK) + par * kTileBytes;
@@ -279,9 +308,8 @@ __device__ __forceinline__ void produce(const ChunkAttnParams &p, unsigned char 
     int slot = 0;              // of the next packed tile, of either parity
     uint32_t landed = 0, free = 1, nq = 1;  // parities: of the slots' arrivals, of the tile's release
     int seg = 0, n = 0;        // n: tiles of the segments before
-    for (int at = begin; at < end; seg++) {
-        const Seg s = next_seg(p, at, end);
-        at = s.end;
+    for (At at(p); at.more(); seg++) {
+        const Seg s = next_seg(p, at);
         if (value && par == 0) {
             // queries: 128-row tiles, rows of tokens' heads; rows behind the last one repeat it
             await(&bar->q_empty, nq & 1, &bar->stop, p.status);
@@ -329,13 +357,13 @@ __device__ __forceinline__ void produce(const ChunkAttnParams &p, unsigned char 
     }
 }
 
-// ---------------------------------------------------------------- group 6: products ---
+// ---------------------------------------------------------------- warps 24-27: products
 // Rows along M and N (keys: tokens, packed values: channels): 16 of the contracted dimension
 // are 32 bytes of a row; fp16 value rows run along the tokens: 16 are two atoms.
 
 // Warp 24 + m: the scores S_m.  A buffer's next scores go over its old weights, once the
 // product that reads those has ended.
-__device__ __forceinline__ void issue_scores(const ChunkAttnParams &p, unsigned char *sm, Bars *bar, uint32_t tm, int m, int begin, int end) {
+__device__ __forceinline__ void issue_scores(const ChunkAttnParams &p, unsigned char *sm, Bars *bar, uint32_t tm, int m) {
     const uint32_t base = smem_u32(sm), lead = (threadIdx.x & 31) == 0;
     uint32_t n = 0, nq = 0;       // key tiles, query tiles
     uint32_t ph = 0, any = 0;     // per buffer h: parity of the products awaited, whether there was one
@@ -356,9 +384,8 @@ __device__ __forceinline__ void issue_scores(const ChunkAttnParams &p, unsigned 
         }
         tc_commit(&bar->s_full[m][h], lead);
     };
-    for (int at = begin; at < end;) {
-        const Seg s = next_seg(p, at, end);
-        at = s.end;
+    for (At at(p); at.more();) {
+        const Seg s = next_seg(p, at);
         wait(&bar->q_full, nq);
         nq++;
         const int tiles = s.k1 - s.k0;
@@ -390,13 +417,12 @@ __device__ __forceinline__ void issue_scores(const ChunkAttnParams &p, unsigned 
 }
 
 // Warp 26 + m: the products O_m += P_m V.
-__device__ __forceinline__ void issue_values(const ChunkAttnParams &p, unsigned char *sm, Bars *bar, uint32_t tm, int m, int begin, int end) {
+__device__ __forceinline__ void issue_values(const ChunkAttnParams &p, unsigned char *sm, Bars *bar, uint32_t tm, int m) {
     const uint32_t base = smem_u32(sm), lead = (threadIdx.x & 31) == 0;
     uint32_t n = 0, ph = 0;       // value tiles; per buffer h: parity of the weights awaited
     auto wait = [&](uint64_t *b, uint32_t parity) { warp_await(b, parity & 1, &bar->stop, p.status); };
-    for (int at = begin; at < end;) {
-        const Seg s = next_seg(p, at, end);
-        at = s.end;
+    for (At at(p); at.more();) {
+        const Seg s = next_seg(p, at);
         const int tiles = s.k1 - s.k0, steps = s.narrow ? 2 * tiles : s.steps;
         bool acc = false;
         for (int j = 0; j < tiles; j++) {
@@ -496,8 +522,9 @@ __device__ __forceinline__ void load_scores(uint32_t *x, uint32_t ts, int y) {
 // The steps of one segment for query tile or key parity m; narrow units: every second key
 // tile.  ts, to: tensor memory of S_m and O_m; lim: fp16 tokens the row may see; any: whether
 // the warp has rows at all.  The weights are formed with a reference mx that some earlier
-// step's maximum gave: their sum tells whether one of them is above 2^(kUp + kLag), and only
-// then the maximum is looked for and the weights are formed again.
+// step's maximum gave: their sum tells whether one of them may be too large for fp16, and
+// only then the maximum is looked for and the weights are formed again (a maximum in every
+// step: 1253 us against 1175).
 template <bool NARROW>
 __device__ __forceinline__ void softmax_steps(const ChunkAttnParams &p, Bars *bar, const Seg &s, RowState &st, uint32_t ts, uint32_t to,
                                               int m, int lim, bool any) {
@@ -610,17 +637,16 @@ __device__ __forceinline__ void softmax_tiles(const ChunkAttnParams &p, Bars *ba
     st.l = l;
 }
 
-__device__ __forceinline__ void softmax(const ChunkAttnParams &p, Bars *bar, uint32_t tm, int m, int begin, int end) {
+__device__ __forceinline__ void softmax(const ChunkAttnParams &p, Bars *bar, uint32_t tm, int m) {
     const int lane_row = threadIdx.x & 127;
     const uint32_t lanes = (uint32_t)(threadIdx.x & 96) << 16;
     const uint32_t ts = tm + lanes + m * 128, to = tm + lanes + 256 + m * 128;
     RowState st = {0, 0, 0, 0.f, 0.f};
     int seg = 0;
-    for (int at = begin; at < end; seg++) {
-        const Seg s = next_seg(p, at, end);
-        const bool last_first = s.k0 == 0 && at != begin;
+    for (At at(p); at.more(); seg++) {
+        const Seg s = next_seg(p, at);
+        const bool last_first = s.k0 == 0 && s.it.first != p.begin[blockIdx.x];
         const int base = s.narrow ? 0 : 128 * m, row = s.rep > 1 ? lane_row & (128 / s.rep - 1) : base + lane_row;
-        at = s.end;
         const int n = s.k1 - s.k0;
         if (base >= s.valid || (s.narrow && m >= n)) continue;
         const bool any = s.rep > 1 || base + (lane_row & 96) < s.valid;
@@ -752,23 +778,22 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attn_kernel(const __grid_co
     tc_fence_after();
     const uint32_t tm = bar->tmem;
     griddep_wait();
-    const int begin = p.begin[blockIdx.x], end = p.begin[blockIdx.x + 1];
     if (w < 8) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
-        softmax(p, bar, tm, w >> 2, begin, end);
+        softmax(p, bar, tm, w >> 2);
     } else if (w < 24) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsTiles));
-        produce(p, sm, bar, w >= 16, (w >> 2) & 1, begin, end);
+        produce(p, sm, bar, w >= 16, (w >> 2) & 1);
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
         if (w < 28) {
-            if (w < 26) issue_scores(p, sm, bar, tm, w & 1, begin, end);
-            else issue_values(p, sm, bar, tm, w & 1, begin, end);
+            if (w < 26) issue_scores(p, sm, bar, tm, w & 1);
+            else issue_values(p, sm, bar, tm, w & 1);
             __syncwarp();
             tc_commit(&bar->drain, (threadIdx.x & 31) == 0);
             mbar_wait(&bar->drain, 0, p.status);  // every product has ended before the tensor memory is freed
         } else if (w < 30 && (threadIdx.x & 31) == 0) {
-            bring(p, sm, bar, w == 29, begin, end);
+            bring(p, sm, bar, w == 29);
         }
     }
     __syncwarp();
@@ -793,7 +818,7 @@ cudaError_t launch_chunk_attn(const ChunkAttnParams &p, cudaStream_t st) {
         if (dev >= 0 && dev < 64) ready[dev] = true;
     }
     if ((e = launch_dependent(chunk_attn_kernel, dim3((unsigned)p.C), kThreads, kSmemBytes, st, p)) != cudaSuccess) return e;
-    return launch_chunk_combine(p, st);
+    return p.cut ? launch_chunk_combine(p, st) : cudaSuccess;
 }
 
 }  // namespace kvq

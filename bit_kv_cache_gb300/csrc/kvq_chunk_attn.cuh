@@ -52,21 +52,21 @@ __device__ __forceinline__ Item make_item(const ChunkAttnParams &p, int b) {
     return r;
 }
 
-__device__ __forceinline__ Item find_item(const ChunkAttnParams &p, int pos) {
+// The unit at a position, given one of the same slot and head at or before it (first
+// position, row tile), or any before.
+__device__ __forceinline__ Item find_item(const ChunkAttnParams &p, int pos, int first, int tile) {
     Item r = make_item(p, slot_of(p, pos));
     const int per = (p.cost0[r.b + 1] - p.cost0[r.b]) / p.H_kv;  // cost of one head
-    int x = pos - p.cost0[r.b];
-    r.h = x / per;
-    x -= r.h * per;
-    int t = 0, a = 0;
-    for (;; t++) {
-        r.n = chunk_tiles(r.s, t, r.rows, p.g);
-        const int c = (r.n + kUnitItems) * r.w;
-        if (x < a + c) break;
-        a += c;
+    r.h = (pos - p.cost0[r.b]) / per;
+    const int head = p.cost0[r.b] + r.h * per;
+    const bool near = first > head;
+    r.t = near ? tile : 0;
+    r.first = near ? first : head;
+    for (;; r.t++) {
+        r.n = chunk_tiles(r.s, r.t, r.rows, p.g);
+        if (pos < r.end()) break;
+        r.first = r.end();
     }
-    r.t = t;
-    r.first = p.cost0[r.b] + r.h * per + a;
     return r;
 }
 
@@ -81,10 +81,7 @@ __device__ __forceinline__ const uint16_t *tail_row(const ChunkAttnParams &p, co
                  : p.k_new + (int64_t)(it.s.cu + x) * p.k_stride + it.h * kD;
 }
 
-// The page-table entry of a key tile, and the page index it stands for.
-__device__ __forceinline__ int32_t page_entry(const ChunkAttnParams &p, const Item &it, int tile) {
-    return p.ptab[(size_t)it.b * p.ptab_stride + (int64_t)tile * kChunkKeys / p.G];
-}
+// The page index that a page-table entry stands for.
 __device__ __forceinline__ int64_t page_index(const ChunkAttnParams &p, const Item &it, int32_t entry) {
     if (entry < 0 || entry >= p.n_pages) {
         report(p.status, KVQ_DEV_BAD_STATE);
