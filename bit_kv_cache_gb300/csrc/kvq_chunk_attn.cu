@@ -13,12 +13,15 @@
 // What bounds it.  Wide units: the tensor core.  A product with M = 128 reads its operands
 // from shared memory at 128 bytes a cycle: K = 16 takes 48 cycles at N = 64, 64 at N = 128, so
 // a key tile of 256 rows takes 2478 cycles when nothing else runs.  2048 tokens of 32 heads
-// over 32868 cached ones (2-bit; 1137 GFLOP): 864 us, 1.32 PFLOP/s, 0.71 of cuBLAS' burst rate;
-// dequantization and softmax take issue slots (0.5 a cycle and scheduler) and shared memory
-// beside it.  Narrow units: the chain scores - softmax - product of a key tile, whose links
-// wait for warps that share their schedulers with the producers; 2300 cycles a tile, of which
-// products need 1024.  Eight slots of 17K to 56K tokens with 1 to 8 new ones: 147 us, where
-// the packed bytes take 24.
+// over 32868 cached ones (2-bit; 1137 GFLOP): 847 us, 1.34 PFLOP/s, 0.72 of the measured rate
+// of a large library product; dequantization and softmax take issue slots and shared memory
+// beside it.  Narrow units: issue slots.  Eight slots of 17K to 56K tokens with 1 to 8 new ones
+// take 148 us, where their packed bytes take 24: 0.61 instructions a cycle and scheduler, the
+// ALU half busy (5600 warp instructions per key tile: one AND and two fused products per two
+// codes, the stores of the fp16 tiles, the softmax, waits), the tensor core 0.44.
+// Tried there and dropped: both groups of a side on one tile (162 us; 77 us against 84 with
+// 8-bit codes, but 911 us in the case above), barriers per half tile (164 us), an early start
+// of the kernel behind (166 us).
 //
 // One CTA per SM, eight groups of four warps:
 //   groups 0, 1  softmax, a thread per row of 128: reads the scores S_m from tensor memory,
