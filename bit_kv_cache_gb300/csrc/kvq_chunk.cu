@@ -126,7 +126,11 @@ cudaError_t launch_plan(const PlanParams &p, cudaStream_t st) {
 // Extend.  The tokens that a slot packs are the stream [residual | chunk behind the sink];
 // page j of the call holds its tokens j G .. j G + G - 1.  One CTA per (page, head, keys or
 // 128 value tokens) gathers its rows from the two places and quantizes them as the prefill
-// kernels do (kvq_quantizer.cuh), so codes and scales are theirs bit for bit.
+// kernels do (kvq_quantizer.cuh), so codes and scales are theirs bit for bit.  Few pages are
+// bound by their dependent reads (plan, rows; a page-table entry only at the end): 13 us for
+// a chunk of 2048 tokens of 8 heads; many by the quantizer's instructions: four prompts of
+// 2K to 12K tokens, 237 MB in two calls, take 69 us (3.4 TB/s).  The slots of the pages come
+// as a parameter (found from the plan's arrays: 71 us).
 // ------------------------------------------------------------------------------
 struct PageJob {
     ChunkSlot s;
@@ -143,27 +147,22 @@ struct PageJob {
     }
 };
 
-// The slot of page i of the call: the number of slots whose pages all come before it.
+// Page i of the call; its slot is the first one whose pages end behind it.
 __device__ __forceinline__ PageJob find_page(const ExtendParams &p, int i) {
-    const int4 *d = reinterpret_cast<const int4 *>(p.desc);
-    int b = 0;
-    for (int k = 0; k < p.B; k += blockDim.x) {
-        const int c = k + threadIdx.x;
-        bool before = false;
-        if (c < p.B) {
-            const int4 x = d[2 * c + 1];
-            before = x.w + x.z / p.G <= i;
-        }
-        b += __syncthreads_count(before);
+    int lo = 0, hi = p.B - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (p.page0[mid + 1] > i) hi = mid;
+        else lo = mid + 1;
     }
-    b = min(b, p.B - 1);
-    const int4 x = d[2 * b], y = d[2 * b + 1];
+    const int4 *d = reinterpret_cast<const int4 *>(p.desc) + 2 * lo;
+    const int4 x = d[0], y = d[1];
     PageJob j;
     j.s = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-    j.b = b;
-    const int k = i - y.w;
+    j.b = lo;
+    const int k = i - p.page0[lo];
     j.t0 = k * p.G;
-    j.entry = p.ptab[(size_t)b * p.ptab_stride + x.y / p.G + k];
+    j.entry = p.ptab[(size_t)lo * p.ptab_stride + x.y / p.G + k];
     return j;
 }
 
@@ -385,38 +384,39 @@ __device__ __forceinline__ void extend_slot(const ExtendParams &p, int b, int h,
         reinterpret_cast<int4 *>(p.lens)[b] = make_int4(x.x + y.y, x.y + y.z, x.z + x.w - y.y - y.z, 1);
 }
 
-// Page blockIdx.x of the call (G = 8 TPW tokens), or, behind them, a slot's fp16 rows.
+// Page blockIdx.x of the call (G = 8 TPW tokens), or, behind them, a slot's fp16 rows.  The
+// values, whose CTAs take longer, come first (four prompts of 2K to 12K tokens: 70 us against 71).
 template <int TPW>
-__global__ void __launch_bounds__(256, TPW == 16 ? 4 : 2) extend_pack_kernel(const ExtendParams p, int kbits, int vbits) {
+__global__ void __launch_bounds__(256, TPW == 16 ? 4 : 2) extend_pack_kernel(const __grid_constant__ ExtendParams p, int kbits, int vbits) {
     __shared__ __align__(16) unsigned char smem[32 * 512 + 512];
     __shared__ int s_first;  // the slot, if this is its first page
-    const int h = blockIdx.y;
+    const int h = blockIdx.y, side = gridDim.z - 1 - blockIdx.z;  // 0: keys, 1 + i: values 128 i ..
     griddep_wait();
     if (blockIdx.x >= p.n_pack) {
-        extend_slot(p, blockIdx.x - p.n_pack, h, blockIdx.z, 0, 1);
+        extend_slot(p, blockIdx.x - p.n_pack, h, side, 0, 1);
         return;
     }
     const PageJob jb = find_page(p, blockIdx.x);
     if (threadIdx.x == 0) s_first = jb.t0 == 0 ? jb.b : -1;
-    if (blockIdx.z == 0) {
+    if (side == 0) {
         if (kbits == 2) extend_keys<2, TPW>(p, jb, h, smem);
         else if (kbits == 4) extend_keys<4, TPW>(p, jb, h, smem);
         else extend_keys<8, TPW>(p, jb, h, smem);
     } else {
-        const int vb = blockIdx.z - 1;
+        const int vb = side - 1;
         if (vbits == 2) extend_values<2>(p, jb, h, vb, smem);
         else if (vbits == 4) extend_values<4>(p, jb, h, vb, smem);
         else extend_values<8>(p, jb, h, vb, smem);
     }
     if (TPW == 16 && extend_once(p) && s_first >= 0) {  // every thread has read its rows (a barrier inside the packing)
         const int4 *d = reinterpret_cast<const int4 *>(p.desc) + 2 * s_first;
-        keep_rows(p, d[0], d[1], s_first, h, blockIdx.z, false, true, threadIdx.x, 256);
+        keep_rows(p, d[0], d[1], s_first, h, side, false, true, threadIdx.x, 256);
     }
 }
 
 // Every slot's fp16 rows: after the pages, which read the old residual rows.
 constexpr int kTailSlices = 4;
-__global__ void __launch_bounds__(256) extend_tail_kernel(const ExtendParams p) {
+__global__ void __launch_bounds__(256) extend_tail_kernel(const __grid_constant__ ExtendParams p) {
     griddep_wait();
     extend_slot(p, blockIdx.x, blockIdx.y >> 1, blockIdx.y & 1, blockIdx.z, kTailSlices);
 }
@@ -915,7 +915,11 @@ int kvq_paged_extend(const kvq_config *c, kvq_paged *pc, const kvq_chunk *ch, co
     p.R = c->R;
     p.TV = vtile_of(c);
     p.ptab_stride = (int)(c->max_T / c->G);
-    for (int b = 0; b < c->B; b++) p.n_pack += slots_of(ch)[b].pk / c->G;
+    for (int b = 0; b < c->B; b++) {
+        p.page0[b] = p.n_pack;
+        p.n_pack += slots_of(ch)[b].pk / c->G;
+    }
+    p.page0[c->B] = p.n_pack;
     if (p.n_pack > 0 && pc->n_pages < 1) return KVQ_ERR_CAPACITY;
     if (launch_extend(p, c->bits, vbits_of(c), st) != cudaSuccess) return KVQ_ERR_CUDA;
     for (int b = 0; b < c->B; b++) {

@@ -35,6 +35,7 @@ struct ExtendParams {
     int64_t n_pages;
     int B, H_kv, G, S, R, TV, ptab_stride;
     int n_pack;                          // pages to pack, over all slots
+    int32_t page0[KVQ_PAGED_MAX_B + 1];  // of the slots before each
 };
 
 struct QkParams {
