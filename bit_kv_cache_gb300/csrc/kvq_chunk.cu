@@ -130,7 +130,7 @@ cudaError_t launch_plan(const PlanParams &p, cudaStream_t st) {
 // bound by their dependent reads (plan, rows; a page-table entry only at the end): 13 us for
 // a chunk of 2048 tokens of 8 heads; many by the quantizer's instructions: four prompts of
 // 2K to 12K tokens, 237 MB in two calls, take 69 us (3.4 TB/s).  The slots of the pages come
-// as a parameter (found from the plan's arrays: 71 us).
+// as a parameter (found from the plan's arrays: 70 us).
 // ------------------------------------------------------------------------------
 struct PageJob {
     ChunkSlot s;

@@ -429,6 +429,34 @@ def test_row_counts(rows):
     attn_check(c, new, q, k, v, c.chunk_attn(c.plan(new), q, k, v))
 
 
+RANGES = {
+    "whole": dict(lens=[300], new=[4]),
+    "parts_of_two": dict(lens=[2000], new=[4]),
+    "parts_and_whole": dict(lens=[3000, 0, 250], new=[2, 0, 5]),
+    "short_slots": dict(lens=[300, 900, 100, 500], new=[1, 1, 1, 1]),
+    "wide": dict(lens=[0], new=[200]),
+    "wide_and_narrow": dict(lens=[2100, 40, 700], new=[301, 3, 20]),
+    "long_units": dict(lens=[9000, 40], new=[3, 1]),
+    "a_unit_per_range": dict(lens=[200] * 19, new=[1] * 19),
+    "more_units": dict(lens=[200] * 20, new=[1] * 20),
+}
+
+
+@pytest.mark.parametrize("name", RANGES)
+def test_ranges(name):
+    """Units whole, in parts of their own, and cut evenly: the attention, and that a second call
+    gives the same bits."""
+    rng = np.random.default_rng(len(name))
+    case = RANGES[name]
+    c = make_cache(rng, case["lens"], H_q=16, H_kv=8, max_T=16384)
+    q, k, v = chunk_inputs(rng, c, sum(case["new"]))
+    ch = c.plan(case["new"])
+    out = c.chunk_attn(ch, q, k, v)
+    attn_check(c, case["new"], q, k, v, out, name)
+    assert torch.equal(out, c.chunk_attn(ch, q, k, v))
+    assert c.read_status() == 0
+
+
 def test_out_may_not_overlap():
     import bit_kv_cache_gb300 as kvq
     rng = np.random.default_rng(14)
