@@ -120,7 +120,7 @@ def decode_bytes_struct(wl, st) -> int:
 DECODE_SOURCES = ("kvq_decode.cu", "kvq_decode.cuh", "kvq_decode_fast.cuh", "kvq_device.cuh", "kvq_internal.h",
                   "kvq_api.cu", "kvq_host.h", "kvq_paged.cu", "kvq_decode_paged.cu", "kvq_decode_rope.cu",
                   "kvq_decode_nvfp4.cu")
-QUANT_SOURCES = ("kvq_quant.cu", "kvq_device.cuh", "kvq_internal.h", "kvq_api.cu", "kvq_host.h")
+QUANT_SOURCES = ("kvq_quant.cu", "kvq_quantizer.cuh", "kvq_device.cuh", "kvq_internal.h", "kvq_api.cu", "kvq_host.h")
 
 
 def kernel_hash(sources=DECODE_SOURCES) -> str:
