@@ -618,6 +618,37 @@ bool overlap(const void *a, size_t na, const void *b, size_t nb) {
     return x < y + nb && y < x + na;
 }
 
+// A positive number m 2^(e - 64), 2^63 <= m.
+struct Mantissa {
+    uint64_t m;
+    int e;
+};
+Mantissa mantissa(double x) {
+    int e;
+    const double f = frexp(x, &e);
+    return {(uint64_t)ldexp(f, 64), e};
+}
+Mantissa operator*(Mantissa a, Mantissa b) {
+    unsigned __int128 p = (unsigned __int128)a.m * b.m;
+    int e = a.e + b.e;
+    if (!(p >> 127)) p <<= 1, e--;
+    return {(uint64_t)(p >> 64), e};
+}
+
+// base^(-1/m) for base > 1 in units of 2^-64, off by a few of them: the double root y and one
+// Newton step, y (1 - (y^m base - 1) / m), whose residual is formed with 64-bit mantissas
+// (a long double power, emulated in software on Arm, took 1.2 us more of the call's 11).
+uint64_t inverse_root(double base, int m) {
+    const Mantissa y = mantissa(std::min(pow(base, -1.0 / m), 1.0 - 0x1p-53));
+    Mantissa z = mantissa(base), sq = y;
+    for (int i = m; i; i >>= 1, sq = sq * sq)
+        if (i & 1) z = z * sq;
+    // z = 1 + d 2^-64
+    const int64_t d = z.e == 1 ? (int64_t)((z.m - (1ull << 63)) << 1) : (int64_t)z.m;
+    const uint64_t f = y.m >> -y.e;
+    return f - (uint64_t)(int64_t)((double)f * ((double)d * 0x1p-64) / m);
+}
+
 // Partials of the attention: two segments' ends per CTA.
 struct ChunkWs {
     size_t ml, o, total;
@@ -987,15 +1018,15 @@ int kvq_qk_norm_rope(const kvq_qk_config *c, const uint16_t *q, const uint16_t *
     p.halves = c->halves;
     p.rotate = c->rotary_dim ? c->rotate : 0;
     p.eps = c->eps;
-    const long double base = c->rope_base > 0.f ? (long double)c->rope_base : 10000.0L;
-    // turn[j] = base^(-2j/n) / (2 pi) in 64-bit fixed point: one power, then integer products
+    const double base = c->rope_base > 0.f ? (double)c->rope_base : 10000.0;
+    // turn[j] = base^(-2j/n) / (2 pi) in 64-bit fixed point: one root, then integer products
     // (a call's host time is a small part of that of a power per pair), each off by 2^-64 at most
-    const long double step = c->rotary_dim ? powl(base, -2.0L / c->rotary_dim) : 0.0L;
-    if (step < 1.0L) {
-        const uint64_t f = (uint64_t)ldexpl(step, 64);
+    if (c->rotary_dim && base > 1.0) {
+        const uint64_t f = inverse_root(base, c->rotary_dim / 2);
         uint64_t turn = 0x28be60db9391054aull;  // 2^64 / (2 pi)
         for (int j = 0; j < c->rotary_dim / 2; j++, turn = (uint64_t)(((unsigned __int128)turn * f) >> 64)) p.turn[j] = turn;
-    } else {
+    } else if (c->rotary_dim) {
+        const long double step = powl((long double)base, -2.0L / c->rotary_dim);
         long double turn = 0.159154943091895335768883763372514362L;
         for (int j = 0; j < c->rotary_dim / 2; j++, turn *= step) p.turn[j] = (uint64_t)ldexpl(turn - floorl(turn), 64);
     }
