@@ -58,11 +58,11 @@ constexpr int kNarrowRows = 128, kWideRows = 256, kNarrowCost = 3, kWideCost = 4
 // item's (kNarrowCost, kWideCost: a tile took 1.5 and 2.0 us) and, before a unit's first item,
 // that of kUnitItems more (the start and the end of a unit).  Measured: a chunk of 517 tokens
 // beside three decoding slots 131, 110, 98, 99 us with 0, 3, 5, 8 of them; a 2048-token chunk
-// 915 us with equal costs of the items against 865, eight decoding slots 152 against 147.  All units, slot-major, then by
-// head and row tile, are cut into C ranges, one per CTA: of equal cost, or, of few units, parts
-// of one unit each.  A unit inside one
-// range is finished there; of one that is cut, each range leaves fp32 partials, and the
-// combine kernels join them in range order.
+// 915 us with equal costs of the items against 865, eight decoding slots 152 against 147.  All
+// units, slot-major, then by head and row tile, are cut into C ranges, one per CTA: of equal
+// cost, or, of few units, parts of one unit each.  A unit inside one range is finished there;
+// of one that is cut, each range leaves fp32 partials, which the combine kernel joins in range
+// order.
 struct ChunkAttnParams {
     const int32_t *desc;
     const int32_t *ptab;
