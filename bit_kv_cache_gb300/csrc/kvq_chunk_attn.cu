@@ -42,7 +42,7 @@
 // that is cut holds them twice (four times) in its query tile, and each copy's softmax takes
 // half (a quarter) of a tile's keys: the tensor core's rows cost nothing, and a step of the
 // softmax, which is what such a unit waits for, is as much shorter (the eight slots above:
-// 171 us against 190 without, when this came in).  The combine kernel joins the copies' partials like those of
+// 148 us against 187 without).  The combine kernel joins the copies' partials like those of
 // the ranges.
 // A step is half a key tile (64 keys).  S_m has two buffers of 64 columns, so that the scores
 // of the next step are made while the softmax of this one runs.  Tensor memory: S_0, S_1,
