@@ -491,9 +491,11 @@ __global__ void __launch_bounds__(256) qk_kernel(const __grid_constant__ QkParam
         }
     };
     // (x, y) -> f (x xx + y xy, x yx + y yy), f the norm's factor: the weights are folded into
-    // sine and cosine
+    // sine and cosine.  Channels that do not rotate take no part of their neighbours, which may
+    // be infinite or NaN
     uint64_t xx[2], xy[2], yx[2], yy[2];
     int side = -1;
+    bool turn = false;
     for (int h = first; __any_sync(0xffffffffu, h < h1); h += kQkRows * PER) {
 #pragma unroll
         for (int r = 0; r < kQkRows; r++) {
@@ -507,7 +509,7 @@ __global__ void __launch_bounds__(256) qk_kernel(const __grid_constant__ QkParam
                     const uint2 u[2] = {__ldg(reinterpret_cast<const uint2 *>(wt + c0)), __ldg(reinterpret_cast<const uint2 *>(wt + c1))};
                     pairs(u, w0, w1);
                 }
-                const bool turn = (HALVES ? split : c0 < p.rotary) && (p.rotate & (key ? 2 : 1));
+                turn = (HALVES ? split : c0 < p.rotary) && (p.rotate & (key ? 2 : 1));
 #pragma unroll
                 for (int e = 0; e < 2; e++) {
                     const int j = (HALVES ? c0 : c0 >> 1) + 2 * e;
@@ -529,8 +531,9 @@ __global__ void __launch_bounds__(256) qk_kernel(const __grid_constant__ QkParam
             const uint64_t f2 = pk2(f, f);
 #pragma unroll
             for (int e = 0; e < 2; e++) {
-                const float2 a = up2(mul_x2(f2, fma_x2(X[e], xx[e], mul_x2(Y[e], xy[e]))));
-                const float2 b = up2(mul_x2(f2, fma_x2(X[e], yx[e], mul_x2(Y[e], yy[e]))));
+                const uint64_t x0 = turn ? fma_x2(X[e], xx[e], mul_x2(Y[e], xy[e])) : mul_x2(X[e], xx[e]);
+                const uint64_t y0 = turn ? fma_x2(X[e], yx[e], mul_x2(Y[e], yy[e])) : mul_x2(Y[e], yy[e]);
+                const float2 a = up2(mul_x2(f2, x0)), b = up2(mul_x2(f2, y0));
                 x[2 * e] = a.x, x[2 * e + 1] = a.y, y[2 * e] = b.x, y[2 * e + 1] = b.y;
             }
             if (hh < h1) {

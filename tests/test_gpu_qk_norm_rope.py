@@ -153,3 +153,36 @@ def test_refusals():
     big = torch.zeros(4, 4, 128, device=DEV).half()
     with pytest.raises(kvq.KvqError):  # an output inside a strided input
         kvq.qk_norm_rope(big[:, :2], pos=pos, out=(big.view(-1)[: 4 * 2 * 128].view(4, 2, 128), None))
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("halves", [False, True])
+@pytest.mark.parametrize("rd", [0, 32, None])
+@pytest.mark.parametrize("norm", [False, True])
+def test_channels_that_do_not_rotate_stay_apart(D, halves, rd, norm):
+    """An infinite or NaN channel behind rotary_dim, or of rows that do not rotate, reaches no
+    other channel but through the norm; without a norm those rows pass through bit for bit."""
+    import bit_kv_cache_gb300 as kvq
+    g = torch.Generator(device=DEV).manual_seed(D)
+    n, H = 12, 3
+    q = torch.randn(n, H, D, generator=g, device=DEV).half()
+    k = torch.randn(n, H, D, generator=g, device=DEV).half()
+    bad = [float("inf"), float("-inf")] + ([] if norm else [float("nan")])
+    for i in range(n):
+        q[i, i % H, D - 1 - i % 3] = bad[i % len(bad)]  # rd <= 32 < D - 3
+        k[i, (i + 1) % H, 5 * i % D] = bad[i % len(bad)]
+    w = torch.randn(D, generator=g, device=DEV).half() if norm else None
+    pos = torch.randint(1, 1000, (n,), generator=g, device=DEV, dtype=torch.int32)
+    rotate_q = rd is not None
+    qo, ko = kvq.qk_norm_rope(q, k, w, w, pos, rotary_dim=rd, halves=halves, rotate_q=rotate_q, rotate_k=False)
+    for got, x, rotate in ((qo, q, rotate_q), (ko, k, False)):
+        ref, mag = reference(x, w, pos, 10000.0, D if rd is None else rd, halves, rotate, 1e-6)
+        got = got.double().cpu()
+        assert torch.equal(torch.isnan(got), torch.isnan(ref))
+        fin = torch.isfinite(ref)
+        assert torch.equal(got[~fin & ~torch.isnan(ref)], ref[~fin & ~torch.isnan(ref)])
+        tol = 2.0 ** -11 * ref.abs() + 2.0 ** -25 + mag * (D * 2.0 ** -25 + 8 * 2.0 ** -24 + np.pi * 2.0 ** -24)
+        assert torch.all((got - ref).abs()[fin] <= tol[fin])
+        if not norm:
+            first = (rd or 0) if rotate else 0
+            assert torch.equal(got[..., first:].nan_to_num(7.0), x[..., first:].double().cpu().nan_to_num(7.0))
