@@ -72,7 +72,7 @@ struct ChunkAttnParams {
     const uint16_t *q, *k_new, *v_new;
     uint16_t *out;
     float *part_o;                       // [2 C][kWideRows][128]
-    float2 *part_ml;                     // [2 C][kWideRows] (max, sum)
+    float2 *part_ml;                     // [2 C][kWideRows] (reference: a score before the scale, sum)
     int32_t *status;
     int64_t q_stride, k_stride, v_stride, n_pages;
     int B, H_kv, g, G, kbits, vbits, S, R, ptab_stride;

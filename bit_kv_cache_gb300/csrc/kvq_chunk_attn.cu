@@ -65,11 +65,16 @@ constexpr int kRawBytes = 4 * (8192 + 512);              // packed tiles: codes 
 constexpr int kMaxRaw = 4;
 constexpr int kOffQ = 0, kOffK = 2 * kTileBytes, kOffV = kOffK + kRing * kTileBytes, kOffRaw = kOffV + kRing * kTileBytes,
               kOffBar = kOffRaw + kRawBytes;
-constexpr float kScale = kLog2e * 0.08838834764831845f;  // log2(e) / sqrt(128)
-// Weights are 2^(s - m + kUp) with a reference m that may lag behind the maximum while 64
-// weights sum to kMostSum at most, below fp16's 65504; kUp more bits keep small weights
-// above fp16's smallest step.
-constexpr float kUp = 6.f, kMostSum = 16384.f;
+// Weights are 2^((x - r) kScale + kUp) of scores x = q . k, with a reference r (one of the row's
+// scores) that may lag behind the maximum while 64 weights sum to kMostSum at most, below
+// fp16's 65504; kUp more bits keep small weights above fp16's smallest step.  With |r| of at
+// most kNear the exponent is one fused product, x kScale + (kUp - r kScale), whose constant is
+// off by 2^-15 at most; beyond it (362 in units of the softmax's exponent) x - r, which is
+// exact where it matters, is formed first in every step, as scaled values of 2^28 and more
+// would differ from their products by more than fp16's range has room for.  (A 2048-token
+// chunk: 871 us against 862 with scaled references alone.  The weights of such rows as a
+// branch of their own, or one body of code for both: 900 to 940, the hot code grows or stalls.)
+constexpr float kUp = 6.f, kMostSum = 16384.f, kNear = 4096.f;
 // registers of a thread after the split; 64 at launch, times 1024 threads
 constexpr int kRegsSoftmax = 112, kRegsTiles = 48, kRegsOther = 48;
 static_assert(256 * kRegsSoftmax + 512 * kRegsTiles + 256 * kRegsOther <= kThreads * 64, "register split");
@@ -483,15 +488,22 @@ __device__ __forceinline__ float max_of(const float *f) {
     for (int e = 0; e < 8; e++) t[e] = fmaxf(t[e], f[N - 8 + e]);
     return fmaxf(max3(t[0], t[1], t[2]), max3(max3(t[3], t[4], t[5]), t[6], t[7]));
 }
-// Weights 2^(s scale + off) of N scores, as N / 2 half2 in place; returns their sum.
-template <int N>
-__device__ __forceinline__ float weights(uint32_t *x, float off) {
+// Weights of N scores to reference r, as N / 2 half2 in place; returns their sum.  FAR: r may
+// be beyond kNear.
+template <int N, bool FAR>
+__device__ __forceinline__ float weights(uint32_t *x, float r) {
     uint64_t l0 = 0, l1 = 0;
-    const uint64_t sc2 = pair_of(kScale, kScale), of2 = pair_of(off, off);
+    const float off = FAR ? kUp : __fmaf_rn(-r, kScale, kUp);
+    const uint64_t sc2 = pair_of(kScale, kScale), of2 = pair_of(off, off), nr2 = pair_of(-r, -r);
     const float *f = reinterpret_cast<const float *>(x);
+    auto exponents = [&](float x0, float x1) {
+        uint64_t y = pair_of(x0, x1);
+        if (FAR) y = add_pair(y, nr2);
+        return of_pair(fma_pair(y, sc2, of2));
+    };
 #pragma unroll
     for (int c = 0; c < N; c += 4) {
-        float2 a = of_pair(fma_pair(pair_of(f[c], f[c + 1]), sc2, of2)), b = of_pair(fma_pair(pair_of(f[c + 2], f[c + 3]), sc2, of2));
+        float2 a = exponents(f[c], f[c + 1]), b = exponents(f[c + 2], f[c + 3]);
         a.x = ex2(a.x);
         a.y = ex2(a.y);
         b.x = ex2(b.x);
@@ -508,8 +520,12 @@ __device__ __forceinline__ float weights(uint32_t *x, float off) {
 // Parities of a softmax group's barriers and the row's state.
 struct RowState {
     uint32_t ns, given, no1;  // per buffer h: parity of the weights given, any given; narrow units joined
-    float mx, l;
+    float r, l;               // reference (-inf: none yet), sum of the weights
 };
+// Whether weights of this sum, formed with a near reference, stand; the reference that weights
+// are formed with in any case.
+__device__ __forceinline__ bool stands(float sum, float r) { return sum <= kMostSum && fabsf(r) <= kNear; }
+__device__ __forceinline__ float some_ref(float r) { return r == -INFINITY ? 0.f : r; }
 
 // N scores from column ts on, those of unseen keys (from the y-th on) as -inf.
 template <int N>
@@ -524,7 +540,7 @@ __device__ __forceinline__ void load_scores(uint32_t *x, uint32_t ts, int y) {
 
 // The steps of one segment for query tile or key parity m; narrow units: every second key
 // tile.  ts, to: tensor memory of S_m and O_m; lim: fp16 tokens the row may see; any: whether
-// the warp has rows at all.  The weights are formed with a reference mx that some earlier
+// the warp has rows at all.  The weights are formed with a reference r that some earlier
 // step's maximum gave: their sum tells whether one of them may be too large for fp16, and
 // only then the maximum is looked for and the weights are formed again (a maximum in every
 // step: 1253 us against 1175).
@@ -532,7 +548,7 @@ template <bool NARROW>
 __device__ __forceinline__ void softmax_steps(const ChunkAttnParams &p, Bars *bar, const Seg &s, RowState &st, uint32_t ts, uint32_t to,
                                               int m, int lim, bool any) {
     const int steps = NARROW ? 2 * ((s.k1 - s.k0 - m + 1) >> 1) : s.steps;
-    float mx = -INFINITY, l = 0.f;
+    float r = -INFINITY, l = 0.f;
     for (int i = 0; i < steps; i++) {
         const int h = i & 1, kt = s.k0 + (NARROW ? 2 * (i >> 1) + m : i >> 1);
         warp_await(&bar->s_full[m][h], (st.ns >> h) & 1, &bar->stop, p.status);
@@ -541,13 +557,13 @@ __device__ __forceinline__ void softmax_steps(const ChunkAttnParams &p, Bars *ba
             const int y = kt >= s.np ? lim - (kt - s.np) * kChunkKeys - 64 * h : 64;  // keys it may see
             uint32_t x[64];
             load_scores<64>(x, ts + 64 * h, y);
-            float add = weights<64>(x, kUp - mx);                  // infinite or NaN without a reference
-            if (__any_sync(0xffffffffu, !(add <= kMostSum))) {
+            float add = weights<64, false>(x, r);  // infinite or NaN without a reference
+            if (__any_sync(0xffffffffu, !stands(add, r))) {
                 load_scores<64>(x, ts + 64 * h, y);
-                const float cand = max_of<64>(reinterpret_cast<const float *>(x)) * kScale;
-                const bool grow = cand > mx;
-                const float corr = grow ? ex2(mx - cand) : 1.f;
-                if (grow) mx = cand;
+                const float cand = max_of<64>(reinterpret_cast<const float *>(x));
+                const bool grow = cand > r;
+                const float corr = grow ? ex2((r - cand) * kScale) : 1.f;
+                if (grow) r = cand;
                 l *= corr;
                 if (i > 0) {
                     // the step before was the last to write O
@@ -564,7 +580,7 @@ __device__ __forceinline__ void softmax_steps(const ChunkAttnParams &p, Bars *ba
                     }
                 }
                 if (i > 0) load_scores<64>(x, ts + 64 * h, y);
-                add = weights<64>(x, kUp - (mx == -INFINITY ? 0.f : mx));
+                add = weights<64, true>(x, some_ref(r));
             }
             tmem_st32(ts + 64 * h, x);  // over the scores
             l += add;
@@ -577,7 +593,7 @@ __device__ __forceinline__ void softmax_steps(const ChunkAttnParams &p, Bars *ba
         st.ns ^= 1u << h;
         st.given |= 1u << h;
     }
-    st.mx = mx;
+    st.r = r;
     st.l = l;
 }
 
@@ -587,7 +603,7 @@ template <int REP>
 __device__ __forceinline__ void softmax_tiles(const ChunkAttnParams &p, Bars *bar, const Seg &s, RowState &st, uint32_t ts, uint32_t to,
                                               int m, int lim, int c) {
     constexpr int KEYS = 128 / REP;
-    float mx = -INFINITY, l = 0.f;
+    float r = -INFINITY, l = 0.f;
     for (int kt = s.k0 + m; kt < s.k1; kt += 2) {
         warp_await(&bar->s_full[m][0], st.ns & 1, &bar->stop, p.status);
         warp_await(&bar->s_full[m][1], (st.ns >> 1) & 1, &bar->stop, p.status);
@@ -595,13 +611,13 @@ __device__ __forceinline__ void softmax_tiles(const ChunkAttnParams &p, Bars *ba
         const int y = kt >= s.np ? lim - (kt - s.np) * kChunkKeys - KEYS * c : KEYS;  // keys it may see
         uint32_t x[KEYS];
         load_scores<KEYS>(x, ts + KEYS * c, y);
-        float add = weights<KEYS>(x, kUp - mx);                  // infinite or NaN without a reference
-        if (__any_sync(0xffffffffu, !(add <= kMostSum))) {
+        float add = weights<KEYS, false>(x, r);  // infinite or NaN without a reference
+        if (__any_sync(0xffffffffu, !stands(add, r))) {
             load_scores<KEYS>(x, ts + KEYS * c, y);
-            const float cand = max_of<KEYS>(reinterpret_cast<const float *>(x)) * kScale;
-            const bool grow = cand > mx;
-            const float corr = grow ? ex2(mx - cand) : 1.f;
-            if (grow) mx = cand;
+            const float cand = max_of<KEYS>(reinterpret_cast<const float *>(x));
+            const bool grow = cand > r;
+            const float corr = grow ? ex2((r - cand) * kScale) : 1.f;
+            if (grow) r = cand;
             l *= corr;
             if (kt > s.k0 + m) {  // the products before these scores have ended
 #pragma unroll 1
@@ -615,7 +631,7 @@ __device__ __forceinline__ void softmax_tiles(const ChunkAttnParams &p, Bars *ba
                 }
                 load_scores<KEYS>(x, ts + KEYS * c, y);
             }
-            add = weights<KEYS>(x, kUp - (mx == -INFINITY ? 0.f : mx));
+            add = weights<KEYS, true>(x, some_ref(r));
         }
         l += add;
         // weights of keys 64 h .. at columns 64 h .., two to a column
@@ -636,7 +652,7 @@ __device__ __forceinline__ void softmax_tiles(const ChunkAttnParams &p, Bars *ba
         st.ns ^= 3;
         st.given = 3;
     }
-    st.mx = mx;
+    st.r = r;
     st.l = l;
 }
 
@@ -660,7 +676,7 @@ __device__ __forceinline__ void softmax(const ChunkAttnParams &p, Bars *bar, uin
         else if (s.rep == 2) softmax_tiles<2>(p, bar, s, st, ts, to, m, lim, lane_row >> 6);
         else if (s.narrow) softmax_steps<true>(p, bar, s, st, ts, to, m, lim, any);
         else softmax_steps<false>(p, bar, s, st, ts, to, m, lim, any);
-        float mx = st.mx, l = st.l;
+        float ref = st.r, l = st.l;
         for (int h = 0; h < 2; h++)  // the last products
             if ((st.given >> h) & 1) warp_await(&bar->pv_done[m][h], (~st.ns >> h) & 1, &bar->stop, p.status);
         tc_fence_after();
@@ -671,7 +687,7 @@ __device__ __forceinline__ void softmax(const ChunkAttnParams &p, Bars *bar, uin
             float2 *state1 = p.part_ml + slot0;
             st.no1++;
             if (m == 1) {
-                state1[lane_row] = make_float2(mx, l);
+                state1[lane_row] = make_float2(ref, l);
                 tc_fence_before();
                 mbar_arrive(&bar->o1_full);
                 continue;
@@ -679,10 +695,10 @@ __device__ __forceinline__ void softmax(const ChunkAttnParams &p, Bars *bar, uin
             warp_await(&bar->o1_full, (st.no1 - 1) & 1, &bar->stop, p.status);
             tc_fence_after();
             const float2 other = state1[lane_row];
-            const float mn = fmaxf(mx, other.x);
-            a0 = mx == mn ? 1.f : ex2(mx - mn);
-            a1 = other.x == mn ? 1.f : ex2(other.x - mn);
-            mx = mn;
+            const float top = fmaxf(ref, other.x);
+            a0 = ref == top ? 1.f : ex2((ref - top) * kScale);
+            a1 = other.x == top ? 1.f : ex2((other.x - top) * kScale);
+            ref = top;
             l = a0 * l + a1 * other.y;
         }
         const bool whole = s.k0 == 0 && s.k1 == s.it.n;
@@ -692,7 +708,7 @@ __device__ __forceinline__ void softmax(const ChunkAttnParams &p, Bars *bar, uin
         const size_t slot = slot0 + (s.rep > 1 ? lane_row : row);
         uint16_t *dst = p.out + ((int64_t)(s.it.s.cu + r / p.g) * p.H_kv * p.g + s.it.h * p.g + r % p.g) * kD;
         if (any) {
-            if (!whole && mine) p.part_ml[slot] = make_float2(mx, l);
+            if (!whole && mine) p.part_ml[slot] = make_float2(ref, l);
 #pragma unroll 1
             for (int c = 0; c < 8; c++) {
                 uint32_t o[16];

@@ -13,6 +13,7 @@ namespace kvq {
 
 constexpr int kD = 128;
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kScale = kLog2e * 0.08838834764831845f;  // log2(e) / sqrt(128)
 
 // A unit: slot, key head, row tile; its first position, number of items, the cost of each,
 // query rows.  Item 0 lies at the unit's first position, item j > 0 at first + (kUnitItems + j) w.

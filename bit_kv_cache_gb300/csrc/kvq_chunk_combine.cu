@@ -10,14 +10,14 @@ namespace kvq {
 
 namespace {
 
-// A row's state: (maximum, sum) and four channels of its output per lane.
+// A row's state: (reference, sum) and four channels of its output per lane.
 struct Part {
     float m, l;
     float4 o;
 };
 __device__ __forceinline__ void join(Part &a, const Part &b) {
     const float m = fmaxf(a.m, b.m);
-    const float x = a.m == m ? 1.f : exp2f(a.m - m), y = b.m == m ? 1.f : exp2f(b.m - m);
+    const float x = a.m == m ? 1.f : exp2f((a.m - m) * kScale), y = b.m == m ? 1.f : exp2f((b.m - m) * kScale);
     a.m = m;
     a.l = x * a.l + y * b.l;
     a.o.x = x * a.o.x + y * b.o.x;
