@@ -24,10 +24,11 @@ using namespace kvq::host;
 namespace kvq {
 namespace host {
 
+// KIVI mode on the decode tiles: D is 128 and G 128 or 256 then.
 int paged_cfg_check(const kvq_config *c) {
     const int e = kvq_config_check(c);
     if (e) return e;
-    if (kitty(c) || c->rope || !fast_supported(c) || c->B > KVQ_PAGED_MAX_B) return KVQ_ERR_UNSUPPORTED;
+    if (c->mode != KVQ_MODE_KIVI || c->rope || !fast_supported(c) || c->B > KVQ_PAGED_MAX_B) return KVQ_ERR_UNSUPPORTED;
     if (c->max_T / c->G < 1) return KVQ_ERR_INVALID_ARG;
     return KVQ_OK;
 }

@@ -185,3 +185,18 @@ def test_python_refusals(kvq):
     wide = torch.zeros(4, 6, 128, dtype=torch.float16)
     assert kvq._rows(wide[:, 2:4], 2, 128, 4, wide.device, "x") == (wide.data_ptr() + 2 * 256, 6 * 128)
     assert kvq._rows(x[:1], 2, 128, 1, x.device, "x")[1] == 256
+
+
+@pytest.mark.parametrize("G", [64, 128, 256])
+def test_nvfp4_configurations_are_unsupported(kvq, G):
+    """Paged pages hold min-max codes; the chunk kernels know pages of 128 and 256 tokens."""
+    cfg = kvq.make_config(B, H_q, H_kv, D, G, 4, 0, 256, 0, "nvfp4", 4096)
+    L = kvq.lib
+    assert L.kvq_config_check(ctypes.byref(cfg)) == 0  # a dense cache has this mode
+    assert L.kvq_paged_chunk_workspace_bytes(ctypes.byref(cfg)) == 0
+    assert L.kvq_paged_workspace_bytes(ctypes.byref(cfg)) == 0 and L.kvq_paged_bytes(ctypes.byref(cfg), 4, 0) == 0
+    f = Fake(kvq, [(0, 256, 40, 1)] * B, R=256)
+    f.cfg = cfg
+    assert f.plan([1, 1, 1, 1]) == UNSUPPORTED
+    f.planned([1, 1, 1, 1])
+    assert f.attn(wsb=1 << 40) == UNSUPPORTED and f.extend() == UNSUPPORTED
