@@ -899,6 +899,7 @@ int kvq_paged_chunk_attn(const kvq_config *c, const kvq_paged *pc, kvq_chunk *ch
             items += (int64_t)n * p.H_kv;
             units += p.H_kv;
         }
+        if (s.n_new && s.T && pc->n_pages < 1) return KVQ_ERR_INVALID_ARG;  // page 0 stands in for bad entries
         if (s.n_new && narrow) p.narrow = std::max(p.narrow, s.n_new * p.g);
         if (s.n_new && !narrow) p.wide = 1;
         cost += per * p.H_kv * (narrow ? kNarrowCost : kWideCost);

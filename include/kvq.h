@@ -494,8 +494,9 @@ size_t kvq_paged_chunk_workspace_bytes(const kvq_config *cfg);
  * fp16 (dequantized keys and values and softmax weights are rounded to it once), sums and
  * softmax statistics fp32.
  * Infinite and NaN values reach the rows that see them and no others.
- * KVQ_ERR_INVALID_ARG if the cache's lengths are not those of the plan.  The call may be
- * captured: a replay attends over the plan's lengths. */
+ * KVQ_ERR_INVALID_ARG if the cache's lengths are not those of the plan, or a slot with new
+ * tokens has packed ones and the pool no page.  The call may be captured: a replay attends
+ * over the plan's lengths. */
 int kvq_paged_chunk_attn(const kvq_config *cfg, const kvq_paged *pc, kvq_chunk *chunk, const uint16_t *q,
                          int64_t q_stride, const uint16_t *k_new, int64_t k_stride, const uint16_t *v_new,
                          int64_t v_stride, uint16_t *out, void *ws, size_t ws_bytes, void *stream);

@@ -200,3 +200,11 @@ def test_nvfp4_configurations_are_unsupported(kvq, G):
     assert f.plan([1, 1, 1, 1]) == UNSUPPORTED
     f.planned([1, 1, 1, 1])
     assert f.attn(wsb=1 << 40) == UNSUPPORTED and f.extend() == UNSUPPORTED
+
+
+def test_attention_needs_pages(kvq):
+    """Packed tokens without a page pool: there is nothing that a table entry could stand for."""
+    f = Fake(kvq, LENS)
+    f.p.n_pages = 0
+    assert f.planned([2, 3, 1, 1]).attn() == INVALID
+    assert f.planned([0, 0, 0, 1]).attn() == INVALID
