@@ -1008,8 +1008,9 @@ int kvq_qk_norm_rope(const kvq_qk_config *c, const uint16_t *q, const uint16_t *
     memset(&p, 0, sizeof(p));
     p.q = q;
     p.k = k;
-    p.w_q = w_q;
-    p.w_k = w_k;
+    // (lanes behind the last head look up a weight as well)
+    p.w_q = c->H_q ? w_q : nullptr;
+    p.w_k = c->H_kv ? w_k : nullptr;
     p.pos = pos;
     p.q_out = q_out;
     p.k_out = k_out;

@@ -532,8 +532,9 @@ typedef struct {
  * pointer is NULL), then the rotation by pos[i], in fp32 with one rounding to fp16; the
  * angles are reduced exactly (64-bit fixed point) at any position before the fp32 sine and
  * cosine.  q, k: device fp16 rows (strides above); w_q, w_k: device fp16 [D] or NULL; pos:
- * device int32 [n]; q_out, k_out: device fp16 [n][H][D], contiguous.  An output may be its own input if that is contiguous; any other
- * overlap of an output with an input or the other output is KVQ_ERR_INVALID_ARG. */
+ * device int32 [n]; q_out, k_out: device fp16 [n][H][D], contiguous.  The pointers of a side
+ * without heads are not used.  An output may be its own input if that is contiguous; any
+ * other overlap of an output with an input or the other output is KVQ_ERR_INVALID_ARG. */
 int kvq_qk_norm_rope(const kvq_qk_config *c, const uint16_t *q, const uint16_t *k, const uint16_t *w_q,
                      const uint16_t *w_k, const int32_t *pos, int64_t n, uint16_t *q_out, uint16_t *k_out,
                      void *stream);

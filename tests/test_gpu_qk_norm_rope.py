@@ -186,3 +186,24 @@ def test_channels_that_do_not_rotate_stay_apart(D, halves, rd, norm):
         if not norm:
             first = (rd or 0) if rotate else 0
             assert torch.equal(got[..., first:].nan_to_num(7.0), x[..., first:].double().cpu().nan_to_num(7.0))
+
+
+def test_weight_of_a_side_without_heads_is_not_read():
+    import ctypes
+
+    import bit_kv_cache_gb300 as kvq
+    g = torch.Generator(device=DEV).manual_seed(4)
+    x = torch.randn(9, 3, 128, generator=g, device=DEV).half()
+    w = torch.randn(128, generator=g, device=DEV).half()
+    pos = torch.arange(9, dtype=torch.int32, device=DEV)
+    want, _ = kvq.qk_norm_rope(x, None, w, None, pos)
+    stray = w.data_ptr() + 2  # aligned for no vector load
+    got = torch.zeros_like(x)
+    for heads, args in (((3, 0), (x.data_ptr(), None, w.data_ptr(), stray, got.data_ptr(), None)),
+                        ((0, 3), (None, x.data_ptr(), stray, w.data_ptr(), None, got.data_ptr()))):
+        got.zero_()
+        c = kvq.QkConfig(*heads, 128, 128, 0, 3, 1e-6, 1e4, 384, 384)
+        q, k, wq, wk, qo, ko = args
+        assert kvq.lib.kvq_qk_norm_rope(ctypes.byref(c), q, k, wq, wk, pos.data_ptr(), 9, qo, ko,
+                                        torch.cuda.current_stream().cuda_stream) == 0
+        assert torch.equal(got, want)
