@@ -166,6 +166,8 @@ __device__ __forceinline__ PageJob find_page(const ExtendParams &p, int i) {
     return j;
 }
 
+// Row t of a page's stream.  Residual rows are read by ordinary loads: where one launch does the
+// call, keep_rows writes over them.
 __device__ __forceinline__ const uint16_t *stream_row(const ExtendParams &p, const PageJob &j, const uint16_t *res,
                                                       const uint16_t *src, int64_t stride, int h, int t) {
     return t < j.s.nr ? res + (((size_t)j.b * p.H_kv + h) * p.R + t) * 128
@@ -184,7 +186,7 @@ __device__ __forceinline__ void extend_keys(const ExtendParams &p, const PageJob
     uint2 x[TPW];
 #pragma unroll
     for (int j = 0; j < TPW; j++)
-        x[j] = __ldg(reinterpret_cast<const uint2 *>(stream_row(p, jb, p.k_res, p.k_new, p.k_stride, h, jb.t0 + w * TPW + j)) + lane);
+        x[j] = reinterpret_cast<const uint2 *>(stream_row(p, jb, p.k_res, p.k_new, p.k_stride, h, jb.t0 + w * TPW + j))[lane];
     __half2 lo0 = *reinterpret_cast<const __half2 *>(&x[0].x), hi0 = lo0;
     __half2 lo1 = *reinterpret_cast<const __half2 *>(&x[0].y), hi1 = lo1;
 #pragma unroll
@@ -281,7 +283,7 @@ __device__ __forceinline__ void extend_values(const ExtendParams &p, const PageJ
         const uint4 *row = reinterpret_cast<const uint4 *>(
             stream_row(p, jb, p.v_res, p.v_new, p.v_stride, h, jb.t0 + vb * 128 + 16 * w + 8 * g + tq));
 #pragma unroll
-        for (int i = 0; i < 4; i++) x[g][i] = __ldg(row + c + 4 * i);
+        for (int i = 0; i < 4; i++) x[g][i] = row[c + 4 * i];
     }
     constexpr uint32_t lim = kMagicBits + (1u << BITS) - 1;
 #pragma unroll

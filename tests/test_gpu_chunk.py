@@ -607,3 +607,27 @@ def test_callers_pages():
     with pytest.raises(kvq.KvqError):
         c.plan([300])
     assert c.lengths(0)["T"] == 256 and c.read_status() == 0
+
+
+@pytest.mark.parametrize("n", [1, 100, 128, 300])
+@pytest.mark.parametrize("R,bits", [(128, 2), (128, 4), (128, 8), (256, 2)])
+def test_extend_over_a_full_residual(R, bits, n):
+    """A residual that append has filled and nothing has flushed: extend packs it and refills
+    it in the same call."""
+    caches = [make_cache(np.random.default_rng(1), [R - 2, 40], R=R, bits=bits, S=0) for _ in range(2)]
+    rng = np.random.default_rng(n)
+    tokens = [(randn(rng, 2, 2, 128), randn(rng, 2, 2, 128)) for _ in range(R // 128 * 128 - (R - 2) % 128)]
+    q, k, v = chunk_inputs(rng, caches[0], n + 3)
+    for c in caches:
+        while c.lens_host[2] < R:
+            c.append(*tokens[c.lens_host[2] % len(tokens)])
+    a, b = caches
+    assert a.lengths(0)["n_res"] == R
+    b.flush()
+    for c in caches:
+        c.extend(c.plan([n, 3]), k, v)
+        assert c.read_status() == 0
+    assert list(a.lens_host) == list(b.lens_host)
+    for s in range(2):
+        for x, y in zip(cached_rows(a, s), cached_rows(b, s)):
+            assert np.array_equal(x, y)
