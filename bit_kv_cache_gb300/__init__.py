@@ -232,7 +232,7 @@ class KVQChunk:
         self.desc = torch.zeros((cfg.B, 8), **i32)
         self.host = (ctypes.c_int32 * (8 * cfg.B))()
         self.ws = torch.empty(lib.kvq_paged_chunk_workspace_bytes(ctypes.byref(cfg)), dtype=torch.uint8, device=device)
-        self.B = cfg.B
+        self.B, self.device = cfg.B, self.cu.device
         self.cache, self.mapping = None, 0  # the cache of the last plan, and its state of page mappings
         pad = torch.zeros(4, **i32) if max_tokens == 0 else None  # an empty tensor has no address
         self._pad = pad
@@ -567,6 +567,11 @@ class KVQPagedCache:
         """Buffers for plans of up to max_tokens new tokens."""
         return KVQChunk(self.cfg, max_tokens, self._dev)
 
+    def _check_chunk(self, chunk):
+        """The library reads a row of the chunk's arrays for each of this cache's slots."""
+        if chunk.B != self.cfg.B or chunk.device != self._dev:
+            raise ValueError("the chunk belongs to another configuration")
+
     def plan(self, n_new, chunk=None, pages=None) -> KVQChunk:
         """Plans n_new[b] new tokens for every slot (kvq_paged_plan): slot maps, positions,
         and the page-table rows of the pages that extend() will pack.  n_new: B integers, or
@@ -585,8 +590,7 @@ class KVQPagedCache:
             np_ = (ctypes.c_int32 * cfg.B)(*n_new)
         if chunk is None:
             chunk = self.new_chunk(int(sum(n_new)))
-        if chunk.B != cfg.B or chunk.cu.device != self._dev:
-            raise ValueError("the chunk belongs to another configuration")
+        self._check_chunk(chunk)
         taken = []  # (slot, page) handed out here
         planned = pages is None
         if not planned and (pages.device != self._dev or pages.dtype != torch.int32 or pages.dim() != 1 or
@@ -642,6 +646,7 @@ class KVQPagedCache:
         chunk (kvq_paged_chunk_attn).  q: float16 [n, H_q, D], k_new, v_new: float16
         [n, H_kv, D], n >= chunk.n_tokens, token-major rows that may be strided; rows behind
         chunk.n_tokens are left alone.  The cache is not changed."""
+        self._check_chunk(chunk)
         torch, cfg, dev, n = self.torch, self.cfg, self._dev, chunk.n_tokens
         qp, qs = _rows(q, cfg.H_q, cfg.D, n, dev, "q")
         kp, ks = _rows(k_new, cfg.H_kv, cfg.D, n, dev, "k_new")
@@ -659,6 +664,7 @@ class KVQPagedCache:
         """The planned chunk's tokens enter the cache (kvq_paged_extend).  The chunk must have
         been planned on this cache, which maps the pages, unless the caller maps them."""
         cfg, dev = self.cfg, self._dev
+        self._check_chunk(chunk)
         if chunk.cache is not self and not self.caller_pages:
             raise KvqError(-1, "the chunk was planned on another cache")
         if chunk.mapping != self.mapping and not self.caller_pages:

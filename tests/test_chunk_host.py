@@ -208,3 +208,39 @@ def test_attention_needs_pages(kvq):
     f.p.n_pages = 0
     assert f.planned([2, 3, 1, 1]).attn() == INVALID
     assert f.planned([0, 0, 0, 1]).attn() == INVALID
+
+
+def host_cache(kvq, B):
+    """A paged cache without device memory, for checks that come before any device work."""
+    torch = pytest.importorskip("torch")
+    c = kvq.KVQPagedCache.__new__(kvq.KVQPagedCache)
+    c.torch, c.cfg, c._dev = torch, kvq.make_config(B, H_q, H_kv, D, G, 2, 0, 128, 0, "kivi", 4096, 0), torch.device("cpu")
+    c.p = kvq.Paged()
+    for i, name in enumerate(("k_codes", "k_meta", "v_codes", "v_meta", "page_table", "k_res", "v_res", "lens", "status")):
+        setattr(c.p, name, 0x10000 * (i + 1))
+    c.lens_host = (ctypes.c_int32 * (4 * B))()
+    c.p.lens_host = ctypes.cast(c.lens_host, ctypes.c_void_p)
+    c.p.n_pages = 8
+    c._refs = ctypes.byref(c.cfg), ctypes.byref(c.p)
+    c.caller_pages, c.mapping = False, 0
+    c.free, c.pages = list(range(8)), [[] for _ in range(B)]
+    return c
+
+
+@pytest.mark.parametrize("caller", [False, True])
+def test_chunk_of_another_configuration(kvq, caller):
+    """A chunk has arrays for its own number of slots; every call that reads them says so."""
+    torch = pytest.importorskip("torch")
+    c = host_cache(kvq, 6)
+    c.caller_pages = caller
+    rows = lambda h: torch.zeros(3, h, D, dtype=torch.float16)  # noqa: E731
+    ch = kvq.KVQChunk(host_cache(kvq, 2).cfg, 3, "cpu")
+    ch.cache = c
+    for call in (lambda: c.plan([1, 1, 1, 0, 0, 0], ch), lambda: c.chunk_attn(ch, rows(H_q), rows(H_kv), rows(H_kv)),
+                 lambda: c.extend(ch, rows(H_kv), rows(H_kv))):
+        with pytest.raises(ValueError, match="another configuration"):
+            call()
+    ch = kvq.KVQChunk(c.cfg, 3, "meta")
+    ch.cache = c
+    with pytest.raises(ValueError, match="another configuration"):
+        c.chunk_attn(ch, rows(H_q), rows(H_kv), rows(H_kv))
