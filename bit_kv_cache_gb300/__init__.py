@@ -499,6 +499,8 @@ class KVQPagedCache:
 
     def _map(self, b, n):
         """Maps the next n logical pages of slot b to free physical pages."""
+        if n == 0:
+            return
         if self.caller_pages:
             raise KvqError(-1, "the caller maps this cache's pages")
         if len(self.free) < n:
@@ -506,8 +508,7 @@ class KVQPagedCache:
         j0 = len(self.pages[b])
         new = [self.free.pop() for _ in range(n)]
         self.pages[b].extend(new)
-        if n:
-            self.table[b, j0:j0 + n] = self.torch.tensor(new, dtype=self.torch.int32)
+        self.table[b, j0:j0 + n] = self.torch.tensor(new, dtype=self.torch.int32)
 
     def prefill(self, b, k, v):
         """k, v: float16 [H_kv][L0][D] of batch slot b (empty)."""
@@ -552,12 +553,13 @@ class KVQPagedCache:
                "paged release")
 
     def clear(self, unmap=True):
-        """Empties every slot.  unmap=False: the pages stay mapped to their slots, which
-        refill them."""
+        """Empties every slot and unmaps its pages; the cache maps its own again if the caller
+        did.  unmap=False: the pages stay mapped to their slots, which refill them."""
         _check(lib.kvq_paged_init(*self._refs, _stream_of(self._dev.index)),
                "paged init")
         if unmap:
             self.mapping += 1
+            self.caller_pages = False
             for b in range(self.cfg.B - 1, -1, -1):
                 self.free.extend(reversed(self.pages[b]))
                 self.pages[b] = []
@@ -576,8 +578,8 @@ class KVQPagedCache:
         """Plans n_new[b] new tokens for every slot (kvq_paged_plan): slot maps, positions,
         and the page-table rows of the pages that extend() will pack.  n_new: B integers, or
         an int32 CPU tensor.  pages: int32 device tensor of physical pages that the caller
-        hands out, in the order slots need them; by default they come from the cache's own
-        free list."""
+        hands out, in the order slots need them, here and in every later call that needs pages,
+        until clear(); by default they come from the cache's own free list."""
         torch, cfg = self.torch, self.cfg
         if isinstance(n_new, torch.Tensor):
             if n_new.device.type != "cpu" or n_new.dtype != torch.int32 or n_new.shape != (cfg.B,) or not n_new.is_contiguous():

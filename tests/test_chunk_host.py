@@ -244,3 +244,13 @@ def test_chunk_of_another_configuration(kvq, caller):
     ch.cache = c
     with pytest.raises(ValueError, match="another configuration"):
         c.chunk_attn(ch, rows(H_q), rows(H_kv), rows(H_kv))
+
+
+def test_no_page_needs_no_list(kvq):
+    """A cache whose pages the caller maps refuses to hand out pages, not to hand out none."""
+    c = host_cache(kvq, 2)
+    c.caller_pages = True
+    c._map(0, 0)
+    with pytest.raises(kvq.KvqError):
+        c._map(0, 1)
+    assert len(c.free) == 8 and c.pages == [[], []]

@@ -631,3 +631,34 @@ def test_extend_over_a_full_residual(R, bits, n):
     for s in range(2):
         for x, y in zip(cached_rows(a, s), cached_rows(b, s)):
             assert np.array_equal(x, y)
+
+
+def test_callers_pages_until_cleared():
+    """Calls that need no page work beside the caller's pages; an emptied cache has its own list
+    again, and a chunk planned before is stale."""
+    import bit_kv_cache_gb300 as kvq
+    rng = np.random.default_rng(34)
+    c = make_cache(rng, [0, 0], spare=8)
+    q, k, v = chunk_inputs(rng, c, 300)
+    ch = c.plan([300, 0], pages=torch.tensor([6, 2], dtype=torch.int32, device=DEV))
+    c.extend(ch, k, v)
+    rows = [randn(rng, 2, 200, 128) for _ in range(2)]
+    c.prefill(1, *(x[:, :5].contiguous() for x in rows))
+    c.append(randn(rng, 2, 2, 128), randn(rng, 2, 2, 128))
+    assert c.flush() == [] and c.lengths(1)["n_res"] == 6
+    c.release(1)
+    with pytest.raises(kvq.KvqError):
+        c.prefill(1, *rows)
+    c.clear(unmap=False)
+    with pytest.raises(kvq.KvqError):
+        c.plan([300, 0])
+    stale = c.plan([130, 0], pages=torch.tensor([6, 2], dtype=torch.int32, device=DEV))
+    c.clear()
+    with pytest.raises(kvq.KvqError):
+        c.extend(stale, k, v)
+    c.prefill(1, *rows)
+    c.extend(c.plan([300, 0]), k, v)
+    assert c.lengths(0)["T"] == 256 and c.lengths(1)["T"] == 128
+    assert sorted(c.free + c.pages[0] + c.pages[1]) == list(range(8))
+    assert c.table[0, :2].tolist() == c.pages[0] and c.table[1, :1].tolist() == c.pages[1]
+    assert c.read_status() == 0
