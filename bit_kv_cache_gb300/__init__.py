@@ -590,9 +590,12 @@ class KVQPagedCache:
             if len(n_new) != cfg.B or any(not 0 <= x < 1 << 31 for x in n_new):
                 raise ValueError("n_new must hold %d counts" % cfg.B)
             np_ = (ctypes.c_int32 * cfg.B)(*n_new)
+        if chunk is not None:
+            self._check_chunk(chunk)
+        if (chunk is None or pages is None) and torch.cuda.is_current_stream_capturing():
+            raise KvqError(-2, "kvq_paged_plan")  # before anything is allocated or copied
         if chunk is None:
             chunk = self.new_chunk(int(sum(n_new)))
-        self._check_chunk(chunk)
         taken = []  # (slot, page) handed out here
         planned = pages is None
         if not planned and (pages.device != self._dev or pages.dtype != torch.int32 or pages.dim() != 1 or

@@ -662,3 +662,26 @@ def test_callers_pages_until_cleared():
     assert sorted(c.free + c.pages[0] + c.pages[1]) == list(range(8))
     assert c.table[0, :2].tolist() == c.pages[0] and c.table[1, :1].tolist() == c.pages[1]
     assert c.read_status() == 0
+
+
+def test_refused_plan_leaves_a_capture_alone():
+    """A plan that would take pages from the cache's list, or make a chunk, is refused while the
+    stream is captured like any other, and the capture goes on."""
+    import bit_kv_cache_gb300 as kvq
+    rng = np.random.default_rng(35)
+    c = make_cache(rng, [100])
+    q, k, v = chunk_inputs(rng, c, 40)
+    ch = c.new_chunk(40)
+    free = list(c.free)
+    x = torch.zeros(4, device=DEV)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        x += 1
+        for call in (lambda: c.plan([40], ch), lambda: c.plan([4]), lambda: c.chunk_step([40], q, k, v)):
+            with pytest.raises(kvq.KvqError) as e:
+                call()
+            assert e.value.code == -2
+    graph.replay()
+    assert x.tolist() == [1.0] * 4 and c.free == free and c.pages == [[]]
+    c.extend(c.plan([40], ch), k, v)
+    assert c.lengths(0)["T"] == 128 and c.read_status() == 0
