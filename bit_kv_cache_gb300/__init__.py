@@ -682,11 +682,14 @@ class KVQPagedCache:
                    halves=False, chunk=None, out=None):
         """One step of n_new[b] new tokens per slot: plan, norm and rotation of q and k at
         their positions, attention, and the tokens' entry into the cache.  q: float16
-        [n, H_q, D], k, v: float16 [n, H_kv, D], n = sum(n_new).  Returns (out, chunk)."""
+        [n, H_q, D], k, v: float16 [n, H_kv, D], n >= sum(n_new); rows behind that sum are left
+        alone.  Returns (out, chunk), out with sum(n_new) rows if it is not the caller's.  A
+        chunk made here (chunk=None) costs its arrays and a workspace in every call; a loop
+        keeps one."""
         chunk = self.plan(n_new, chunk)
         n = chunk.n_tokens
         if n == 0:
-            return q.new_empty(q.shape) if out is None else out, chunk
+            return q.new_empty((0,) + q.shape[1:]) if out is None else out, chunk
         q, k = qk_norm_rope(q[:n], k[:n], w_q, w_k, chunk.pos[:n], eps, rope_base, rotary_dim, halves)
         out = self.chunk_attn(chunk, q, k, v, out)
         self.extend(chunk, k, v)

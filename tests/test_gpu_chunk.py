@@ -685,3 +685,18 @@ def test_refused_plan_leaves_a_capture_alone():
     assert x.tolist() == [1.0] * 4 and c.free == free and c.pages == [[]]
     c.extend(c.plan([40], ch), k, v)
     assert c.lengths(0)["T"] == 128 and c.read_status() == 0
+
+
+def test_step_without_tokens():
+    """A padded batch in which no slot has a token: no rows out, or the caller's left alone."""
+    rng = np.random.default_rng(36)
+    c = make_cache(rng, [100, 0])
+    state = list(c.lens_host)
+    q, k, v = chunk_inputs(rng, c, 0, 3)
+    out, chunk = c.chunk_step([0, 0], q, k, v)
+    assert out.shape == (0, c.cfg.H_q, 128) and out.dtype == torch.float16 and chunk.n_tokens == 0
+    mine = torch.full((3, c.cfg.H_q, 128), 7.0, dtype=torch.float16, device=DEV)
+    out, chunk = c.chunk_step([0, 0], q, k, v, chunk=chunk, out=mine)
+    assert out is mine and (mine == 7.0).all()
+    out, _ = c.chunk_step([2, 0], q, k, v, chunk=c.new_chunk(3))
+    assert out.shape[0] == 2 and state != list(c.lens_host) and c.read_status() == 0
