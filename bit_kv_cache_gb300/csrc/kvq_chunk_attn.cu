@@ -89,7 +89,7 @@ struct Bars {
     uint64_t readk[kMaxRaw], readv[kMaxRaw];          // packed tile read by all producers
     uint32_t tmem;
     int stop;
-    int odd[4];              // segment (+ 1) whose tail values are not all finite, by segment mod 4
+    int odd;                 // whether a tail value of any segment so far was not finite
 };
 constexpr int kSmemBytes = kOffBar + (int)sizeof(Bars);
 static_assert(kSmemBytes <= 232448, "shared memory");
@@ -315,8 +315,8 @@ __device__ __forceinline__ void produce(const ChunkAttnParams &p, unsigned char 
     uint64_t *full = (value ? bar->v_full : bar->k_full) + par, *empty = (value ? bar->v_empty : bar->k_empty) + par;
     int slot = 0;              // of the next packed tile, of either parity
     uint32_t landed = 0, free = 1, nq = 1;  // parities: of the slots' arrivals, of the tile's release
-    int seg = 0, n = 0;        // n: tiles of the segments before
-    for (At at(p); at.more(); seg++) {
+    int n = 0;                 // tiles of the segments before
+    for (At at(p); at.more();) {
         const Seg s = next_seg(p, at);
         if (value && par == 0) {
             // queries: 128-row tiles, rows of tokens' heads; rows behind the last one repeat it
@@ -354,7 +354,7 @@ __device__ __forceinline__ void produce(const ChunkAttnParams &p, unsigned char 
                 if (make_tail(p, s, (kt - s.np) * kChunkKeys, value, dst, tid)) {
                     // infinite and NaN values enter the product as 0 (0 weights of rows that may
                     // not see them would spread them) and are added to their rows at the end
-                    *(volatile int *)&bar->odd[seg & 3] = seg + 1;
+                    *(volatile int *)&bar->odd = 1;
                 }
             }
             fence_proxy_async();
@@ -661,8 +661,7 @@ __device__ __forceinline__ void softmax(const ChunkAttnParams &p, Bars *bar, uin
     const uint32_t lanes = (uint32_t)(threadIdx.x & 96) << 16;
     const uint32_t ts = tm + lanes + m * 128, to = tm + lanes + 256 + m * 128;
     RowState st = {0, 0, 0, 0.f, 0.f};
-    int seg = 0;
-    for (At at(p); at.more(); seg++) {
+    for (At at(p); at.more();) {
         const Seg s = next_seg(p, at);
         const bool last_first = s.k0 == 0 && s.it.first != p.begin[blockIdx.x];
         const int base = s.narrow ? 0 : 128 * m, row = s.rep > 1 ? lane_row & (128 / s.rep - 1) : base + lane_row;
@@ -702,7 +701,9 @@ __device__ __forceinline__ void softmax(const ChunkAttnParams &p, Bars *bar, uin
             l = a0 * l + a1 * other.y;
         }
         const bool whole = s.k0 == 0 && s.k1 == s.it.n;
-        const bool odd = *(volatile int *)&bar->odd[seg & 3] == seg + 1;
+        // set before the tile's products; it stays set, as a group that has no rows in the segments
+        // between may run any number of them ahead of the other
+        const bool odd = *(volatile int *)&bar->odd;
         const float inv = 1.f / l;
         const bool mine = s.rep > 1 || row < s.valid;
         const size_t slot = slot0 + (s.rep > 1 ? lane_row : row);
@@ -788,7 +789,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attn_kernel(const __grid_co
             mbar_init(&bar->readv[i], 128);
         }
         bar->stop = 0;
-        for (int i = 0; i < 4; i++) bar->odd[i] = 0;
+        bar->odd = 0;
         fence_barrier_init();
     }
     if (w == 24) tmem_alloc(&bar->tmem);

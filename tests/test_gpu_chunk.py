@@ -700,3 +700,22 @@ def test_step_without_tokens():
     assert out is mine and (mine == 7.0).all()
     out, _ = c.chunk_step([2, 0], q, k, v, chunk=c.new_chunk(3))
     assert out.shape[0] == 2 and state != list(c.lens_host) and c.read_status() == 0
+
+
+def test_values_not_finite_in_some_of_many_units():
+    """Ranges of many short units, wide ones among them: an infinite or NaN value reaches the rows
+    of its own slot that see it, in whichever unit of a range it lies."""
+    rng = np.random.default_rng(37)
+    new = [70 if b % 9 == 4 else 1 + b % 3 for b in range(90)]
+    c = make_cache(rng, [int(x) for x in rng.integers(0, 120, 90)], H_q=16, H_kv=4, max_T=512)
+    n = sum(new)
+    q, k, v = (x.clone() for x in chunk_inputs(rng, c, n))
+    at = np.cumsum([0] + new)
+    for b in list(range(0, 90, 7)) + [4, 5, 6, 9, 13, 14]:
+        v[at[b] + new[b] // 2, b % 4, b] = [float("inf"), float("nan"), float("-inf")][b % 3]
+    c.view("v_res")[20, 1, 0, 3] = float("inf")
+    assert c.lengths(20)["n_res"] > 0
+    ch = c.plan(new)
+    out = c.chunk_attn(ch, q, k, v)
+    attn_check(c, new, q, k, v, out)
+    assert torch.equal(out.view(torch.int16), c.chunk_attn(ch, q, k, v).view(torch.int16))
