@@ -26,7 +26,7 @@ EXPORTS = ("kvq_status_str", "kvq_config_check", "kvq_buffer_bytes", "kvq_quant_
            "kvq_quant_pack_v", "kvq_append_token", "kvq_flush_group",
            "kvq_decode_attn_workspace_bytes", "kvq_workspace_init", "kvq_decode_attn",
            "kvq_read_status", "kvq_decode_attn_noalloc", "kvq_step_io_bytes", "kvq_decode_step_host",
-           "kvq_decode_step_host_wait", "kvq_selftest_wait_timeout", "kvq_append_decode",
+           "kvq_decode_step_host_wait", "kvq_selftest_wait_timeout", "kvq_selftest_roles_timeout", "kvq_append_decode",
            "kvq_paged_bytes", "kvq_paged_init",
            "kvq_paged_prefill", "kvq_paged_append", "kvq_paged_flush_plan", "kvq_paged_flush",
            "kvq_paged_release", "kvq_paged_workspace_bytes", "kvq_paged_decode_attn",
@@ -103,6 +103,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "kvq_decode_step_host": ([CP, KP, P, P, P, P, P, Sz, P, Sz, IP, IP, P], I),
         "kvq_decode_step_host_wait": ([CP, KP, P, P, P, P, P, P, Sz, IP, IP, P], I),
         "kvq_selftest_wait_timeout": ([P, P], I),
+        "kvq_selftest_roles_timeout": ([P, P, P], I),
         "kvq_paged_bytes": ([CP, I64, I], Sz),
         "kvq_paged_init": ([CP, PP, P], I),
         "kvq_paged_prefill": ([CP, PP, I, P, P, I64, P], I),

@@ -296,6 +296,12 @@ int kvq_decode_step_host_wait(const kvq_config *cfg, kvq_cache *cache, const uin
  * KVQ_ERR_INVALID_ARG for a missing or misaligned status word. */
 int kvq_selftest_wait_timeout(int32_t *status, void *stream);
 
+/* The same for the waits of a block whose warps take different roles (kvq_paged_chunk_attn):
+ * eight warps make three waits each that nothing completes.  The first one that runs out ends
+ * all: *status gets KVQ_DEV_TIMEOUT, and left (device int32 [8]) the waits that each warp came
+ * through, 3. */
+int kvq_selftest_roles_timeout(int32_t *status, int32_t *left, void *stream);
+
 /* Stages (1) and (2) together: kvq_append_token(k_new, v_new), then kvq_decode_attn(q,
  * out), with the same arguments, layouts, results and errors.  Where the token goes to
  * the key and value residuals of a KIVI cache (sink full) and the packed-tile path

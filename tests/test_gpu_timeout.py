@@ -44,3 +44,22 @@ def test_wait_runs_out_and_reports(kvq):
     out = gpu.decode_attn(to_dev(q, DEV)).float().cpu().numpy()
     assert_close(out, ora.attend(q))
     assert gpu.read_status() == 0
+
+
+def test_waits_of_roles_end_together(kvq):
+    """The first of many waits to run out ends all waits of its block."""
+    import torch
+    status = torch.zeros(4, dtype=torch.int32, device=DEV)
+    left = torch.zeros(16, dtype=torch.int32, device=DEV)
+    stream = torch.cuda.current_stream().cuda_stream
+    assert kvq.lib.kvq_selftest_roles_timeout(status.data_ptr(), None, stream) == -1
+    torch.cuda.synchronize()
+    t0 = time.perf_counter()
+    assert kvq.lib.kvq_selftest_roles_timeout(status.data_ptr(), left.data_ptr(), stream) == 0
+    torch.cuda.synchronize()
+    dt = time.perf_counter() - t0
+    assert int(status[0].item()) == kvq.KVQ_DEV_TIMEOUT and int(status[1:].abs().sum().item()) == 0
+    assert left.tolist() == [3] * 8 + [0] * 8
+    assert 0.5 < dt < 5.0                             # one bound of about 2 s, not three
+    x = torch.arange(8, device=DEV)
+    assert int((x * 2).sum().item()) == 56
