@@ -269,6 +269,7 @@ class KVQCache:
             t = torch.zeros(max(n, 16), dtype=torch.uint8, device=self.device)
             self.buf[name] = t
             setattr(self.c, name, t.data_ptr() if n else None)
+        self.device = t.device  # with its index, as the callers' tensors have it
         vs = torch.zeros(max(self.buf["k_sink"].numel(), 16), dtype=torch.uint8, device=self.device)
         self.buf["v_sink"] = vs
         self.c.v_sink = vs.data_ptr() if self.cfg.S else None
@@ -472,6 +473,7 @@ class KVQPagedCache:
             t = torch.zeros(max(n, 16), dtype=torch.uint8, device=self.device)
             self.buf[name] = t
             setattr(self.p, name, t.data_ptr() if n else None)
+        self.device = self._dev = t.device  # with its index, as the callers' tensors have it
         self.max_pages = max_T // G
         self.table = torch.zeros((B, self.max_pages), dtype=torch.int32, device=self.device)
         self.lens = torch.zeros((B, 4), dtype=torch.int32, device=self.device)
@@ -483,7 +485,6 @@ class KVQPagedCache:
         self.p.lens_host = ctypes.cast(self.lens_host, ctypes.c_void_p)
         self.p.status = self.status.data_ptr()
         self.ws = torch.zeros(lib.kvq_paged_workspace_bytes(cp), dtype=torch.uint8, device=self.device)
-        self._dev = self.table.device                 # with its index
         self._refs = ctypes.byref(self.cfg), ctypes.byref(self.p)
         self.caller_pages = False                     # plan() was given pages of the caller's
         self.mapping = 0                              # counts the calls that took pages away from slots

@@ -719,3 +719,22 @@ def test_values_not_finite_in_some_of_many_units():
     out = c.chunk_attn(ch, q, k, v)
     attn_check(c, new, q, k, v, out)
     assert torch.equal(out.view(torch.int16), c.chunk_attn(ch, q, k, v).view(torch.int16))
+
+
+def test_default_device():
+    """A cache made without a device index takes the tensors of the current device in every call,
+    chunk calls and the others alike."""
+    import bit_kv_cache_gb300 as kvq
+    rng = np.random.default_rng(38)
+    with torch.cuda.device(0):
+        c = kvq.KVQPagedCache(2, 8, 2, 128, 128, 2, n_pages=8, max_T=512)
+        q, k, v = (x.contiguous() for x in chunk_inputs(rng, c, 4))
+        c.prefill(0, randn(rng, 2, 200, 128), randn(rng, 2, 200, 128))
+        out, _ = c.chunk_step([1, 3], q, k, v)
+        attended = c.decode_attn(q[:2])
+        c.append(k[:2], v[:2])
+        dense = kvq.KVQCache(1, 8, 2, 128, 128, 2, max_T=512)
+        dense.prefill(randn(rng, 1, 2, 200, 128), randn(rng, 1, 2, 200, 128))
+        dense.decode_attn(q[:1])
+    assert out.device == attended.device == torch.device(DEV)
+    assert c.lengths(0) == dict(n_sink=0, T=128, n_res=74, active=1) and c.read_status() == 0
