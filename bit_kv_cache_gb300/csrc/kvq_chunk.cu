@@ -128,9 +128,11 @@ cudaError_t launch_plan(const PlanParams &p, cudaStream_t st) {
 // 128 value tokens) gathers its rows from the two places and quantizes them as the prefill
 // kernels do (kvq_quantizer.cuh), so codes and scales are theirs bit for bit.  Few pages are
 // bound by their dependent reads (plan, rows; a page-table entry only at the end): 13 us for
-// a chunk of 2048 tokens of 8 heads; many by the quantizer's instructions: four prompts of
-// 2K to 12K tokens, 237 MB in two calls, take 69 us (3.4 TB/s).  The slots of the pages come
-// as a parameter (found from the plan's arrays: 70 us).
+// a chunk of 2048 tokens of 8 heads.  Many: four prompts of 2K to 12K tokens, 237 MB in two
+// calls, take 69 us (3.4 TB/s) with nothing saturated (issue 0.60 a cycle, ALU 0.46): four CTAs
+// per SM at 64 registers, and in each the chain of search, plan row and table entry before its
+// loads; the prefill quantizers, with the same arithmetic and without that chain, reach 4.5
+// TB/s.  The slots of the pages come as a parameter (found from the plan's arrays: 70 us).
 // ------------------------------------------------------------------------------
 struct PageJob {
     ChunkSlot s;
@@ -440,8 +442,8 @@ cudaError_t launch_extend(const ExtendParams &p, int kbits, int vbits, cudaStrea
 // pairs each (both channels of a pair in one thread), a warp a token's heads or a part of
 // them; a thread's channels are the same in all its rows, so that their weights, sines and
 // cosines are formed once.  An angle pos * base^(-2j/n) is reduced in 64-bit fixed point:
-// pos * turn[j] mod 2^64 is the exact fraction of a turn, whose upper 32 bits go to
-// sincospif.  8191 tokens of 32 + 8 heads of 128 channels, 168 MB, take 30 us (5.6 TB/s);
+// pos * turn[j] mod 2^64 is the fraction of a turn, exact but for turn[j]'s error of some
+// tens of 2^-64 (times pos: below 2^-27), and its upper 32 bits go to sincospif.  8191 tokens of 32 + 8 heads of 128 channels, 168 MB, take 30 us (5.6 TB/s);
 // bound by instructions before: 63 us with a CTA per token, a row per warp and a shuffle per
 // channel, 45 us with both channels of a pair in one thread and fp32 pairs, 41 us with the
 // weights folded into sine and cosine, 30 us with a warp per token, which forms them once
@@ -1034,7 +1036,10 @@ int kvq_qk_norm_rope(const kvq_qk_config *c, const uint16_t *q, const uint16_t *
     p.eps = c->eps;
     const double base = c->rope_base > 0.f ? (double)c->rope_base : 10000.0;
     // turn[j] = base^(-2j/n) / (2 pi) in 64-bit fixed point: one root, then integer products
-    // (a call's host time is a small part of that of a power per pair), each off by 2^-64 at most
+    // (a call's host time is a small part of that of a power per pair).  The root's error and the
+    // products' truncations add up: a step is off by n/4 + 1 units of 2^-64 at most (64.3 for
+    // n = 256 and bases next to 1, 9 for a base of 10000, against 80 digits), so an angle by
+    // 2^-27 of a turn at positions below 2^31
     if (c->rotary_dim && base > 1.0) {
         const uint64_t f = inverse_root(base, c->rotary_dim / 2);
         uint64_t turn = 0x28be60db9391054aull;  // 2^64 / (2 pi)

@@ -6,22 +6,26 @@
 // in one pass over the keys with a running maximum and sum per row.  Sums, maxima and the
 // output's accumulators are fp32.  Dequantized keys and values and the softmax weights are
 // rounded once to fp16, the operand type of the products: outputs of unit-variance values are
-// then off by 3.1e-4 to 5.6e-4 of their size (2.1e-4 is the rounding of the output itself).
-// Exact operands would be codes with the scales folded into the other operand, which differ
-// from page to page (keys: another Q tile per page) and would be rounded there instead.
+// then off by 3.1e-4 to 5.6e-4 of their size.  Alone, the output's own rounding makes 2.1e-4 of
+// it, the keys' 2.1e-4 (2-bit) to 4.1e-4 (8-bit, a few channels of five times the size), the
+// values' 1.3e-4 to 2.2e-4, the weights' 1.2e-4 to 1.9e-4.  Exact operands would be codes with
+// the scales folded into the other operand, which differ from page to page (keys: another Q
+// tile per page) and would be rounded there instead, or a second operand for the remainders:
+// a second product per key tile, and no room in shared memory for its tiles.
 //
 // What bounds it.  Wide units: the tensor core.  A product with M = 128 reads its operands
 // from shared memory at 128 bytes a cycle: K = 16 takes 48 cycles at N = 64, 64 at N = 128, so
 // a key tile of 256 rows takes 2478 cycles when nothing else runs.  2048 tokens of 32 heads
-// over 32868 cached ones (2-bit; 1137 GFLOP): 847 us, 1.34 PFLOP/s, 0.72 of the measured rate
-// of a large library product; dequantization and softmax take issue slots and shared memory
-// beside it.  Narrow units: issue slots.  Eight slots of 17K to 56K tokens with 1 to 8 new ones
-// take 148 us, where their packed bytes take 24: 0.61 instructions a cycle and scheduler, the
-// ALU half busy (5600 warp instructions per key tile: one AND and two fused products per two
-// codes, the stores of the fp16 tiles, the softmax, waits), the tensor core 0.44.
-// Tried there and dropped: both groups of a side on one tile (162 us; 77 us against 84 with
-// 8-bit codes, but 911 us in the case above), barriers per half tile (164 us), an early start
-// of the kernel behind (166 us).
+// over 32868 cached ones (2-bit; 1137 GFLOP): 865 to 903 us, 1.26 to 1.31 PFLOP/s, 0.68 to 0.71
+// of the measured rate of a large library product; dequantization and softmax take issue slots
+// and shared memory beside it.  Narrow units: issue slots.  Eight slots of 17K to 56K tokens
+// with 1 to 8 new ones take 145 us, where their packed bytes take 24: 0.62 instructions a cycle
+// and scheduler, the ALU half busy (5600 warp instructions per key tile: one AND and two fused
+// products per two codes, the stores of the fp16 tiles, the softmax, waits), the tensor core
+// 0.45.  The kernel keeps 48 bytes of a thread on the stack (104 stored, 144 loaded).
+// Tried there and dropped, when these cases stood at 148 and 847 us: both groups of a side on
+// one tile (162 us; 77 us against 84 with 8-bit codes, but 911 us in the case above), barriers
+// per half tile (164 us), an early start of the kernel behind (166 us).
 //
 // One CTA per SM, eight groups of four warps:
 //   groups 0, 1  softmax, a thread per row of 128: reads the scores S_m from tensor memory,
@@ -42,7 +46,7 @@
 // that is cut holds them twice (four times) in its query tile, and each copy's softmax takes
 // half (a quarter) of a tile's keys: the tensor core's rows cost nothing, and a step of the
 // softmax, which is what such a unit waits for, is as much shorter (the eight slots above:
-// 148 us against 187 without).  The combine kernel joins the copies' partials like those of
+// 148 us then, against 187 without).  The combine kernel joins the copies' partials like those of
 // the ranges.
 // A step is half a key tile (64 keys).  S_m has two buffers of 64 columns, so that the scores
 // of the next step are made while the softmax of this one runs.  Tensor memory: S_0, S_1,
@@ -72,7 +76,7 @@ constexpr int kOffQ = 0, kOffK = 2 * kTileBytes, kOffV = kOffK + kRing * kTileBy
 // off by 2^-15 at most; beyond it (362 in units of the softmax's exponent) x - r, which is
 // exact where it matters, is formed first in every step, as scaled values of 2^28 and more
 // would differ from their products by more than fp16's range has room for.  (A 2048-token
-// chunk: 871 us against 862 with scaled references alone.  The weights of such rows as a
+// chunk: 867 us against 859 with scaled references alone.  The weights of such rows as a
 // branch of their own, or one body of code for both: 900 to 940, the hot code grows or stalls.)
 constexpr float kUp = 6.f, kMostSum = 16384.f, kNear = 4096.f;
 // registers of a thread after the split; 64 at launch, times 1024 threads

@@ -440,9 +440,10 @@ int kvq_paged_read_status(const kvq_paged *pc, void *ws, int32_t *dev_status, vo
  * Chunks of new tokens over the paged cache.  A serving step adds n_new[b] >= 0 tokens
  * to every batch slot b: the next chunk of a prompt, drafted tokens to verify, or one
  * token each.  The order of a step is
- *   kvq_paged_plan        slot maps, positions and block-table rows (once per step; any
- *                         number of caches of the same configuration and lengths, such
- *                         as the layers of a model, may use one plan)
+ *   kvq_paged_plan        slot maps, positions and block-table rows (once per step: caches
+ *                         of the same configuration and lengths, such as the layers of a
+ *                         model, may use one plan, if their page tables map its pages too
+ *                         when they are extended)
  *   kvq_qk_norm_rope      norm and rotation of the new queries and keys
  *   kvq_paged_chunk_attn  every new token attends to its slot's cached tokens and to the
  *                         chunk's tokens up to itself
@@ -498,11 +499,18 @@ size_t kvq_paged_chunk_workspace_bytes(const kvq_config *cfg);
  * [n_tokens][H_q][D], contiguous, overlapping none of the inputs.  Rows of the tensors
  * behind n_tokens are neither read nor written.  The cache is not changed.  Operands are
  * fp16 (dequantized keys and values and softmax weights are rounded to it once), sums and
- * softmax statistics fp32.
- * Infinite and NaN values reach the rows that see them and no others.
+ * softmax statistics fp32: an output is off by 3e-4 to 6e-4 of its size where
+ * kvq_paged_decode_attn, which does not round the cached codes, is off by little more than
+ * the output's own rounding, 2e-4.  For one token per slot that call is also the faster one
+ * (eight slots of 17K to 56K tokens: 71 us against 139).
+ * Infinite and NaN values reach the rows that see them and no others.  A page-table entry
+ * that is no page is reported (KVQ_DEV_BAD_STATE) and page 0 read in its place.
+ * KVQ_ERR_UNSUPPORTED if the work of the call exceeds 2^30 units (4 for 128 keys of a key
+ * head and 256 query rows: a 2048-token chunk of 8 key heads over 100 million tokens).
  * KVQ_ERR_INVALID_ARG if the cache's lengths are not those of the plan, or a slot with new
  * tokens has packed ones and the pool no page.  The call may be captured: a replay attends
- * over the plan's lengths. */
+ * over the plan's lengths, to what the cache then holds there, so it is of use until the cache
+ * is extended, appended to or flushed. */
 int kvq_paged_chunk_attn(const kvq_config *cfg, const kvq_paged *pc, kvq_chunk *chunk, const uint16_t *q,
                          int64_t q_stride, const uint16_t *k_new, int64_t k_stride, const uint16_t *v_new,
                          int64_t v_stride, uint16_t *out, void *ws, size_t ws_bytes, void *stream);
@@ -536,8 +544,8 @@ typedef struct {
 
 /* y = x / sqrt(mean(x^2) + eps) * w over each head's D channels (skipped where the weight
  * pointer is NULL), then the rotation by pos[i], in fp32 with one rounding to fp16; the
- * angles are reduced exactly (64-bit fixed point) at any position before the fp32 sine and
- * cosine.  q, k: device fp16 rows (strides above); w_q, w_k: device fp16 [D] or NULL; pos:
+ * angles are reduced in 64-bit fixed point, to 2^-27 of a turn at any position, before the
+ * fp32 sine and cosine.  q, k: device fp16 rows (strides above); w_q, w_k: device fp16 [D] or NULL; pos:
  * device int32 [n]; q_out, k_out: device fp16 [n][H][D], contiguous.  The pointers of a side
  * without heads are not used.  An output may be its own input if that is contiguous; any
  * other overlap of an output with an input or the other output is KVQ_ERR_INVALID_ARG. */
