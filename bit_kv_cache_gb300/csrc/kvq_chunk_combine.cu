@@ -15,9 +15,11 @@ struct Part {
     float m, l;
     float4 o;
 };
+// The factor of a part below the maximum; positive, as an infinite value in it stays infinite
+// (2^-126 of a finite part is far below the other's smallest step).
+__device__ __forceinline__ float factor(float m, float top) { return m == top ? 1.f : fmaxf(exp2f((m - top) * kScale), 0x1p-126f); }
 __device__ __forceinline__ void join(Part &a, const Part &b) {
-    const float m = fmaxf(a.m, b.m);
-    const float x = a.m == m ? 1.f : exp2f((a.m - m) * kScale), y = b.m == m ? 1.f : exp2f((b.m - m) * kScale);
+    const float m = fmaxf(a.m, b.m), x = factor(a.m, m), y = factor(b.m, m);
     a.m = m;
     a.l = x * a.l + y * b.l;
     a.o.x = x * a.o.x + y * b.o.x;

@@ -125,3 +125,28 @@ def test_largest_scores(form, sign):
     out = c.chunk_attn(c.plan(new), q, k, v)
     check(c, new, q, k, v, out)
     assert c.read_status() == 0
+
+
+@pytest.mark.parametrize("cached", [1300, 2000, 3100])
+@pytest.mark.parametrize("new", [3, 12, 25, 90])
+def test_infinite_value_under_a_small_weight(new, cached):
+    """A weight is positive however small: an infinite value of a key far below the others makes
+    the output infinite, whole or joined from parts."""
+    import bit_kv_cache_gb300 as kvq
+    rng = np.random.default_rng(new)
+    H, S = 2, 256
+    c = kvq.KVQPagedCache(1, 8, H, D, 128, 2, n_pages=40, max_T=4096, S=S, device=DEV)
+    k, v = randn(rng, H, cached, D, scale=0.25), randn(rng, H, cached, D)
+    k[:, :, 0], k[:, :S, 0] = 500.0, 0.0                 # 177 below the others
+    v[0, 7, 3], v[0, 200, 4], v[1, 255, 5] = float("inf"), float("-inf"), float("inf")
+    c.prefill(0, k, v)
+    q = randn(rng, new, 8, D, scale=0.25)
+    q[..., 0] = 4.0
+    kn, vn = randn(rng, new, H, D, scale=0.25), randn(rng, new, H, D)
+    kn[..., 0] = 500.0
+    out = c.chunk_attn(c.plan([new]), q, kn, vn).float()
+    want = torch.zeros(new, 8, D, device=DEV)
+    want[:, :4, 3], want[:, :4, 4], want[:, 4:, 5] = float("inf"), float("-inf"), float("inf")
+    bad = ~torch.isfinite(want)
+    assert torch.equal(out[bad], want[bad])
+    assert torch.isfinite(out[~bad]).all()
