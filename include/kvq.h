@@ -503,8 +503,9 @@ size_t kvq_paged_chunk_workspace_bytes(const kvq_config *cfg);
  * kvq_paged_decode_attn, which does not round the cached codes, is off by little more than
  * the output's own rounding, 2e-4.  For one token per slot that call is also the faster one
  * (eight slots of 17K to 56K tokens: 71 us against 139).
- * Infinite and NaN values reach the rows that see them and no others; a dequantized key or
- * value that rounds beyond fp16's largest counts as infinite.  A page-table entry
+ * Infinite and NaN values reach the rows that see them and no others.  A packed key or value
+ * that rounds beyond fp16's largest when dequantized counts as one of them: the rows of its
+ * slot become infinite or NaN.  A page-table entry
  * that is no page is reported (KVQ_DEV_BAD_STATE) and page 0 read in its place.
  * KVQ_ERR_UNSUPPORTED if the work of the call exceeds 2^30 units (4 for 128 keys of a key
  * head and 256 query rows: a 2048-token chunk of 8 key heads over 100 million tokens).
