@@ -499,14 +499,14 @@ size_t kvq_paged_chunk_workspace_bytes(const kvq_config *cfg);
  * [n_tokens][H_q][D], contiguous, overlapping none of the inputs.  Rows of the tensors
  * behind n_tokens are neither read nor written.  The cache is not changed.  Operands are
  * fp16 (dequantized keys and values and softmax weights are rounded to it once), sums and
- * softmax statistics fp32: an output is off by 3e-4 to 6e-4 of its size where
- * kvq_paged_decode_attn, which does not round the cached codes, is off by little more than
- * the output's own rounding, 2e-4.  For one token per slot that call is also the faster one
- * (eight slots of 17K to 56K tokens: 71 us against 139).
+ * softmax statistics fp32: an output is off by 3e-4 to 6e-4 of its size, of which 2e-4 is
+ * its own rounding (kvq_paged_decode_attn: 4.1e-4 to 4.3e-4 where this call is off by 3.5e-4
+ * to 4.0e-4).  For one token per slot that call is the faster one (eight slots of 17K to 56K
+ * tokens: 71 us against 139).
  * Infinite and NaN values reach the rows that see them and no others.  A packed key or value
  * that rounds beyond fp16's largest when dequantized counts as one of them: the rows of its
- * slot become infinite or NaN.  A page-table entry
- * that is no page is reported (KVQ_DEV_BAD_STATE) and page 0 read in its place.
+ * slot become infinite or NaN.  A page-table entry that is no page is reported
+ * (KVQ_DEV_BAD_STATE) and page 0 read in its place.
  * KVQ_ERR_UNSUPPORTED if the work of the call exceeds 2^30 units (4 for 128 keys of a key
  * head and 256 query rows: a 2048-token chunk of 8 key heads over 100 million tokens).
  * KVQ_ERR_INVALID_ARG if the cache's lengths are not those of the plan, or a slot with new
