@@ -15,7 +15,7 @@ from typing import Optional, Tuple
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "_build", "libkvq.so")
 
-KVQ_MODE_KIVI, KVQ_MODE_KITTY, KVQ_MODE_NVFP4 = 0, 1, 2
+KVQ_MODE_KIVI, KVQ_MODE_KITTY, KVQ_MODE_NVFP4, KVQ_MODE_E4M3, KVQ_MODE_INT8 = 0, 1, 2, 3, 4
 KVQ_DEV_TIMEOUT, KVQ_DEV_BAD_STATE = 1, 2  # device status-word bits
 STATUS = {0: "ok", -1: "invalid argument", -2: "unsupported configuration",
           -3: "capacity exceeded", -4: "workspace missing or too small", -5: "CUDA error",
@@ -145,7 +145,8 @@ def v_tile_tokens(cfg) -> int:
 def make_config(B, H_q, H_kv, D, G, bits, S=0, R=None, n_boost=0, mode="kivi", max_T=0,
                 v_bits=0, rope_base=0.0) -> Config:
     """rope_base > 0: keys are stored before RoPE and rotated in decode attention."""
-    m = {"kivi": KVQ_MODE_KIVI, "kitty": KVQ_MODE_KITTY, "nvfp4": KVQ_MODE_NVFP4}[mode]
+    m = {"kivi": KVQ_MODE_KIVI, "kitty": KVQ_MODE_KITTY, "nvfp4": KVQ_MODE_NVFP4, "e4m3": KVQ_MODE_E4M3,
+         "int8": KVQ_MODE_INT8}[mode]
     return Config(B, H_q, H_kv, D, G, bits, S, G if R is None else R, n_boost, m, v_bits or 0, max_T,
                   1 if rope_base else 0, float(rope_base or 0.0))
 
@@ -449,17 +450,18 @@ class KVQCache:
 
 
 class KVQPagedCache:
-    """A paged low-bit KV cache (KIVI mode): B batch slots of their own lengths over a
-    pool of n_pages physical pages, each holding one group of G tokens of all H_kv
-    heads of one slot.  The page table and the pool live in torch device memory; this
-    class keeps the free list on the host and writes the table rows a slot needs before
-    the library packs into them (prefill, flush).  ``max_T`` is the packed-token
-    capacity of one slot."""
+    """A paged low-bit KV cache: B batch slots of their own lengths over a pool of n_pages
+    physical pages, each holding one group of G tokens of all H_kv heads of one slot.  The
+    page table and the pool live in torch device memory; this class keeps the free list on
+    the host and writes the table rows a slot needs before the library packs into them
+    (prefill, flush).  ``max_T`` is the packed-token capacity of one slot.  mode: "kivi"
+    (min-max codes of 2, 4 or 8 bits), or "e4m3" and "int8" (bits=8): codes of that type with
+    one scale for each page and head, on their own for keys and values."""
 
-    def __init__(self, B, H_q, H_kv, D, G, bits, n_pages, max_T, S=0, R=None, device="cuda", v_bits=0):
+    def __init__(self, B, H_q, H_kv, D, G, bits, n_pages, max_T, S=0, R=None, device="cuda", v_bits=0, mode="kivi"):
         import torch
         self.torch = torch
-        self.cfg = make_config(B, H_q, H_kv, D, G, bits, S, R, 0, "kivi", max_T, v_bits)
+        self.cfg = make_config(B, H_q, H_kv, D, G, bits, S, R, 0, mode, max_T, v_bits)
         self.device = torch.device(device)
         self.n_pages = n_pages
         cp = ctypes.byref(self.cfg)
@@ -721,6 +723,14 @@ class KVQPagedCache:
         P, H, D, G = self.n_pages, cfg.H_kv, cfg.D, cfg.G
         kfpi, vfpi, Gv = 32 // cfg.bits, 32 // (cfg.v_bits or cfg.bits), min(G, D)
         b = self.buf[name]
+        if cfg.mode in (KVQ_MODE_E4M3, KVQ_MODE_INT8) and P > 0:
+            code = torch.float8_e4m3fn if cfg.mode == KVQ_MODE_E4M3 else torch.int8
+            if name == "k_codes":  # 16-byte chunk j of row t at position j ^ (4 * (t mod 2))
+                return b.view(code).view(P, H, G, D)
+            if name == "v_codes":
+                return b.view(code).view(P, H, G // 64, D, 64)
+            if name in ("k_meta", "v_meta"):  # the scales
+                return b.view(torch.float32).view(P, H, 4)[..., 0]
         if name == "k_codes":
             return b.view(torch.int32).view(P, H, G // kfpi, D)
         if name == "k_meta":

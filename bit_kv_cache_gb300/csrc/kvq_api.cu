@@ -223,7 +223,7 @@ int kvq_config_check(const kvq_config *c) {
         c->R < 0 || c->n_boost < 0)
         return KVQ_ERR_INVALID_ARG;
     if (c->mode != KVQ_MODE_KIVI && c->mode != KVQ_MODE_KITTY && c->mode != KVQ_MODE_NVFP4)
-        return KVQ_ERR_INVALID_ARG;
+        return block8(c) ? KVQ_ERR_UNSUPPORTED : KVQ_ERR_INVALID_ARG;
     if (nvfp4(c)) {
         if (c->bits != 4 || (c->v_bits != 0 && c->v_bits != 4)) return KVQ_ERR_UNSUPPORTED;
         if (c->G % 16 || c->D % 16 || c->G > 256) return KVQ_ERR_UNSUPPORTED;

@@ -1,0 +1,47 @@
+// kvq_block.h -- parameter blocks and launchers of the 8-bit caches with one scale per page and
+// head (kvq_block.cu, kvq_block_decode.cu); not part of the public ABI.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "kvq.h"
+#include "kvq_chunk.h"
+
+namespace kvq {
+
+// Pages of listed slots: page i of the call is page i % per of slot seq[i / per], and logical page
+// lp0[i / per] + i % per there.  Its rows come from the residual (the first nr of the stream) and
+// then from k_new, v_new, whose row row0 + t - nr of head h starts at h h_stride + that t stride.
+// commit: the slots' lengths become T + R and no residual.
+struct BlockListParams : ExtendParams {
+    int64_t h_stride;
+    int per, nr, row0, commit;
+    int16_t seq[KVQ_PAGED_MAX_B];
+    int32_t lp0[KVQ_PAGED_MAX_B];
+};
+
+// Decode attention.  A CTA is (key head, part of a slot): the slot's items, packed tiles of 64
+// tokens and then 16-token tiles of the fp16 tokens [sink | residual], are cut into equal parts.
+struct BlockDecodeParams {
+    const uint16_t *q;
+    uint16_t *out;
+    const uint8_t *k_codes, *v_codes;
+    const float4 *k_scale, *v_scale;     // a page's scale in the first component
+    const uint16_t *k_sink, *v_sink, *k_res, *v_res;
+    const int32_t *ptab, *lens;
+    float *part_o;                       // [parts][H_kv][g][128], of slots in several parts
+    float2 *part_ml;                     // [parts][H_kv][g]
+    int32_t *status;
+    int64_t n_pages;
+    int B, H_kv, g, g_shift, S, R, ptab_stride;  // g_shift: log2(G)
+    int32_t part0[KVQ_PAGED_MAX_B + 1];  // parts of the slots before each
+};
+
+cudaError_t launch_block_extend(const ExtendParams &p, bool e4m3, cudaStream_t st);
+cudaError_t launch_block_list(const BlockListParams &p, bool e4m3, cudaStream_t st);
+size_t block_decode_ws_bytes(const kvq_config *c);
+int block_decode(const kvq_config *c, const kvq_paged *pc, const uint16_t *q, uint16_t *out, void *ws, size_t ws_bytes,
+                 cudaStream_t st);
+
+}  // namespace kvq

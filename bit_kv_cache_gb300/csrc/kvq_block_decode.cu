@@ -1,0 +1,351 @@
+// kvq_block_decode.cu -- attention of one token per slot over an 8-bit cache with one scale per
+// page and head (kvq_paged_decode_attn).
+//
+// For head e of a key head's group and token t, with the page's scales s_K and s_V,
+//   y_t = (q . code_t) s_K log2(e) / sqrt(D) + log2(s_V),   w_t = 2^(y_t - m),
+//   O = sum w_t code_t,   l = sum w_t / s_V,   out = O / l:
+// the value scale is part of the exponent, so both products have exact operands (codes in fp16)
+// and only w is rounded to fp16, once.  Sums, m and l are fp32; m follows the running maximum with
+// up to kSlack of lag, which keeps w below fp16's largest value and O unscaled in most steps.
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+#include <string.h>
+
+#include <algorithm>
+
+#include "kvq_block.cuh"
+#include "kvq_block.h"
+#include "kvq_host.h"
+#include "kvq_tcgen05.cuh"
+
+namespace kvq {
+
+namespace {
+
+constexpr int kWarps = 4, kThreads = 32 * kWarps;
+constexpr int kTokens = 64, kTailTokens = 16;            // of an item: packed, fp16
+constexpr float kScoreScale = 1.4426950408889634f * 0.08838834764831845f;  // log2(e) / sqrt(128)
+constexpr float kUp = 6.f, kSlack = 8.f;                 // w <= 2^(kUp + kSlack); small weights stay normal numbers
+
+// A warp's state: lane (r, c) = (lane / 4, lane % 4) has heads 2 c, 2 c + 1 (columns of the
+// products) and, of the output, channels of rows r and r + 8 of eight 16-row tiles.
+struct State {
+    float m[2], l[2];   // l: the lane's own share
+    float o[8][4];
+};
+
+// The channel of output row r (hi: r + 8) of tile i.
+__device__ __forceinline__ int out_channel(int i, int r, int hi) { return 32 * (i >> 1) + 8 * (r >> 1) + 4 * (i & 1) + 2 * hi + (r & 1); }
+
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+    uint32_t y;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
+// Scores of 16 N tokens (x[s]: rows r and r + 8 of group s, heads 2 c, 2 c + 1) to weights, as B
+// operands of the value product.  a, lsv: y = x a + lsv; inv: 1 / s_V.
+template <int N>
+__device__ __forceinline__ void weights(State &st, float (&x)[N][4], float a, float lsv, float inv, uint32_t (&b)[N][2]) {
+#pragma unroll
+    for (int s = 0; s < N; s++)
+#pragma unroll
+        for (int e = 0; e < 4; e++) x[s][e] = fmaf(x[s][e], a, lsv);
+    float top[2];
+#pragma unroll
+    for (int e = 0; e < 2; e++) {
+        top[e] = fmaxf(x[0][e], x[0][2 + e]);
+#pragma unroll
+        for (int s = 1; s < N; s++) top[e] = fmaxf(top[e], fmaxf(x[s][e], x[s][2 + e]));
+    }
+    if (__any_sync(0xffffffffu, top[0] > st.m[0] + kSlack || top[1] > st.m[1] + kSlack)) {
+#pragma unroll
+        for (int e = 0; e < 2; e++) {
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], o));
+            const float m = fmaxf(st.m[e], top[e]), f = m == st.m[e] ? 1.f : ex2(st.m[e] - m);
+            st.m[e] = m;
+            st.l[e] *= f;
+#pragma unroll
+            for (int i = 0; i < 8; i++) {
+                st.o[i][e] *= f;
+                st.o[i][2 + e] *= f;
+            }
+        }
+    }
+    const float off[2] = {st.m[0] == -INFINITY ? 0.f : kUp - st.m[0], st.m[1] == -INFINITY ? 0.f : kUp - st.m[1]};
+    float sum[2] = {0.f, 0.f};
+#pragma unroll
+    for (int s = 0; s < N; s++) {
+#pragma unroll
+        for (int e = 0; e < 4; e++) {
+            x[s][e] = ex2(x[s][e] + off[e & 1]);
+            sum[e & 1] += x[s][e];
+        }
+        b[s][0] = transpose8(pack_half2(x[s][0], x[s][1]));
+        b[s][1] = transpose8(pack_half2(x[s][2], x[s][3]));
+    }
+    st.l[0] = fmaf(sum[0], inv, st.l[0]);
+    st.l[1] = fmaf(sum[1], inv, st.l[1]);
+}
+
+// A packed tile.  The order of the contracted dimension is free as long as both operands share
+// it.  Keys: lane c's words of a row are its 16-byte chunks c and c + 4, so a word (four
+// neighbouring channels) is one step's operand; q is held in that order.  Values: a lane's 16 bytes
+// are 16 neighbouring tokens of a channel, word s those of step s: step s takes tokens 16 c + 4 s
+// .. + 3 of every c, and the score rows are arranged so.
+template <bool E4M3>
+__device__ __forceinline__ void packed_tile(State &st, const uint32_t (&q)[8][2], const uint8_t *k, const uint8_t *v, float sk, float sv,
+                                            int lane) {
+    const int r = lane >> 2, c = lane & 3;
+    float x[4][4];
+#pragma unroll
+    for (int s = 0; s < 4; s++) {
+        const uint8_t *row = k + (16 * (r >> 1) + 4 * s + (r & 1)) * 128 + c * 16;
+        const int near = (r & 1) << 6, far = 64 - near;
+        uint4 w[2][2];
+        w[0][0] = *reinterpret_cast<const uint4 *>(row + near);
+        w[0][1] = *reinterpret_cast<const uint4 *>(row + far);
+        w[1][0] = *reinterpret_cast<const uint4 *>(row + 256 + near);
+        w[1][1] = *reinterpret_cast<const uint4 *>(row + 256 + far);
+#pragma unroll
+        for (int e = 0; e < 4; e++) x[s][e] = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+            uint32_t a[4];
+            code_pairs<E4M3>((&w[0][i >> 2].x)[i & 3], a[0], a[2]);
+            code_pairs<E4M3>((&w[1][i >> 2].x)[i & 3], a[1], a[3]);
+            mma_16816(x[s], a[0], a[1], a[2], a[3], q[i][0], q[i][1]);
+        }
+    }
+    uint32_t b[4][2];
+    weights<4>(st, x, kScoreScale * sk, log2f(sv), 1.f / sv, b);
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+        const uint4 lo = *reinterpret_cast<const uint4 *>(v + out_channel(i, r, 0) * 64 + c * 16);
+        const uint4 hi = *reinterpret_cast<const uint4 *>(v + out_channel(i, r, 1) * 64 + c * 16);
+#pragma unroll
+        for (int s = 0; s < 4; s++) {
+            uint32_t a[4];
+            code_pairs<E4M3>((&lo.x)[s], a[0], a[2]);
+            code_pairs<E4M3>((&hi.x)[s], a[1], a[3]);
+            mma_16816(st.o[i], a[0], a[1], a[2], a[3], b[s][0], b[s][1]);
+        }
+    }
+}
+
+// 16 fp16 tokens, n of which exist: rows r and r + 8 (k0, k1, v0, v1).  A value row's 8 channels
+// 32 j + 8 c .. of lane c are turned into operand rows by 8 x 8 transposes.
+__device__ __forceinline__ void tail_tile(State &st, const uint32_t (&q)[8][2], const uint16_t *k0, const uint16_t *k1,
+                                          const uint16_t *v0, const uint16_t *v1, int n, int lane) {
+    const int r = lane >> 2, c = lane & 3;
+    const bool on0 = r < n, on1 = r + 8 < n;
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+    float x[1][4] = {{0.f, 0.f, 0.f, 0.f}};
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        const int ch = (i >> 1) * 64 + c * 16 + (i & 1) * 8;
+        const uint4 a = on0 ? *reinterpret_cast<const uint4 *>(k0 + ch) : zero, b = on1 ? *reinterpret_cast<const uint4 *>(k1 + ch) : zero;
+        mma_16816(x[0], a.x, b.x, a.y, b.y, q[2 * i][0], q[2 * i][1]);
+        mma_16816(x[0], a.z, b.z, a.w, b.w, q[2 * i + 1][0], q[2 * i + 1][1]);
+    }
+    if (!on0) x[0][0] = x[0][1] = -INFINITY;
+    if (!on1) x[0][2] = x[0][3] = -INFINITY;
+    uint32_t b[1][2];
+    weights<1>(st, x, kScoreScale, 0.f, 1.f, b);
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
+        const uint4 x0 = on0 ? *reinterpret_cast<const uint4 *>(v0 + 32 * j + 8 * c) : zero;
+        const uint4 x1 = on1 ? *reinterpret_cast<const uint4 *>(v1 + 32 * j + 8 * c) : zero;
+        mma_16816(st.o[2 * j], transpose8(x0.x), transpose8(x0.y), transpose8(x1.x), transpose8(x1.y), b[0][0], b[0][1]);
+        mma_16816(st.o[2 * j + 1], transpose8(x0.z), transpose8(x0.w), transpose8(x1.z), transpose8(x1.w), b[0][0], b[0][1]);
+    }
+}
+
+__device__ __forceinline__ float factor(float m, float top) { return m == top ? 1.f : ex2(m - top); }
+
+template <bool E4M3>
+__global__ void __launch_bounds__(kThreads) block_decode_kernel(const __grid_constant__ BlockDecodeParams p) {
+    __shared__ float s_o[kWarps][8][128];
+    __shared__ float s_m[kWarps][8], s_l[kWarps][8];
+    const int h = blockIdx.x, w = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
+    griddep_wait();
+    int lo = 0, hi = p.B - 1;  // the slot
+    while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (p.part0[mid + 1] > (int)blockIdx.y) hi = mid;
+        else lo = mid + 1;
+    }
+    const int b = lo, parts = p.part0[b + 1] - p.part0[b], part = blockIdx.y - p.part0[b];
+    const int4 ln = reinterpret_cast<const int4 *>(p.lens)[b];
+    const int np = ln.y / kTokens, seen = ln.x + ln.z, n = np + (seen + kTailTokens - 1) / kTailTokens;
+    const int begin = (int)((int64_t)n * part / parts), end = (int)((int64_t)n * (part + 1) / parts);
+    const size_t u = (size_t)b * p.H_kv + h;
+    uint32_t q[8][2];
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        uint4 x = make_uint4(0, 0, 0, 0);
+        if (r < p.g) x = *reinterpret_cast<const uint4 *>(p.q + (u * p.g + r) * 128 + (i >> 1) * 64 + c * 16 + (i & 1) * 8);
+        q[2 * i][0] = x.x, q[2 * i][1] = x.y, q[2 * i + 1][0] = x.z, q[2 * i + 1][1] = x.w;
+    }
+    State st;
+#pragma unroll
+    for (int e = 0; e < 2; e++) st.m[e] = -INFINITY, st.l[e] = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; i++)
+#pragma unroll
+        for (int e = 0; e < 4; e++) st.o[i][e] = 0.f;
+    const int32_t *row = p.ptab + (size_t)b * p.ptab_stride;
+    for (int i = begin + w; i < end; i += kWarps) {
+        if (i < np) {
+            int page = row[(i * kTokens) >> p.g_shift];
+            if (page < 0 || page >= p.n_pages) {
+                if (lane == 0) report(p.status, KVQ_DEV_BAD_STATE);
+                page = 0;
+            }
+            const size_t pg = (size_t)page * p.H_kv + h;
+            const size_t at = ((pg << p.g_shift) + ((i * kTokens) & ((1 << p.g_shift) - 1))) * 128;
+            packed_tile<E4M3>(st, q, p.k_codes + at, p.v_codes + at, p.k_scale[pg].x, p.v_scale[pg].x, lane);
+        } else {
+            const int x = (i - np) * kTailTokens;
+            auto at = [&](const uint16_t *sink, const uint16_t *res, int t) {
+                t = min(t, seen - 1);
+                return t < ln.x ? sink + (u * p.S + t) * 128 : res + (u * p.R + t - ln.x) * 128;
+            };
+            tail_tile(st, q, at(p.k_sink, p.k_res, x + r), at(p.k_sink, p.k_res, x + r + 8), at(p.v_sink, p.v_res, x + r),
+                      at(p.v_sink, p.v_res, x + r + 8), seen - x, lane);
+        }
+    }
+    // the warps' states, joined in warp order
+#pragma unroll
+    for (int e = 0; e < 2; e++) {
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) st.l[e] += __shfl_xor_sync(0xffffffffu, st.l[e], o);
+        if (r == 0) {
+            s_m[w][2 * c + e] = st.m[e];
+            s_l[w][2 * c + e] = st.l[e];
+        }
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+            s_o[w][2 * c + e][out_channel(i, r, 0)] = st.o[i][e];
+            s_o[w][2 * c + e][out_channel(i, r, 1)] = st.o[i][2 + e];
+        }
+    }
+    __syncthreads();
+    const int d = threadIdx.x;
+    for (int e = 0; e < p.g; e++) {
+        float m = s_m[0][e], l = 0.f, o = 0.f;
+#pragma unroll
+        for (int i = 1; i < kWarps; i++) m = fmaxf(m, s_m[i][e]);
+#pragma unroll
+        for (int i = 0; i < kWarps; i++) {
+            const float f = factor(s_m[i][e], m);
+            l = fmaf(f, s_l[i][e], l);
+            o = fmaf(f, s_o[i][e][d], o);
+        }
+        if (parts == 1) {
+            p.out[(u * p.g + e) * 128 + d] = __half_as_ushort(__float2half_rn(o / l));
+        } else {
+            const size_t at = ((size_t)blockIdx.y * p.H_kv + h) * p.g + e;
+            p.part_o[at * 128 + d] = o;
+            if (d == 0) p.part_ml[at] = make_float2(m, l);
+        }
+    }
+}
+
+// Slots in several parts: a CTA per (query head of a key head, key head, slot).
+__global__ void __launch_bounds__(128) block_combine_kernel(const __grid_constant__ BlockDecodeParams p) {
+    const int e = blockIdx.x % p.g, h = blockIdx.x / p.g, b = blockIdx.y, d = threadIdx.x;
+    const int first = p.part0[b], parts = p.part0[b + 1] - first;
+    if (parts < 2) return;
+    griddep_wait();
+    const size_t step = (size_t)p.H_kv * p.g, at = ((size_t)first * p.H_kv + h) * p.g + e;
+    float m = -INFINITY;
+    for (int i = 0; i < parts; i++) m = fmaxf(m, p.part_ml[at + i * step].x);
+    float l = 0.f, o = 0.f;
+    for (int i = 0; i < parts; i++) {
+        const float2 ml = p.part_ml[at + i * step];
+        const float f = factor(ml.x, m);
+        l = fmaf(f, ml.y, l);
+        o = fmaf(f, p.part_o[(at + i * step) * 128 + d], o);
+    }
+    p.out[(((size_t)b * p.H_kv + h) * p.g + e) * 128 + d] = __half_as_ushort(__float2half_rn(o / l));
+}
+
+// CTAs that run at once, and the most parts of a call: each of them and one more per slot.
+int resident() { return 2 * host::num_sms(); }
+int64_t most_parts(const kvq_config *c) { return host::cdiv(resident(), c->H_kv) + c->B; }
+
+size_t ml_bytes(const kvq_config *c) { return (size_t)host::cdiv(most_parts(c) * c->H_q * 8, 256) * 256; }
+
+}  // namespace
+
+size_t block_decode_ws_bytes(const kvq_config *c) { return 256 + ml_bytes(c) + (size_t)most_parts(c) * c->H_q * 128 * 4; }
+
+int block_decode(const kvq_config *c, const kvq_paged *pc, const uint16_t *q, uint16_t *out, void *ws, size_t ws_bytes,
+                 cudaStream_t st) {
+    if (!ws || !host::aligned16(ws) || ws_bytes < block_decode_ws_bytes(c)) return KVQ_ERR_WORKSPACE;
+    BlockDecodeParams p;
+    memset(&p, 0, sizeof(p));
+    char *w = static_cast<char *>(ws);
+    p.status = reinterpret_cast<int32_t *>(w);
+    p.part_ml = reinterpret_cast<float2 *>(w + 256);
+    p.part_o = reinterpret_cast<float *>(w + 256 + ml_bytes(c));
+    p.q = q;
+    p.out = out;
+    p.k_codes = reinterpret_cast<const uint8_t *>(pc->k_codes);
+    p.v_codes = reinterpret_cast<const uint8_t *>(pc->v_codes);
+    p.k_scale = reinterpret_cast<const float4 *>(pc->k_meta);
+    p.v_scale = reinterpret_cast<const float4 *>(pc->v_meta);
+    p.k_sink = pc->k_sink;
+    p.v_sink = pc->v_sink;
+    p.k_res = pc->k_res;
+    p.v_res = pc->v_res;
+    p.ptab = pc->page_table;
+    p.lens = pc->lens;
+    p.n_pages = pc->n_pages;
+    p.B = c->B;
+    p.H_kv = c->H_kv;
+    p.g = c->H_q / c->H_kv;
+    p.g_shift = c->G == 64 ? 6 : c->G == 128 ? 7 : 8;
+    p.S = c->S;
+    p.R = c->R;
+    p.ptab_stride = (int)(c->max_T / c->G);
+    int items[KVQ_PAGED_MAX_B], longest = 0, active = 0;
+    for (int b = 0; b < c->B; b++) {
+        const int32_t *l = pc->lens_host + 4 * b;
+        items[b] = l[3] ? l[1] / kTokens + (l[0] + l[2] + kTailTokens - 1) / kTailTokens : 0;
+        if (l[3] && l[1] && pc->n_pages < 1) return KVQ_ERR_INVALID_ARG;  // page 0 stands in for bad entries
+        longest = std::max(longest, items[b]);
+        active += items[b] > 0;
+    }
+    if (!active) return KVQ_OK;
+    // parts of at most X items, the smallest X whose parts are all resident at once (a part each
+    // where there are more slots than that)
+    const int64_t room = std::max<int64_t>(active, host::cdiv(resident(), c->H_kv));
+    int lo = 1, hi = longest;
+    while (lo < hi) {
+        const int X = (lo + hi) / 2;
+        int64_t parts = 0;
+        for (int b = 0; b < c->B; b++) parts += (items[b] + X - 1) / X;
+        if (parts <= room) hi = X;
+        else lo = X + 1;
+    }
+    bool cut = false;
+    int parts = 0;
+    for (int b = 0; b < c->B; b++) {
+        p.part0[b] = parts;
+        const int n = (items[b] + lo - 1) / lo;
+        cut |= n > 1;
+        parts += n;
+    }
+    for (int b = c->B; b <= KVQ_PAGED_MAX_B; b++) p.part0[b] = parts;
+    const dim3 grid((unsigned)c->H_kv, (unsigned)parts);
+    cudaError_t e = c->mode == KVQ_MODE_E4M3 ? launch_dependent(block_decode_kernel<true>, grid, kThreads, 0, st, p)
+                                             : launch_dependent(block_decode_kernel<false>, grid, kThreads, 0, st, p);
+    if (e == cudaSuccess && cut) e = launch_dependent(block_combine_kernel, dim3((unsigned)c->H_q, (unsigned)c->B), 128, 0, st, p);
+    return host::status_of(e);
+}
+
+}  // namespace kvq

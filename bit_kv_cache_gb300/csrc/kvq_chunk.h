@@ -35,6 +35,8 @@ struct ExtendParams {
     int64_t n_pages;
     int B, H_kv, G, S, R, TV, ptab_stride;
     int n_pack;                          // pages to pack, over all slots
+    int once;                            // one page holds all old residual rows of a slot, so that the CTA that packs
+                                         // it may overwrite them: then one launch does the whole call
     int32_t page0[KVQ_PAGED_MAX_B + 1];  // of the slots before each
 };
 
@@ -85,6 +87,7 @@ struct ChunkAttnParams {
 
 cudaError_t launch_plan(const PlanParams &p, cudaStream_t st);
 cudaError_t launch_extend(const ExtendParams &p, int kbits, int vbits, cudaStream_t st);
+cudaError_t launch_extend_tail(const ExtendParams &p, cudaStream_t st);  // fp16 rows and lengths of every slot
 cudaError_t launch_qk(const QkParams &p, int D, cudaStream_t st);
 cudaError_t launch_chunk_attn(const ChunkAttnParams &p, cudaStream_t st);
 
@@ -116,7 +119,7 @@ constexpr int kChunkKeys = 128;          // tokens per key tile
 __host__ __device__ inline int chunk_tiles(const ChunkSlot &s, int t, int rows, int g) {
     const int last = ((t + 1) * rows - 1) / g + 1;                 // new tokens up to the tile's last
     const int seen = s.ns + s.nr + (last < s.n_new ? last : s.n_new);
-    return s.T / kChunkKeys + (seen + kChunkKeys - 1) / kChunkKeys;
+    return (s.T + kChunkKeys - 1) / kChunkKeys + (seen + kChunkKeys - 1) / kChunkKeys;
 }
 
 }  // namespace kvq

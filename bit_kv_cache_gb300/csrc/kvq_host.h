@@ -25,6 +25,8 @@ inline int gv_of(const kvq_config *c) { return std::min(c->G, c->D); }
 inline int vtile_of(const kvq_config *c) { return v_tile_tokens(c->mode == KVQ_MODE_KITTY ? 2 : c->bits, c->G); }
 inline bool kitty(const kvq_config *c) { return c->mode == KVQ_MODE_KITTY; }
 inline bool nvfp4(const kvq_config *c) { return c->mode == KVQ_MODE_NVFP4; }
+// 8-bit codes with one scale per page and head (paged caches only)
+inline bool block8(const kvq_config *c) { return c->mode == KVQ_MODE_E4M3 || c->mode == KVQ_MODE_INT8; }
 inline int64_t nvfp4_page_bytes(const kvq_config *c) { return 16 + (int64_t)c->G * c->D / 16; }
 inline int64_t cap_k(const kvq_config *c) { return kitty(c) ? c->G : c->R; }
 inline int64_t cap_v(const kvq_config *c) { return kitty(c) ? c->G : c->R; }

@@ -15,6 +15,7 @@
 #include <vector>
 
 #include "kvq.h"
+#include "kvq_block.h"
 #include "kvq_host.h"
 #include "kvq_internal.h"
 
@@ -24,8 +25,23 @@ using namespace kvq::host;
 namespace kvq {
 namespace host {
 
+// The 8-bit modes with a scale per page and head.
+static int block_cfg_check(const kvq_config *c) {
+    if (c->B <= 0 || c->H_q <= 0 || c->H_kv <= 0 || c->max_T < 0 || c->S < 0 || c->n_boost != 0 || c->H_q % c->H_kv)
+        return KVQ_ERR_INVALID_ARG;
+    if (c->D != 128 || c->H_q / c->H_kv > 8 || (c->G != 64 && c->G != 128 && c->G != 256)) return KVQ_ERR_UNSUPPORTED;
+    if (c->bits != 8 || (c->v_bits != 0 && c->v_bits != 8) || c->rope) return KVQ_ERR_UNSUPPORTED;
+    if (c->R < c->G || c->R % c->G || c->max_T % c->G) return KVQ_ERR_INVALID_ARG;
+    return KVQ_OK;
+}
+
 // KIVI mode on the decode tiles: D is 128 and G 128 or 256 then.
 int paged_cfg_check(const kvq_config *c) {
+    if (c && block8(c)) {
+        const int e = block_cfg_check(c);
+        if (e) return e;
+        return c->B > KVQ_PAGED_MAX_B ? KVQ_ERR_UNSUPPORTED : c->max_T / c->G < 1 ? KVQ_ERR_INVALID_ARG : KVQ_OK;
+    }
     const int e = kvq_config_check(c);
     if (e) return e;
     if (c->mode != KVQ_MODE_KIVI || c->rope || !fast_supported(c) || c->B > KVQ_PAGED_MAX_B) return KVQ_ERR_UNSUPPORTED;
@@ -125,6 +141,30 @@ QuantVParams qv_paged(const kvq_config *c, const kvq_paged *pc) {
     return p;
 }
 
+BlockListParams block_list(const kvq_config *c, const kvq_paged *pc) {
+    BlockListParams p;
+    memset(&p, 0, sizeof(p));
+    p.lens = pc->lens;
+    p.status = pc->status;
+    p.k_sink = pc->k_sink;
+    p.v_sink = pc->v_sink;
+    p.k_res = pc->k_res;
+    p.v_res = pc->v_res;
+    p.k_codes = pc->k_codes;
+    p.v_codes = pc->v_codes;
+    p.k_meta = pc->k_meta;
+    p.v_meta = pc->v_meta;
+    p.ptab = pc->page_table;
+    p.n_pages = pc->n_pages;
+    p.B = c->B;
+    p.H_kv = c->H_kv;
+    p.G = c->G;
+    p.S = c->S;
+    p.R = c->R;
+    p.ptab_stride = (int)max_pages(c);
+    return p;
+}
+
 // Rows [r0, r0 + n) of a one-sequence source [H_kv][L0][D] -> rows [0, n) of batch
 // slot b's buffer [U][rows][D].
 cudaError_t copy_slot_rows(const kvq_config *c, const uint16_t *src, int64_t L0, int64_t r0, uint16_t *dst,
@@ -168,6 +208,7 @@ extern "C" {
 size_t kvq_paged_bytes(const kvq_config *c, int64_t n_pages, int which) {
     if (paged_cfg_check(c) != KVQ_OK || n_pages < 0) return 0;
     const size_t P = (size_t)n_pages, H = (size_t)c->H_kv, D = c->D, G = c->G, U = (size_t)units(c);
+    if (block8(c) && (which == 3 || which == 5)) return P * H * 16;
     switch (which) {
         case 0: return P * H * (G / kfpi(c)) * D * 4;
         case 3: return P * H * D * 4;
@@ -202,7 +243,17 @@ int kvq_paged_prefill(const kvq_config *c, kvq_paged *pc, int b, const uint16_t 
     cudaError_t ce = cudaSuccess;
     if (ns > 0) ce = copy_slot_rows(c, k, L0, 0, pc->k_sink, c->S, b, ns, st);
     if (ce == cudaSuccess && ns > 0) ce = copy_slot_rows(c, v, L0, 0, pc->v_sink, c->S, b, ns, st);
-    if (ce == cudaSuccess && T > 0) {
+    if (ce == cudaSuccess && T > 0 && block8(c)) {
+        BlockListParams p = block_list(c, pc);
+        p.k_new = k;
+        p.v_new = v;
+        p.k_stride = p.v_stride = c->D;
+        p.h_stride = L0 * c->D;
+        p.row0 = (int)ns;
+        p.per = p.n_pack = (int)(T / c->G);
+        p.seq[0] = (int16_t)b;
+        ce = launch_block_list(p, c->mode == KVQ_MODE_E4M3, st);
+    } else if (ce == cudaSuccess && T > 0) {
         QuantKParams p = qk_paged(c, pc);
         p.src = k;
         p.src_ustride = L0 * c->D;
@@ -297,7 +348,23 @@ int kvq_paged_flush(const kvq_config *c, kvq_paged *pc, int *n_flushed, void *st
         }
     }
     cudaStream_t st = (cudaStream_t)stream;
-    for (size_t i0 = 0; i0 < list.size(); i0 += kMaxListSeq) {
+    if (block8(c) && !list.empty()) {
+        BlockListParams p = block_list(c, pc);
+        p.nr = c->R;
+        p.per = c->R / c->G;
+        p.n_pack = p.per * (int)list.size();
+        p.commit = 1;
+        for (size_t i = 0; i < list.size(); i++) {
+            p.seq[i] = (int16_t)list[i];
+            p.lp0[i] = pc->lens_host[4 * list[i] + 1] / c->G;
+        }
+        if (launch_block_list(p, c->mode == KVQ_MODE_E4M3, st) != cudaSuccess) return KVQ_ERR_CUDA;
+        for (int b : list) {
+            pc->lens_host[4 * b + 1] += c->R;
+            pc->lens_host[4 * b + 2] = 0;
+        }
+    }
+    for (size_t i0 = 0; !block8(c) && i0 < list.size(); i0 += kMaxListSeq) {
         const int n = (int)std::min<size_t>(kMaxListSeq, list.size() - i0);
         QuantKParams p = qk_paged(c, pc);
         p.src = pc->k_res;
@@ -344,7 +411,7 @@ int kvq_paged_release(const kvq_config *c, kvq_paged *pc, int b, void *stream) {
 
 size_t kvq_paged_workspace_bytes(const kvq_config *c) {
     if (paged_cfg_check(c) != KVQ_OK) return 0;
-    return paged_ws_layout(c).total;
+    return block8(c) ? block_decode_ws_bytes(c) : paged_ws_layout(c).total;
 }
 
 int kvq_paged_decode_attn(const kvq_config *c, const kvq_paged *pc, const uint16_t *q, uint16_t *out, void *ws,
@@ -352,6 +419,7 @@ int kvq_paged_decode_attn(const kvq_config *c, const kvq_paged *pc, const uint16
     int e = check_paged(c, pc);
     if (e) return e;
     if (!q || !out || !aligned16(q) || !aligned16(out)) return KVQ_ERR_INVALID_ARG;
+    if (block8(c)) return block_decode(c, pc, q, out, ws, ws_bytes, (cudaStream_t)stream);
     const PagedWs wl = paged_ws_layout(c);
     if (!ws || !aligned16(ws) || ws_bytes < wl.total) return KVQ_ERR_WORKSPACE;
 

@@ -63,7 +63,7 @@ typedef enum {
     KVQ_ERR_DEVICE = -6        /* a kernel reported an error in the status word   */
 } kvq_status;
 
-enum { KVQ_MODE_KIVI = 0, KVQ_MODE_KITTY = 1, KVQ_MODE_NVFP4 = 2 };
+enum { KVQ_MODE_KIVI = 0, KVQ_MODE_KITTY = 1, KVQ_MODE_NVFP4 = 2, KVQ_MODE_E4M3 = 3, KVQ_MODE_INT8 = 4 };
 
 /* Device status bits (see kvq_read_status). */
 enum { KVQ_DEV_TIMEOUT = 1, KVQ_DEV_BAD_STATE = 2 };
