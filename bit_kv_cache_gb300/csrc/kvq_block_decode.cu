@@ -25,7 +25,6 @@ namespace {
 
 constexpr int kWarps = 4, kThreads = 32 * kWarps;
 constexpr int kTokens = 64, kTailTokens = 16;            // of an item: packed, fp16
-constexpr float kScoreScale = 1.4426950408889634f * 0.08838834764831845f;  // log2(e) / sqrt(128)
 constexpr float kUp = 6.f, kSlack = 8.f;                 // w <= 2^(kUp + kSlack); small weights stay normal numbers
 
 // A warp's state: lane (r, c) = (lane / 4, lane % 4) has heads 2 c, 2 c + 1 (columns of the
@@ -120,7 +119,7 @@ __device__ __forceinline__ void packed_tile(State &st, const uint32_t (&q)[8][2]
         }
     }
     uint32_t b[4][2];
-    weights<4>(st, x, kScoreScale * sk, log2f(sv), 1.f / sv, b);
+    weights<4>(st, x, kScale * sk, log2f(sv), 1.f / sv, b);
 #pragma unroll
     for (int i = 0; i < 8; i++) {
         const uint4 lo = *reinterpret_cast<const uint4 *>(v + out_channel(i, r, 0) * 64 + c * 16);
@@ -153,7 +152,7 @@ __device__ __forceinline__ void tail_tile(State &st, const uint32_t (&q)[8][2], 
     if (!on0) x[0][0] = x[0][1] = -INFINITY;
     if (!on1) x[0][2] = x[0][3] = -INFINITY;
     uint32_t b[1][2];
-    weights<1>(st, x, kScoreScale, 0.f, 1.f, b);
+    weights<1>(st, x, kScale, 0.f, 1.f, b);
 #pragma unroll
     for (int j = 0; j < 4; j++) {
         const uint4 x0 = on0 ? *reinterpret_cast<const uint4 *>(v0 + 32 * j + 8 * c) : zero;

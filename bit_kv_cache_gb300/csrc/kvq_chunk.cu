@@ -670,7 +670,10 @@ int kvq_paged_chunk_attn(const kvq_config *c, const kvq_paged *pc, kvq_chunk *ch
     p.cost = (int)cost;
     p.C = (int)std::min<int64_t>(items, std::min(num_sms(), kMaxRanges));
     if (!unit_ranges(c, slots_of(ch), units, p)) even_ranges(c, slots_of(ch), p);
-    if (launch_chunk_attn(p, (cudaStream_t)stream) != cudaSuccess) return KVQ_ERR_CUDA;
+    p.ref_unit = block8(c) ? 1.f : kScale;
+    if ((block8(c) ? launch_chunk_attn_block(p, c->mode == KVQ_MODE_E4M3, (cudaStream_t)stream)
+                   : launch_chunk_attn(p, (cudaStream_t)stream)) != cudaSuccess)
+        return KVQ_ERR_CUDA;
     if (!ch->captured && capturing((cudaStream_t)stream)) ch->captured = 1;
     return KVQ_OK;
 }

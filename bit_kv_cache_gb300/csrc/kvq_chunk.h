@@ -50,6 +50,8 @@ struct QkParams {
     uint64_t turn[128];                  // base^(-2j/rotary) / (2 pi) in units of 2^-64 turns
 };
 
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kScale = kLog2e * 0.08838834764831845f;  // log2(e) / sqrt(128)
 constexpr int kNarrowRows = 128, kWideRows = 256, kNarrowCost = 3, kWideCost = 4, kUnitItems = 5, kCombineCost = 6, kPartItems = 2, kMaxRanges = 256;
 
 // Chunk attention.  A unit is (slot, key head, tile of query rows): row r of a slot is its
@@ -74,7 +76,8 @@ struct ChunkAttnParams {
     const uint16_t *q, *k_new, *v_new;
     uint16_t *out;
     float *part_o;                       // [2 C][kWideRows][128]
-    float2 *part_ml;                     // [2 C][kWideRows] (reference: a score before the scale, sum)
+    float2 *part_ml;                     // [2 C][kWideRows] (reference, sum)
+    float ref_unit;                      // of a reference, as an exponent: a score before the scale, or 1
     int32_t *status;
     int64_t q_stride, k_stride, v_stride, n_pages;
     int B, H_kv, g, G, kbits, vbits, S, R, ptab_stride;
@@ -90,6 +93,7 @@ cudaError_t launch_extend(const ExtendParams &p, int kbits, int vbits, cudaStrea
 cudaError_t launch_extend_tail(const ExtendParams &p, cudaStream_t st);  // fp16 rows and lengths of every slot
 cudaError_t launch_qk(const QkParams &p, int D, cudaStream_t st);
 cudaError_t launch_chunk_attn(const ChunkAttnParams &p, cudaStream_t st);
+cudaError_t launch_chunk_attn_block(const ChunkAttnParams &p, bool e4m3, cudaStream_t st);
 
 __host__ __device__ inline bool chunk_narrow(int n_new, int g) { return (int64_t)n_new * g <= kNarrowRows; }
 // Copies of a narrow unit's rows in its query tile.

@@ -17,9 +17,10 @@ struct Part {
 };
 // The factor of a part below the maximum; positive, as an infinite value in it stays infinite
 // (2^-126 of a finite part is far below the other's smallest step).
-__device__ __forceinline__ float factor(float m, float top) { return m == top ? 1.f : fmaxf(exp2f((m - top) * kScale), 0x1p-126f); }
-__device__ __forceinline__ void join(Part &a, const Part &b) {
-    const float m = fmaxf(a.m, b.m), x = factor(a.m, m), y = factor(b.m, m);
+// unit: of the references, as an exponent.
+__device__ __forceinline__ float factor(float m, float top, float unit) { return m == top ? 1.f : fmaxf(exp2f((m - top) * unit), 0x1p-126f); }
+__device__ __forceinline__ void join(Part &a, const Part &b, float unit) {
+    const float m = fmaxf(a.m, b.m), x = factor(a.m, m, unit), y = factor(b.m, m, unit);
     a.m = m;
     a.l = x * a.l + y * b.l;
     a.o.x = x * a.o.x + y * b.o.x;
@@ -73,12 +74,12 @@ __device__ __forceinline__ void combine_narrow(const ChunkAttnParams &p, int h, 
         Part acc = kNone;
         for (int i = w; i < parts * rep; i += 8) {
             const int k = i / rep;
-            join(acc, load_part(p, (size_t)s_slot[k] * kWideRows + (i - k * rep) * R + row, lane));
+            join(acc, load_part(p, (size_t)s_slot[k] * kWideRows + (i - k * rep) * R + row, lane), p.ref_unit);
         }
         s_part[w][lane] = acc;
         __syncthreads();
         if (w == 0) {
-            for (int i = 1; i < min(8, parts * rep); i++) join(acc, s_part[i][lane]);
+            for (int i = 1; i < min(8, parts * rep); i++) join(acc, s_part[i][lane], p.ref_unit);
             store_row(p, it, row, acc, lane);
         }
         __syncthreads();
@@ -108,7 +109,7 @@ __device__ __forceinline__ void combine_wide(const ChunkAttnParams &p, int c, in
         if (next > at) {
             load(x, 2 * (size_t)k);
 #pragma unroll
-            for (int i = 0; i < kCombineRows; i++) join(acc[i], x[i]);
+            for (int i = 0; i < kCombineRows; i++) join(acc[i], x[i], p.ref_unit);
         }
         at = next;
     }
