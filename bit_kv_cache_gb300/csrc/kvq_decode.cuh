@@ -600,7 +600,8 @@ __global__ void __launch_bounds__(NW * 32, 1) decode_kernel(const DecodeParams p
         // merged sequences: first and last of each unit range, ascending and distinct
         if (tid < 2 * p.wpc) {
             const int k = kc + (tid >> 1);
-            const int x = (tid & 1) ? pool_a(P, k + 1) - 1 : pool_a(P, k);
+            // (fewer items than warps: one without any stands for the item behind its empty range)
+            const int x = min(max((tid & 1) ? pool_a(P, k + 1) - 1 : 0, pool_a(P, k)), P.n - 1);
             s_fl[tid] = seg_of<RG>(p, P, pfx, x).u;
         }
         __syncthreads();
