@@ -9,6 +9,7 @@ is no CPU fallback: importing this package fails if ``libkvq.so`` is missing
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 from typing import Optional, Tuple
 
@@ -31,7 +32,8 @@ EXPORTS = ("kvq_status_str", "kvq_config_check", "kvq_buffer_bytes", "kvq_quant_
            "kvq_paged_prefill", "kvq_paged_append", "kvq_paged_flush_plan", "kvq_paged_flush",
            "kvq_paged_release", "kvq_paged_workspace_bytes", "kvq_paged_decode_attn",
            "kvq_paged_read_status", "kvq_paged_plan", "kvq_paged_chunk_workspace_bytes",
-           "kvq_paged_chunk_attn", "kvq_paged_extend", "kvq_qk_norm_rope")
+           "kvq_paged_chunk_attn", "kvq_paged_extend", "kvq_qk_norm_rope", "kvq_qk_norm_rope_freq",
+           "kvq_paged_append_rope")
 PAGED_MAX_B = 512
 
 
@@ -82,7 +84,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     if not os.path.exists(path):
         raise ImportError("libkvq.so not built (%s); run: python bit_kv_cache_gb300/build.py" % path)
     L = ctypes.CDLL(path)
-    P, I, I64, Sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t
+    P, I, I64, Sz, F = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float
     CP, KP, PP = ctypes.POINTER(Config), ctypes.POINTER(Cache), ctypes.POINTER(Paged)
     IP, HP = ctypes.POINTER(I), ctypes.POINTER(ChunkDesc)
     sig = {
@@ -119,6 +121,8 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "kvq_paged_chunk_attn": ([CP, PP, HP, P, I64, P, I64, P, I64, P, P, Sz, P], I),
         "kvq_paged_extend": ([CP, PP, HP, P, I64, P, I64, P], I),
         "kvq_qk_norm_rope": ([ctypes.POINTER(QkConfig), P, P, P, P, P, I64, P, P, P], I),
+        "kvq_qk_norm_rope_freq": ([ctypes.POINTER(QkConfig), P, F, P, P, P, P, P, I64, P, P, P], I),
+        "kvq_paged_append_rope": ([CP, PP, ctypes.POINTER(QkConfig), P, F, P, P, P, I64, P, P, P, P, I64, P], I),
     }
     for name, (args, res) in sig.items():
         f = getattr(L, name)
@@ -176,8 +180,84 @@ def _float16():
     return torch.float16
 
 
+class Rope:
+    """Angles of a rotary position embedding: channel pair j of the first ``rotary_dim`` channels
+    turns by pos * freq[j], and rotated channels are multiplied by ``amp``.  halves: pairs
+    (j, j + rotary_dim/2) instead of (2j, 2j+1).  scaling: how positions beyond a model's
+    training length are brought back into its range,
+      None                                    freq[j] = base^(-2j/rotary_dim)
+      dict(kind="linear", factor)             every frequency divided by factor
+      dict(kind="ntk", factor)                a base larger by factor^(n/(n-2)): the last pair turns
+                                              `factor` times slower, the first as before
+      dict(kind="bands", factor, original, low=1.0, high=4.0)
+                                              pairs that turn more than `high` times within
+                                              `original` positions stay, those below `low` are
+                                              divided by factor, in between linear in the turns
+      dict(kind="yarn", factor, original, fast=32.0, slow=1.0)
+                                              the same by a ramp over the pairs' indices, from the
+                                              pair that turns `fast` times to the one of `slow`;
+                                              amp = 0.1 ln(factor) + 1
+    or ``freq`` gives the frequencies themselves (radians per position), with ``amp``."""
+
+    def __init__(self, rotary_dim, base=10000.0, halves=False, scaling=None, freq=None, amp=None):
+        n = int(rotary_dim)
+        if n <= 0 or n % 2:
+            raise ValueError("rotary_dim must be a positive even number")
+        if freq is not None and scaling is not None:
+            raise ValueError("freq and scaling exclude each other")
+        gain = 1.0
+        if freq is None:
+            if not (math.isfinite(base) and base > 0):
+                raise ValueError("base must be positive")
+            freq, gain = self._frequencies(n, float(base), dict(scaling or {}))
+        freq = [float(x) for x in freq]
+        self.amp = float(gain if amp is None else amp)
+        if len(freq) != n // 2 or not all(0 <= x <= 2.0 ** 31 for x in freq) or not math.isfinite(self.amp):
+            raise ValueError("freq must hold rotary_dim / 2 frequencies of 0 to 2^31 radians, amp must be finite")
+        self.rotary_dim, self.halves, self.freq = n, bool(halves), freq
+        self._table = (ctypes.c_double * (n // 2))(*freq)
+        self._ptr = ctypes.addressof(self._table)
+
+    @staticmethod
+    def _frequencies(n, base, scaling):
+        kind = scaling.pop("kind", None)
+        if kind is None and not scaling:
+            return [base ** (-2.0 * j / n) for j in range(n // 2)], 1.0
+        need = {"linear": {"factor"}, "ntk": {"factor"}, "bands": {"factor", "original"}, "yarn": {"factor", "original"}}
+        may = {"bands": {"low": 1.0, "high": 4.0}, "yarn": {"fast": 32.0, "slow": 1.0}}
+        if kind not in need or not need[kind] <= set(scaling) <= need[kind] | set(may.get(kind, ())):
+            raise ValueError("unknown scaling: kind %r with %s" % (kind, sorted(scaling)))
+        s = {m: float(x) for m, x in {**may.get(kind, {}), **scaling}.items()}
+        if not all(math.isfinite(x) and x > 0 for x in s.values()):
+            raise ValueError("the numbers of a scaling must be positive")
+        k = s["factor"]
+        if kind == "ntk":
+            if n == 2:
+                raise ValueError("one pair has no base to scale")
+            base *= k ** (n / (n - 2))
+        f = [base ** (-2.0 * j / n) for j in range(n // 2)]
+        if kind == "ntk":
+            return f, 1.0
+        if kind == "linear":
+            return [x / k for x in f], 1.0
+        if kind == "bands":
+            if s["high"] <= s["low"]:
+                raise ValueError("high must be above low")
+            keep = [(s["original"] * x / (2 * math.pi) - s["low"]) / (s["high"] - s["low"]) for x in f]
+            gain = 1.0
+        else:
+            if base == 1.0:
+                raise ValueError("a base of 1 has no pairs to choose from")
+            at = lambda turns: n * math.log(s["original"] / (2 * math.pi * turns)) / (2 * math.log(base))  # noqa: E731
+            lo, hi = max(math.floor(at(s["fast"])), 0), min(math.ceil(at(s["slow"])), n - 1)
+            keep = [1 - (j - lo) / max(hi - lo, 0.001) for j in range(n // 2)]
+            gain = 0.1 * math.log(k) + 1.0 if k > 1 else 1.0
+        keep = [min(1.0, max(0.0, x)) for x in keep]
+        return [x * p + x / k * (1 - p) for x, p in zip(f, keep)], gain
+
+
 def qk_norm_rope(q, k=None, w_q=None, w_k=None, pos=None, eps=1e-6, rope_base=10000.0, rotary_dim=None,
-                 halves=False, rotate_q=True, rotate_k=True, out=None):
+                 halves=False, rotate_q=True, rotate_k=True, out=None, rope=None):
     """RMS norm of every query and key head and the rotary position embedding in one pass
     (kvq_qk_norm_rope).
 
@@ -186,7 +266,8 @@ def qk_norm_rope(q, k=None, w_q=None, w_k=None, pos=None, eps=1e-6, rope_base=10
     device.  rotary_dim: the first channels, which rotate (all of them by default); halves:
     pairs (j, j + rotary_dim/2) instead of (2j, 2j+1).  rotate_q, rotate_k: a cache that
     stores keys before RoPE takes rotate_k=False.  out: (q_out, k_out), contiguous; an
-    output may be its own contiguous input.  Returns (q_out, k_out)."""
+    output may be its own contiguous input.  rope: a Rope, instead of rope_base, rotary_dim and
+    halves (kvq_qk_norm_rope_freq).  Returns (q_out, k_out)."""
     import torch
     n, H_q, D = q.shape
     dev = q.device
@@ -211,6 +292,13 @@ def qk_norm_rope(q, k=None, w_q=None, w_k=None, pos=None, eps=1e-6, rope_base=10
             raise ValueError("%s must be a contiguous float16 tensor [%d, %d, %d] on %s" % (what, n, H, D, dev))
     c = QkConfig(H_q, H_kv, D, D if rotary_dim is None else rotary_dim, int(bool(halves)),
                  int(bool(rotate_q)) + 2 * int(bool(rotate_k)), eps, rope_base, qs, ks)
+    if rope is not None:
+        c.rotary_dim, c.halves = rope.rotary_dim, int(rope.halves)
+        _check(lib.kvq_qk_norm_rope_freq(ctypes.byref(c), rope._ptr, rope.amp, qp, kp, None if w_q is None else w_q.data_ptr(),
+                                         None if w_k is None else w_k.data_ptr(), pos.data_ptr(), n, q_out.data_ptr(),
+                                         None if k_out is None else k_out.data_ptr(), _stream_of(dev.index)),
+               "kvq_qk_norm_rope_freq")
+        return q_out, k_out
     _check(lib.kvq_qk_norm_rope(ctypes.byref(c), qp, kp, None if w_q is None else w_q.data_ptr(),
                                 None if w_k is None else w_k.data_ptr(), pos.data_ptr(), n, q_out.data_ptr(),
                                 None if k_out is None else k_out.data_ptr(), _stream_of(dev.index)), "kvq_qk_norm_rope")
@@ -534,6 +622,78 @@ class KVQPagedCache:
         _check(lib.kvq_paged_append(ctypes.byref(self.cfg), ctypes.byref(self.p), kp, vp, KVQCache._stream()),
                "paged append")
 
+    def append_rope(self, q, k, v, rope=None, w_q=None, w_k=None, eps=1e-6, rotate_q=True, rotate_k=True, pages=None,
+                    out=None):
+        """One new token for every active slot: full residuals are packed, the queries and keys
+        are normalized (w_q, w_k: float16 [D], or None for no norm) and rotated at the tokens'
+        positions, and keys and values enter the cache, in one launch (kvq_paged_append_rope).
+        q: float16 [B, H_q, D], k, v: float16 [B, H_kv, D], row b for slot b; rows may be strided
+        (views of a fused projection), those of empty slots are ignored.  rope: a Rope; by
+        default all channels, interleaved, base 10000.  pages: ids of physical pages that the
+        caller hands out to the full residuals (host integers, or an int32 CPU tensor), here and
+        in every later call that needs pages, until clear(); by default they come from the
+        cache's own free list.  Returns the queries for decode_attn, out if it is given
+        (contiguous [B, H_q, D]; it may be q)."""
+        torch, cfg, dev = self.torch, self.cfg, self._dev
+        B, D = cfg.B, cfg.D
+        qp, qs = _rows(q, cfg.H_q, D, B, dev, "q")
+        kp, ks = _rows(k, cfg.H_kv, D, B, dev, "k")
+        vp, vs = _rows(v, cfg.H_kv, D, B, dev, "v")
+        for w, what in ((w_q, "w_q"), (w_k, "w_k")):
+            if w is not None and (w.device != dev or w.dtype != torch.float16 or w.shape != (D,) or not w.is_contiguous()):
+                raise ValueError("%s must be a contiguous float16 tensor [%d] on %s" % (what, D, dev))
+        if out is None:
+            if torch.cuda.is_current_stream_capturing():
+                raise KvqError(-2, "kvq_paged_append_rope")  # before anything is allocated
+            out = torch.zeros((B, cfg.H_q, D), dtype=torch.float16, device=dev)
+        op, os_ = _rows(out, cfg.H_q, D, B, dev, "out")
+        if os_ != cfg.H_q * D or out.shape[0] != B:
+            raise ValueError("out must be contiguous [%d, %d, %d]" % (B, cfg.H_q, D))
+        if rope is None:
+            rope = self._rope = getattr(self, "_rope", None) or Rope(D)
+        c = QkConfig(cfg.H_q, cfg.H_kv, D, rope.rotary_dim, int(rope.halves), int(bool(rotate_q)) + 2 * int(bool(rotate_k)),
+                     eps, 0.0, qs, ks)
+        own, taken = pages is None, []
+        if own:
+            n = ctypes.c_int(0)
+            seqs = (ctypes.c_int32 * B)()
+            _check(lib.kvq_paged_flush_plan(*self._refs, seqs, ctypes.byref(n)), "flush plan")
+            ids = []
+            per, full = cfg.R // cfg.G, seqs[: n.value]
+            if full and self.caller_pages:
+                raise KvqError(-1, "the caller maps this cache's pages")
+            j0 = [self.lens_host[4 * b + 1] // cfg.G for b in full]
+            if sum(max(0, j + per - len(self.pages[b])) for b, j in zip(full, j0)) > len(self.free):
+                raise KvqError(-3, "page pool exhausted")
+            for b, j in zip(full, j0):
+                while len(self.pages[b]) < j + per:
+                    taken.append(b)
+                    self.pages[b].append(self.free.pop())
+                ids += self.pages[b][j: j + per]
+            ids = (ctypes.c_int32 * len(ids))(*ids)
+            pp, np_ = ids, len(ids)
+        elif isinstance(pages, torch.Tensor):
+            if pages.device.type != "cpu" or pages.dtype != torch.int32 or pages.dim() != 1 or not pages.is_contiguous():
+                raise ValueError("pages must be a contiguous int32 CPU tensor")
+            pp, np_ = (pages.data_ptr() or ctypes.addressof(self.lens_host)), pages.numel()
+        else:
+            ids = (ctypes.c_int32 * max(1, len(pages)))(*[int(x) for x in pages])
+            pp, np_ = ids, len(pages)
+        try:
+            _check(lib.kvq_paged_append_rope(*self._refs, ctypes.byref(c), rope._ptr, rope.amp, qp, kp, vp, vs,
+                                             None if w_q is None else w_q.data_ptr(), None if w_k is None else w_k.data_ptr(), op,
+                                             pp, np_, _stream_of(dev.index)), "kvq_paged_append_rope")
+        except Exception:
+            for b in reversed(taken):  # their table rows are not written
+                self.free.append(self.pages[b].pop())
+            raise
+        self.caller_pages |= not own
+        return out
+
+    def decode_step(self, q, k, v, rope=None, w_q=None, w_k=None, eps=1e-6, out=None):
+        """One decode step of every active slot: append_rope, then decode_attn."""
+        return self.decode_attn(self.append_rope(q, k, v, rope, w_q, w_k, eps), out)
+
     def flush(self) -> list:
         """Packs every full residual into new pages; returns the flushed slots."""
         cfg = self.cfg
@@ -683,18 +843,18 @@ class KVQPagedCache:
         _check(lib.kvq_paged_extend(*self._refs, chunk.ref, kp, ks, vp, vs, _stream_of(dev.index)), "kvq_paged_extend")
 
     def chunk_step(self, n_new, q, k, v, w_q=None, w_k=None, eps=1e-6, rope_base=10000.0, rotary_dim=None,
-                   halves=False, chunk=None, out=None):
+                   halves=False, chunk=None, out=None, rope=None):
         """One step of n_new[b] new tokens per slot: plan, norm and rotation of q and k at
         their positions, attention, and the tokens' entry into the cache.  q: float16
         [n, H_q, D], k, v: float16 [n, H_kv, D], n >= sum(n_new); rows behind that sum are left
-        alone.  Returns (out, chunk), out with sum(n_new) rows if it is not the caller's.  A
+        alone.  rope: a Rope, instead of rope_base, rotary_dim and halves.  Returns (out, chunk), out with sum(n_new) rows if it is not the caller's.  A
         chunk made here (chunk=None) costs its arrays and a workspace in every call; a loop
         keeps one."""
         chunk = self.plan(n_new, chunk)
         n = chunk.n_tokens
         if n == 0:
             return q.new_empty((0,) + q.shape[1:]) if out is None else out, chunk
-        q, k = qk_norm_rope(q[:n], k[:n], w_q, w_k, chunk.pos[:n], eps, rope_base, rotary_dim, halves)
+        q, k = qk_norm_rope(q[:n], k[:n], w_q, w_k, chunk.pos[:n], eps, rope_base, rotary_dim, halves, rope=rope)
         out = self.chunk_attn(chunk, q, k, v, out)
         self.extend(chunk, k, v)
         return out, chunk

@@ -20,10 +20,12 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libkvq.so")
 SOURCES = ["kvq_api.cu", "kvq_quant.cu", "kvq_decode.cu", "kvq_noalloc.cu", "kvq_paged.cu",
            "kvq_decode_paged.cu", "kvq_decode_rope.cu", "kvq_decode_nvfp4.cu", "kvq_selftest.cu",
-           "kvq_chunk.cu", "kvq_chunk_attn.cu", "kvq_chunk_attn_block.cu", "kvq_chunk_combine.cu", "kvq_block.cu", "kvq_block_decode.cu"]
+           "kvq_chunk.cu", "kvq_chunk_attn.cu", "kvq_chunk_attn_block.cu", "kvq_chunk_combine.cu", "kvq_block.cu", "kvq_block_decode.cu",
+           "kvq_append_rope.cu"]
 HEADERS = ["kvq_device.cuh", "kvq_internal.h", "kvq_decode_fast.cuh", "kvq_host.h",
            "kvq_decode.cuh", "kvq_quantizer.cuh", "kvq_chunk.h",
-           "kvq_chunk_attn.cuh", "kvq_chunk_attn_kernel.cuh", "kvq_tcgen05.cuh", "kvq_extend.cuh", "kvq_block.h", "kvq_block.cuh"]
+           "kvq_chunk_attn.cuh", "kvq_chunk_attn_kernel.cuh", "kvq_tcgen05.cuh", "kvq_extend.cuh", "kvq_block.h", "kvq_block.cuh",
+           "kvq_rope.h"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",

@@ -16,7 +16,7 @@ struct Sides {
     const uint16_t *res, *src;
     int64_t stride;
 };
-__device__ __forceinline__ Sides sides(const ExtendParams &p, bool value) {
+__device__ __forceinline__ Sides sides(const PackParams &p, bool value) {
     return {reinterpret_cast<uint8_t *>(value ? p.v_codes : p.k_codes), reinterpret_cast<float4 *>(value ? p.v_meta : p.k_meta),
             value ? p.v_res : p.k_res, value ? p.v_new : p.k_new, value ? p.v_stride : p.k_stride};
 }

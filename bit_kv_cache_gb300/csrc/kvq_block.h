@@ -14,9 +14,9 @@ namespace kvq {
 // lp0[i / per] + i % per there.  Its rows come from the residual (the first nr of the stream) and
 // then from k_new, v_new, whose row row0 + t - nr of head h starts at h h_stride + that t stride.
 // commit: the slots' lengths become T + R and no residual.
-struct BlockListParams : ExtendParams {
+struct BlockListParams : PackParams {
     int64_t h_stride;
-    int per, nr, row0, commit;
+    int n_pack, per, nr, row0, commit;
     int16_t seq[KVQ_PAGED_MAX_B];
     int32_t lp0[KVQ_PAGED_MAX_B];
 };

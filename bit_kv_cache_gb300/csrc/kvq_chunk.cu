@@ -16,6 +16,7 @@
 #include "kvq_chunk.h"
 #include "kvq_extend.cuh"
 #include "kvq_host.h"
+#include "kvq_rope.h"
 
 using namespace kvq;
 using namespace kvq::host;
@@ -232,7 +233,7 @@ __global__ void __launch_bounds__(256) qk_kernel(const __grid_constant__ QkParam
         const uint64_t a = (uint64_t)pos * p.turn[j];
         float s, c;
         sincospif((float)(int32_t)(a >> 32) * 0x1p-31f, &s, &c);
-        s_cs[j] = make_float2(c, s);
+        s_cs[j] = make_float2(p.amp * c, p.amp * s);
     }
     __syncwarp();
     // first and second channels of the four pairs of eight halves
@@ -336,15 +337,6 @@ cudaError_t launch_qk(const QkParams &p, int D, cudaStream_t st) {
 // ------------------------------------------------------------------------------
 namespace {
 
-bool capturing(cudaStream_t st) {
-    cudaStreamCaptureStatus s = cudaStreamCaptureStatusNone;
-    if (cudaStreamIsCapturing(st, &s) != cudaSuccess) {
-        cudaGetLastError();  // a legacy-stream query that a global capture forbids
-        return true;
-    }
-    return s != cudaStreamCaptureStatusNone;
-}
-
 int check_chunk(const kvq_chunk *ch) {
     if (!ch || !ch->host || ch->max_tokens < 0) return KVQ_ERR_INVALID_ARG;
     const void *need[] = {ch->cu, ch->slot, ch->pos, ch->desc};
@@ -371,46 +363,6 @@ bool plan_holds(const kvq_config *c, const kvq_paged *pc, const kvq_chunk *ch) {
         rows += s[b].n_new;
     }
     return rows == ch->n_tokens;
-}
-
-bool rows_ok(const uint16_t *p, int64_t stride, int64_t heads, int64_t D) {
-    return p && aligned16(p) && stride >= heads * D && stride % 8 == 0;
-}
-
-bool overlap(const void *a, size_t na, const void *b, size_t nb) {
-    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-    return x < y + nb && y < x + na;
-}
-
-// A positive number m 2^(e - 64), 2^63 <= m.
-struct Mantissa {
-    uint64_t m;
-    int e;
-};
-Mantissa mantissa(double x) {
-    int e;
-    const double f = frexp(x, &e);
-    return {(uint64_t)ldexp(f, 64), e};
-}
-Mantissa operator*(Mantissa a, Mantissa b) {
-    unsigned __int128 p = (unsigned __int128)a.m * b.m;
-    int e = a.e + b.e;
-    if (!(p >> 127)) p <<= 1, e--;
-    return {(uint64_t)(p >> 64), e};
-}
-
-// base^(-1/m) for base > 1 in units of 2^-64, off by a few of them: the double root y and one
-// Newton step, y (1 - (y^m base - 1) / m), whose residual is formed with 64-bit mantissas
-// (a long double power, emulated in software on Arm, took 1.2 us more of the call's 11).
-uint64_t inverse_root(double base, int m) {
-    const Mantissa y = mantissa(std::min(pow(base, -1.0 / m), 1.0 - 0x1p-53));
-    Mantissa z = mantissa(base), sq = y;
-    for (int i = m; i; i >>= 1, sq = sq * sq)
-        if (i & 1) z = z * sq;
-    // z = 1 + d 2^-64
-    const int64_t d = z.e == 1 ? (int64_t)((z.m - (1ull << 63)) << 1) : (int64_t)z.m;
-    const uint64_t f = y.m >> -y.e;
-    return f - (uint64_t)(int64_t)((double)f * ((double)d * 0x1p-64) / m);
 }
 
 // Partials of the attention: two segments' ends per CTA.
@@ -738,13 +690,16 @@ int kvq_paged_extend(const kvq_config *c, kvq_paged *pc, const kvq_chunk *ch, co
 int kvq_qk_norm_rope(const kvq_qk_config *c, const uint16_t *q, const uint16_t *k, const uint16_t *w_q,
                      const uint16_t *w_k, const int32_t *pos, int64_t n, uint16_t *q_out, uint16_t *k_out,
                      void *stream) {
+    return kvq_qk_norm_rope_freq(c, nullptr, 1.f, q, k, w_q, w_k, pos, n, q_out, k_out, stream);
+}
+
+int kvq_qk_norm_rope_freq(const kvq_qk_config *c, const double *freq, float amp, const uint16_t *q, const uint16_t *k,
+                          const uint16_t *w_q, const uint16_t *w_k, const int32_t *pos, int64_t n, uint16_t *q_out,
+                          uint16_t *k_out, void *stream) {
     if (!c || c->H_q < 0 || c->H_kv < 0 || c->H_q + (int64_t)c->H_kv < 1 || c->H_q > 65535 || c->H_kv > 65535 || n < 0)
         return KVQ_ERR_INVALID_ARG;
-    if (c->D != 64 && c->D != 128 && c->D != 256) return KVQ_ERR_UNSUPPORTED;
-    if (c->rotary_dim < 0 || c->rotary_dim > c->D || (c->halves & ~1) || (c->rotate & ~3)) return KVQ_ERR_INVALID_ARG;
-    if (c->rotary_dim % 16) return KVQ_ERR_UNSUPPORTED;
-    if (!(c->eps >= 0.f) || !std::isfinite(c->eps) || !(c->rope_base >= 0.f) || !std::isfinite(c->rope_base))
-        return KVQ_ERR_INVALID_ARG;
+    const int e = rope_check(c, freq, amp);
+    if (e) return e;
     if (n == 0) return KVQ_OK;
     if (n > INT32_MAX) return KVQ_ERR_UNSUPPORTED;
     if (!pos || (reinterpret_cast<uintptr_t>(pos) & 3u)) return KVQ_ERR_INVALID_ARG;
@@ -789,21 +744,9 @@ int kvq_qk_norm_rope(const kvq_qk_config *c, const uint16_t *q, const uint16_t *
     p.halves = c->halves;
     p.rotate = c->rotary_dim ? c->rotate : 0;
     p.eps = c->eps;
-    const double base = c->rope_base > 0.f ? (double)c->rope_base : 10000.0;
-    // turn[j] = base^(-2j/n) / (2 pi) in 64-bit fixed point: one root, then integer products
-    // (a call's host time is a small part of that of a power per pair).  The root's error and the
-    // products' truncations add up: a step is off by n/4 + 1 units of 2^-64 at most (64.3 for
-    // n = 256 and bases next to 1, 9 for a base of 10000, against 80 digits), so an angle by
-    // 2^-27 of a turn at positions below 2^31
-    if (c->rotary_dim && base > 1.0) {
-        const uint64_t f = inverse_root(base, c->rotary_dim / 2);
-        uint64_t turn = 0x28be60db9391054aull;  // 2^64 / (2 pi)
-        for (int j = 0; j < c->rotary_dim / 2; j++, turn = (uint64_t)(((unsigned __int128)turn * f) >> 64)) p.turn[j] = turn;
-    } else if (c->rotary_dim) {
-        const long double step = powl((long double)base, -2.0L / c->rotary_dim);
-        long double turn = 0.159154943091895335768883763372514362L;
-        for (int j = 0; j < c->rotary_dim / 2; j++, turn *= step) p.turn[j] = (uint64_t)ldexpl(turn - floorl(turn), 64);
-    }
+    p.amp = amp;
+    if (c->rotary_dim && freq) turns_of_freq(freq, c->rotary_dim, p.turn);
+    else if (c->rotary_dim) turns_of_base(c->rope_base, c->rotary_dim, p.turn);
     return status_of(launch_qk(p, c->D, (cudaStream_t)stream));
 }
 

@@ -23,8 +23,8 @@ struct PlanParams {
     int32_t n_new[KVQ_PAGED_MAX_B];
 };
 
-struct ExtendParams {
-    const int32_t *desc;
+// Rows, pages and fp16 buffers of a call that packs pages.
+struct PackParams {
     int32_t *lens, *status;
     const uint16_t *k_new, *v_new;
     int64_t k_stride, v_stride;
@@ -34,6 +34,10 @@ struct ExtendParams {
     const int32_t *ptab;
     int64_t n_pages;
     int B, H_kv, G, S, R, TV, ptab_stride;
+};
+
+struct ExtendParams : PackParams {
+    const int32_t *desc;
     int n_pack;                          // pages to pack, over all slots
     int once;                            // one page holds all old residual rows of a slot, so that the CTA that packs
                                          // it may overwrite them: then one launch does the whole call
@@ -46,8 +50,8 @@ struct QkParams {
     uint16_t *q_out, *k_out;
     int64_t n, q_stride, k_stride;
     int H_q, H_kv, rotary, halves, rotate;
-    float eps;
-    uint64_t turn[128];                  // base^(-2j/rotary) / (2 pi) in units of 2^-64 turns
+    float eps, amp;                      // amp: factor of the channels that rotate
+    uint64_t turn[128];                  // radians per position of pair j / (2 pi), in units of 2^-64 turns
 };
 
 constexpr float kLog2e = 1.4426950408889634f;

@@ -19,7 +19,7 @@ struct PageJob {
     int entry;             // of the page table; read early, checked and used by page() at the end
     int t0;                // first stream token
     // -1: no page, nothing may be stored
-    __device__ __forceinline__ int64_t page(const ExtendParams &p, int h) const {
+    __device__ __forceinline__ int64_t page(const PackParams &p, int h) const {
         if (entry < 0 || entry >= p.n_pages) {
             if (threadIdx.x == 0) report(p.status, KVQ_DEV_BAD_STATE);
             return -1;
@@ -49,7 +49,7 @@ __device__ __forceinline__ PageJob find_page(const ExtendParams &p, int i) {
 
 // Row t of a page's stream.  Residual rows are read by ordinary loads: where one launch does the
 // call, keep_rows writes over them.
-__device__ __forceinline__ const uint16_t *stream_row(const ExtendParams &p, const PageJob &j, const uint16_t *res,
+__device__ __forceinline__ const uint16_t *stream_row(const PackParams &p, const PageJob &j, const uint16_t *res,
                                                       const uint16_t *src, int64_t stride, int h, int t) {
     return t < j.s.nr ? res + (((size_t)j.b * p.H_kv + h) * p.R + t) * 128
                       : src + (int64_t)(j.s.cu + j.s.to_sink + t - j.s.nr) * stride + h * 128;
@@ -57,7 +57,7 @@ __device__ __forceinline__ const uint16_t *stream_row(const ExtendParams &p, con
 
 // Keys of one page: TPW tokens per warp, lane l holds channels 4 l .. 4 l + 3 of them.
 template <int BITS, int TPW>
-__device__ __forceinline__ void extend_keys(const ExtendParams &p, const PageJob &jb, int h, unsigned char *smem) {
+__device__ __forceinline__ void extend_keys(const PackParams &p, const PageJob &jb, int h, unsigned char *smem) {
     constexpr int D = 128, FPI = 32 / BITS, NWR = TPW / FPI, MAXI = (1 << BITS) - 1;
     uint16_t(*s_lo)[D] = reinterpret_cast<uint16_t(*)[D]>(smem);
     uint16_t(*s_hi)[D] = s_lo + 8;
@@ -153,7 +153,7 @@ static __device__ __noinline__ uint2 exact_codes8(uint4 x, uint32_t m, int bits)
 // 128 value tokens of one page (block vb of it): 16 tokens per warp, lane (tq, c) holds
 // tokens 8 g + tq and of each the 8-channel chunks c, c + 4, c + 8, c + 12.
 template <int BITS>
-__device__ __forceinline__ void extend_values(const ExtendParams &p, const PageJob &jb, int h, int vb, unsigned char *smem) {
+__device__ __forceinline__ void extend_values(const PackParams &p, const PageJob &jb, int h, int vb, unsigned char *smem) {
     constexpr int D = 128, FPI = 32 / BITS, NWORD = D / FPI;
     uint32_t(*s_codes)[128] = reinterpret_cast<uint32_t(*)[128]>(smem);
     uint32_t *s_meta = reinterpret_cast<uint32_t *>(smem + NWORD * 512);

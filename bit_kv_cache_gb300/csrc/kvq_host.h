@@ -47,6 +47,26 @@ inline bool key_slices_ok(const kvq_config *c) { return key_slices(c) > 0; }
 
 inline int status_of(cudaError_t e) { return e == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA; }
 
+// Whether a stream is capturing.
+inline bool capturing(cudaStream_t st) {
+    cudaStreamCaptureStatus s = cudaStreamCaptureStatusNone;
+    if (cudaStreamIsCapturing(st, &s) != cudaSuccess) {
+        cudaGetLastError();  // a legacy-stream query that a global capture forbids
+        return true;
+    }
+    return s != cudaStreamCaptureStatusNone;
+}
+
+// Token-major rows: address and stride; whether two ranges of bytes share one.
+inline bool rows_ok(const uint16_t *p, int64_t stride, int64_t heads, int64_t D) {
+    return p && aligned16(p) && stride >= heads * D && stride % 8 == 0;
+}
+
+inline bool overlap(const void *a, size_t na, const void *b, size_t nb) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y + nb && y < x + na;
+}
+
 // SM count of the current device (cached per device; 148 if no device is usable).
 inline int num_sms() {
     static int cache[64] = {0};

@@ -555,6 +555,39 @@ int kvq_qk_norm_rope(const kvq_qk_config *c, const uint16_t *q, const uint16_t *
                      const uint16_t *w_k, const int32_t *pos, int64_t n, uint16_t *q_out, uint16_t *k_out,
                      void *stream);
 
+/* kvq_qk_norm_rope with given frequencies: pair j of a position turns by pos * freq[j] radians
+ * (freq: host double [rotary_dim/2], 0 <= freq[j] <= 2^31, read before the call returns; NULL:
+ * those of rope_base), and rotated channels are multiplied by amp.  So positions scaled for
+ * contexts longer than a model was trained on (linear, by the base, by bands of wavelengths, ...)
+ * are one table.  Angles are reduced as there: off by pos units of 2^-64 turns, and by pos times
+ * the rounding of freq[j].  KVQ_ERR_INVALID_ARG for a frequency out of range or an amp that is
+ * not finite. */
+int kvq_qk_norm_rope_freq(const kvq_qk_config *c, const double *freq, float amp, const uint16_t *q, const uint16_t *k,
+                          const uint16_t *w_q, const uint16_t *w_k, const int32_t *pos, int64_t n, uint16_t *q_out,
+                          uint16_t *k_out, void *stream);
+
+/* One new token for every active sequence of a paged cache of any mode, in one launch: what
+ * kvq_paged_flush, kvq_qk_norm_rope_freq at the tokens' positions and kvq_paged_append give, bit
+ * for bit, in this order.
+ *   - Residuals that are full (kvq_paged_flush_plan) are packed into their next R/G pages.  If
+ *     new_pages (host int32 [n_new_pages], read before the call returns) is given, the page table
+ *     gets its ids, slot after slot in ascending order; if it is NULL the caller has mapped them.
+ *   - Row b of q, k and v (device fp16 rows of H_q, H_kv and H_kv heads; strides qk->q_stride,
+ *     qk->k_stride and v_stride in elements, as in a chunk) is slot b's new token.  Its query and
+ *     key are normalized and rotated at its position (qk, freq, amp, w_q, w_k as in
+ *     kvq_qk_norm_rope_freq; qk's heads and D are cfg's), the query goes to q_out (device fp16
+ *     [B][H_q][D], contiguous; it may be q, if that is contiguous), key and value to the sink
+ *     while it is not full, else to the residual.  Rows of empty slots are neither read nor
+ *     written.
+ * KVQ_ERR_CAPACITY if a full slot would exceed max_T, or new_pages is too short;
+ * KVQ_ERR_INVALID_ARG also for an id outside [0, n_pages) and for a q_out that overlaps another
+ * input; KVQ_ERR_UNSUPPORTED for R/G above 1024 with a full residual and while `stream` is
+ * capturing (a replay would not advance the host lengths).  Nothing is enqueued then.  A
+ * page-table entry that is no page is reported (KVQ_DEV_BAD_STATE) and its page not stored. */
+int kvq_paged_append_rope(const kvq_config *cfg, kvq_paged *pc, const kvq_qk_config *qk, const double *freq, float amp,
+                          const uint16_t *q, const uint16_t *k, const uint16_t *v, int64_t v_stride, const uint16_t *w_q,
+                          const uint16_t *w_k, uint16_t *q_out, const int32_t *new_pages, int64_t n_new_pages, void *stream);
+
 /* Synchronizes `stream`, then returns in *dev_status the OR of the error bits the
  * kernels wrote into the workspace status word and into cache->status (if cache is
  * not NULL and its status pointer is set), and clears both.  KVQ_ERR_DEVICE if any
