@@ -24,6 +24,7 @@ namespace kvq {
 namespace {
 
 constexpr int kWarps = 4, kThreads = 32 * kWarps;
+constexpr int kStages = 3, kPiece = 8192;                // of a warp's ring: keys or values of a packed tile
 constexpr int kTokens = 64, kTailTokens = 16;            // of an item: packed, fp16
 constexpr float kUp = 6.f, kSlack = 8.f;                 // w <= 2^(kUp + kSlack); small weights stay normal numbers
 
@@ -95,10 +96,8 @@ __device__ __forceinline__ void weights(State &st, float (&x)[N][4], float a, fl
 // are 16 neighbouring tokens of a channel, word s those of step s: step s takes tokens 16 c + 4 s
 // .. + 3 of every c, and the score rows are arranged so.
 template <bool E4M3>
-__device__ __forceinline__ void packed_tile(State &st, const uint32_t (&q)[8][2], const uint8_t *k, const uint8_t *v, float sk, float sv,
-                                            int lane) {
+__device__ __forceinline__ void key_tile(const uint32_t (&q)[8][2], const uint8_t *k, float (&x)[4][4], int lane) {
     const int r = lane >> 2, c = lane & 3;
-    float x[4][4];
 #pragma unroll
     for (int s = 0; s < 4; s++) {
         const uint8_t *row = k + (16 * (r >> 1) + 4 * s + (r & 1)) * 128 + c * 16;
@@ -118,8 +117,10 @@ __device__ __forceinline__ void packed_tile(State &st, const uint32_t (&q)[8][2]
             mma_16816(x[s], a[0], a[1], a[2], a[3], q[i][0], q[i][1]);
         }
     }
-    uint32_t b[4][2];
-    weights<4>(st, x, kScale * sk, log2f(sv), 1.f / sv, b);
+}
+template <bool E4M3>
+__device__ __forceinline__ void value_tile(State &st, const uint8_t *v, const uint32_t (&b)[4][2], int lane) {
+    const int r = lane >> 2, c = lane & 3;
 #pragma unroll
     for (int i = 0; i < 8; i++) {
         const uint4 lo = *reinterpret_cast<const uint4 *>(v + out_channel(i, r, 0) * 64 + c * 16);
@@ -164,12 +165,26 @@ __device__ __forceinline__ void tail_tile(State &st, const uint32_t (&q)[8][2], 
 
 __device__ __forceinline__ float factor(float m, float top) { return m == top ? 1.f : ex2(m - top); }
 
+struct Bars {
+    uint64_t full[kWarps][kStages];
+    int stop;
+};
+constexpr int kSmemBytes = kWarps * kStages * kPiece + (int)sizeof(Bars);
+// the joined states lie in the rings
+static_assert(kWarps * (8 * 128 + 16) * 4 <= kWarps * kStages * kPiece, "shared memory");
+
 template <bool E4M3>
-__global__ void __launch_bounds__(kThreads) block_decode_kernel(const __grid_constant__ BlockDecodeParams p) {
-    __shared__ float s_o[kWarps][8][128];
-    __shared__ float s_m[kWarps][8], s_l[kWarps][8];
+__global__ void __launch_bounds__(kThreads, 2) block_decode_kernel(const __grid_constant__ BlockDecodeParams p) {
+    extern __shared__ __align__(128) unsigned char sm[];
+    Bars *bar = reinterpret_cast<Bars *>(sm + kWarps * kStages * kPiece);
     const int h = blockIdx.x, w = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
-    griddep_wait();
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kWarps; i++)
+            for (int j = 0; j < kStages; j++) mbar_init(&bar->full[i][j], 1);
+        bar->stop = 0;
+        fence_barrier_init();
+    }
+    __syncthreads();
     int lo = 0, hi = p.B - 1;  // the slot
     while (lo < hi) {
         const int mid = (lo + hi) >> 1;
@@ -177,10 +192,9 @@ __global__ void __launch_bounds__(kThreads) block_decode_kernel(const __grid_con
         else lo = mid + 1;
     }
     const int b = lo, parts = p.part0[b + 1] - p.part0[b], part = blockIdx.y - p.part0[b];
-    const int4 ln = reinterpret_cast<const int4 *>(p.lens)[b];
-    const int np = ln.y / kTokens, seen = ln.x + ln.z, n = np + (seen + kTailTokens - 1) / kTailTokens;
-    const int begin = (int)((int64_t)n * part / parts), end = (int)((int64_t)n * (part + 1) / parts);
     const size_t u = (size_t)b * p.H_kv + h;
+    griddep_wait();
+    const int4 ln = reinterpret_cast<const int4 *>(p.lens)[b];
     uint32_t q[8][2];
 #pragma unroll
     for (int i = 0; i < 4; i++) {
@@ -188,6 +202,9 @@ __global__ void __launch_bounds__(kThreads) block_decode_kernel(const __grid_con
         if (r < p.g) x = *reinterpret_cast<const uint4 *>(p.q + (u * p.g + r) * 128 + (i >> 1) * 64 + c * 16 + (i & 1) * 8);
         q[2 * i][0] = x.x, q[2 * i][1] = x.y, q[2 * i + 1][0] = x.z, q[2 * i + 1][1] = x.w;
     }
+    if (!ln.w || ln.x + ln.y + ln.z == 0) return;
+    const int np = ln.y / kTokens, seen = ln.x + ln.z, n = np + (seen + kTailTokens - 1) / kTailTokens;
+    const int begin = (int)((int64_t)n * part / parts), end = (int)((int64_t)n * (part + 1) / parts);
     State st;
 #pragma unroll
     for (int e = 0; e < 2; e++) st.m[e] = -INFINITY, st.l[e] = 0.f;
@@ -195,27 +212,66 @@ __global__ void __launch_bounds__(kThreads) block_decode_kernel(const __grid_con
     for (int i = 0; i < 8; i++)
 #pragma unroll
         for (int e = 0; e < 4; e++) st.o[i][e] = 0.f;
+
+    // Packed tiles begin + w, begin + w + kWarps, ...: their pieces, keys and values in turn, are
+    // brought by bulk copies kStages ahead.  Lane j holds page and scales of tile j of 32.
+    const int tiles = begin + w < min(end, np) ? (min(end, np) - begin - w + kWarps - 1) / kWarps : 0;
+    unsigned char *ring = sm + w * kStages * kPiece;
+    uint64_t *full = bar->full[w];
     const int32_t *row = p.ptab + (size_t)b * p.ptab_stride;
-    for (int i = begin + w; i < end; i += kWarps) {
-        if (i < np) {
-            int page = row[(i * kTokens) >> p.g_shift];
+    for (int t0 = 0; t0 < tiles; t0 += 32) {
+        const int m = min(32, tiles - t0);
+        size_t at = 0;
+        float sk = 0.f, sv = 0.f;
+        if (lane < m) {
+            const int tok = (begin + w + (t0 + lane) * kWarps) * kTokens;
+            int page = row[tok >> p.g_shift];
             if (page < 0 || page >= p.n_pages) {
-                if (lane == 0) report(p.status, KVQ_DEV_BAD_STATE);
+                report(p.status, KVQ_DEV_BAD_STATE);
                 page = 0;
             }
             const size_t pg = (size_t)page * p.H_kv + h;
-            const size_t at = ((pg << p.g_shift) + ((i * kTokens) & ((1 << p.g_shift) - 1))) * 128;
-            packed_tile<E4M3>(st, q, p.k_codes + at, p.v_codes + at, p.k_scale[pg].x, p.v_scale[pg].x, lane);
-        } else {
-            const int x = (i - np) * kTailTokens;
-            auto at = [&](const uint16_t *sink, const uint16_t *res, int t) {
-                t = min(t, seen - 1);
-                return t < ln.x ? sink + (u * p.S + t) * 128 : res + (u * p.R + t - ln.x) * 128;
-            };
-            tail_tile(st, q, at(p.k_sink, p.k_res, x + r), at(p.k_sink, p.k_res, x + r + 8), at(p.v_sink, p.v_res, x + r),
-                      at(p.v_sink, p.v_res, x + r + 8), seen - x, lane);
+            at = ((pg << p.g_shift) + (tok & ((1 << p.g_shift) - 1))) * 128;
+            sk = p.k_scale[pg].x;
+            sv = p.v_scale[pg].x;
+        }
+        auto bring = [&](int i) {  // piece i of these tiles
+            const size_t from = __shfl_sync(0xffffffffu, at, i >> 1);
+            if (lane) return;
+            const int stage = (2 * t0 + i) % kStages;
+            mbar_arrive_expect_tx(&full[stage], kPiece);
+            bulk_g2s(ring + stage * kPiece, (i & 1 ? p.v_codes : p.k_codes) + from, kPiece, &full[stage]);
+        };
+        for (int i = 0; i < min(kStages, 2 * m); i++) bring(i);
+        for (int t = 0; t < m; t++) {
+            float x[4][4];
+            uint32_t bp[4][2];
+            const int i = 2 * t, k = 2 * t0 + i;  // pieces: of these tiles, of all
+            warp_await(&full[k % kStages], (k / kStages) & 1, &bar->stop, p.status);
+            key_tile<E4M3>(q, ring + k % kStages * kPiece, x, lane);
+            __syncwarp();
+            if (i + kStages < 2 * m) bring(i + kStages);
+            const float tk = __shfl_sync(0xffffffffu, sk, t), tv = __shfl_sync(0xffffffffu, sv, t);
+            weights<4>(st, x, kScale * tk, log2f(tv), 1.f / tv, bp);
+            warp_await(&full[(k + 1) % kStages], ((k + 1) / kStages) & 1, &bar->stop, p.status);
+            value_tile<E4M3>(st, ring + (k + 1) % kStages * kPiece, bp, lane);
+            __syncwarp();
+            if (i + 1 + kStages < 2 * m) bring(i + 1 + kStages);
         }
     }
+    // fp16 tiles, from where the packed ones end
+    for (int i = max(begin, np) + w; i < end; i += kWarps) {
+        const int x = (i - np) * kTailTokens;
+        auto at = [&](const uint16_t *sink, const uint16_t *res, int t) {
+            t = min(t, seen - 1);
+            return t < ln.x ? sink + (u * p.S + t) * 128 : res + (u * p.R + t - ln.x) * 128;
+        };
+        tail_tile(st, q, at(p.k_sink, p.k_res, x + r), at(p.k_sink, p.k_res, x + r + 8), at(p.v_sink, p.v_res, x + r),
+                  at(p.v_sink, p.v_res, x + r + 8), seen - x, lane);
+    }
+    __syncthreads();  // every piece has arrived and been read
+    float(*s_o)[8][128] = reinterpret_cast<float(*)[8][128]>(sm);
+    float(*s_m)[8] = reinterpret_cast<float(*)[8]>(sm + kWarps * 8 * 128 * 4), (*s_l)[8] = s_m + kWarps;
     // the warps' states, joined in warp order
 #pragma unroll
     for (int e = 0; e < 2; e++) {
@@ -259,6 +315,8 @@ __global__ void __launch_bounds__(128) block_combine_kernel(const __grid_constan
     const int first = p.part0[b], parts = p.part0[b + 1] - first;
     if (parts < 2) return;
     griddep_wait();
+    const int4 ln = reinterpret_cast<const int4 *>(p.lens)[b];
+    if (!ln.w || ln.x + ln.y + ln.z == 0) return;
     const size_t step = (size_t)p.H_kv * p.g, at = ((size_t)first * p.H_kv + h) * p.g + e;
     float m = -INFINITY;
     for (int i = 0; i < parts; i++) m = fmaxf(m, p.part_ml[at + i * step].x);
@@ -270,6 +328,20 @@ __global__ void __launch_bounds__(128) block_combine_kernel(const __grid_constan
         o = fmaf(f, p.part_o[(at + i * step) * 128 + d], o);
     }
     p.out[(((size_t)b * p.H_kv + h) * p.g + e) * 128 + d] = __half_as_ushort(__float2half_rn(o / l));
+}
+
+template <bool E4M3>
+cudaError_t launch(dim3 grid, const BlockDecodeParams &p, cudaStream_t st) {
+    static bool ready[64];  // per device
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64 || !ready[dev]) {
+        e = cudaFuncSetAttribute(block_decode_kernel<E4M3>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+        if (e != cudaSuccess) return e;
+        if (dev >= 0 && dev < 64) ready[dev] = true;
+    }
+    return launch_dependent(block_decode_kernel<E4M3>, grid, kThreads, kSmemBytes, st, p);
 }
 
 // CTAs that run at once, and the most parts of a call: each of them and one more per slot.
@@ -341,8 +413,7 @@ int block_decode(const kvq_config *c, const kvq_paged *pc, const uint16_t *q, ui
     }
     for (int b = c->B; b <= KVQ_PAGED_MAX_B; b++) p.part0[b] = parts;
     const dim3 grid((unsigned)c->H_kv, (unsigned)parts);
-    cudaError_t e = c->mode == KVQ_MODE_E4M3 ? launch_dependent(block_decode_kernel<true>, grid, kThreads, 0, st, p)
-                                             : launch_dependent(block_decode_kernel<false>, grid, kThreads, 0, st, p);
+    cudaError_t e = c->mode == KVQ_MODE_E4M3 ? launch<true>(grid, p, st) : launch<false>(grid, p, st);
     if (e == cudaSuccess && cut) e = launch_dependent(block_combine_kernel, dim3((unsigned)c->H_q, (unsigned)c->B), 128, 0, st, p);
     return host::status_of(e);
 }
