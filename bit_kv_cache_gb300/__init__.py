@@ -576,6 +576,7 @@ class KVQPagedCache:
         self.p.status = self.status.data_ptr()
         self.ws = torch.zeros(lib.kvq_paged_workspace_bytes(cp), dtype=torch.uint8, device=self.device)
         self._refs = ctypes.byref(self.cfg), ctypes.byref(self.p)
+        self._ws = self.ws.data_ptr(), self.ws.numel()
         self.caller_pages = False                     # plan() was given pages of the caller's
         self.mapping = 0                              # counts the calls that took pages away from slots
         self.free = list(range(n_pages - 1, -1, -1))  # pop() hands out the lowest id first
@@ -860,14 +861,20 @@ class KVQPagedCache:
         return out, chunk
 
     def decode_attn(self, q, out=None):
-        cfg = self.cfg
-        qp = self._ptr(q, (cfg.B, cfg.H_q, cfg.D), "q")
+        """Attention of one query token per active slot over its cached tokens
+        (kvq_paged_decode_attn).  q, out: float16 [B, H_q, D], contiguous; rows of empty slots are
+        not written (zeros where out is made here)."""
+        cfg, dev = self.cfg, self._dev
+        shape = (cfg.B, cfg.H_q, cfg.D)
         if out is None:
             out = self.torch.zeros_like(q)
-        op = self._ptr(out, (cfg.B, cfg.H_q, cfg.D), "out")
-        _check(lib.kvq_paged_decode_attn(ctypes.byref(self.cfg), ctypes.byref(self.p), qp, op,
-                                         ctypes.c_void_p(self.ws.data_ptr()), self.ws.numel(),
-                                         KVQCache._stream()), "paged decode")
+        for t, what in ((q, "q"), (out, "out")):
+            if t.device != dev or t.dtype != self.torch.float16 or not t.is_contiguous():
+                raise ValueError("%s must be a contiguous float16 tensor on %s" % (what, dev))
+            if t.shape != shape:
+                raise ValueError("%s has shape %s, expected %s" % (what, tuple(t.shape), shape))
+        _check(lib.kvq_paged_decode_attn(*self._refs, q.data_ptr(), out.data_ptr(), *self._ws, _stream_of(dev.index)),
+               "paged decode")
         return out
 
     def read_status(self) -> int:

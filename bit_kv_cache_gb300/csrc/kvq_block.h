@@ -35,7 +35,9 @@ struct BlockDecodeParams {
     int32_t *status;
     int64_t n_pages;
     int B, H_kv, g, g_shift, S, R, ptab_stride;  // g_shift: log2(G)
-    int32_t part0[KVQ_PAGED_MAX_B + 1];  // parts of the slots before each
+    int n_slots;                         // that hold tokens
+    int16_t slot[KVQ_PAGED_MAX_B];       // those
+    int32_t part0[KVQ_PAGED_MAX_B + 1];  // parts of the ones before each
 };
 
 cudaError_t launch_block_extend(const ExtendParams &p, bool e4m3, cudaStream_t st);

@@ -24,8 +24,9 @@ namespace kvq {
 namespace {
 
 constexpr int kWarps = 4, kThreads = 32 * kWarps;
-constexpr int kStages = 3, kPiece = 8192;                // of a warp's ring: keys or values of a packed tile
+constexpr int kStages = 2, kPiece = 8192;                // of a warp's ring: keys or values of a packed tile
 constexpr int kTokens = 64, kTailTokens = 16;            // of an item: packed, fp16
+constexpr int kLeast = 16;                               // items of a part, if the slot has as many
 constexpr float kUp = 6.f, kSlack = 8.f;                 // w <= 2^(kUp + kSlack); small weights stay normal numbers
 
 // A warp's state: lane (r, c) = (lane / 4, lane % 4) has heads 2 c, 2 c + 1 (columns of the
@@ -142,13 +143,23 @@ __device__ __forceinline__ void tail_tile(State &st, const uint32_t (&q)[8][2], 
     const int r = lane >> 2, c = lane & 3;
     const bool on0 = r < n, on1 = r + 8 < n;
     const uint4 zero = make_uint4(0, 0, 0, 0);
-    float x[1][4] = {{0.f, 0.f, 0.f, 0.f}};
+    uint4 k[4][2], v[4][2];  // all loads before the first use
 #pragma unroll
     for (int i = 0; i < 4; i++) {
         const int ch = (i >> 1) * 64 + c * 16 + (i & 1) * 8;
-        const uint4 a = on0 ? *reinterpret_cast<const uint4 *>(k0 + ch) : zero, b = on1 ? *reinterpret_cast<const uint4 *>(k1 + ch) : zero;
-        mma_16816(x[0], a.x, b.x, a.y, b.y, q[2 * i][0], q[2 * i][1]);
-        mma_16816(x[0], a.z, b.z, a.w, b.w, q[2 * i + 1][0], q[2 * i + 1][1]);
+        k[i][0] = on0 ? *reinterpret_cast<const uint4 *>(k0 + ch) : zero;
+        k[i][1] = on1 ? *reinterpret_cast<const uint4 *>(k1 + ch) : zero;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        v[i][0] = on0 ? *reinterpret_cast<const uint4 *>(v0 + 32 * i + 8 * c) : zero;
+        v[i][1] = on1 ? *reinterpret_cast<const uint4 *>(v1 + 32 * i + 8 * c) : zero;
+    }
+    float x[1][4] = {{0.f, 0.f, 0.f, 0.f}};
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        mma_16816(x[0], k[i][0].x, k[i][1].x, k[i][0].y, k[i][1].y, q[2 * i][0], q[2 * i][1]);
+        mma_16816(x[0], k[i][0].z, k[i][1].z, k[i][0].w, k[i][1].w, q[2 * i + 1][0], q[2 * i + 1][1]);
     }
     if (!on0) x[0][0] = x[0][1] = -INFINITY;
     if (!on1) x[0][2] = x[0][3] = -INFINITY;
@@ -156,10 +167,9 @@ __device__ __forceinline__ void tail_tile(State &st, const uint32_t (&q)[8][2], 
     weights<1>(st, x, kScale, 0.f, 1.f, b);
 #pragma unroll
     for (int j = 0; j < 4; j++) {
-        const uint4 x0 = on0 ? *reinterpret_cast<const uint4 *>(v0 + 32 * j + 8 * c) : zero;
-        const uint4 x1 = on1 ? *reinterpret_cast<const uint4 *>(v1 + 32 * j + 8 * c) : zero;
-        mma_16816(st.o[2 * j], transpose8(x0.x), transpose8(x0.y), transpose8(x1.x), transpose8(x1.y), b[0][0], b[0][1]);
-        mma_16816(st.o[2 * j + 1], transpose8(x0.z), transpose8(x0.w), transpose8(x1.z), transpose8(x1.w), b[0][0], b[0][1]);
+        mma_16816(st.o[2 * j], transpose8(v[j][0].x), transpose8(v[j][0].y), transpose8(v[j][1].x), transpose8(v[j][1].y), b[0][0], b[0][1]);
+        mma_16816(st.o[2 * j + 1], transpose8(v[j][0].z), transpose8(v[j][0].w), transpose8(v[j][1].z), transpose8(v[j][1].w), b[0][0],
+                  b[0][1]);
     }
 }
 
@@ -174,7 +184,7 @@ constexpr int kSmemBytes = kWarps * kStages * kPiece + (int)sizeof(Bars);
 static_assert(kWarps * (8 * 128 + 16) * 4 <= kWarps * kStages * kPiece, "shared memory");
 
 template <bool E4M3>
-__global__ void __launch_bounds__(kThreads, 2) block_decode_kernel(const __grid_constant__ BlockDecodeParams p) {
+__global__ void __launch_bounds__(kThreads, 3) block_decode_kernel(const __grid_constant__ BlockDecodeParams p) {
     extern __shared__ __align__(128) unsigned char sm[];
     Bars *bar = reinterpret_cast<Bars *>(sm + kWarps * kStages * kPiece);
     const int h = blockIdx.x, w = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
@@ -185,13 +195,13 @@ __global__ void __launch_bounds__(kThreads, 2) block_decode_kernel(const __grid_
         fence_barrier_init();
     }
     __syncthreads();
-    int lo = 0, hi = p.B - 1;  // the slot
+    int lo = 0, hi = p.n_slots - 1;  // the slot
     while (lo < hi) {
         const int mid = (lo + hi) >> 1;
         if (p.part0[mid + 1] > (int)blockIdx.y) hi = mid;
         else lo = mid + 1;
     }
-    const int b = lo, parts = p.part0[b + 1] - p.part0[b], part = blockIdx.y - p.part0[b];
+    const int b = p.slot[lo], parts = p.part0[lo + 1] - p.part0[lo], part = blockIdx.y - p.part0[lo];
     const size_t u = (size_t)b * p.H_kv + h;
     griddep_wait();
     const int4 ln = reinterpret_cast<const int4 *>(p.lens)[b];
@@ -219,7 +229,7 @@ __global__ void __launch_bounds__(kThreads, 2) block_decode_kernel(const __grid_
     unsigned char *ring = sm + w * kStages * kPiece;
     uint64_t *full = bar->full[w];
     const int32_t *row = p.ptab + (size_t)b * p.ptab_stride;
-    for (int t0 = 0; t0 < tiles; t0 += 32) {
+    for (int t0 = 0; t0 == 0 || t0 < tiles; t0 += 32) {
         const int m = min(32, tiles - t0);
         size_t at = 0;
         float sk = 0.f, sv = 0.f;
@@ -243,6 +253,16 @@ __global__ void __launch_bounds__(kThreads, 2) block_decode_kernel(const __grid_
             bulk_g2s(ring + stage * kPiece, (i & 1 ? p.v_codes : p.k_codes) + from, kPiece, &full[stage]);
         };
         for (int i = 0; i < min(kStages, 2 * m); i++) bring(i);
+        // the warp's fp16 tiles, while the first pieces are on their way
+        for (int i = t0 ? end : begin + w + (max(np - begin - w, 0) + kWarps - 1) / kWarps * kWarps; i < end; i += kWarps) {
+            const int x = (i - np) * kTailTokens;
+            auto at = [&](const uint16_t *sink, const uint16_t *res, int t) {
+                t = min(t, seen - 1);
+                return t < ln.x ? sink + (u * p.S + t) * 128 : res + (u * p.R + t - ln.x) * 128;
+            };
+            tail_tile(st, q, at(p.k_sink, p.k_res, x + r), at(p.k_sink, p.k_res, x + r + 8), at(p.v_sink, p.v_res, x + r),
+                      at(p.v_sink, p.v_res, x + r + 8), seen - x, lane);
+        }
         for (int t = 0; t < m; t++) {
             float x[4][4];
             uint32_t bp[4][2];
@@ -258,16 +278,6 @@ __global__ void __launch_bounds__(kThreads, 2) block_decode_kernel(const __grid_
             __syncwarp();
             if (i + 1 + kStages < 2 * m) bring(i + 1 + kStages);
         }
-    }
-    // fp16 tiles, from where the packed ones end
-    for (int i = max(begin, np) + w; i < end; i += kWarps) {
-        const int x = (i - np) * kTailTokens;
-        auto at = [&](const uint16_t *sink, const uint16_t *res, int t) {
-            t = min(t, seen - 1);
-            return t < ln.x ? sink + (u * p.S + t) * 128 : res + (u * p.R + t - ln.x) * 128;
-        };
-        tail_tile(st, q, at(p.k_sink, p.k_res, x + r), at(p.k_sink, p.k_res, x + r + 8), at(p.v_sink, p.v_res, x + r),
-                  at(p.v_sink, p.v_res, x + r + 8), seen - x, lane);
     }
     __syncthreads();  // every piece has arrived and been read
     float(*s_o)[8][128] = reinterpret_cast<float(*)[8][128]>(sm);
@@ -309,25 +319,51 @@ __global__ void __launch_bounds__(kThreads, 2) block_decode_kernel(const __grid_
     }
 }
 
-// Slots in several parts: a CTA per (query head of a key head, key head, slot).
-__global__ void __launch_bounds__(128) block_combine_kernel(const __grid_constant__ BlockDecodeParams p) {
-    const int e = blockIdx.x % p.g, h = blockIdx.x / p.g, b = blockIdx.y, d = threadIdx.x;
-    const int first = p.part0[b], parts = p.part0[b + 1] - first;
+// Slots in several parts: a CTA per (query head of a key head, key head, slot), its eight warps
+// every eighth part each, four at a time; then the warps' states in warp order.
+constexpr int kJoinWarps = 8;
+__global__ void __launch_bounds__(32 * kJoinWarps) block_combine_kernel(const __grid_constant__ BlockDecodeParams p) {
+    __shared__ float4 s_o[kJoinWarps][32];
+    __shared__ float2 s_ml[kJoinWarps];
+    const int e = blockIdx.x % p.g, h = blockIdx.x / p.g, at_slot = blockIdx.y, w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int first = p.part0[at_slot], parts = p.part0[at_slot + 1] - first, b = p.slot[at_slot];
     if (parts < 2) return;
     griddep_wait();
     const int4 ln = reinterpret_cast<const int4 *>(p.lens)[b];
     if (!ln.w || ln.x + ln.y + ln.z == 0) return;
     const size_t step = (size_t)p.H_kv * p.g, at = ((size_t)first * p.H_kv + h) * p.g + e;
-    float m = -INFINITY;
-    for (int i = 0; i < parts; i++) m = fmaxf(m, p.part_ml[at + i * step].x);
-    float l = 0.f, o = 0.f;
-    for (int i = 0; i < parts; i++) {
-        const float2 ml = p.part_ml[at + i * step];
-        const float f = factor(ml.x, m);
-        l = fmaf(f, ml.y, l);
-        o = fmaf(f, p.part_o[(at + i * step) * 128 + d], o);
+    float m = -INFINITY, l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    auto join = [&](const float2 &ml, const float4 &x) {
+        const float top = fmaxf(m, ml.x), f0 = factor(m, top), f1 = factor(ml.x, top);
+        m = top;
+        l = fmaf(f0, l, f1 * ml.y);
+        o.x = fmaf(f0, o.x, f1 * x.x);
+        o.y = fmaf(f0, o.y, f1 * x.y);
+        o.z = fmaf(f0, o.z, f1 * x.z);
+        o.w = fmaf(f0, o.w, f1 * x.w);
+    };
+    for (int i0 = w; i0 < parts; i0 += 4 * kJoinWarps) {
+        float2 ml[4];
+        float4 x[4];
+#pragma unroll
+        for (int k = 0; k < 4; k++) {
+            const size_t y = at + min(i0 + k * kJoinWarps, parts - 1) * step;
+            ml[k] = p.part_ml[y];
+            x[k] = reinterpret_cast<const float4 *>(p.part_o + y * 128)[lane];
+        }
+#pragma unroll
+        for (int k = 0; k < 4; k++)
+            if (i0 + k * kJoinWarps < parts) join(ml[k], x[k]);
     }
-    p.out[(((size_t)b * p.H_kv + h) * p.g + e) * 128 + d] = __half_as_ushort(__float2half_rn(o / l));
+    s_o[w][lane] = o;
+    if (lane == 0) s_ml[w] = make_float2(m, l);
+    __syncthreads();
+    if (w) return;
+    for (int i = 1; i < min(kJoinWarps, parts); i++) join(s_ml[i], s_o[i][lane]);
+    const float inv = 1.f / l;
+    uint16_t *dst = p.out + (((size_t)b * p.H_kv + h) * p.g + e) * 128;
+    reinterpret_cast<uint2 *>(dst)[lane] = make_uint2(pack_half2(o.x * inv, o.y * inv), pack_half2(o.z * inv, o.w * inv));
 }
 
 template <bool E4M3>
@@ -345,7 +381,7 @@ cudaError_t launch(dim3 grid, const BlockDecodeParams &p, cudaStream_t st) {
 }
 
 // CTAs that run at once, and the most parts of a call: each of them and one more per slot.
-int resident() { return 2 * host::num_sms(); }
+int resident() { return 3 * host::num_sms(); }
 int64_t most_parts(const kvq_config *c) { return host::cdiv(resident(), c->H_kv) + c->B; }
 
 size_t ml_bytes(const kvq_config *c) { return (size_t)host::cdiv(most_parts(c) * c->H_q * 8, 256) * 256; }
@@ -383,19 +419,31 @@ int block_decode(const kvq_config *c, const kvq_paged *pc, const uint16_t *q, ui
     p.S = c->S;
     p.R = c->R;
     p.ptab_stride = (int)(c->max_T / c->G);
-    int items[KVQ_PAGED_MAX_B], longest = 0, active = 0;
+    // items of the slots; slots of more items first (64 classes), so that what runs last is short
+    int items[KVQ_PAGED_MAX_B], count[64] = {0}, longest = 0, active = 0;
+    int64_t total = 0;
     for (int b = 0; b < c->B; b++) {
         const int32_t *l = pc->lens_host + 4 * b;
         items[b] = l[3] ? l[1] / kTokens + (l[0] + l[2] + kTailTokens - 1) / kTailTokens : 0;
         if (l[3] && l[1] && pc->n_pages < 1) return KVQ_ERR_INVALID_ARG;  // page 0 stands in for bad entries
         longest = std::max(longest, items[b]);
         active += items[b] > 0;
+        total += items[b];
     }
     if (!active) return KVQ_OK;
-    // parts of at most X items, the smallest X whose parts are all resident at once (a part each
-    // where there are more slots than that)
+    auto size_class = [&](int n) { return 63 - (int)((int64_t)n * 63 / longest); };
+    for (int b = 0; b < c->B; b++)
+        if (items[b]) count[size_class(items[b])]++;
+    for (int i = 0, at = 0; i < 64; i++) {
+        const int n = count[i];
+        count[i] = at;
+        at += n;
+    }
+    for (int b = 0; b < c->B; b++)
+        if (items[b]) p.slot[count[size_class(items[b])]++] = (int16_t)b;
+    // parts of at most X items, the smallest X whose parts are all resident at once
     const int64_t room = std::max<int64_t>(active, host::cdiv(resident(), c->H_kv));
-    int lo = 1, hi = longest;
+    int lo = std::min(longest, kLeast), hi = longest;
     while (lo < hi) {
         const int X = (lo + hi) / 2;
         int64_t parts = 0;
@@ -405,16 +453,17 @@ int block_decode(const kvq_config *c, const kvq_paged *pc, const uint16_t *q, ui
     }
     bool cut = false;
     int parts = 0;
-    for (int b = 0; b < c->B; b++) {
-        p.part0[b] = parts;
-        const int n = (items[b] + lo - 1) / lo;
+    for (int i = 0; i < active; i++) {
+        p.part0[i] = parts;
+        const int n = (items[p.slot[i]] + lo - 1) / lo;
         cut |= n > 1;
         parts += n;
     }
-    for (int b = c->B; b <= KVQ_PAGED_MAX_B; b++) p.part0[b] = parts;
+    p.n_slots = active;
+    p.part0[active] = parts;
     const dim3 grid((unsigned)c->H_kv, (unsigned)parts);
     cudaError_t e = c->mode == KVQ_MODE_E4M3 ? launch<true>(grid, p, st) : launch<false>(grid, p, st);
-    if (e == cudaSuccess && cut) e = launch_dependent(block_combine_kernel, dim3((unsigned)c->H_q, (unsigned)c->B), 128, 0, st, p);
+    if (e == cudaSuccess && cut) e = launch_dependent(block_combine_kernel, dim3((unsigned)c->H_q, (unsigned)active), 32 * kJoinWarps, 0, st, p);
     return host::status_of(e);
 }
 
