@@ -220,28 +220,29 @@ __device__ __forceinline__ void make_tile(uint32_t raw, uint32_t tile, int t, in
     }
 }
 
-// The same of 8-bit codes with a scale per page, without it.  raw: two pieces of 64 tokens as they
-// lie in a page; the second one, where it does not exist, becomes zeros.  Sixteen codes make two
-// 16-byte chunks; of keys, lanes with the upper channels store the second one first, so that the
-// lanes of a row use all banks.
+// The same of 64 tokens (half h of a tile) of 8-bit codes with a scale per page, without it.  raw:
+// the tokens as they lie in a page; those of a half that does not exist become zeros.  Sixteen
+// codes make two 16-byte chunks; of keys, lanes with the upper channels store the second one
+// first, so that the lanes of a row use all banks.
 template <bool E4M3>
-__device__ __forceinline__ void make_block_tile(uint32_t raw, uint32_t tile, int t, bool value, bool both) {
+__device__ __forceinline__ void make_block_half(uint32_t raw, uint32_t tile, int t, bool value, int h, bool exists) {
 #pragma unroll 1
-    for (int i = 0; i < 8; i++) {
-        int row, half, j, second = 0;
+    for (int i = 0; i < 4; i++) {
+        const int j = t & 3, second = value ? 0 : (t >> 2) & 1;
+        int row;
         uint32_t from, to;
         if (value) {
-            half = i >> 2, row = (t >> 2) + 32 * (i & 3), j = t & 3;
-            from = raw + half * 8192 + row * 64 + j * 16;
-            to = tile + half * 16384 + row * 128;
+            row = (t >> 2) + 32 * i;
+            from = raw + row * 64 + j * 16;
+            to = tile + h * 16384 + row * 128;
         } else {
-            row = (t >> 3) + 16 * i, half = i >> 2, j = t & 3, second = (t >> 2) & 1;
+            row = (t >> 3) + 16 * i;
             from = raw + row * 128 + (((t & 7) ^ ((row & 1) << 2)) << 4);
-            to = tile + second * 16384 + row * 128;
+            to = tile + second * 16384 + (64 * h + row) * 128;
         }
         uint32_t w[4], y[8];
         lds128(w, from);
-        if (half && !both) w[0] = w[1] = w[2] = w[3] = 0;
+        if (!exists) w[0] = w[1] = w[2] = w[3] = 0;
 #pragma unroll
         for (int e = 0; e < 4; e++) code_pairs<E4M3>(w[e], y[2 * e], y[2 * e + 1]);
 #pragma unroll
@@ -303,13 +304,14 @@ struct Ring {
     }
 };
 
-// Shared memory of the packed tiles of one side.
+// Shared memory of the packed tiles of one side; FMT > 0: of a tile's halves, each with a slot of
+// its own (whole tiles, one slot a side: 2.4 us a tile of 256 rows against XX).
 template <int FMT>
 struct Raw {
     int slots, size, off;
     __device__ __forceinline__ Raw(const ChunkAttnParams &p, bool value) {
-        const int kraw = FMT ? 16384 + 64 : 2048 * p.kbits + 512, vraw = FMT ? 16384 : 2048 * p.vbits + 512;
-        slots = min(kMaxRaw, kRawBytes / (kraw + vraw));
+        const int kraw = FMT ? 8192 + 32 : 2048 * p.kbits + 512, vraw = FMT ? 8192 : 2048 * p.vbits + 512;
+        slots = FMT ? 2 : min(kMaxRaw, kRawBytes / (kraw + vraw));
         size = value ? vraw : kraw;
         off = kOffRaw + (value ? slots * kraw : 0);
     }
@@ -337,33 +339,33 @@ __device__ __forceinline__ void bring(const ChunkAttnParams &p, unsigned char *s
         const int32_t *row = p.ptab + (size_t)s.it.b * p.ptab_stride;
         if (s.k0 >= npk) continue;
         if (FMT) {
-            // two pieces of 64 tokens with their pages' scales (those of the values come with the
-            // keys: the softmax needs them before the value tile is made)
-            const int sh = p.G == 64 ? 6 : p.G == 128 ? 7 : 8, last = (s.it.s.T >> 6) - 1;
-            auto entry_of = [&](int piece) { return row[(min(piece, last) << 6) >> sh]; };
-            int32_t e0 = entry_of(2 * s.k0), e1 = entry_of(2 * s.k0 + 1);
-            for (int kt = s.k0; kt < npk; kt++) {
-                const int32_t a0 = entry_of(2 * kt + 2), a1 = entry_of(2 * kt + 3);
+            // halves of 64 tokens, with their pages' scales (those of the values come with the keys:
+            // the softmax needs them before the value tile is made)
+            const int sh = p.G == 64 ? 6 : p.G == 128 ? 7 : 8, pieces = s.it.s.T >> 6;
+            auto entry_of = [&](int piece) { return row[(min(piece, pieces - 1) << 6) >> sh]; };
+            int32_t entry = entry_of(2 * s.k0);
+            for (int i = 2 * s.k0; i < 2 * npk; i++) {
+                const int32_t ahead = entry_of(i + 1);
                 await(&read[cp.i], cp.parity, &bar->stop, p.status);
                 if (*(volatile int *)&bar->stop) break;
                 unsigned char *dst = sm + raw.off + cp.i * raw.size;
-                const int par = (n0 + kt) & 1, bit = 1 << (kMaxRaw * par + cp.i), pieces = 2 * kt < last ? 2 : 1;
+                const int par = (n0 + (i >> 1)) & 1, bit = 1 << (kMaxRaw * par + cp.i);
                 uint64_t *b = &arrived[par][cp.i];
-                mbar_arrive_expect_tx(b, pieces * (8192 + (value ? 0 : 32)));
-                for (int j = 0; j < pieces; j++) {
-                    const int64_t page = page_index(p, s.it, j ? e1 : e0);
-                    const int t0 = (kt * kChunkKeys + 64 * j) & (p.G - 1);
-                    bulk_g2s(dst + 8192 * j, reinterpret_cast<const unsigned char *>(codes) + ((size_t)page * p.G + t0) * kD, 8192, b);
+                if (i < pieces) {
+                    const int64_t page = page_index(p, s.it, entry);
+                    mbar_arrive_expect_tx(b, 8192 + (value ? 0 : 32));
+                    bulk_g2s(dst, reinterpret_cast<const unsigned char *>(codes) + ((size_t)page * p.G + (i * 64 & (p.G - 1))) * kD, 8192, b);
                     if (!value) {
-                        bulk_g2s(dst + 16384 + 32 * j, reinterpret_cast<const float4 *>(p.k_meta) + page, 16, b);
-                        bulk_g2s(dst + 16384 + 32 * j + 16, reinterpret_cast<const float4 *>(p.v_meta) + page, 16, b);
+                        bulk_g2s(dst + 8192, reinterpret_cast<const float4 *>(p.k_meta) + page, 16, b);
+                        bulk_g2s(dst + 8208, reinterpret_cast<const float4 *>(p.v_meta) + page, 16, b);
                     }
+                } else {
+                    mbar_arrive(b);  // the last tile's second half
                 }
-                cp.next(raw.slots);
+                cp.next(2);
                 used |= bit;
                 parity ^= bit;
-                e0 = a0;
-                e1 = a1;
+                entry = ahead;
             }
             continue;
         }
@@ -429,20 +431,28 @@ __device__ __forceinline__ void produce(const ChunkAttnParams &p, unsigned char 
                 if (kt < s.np && ++slot == raw.slots) slot = 0;
                 continue;
             }
-            if (kt < s.np) {
+            if (FMT && kt < s.np) {
+                await(empty, free, &bar->stop, p.status);
+#pragma unroll 1
+                for (int h = 0; h < 2; h++) {
+                    await(&arrived[h], (landed >> h) & 1, &bar->stop, p.status);
+                    landed ^= 1u << h;
+                    const unsigned char *from = sm + raw.off + h * raw.size;
+                    const bool exists = 2 * kt + h < s.it.s.T >> 6;
+                    if (!value && tid == 0) {
+                        const float *m = reinterpret_cast<const float *>(from + 8192);
+                        bar->scale[(n + kt - s.k0) % kScaleRing][h] =
+                            exists ? make_float4(m[0] * kScale, log2f(m[4]), 1.f / m[4], 0.f) : make_float4(kScale, 0.f, 1.f, 0.f);
+                    }
+                    make_block_half<FMT == kE4m3>(smem_u32(from), smem_u32(dst), tid, value, h, exists);
+                    mbar_arrive(&read[h]);
+                }
+            } else if (kt < s.np) {
                 await(&arrived[slot], (landed >> slot) & 1, &bar->stop, p.status);
                 landed ^= 1u << slot;
                 await(empty, free, &bar->stop, p.status);
                 const uint32_t from = smem_u32(sm + raw.off + slot * raw.size), to = smem_u32(dst);
-                if (FMT) {
-                    const bool both = 2 * kt + 1 < s.it.s.T >> 6;
-                    if (!value && tid < 2) {
-                        const float *m = reinterpret_cast<const float *>(sm + raw.off + slot * raw.size + 16384 + 32 * tid);
-                        bar->scale[(n + kt - s.k0) % kScaleRing][tid] =
-                            tid == 0 || both ? make_float4(m[0] * kScale, log2f(m[4]), 1.f / m[4], 0.f) : make_float4(kScale, 0.f, 1.f, 0.f);
-                    }
-                    make_block_tile<FMT == kE4m3>(from, to, tid, value, both);
-                } else if (bits == 2) make_tile<2>(from, to, tid, TV);
+                if (bits == 2) make_tile<2>(from, to, tid, TV);
                 else if (bits == 4) make_tile<4>(from, to, tid, TV);
                 else make_tile<8>(from, to, tid, TV);
                 mbar_arrive(&read[slot]);
