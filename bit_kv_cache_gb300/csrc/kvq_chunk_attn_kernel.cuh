@@ -95,8 +95,13 @@ constexpr float kNearExp = 512.f;
 enum { kMinMax = 0, kE4m3 = 1, kInt8 = 2 };
 constexpr int kScaleRing = 8;  // tiles whose scales are held; producers are at most five tiles ahead of a softmax group
 // registers of a thread after the split; 64 at launch, times 1024 threads
-constexpr int kRegsSoftmax = 112, kRegsTiles = 48, kRegsOther = 48;
-static_assert(256 * kRegsSoftmax + 512 * kRegsTiles + 256 * kRegsOther <= kThreads * 64, "register split");
+constexpr int kRegsSoftmax = 112;
+template <int FMT>
+constexpr int kRegsTiles = FMT ? 56 : 48;
+template <int FMT>
+constexpr int kRegsOther = FMT ? 32 : 48;
+static_assert(256 * kRegsSoftmax + 512 * 48 + 256 * 48 <= kThreads * 64 && 256 * kRegsSoftmax + 512 * 56 + 256 * 32 <= kThreads * 64,
+              "register split");
 
 struct Bars {
     uint64_t q_full, q_empty, k_full[kRing], k_empty[kRing], v_full[kRing], v_empty[kRing];
@@ -220,42 +225,46 @@ __device__ __forceinline__ void make_tile(uint32_t raw, uint32_t tile, int t, in
     }
 }
 
-// The same of 64 tokens (half h of a tile) of 8-bit codes with a scale per page, without it.  raw:
-// the tokens as they lie in a page; those of a half that does not exist become zeros.  Sixteen
-// codes make two 16-byte chunks; of keys, lanes with the upper channels store the second one
-// first, so that the lanes of a row use all banks.
-template <bool E4M3>
-__device__ __forceinline__ void make_block_half(uint32_t raw, uint32_t tile, int t, bool value, int h, bool exists) {
-#pragma unroll 1
-    for (int i = 0; i < 4; i++) {
-        const int j = t & 3, second = value ? 0 : (t >> 2) & 1;
-        int row;
-        uint32_t from, to;
+// A tile of 8-bit codes with a scale per page, made from registers: a thread of the group holds 16
+// codes of eight rows, loaded while the tile before was made.  Keys: rows (tokens) t / 8 + 16 i,
+// 16-byte chunk t mod 8 as stored; values: rows (channels) t / 4 + 32 (i mod 4) of half i / 4,
+// chunk t mod 4.  Sixteen codes make two 16-byte chunks of the fp16 row; of keys, lanes with the
+// upper channels store the second one first, so that the lanes of a row use all banks.
+struct BlockTile {
+    uint4 w[8];
+    uint32_t to0, to1;     // of row 0: first and second chunk stored
+    int from;              // offset of row 0 in a half
+    __device__ __forceinline__ BlockTile(uint32_t tile, int t, bool value) {
         if (value) {
-            row = (t >> 2) + 32 * i;
-            from = raw + row * 64 + j * 16;
-            to = tile + h * 16384 + row * 128;
+            const int row = t >> 2, j = t & 3;
+            from = row * 64 + j * 16;
+            to0 = tile + row * 128 + (((2 * j) ^ (row & 7)) << 4);
+            to1 = tile + row * 128 + (((2 * j + 1) ^ (row & 7)) << 4);
         } else {
-            row = (t >> 3) + 16 * i;
-            from = raw + row * 128 + (((t & 7) ^ ((row & 1) << 2)) << 4);
-            to = tile + second * 16384 + (64 * h + row) * 128;
-        }
-        uint32_t w[4], y[8];
-        lds128(w, from);
-        if (!exists) w[0] = w[1] = w[2] = w[3] = 0;
-#pragma unroll
-        for (int e = 0; e < 4; e++) code_pairs<E4M3>(w[e], y[2 * e], y[2 * e + 1]);
-#pragma unroll
-        for (int e = 0; e < 2; e++) {
-            const int k = e ^ second;
-            const uint32_t at = to + (((2 * j + k) ^ (row & 7)) << 4);
-            const uint32_t *z = y + 4 * e;
-            uint32_t z0 = z[0], z1 = z[1], z2 = z[2], z3 = z[3];
-            if (second) z0 = y[4 - 4 * e], z1 = y[5 - 4 * e], z2 = y[6 - 4 * e], z3 = y[7 - 4 * e];
-            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(z0), "r"(z1), "r"(z2), "r"(z3) : "memory");
+            const int row = t >> 3, j = t & 3, upper = (t >> 2) & 1;
+            from = row * 128 + (((t & 7) ^ ((row & 1) << 2)) << 4);
+            to0 = tile + upper * 16384 + row * 128 + (((2 * j + upper) ^ (row & 7)) << 4);
+            to1 = tile + upper * 16384 + row * 128 + (((2 * j + 1 - upper) ^ (row & 7)) << 4);
         }
     }
-}
+    __device__ __forceinline__ void load(int i, const unsigned char *half) {  // null: no such tokens
+        w[i] = half ? __ldcg(reinterpret_cast<const uint4 *>(half + from + (i & 3) * 2048)) : make_uint4(0, 0, 0, 0);
+    }
+    template <bool E4M3>
+    __device__ __forceinline__ void store(int i, bool value, bool swap) const {
+        uint32_t y[8];
+        code_pairs<E4M3>(w[i].x, y[0], y[1]);
+        code_pairs<E4M3>(w[i].y, y[2], y[3]);
+        code_pairs<E4M3>(w[i].z, y[4], y[5]);
+        code_pairs<E4M3>(w[i].w, y[6], y[7]);
+        const uint32_t off = value ? (i >> 2) * 16384 + (i & 3) * 4096 : i * 2048;
+#pragma unroll
+        for (int e = 0; e < 2; e++)
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"((e ? to1 : to0) + off), "r"(swap ? y[4 - 4 * e] : y[4 * e]),
+                         "r"(swap ? y[5 - 4 * e] : y[4 * e + 1]), "r"(swap ? y[6 - 4 * e] : y[4 * e + 2]),
+                         "r"(swap ? y[7 - 4 * e] : y[4 * e + 3]) : "memory");
+    }
+};
 
 // 16 bytes from global to shared memory without registers (zeros if !ok).
 __device__ __forceinline__ void copy16(void *dst, const void *src, bool ok) {
@@ -304,14 +313,12 @@ struct Ring {
     }
 };
 
-// Shared memory of the packed tiles of one side; FMT > 0: of a tile's halves, each with a slot of
-// its own (whole tiles, one slot a side: 2.4 us a tile of 256 rows against XX).
-template <int FMT>
+// Shared memory of the packed tiles of one side.
 struct Raw {
     int slots, size, off;
     __device__ __forceinline__ Raw(const ChunkAttnParams &p, bool value) {
-        const int kraw = FMT ? 8192 + 32 : 2048 * p.kbits + 512, vraw = FMT ? 8192 : 2048 * p.vbits + 512;
-        slots = FMT ? 2 : min(kMaxRaw, kRawBytes / (kraw + vraw));
+        const int kraw = 2048 * p.kbits + 512, vraw = 2048 * p.vbits + 512;
+        slots = min(kMaxRaw, kRawBytes / (kraw + vraw));
         size = value ? vraw : kraw;
         off = kOffRaw + (value ? slots * kraw : 0);
     }
@@ -321,9 +328,8 @@ struct Raw {
 // One lane brings the packed tiles of the keys (values) into their ring, as far ahead as it
 // has slots.  The page-table entry of a tile is read before the copy of the tile before it
 // is waited for.
-template <int FMT>
 __device__ __forceinline__ void bring(const ChunkAttnParams &p, unsigned char *sm, Bars *bar, bool value) {
-    const Raw<FMT> raw(p, value);
+    const Raw raw(p, value);
     const int bits = value ? p.vbits : p.kbits;
     uint64_t(*arrived)[kMaxRaw] = value ? bar->rawv : bar->rawk, *read = value ? bar->readv : bar->readk;
     const int32_t *codes = value ? p.v_codes : p.k_codes;
@@ -338,37 +344,6 @@ __device__ __forceinline__ void bring(const ChunkAttnParams &p, unsigned char *s
         n += s.k1 - s.k0;
         const int32_t *row = p.ptab + (size_t)s.it.b * p.ptab_stride;
         if (s.k0 >= npk) continue;
-        if (FMT) {
-            // halves of 64 tokens, with their pages' scales (those of the values come with the keys:
-            // the softmax needs them before the value tile is made)
-            const int sh = p.G == 64 ? 6 : p.G == 128 ? 7 : 8, pieces = s.it.s.T >> 6;
-            auto entry_of = [&](int piece) { return row[(min(piece, pieces - 1) << 6) >> sh]; };
-            int32_t entry = entry_of(2 * s.k0);
-            for (int i = 2 * s.k0; i < 2 * npk; i++) {
-                const int32_t ahead = entry_of(i + 1);
-                await(&read[cp.i], cp.parity, &bar->stop, p.status);
-                if (*(volatile int *)&bar->stop) break;
-                unsigned char *dst = sm + raw.off + cp.i * raw.size;
-                const int par = (n0 + (i >> 1)) & 1, bit = 1 << (kMaxRaw * par + cp.i);
-                uint64_t *b = &arrived[par][cp.i];
-                if (i < pieces) {
-                    const int64_t page = page_index(p, s.it, entry);
-                    mbar_arrive_expect_tx(b, 8192 + (value ? 0 : 32));
-                    bulk_g2s(dst, reinterpret_cast<const unsigned char *>(codes) + ((size_t)page * p.G + (i * 64 & (p.G - 1))) * kD, 8192, b);
-                    if (!value) {
-                        bulk_g2s(dst + 8192, reinterpret_cast<const float4 *>(p.k_meta) + page, 16, b);
-                        bulk_g2s(dst + 8208, reinterpret_cast<const float4 *>(p.v_meta) + page, 16, b);
-                    }
-                } else {
-                    mbar_arrive(b);  // the last tile's second half
-                }
-                cp.next(2);
-                used |= bit;
-                parity ^= bit;
-                entry = ahead;
-            }
-            continue;
-        }
         int32_t entry = row[s.k0 >> gshift];
         for (int kt = s.k0; kt < npk; kt++) {
             const int32_t ahead = row[min(kt + 1, npk - 1) >> gshift];
@@ -401,10 +376,13 @@ __device__ __forceinline__ void bring(const ChunkAttnParams &p, unsigned char *s
 template <int FMT>
 __device__ __forceinline__ void produce(const ChunkAttnParams &p, unsigned char *sm, Bars *bar, bool value, int par) {
     const int tid = threadIdx.x & 127, bits = value ? p.vbits : p.kbits, TV = value ? 256 / p.kbits : kChunkKeys;
-    const Raw<FMT> raw(p, value);
+    const Raw raw(p, value);
     unsigned char *dst = sm + (value ? kOffV : kOffK) + par * kTileBytes;
     uint64_t *arrived = (value ? bar->rawv : bar->rawk)[par], *read = value ? bar->readv : bar->readk;
     uint64_t *full = (value ? bar->v_full : bar->k_full) + par, *empty = (value ? bar->v_empty : bar->k_empty) + par;
+    BlockTile bt(smem_u32(dst), tid, value);
+    const unsigned char *codes = reinterpret_cast<const unsigned char *>(value ? p.v_codes : p.k_codes);
+    const int sh = p.G == 64 ? 6 : p.G == 128 ? 7 : 8;
     int slot = 0;              // of the next packed tile, of either parity
     uint32_t landed = 0, free = 1, nq = 1;  // parities: of the slots' arrivals, of the tile's release
     int n = 0;                 // tiles of the segments before
@@ -426,6 +404,35 @@ __device__ __forceinline__ void produce(const ChunkAttnParams &p, unsigned char 
             fence_proxy_async();
             mbar_arrive(&bar->q_full);
         }
+        // 8-bit tiles: the registers hold the group's next one, ent the page-table entries of the one
+        // behind it, sk and sv (keys, threads 0 and 1) the scales of a half
+        int32_t ent[2] = {0, 0};
+        float sk = 0.f, sv = 0.f;
+        const int npk = min(s.k1, s.np), pieces = s.it.s.T >> 6;
+        auto entries = [&](int kt) {
+            const int32_t *row = p.ptab + (size_t)s.it.b * p.ptab_stride;
+#pragma unroll
+            for (int h = 0; h < 2; h++) ent[h] = row[(min(2 * kt + h, pieces - 1) << 6) >> sh];
+        };
+        auto half_of = [&](int kt, int h) -> const unsigned char * {
+            if (2 * kt + h >= pieces) return nullptr;
+            const int64_t page = page_index(p, s.it, ent[h]);
+            if (!value && tid == h) {
+                sk = __ldcg(reinterpret_cast<const float *>(p.k_meta) + 4 * page);
+                sv = __ldcg(reinterpret_cast<const float *>(p.v_meta) + 4 * page);
+            }
+            return codes + ((size_t)page * p.G + ((2 * kt + h) * 64 & (p.G - 1))) * kD;
+        };
+        if (FMT) {
+            const int kt = s.k0 + ((n & 1) != par);
+            if (kt < npk) {
+                entries(kt);
+                const unsigned char *h0 = half_of(kt, 0), *h1 = half_of(kt, 1);
+#pragma unroll
+                for (int i = 0; i < 8; i++) bt.load(i, i < 4 ? h0 : h1);
+                if (kt + 2 < npk) entries(kt + 2);
+            }
+        }
         for (int kt = s.k0; kt < s.k1; kt++) {
             if (((n + kt - s.k0) & 1) != par) {
                 if (kt < s.np && ++slot == raw.slots) slot = 0;
@@ -433,19 +440,20 @@ __device__ __forceinline__ void produce(const ChunkAttnParams &p, unsigned char 
             }
             if (FMT && kt < s.np) {
                 await(empty, free, &bar->stop, p.status);
-#pragma unroll 1
-                for (int h = 0; h < 2; h++) {
-                    await(&arrived[h], (landed >> h) & 1, &bar->stop, p.status);
-                    landed ^= 1u << h;
-                    const unsigned char *from = sm + raw.off + h * raw.size;
-                    const bool exists = 2 * kt + h < s.it.s.T >> 6;
-                    if (!value && tid == 0) {
-                        const float *m = reinterpret_cast<const float *>(from + 8192);
-                        bar->scale[(n + kt - s.k0) % kScaleRing][h] =
-                            exists ? make_float4(m[0] * kScale, log2f(m[4]), 1.f / m[4], 0.f) : make_float4(kScale, 0.f, 1.f, 0.f);
-                    }
-                    make_block_half<FMT == kE4m3>(smem_u32(from), smem_u32(dst), tid, value, h, exists);
-                    mbar_arrive(&read[h]);
+                if (!value && tid < 2)
+                    bar->scale[(n + kt - s.k0) % kScaleRing][tid] =
+                        2 * kt + tid < pieces ? make_float4(sk * kScale, log2f(sv), 1.f / sv, 0.f) : make_float4(kScale, 0.f, 1.f, 0.f);
+                const bool more = kt + 2 < npk;
+                const unsigned char *h0 = nullptr, *h1 = nullptr;
+                if (more) {
+                    h0 = half_of(kt + 2, 0);
+                    h1 = half_of(kt + 2, 1);
+                    if (kt + 4 < npk) entries(kt + 4);
+                }
+#pragma unroll
+                for (int i = 0; i < 8; i++) {
+                    bt.store<FMT == kE4m3>(i, value, !value && (tid & 4));
+                    if (more) bt.load(i, i < 4 ? h0 : h1);
                 }
             } else if (kt < s.np) {
                 await(&arrived[slot], (landed >> slot) & 1, &bar->stop, p.status);
@@ -935,10 +943,10 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attn_kernel(const __grid_co
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
         softmax<FMT>(p, bar, tm, w >> 2);
     } else if (w < 24) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsTiles));
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsTiles<FMT>));
         produce<FMT>(p, sm, bar, w >= 16, (w >> 2) & 1);
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther<FMT>));
         if (w < 28) {
             if (w < 26) issue_scores(p, sm, bar, tm, w & 1);
             else issue_values(p, sm, bar, tm, w & 1);
@@ -946,7 +954,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_attn_kernel(const __grid_co
             tc_commit(&bar->drain, (threadIdx.x & 31) == 0);
             mbar_wait(&bar->drain, 0, p.status);  // every product has ended before the tensor memory is freed
         } else if (w < 30 && (threadIdx.x & 31) == 0) {
-            bring<FMT>(p, sm, bar, w == 29);
+            if (FMT == kMinMax) bring(p, sm, bar, w == 29);
         }
     }
     __syncwarp();
