@@ -21,21 +21,25 @@ struct BlockListParams : PackParams {
     int32_t lp0[KVQ_PAGED_MAX_B];
 };
 
-// Decode attention.  A CTA is (key head, part of a slot): the slot's items, packed tiles of 64
-// tokens and then 16-token tiles of the fp16 tokens [sink | residual], are cut into equal parts.
+// Attention of at most kFewRows rows (new tokens times query heads) per key head of a slot.  A CTA
+// is (key head, part of a slot): the slot's items, packed tiles of 64 tokens and then 16-token tiles
+// of the fp16 tokens [sink | residual | new ones], are cut into equal parts.
+constexpr int kFewRows = 32, kFewTiles = 4096;
 struct BlockDecodeParams {
-    const uint16_t *q;
+    const uint16_t *q, *k_new, *v_new;   // new rows of a chunk (decode: none, the cache holds the token)
+    int64_t q_stride, k_stride, v_stride;
     uint16_t *out;
     const uint8_t *k_codes, *v_codes;
     const float4 *k_scale, *v_scale;     // a page's scale in the first component
     const uint16_t *k_sink, *v_sink, *k_res, *v_res;
-    const int32_t *ptab, *lens;
-    float *part_o;                       // [parts][H_kv][g][128], of slots in several parts
-    float2 *part_ml;                     // [parts][H_kv][g]
+    const int32_t *ptab, *lens, *desc;   // desc: of a plan (null: lens, one row per query head)
+    float *part_o;                       // [parts][H_kv][most_rows][128], of slots in several parts
+    float2 *part_ml;                     // [parts][H_kv][most_rows]
     int32_t *status;
     int64_t n_pages;
-    int B, H_kv, g, g_shift, S, R, ptab_stride;  // g_shift: log2(G)
-    int n_slots;                         // that hold tokens
+    int H_kv, g, g_shift, S, R, ptab_stride;  // g_shift: log2(G)
+    int most_rows;                       // of a slot
+    int n_slots;                         // of the call
     int16_t slot[KVQ_PAGED_MAX_B];       // those
     int32_t part0[KVQ_PAGED_MAX_B + 1];  // parts of the ones before each
 };
@@ -45,5 +49,8 @@ cudaError_t launch_block_list(const BlockListParams &p, bool e4m3, cudaStream_t 
 size_t block_decode_ws_bytes(const kvq_config *c);
 int block_decode(const kvq_config *c, const kvq_paged *pc, const uint16_t *q, uint16_t *out, void *ws, size_t ws_bytes,
                  cudaStream_t st);
+// The chunk attention of the slots few[]; inputs, output and partials as of `a`.
+int block_chunk_few(const kvq_config *c, const kvq_paged *pc, const ChunkSlot *slots, const bool *few, const ChunkAttnParams &a,
+                    cudaStream_t st);
 
 }  // namespace kvq

@@ -1,7 +1,8 @@
 // kvq_block_decode.cu -- attention of one token per slot over an 8-bit cache with one scale per
-// page and head (kvq_paged_decode_attn).
+// page and head (kvq_paged_decode_attn), and of a few new tokens per slot (kvq_paged_chunk_attn).
 //
-// For head e of a key head's group and token t, with the page's scales s_K and s_V,
+// For a row (query head of a key head's group, token) and cached token t, with the page's scales
+// s_K and s_V,
 //   y_t = (q . code_t) s_K log2(e) / sqrt(D) + log2(s_V),   w_t = 2^(y_t - m),
 //   O = sum w_t code_t,   l = sum w_t / s_V,   out = O / l:
 // the value scale is part of the exponent, so both products have exact operands (codes in fp16)
@@ -13,6 +14,7 @@
 #include <string.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "kvq_block.cuh"
 #include "kvq_block.h"
@@ -28,12 +30,28 @@ constexpr int kStages = 2, kPiece = 8192;                // of a warp's ring: ke
 constexpr int kTokens = 64, kTailTokens = 16;            // of an item: packed, fp16
 constexpr int kLeast = 16;                               // items of a part, if the slot has as many
 constexpr float kUp = 6.f, kSlack = 8.f;                 // w <= 2^(kUp + kSlack); small weights stay normal numbers
+static_assert(kFewRows == 32, "row tiles of the largest form");
 
-// A warp's state: lane (r, c) = (lane / 4, lane % 4) has heads 2 c, 2 c + 1 (columns of the
-// products) and, of the output, channels of rows r and r + 8 of eight 16-row tiles.
+// A warp's state for NT tiles of 8 rows: lane (r, c) = (lane / 4, lane % 4) has rows 2 c, 2 c + 1 of
+// each (columns of the products) and, of the output, channels of rows r and r + 8 of eight 16-row
+// tiles.
+template <int NT>
 struct State {
-    float m[2], l[2];   // l: the lane's own share
-    float o[8][4];
+    float m[NT][2], l[NT][2];   // l: the lane's own share
+    float o[NT][8][4];
+};
+
+// Query operands: rows of tile n, step i, of a lane.  One tile stays in registers, more in shared
+// memory.
+template <int NT>
+struct Queries {
+    const uint2 *sm;
+    __device__ __forceinline__ uint2 get(int i, int n, int lane) const { return sm[(i * NT + n) * 32 + lane]; }
+};
+template <>
+struct Queries<1> {
+    uint2 x[8];
+    __device__ __forceinline__ uint2 get(int i, int, int) const { return x[i]; }
 };
 
 // The channel of output row r (hi: r + 8) of tile i.
@@ -45,10 +63,10 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
     return y;
 }
 
-// Scores of 16 N tokens (x[s]: rows r and r + 8 of group s, heads 2 c, 2 c + 1) to weights, as B
-// operands of the value product.  a, lsv: y = x a + lsv; inv: 1 / s_V.
-template <int N>
-__device__ __forceinline__ void weights(State &st, float (&x)[N][4], float a, float lsv, float inv, uint32_t (&b)[N][2]) {
+// Scores of 16 N tokens (x[s]: tokens r and r + 8 of group s, rows 2 c, 2 c + 1 of row tile n) to
+// weights, as B operands of the value product.  a, lsv: y = x a + lsv; inv: 1 / s_V.
+template <int N, int NT>
+__device__ __forceinline__ void weights(State<NT> &st, int n, float (&x)[N][4], float a, float lsv, float inv, uint32_t (&b)[N][2]) {
 #pragma unroll
     for (int s = 0; s < N; s++)
 #pragma unroll
@@ -60,22 +78,22 @@ __device__ __forceinline__ void weights(State &st, float (&x)[N][4], float a, fl
 #pragma unroll
         for (int s = 1; s < N; s++) top[e] = fmaxf(top[e], fmaxf(x[s][e], x[s][2 + e]));
     }
-    if (__any_sync(0xffffffffu, top[0] > st.m[0] + kSlack || top[1] > st.m[1] + kSlack)) {
+    if (__any_sync(0xffffffffu, top[0] > st.m[n][0] + kSlack || top[1] > st.m[n][1] + kSlack)) {
 #pragma unroll
         for (int e = 0; e < 2; e++) {
 #pragma unroll
             for (int o = 4; o < 32; o <<= 1) top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], o));
-            const float m = fmaxf(st.m[e], top[e]), f = m == st.m[e] ? 1.f : ex2(st.m[e] - m);
-            st.m[e] = m;
-            st.l[e] *= f;
+            const float m = fmaxf(st.m[n][e], top[e]), f = m == st.m[n][e] ? 1.f : ex2(st.m[n][e] - m);
+            st.m[n][e] = m;
+            st.l[n][e] *= f;
 #pragma unroll
             for (int i = 0; i < 8; i++) {
-                st.o[i][e] *= f;
-                st.o[i][2 + e] *= f;
+                st.o[n][i][e] *= f;
+                st.o[n][i][2 + e] *= f;
             }
         }
     }
-    const float off[2] = {st.m[0] == -INFINITY ? 0.f : kUp - st.m[0], st.m[1] == -INFINITY ? 0.f : kUp - st.m[1]};
+    const float off[2] = {st.m[n][0] == -INFINITY ? 0.f : kUp - st.m[n][0], st.m[n][1] == -INFINITY ? 0.f : kUp - st.m[n][1]};
     float sum[2] = {0.f, 0.f};
 #pragma unroll
     for (int s = 0; s < N; s++) {
@@ -87,8 +105,8 @@ __device__ __forceinline__ void weights(State &st, float (&x)[N][4], float a, fl
         b[s][0] = transpose8(pack_half2(x[s][0], x[s][1]));
         b[s][1] = transpose8(pack_half2(x[s][2], x[s][3]));
     }
-    st.l[0] = fmaf(sum[0], inv, st.l[0]);
-    st.l[1] = fmaf(sum[1], inv, st.l[1]);
+    st.l[n][0] = fmaf(sum[0], inv, st.l[n][0]);
+    st.l[n][1] = fmaf(sum[1], inv, st.l[n][1]);
 }
 
 // A packed tile.  The order of the contracted dimension is free as long as both operands share
@@ -96,8 +114,8 @@ __device__ __forceinline__ void weights(State &st, float (&x)[N][4], float a, fl
 // neighbouring channels) is one step's operand; q is held in that order.  Values: a lane's 16 bytes
 // are 16 neighbouring tokens of a channel, word s those of step s: step s takes tokens 16 c + 4 s
 // .. + 3 of every c, and the score rows are arranged so.
-template <bool E4M3>
-__device__ __forceinline__ void key_tile(const uint32_t (&q)[8][2], const uint8_t *k, float (&x)[4][4], int lane) {
+template <bool E4M3, int NT>
+__device__ __forceinline__ void key_tile(const Queries<NT> &q, const uint8_t *k, float (&x)[NT][4][4], int lane) {
     const int r = lane >> 2, c = lane & 3;
 #pragma unroll
     for (int s = 0; s < 4; s++) {
@@ -109,18 +127,24 @@ __device__ __forceinline__ void key_tile(const uint32_t (&q)[8][2], const uint8_
         w[1][0] = *reinterpret_cast<const uint4 *>(row + 256 + near);
         w[1][1] = *reinterpret_cast<const uint4 *>(row + 256 + far);
 #pragma unroll
-        for (int e = 0; e < 4; e++) x[s][e] = 0.f;
+        for (int n = 0; n < NT; n++)
+#pragma unroll
+            for (int e = 0; e < 4; e++) x[n][s][e] = 0.f;
 #pragma unroll
         for (int i = 0; i < 8; i++) {
             uint32_t a[4];
             code_pairs<E4M3>((&w[0][i >> 2].x)[i & 3], a[0], a[2]);
             code_pairs<E4M3>((&w[1][i >> 2].x)[i & 3], a[1], a[3]);
-            mma_16816(x[s], a[0], a[1], a[2], a[3], q[i][0], q[i][1]);
+#pragma unroll
+            for (int n = 0; n < NT; n++) {
+                const uint2 y = q.get(i, n, lane);
+                mma_16816(x[n][s], a[0], a[1], a[2], a[3], y.x, y.y);
+            }
         }
     }
 }
-template <bool E4M3>
-__device__ __forceinline__ void value_tile(State &st, const uint8_t *v, const uint32_t (&b)[4][2], int lane) {
+template <bool E4M3, int NT>
+__device__ __forceinline__ void value_tile(State<NT> &st, const uint8_t *v, const uint32_t (&b)[NT][4][2], int lane) {
     const int r = lane >> 2, c = lane & 3;
 #pragma unroll
     for (int i = 0; i < 8; i++) {
@@ -131,70 +155,133 @@ __device__ __forceinline__ void value_tile(State &st, const uint8_t *v, const ui
             uint32_t a[4];
             code_pairs<E4M3>((&lo.x)[s], a[0], a[2]);
             code_pairs<E4M3>((&hi.x)[s], a[1], a[3]);
-            mma_16816(st.o[i], a[0], a[1], a[2], a[3], b[s][0], b[s][1]);
+#pragma unroll
+            for (int n = 0; n < NT; n++) mma_16816(st.o[n][i], a[0], a[1], a[2], a[3], b[n][s][0], b[n][s][1]);
         }
     }
 }
 
-// 16 fp16 tokens, n of which exist: rows r and r + 8 (k0, k1, v0, v1).  A value row's 8 channels
-// 32 j + 8 c .. of lane c are turned into operand rows by 8 x 8 transposes.
-__device__ __forceinline__ void tail_tile(State &st, const uint32_t (&q)[8][2], const uint16_t *k0, const uint16_t *k1,
-                                          const uint16_t *v0, const uint16_t *v1, int n, int lane) {
+// Infinite and NaN values of eight channels become 0 (a weight of 0 would make them NaN in rows
+// that may not see them); true if there are any.
+__device__ __forceinline__ bool drop_odd(uint4 &v) {
+    bool odd = false;
+#pragma unroll
+    for (int e = 0; e < 4; e++) {
+        uint32_t &x = (&v.x)[e];
+        if ((x & 0x7c00u) == 0x7c00u) x &= 0xffff0000u, odd = true;
+        if ((x & 0x7c000000u) == 0x7c000000u) x &= 0xffffu, odd = true;
+    }
+    return odd;
+}
+
+// 16 fp16 tokens from x0 on: rows r and r + 8 (k0, k1, v0, v1), seen by a row if below its lim.  A
+// value row's 8 channels 32 j + 8 c .. of lane c are turned into operand rows by 8 x 8 transposes.
+// True if a value was infinite or NaN.
+template <int NT>
+__device__ __forceinline__ bool tail_tile(State<NT> &st, const Queries<NT> &q, const uint16_t *k0, const uint16_t *k1,
+                                          const uint16_t *v0, const uint16_t *v1, int x0, int seen, const int (&lim)[NT][2], int lane) {
     const int r = lane >> 2, c = lane & 3;
-    const bool on0 = r < n, on1 = r + 8 < n;
+    const bool on0 = x0 + r < seen, on1 = x0 + r + 8 < seen;
     const uint4 zero = make_uint4(0, 0, 0, 0);
-    uint4 k[4][2], v[4][2];  // all loads before the first use
+    uint4 k[4][2], v[4][2];
 #pragma unroll
     for (int i = 0; i < 4; i++) {
         const int ch = (i >> 1) * 64 + c * 16 + (i & 1) * 8;
         k[i][0] = on0 ? *reinterpret_cast<const uint4 *>(k0 + ch) : zero;
         k[i][1] = on1 ? *reinterpret_cast<const uint4 *>(k1 + ch) : zero;
     }
+    auto load_values = [&] {
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
-        v[i][0] = on0 ? *reinterpret_cast<const uint4 *>(v0 + 32 * i + 8 * c) : zero;
-        v[i][1] = on1 ? *reinterpret_cast<const uint4 *>(v1 + 32 * i + 8 * c) : zero;
-    }
-    float x[1][4] = {{0.f, 0.f, 0.f, 0.f}};
+        for (int i = 0; i < 4; i++) {
+            v[i][0] = on0 ? *reinterpret_cast<const uint4 *>(v0 + 32 * i + 8 * c) : zero;
+            v[i][1] = on1 ? *reinterpret_cast<const uint4 *>(v1 + 32 * i + 8 * c) : zero;
+        }
+    };
+    if (NT < 4) load_values();  // before the first use of the keys, if there are registers for both
+    uint32_t b[NT][1][2];
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
-        mma_16816(x[0], k[i][0].x, k[i][1].x, k[i][0].y, k[i][1].y, q[2 * i][0], q[2 * i][1]);
-        mma_16816(x[0], k[i][0].z, k[i][1].z, k[i][0].w, k[i][1].w, q[2 * i + 1][0], q[2 * i + 1][1]);
+    for (int n = 0; n < NT; n++) {
+        float x[1][4] = {{0.f, 0.f, 0.f, 0.f}};
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            const uint2 y = q.get(2 * i, n, lane), z = q.get(2 * i + 1, n, lane);
+            mma_16816(x[0], k[i][0].x, k[i][1].x, k[i][0].y, k[i][1].y, y.x, y.y);
+            mma_16816(x[0], k[i][0].z, k[i][1].z, k[i][0].w, k[i][1].w, z.x, z.y);
+        }
+#pragma unroll
+        for (int e = 0; e < 2; e++) {
+            if (x0 + r >= lim[n][e]) x[0][e] = -INFINITY;
+            if (x0 + r + 8 >= lim[n][e]) x[0][2 + e] = -INFINITY;
+        }
+        weights<1, NT>(st, n, x, kScale, 0.f, 1.f, b[n]);
     }
-    if (!on0) x[0][0] = x[0][1] = -INFINITY;
-    if (!on1) x[0][2] = x[0][3] = -INFINITY;
-    uint32_t b[1][2];
-    weights<1>(st, x, kScale, 0.f, 1.f, b);
+    if (NT == 4) load_values();
+    bool odd = false;
 #pragma unroll
     for (int j = 0; j < 4; j++) {
-        mma_16816(st.o[2 * j], transpose8(v[j][0].x), transpose8(v[j][0].y), transpose8(v[j][1].x), transpose8(v[j][1].y), b[0][0], b[0][1]);
-        mma_16816(st.o[2 * j + 1], transpose8(v[j][0].z), transpose8(v[j][0].w), transpose8(v[j][1].z), transpose8(v[j][1].w), b[0][0],
-                  b[0][1]);
+        odd |= drop_odd(v[j][0]);
+        odd |= drop_odd(v[j][1]);
+        const uint32_t a[8] = {transpose8(v[j][0].x), transpose8(v[j][0].y), transpose8(v[j][1].x), transpose8(v[j][1].y),
+                               transpose8(v[j][0].z), transpose8(v[j][0].w), transpose8(v[j][1].z), transpose8(v[j][1].w)};
+#pragma unroll
+        for (int n = 0; n < NT; n++) {
+            mma_16816(st.o[n][2 * j], a[0], a[1], a[2], a[3], b[n][0][0], b[n][0][1]);
+            mma_16816(st.o[n][2 * j + 1], a[4], a[5], a[6], a[7], b[n][0][0], b[n][0][1]);
+        }
     }
+    return odd;
 }
 
-__device__ __forceinline__ float factor(float m, float top) { return m == top ? 1.f : ex2(m - top); }
+// Of a state below the largest reference: positive, so that an infinite value stays infinite
+// (2^-126 of a finite one is far below the other's smallest step).
+__device__ __forceinline__ float factor(float m, float top) { return m == top ? 1.f : fmaxf(ex2(m - top), 0x1p-126f); }
 
 struct Bars {
     uint64_t full[kWarps][kStages];
-    int stop;
+    int stop, odd;
 };
-constexpr int kSmemBytes = kWarps * kStages * kPiece + (int)sizeof(Bars);
-// the joined states lie in the rings
-static_assert(kWarps * (8 * 128 + 16) * 4 <= kWarps * kStages * kPiece, "shared memory");
+// the joined states lie in the rings: of a row tile at a time
+constexpr int kRingBytes = kWarps * kStages * kPiece, kStateBytes = kWarps * (8 * 128 + 16) * 4;
+static_assert(kStateBytes <= kRingBytes, "shared memory");
+template <int NT>
+constexpr int kSmemBytes = kRingBytes + (NT > 1 ? NT * 2048 : 0) + (int)sizeof(Bars);
 
-template <bool E4M3>
-__global__ void __launch_bounds__(kThreads, 3) block_decode_kernel(const __grid_constant__ BlockDecodeParams p) {
+// Lengths of a slot: {sink, packed, residual, new tokens (decode: 0)}, the row of its first query.
+struct Slot {
+    int ns, T, nr, n_new;
+    int64_t q0;
+    bool on;
+    __device__ __forceinline__ int seen() const { return ns + nr + n_new; }
+};
+__device__ __forceinline__ Slot slot_at(const BlockDecodeParams &p, int b) {
+    if (p.desc) {
+        const int4 x = reinterpret_cast<const int4 *>(p.desc)[2 * b];
+        return {x.x, x.y, x.z, x.w, p.desc[8 * b + 4], x.w > 0};
+    }
+    const int4 x = reinterpret_cast<const int4 *>(p.lens)[b];
+    return {x.x, x.y, x.z, 0, b, x.w && x.x + x.y + x.z > 0};
+}
+// Row x of a slot's [sink | residual | new tokens].
+__device__ __forceinline__ const uint16_t *tail_at(const BlockDecodeParams &p, const Slot &s, size_t u, int h, int x, bool value) {
+    if (x < s.ns) return (value ? p.v_sink : p.k_sink) + (u * p.S + x) * 128;
+    x -= s.ns;
+    if (x < s.nr) return (value ? p.v_res : p.k_res) + (u * p.R + x) * 128;
+    x -= s.nr;
+    return value ? p.v_new + (s.q0 + x) * p.v_stride + h * 128 : p.k_new + (s.q0 + x) * p.k_stride + h * 128;
+}
+
+template <bool E4M3, int NT>
+__global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) block_decode_kernel(const __grid_constant__ BlockDecodeParams p) {
     extern __shared__ __align__(128) unsigned char sm[];
-    Bars *bar = reinterpret_cast<Bars *>(sm + kWarps * kStages * kPiece);
+    uint2 *s_q = reinterpret_cast<uint2 *>(sm + kRingBytes);
+    Bars *bar = reinterpret_cast<Bars *>(sm + kSmemBytes<NT> - sizeof(Bars));
     const int h = blockIdx.x, w = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
     if (threadIdx.x == 0) {
         for (int i = 0; i < kWarps; i++)
             for (int j = 0; j < kStages; j++) mbar_init(&bar->full[i][j], 1);
-        bar->stop = 0;
+        bar->stop = bar->odd = 0;
         fence_barrier_init();
     }
-    __syncthreads();
     int lo = 0, hi = p.n_slots - 1;  // the slot
     while (lo < hi) {
         const int mid = (lo + hi) >> 1;
@@ -204,24 +291,49 @@ __global__ void __launch_bounds__(kThreads, 3) block_decode_kernel(const __grid_
     const int b = p.slot[lo], parts = p.part0[lo + 1] - p.part0[lo], part = blockIdx.y - p.part0[lo];
     const size_t u = (size_t)b * p.H_kv + h;
     griddep_wait();
-    const int4 ln = reinterpret_cast<const int4 *>(p.lens)[b];
-    uint32_t q[8][2];
+    const Slot sl = slot_at(p, b);
+    if (!sl.on) return;
+    const int rows = max(sl.n_new, 1) * p.g;
+    Queries<NT> q;
+    auto operand = [&](int n, uint2 (&x)[8]) {  // rows behind the last one are zeros
+        const int row = 8 * n + r;
+        const uint16_t *src = p.q + (sl.q0 + row / p.g) * p.q_stride + (h * p.g + row % p.g) * 128;
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
-        uint4 x = make_uint4(0, 0, 0, 0);
-        if (r < p.g) x = *reinterpret_cast<const uint4 *>(p.q + (u * p.g + r) * 128 + (i >> 1) * 64 + c * 16 + (i & 1) * 8);
-        q[2 * i][0] = x.x, q[2 * i][1] = x.y, q[2 * i + 1][0] = x.z, q[2 * i + 1][1] = x.w;
+        for (int i = 0; i < 4; i++) {
+            uint4 y = make_uint4(0, 0, 0, 0);
+            if (row < rows) y = *reinterpret_cast<const uint4 *>(src + (i >> 1) * 64 + c * 16 + (i & 1) * 8);
+            x[2 * i] = make_uint2(y.x, y.y);
+            x[2 * i + 1] = make_uint2(y.z, y.w);
+        }
+    };
+    if constexpr (NT == 1) {
+        operand(0, q.x);
+    } else {
+        q.sm = s_q;
+        if (w < NT) {
+            uint2 x[8];
+            operand(w, x);
+#pragma unroll
+            for (int i = 0; i < 8; i++) s_q[(i * NT + w) * 32 + lane] = x[i];
+        }
     }
-    if (!ln.w || ln.x + ln.y + ln.z == 0) return;
-    const int np = ln.y / kTokens, seen = ln.x + ln.z, n = np + (seen + kTailTokens - 1) / kTailTokens;
+    __syncthreads();
+    const int np = sl.T / kTokens, seen = sl.seen(), n = np + (seen + kTailTokens - 1) / kTailTokens;
     const int begin = (int)((int64_t)n * part / parts), end = (int)((int64_t)n * (part + 1) / parts);
-    State st;
+    int lim[NT][2];  // fp16 tokens that a row may see
+    State<NT> st;
 #pragma unroll
-    for (int e = 0; e < 2; e++) st.m[e] = -INFINITY, st.l[e] = 0.f;
+    for (int t = 0; t < NT; t++) {
 #pragma unroll
-    for (int i = 0; i < 8; i++)
+        for (int e = 0; e < 2; e++) {
+            st.m[t][e] = -INFINITY, st.l[t][e] = 0.f;
+            lim[t][e] = sl.n_new ? sl.ns + sl.nr + min(8 * t + 2 * c + e, rows - 1) / p.g + 1 : seen;
+        }
 #pragma unroll
-        for (int e = 0; e < 4; e++) st.o[i][e] = 0.f;
+        for (int i = 0; i < 8; i++)
+#pragma unroll
+            for (int e = 0; e < 4; e++) st.o[t][i][e] = 0.f;
+    }
 
     // Packed tiles begin + w, begin + w + kWarps, ...: their pieces, keys and values in turn, are
     // brought by bulk copies kStages ahead.  Lane j holds page and scales of tile j of 32.
@@ -255,83 +367,93 @@ __global__ void __launch_bounds__(kThreads, 3) block_decode_kernel(const __grid_
         for (int i = 0; i < min(kStages, 2 * m); i++) bring(i);
         // the warp's fp16 tiles, while the first pieces are on their way
         for (int i = t0 ? end : begin + w + (max(np - begin - w, 0) + kWarps - 1) / kWarps * kWarps; i < end; i += kWarps) {
-            const int x = (i - np) * kTailTokens;
-            auto at = [&](const uint16_t *sink, const uint16_t *res, int t) {
-                t = min(t, seen - 1);
-                return t < ln.x ? sink + (u * p.S + t) * 128 : res + (u * p.R + t - ln.x) * 128;
-            };
-            tail_tile(st, q, at(p.k_sink, p.k_res, x + r), at(p.k_sink, p.k_res, x + r + 8), at(p.v_sink, p.v_res, x + r),
-                      at(p.v_sink, p.v_res, x + r + 8), seen - x, lane);
+            const int x = (i - np) * kTailTokens, x0 = min(x + r, seen - 1), x1 = min(x + r + 8, seen - 1);
+            if (tail_tile<NT>(st, q, tail_at(p, sl, u, h, x0, false), tail_at(p, sl, u, h, x1, false), tail_at(p, sl, u, h, x0, true),
+                              tail_at(p, sl, u, h, x1, true), x, seen, lim, lane))
+                *(volatile int *)&bar->odd = 1;
         }
         for (int t = 0; t < m; t++) {
-            float x[4][4];
-            uint32_t bp[4][2];
+            float x[NT][4][4];
+            uint32_t bp[NT][4][2];
             const int i = 2 * t, k = 2 * t0 + i;  // pieces: of these tiles, of all
             warp_await(&full[k % kStages], (k / kStages) & 1, &bar->stop, p.status);
-            key_tile<E4M3>(q, ring + k % kStages * kPiece, x, lane);
+            key_tile<E4M3, NT>(q, ring + k % kStages * kPiece, x, lane);
             __syncwarp();
             if (i + kStages < 2 * m) bring(i + kStages);
-            const float tk = __shfl_sync(0xffffffffu, sk, t), tv = __shfl_sync(0xffffffffu, sv, t);
-            weights<4>(st, x, kScale * tk, log2f(tv), 1.f / tv, bp);
+            const float tk = kScale * __shfl_sync(0xffffffffu, sk, t), tv = __shfl_sync(0xffffffffu, sv, t), lsv = log2f(tv), inv = 1.f / tv;
+#pragma unroll
+            for (int y = 0; y < NT; y++) weights<4, NT>(st, y, x[y], tk, lsv, inv, bp[y]);
             warp_await(&full[(k + 1) % kStages], ((k + 1) / kStages) & 1, &bar->stop, p.status);
-            value_tile<E4M3>(st, ring + (k + 1) % kStages * kPiece, bp, lane);
+            value_tile<E4M3, NT>(st, ring + (k + 1) % kStages * kPiece, bp, lane);
             __syncwarp();
             if (i + 1 + kStages < 2 * m) bring(i + 1 + kStages);
         }
     }
-    __syncthreads();  // every piece has arrived and been read
+    // the warps' states, joined in warp order, a tile of 8 rows at a time
     float(*s_o)[8][128] = reinterpret_cast<float(*)[8][128]>(sm);
     float(*s_m)[8] = reinterpret_cast<float(*)[8]>(sm + kWarps * 8 * 128 * 4), (*s_l)[8] = s_m + kWarps;
-    // the warps' states, joined in warp order
 #pragma unroll
-    for (int e = 0; e < 2; e++) {
+    for (int t = 0; t < NT; t++) {
+        __syncthreads();  // every piece has arrived and been read; the rows before are written
+        if (8 * t >= rows) break;
 #pragma unroll
-        for (int o = 4; o < 32; o <<= 1) st.l[e] += __shfl_xor_sync(0xffffffffu, st.l[e], o);
-        if (r == 0) {
-            s_m[w][2 * c + e] = st.m[e];
-            s_l[w][2 * c + e] = st.l[e];
+        for (int e = 0; e < 2; e++) {
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) st.l[t][e] += __shfl_xor_sync(0xffffffffu, st.l[t][e], o);
+            if (r == 0) {
+                s_m[w][2 * c + e] = st.m[t][e];
+                s_l[w][2 * c + e] = st.l[t][e];
+            }
+#pragma unroll
+            for (int i = 0; i < 8; i++) {
+                s_o[w][2 * c + e][out_channel(i, r, 0)] = st.o[t][i][e];
+                s_o[w][2 * c + e][out_channel(i, r, 1)] = st.o[t][i][2 + e];
+            }
         }
+        __syncthreads();
+        const int d = threadIdx.x, odd = *(volatile int *)&bar->odd;
+        for (int e = 0; e < min(8, rows - 8 * t); e++) {
+            const int y = 8 * t + e;
+            float m = s_m[0][e], l = 0.f, o = 0.f;
 #pragma unroll
-        for (int i = 0; i < 8; i++) {
-            s_o[w][2 * c + e][out_channel(i, r, 0)] = st.o[i][e];
-            s_o[w][2 * c + e][out_channel(i, r, 1)] = st.o[i][2 + e];
-        }
-    }
-    __syncthreads();
-    const int d = threadIdx.x;
-    for (int e = 0; e < p.g; e++) {
-        float m = s_m[0][e], l = 0.f, o = 0.f;
+            for (int i = 1; i < kWarps; i++) m = fmaxf(m, s_m[i][e]);
 #pragma unroll
-        for (int i = 1; i < kWarps; i++) m = fmaxf(m, s_m[i][e]);
-#pragma unroll
-        for (int i = 0; i < kWarps; i++) {
-            const float f = factor(s_m[i][e], m);
-            l = fmaf(f, s_l[i][e], l);
-            o = fmaf(f, s_o[i][e][d], o);
-        }
-        if (parts == 1) {
-            p.out[(u * p.g + e) * 128 + d] = __half_as_ushort(__float2half_rn(o / l));
-        } else {
-            const size_t at = ((size_t)blockIdx.y * p.H_kv + h) * p.g + e;
-            p.part_o[at * 128 + d] = o;
-            if (d == 0) p.part_ml[at] = make_float2(m, l);
+            for (int i = 0; i < kWarps; i++) {
+                const float f = factor(s_m[i][e], m);
+                l = fmaf(f, s_l[i][e], l);
+                o = fmaf(f, s_o[i][e][d], o);
+            }
+            if (odd) {  // infinite and NaN values of the part's fp16 tokens
+                const int to = min(sl.n_new ? sl.ns + sl.nr + y / p.g + 1 : seen, (end - np) * kTailTokens);
+                for (int x = max(begin - np, 0) * kTailTokens; x < to; x++) {
+                    const float f = h2f(tail_at(p, sl, u, h, x, true)[d]);
+                    if (!isfinite(f)) o += f;
+                }
+            }
+            if (parts == 1) {
+                p.out[((sl.q0 + y / p.g) * p.H_kv * p.g + h * p.g + y % p.g) * 128 + d] = __half_as_ushort(__float2half_rn(o / l));
+            } else {
+                const size_t at = ((size_t)blockIdx.y * p.H_kv + h) * p.most_rows + y;
+                p.part_o[at * 128 + d] = o;
+                if (d == 0) p.part_ml[at] = make_float2(m, l);
+            }
         }
     }
 }
 
-// Slots in several parts: a CTA per (query head of a key head, key head, slot), its eight warps
-// every eighth part each, four at a time; then the warps' states in warp order.
+// Slots in several parts: a CTA per (row of a key head, key head, slot), its eight warps every
+// eighth part each, four at a time; then the warps' states in warp order.
 constexpr int kJoinWarps = 8;
 __global__ void __launch_bounds__(32 * kJoinWarps) block_combine_kernel(const __grid_constant__ BlockDecodeParams p) {
     __shared__ float4 s_o[kJoinWarps][32];
     __shared__ float2 s_ml[kJoinWarps];
-    const int e = blockIdx.x % p.g, h = blockIdx.x / p.g, at_slot = blockIdx.y, w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int y = blockIdx.x % p.most_rows, h = blockIdx.x / p.most_rows, at_slot = blockIdx.y, w = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int first = p.part0[at_slot], parts = p.part0[at_slot + 1] - first, b = p.slot[at_slot];
     if (parts < 2) return;
     griddep_wait();
-    const int4 ln = reinterpret_cast<const int4 *>(p.lens)[b];
-    if (!ln.w || ln.x + ln.y + ln.z == 0) return;
-    const size_t step = (size_t)p.H_kv * p.g, at = ((size_t)first * p.H_kv + h) * p.g + e;
+    const Slot sl = slot_at(p, b);
+    if (!sl.on || y >= max(sl.n_new, 1) * p.g) return;
+    const size_t step = (size_t)p.H_kv * p.most_rows, at = ((size_t)first * p.H_kv + h) * p.most_rows + y;
     float m = -INFINITY, l = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     auto join = [&](const float2 &ml, const float4 &x) {
@@ -348,9 +470,9 @@ __global__ void __launch_bounds__(32 * kJoinWarps) block_combine_kernel(const __
         float4 x[4];
 #pragma unroll
         for (int k = 0; k < 4; k++) {
-            const size_t y = at + min(i0 + k * kJoinWarps, parts - 1) * step;
-            ml[k] = p.part_ml[y];
-            x[k] = reinterpret_cast<const float4 *>(p.part_o + y * 128)[lane];
+            const size_t z = at + min(i0 + k * kJoinWarps, parts - 1) * step;
+            ml[k] = p.part_ml[z];
+            x[k] = reinterpret_cast<const float4 *>(p.part_o + z * 128)[lane];
         }
 #pragma unroll
         for (int k = 0; k < 4; k++)
@@ -362,75 +484,38 @@ __global__ void __launch_bounds__(32 * kJoinWarps) block_combine_kernel(const __
     if (w) return;
     for (int i = 1; i < min(kJoinWarps, parts); i++) join(s_ml[i], s_o[i][lane]);
     const float inv = 1.f / l;
-    uint16_t *dst = p.out + (((size_t)b * p.H_kv + h) * p.g + e) * 128;
+    uint16_t *dst = p.out + ((sl.q0 + y / p.g) * p.H_kv * p.g + h * p.g + y % p.g) * 128;
     reinterpret_cast<uint2 *>(dst)[lane] = make_uint2(pack_half2(o.x * inv, o.y * inv), pack_half2(o.z * inv, o.w * inv));
 }
 
-template <bool E4M3>
+template <bool E4M3, int NT>
 cudaError_t launch(dim3 grid, const BlockDecodeParams &p, cudaStream_t st) {
     static bool ready[64];  // per device
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64 || !ready[dev]) {
-        e = cudaFuncSetAttribute(block_decode_kernel<E4M3>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+        e = cudaFuncSetAttribute(block_decode_kernel<E4M3, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes<NT>);
         if (e != cudaSuccess) return e;
         if (dev >= 0 && dev < 64) ready[dev] = true;
     }
-    return launch_dependent(block_decode_kernel<E4M3>, grid, kThreads, kSmemBytes, st, p);
+    return launch_dependent(block_decode_kernel<E4M3, NT>, grid, kThreads, kSmemBytes<NT>, st, p);
 }
 
-// CTAs that run at once, and the most parts of a call: each of them and one more per slot.
-int resident() { return 3 * host::num_sms(); }
-int64_t most_parts(const kvq_config *c) { return host::cdiv(resident(), c->H_kv) + c->B; }
+// CTAs that run at once; parts of the slots that are cut (none where there are as many slots as
+// that).
+int resident(int tiles) { return (tiles == 1 ? 3 : 2) * host::num_sms(); }
+int64_t most_parts(const kvq_config *c) { return host::cdiv(resident(1), c->H_kv); }
 
-size_t ml_bytes(const kvq_config *c) { return (size_t)host::cdiv(most_parts(c) * c->H_q * 8, 256) * 256; }
-
-}  // namespace
-
-size_t block_decode_ws_bytes(const kvq_config *c) { return 256 + ml_bytes(c) + (size_t)most_parts(c) * c->H_q * 128 * 4; }
-
-int block_decode(const kvq_config *c, const kvq_paged *pc, const uint16_t *q, uint16_t *out, void *ws, size_t ws_bytes,
-                 cudaStream_t st) {
-    if (!ws || !host::aligned16(ws) || ws_bytes < block_decode_ws_bytes(c)) return KVQ_ERR_WORKSPACE;
-    BlockDecodeParams p;
-    memset(&p, 0, sizeof(p));
-    char *w = static_cast<char *>(ws);
-    p.status = reinterpret_cast<int32_t *>(w);
-    p.part_ml = reinterpret_cast<float2 *>(w + 256);
-    p.part_o = reinterpret_cast<float *>(w + 256 + ml_bytes(c));
-    p.q = q;
-    p.out = out;
-    p.k_codes = reinterpret_cast<const uint8_t *>(pc->k_codes);
-    p.v_codes = reinterpret_cast<const uint8_t *>(pc->v_codes);
-    p.k_scale = reinterpret_cast<const float4 *>(pc->k_meta);
-    p.v_scale = reinterpret_cast<const float4 *>(pc->v_meta);
-    p.k_sink = pc->k_sink;
-    p.v_sink = pc->v_sink;
-    p.k_res = pc->k_res;
-    p.v_res = pc->v_res;
-    p.ptab = pc->page_table;
-    p.lens = pc->lens;
-    p.n_pages = pc->n_pages;
-    p.B = c->B;
-    p.H_kv = c->H_kv;
-    p.g = c->H_q / c->H_kv;
-    p.g_shift = c->G == 64 ? 6 : c->G == 128 ? 7 : 8;
-    p.S = c->S;
-    p.R = c->R;
-    p.ptab_stride = (int)(c->max_T / c->G);
-    // items of the slots; slots of more items first (64 classes), so that what runs last is short
-    int items[KVQ_PAGED_MAX_B], count[64] = {0}, longest = 0, active = 0;
-    int64_t total = 0;
+// Cuts the slots (items each, 0: not part of the call) into parts and launches.
+cudaError_t run(const kvq_config *c, const int *items, BlockDecodeParams &p, cudaStream_t st) {
+    const int tiles = p.most_rows <= 8 ? 1 : p.most_rows <= 16 ? 2 : 4;
+    int count[64] = {0}, longest = 0, active = 0;
     for (int b = 0; b < c->B; b++) {
-        const int32_t *l = pc->lens_host + 4 * b;
-        items[b] = l[3] ? l[1] / kTokens + (l[0] + l[2] + kTailTokens - 1) / kTailTokens : 0;
-        if (l[3] && l[1] && pc->n_pages < 1) return KVQ_ERR_INVALID_ARG;  // page 0 stands in for bad entries
         longest = std::max(longest, items[b]);
         active += items[b] > 0;
-        total += items[b];
     }
-    if (!active) return KVQ_OK;
+    // slots of more items first (64 classes), so that what runs last is short
     auto size_class = [&](int n) { return 63 - (int)((int64_t)n * 63 / longest); };
     for (int b = 0; b < c->B; b++)
         if (items[b]) count[size_class(items[b])]++;
@@ -442,12 +527,12 @@ int block_decode(const kvq_config *c, const kvq_paged *pc, const uint16_t *q, ui
     for (int b = 0; b < c->B; b++)
         if (items[b]) p.slot[count[size_class(items[b])]++] = (int16_t)b;
     // parts of at most X items, the smallest X whose parts are all resident at once
-    const int64_t room = std::max<int64_t>(active, host::cdiv(resident(), c->H_kv));
+    const int64_t room = std::max<int64_t>(active, host::cdiv(resident(tiles), c->H_kv));
     int lo = std::min(longest, kLeast), hi = longest;
     while (lo < hi) {
         const int X = (lo + hi) / 2;
         int64_t parts = 0;
-        for (int b = 0; b < c->B; b++) parts += (items[b] + X - 1) / X;
+        for (int i = 0; i < active; i++) parts += (items[p.slot[i]] + X - 1) / X;
         if (parts <= room) hi = X;
         else lo = X + 1;
     }
@@ -462,9 +547,91 @@ int block_decode(const kvq_config *c, const kvq_paged *pc, const uint16_t *q, ui
     p.n_slots = active;
     p.part0[active] = parts;
     const dim3 grid((unsigned)c->H_kv, (unsigned)parts);
-    cudaError_t e = c->mode == KVQ_MODE_E4M3 ? launch<true>(grid, p, st) : launch<false>(grid, p, st);
-    if (e == cudaSuccess && cut) e = launch_dependent(block_combine_kernel, dim3((unsigned)c->H_q, (unsigned)active), 32 * kJoinWarps, 0, st, p);
-    return host::status_of(e);
+    auto go = [&](auto form) {
+        constexpr bool F = decltype(form)::value;
+        return tiles == 1 ? launch<F, 1>(grid, p, st) : tiles == 2 ? launch<F, 2>(grid, p, st) : launch<F, 4>(grid, p, st);
+    };
+    const cudaError_t e = c->mode == KVQ_MODE_E4M3 ? go(std::true_type()) : go(std::false_type());
+    if (e != cudaSuccess || !cut) return e;
+    return launch_dependent(block_combine_kernel, dim3((unsigned)(p.most_rows * c->H_kv), (unsigned)active), 32 * kJoinWarps, 0, st, p);
+}
+
+// What both calls read of the cache.
+void fill(const kvq_config *c, const kvq_paged *pc, BlockDecodeParams &p) {
+    memset(&p, 0, sizeof(p));
+    p.k_codes = reinterpret_cast<const uint8_t *>(pc->k_codes);
+    p.v_codes = reinterpret_cast<const uint8_t *>(pc->v_codes);
+    p.k_scale = reinterpret_cast<const float4 *>(pc->k_meta);
+    p.v_scale = reinterpret_cast<const float4 *>(pc->v_meta);
+    p.k_sink = pc->k_sink;
+    p.v_sink = pc->v_sink;
+    p.k_res = pc->k_res;
+    p.v_res = pc->v_res;
+    p.ptab = pc->page_table;
+    p.n_pages = pc->n_pages;
+    p.H_kv = c->H_kv;
+    p.g = c->H_q / c->H_kv;
+    p.g_shift = c->G == 64 ? 6 : c->G == 128 ? 7 : 8;
+    p.S = c->S;
+    p.R = c->R;
+    p.ptab_stride = (int)(c->max_T / c->G);
+}
+
+int items_of(int ns, int T, int nr, int n_new) { return T / kTokens + (ns + nr + n_new + kTailTokens - 1) / kTailTokens; }
+
+size_t ml_bytes(const kvq_config *c) { return (size_t)host::cdiv(most_parts(c) * c->H_q * 8, 256) * 256; }
+
+}  // namespace
+
+size_t block_decode_ws_bytes(const kvq_config *c) { return 256 + ml_bytes(c) + (size_t)most_parts(c) * c->H_q * 128 * 4; }
+
+int block_decode(const kvq_config *c, const kvq_paged *pc, const uint16_t *q, uint16_t *out, void *ws, size_t ws_bytes,
+                 cudaStream_t st) {
+    if (!ws || !host::aligned16(ws) || ws_bytes < block_decode_ws_bytes(c)) return KVQ_ERR_WORKSPACE;
+    BlockDecodeParams p;
+    fill(c, pc, p);
+    char *w = static_cast<char *>(ws);
+    p.status = reinterpret_cast<int32_t *>(w);
+    p.part_ml = reinterpret_cast<float2 *>(w + 256);
+    p.part_o = reinterpret_cast<float *>(w + 256 + ml_bytes(c));
+    p.q = q;
+    p.q_stride = (int64_t)c->H_q * c->D;
+    p.out = out;
+    p.lens = pc->lens;
+    p.most_rows = p.g;
+    int items[KVQ_PAGED_MAX_B];
+    bool any = false;
+    for (int b = 0; b < c->B; b++) {
+        const int32_t *l = pc->lens_host + 4 * b;
+        items[b] = l[3] ? items_of(l[0], l[1], l[2], 0) : 0;
+        if (l[3] && l[1] && pc->n_pages < 1) return KVQ_ERR_INVALID_ARG;  // page 0 stands in for bad entries
+        any |= items[b] > 0;
+    }
+    return any ? host::status_of(run(c, items, p, st)) : KVQ_OK;
+}
+
+int block_chunk_few(const kvq_config *c, const kvq_paged *pc, const ChunkSlot *slots, const bool *few, const ChunkAttnParams &a,
+                    cudaStream_t st) {
+    BlockDecodeParams p;
+    fill(c, pc, p);
+    p.desc = a.desc;
+    p.status = a.status;
+    p.part_ml = a.part_ml;
+    p.part_o = a.part_o;
+    p.q = a.q;
+    p.k_new = a.k_new;
+    p.v_new = a.v_new;
+    p.q_stride = a.q_stride;
+    p.k_stride = a.k_stride;
+    p.v_stride = a.v_stride;
+    p.out = a.out;
+    int items[KVQ_PAGED_MAX_B];
+    for (int b = 0; b < c->B; b++) {
+        const ChunkSlot &s = slots[b];
+        items[b] = few[b] ? items_of(s.ns, s.T, s.nr, s.n_new) : 0;
+        if (few[b]) p.most_rows = std::max(p.most_rows, s.n_new * p.g);
+    }
+    return host::status_of(run(c, items, p, st));
 }
 
 }  // namespace kvq

@@ -599,9 +599,31 @@ int kvq_paged_chunk_attn(const kvq_config *c, const kvq_paged *pc, kvq_chunk *ch
     p.S = c->S;
     p.R = c->R;
     p.ptab_stride = (int)(c->max_T / c->G);
+    // over 8-bit codes, slots of few rows have a kernel of their own, if all are such slots, or if it
+    // gains more than its launches cost
+    bool few[KVQ_PAGED_MAX_B], any_few = false, all_few = block8(c);
+    ChunkSlot rest[KVQ_PAGED_MAX_B];
+    const ChunkSlot *slots = slots_of(ch);
+    if (block8(c)) {
+        int64_t tiles = 0;
+        for (int b = 0; b < c->B; b++) {
+            const ChunkSlot &s = slots[b];
+            if (s.n_new && s.T && pc->n_pages < 1) return KVQ_ERR_INVALID_ARG;
+            few[b] = s.n_new && (int64_t)s.n_new * p.g <= kFewRows;
+            any_few |= few[b];
+            all_few &= few[b] || !s.n_new;
+            if (few[b]) tiles += (int64_t)p.H_kv * (s.T / kChunkKeys);
+        }
+        any_few &= all_few || tiles >= kFewTiles;
+        for (int b = 0; any_few && b < c->B; b++) {
+            rest[b] = slots[b];
+            if (few[b]) rest[b].n_new = 0;
+        }
+        if (any_few) slots = rest;
+    }
     int64_t cost = 0, items = 0, units = 0;
     for (int b = 0; b < c->B; b++) {
-        const ChunkSlot &s = slots_of(ch)[b];
+        const ChunkSlot &s = slots[b];
         p.cost0[b] = (int32_t)cost;
         const bool narrow = chunk_narrow(s.n_new, p.g);
         const int rows = narrow ? kNarrowRows : kWideRows;
@@ -621,9 +643,10 @@ int kvq_paged_chunk_attn(const kvq_config *c, const kvq_paged *pc, kvq_chunk *ch
     for (int b = c->B; b <= KVQ_PAGED_MAX_B; b++) p.cost0[b] = (int32_t)cost;
     p.cost = (int)cost;
     p.C = (int)std::min<int64_t>(items, std::min(num_sms(), kMaxRanges));
-    if (!unit_ranges(c, slots_of(ch), units, p)) even_ranges(c, slots_of(ch), p);
+    if (any_few && (e = block_chunk_few(c, pc, slots_of(ch), few, p, (cudaStream_t)stream))) return e;
+    if (!all_few && !unit_ranges(c, slots, units, p)) even_ranges(c, slots, p);
     p.ref_unit = block8(c) ? 1.f : kScale;
-    if ((block8(c) ? launch_chunk_attn_block(p, c->mode == KVQ_MODE_E4M3, (cudaStream_t)stream)
+    if (!all_few && (block8(c) ? launch_chunk_attn_block(p, c->mode == KVQ_MODE_E4M3, (cudaStream_t)stream)
                    : launch_chunk_attn(p, (cudaStream_t)stream)) != cudaSuccess)
         return KVQ_ERR_CUDA;
     if (!ch->captured && capturing((cudaStream_t)stream)) ch->captured = 1;

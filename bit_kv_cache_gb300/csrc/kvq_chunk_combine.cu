@@ -50,7 +50,7 @@ __device__ __forceinline__ void combine_narrow(const ChunkAttnParams &p, int h, 
     const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
     Item it = make_item(p, b);
     const int valid = it.s.n_new * p.g;
-    if (valid == 0 || it.rows != kNarrowRows || z >= valid) return;
+    if (valid == 0 || it.rows != kNarrowRows || z >= valid || p.cost0[b + 1] == p.cost0[b]) return;  // (no units: another kernel's)
     it.h = h;
     it.t = 0;
     it.n = chunk_tiles(it.s, 0, it.rows, p.g);

@@ -97,21 +97,29 @@ def cached_rows(c, b):
 
 
 def softmax_rows(q, K, V, hid=None):
-    """Rows q [n][D] over K, V [L][D] in float64: (outputs, sum of p |v|, largest |q| . |k| / sqrt D)."""
+    """Rows q [n][D] over K, V [L][D] in float64: (outputs, their size for bound_of, largest
+    |q| . |k| / sqrt D)."""
     s = q @ K.T / math.sqrt(D)
     mag = np.abs(q) @ np.abs(K).T / math.sqrt(D)
     if hid is not None:
         s, mag = np.where(hid, -np.inf, s), np.where(hid, 0.0, mag)
     p = np.exp(s - s.max(1, keepdims=True))
     p /= p.sum(1, keepdims=True)
-    return p @ V, p @ np.abs(V), mag.max(1, keepdims=True)
+    return p @ V, p @ np.abs(V) + TINY * len(V) * np.abs(V).max(), mag.max(1, keepdims=True)
+
+
+# Weights below fp16's normal numbers are off by half its smallest step, 2^-25, where the largest
+# weight of the row is 2^6 at least.  A weight counts the value scale s in: w = 2^x p s, with
+# sum w / s >= 2^6 / s_top for the token of the largest weight, so an output is off by
+#   2^-25 sum |code_t| / (2^6 / s_top) <= 2^-31 L (M s_top) <= 2^-31 L max |v|
+# (fp16 tokens: s = 1 and |v| in place of the code, the same).  In units of U16:
+TINY = 2.0 ** -31 / U16
 
 
 def bound_of(ref, size, mag):
     """What rounding may do to an element: operands are exact; a weight is rounded to fp16 once
-    (U16 of its product, and half of fp16's smallest step, 2^-25, below the largest weight, 2^6 at
-    least), the output once; scores are fp32 sums of 128 products (2^-24 of the magnitudes each, an
-    error of the exponent, twice in numerator and denominator), the exponential and the fp32 sums
-    over tiles add 2^-19."""
+    (U16 of its product; TINY is in the size), the output once; scores are fp32 sums of 128
+    products (2^-24 of the magnitudes each, an error of the exponent, twice in numerator and
+    denominator), the exponential and the fp32 sums over tiles add 2^-19."""
     ds = mag * 128 * 2.0 ** -24 + 2.0 ** -20
     return size * (2 * ds + 1.1 * U16 + 2.0 ** -19) + U16 * np.abs(ref) + 2.0 ** -24

@@ -91,6 +91,49 @@ def test_chunk_attention(name, mode):
 
 
 @pytest.mark.parametrize("mode", MODES)
+@pytest.mark.parametrize("H_q, new", [(4, [1, 0, 1]), (4, [2, 1, 2]), (4, [4, 0, 3]), (4, [8, 8, 5]), (3, [10, 1, 4]), (8, [4, 1, 3]), (8, [5, 4, 40]),
+                                      (5, [6, 100, 1]), (1, [32, 33, 7])], ids=str)
+def test_few_rows(H_q, new, mode):
+    """Slots of up to 32 rows a key head, alone and beside slots of more, whole and cut into
+    parts; infinite and NaN values of new, cached and sink tokens."""
+    rng = np.random.default_rng(sum(new))
+    c = make_cache(rng, [3000, 200, 0], mode, H_q=H_q, H_kv=1, S=3)
+    q, k, v = chunk_inputs(rng, c, sum(new))
+    attn_check(c, new, q, k, v, c.chunk_attn(c.plan(new), q, k, v))
+    v[new[0] - 1, 0, 5] = float("inf")
+    v[sum(new) - 1, 0, 7] = -float("inf")
+    v[0, 0, 9] = float("nan")
+    c.view("v_sink")[0, 0, 1, 3] = float("inf")
+    c.view("v_res")[1, 0, 2, 4] = -float("inf")
+    ch = c.plan(new)
+    out = c.chunk_attn(ch, q, k, v)
+    attn_check(c, new, q, k, v, out)
+    assert torch.equal(out.view(torch.int16), c.chunk_attn(ch, q, k, v).view(torch.int16))
+    assert c.read_status() == 0
+
+
+@pytest.mark.parametrize("mode", MODES)
+def test_decode_infinite_values(mode):
+    """Infinite and NaN values in the sink and the residual, of a slot in several parts too."""
+    rng = np.random.default_rng(14)
+    c = make_cache(rng, [5000, 90], mode, S=2, H_kv=1, H_q=4, max_T=8192)
+    c.view("v_sink")[0, 0, 1, 3] = float("inf")
+    c.view("v_res")[1, 0, 2, 4] = float("nan")
+    c.view("v_res")[0, 0, 3, 6] = -float("inf")
+    q = randn(rng, 2, 4, D)
+    out = c.decode_attn(q).cpu().double().numpy()
+    for b in range(2):
+        K, V = cached_rows(c, b)
+        Vf = np.where(np.isfinite(V[0]), V[0], 0.0)
+        ref, size, mag = softmax_rows(q[b].cpu().double().numpy(), K[0], Vf)
+        bound = bound_of(ref, size, mag)
+        ref = ref + np.where(np.isfinite(V[0]), 0.0, V[0]).sum(0)
+        fin = np.isfinite(ref)
+        assert np.array_equal(np.isnan(out[b]), np.isnan(ref)) and np.array_equal(out[b][~fin & ~np.isnan(ref)], ref[~fin & ~np.isnan(ref)])
+        assert (~fin).sum() == (8 if b == 0 else 4) and np.all(np.abs(out[b] - ref)[fin] <= bound[fin])
+
+
+@pytest.mark.parametrize("mode", MODES)
 def test_chunk_attention_long_split(mode):
     """One short chunk over a long cache: its key tiles are spread over many ranges."""
     rng = np.random.default_rng(3)
