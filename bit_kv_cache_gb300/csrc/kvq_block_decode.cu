@@ -290,6 +290,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) block_decode_kernel
     }
     const int b = p.slot[lo], parts = p.part0[lo + 1] - p.part0[lo], part = blockIdx.y - p.part0[lo];
     const size_t u = (size_t)b * p.H_kv + h;
+    const int32_t *row = p.ptab + (size_t)b * p.ptab_stride;
     griddep_wait();
     const Slot sl = slot_at(p, b);
     if (!sl.on) return;
@@ -340,7 +341,6 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) block_decode_kernel
     const int tiles = begin + w < min(end, np) ? (min(end, np) - begin - w + kWarps - 1) / kWarps : 0;
     unsigned char *ring = sm + w * kStages * kPiece;
     uint64_t *full = bar->full[w];
-    const int32_t *row = p.ptab + (size_t)b * p.ptab_stride;
     for (int t0 = 0; t0 == 0 || t0 < tiles; t0 += 32) {
         const int m = min(32, tiles - t0);
         size_t at = 0;
@@ -411,9 +411,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) block_decode_kernel
             }
         }
         __syncthreads();
-        const int d = threadIdx.x, odd = *(volatile int *)&bar->odd;
-        for (int e = 0; e < min(8, rows - 8 * t); e++) {
-            const int y = 8 * t + e;
+        const int odd = *(volatile int *)&bar->odd;
+        for (int i = threadIdx.x; i < 128 * min(8, rows - 8 * t); i += kThreads) {
+            const int e = i >> 7, d = i & 127, y = 8 * t + e;
             float m = s_m[0][e], l = 0.f, o = 0.f;
 #pragma unroll
             for (int i = 1; i < kWarps; i++) m = fmaxf(m, s_m[i][e]);
@@ -536,12 +536,11 @@ cudaError_t run(const kvq_config *c, const int *items, BlockDecodeParams &p, cud
         if (parts <= room) hi = X;
         else lo = X + 1;
     }
-    bool cut = false;
-    int parts = 0;
+    int parts = 0, cut = 0;  // cut: the slots before it are in several parts
     for (int i = 0; i < active; i++) {
         p.part0[i] = parts;
         const int n = (items[p.slot[i]] + lo - 1) / lo;
-        cut |= n > 1;
+        if (n > 1) cut = i + 1;
         parts += n;
     }
     p.n_slots = active;
@@ -553,7 +552,7 @@ cudaError_t run(const kvq_config *c, const int *items, BlockDecodeParams &p, cud
     };
     const cudaError_t e = c->mode == KVQ_MODE_E4M3 ? go(std::true_type()) : go(std::false_type());
     if (e != cudaSuccess || !cut) return e;
-    return launch_dependent(block_combine_kernel, dim3((unsigned)(p.most_rows * c->H_kv), (unsigned)active), 32 * kJoinWarps, 0, st, p);
+    return launch_dependent(block_combine_kernel, dim3((unsigned)(p.most_rows * c->H_kv), (unsigned)cut), 32 * kJoinWarps, 0, st, p);
 }
 
 // What both calls read of the cache.
