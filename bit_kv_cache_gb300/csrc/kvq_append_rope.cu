@@ -4,9 +4,9 @@
 // One launch does what kvq_paged_flush, kvq_qk_norm_rope and kvq_paged_append do.  The CTAs of a
 // page come first: each packs one side of a page of a full residual; the one that holds the
 // residual's first row then writes the new token's row there, which no other CTA reads.  Behind
-// them come the slots' own CTAs, with 16 heads a pass: 16 lanes hold a head's row, both channels of
-// a pair in one thread, so that a row needs one reduction and no exchange; sines and cosines are
-// formed once per CTA.  Positions and destinations come as a parameter, from the host's lengths:
+// them come the slots' own CTAs, with 16 heads each: 16 lanes hold a head's row, both channels of a
+// pair in one thread, so that a row needs one reduction and no exchange; sines and cosines are
+// formed once per CTA, while the rows arrive.  Positions and destinations come as a parameter, from the host's lengths:
 // no CTA reads the lengths that another one advances.
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -61,80 +61,89 @@ __device__ __forceinline__ void angles(const AppendRopeParams &p, int64_t pos, f
 // One head's row by 16 lanes (all lanes of the warp call): norm, if there are weights w, and
 // rotation, if turn; the arithmetic of kvq_qk_norm_rope, bit for bit.  Lane l has two pieces of
 // four channels: of halves a piece of the first half and its partners, else neighbours.
-__device__ __forceinline__ void head_row(const AppendRopeParams &p, const uint16_t *src, const uint16_t *w, bool rotate, uint16_t *dst,
-                                         const float2 *cs) {
-    const int l = threadIdx.x & 15, half = p.rotary >> 1;
-    const bool split = p.halves && 4 * l < half;
-    const int c0 = split ? 4 * l : 8 * l, c1 = split ? c0 + half : c0 + 4;
-    uint2 v[2] = {make_uint2(0, 0), make_uint2(0, 0)};
-    if (src) {
-        v[0] = *reinterpret_cast<const uint2 *>(src + c0);
-        v[1] = *reinterpret_cast<const uint2 *>(src + c1);
-    }
-    auto pairs = [&](const uint2 (&r)[2], float (&x)[4], float (&y)[4]) {
-        const float2 f0 = unpack_half2(r[0].x), f1 = unpack_half2(r[0].y), f2 = unpack_half2(r[1].x), f3 = unpack_half2(r[1].y);
-        if (p.halves) {
-            x[0] = f0.x, x[1] = f0.y, x[2] = f1.x, x[3] = f1.y;
-            y[0] = f2.x, y[1] = f2.y, y[2] = f3.x, y[3] = f3.y;
-        } else {
-            x[0] = f0.x, x[1] = f1.x, x[2] = f2.x, x[3] = f3.x;
-            y[0] = f0.y, y[1] = f1.y, y[2] = f2.y, y[3] = f3.y;
+struct HeadRow {
+    uint2 v[2], w[2];
+    int c0, c1;
+    bool split;
+    __device__ __forceinline__ HeadRow(const AppendRopeParams &p, const uint16_t *src, const uint16_t *wt) {
+        const int l = threadIdx.x & 15, half = p.rotary >> 1;
+        split = p.halves && 4 * l < half;
+        c0 = split ? 4 * l : 8 * l, c1 = split ? c0 + half : c0 + 4;
+        v[0] = v[1] = make_uint2(0, 0);
+        w[0] = w[1] = make_uint2(0x3c003c00u, 0x3c003c00u);
+        if (src) {
+            v[0] = *reinterpret_cast<const uint2 *>(src + c0);
+            v[1] = *reinterpret_cast<const uint2 *>(src + c1);
         }
-    };
-    float x[4], y[4], w0[4] = {1.f, 1.f, 1.f, 1.f}, w1[4] = {1.f, 1.f, 1.f, 1.f};
-    pairs(v, x, y);
-    if (w) {
-        const uint2 u[2] = {__ldg(reinterpret_cast<const uint2 *>(w + c0)), __ldg(reinterpret_cast<const uint2 *>(w + c1))};
-        pairs(u, w0, w1);
+        if (wt) {
+            w[0] = __ldg(reinterpret_cast<const uint2 *>(wt + c0));
+            w[1] = __ldg(reinterpret_cast<const uint2 *>(wt + c1));
+        }
     }
-    const float a = fmaf(x[0], x[0], fmaf(x[2], x[2], fmaf(y[0], y[0], y[2] * y[2])));
-    const float b = fmaf(x[1], x[1], fmaf(x[3], x[3], fmaf(y[1], y[1], y[3] * y[3])));
-    float ss = a + b;
+    __device__ __forceinline__ void store(const AppendRopeParams &p, bool norm, bool rotate, uint16_t *dst, const float2 *cs) const {
+        auto pairs = [&](const uint2 (&r)[2], float (&x)[4], float (&y)[4]) {
+            const float2 f0 = unpack_half2(r[0].x), f1 = unpack_half2(r[0].y), f2 = unpack_half2(r[1].x), f3 = unpack_half2(r[1].y);
+            if (p.halves) {
+                x[0] = f0.x, x[1] = f0.y, x[2] = f1.x, x[3] = f1.y;
+                y[0] = f2.x, y[1] = f2.y, y[2] = f3.x, y[3] = f3.y;
+            } else {
+                x[0] = f0.x, x[1] = f1.x, x[2] = f2.x, x[3] = f3.x;
+                y[0] = f0.y, y[1] = f1.y, y[2] = f2.y, y[3] = f3.y;
+            }
+        };
+        float x[4], y[4], w0[4], w1[4];
+        pairs(v, x, y);
+        pairs(w, w0, w1);
+        const float a = fmaf(x[0], x[0], fmaf(x[2], x[2], fmaf(y[0], y[0], y[2] * y[2])));
+        const float b = fmaf(x[1], x[1], fmaf(x[3], x[3], fmaf(y[1], y[1], y[3] * y[3])));
+        float ss = a + b;
 #pragma unroll
-    for (int o = 8; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    const float f = w ? rsqrtf(ss * (1.0f / 128) + p.eps) : 1.f;
-    const bool turn = rotate && (p.halves ? split : c0 < p.rotary);
+        for (int o = 8; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        const float f = norm ? rsqrtf(ss * (1.0f / 128) + p.eps) : 1.f;
+        const bool turn = rotate && (p.halves ? split : c0 < p.rotary);
 #pragma unroll
-    for (int e = 0; e < 4; e++) {
-        const float2 c = turn ? cs[(p.halves ? c0 : c0 >> 1) + e] : make_float2(1.f, 0.f);
-        const float xx = w0[e] * c.x, xy = -w1[e] * c.y, yx = w0[e] * c.y, yy = w1[e] * c.x;
-        const float x0 = turn ? fmaf(x[e], xx, __fmul_rn(y[e], xy)) : __fmul_rn(x[e], xx);
-        const float y0 = turn ? fmaf(x[e], yx, __fmul_rn(y[e], yy)) : __fmul_rn(y[e], yy);
-        x[e] = __fmul_rn(f, x0);
-        y[e] = __fmul_rn(f, y0);
+        for (int e = 0; e < 4; e++) {
+            const float2 c = turn ? cs[(p.halves ? c0 : c0 >> 1) + e] : make_float2(1.f, 0.f);
+            const float xx = w0[e] * c.x, xy = -w1[e] * c.y, yx = w0[e] * c.y, yy = w1[e] * c.x;
+            const float x0 = turn ? fmaf(x[e], xx, __fmul_rn(y[e], xy)) : __fmul_rn(x[e], xx);
+            const float y0 = turn ? fmaf(x[e], yx, __fmul_rn(y[e], yy)) : __fmul_rn(y[e], yy);
+            x[e] = __fmul_rn(f, x0);
+            y[e] = __fmul_rn(f, y0);
+        }
+        if (!dst) return;
+        if (p.halves) {
+            *reinterpret_cast<uint2 *>(dst + c0) = make_uint2(pack_half2(x[0], x[1]), pack_half2(x[2], x[3]));
+            *reinterpret_cast<uint2 *>(dst + c1) = make_uint2(pack_half2(y[0], y[1]), pack_half2(y[2], y[3]));
+        } else {
+            *reinterpret_cast<uint2 *>(dst + c0) = make_uint2(pack_half2(x[0], y[0]), pack_half2(x[1], y[1]));
+            *reinterpret_cast<uint2 *>(dst + c1) = make_uint2(pack_half2(x[2], y[2]), pack_half2(x[3], y[3]));
+        }
     }
-    if (!dst) return;
-    if (p.halves) {
-        *reinterpret_cast<uint2 *>(dst + c0) = make_uint2(pack_half2(x[0], x[1]), pack_half2(x[2], x[3]));
-        *reinterpret_cast<uint2 *>(dst + c1) = make_uint2(pack_half2(y[0], y[1]), pack_half2(y[2], y[3]));
-    } else {
-        *reinterpret_cast<uint2 *>(dst + c0) = make_uint2(pack_half2(x[0], y[0]), pack_half2(x[1], y[1]));
-        *reinterpret_cast<uint2 *>(dst + c1) = make_uint2(pack_half2(x[2], y[2]), pack_half2(x[3], y[3]));
-    }
-}
+};
 
 __device__ __forceinline__ void copy_row(const uint16_t *src, uint16_t *dst) {
     reinterpret_cast<uint4 *>(dst)[threadIdx.x & 15] = reinterpret_cast<const uint4 *>(src)[threadIdx.x & 15];
 }
 
-// Part `part` of a slot's heads: queries, keys, values.
-__device__ __forceinline__ void slot_rows(const AppendRopeParams &p, int b, int part, const float2 *cs) {
+// Sixteen of a slot's heads: queries, keys, values.
+__device__ __forceinline__ void slot_rows(const AppendRopeParams &p, int b, int part, float2 *cs) {
     const int dst = p.dst[b], row = dst & (kFull - 1), heads = p.H_q + 2 * p.H_kv;
-    for (int i0 = part * kRowsPerPass; i0 < heads; i0 += p.parts * kRowsPerPass) {
-        const int i = i0 + (threadIdx.x >> 4), h = i < p.H_q ? i : (i - p.H_q) % p.H_kv, kind = i < p.H_q ? 0 : 1 + (i - p.H_q) / p.H_kv;
-        const uint16_t *src = nullptr;
-        uint16_t *to = nullptr;
-        if (i < p.H_q) {
-            src = p.q + b * p.q_stride + h * 128;
-            to = p.q_out + ((int64_t)b * p.H_q + h) * 128;
-        } else if (i < heads && !(dst & kFull)) {
-            const size_t u = (size_t)b * p.H_kv + h;
-            src = kind == 1 ? p.k_new + b * p.k_stride + h * 128 : p.v_new + b * p.v_stride + h * 128;
-            to = dst & kToSink ? (kind == 1 ? p.k_sink : p.v_sink) + (u * p.S + row) * 128 : (kind == 1 ? p.k_res : p.v_res) + (u * p.R + row) * 128;
-        }
-        if (kind == 2 && to) copy_row(src, to);
-        head_row(p, kind == 2 ? nullptr : src, kind ? p.w_k : p.w_q, p.rotate & (kind ? 2 : 1), kind == 2 ? nullptr : to, cs);
+    const int i = part * kRowsPerPass + (threadIdx.x >> 4), kind = i < p.H_q ? 0 : i < p.H_q + p.H_kv ? 1 : 2, h = kind ? i - p.H_q - (kind - 1) * p.H_kv : i;
+    const uint16_t *src = nullptr;
+    uint16_t *to = nullptr;
+    if (kind == 0) {
+        src = p.q + b * p.q_stride + h * 128;
+        to = p.q_out + ((int64_t)b * p.H_q + h) * 128;
+    } else if (i < heads && !(dst & kFull)) {
+        const size_t u = (size_t)b * p.H_kv + h;
+        src = kind == 1 ? p.k_new + b * p.k_stride + h * 128 : p.v_new + b * p.v_stride + h * 128;
+        to = dst & kToSink ? (kind == 1 ? p.k_sink : p.v_sink) + (u * p.S + row) * 128 : (kind == 1 ? p.k_res : p.v_res) + (u * p.R + row) * 128;
     }
+    const uint16_t *w = kind == 0 ? p.w_q : kind == 1 ? p.w_k : nullptr;
+    const HeadRow r(p, src, w);
+    angles(p, p.pos[b], cs);  // while the rows arrive
+    __syncthreads();
+    r.store(p, w, kind == 0 ? p.rotate & 1 : kind == 1 ? p.rotate & 2 : 0, to, cs);
     if (part == 0 && threadIdx.x == 0) {
         int32_t *l = p.lens + 4 * b;
         if (dst & kToSink) {
@@ -150,7 +159,7 @@ __device__ __forceinline__ void slot_rows(const AppendRopeParams &p, int b, int 
 
 // FORM: 0 min-max codes, 1 e4m3, 2 int8; G tokens a page.
 template <int FORM, int G>
-__global__ void __launch_bounds__(kThreads, G == 256 ? 2 : 4) append_rope_kernel(const __grid_constant__ AppendRopeParams p) {
+__global__ void __launch_bounds__(kThreads, FORM == 0 ? (G == 256 ? 2 : 4) : G == 64 ? 8 : G == 128 ? 5 : 3) append_rope_kernel(const __grid_constant__ AppendRopeParams p) {
     __shared__ __align__(16) unsigned char smem[FORM ? 16 : 32 * 512 + 512];
     __shared__ float2 s_cs[64];
     griddep_wait();
@@ -160,8 +169,6 @@ __global__ void __launch_bounds__(kThreads, G == 256 ? 2 : 4) append_rope_kernel
         i -= n_page;
         const int b = p.b0 + i / p.parts;
         if (p.dst[b] == kNone) return;
-        angles(p, p.pos[b], s_cs);
-        __syncthreads();
         slot_rows(p, b, i % p.parts, s_cs);
         return;
     }
@@ -194,7 +201,7 @@ __global__ void __launch_bounds__(kThreads, G == 256 ? 2 : 4) append_rope_kernel
     if (!first || threadIdx.x >= 32) return;
     const size_t u = (size_t)b * p.H_kv + h;
     if (side == 0)
-        head_row(p, p.k_new + b * p.k_stride + h * 128, p.w_k, p.rotate & 2, threadIdx.x < 16 ? p.k_res + u * p.R * 128 : nullptr, s_cs);
+        HeadRow(p, p.k_new + b * p.k_stride + h * 128, p.w_k).store(p, p.w_k, p.rotate & 2, threadIdx.x < 16 ? p.k_res + u * p.R * 128 : nullptr, s_cs);
     else if (threadIdx.x < 16)
         copy_row(p.v_new + b * p.v_stride + h * 128, p.v_res + u * p.R * 128);
 }
@@ -295,10 +302,7 @@ extern "C" int kvq_paged_append_rope(const kvq_config *c, kvq_paged *pc, const k
     p.per = per;
     p.sides = block8(c) ? 2 : 1 + c->G / 128;
     p.map = new_pages != nullptr;
-    // a slot's heads in as many CTAs as it has passes where there are few slots, in one where there
-    // are many (a CTA forms the sines and cosines)
-    const int passes = (c->H_q + 2 * c->H_kv + kRowsPerPass - 1) / kRowsPerPass;
-    p.parts = std::max(1, std::min(passes, 4 * num_sms() / active));
+    p.parts = (c->H_q + 2 * c->H_kv + kRowsPerPass - 1) / kRowsPerPass;
     if (qk->rotary_dim && freq) turns_of_freq(freq, qk->rotary_dim, p.turn);
     else if (qk->rotary_dim) turns_of_base(qk->rope_base, qk->rotary_dim, p.turn);
     const int form = c->mode == KVQ_MODE_E4M3 ? 1 : c->mode == KVQ_MODE_INT8 ? 2 : 0;

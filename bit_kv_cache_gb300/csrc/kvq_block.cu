@@ -21,27 +21,50 @@ __device__ __forceinline__ Sides sides(const PackParams &p, bool value) {
             value ? p.v_res : p.k_res, value ? p.v_new : p.k_new, value ? p.v_stride : p.k_stride};
 }
 
+// The page index of a page-table entry; -1 (reported) if it is no page.
+__device__ __forceinline__ int64_t page_of(const PackParams &p, int entry, int h) {
+    if (entry >= 0 && entry < p.n_pages) return (int64_t)entry * p.H_kv + h;
+    if (threadIdx.x == 0) report(p.status, KVQ_DEV_BAD_STATE);
+    return -1;
+}
+
+// CTAs per SM: as many as the registers of G / 16 loads per thread leave room for (four prompts of
+// 2K to 12K tokens in pages of 64: 62 us with four CTAs, 55 with eight).
+template <int G>
+constexpr int kCtas = G == 64 ? 8 : G == 128 ? 5 : 3;
+
 // Page blockIdx.x of a planned chunk, or, behind them, a slot's fp16 rows.
 template <bool E4M3, int G>
-__global__ void __launch_bounds__(256, G == 256 ? 2 : 4) block_extend_kernel(const __grid_constant__ ExtendParams p) {
-    const int h = blockIdx.y, side = blockIdx.z;
+__global__ void __launch_bounds__(256, kCtas<G>) block_extend_kernel(const __grid_constant__ BlockExtendParams p) {
+    const int h = blockIdx.y, side = blockIdx.z, i = blockIdx.x;
     griddep_wait();
-    if (blockIdx.x >= p.n_pack) {
-        extend_slot(p, blockIdx.x - p.n_pack, h, side, 0, 1);
+    if (i >= p.n_pack) {
+        extend_slot(p, i - p.n_pack, h, side, 0, 1);
         return;
     }
-    const PageJob jb = find_page(p, blockIdx.x);
+    int lo = 0, hi = p.B - 1;  // the slot: the first one whose pages end behind page i
+    while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (p.page0[mid + 1] > i) hi = mid;
+        else lo = mid + 1;
+    }
+    const int b = lo, j = i - p.page0[b], t0 = j * G, nr = p.nr[b];
     const Sides s = sides(p, side);
-    pack_block<E4M3, G>([&](int t) { return stream_row(p, jb, s.res, s.src, s.stride, h, jb.t0 + t); }, [&] { return jb.page(p, h); },
-                        side, s.codes, s.scales);
-    if (p.once && jb.t0 == 0) {  // every thread has read its rows (the barrier inside the packing)
-        const int4 *d = reinterpret_cast<const int4 *>(p.desc) + 2 * jb.b;
-        keep_rows(p, d[0], d[1], jb.b, h, side, false, true, threadIdx.x, 256);
+    const int entry = p.ptab[(size_t)b * p.ptab_stride + p.lp0[b] + j];
+    const uint16_t *res = s.res + (((size_t)b * p.H_kv + h) * p.R + t0) * 128, *src = s.src + (int64_t)(p.row0[b] + t0) * s.stride + h * 128;
+    // residual rows are read by ordinary loads: a CTA of the slot writes over them
+    pack_block<E4M3, G>([&](int t) { return t0 + t < nr ? res + t * 128 : src + t * s.stride; }, [&] { return page_of(p, entry, h); }, side,
+                        s.codes, s.scales);
+    // a slot that packs has a page for each G rows of its residual: the CTA that has read the old rows
+    // (the barrier inside the packing) writes the new ones
+    if (t0 < p.R) {
+        const int4 *d = reinterpret_cast<const int4 *>(p.desc) + 2 * b;
+        keep_rows(p, d[0], d[1], b, h, side, false, true, threadIdx.x, 256, t0, t0 + G);
     }
 }
 
 template <bool E4M3, int G>
-__global__ void __launch_bounds__(256, G == 256 ? 2 : 4) block_list_kernel(const __grid_constant__ BlockListParams p) {
+__global__ void __launch_bounds__(256, kCtas<G>) block_list_kernel(const __grid_constant__ BlockListParams p) {
     const int h = blockIdx.y, side = blockIdx.z, k = blockIdx.x / p.per, j = blockIdx.x - k * p.per, b = p.seq[k];
     griddep_wait();
     const Sides s = sides(p, side);
@@ -51,12 +74,7 @@ __global__ void __launch_bounds__(256, G == 256 ? 2 : 4) block_list_kernel(const
         t += j * G;
         return t < p.nr ? res + (size_t)t * 128 : src + (int64_t)(p.row0 + t - p.nr) * s.stride;
     };
-    auto page = [&]() -> int64_t {
-        if (entry >= 0 && entry < p.n_pages) return (int64_t)entry * p.H_kv + h;
-        if (threadIdx.x == 0) report(p.status, KVQ_DEV_BAD_STATE);
-        return -1;
-    };
-    pack_block<E4M3, G>(row, page, side, s.codes, s.scales);
+    pack_block<E4M3, G>(row, [&] { return page_of(p, entry, h); }, side, s.codes, s.scales);
     if (p.commit && j == 0 && h == 0 && side == 0 && threadIdx.x == 0) {
         p.lens[4 * b + 1] += p.R;
         p.lens[4 * b + 2] = 0;
@@ -74,16 +92,19 @@ cudaError_t by_form(int G, bool e4m3, F f) {
 
 }  // namespace
 
-cudaError_t launch_block_extend(const ExtendParams &p, bool e4m3, cudaStream_t st) {
-    const bool once = p.once && p.n_pack > 0;
-    if (p.n_pack > 0) {
-        const dim3 grid((unsigned)(p.n_pack + (once ? p.B : 0)), (unsigned)p.H_kv, 2);
-        const cudaError_t e = by_form(p.G, e4m3, [&](auto form, auto g) {
-            return launch_dependent(block_extend_kernel<decltype(form)::value, decltype(g)::value>, grid, 256, 0, st, p);
-        });
-        if (e != cudaSuccess || once) return e;
+cudaError_t launch_block_extend(const ExtendParams &x, const ChunkSlot *slots, bool e4m3, cudaStream_t st) {
+    if (x.n_pack == 0) return launch_extend_tail(x, st);
+    BlockExtendParams p;
+    static_cast<ExtendParams &>(p) = x;
+    for (int b = 0; b < x.B; b++) {
+        p.nr[b] = slots[b].nr;
+        p.row0[b] = slots[b].cu + slots[b].to_sink - slots[b].nr;
+        p.lp0[b] = slots[b].T / x.G;
     }
-    return launch_extend_tail(p, st);
+    const dim3 grid((unsigned)(p.n_pack + p.B), (unsigned)p.H_kv, 2);
+    return by_form(p.G, e4m3, [&](auto form, auto g) {
+        return launch_dependent(block_extend_kernel<decltype(form)::value, decltype(g)::value>, grid, 256, 0, st, p);
+    });
 }
 
 cudaError_t launch_block_list(const BlockListParams &p, bool e4m3, cudaStream_t st) {

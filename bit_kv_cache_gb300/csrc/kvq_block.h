@@ -10,6 +10,12 @@
 
 namespace kvq {
 
+// A planned chunk's pages, with what a page's CTA has to know of its slot: residual tokens before the
+// chunk, the chunk row behind them (as if the residual had come from the chunk), first logical page.
+struct BlockExtendParams : ExtendParams {
+    int32_t nr[KVQ_PAGED_MAX_B], row0[KVQ_PAGED_MAX_B], lp0[KVQ_PAGED_MAX_B];
+};
+
 // Pages of listed slots: page i of the call is page i % per of slot seq[i / per], and logical page
 // lp0[i / per] + i % per there.  Its rows come from the residual (the first nr of the stream) and
 // then from k_new, v_new, whose row row0 + t - nr of head h starts at h h_stride + that t stride.
@@ -44,7 +50,7 @@ struct BlockDecodeParams {
     int32_t part0[KVQ_PAGED_MAX_B + 1];  // parts of the ones before each
 };
 
-cudaError_t launch_block_extend(const ExtendParams &p, bool e4m3, cudaStream_t st);
+cudaError_t launch_block_extend(const ExtendParams &p, const ChunkSlot *slots, bool e4m3, cudaStream_t st);
 cudaError_t launch_block_list(const BlockListParams &p, bool e4m3, cudaStream_t st);
 size_t block_decode_ws_bytes(const kvq_config *c);
 int block_decode(const kvq_config *c, const kvq_paged *pc, const uint16_t *q, uint16_t *out, void *ws, size_t ws_bytes,

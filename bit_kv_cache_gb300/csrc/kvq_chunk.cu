@@ -695,8 +695,8 @@ int kvq_paged_extend(const kvq_config *c, kvq_paged *pc, const kvq_chunk *ch, co
     }
     p.page0[c->B] = p.n_pack;
     if (p.n_pack > 0 && pc->n_pages < 1) return KVQ_ERR_CAPACITY;
-    p.once = c->R == c->G && (block8(c) || c->G == 128);
-    if ((block8(c) ? launch_block_extend(p, c->mode == KVQ_MODE_E4M3, st) : launch_extend(p, c->bits, vbits_of(c), st)) != cudaSuccess)
+    p.once = block8(c) || (c->R == c->G && c->G == 128);
+    if ((block8(c) ? launch_block_extend(p, slots_of(ch), c->mode == KVQ_MODE_E4M3, st) : launch_extend(p, c->bits, vbits_of(c), st)) != cudaSuccess)
         return KVQ_ERR_CUDA;
     for (int b = 0; b < c->B; b++) {
         const ChunkSlot &s = slots_of(ch)[b];

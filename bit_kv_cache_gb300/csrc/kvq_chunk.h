@@ -39,8 +39,8 @@ struct PackParams {
 struct ExtendParams : PackParams {
     const int32_t *desc;
     int n_pack;                          // pages to pack, over all slots
-    int once;                            // one page holds all old residual rows of a slot, so that the CTA that packs
-                                         // it may overwrite them: then one launch does the whole call
+    int once;                            // the CTAs that pack a slot's old residual rows write its new ones: then one
+                                         // launch does the whole call
     int32_t page0[KVQ_PAGED_MAX_B + 1];  // of the slots before each
 };
 

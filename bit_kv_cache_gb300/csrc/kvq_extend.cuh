@@ -236,15 +236,16 @@ __device__ __forceinline__ void extend_values(const PackParams &p, const PageJob
 
 // Rows of a slot that stay fp16: its new sink rows and, from row lo on, its residual's new
 // rows up to hi, which are the chunk's last tokens (a slot that packs nothing keeps its old
-// rows, one that packs takes all of them).  Sixteen threads per row, thread t of n.
+// rows, one that packs takes all of them), of these rows from .. to - 1.  Sixteen threads per row,
+// thread t of n.
 __device__ __forceinline__ void keep_rows(const ExtendParams &p, const int4 &x, const int4 &y, int b, int h, int side, bool sink,
-                                          bool residual, int t, int n) {
-    const int to_sink = sink ? y.y : 0, pk = y.z, lo = pk ? 0 : x.z, hi = residual ? x.z + x.w - y.y - pk : lo;
+                                          bool residual, int t, int n, int from = 0, int to = INT32_MAX) {
+    const int to_sink = sink ? y.y : 0, pk = y.z, lo = max(from, pk ? 0 : x.z), hi = residual ? min(to, x.z + x.w - y.y - pk) : lo;
     const int64_t stride = side ? p.v_stride : p.k_stride;
     const uint16_t *src = (side ? p.v_new : p.k_new) + h * 128;
     const size_t u = (size_t)b * p.H_kv + h;
     uint16_t *sk = side ? p.v_sink : p.k_sink, *res = side ? p.v_res : p.k_res;
-    const int rows = to_sink + hi - lo, c = t & 15;
+    const int rows = to_sink + max(hi - lo, 0), c = t & 15;
     for (int i = t >> 4; i < rows; i += n >> 4) {
         const int r = i - to_sink + lo;
         const int tok = i < to_sink ? i : y.y + pk + r - x.z;
