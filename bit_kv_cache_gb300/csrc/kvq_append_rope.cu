@@ -194,8 +194,8 @@ __global__ void __launch_bounds__(kThreads, FORM == 0 ? (G == 256 ? 2 : 4) : G =
             else extend_values<8>(p, jb, h, side - 1, smem);
         }
     } else {
-        pack_block<FORM == 1, G>([&](int t) { return stream_row(p, jb, side ? p.v_res : p.k_res, nullptr, 0, h, jb.t0 + t); },
-                                 [&] { return jb.page(p, h); }, side, reinterpret_cast<uint8_t *>(side ? p.v_codes : p.k_codes),
+        const uint16_t *src = (side ? p.v_res : p.k_res) + (((size_t)b * p.H_kv + h) * p.R + jb.t0) * 128;
+        pack_block<FORM == 1, G>(nullptr, 0, src, 128, [&] { return jb.page(p, h); }, side, reinterpret_cast<uint8_t *>(side ? p.v_codes : p.k_codes),
                                  reinterpret_cast<float4 *>(side ? p.v_meta : p.k_meta));
     }
     if (!first || threadIdx.x >= 32) return;

@@ -53,8 +53,7 @@ __global__ void __launch_bounds__(256, kCtas<G>) block_extend_kernel(const __gri
     const int entry = p.ptab[(size_t)b * p.ptab_stride + p.lp0[b] + j];
     const uint16_t *res = s.res + (((size_t)b * p.H_kv + h) * p.R + t0) * 128, *src = s.src + (int64_t)(p.row0[b] + t0) * s.stride + h * 128;
     // residual rows are read by ordinary loads: a CTA of the slot writes over them
-    pack_block<E4M3, G>([&](int t) { return t0 + t < nr ? res + t * 128 : src + t * s.stride; }, [&] { return page_of(p, entry, h); }, side,
-                        s.codes, s.scales);
+    pack_block<E4M3, G>(res, nr - t0, src, s.stride, [&] { return page_of(p, entry, h); }, side, s.codes, s.scales);
     // a slot that packs has a page for each G rows of its residual: the CTA that has read the old rows
     // (the barrier inside the packing) writes the new ones
     if (t0 < p.R) {
@@ -68,14 +67,11 @@ __global__ void __launch_bounds__(256, kCtas<G>) block_list_kernel(const __grid_
     const int h = blockIdx.y, side = blockIdx.z, k = blockIdx.x / p.per, j = blockIdx.x - k * p.per, b = p.seq[k];
     griddep_wait();
     const Sides s = sides(p, side);
-    const uint16_t *res = s.res + ((size_t)b * p.H_kv + h) * p.R * 128, *src = s.src + h * p.h_stride;
     const int entry = p.ptab[(size_t)b * p.ptab_stride + p.lp0[k] + j];
-    auto row = [&](int t) {
-        t += j * G;
-        return t < p.nr ? res + (size_t)t * 128 : src + (int64_t)(p.row0 + t - p.nr) * s.stride;
-    };
-    pack_block<E4M3, G>(row, [&] { return page_of(p, entry, h); }, side, s.codes, s.scales);
-    if (p.commit && j == 0 && h == 0 && side == 0 && threadIdx.x == 0) {
+    const uint16_t *src = p.residual ? s.res + (((size_t)b * p.H_kv + h) * p.R + j * G) * 128
+                                     : s.src + h * p.h_stride + (int64_t)(p.row0 + j * G) * s.stride;
+    pack_block<E4M3, G>(nullptr, 0, src, p.residual ? 128 : s.stride, [&] { return page_of(p, entry, h); }, side, s.codes, s.scales);
+    if (p.residual && j == 0 && h == 0 && side == 0 && threadIdx.x == 0) {
         p.lens[4 * b + 1] += p.R;
         p.lens[4 * b + 2] = 0;
     }

@@ -27,55 +27,66 @@ __device__ __forceinline__ void code_pairs(uint32_t w, uint32_t &lo, uint32_t &h
     }
 }
 
-// Four values to codes (a in the low byte): the fp32 product with inv, rounded to nearest even.
+// Four fp16 values to codes (the low half of x in the low byte): the fp32 product with inv, rounded
+// to nearest even.
 template <bool E4M3>
-__device__ __forceinline__ uint32_t to_codes(float a, float b, float c, float d, float inv) {
-    a = __fmul_rn(a, inv);
-    b = __fmul_rn(b, inv);
-    c = __fmul_rn(c, inv);
-    d = __fmul_rn(d, inv);
+__device__ __forceinline__ uint32_t to_codes(uint32_t x, uint32_t y, uint64_t inv2) {
+    const float2 a = unpack_half2(x), b = unpack_half2(y);
+    const float2 c = up2(mul_x2(pk2(a.x, a.y), inv2)), d = up2(mul_x2(pk2(b.x, b.y), inv2));
     if (E4M3) {
-        uint16_t x, y;
-        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(x) : "f"(b), "f"(a));
-        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(y) : "f"(d), "f"(c));
-        return (uint32_t)x | ((uint32_t)y << 16);
+        uint32_t r;
+        asm("{.reg .b16 l, h;\n cvt.rn.satfinite.e4m3x2.f32 l, %2, %1;\n cvt.rn.satfinite.e4m3x2.f32 h, %4, %3;\n mov.b32 %0, {l, h};}"
+            : "=r"(r) : "f"(c.x), "f"(c.y), "f"(d.x), "f"(d.y));
+        return r;
     }
-    // 1.5 * 2^23 more, the low byte is the integer (at most 127: x * (127 / amax) <= 127 (1 + 2^-23))
+    // 1.5 * 2^23 more, the low byte is the integer (at most 127: x * (127 / amax) <= 127 (1 + 2^-23)).
+    // The additions are scalar: a pair's product and sum were joined to one rounding
     const float m = 12582912.f;
-    const uint32_t i = __float_as_uint(__fadd_rn(a, m)), j = __float_as_uint(__fadd_rn(b, m));
-    const uint32_t k = __float_as_uint(__fadd_rn(c, m)), l = __float_as_uint(__fadd_rn(d, m));
+    const uint32_t i = __float_as_uint(__fadd_rn(c.x, m)), j = __float_as_uint(__fadd_rn(c.y, m));
+    const uint32_t k = __float_as_uint(__fadd_rn(d.x, m)), l = __float_as_uint(__fadd_rn(d.y, m));
     return prmt(prmt(i, j, 0x0040), prmt(k, l, 0x0040), 0x5410);
 }
 
-__device__ __forceinline__ uint32_t max_abs2(uint32_t m, uint32_t x) { return __vmaxu2(m, x & 0x7fff7fffu); }
+// The larger magnitudes of two pairs, NaN if one is.
+__device__ __forceinline__ __half2 max_abs2(__half2 m, uint32_t x) { return __hmax2_nan(m, __habs2(*reinterpret_cast<const __half2 *>(&x))); }
 
 // One side of a page of G tokens by a CTA of 256 threads:
 //   scale = amax / M, code = rn(x (M / amax)),  M = 448 (e4m3) or 127 (int8); 1 and 0 of zeros.
-// row(t): address of token t's 128 fp16 channels; page(): the page's index, asked for once the
-// rows are in registers (-1: nothing is stored).  Largest magnitudes are compared as integers, in
-// which NaN is above infinity: a page that holds one gets an infinite or NaN scale, so that all
-// its values count as NaN.
+// Token t's 128 fp16 channels lie at res + 128 t for t < nr, behind that at src + t stride (nr <= 0:
+// all there, the common case, which has loads of its own: one addition for an address); page(): the
+// page's index, asked for once the rows are in registers (-1: nothing is stored).  A page that holds
+// an infinity or NaN gets an infinite or NaN scale, so that all its values count as NaN.
 // Keys: thread (tid / 16, tid % 16) holds 8 channels of every 16th row, so that loads and stores
 // are whole rows.  Values are stored with tokens contiguous: a thread holds four neighbouring
 // tokens of 8 channels and turns their bytes in registers (16 lanes store 64 contiguous bytes; no
 // staging in shared memory, no second barrier).
-template <bool E4M3, int G, typename Row, typename Page>
-__device__ __forceinline__ void pack_block(Row row, Page page, bool value, uint8_t *codes, float4 *scales) {
+template <bool E4M3, int G, typename Page>
+__device__ __forceinline__ void pack_block(const uint16_t *res, int nr, const uint16_t *src, int64_t stride, Page page, bool value,
+                                           uint8_t *codes, float4 *scales) {
     constexpr int N = G / 16;
     __shared__ uint32_t s_max[8];
     const int tid = threadIdx.x, lo = tid & 15, hi = tid >> 4;
     const int cg = value ? hi : lo;  // eight channels
     uint4 x[N];
+    const int first = value ? 4 * lo : hi;  // the thread's rows: first, and from there
+    auto row = [&](int i) { return value ? 64 * (i >> 2) + (i & 3) : 16 * i; };
+    if (nr <= 0) {
+        const uint16_t *at = src + first * stride + 8 * cg;
 #pragma unroll
-    for (int i = 0; i < N; i++) {
-        const int t = value ? 64 * (i >> 2) + 4 * lo + (i & 3) : 16 * i + hi;
-        x[i] = reinterpret_cast<const uint4 *>(row(t))[cg];
+        for (int i = 0; i < N; i++) x[i] = *reinterpret_cast<const uint4 *>(at + row(i) * stride);
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; i++) {
+            const int t = first + row(i);
+            x[i] = *reinterpret_cast<const uint4 *>((t < nr ? res + t * 128 : src + t * stride) + 8 * cg);
+        }
     }
-    uint32_t m = 0;
+    __half2 m2 = __half2half2(__ushort_as_half(0));
 #pragma unroll
-    for (int i = 0; i < N; i++) m = max_abs2(max_abs2(max_abs2(max_abs2(m, x[i].x), x[i].y), x[i].z), x[i].w);
-    m = max(m & 0xffffu, m >> 16);
-    m = __reduce_max_sync(0xffffffffu, m);
+    for (int i = 0; i < N; i++) m2 = max_abs2(max_abs2(max_abs2(max_abs2(m2, x[i].x), x[i].y), x[i].z), x[i].w);
+    // magnitudes as integers: NaN (0x7fff) is above infinity
+    const uint32_t mm = *reinterpret_cast<const uint32_t *>(&m2);
+    uint32_t m = __reduce_max_sync(0xffffffffu, max(mm & 0x7fffu, mm >> 16 & 0x7fffu));
     if ((tid & 31) == 0) s_max[tid >> 5] = m;
     __syncthreads();
     const int64_t pg = page();
@@ -84,14 +95,14 @@ __device__ __forceinline__ void pack_block(Row row, Page page, bool value, uint8
     for (int i = 0; i < 8; i++) m = max(m, s_max[i]);
     const float amax = h2f((uint16_t)m), top = E4M3 ? 448.f : 127.f;
     const float inv = m ? __fdiv_rn(top, amax) : 0.f;
+    const uint64_t inv2 = pk2(inv, inv);
     if (tid == 0) scales[pg] = make_float4(m ? __fdiv_rn(amax, top) : 1.f, 0.f, 0.f, 0.f);
     uint8_t *dst = codes + (size_t)pg * (G * 128);
     uint32_t c[N][2];
 #pragma unroll
     for (int i = 0; i < N; i++) {
-        const float2 a = unpack_half2(x[i].x), b = unpack_half2(x[i].y), e = unpack_half2(x[i].z), f = unpack_half2(x[i].w);
-        c[i][0] = to_codes<E4M3>(a.x, a.y, b.x, b.y, inv);
-        c[i][1] = to_codes<E4M3>(e.x, e.y, f.x, f.y, inv);
+        c[i][0] = to_codes<E4M3>(x[i].x, x[i].y, inv2);
+        c[i][1] = to_codes<E4M3>(x[i].z, x[i].w, inv2);
     }
     if (!value) {
 #pragma unroll

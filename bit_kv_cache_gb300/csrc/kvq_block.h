@@ -17,12 +17,11 @@ struct BlockExtendParams : ExtendParams {
 };
 
 // Pages of listed slots: page i of the call is page i % per of slot seq[i / per], and logical page
-// lp0[i / per] + i % per there.  Its rows come from the residual (the first nr of the stream) and
-// then from k_new, v_new, whose row row0 + t - nr of head h starts at h h_stride + that t stride.
-// commit: the slots' lengths become T + R and no residual.
+// lp0[i / per] + i % per there.  Its rows are the residual's, whose lengths then become T + R and 0
+// (residual), or those of k_new, v_new from row row0 on; heads lie h_stride apart there.
 struct BlockListParams : PackParams {
     int64_t h_stride;
-    int n_pack, per, nr, row0, commit;
+    int n_pack, per, row0, residual;
     int16_t seq[KVQ_PAGED_MAX_B];
     int32_t lp0[KVQ_PAGED_MAX_B];
 };

@@ -350,10 +350,9 @@ int kvq_paged_flush(const kvq_config *c, kvq_paged *pc, int *n_flushed, void *st
     cudaStream_t st = (cudaStream_t)stream;
     if (block8(c) && !list.empty()) {
         BlockListParams p = block_list(c, pc);
-        p.nr = c->R;
+        p.residual = 1;
         p.per = c->R / c->G;
         p.n_pack = p.per * (int)list.size();
-        p.commit = 1;
         for (size_t i = 0; i < list.size(); i++) {
             p.seq[i] = (int16_t)list[i];
             p.lp0[i] = pc->lens_host[4 * list[i] + 1] / c->G;
