@@ -165,19 +165,35 @@ def _stream_of(index):
 
 def _rows(t, heads, D, n, device, what):
     """(address, row stride) of token-major rows [>= n][heads][D], float16, heads adjacent."""
-    if t.device != device or t.dtype != _float16():
+    if t.get_device() != device.index or t.dtype is not _float16():
         raise ValueError("%s must be a float16 tensor on %s" % (what, device))
-    shape, stride = t.shape, t.stride()
-    if len(shape) != 3 or shape[0] < n or shape[1] != heads or shape[2] != D:
-        raise ValueError("%s has shape %s, expected at least [%d, %d, %d]" % (what, tuple(shape), n, heads, D))
-    if stride[2] != 1 or (heads > 1 and stride[1] != D):
+    if t.dim() != 3:
+        raise ValueError("%s has shape %s, expected at least [%d, %d, %d]" % (what, tuple(t.shape), n, heads, D))
+    (r, h, d), (s0, s1, s2) = t.shape, t.stride()
+    if r < n or h != heads or d != D:
+        raise ValueError("%s has shape %s, expected at least [%d, %d, %d]" % (what, (r, h, d), n, heads, D))
+    if s2 != 1 or (heads > 1 and s1 != D):
         raise ValueError("%s must hold each token's heads contiguously" % what)
-    return t.data_ptr(), (stride[0] if shape[0] > 1 else heads * D)
+    return t.data_ptr(), (s0 if r > 1 else heads * D)
+
+
+def _weight(w, D, device, what):
+    """Address of a norm's weights (None: no norm)."""
+    if w is None:
+        return None
+    if w.get_device() != device.index or w.dtype is not _float16() or w.dim() != 1 or w.numel() != D or not w.is_contiguous():
+        raise ValueError("%s must be a contiguous float16 tensor [%d] on %s" % (what, D, device))
+    return w.data_ptr()
+
+
+_types = []
 
 
 def _float16():
-    import torch
-    return torch.float16
+    if not _types:
+        import torch
+        _types.append(torch.float16)
+    return _types[0]
 
 
 class Rope:
@@ -577,6 +593,7 @@ class KVQPagedCache:
         self.ws = torch.zeros(lib.kvq_paged_workspace_bytes(cp), dtype=torch.uint8, device=self.device)
         self._refs = ctypes.byref(self.cfg), ctypes.byref(self.p)
         self._ws = self.ws.data_ptr(), self.ws.numel()
+        self._dims, self._rope = (B, H_q, H_kv, D), None
         self.caller_pages = False                     # plan() was given pages of the caller's
         self.mapping = 0                              # counts the calls that took pages away from slots
         self.free = list(range(n_pages - 1, -1, -1))  # pop() hands out the lowest id first
@@ -635,61 +652,60 @@ class KVQPagedCache:
         in every later call that needs pages, until clear(); by default they come from the
         cache's own free list.  Returns the queries for decode_attn, out if it is given
         (contiguous [B, H_q, D]; it may be q)."""
-        torch, cfg, dev = self.torch, self.cfg, self._dev
-        B, D = cfg.B, cfg.D
-        qp, qs = _rows(q, cfg.H_q, D, B, dev, "q")
-        kp, ks = _rows(k, cfg.H_kv, D, B, dev, "k")
-        vp, vs = _rows(v, cfg.H_kv, D, B, dev, "v")
-        for w, what in ((w_q, "w_q"), (w_k, "w_k")):
-            if w is not None and (w.device != dev or w.dtype != torch.float16 or w.shape != (D,) or not w.is_contiguous()):
-                raise ValueError("%s must be a contiguous float16 tensor [%d] on %s" % (what, D, dev))
+        dev = self._dev
+        B, H_q, H_kv, D = self._dims
+        qp, qs = _rows(q, H_q, D, B, dev, "q")
+        kp, ks = _rows(k, H_kv, D, B, dev, "k")
+        vp, vs = _rows(v, H_kv, D, B, dev, "v")
+        wq, wk = _weight(w_q, D, dev, "w_q"), _weight(w_k, D, dev, "w_k")
         if out is None:
-            if torch.cuda.is_current_stream_capturing():
+            if self.torch.cuda.is_current_stream_capturing():
                 raise KvqError(-2, "kvq_paged_append_rope")  # before anything is allocated
-            out = torch.zeros((B, cfg.H_q, D), dtype=torch.float16, device=dev)
-        op, os_ = _rows(out, cfg.H_q, D, B, dev, "out")
-        if os_ != cfg.H_q * D or out.shape[0] != B:
-            raise ValueError("out must be contiguous [%d, %d, %d]" % (B, cfg.H_q, D))
+            out = self.torch.zeros((B, H_q, D), dtype=self.torch.float16, device=dev)
+        op, os_ = _rows(out, H_q, D, B, dev, "out")
+        if os_ != H_q * D or out.numel() != B * H_q * D:
+            raise ValueError("out must be contiguous [%d, %d, %d]" % (B, H_q, D))
         if rope is None:
-            rope = self._rope = getattr(self, "_rope", None) or Rope(D)
-        c = QkConfig(cfg.H_q, cfg.H_kv, D, rope.rotary_dim, int(rope.halves), int(bool(rotate_q)) + 2 * int(bool(rotate_k)),
-                     eps, 0.0, qs, ks)
-        own, taken = pages is None, []
+            rope = self._rope = self._rope or Rope(D)
+        c = QkConfig(H_q, H_kv, D, rope.rotary_dim, rope.halves, (1 if rotate_q else 0) + (2 if rotate_k else 0), eps, 0.0, qs, ks)
+        own, taken = pages is None, ()
         if own:
-            n = ctypes.c_int(0)
-            seqs = (ctypes.c_int32 * B)()
-            _check(lib.kvq_paged_flush_plan(*self._refs, seqs, ctypes.byref(n)), "flush plan")
-            ids = []
-            per, full = cfg.R // cfg.G, seqs[: n.value]
-            if full and self.caller_pages:
-                raise KvqError(-1, "the caller maps this cache's pages")
-            j0 = [self.lens_host[4 * b + 1] // cfg.G for b in full]
-            if sum(max(0, j + per - len(self.pages[b])) for b, j in zip(full, j0)) > len(self.free):
-                raise KvqError(-3, "page pool exhausted")
-            for b, j in zip(full, j0):
-                while len(self.pages[b]) < j + per:
-                    taken.append(b)
-                    self.pages[b].append(self.free.pop())
-                ids += self.pages[b][j: j + per]
-            ids = (ctypes.c_int32 * len(ids))(*ids)
-            pp, np_ = ids, len(ids)
-        elif isinstance(pages, torch.Tensor):
-            if pages.device.type != "cpu" or pages.dtype != torch.int32 or pages.dim() != 1 or not pages.is_contiguous():
+            pp, np_, taken = self._full_pages()
+        elif isinstance(pages, self.torch.Tensor):
+            if pages.get_device() >= 0 or pages.dtype is not self.torch.int32 or pages.dim() != 1 or not pages.is_contiguous():
                 raise ValueError("pages must be a contiguous int32 CPU tensor")
             pp, np_ = (pages.data_ptr() or ctypes.addressof(self.lens_host)), pages.numel()
         else:
             ids = (ctypes.c_int32 * max(1, len(pages)))(*[int(x) for x in pages])
             pp, np_ = ids, len(pages)
         try:
-            _check(lib.kvq_paged_append_rope(*self._refs, ctypes.byref(c), rope._ptr, rope.amp, qp, kp, vp, vs,
-                                             None if w_q is None else w_q.data_ptr(), None if w_k is None else w_k.data_ptr(), op,
-                                             pp, np_, _stream_of(dev.index)), "kvq_paged_append_rope")
+            _check(lib.kvq_paged_append_rope(*self._refs, ctypes.byref(c), rope._ptr, rope.amp, qp, kp, vp, vs, wq, wk, op, pp, np_,
+                                             _stream_of(dev.index)), "kvq_paged_append_rope")
         except Exception:
             for b in reversed(taken):  # their table rows are not written
                 self.free.append(self.pages[b].pop())
             raise
         self.caller_pages |= not own
         return out
+
+    def _full_pages(self):
+        """Pages for the full residuals, slot after slot, from the free list: (ids, their number,
+        the slots that got one each time)."""
+        cfg = self.cfg
+        n, seqs = ctypes.c_int(0), (ctypes.c_int32 * cfg.B)()
+        _check(lib.kvq_paged_flush_plan(*self._refs, seqs, ctypes.byref(n)), "flush plan")
+        ids, taken, per, full = [], [], cfg.R // cfg.G, seqs[: n.value]
+        if full and self.caller_pages:
+            raise KvqError(-1, "the caller maps this cache's pages")
+        j0 = [self.lens_host[4 * b + 1] // cfg.G for b in full]
+        if sum(max(0, j + per - len(self.pages[b])) for b, j in zip(full, j0)) > len(self.free):
+            raise KvqError(-3, "page pool exhausted")
+        for b, j in zip(full, j0):
+            while len(self.pages[b]) < j + per:
+                taken.append(b)
+                self.pages[b].append(self.free.pop())
+            ids += self.pages[b][j: j + per]
+        return (ctypes.c_int32 * len(ids))(*ids), len(ids), taken
 
     def decode_step(self, q, k, v, rope=None, w_q=None, w_k=None, eps=1e-6, out=None):
         """One decode step of every active slot: append_rope, then decode_attn."""
@@ -869,7 +885,7 @@ class KVQPagedCache:
         if out is None:
             out = self.torch.zeros_like(q)
         for t, what in ((q, "q"), (out, "out")):
-            if t.device != dev or t.dtype != self.torch.float16 or not t.is_contiguous():
+            if t.get_device() != dev.index or t.dtype is not _float16() or not t.is_contiguous():
                 raise ValueError("%s must be a contiguous float16 tensor on %s" % (what, dev))
             if t.shape != shape:
                 raise ValueError("%s has shape %s, expected %s" % (what, tuple(t.shape), shape))
