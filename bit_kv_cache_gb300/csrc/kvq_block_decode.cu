@@ -66,7 +66,7 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
 // Scores of 16 N tokens (x[s]: tokens r and r + 8 of group s, rows 2 c, 2 c + 1 of row tile n) to
 // weights, as B operands of the value product.  a, lsv: y = x a + lsv; inv: 1 / s_V.
 template <int N, int NT>
-__device__ __forceinline__ void weights(State<NT> &st, int n, float (&x)[N][4], float a, float lsv, float inv, uint32_t (&b)[N][2]) {
+__device__ __forceinline__ void weights(State<NT> &st, int n, float (&x)[N][4], float a, float lsv, float inv, uint32_t (*b)[2]) {
 #pragma unroll
     for (int s = 0; s < N; s++)
 #pragma unroll
@@ -240,11 +240,11 @@ struct Bars {
     uint64_t full[kWarps][kStages];
     int stop, odd;
 };
-// the joined states lie in the rings: of a row tile at a time
-constexpr int kRingBytes = kWarps * kStages * kPiece, kStateBytes = kWarps * (8 * 128 + 16) * 4;
-static_assert(kStateBytes <= kRingBytes, "shared memory");
+// Shared memory: rings (then the outputs of the warps' states), queries, references and sums, barriers.
+constexpr int kRingBytes = kWarps * kStages * kPiece;
+static_assert(kWarps * kFewRows * 128 * 4 <= kRingBytes, "shared memory");
 template <int NT>
-constexpr int kSmemBytes = kRingBytes + (NT > 1 ? NT * 2048 : 0) + (int)sizeof(Bars);
+constexpr int kSmemBytes = kRingBytes + (NT > 1 ? NT * 2048 : 0) + kWarps * 8 * NT * 8 + (int)sizeof(Bars);
 
 // Lengths of a slot: {sink, packed, residual, new tokens (decode: 0)}, the row of its first query.
 struct Slot {
@@ -321,14 +321,12 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) block_decode_kernel
     __syncthreads();
     const int np = sl.T / kTokens, seen = sl.seen(), n = np + (seen + kTailTokens - 1) / kTailTokens;
     const int begin = (int)((int64_t)n * part / parts), end = (int)((int64_t)n * (part + 1) / parts);
-    int lim[NT][2];  // fp16 tokens that a row may see
     State<NT> st;
 #pragma unroll
     for (int t = 0; t < NT; t++) {
 #pragma unroll
         for (int e = 0; e < 2; e++) {
             st.m[t][e] = -INFINITY, st.l[t][e] = 0.f;
-            lim[t][e] = sl.n_new ? sl.ns + sl.nr + min(8 * t + 2 * c + e, rows - 1) / p.g + 1 : seen;
         }
 #pragma unroll
         for (int i = 0; i < 8; i++)
@@ -367,20 +365,25 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) block_decode_kernel
         for (int i = 0; i < min(kStages, 2 * m); i++) bring(i);
         // the warp's fp16 tiles, while the first pieces are on their way
         for (int i = t0 ? end : begin + w + (max(np - begin - w, 0) + kWarps - 1) / kWarps * kWarps; i < end; i += kWarps) {
+            int lim[NT][2];  // fp16 tokens that a row may see
+#pragma unroll
+            for (int t = 0; t < NT; t++)
+#pragma unroll
+                for (int e = 0; e < 2; e++) lim[t][e] = sl.n_new ? sl.ns + sl.nr + min(8 * t + 2 * c + e, rows - 1) / p.g + 1 : seen;
             const int x = (i - np) * kTailTokens, x0 = min(x + r, seen - 1), x1 = min(x + r + 8, seen - 1);
             if (tail_tile<NT>(st, q, tail_at(p, sl, u, h, x0, false), tail_at(p, sl, u, h, x1, false), tail_at(p, sl, u, h, x0, true),
                               tail_at(p, sl, u, h, x1, true), x, seen, lim, lane))
                 *(volatile int *)&bar->odd = 1;
         }
         for (int t = 0; t < m; t++) {
-            float x[NT][4][4];
             uint32_t bp[NT][4][2];
             const int i = 2 * t, k = 2 * t0 + i;  // pieces: of these tiles, of all
             warp_await(&full[k % kStages], (k / kStages) & 1, &bar->stop, p.status);
+            const float tk = kScale * __shfl_sync(0xffffffffu, sk, t), tv = __shfl_sync(0xffffffffu, sv, t), lsv = log2f(tv), inv = 1.f / tv;
+            float x[NT][4][4];
             key_tile<E4M3, NT>(q, ring + k % kStages * kPiece, x, lane);
             __syncwarp();
             if (i + kStages < 2 * m) bring(i + kStages);
-            const float tk = kScale * __shfl_sync(0xffffffffu, sk, t), tv = __shfl_sync(0xffffffffu, sv, t), lsv = log2f(tv), inv = 1.f / tv;
 #pragma unroll
             for (int y = 0; y < NT; y++) weights<4, NT>(st, y, x[y], tk, lsv, inv, bp[y]);
             warp_await(&full[(k + 1) % kStages], ((k + 1) / kStages) & 1, &bar->stop, p.status);
@@ -389,65 +392,79 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) block_decode_kernel
             if (i + 1 + kStages < 2 * m) bring(i + 1 + kStages);
         }
     }
-    // the warps' states, joined in warp order, a tile of 8 rows at a time
-    float(*s_o)[8][128] = reinterpret_cast<float(*)[8][128]>(sm);
-    float(*s_m)[8] = reinterpret_cast<float(*)[8]>(sm + kWarps * 8 * 128 * 4), (*s_l)[8] = s_m + kWarps;
+    // the warps' states, joined in warp order: 8 NT rows of 128 channels each, in the rings
+    constexpr int kRows = 8 * NT;
+    float(*s_o)[kRows][128] = reinterpret_cast<float(*)[kRows][128]>(sm);
+    float(*s_m)[kRows] = reinterpret_cast<float(*)[kRows]>(sm + kRingBytes + (NT > 1 ? NT * 2048 : 0)), (*s_l)[kRows] = s_m + kWarps;
+    __syncthreads();  // every piece has arrived and been read
 #pragma unroll
-    for (int t = 0; t < NT; t++) {
-        __syncthreads();  // every piece has arrived and been read; the rows before are written
-        if (8 * t >= rows) break;
+    for (int t = 0; t < NT; t++)
 #pragma unroll
         for (int e = 0; e < 2; e++) {
+            const int y = 8 * t + 2 * c + e;
 #pragma unroll
             for (int o = 4; o < 32; o <<= 1) st.l[t][e] += __shfl_xor_sync(0xffffffffu, st.l[t][e], o);
             if (r == 0) {
-                s_m[w][2 * c + e] = st.m[t][e];
-                s_l[w][2 * c + e] = st.l[t][e];
+                s_m[w][y] = st.m[t][e];
+                s_l[w][y] = st.l[t][e];
             }
 #pragma unroll
             for (int i = 0; i < 8; i++) {
-                s_o[w][2 * c + e][out_channel(i, r, 0)] = st.o[t][i][e];
-                s_o[w][2 * c + e][out_channel(i, r, 1)] = st.o[t][i][2 + e];
+                s_o[w][y][out_channel(i, r, 0)] = st.o[t][i][e];
+                s_o[w][y][out_channel(i, r, 1)] = st.o[t][i][2 + e];
             }
         }
-        __syncthreads();
-        const int odd = *(volatile int *)&bar->odd;
-        for (int i = threadIdx.x; i < 128 * min(8, rows - 8 * t); i += kThreads) {
-            const int e = i >> 7, d = i & 127, y = 8 * t + e;
-            float m = s_m[0][e], l = 0.f, o = 0.f;
+    __syncthreads();
+    const int odd = *(volatile int *)&bar->odd;
+#pragma unroll 2
+    for (int y = w; y < rows; y += kWarps) {  // a warp per row, four channels a lane
+        float m = s_m[0][y], l = 0.f;
 #pragma unroll
-            for (int i = 1; i < kWarps; i++) m = fmaxf(m, s_m[i][e]);
+        for (int i = 1; i < kWarps; i++) m = fmaxf(m, s_m[i][y]);
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-            for (int i = 0; i < kWarps; i++) {
-                const float f = factor(s_m[i][e], m);
-                l = fmaf(f, s_l[i][e], l);
-                o = fmaf(f, s_o[i][e][d], o);
+        for (int i = 0; i < kWarps; i++) {
+            const float f = factor(s_m[i][y], m);
+            const float4 v = reinterpret_cast<const float4 *>(s_o[i][y])[lane];
+            l = fmaf(f, s_l[i][y], l);
+            o.x = fmaf(f, v.x, o.x), o.y = fmaf(f, v.y, o.y), o.z = fmaf(f, v.z, o.z), o.w = fmaf(f, v.w, o.w);
+        }
+        const int tok = y / p.g;
+        if (odd) {  // infinite and NaN values of the part's fp16 tokens
+            const int to = min(sl.n_new ? sl.ns + sl.nr + tok + 1 : seen, (end - np) * kTailTokens);
+            for (int x = max(begin - np, 0) * kTailTokens; x < to; x++) {
+                const uint2 v = reinterpret_cast<const uint2 *>(tail_at(p, sl, u, h, x, true))[lane];
+                const float2 v0 = unpack_half2(v.x), v1 = unpack_half2(v.y);
+                if (!isfinite(v0.x)) o.x += v0.x;
+                if (!isfinite(v0.y)) o.y += v0.y;
+                if (!isfinite(v1.x)) o.z += v1.x;
+                if (!isfinite(v1.y)) o.w += v1.y;
             }
-            if (odd) {  // infinite and NaN values of the part's fp16 tokens
-                const int to = min(sl.n_new ? sl.ns + sl.nr + y / p.g + 1 : seen, (end - np) * kTailTokens);
-                for (int x = max(begin - np, 0) * kTailTokens; x < to; x++) {
-                    const float f = h2f(tail_at(p, sl, u, h, x, true)[d]);
-                    if (!isfinite(f)) o += f;
-                }
-            }
-            if (parts == 1) {
-                p.out[((sl.q0 + y / p.g) * p.H_kv * p.g + h * p.g + y % p.g) * 128 + d] = __half_as_ushort(__float2half_rn(o / l));
-            } else {
-                const size_t at = ((size_t)blockIdx.y * p.H_kv + h) * p.most_rows + y;
-                p.part_o[at * 128 + d] = o;
-                if (d == 0) p.part_ml[at] = make_float2(m, l);
-            }
+        }
+        if (parts == 1) {
+            const float inv = 1.f / l;
+            uint16_t *dst = p.out + ((sl.q0 + tok) * p.H_kv * p.g + h * p.g + y - tok * p.g) * 128;
+            reinterpret_cast<uint2 *>(dst)[lane] = make_uint2(pack_half2(o.x * inv, o.y * inv), pack_half2(o.z * inv, o.w * inv));
+        } else {
+            const size_t at = ((size_t)blockIdx.y * p.H_kv + h) * p.most_rows + y;
+            reinterpret_cast<float4 *>(p.part_o + at * 128)[lane] = o;
+            if (lane == 0) p.part_ml[at] = make_float2(m, l);
         }
     }
 }
 
-// Slots in several parts: a CTA per (row of a key head, key head, slot), its eight warps every
-// eighth part each, four at a time; then the warps' states in warp order.
+// Slots in several parts: WARPS warps (1 or 8) per row of a key head, every WARPS-th part each, four
+// at a time; then the warps' states in warp order.  Eight for slots in many parts (one slot of 131K
+// tokens in 57: 22 us with one after the other, 5 with eight), one for a few (drafts over 8 slots in
+// 38 parts together: XX).
 constexpr int kJoinWarps = 8;
+template <int WARPS>
 __global__ void __launch_bounds__(32 * kJoinWarps) block_combine_kernel(const __grid_constant__ BlockDecodeParams p) {
     __shared__ float4 s_o[kJoinWarps][32];
     __shared__ float2 s_ml[kJoinWarps];
-    const int y = blockIdx.x % p.most_rows, h = blockIdx.x / p.most_rows, at_slot = blockIdx.y, w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int w = WARPS == 1 ? 0 : threadIdx.x >> 5, lane = threadIdx.x & 31, at_slot = blockIdx.y;
+    const int x = WARPS == 1 ? blockIdx.x * kJoinWarps + (threadIdx.x >> 5) : blockIdx.x, y = x % p.most_rows, h = x / p.most_rows;
+    if (h >= p.H_kv) return;
     const int first = p.part0[at_slot], parts = p.part0[at_slot + 1] - first, b = p.slot[at_slot];
     if (parts < 2) return;
     griddep_wait();
@@ -465,24 +482,26 @@ __global__ void __launch_bounds__(32 * kJoinWarps) block_combine_kernel(const __
         o.z = fmaf(f0, o.z, f1 * x.z);
         o.w = fmaf(f0, o.w, f1 * x.w);
     };
-    for (int i0 = w; i0 < parts; i0 += 4 * kJoinWarps) {
+    for (int i0 = w; i0 < parts; i0 += 4 * WARPS) {
         float2 ml[4];
-        float4 x[4];
+        float4 v[4];
 #pragma unroll
         for (int k = 0; k < 4; k++) {
-            const size_t z = at + min(i0 + k * kJoinWarps, parts - 1) * step;
+            const size_t z = at + min(i0 + k * WARPS, parts - 1) * step;
             ml[k] = p.part_ml[z];
-            x[k] = reinterpret_cast<const float4 *>(p.part_o + z * 128)[lane];
+            v[k] = reinterpret_cast<const float4 *>(p.part_o + z * 128)[lane];
         }
 #pragma unroll
         for (int k = 0; k < 4; k++)
-            if (i0 + k * kJoinWarps < parts) join(ml[k], x[k]);
+            if (i0 + k * WARPS < parts) join(ml[k], v[k]);
     }
-    s_o[w][lane] = o;
-    if (lane == 0) s_ml[w] = make_float2(m, l);
-    __syncthreads();
-    if (w) return;
-    for (int i = 1; i < min(kJoinWarps, parts); i++) join(s_ml[i], s_o[i][lane]);
+    if (WARPS > 1) {
+        s_o[w][lane] = o;
+        if (lane == 0) s_ml[w] = make_float2(m, l);
+        __syncthreads();
+        if (w) return;
+        for (int i = 1; i < min(WARPS, parts); i++) join(s_ml[i], s_o[i][lane]);
+    }
     const float inv = 1.f / l;
     uint16_t *dst = p.out + ((sl.q0 + y / p.g) * p.H_kv * p.g + h * p.g + y % p.g) * 128;
     reinterpret_cast<uint2 *>(dst)[lane] = make_uint2(pack_half2(o.x * inv, o.y * inv), pack_half2(o.z * inv, o.w * inv));
@@ -552,7 +571,10 @@ cudaError_t run(const kvq_config *c, const int *items, BlockDecodeParams &p, cud
     };
     const cudaError_t e = c->mode == KVQ_MODE_E4M3 ? go(std::true_type()) : go(std::false_type());
     if (e != cudaSuccess || !cut) return e;
-    return launch_dependent(block_combine_kernel, dim3((unsigned)(p.most_rows * c->H_kv), (unsigned)cut), 32 * kJoinWarps, 0, st, p);
+    const int64_t joined = (int64_t)p.most_rows * c->H_kv;
+    if (p.part0[1] > kJoinWarps)  // the longest slot's parts
+        return launch_dependent(block_combine_kernel<kJoinWarps>, dim3((unsigned)joined, (unsigned)cut), 32 * kJoinWarps, 0, st, p);
+    return launch_dependent(block_combine_kernel<1>, dim3((unsigned)host::cdiv(joined, kJoinWarps), (unsigned)cut), 32 * kJoinWarps, 0, st, p);
 }
 
 // What both calls read of the cache.
