@@ -879,7 +879,8 @@ class KVQPagedCache:
     def decode_attn(self, q, out=None):
         """Attention of one query token per active slot over its cached tokens
         (kvq_paged_decode_attn).  q, out: float16 [B, H_q, D], contiguous; rows of empty slots are
-        not written (zeros where out is made here)."""
+        not written (zeros where out is made here).  The cache's workspace serves one call at a
+        time: calls on streams that may overlap, or replays of captured ones, must be ordered."""
         cfg, dev = self.cfg, self._dev
         shape = (cfg.B, cfg.H_q, cfg.D)
         if out is None:
@@ -906,14 +907,14 @@ class KVQPagedCache:
         P, H, D, G = self.n_pages, cfg.H_kv, cfg.D, cfg.G
         kfpi, vfpi, Gv = 32 // cfg.bits, 32 // (cfg.v_bits or cfg.bits), min(G, D)
         b = self.buf[name]
-        if cfg.mode in (KVQ_MODE_E4M3, KVQ_MODE_INT8) and P > 0:
+        if cfg.mode in (KVQ_MODE_E4M3, KVQ_MODE_INT8):
             code = torch.float8_e4m3fn if cfg.mode == KVQ_MODE_E4M3 else torch.int8
             if name == "k_codes":  # 16-byte chunk j of row t at position j ^ (4 * (t mod 2))
-                return b.view(code).view(P, H, G, D)
+                return b[: P * H * G * D].view(code).view(P, H, G, D)
             if name == "v_codes":
-                return b.view(code).view(P, H, G // 64, D, 64)
+                return b[: P * H * G * D].view(code).view(P, H, G // 64, D, 64)
             if name in ("k_meta", "v_meta"):  # the scales
-                return b.view(torch.float32).view(P, H, 4)[..., 0]
+                return b[: P * H * 16].view(torch.float32).view(P, H, 4)[..., 0]
         if name == "k_codes":
             return b.view(torch.int32).view(P, H, G // kfpi, D)
         if name == "k_meta":

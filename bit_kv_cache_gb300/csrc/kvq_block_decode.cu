@@ -455,8 +455,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) block_decode_kernel
 
 // Slots in several parts: WARPS warps (1 or 8) per row of a key head, every WARPS-th part each, four
 // at a time; then the warps' states in warp order.  Eight for slots in many parts (one slot of 131K
-// tokens in 57: 22 us with one after the other, 5 with eight), one for a few (drafts over 8 slots in
-// 38 parts together: XX).
+// tokens in 57, cold: 22 us with a CTA per row and one part after the other), one for at most eight.
 constexpr int kJoinWarps = 8;
 template <int WARPS>
 __global__ void __launch_bounds__(32 * kJoinWarps) block_combine_kernel(const __grid_constant__ BlockDecodeParams p) {

@@ -84,7 +84,8 @@ enum { KVQ_DEV_TIMEOUT = 1, KVQ_DEV_BAD_STATE = 2 };
  *                     groups once full.  Kitty: the value local window.
  *   n_boost         : Kitty: key channels per page kept at INT4 (0..min(D,254)).
  *                     Must be 0 in KIVI mode.
- *   mode            : KVQ_MODE_KIVI, KVQ_MODE_KITTY or KVQ_MODE_NVFP4 (below)
+ *   mode            : KVQ_MODE_KIVI, KVQ_MODE_KITTY or KVQ_MODE_NVFP4 (below); paged
+ *                     caches also KVQ_MODE_E4M3 and KVQ_MODE_INT8 (kvq_paged)
  *   max_T           : packed-token capacity per sequence, a multiple of G
  *   rope            : 0: keys are attended as stored.  1: keys are stored before
  *                     the rotary position embedding and decode attention rotates
@@ -177,7 +178,9 @@ const char *kvq_status_str(int status);
  * D % fpi, Gv | D, R % G (KIVI), n_boost range, max_T % G, non-positive sizes) or
  * KVQ_ERR_UNSUPPORTED (bits or v_bits not 2/4/8, Kitty with bits != 2, D not 64,
  * 128 or 256, more than 8 query heads per KV head, rope with Kitty; rope not 0/1 or
- * a negative or non-finite rope_base is KVQ_ERR_INVALID_ARG). */
+ * a negative or non-finite rope_base is KVQ_ERR_INVALID_ARG).  KVQ_ERR_UNSUPPORTED for
+ * KVQ_MODE_E4M3 and KVQ_MODE_INT8, which only the kvq_paged_ calls know: kvq_paged_bytes
+ * is 0 for what they do not support. */
 int kvq_config_check(const kvq_config *cfg);
 
 /* Byte size of each cache buffer for cfg: which = 0 k_codes, 1 k_hi, 2 k_bidx,
@@ -371,7 +374,19 @@ int kvq_decode_attn_noalloc(const kvq_config *cfg, const kvq_cache *cache, const
  * them and calls kvq_paged_init once.  Sequence b's logical tokens are
  * [sink | packed pages | residual].
  * Supported: KIVI mode, any widths, D = 128, H_q/H_kv <= 4, G a multiple of the tile
- * (256/bits tokens) and a power of two, B <= KVQ_PAGED_MAX_B, rope = 0.
+ * (256/bits tokens) and a power of two, B <= KVQ_PAGED_MAX_B, rope = 0; or one of
+ *   KVQ_MODE_E4M3, KVQ_MODE_INT8: bits = 8 (v_bits 0 or 8), D = 128, H_q/H_kv <= 8,
+ * G 64, 128 or 256, R a multiple of G, n_boost = rope = 0.  Keys and values of a page and
+ * head are then codes of that type (e4m3: 8-bit floats of 4 exponent and 3 mantissa bits,
+ * up to 448; int8: -127 .. 127) with one scale each:
+ *   scale = amax / M,  code = x * (M / amax) rounded to nearest even,  M = 448 or 127,
+ * in fp32 IEEE operations; scale 1 and codes 0 where all is 0.  A page with an infinite or
+ * NaN value has an infinite or NaN scale and counts as NaN throughout.
+ *   k_codes  [n_pages][H_kv][G][D] bytes: 16-byte chunk j of token t at position
+ *            j ^ (4 * (t mod 2)) of its row (reads of two rows use all banks)
+ *   v_codes  [n_pages][H_kv][G/64][D][64] bytes: 64 tokens of a channel are contiguous
+ *   k_meta, v_meta  [n_pages][H_kv] records of 16 bytes, an fp32 scale and padding
+ * The other buffers, the calls and their order are those of KIVI mode.
  * --------------------------------------------------------------------------------- */
 #define KVQ_PAGED_MAX_B 512
 
@@ -425,11 +440,17 @@ int kvq_paged_flush(const kvq_config *cfg, kvq_paged *pc, int *n_flushed, void *
 /* Empties batch slot b (its pages may then be reused by the caller). */
 int kvq_paged_release(const kvq_config *cfg, kvq_paged *pc, int b, void *stream);
 
-/* Workspace bytes kvq_paged_decode_attn needs (zero-filled once, kvq_workspace_init). */
+/* Workspace bytes kvq_paged_decode_attn needs (zero-filled once, kvq_workspace_init).  Calls
+ * that may overlap, replays of captured ones among them, need a workspace each. */
 size_t kvq_paged_workspace_bytes(const kvq_config *cfg);
 
 /* Decode attention, as kvq_decode_attn, for every active sequence over its own
- * length: q, out device fp16 [B][H_q][D]; rows of empty slots are not written. */
+ * length: q, out device fp16 [B][H_q][D]; rows of empty slots are not written.
+ * KVQ_MODE_E4M3, KVQ_MODE_INT8: codes are exact fp16 operands, the scales enter the softmax;
+ * only its weights (fp16) and the output are rounded, sums are fp32: an output is off by 2.3e-4
+ * to 2.9e-4 of its size, of which 2e-4 is its own rounding.  Infinite and NaN values of fp16
+ * tokens reach the output as they are.  The call may be captured: a replay attends over the
+ * lengths that the cache then has, for the slots that held tokens at the capture. */
 int kvq_paged_decode_attn(const kvq_config *cfg, const kvq_paged *pc, const uint16_t *q,
                           uint16_t *out, void *ws, size_t ws_bytes, void *stream);
 
@@ -502,7 +523,8 @@ size_t kvq_paged_chunk_workspace_bytes(const kvq_config *cfg);
  * softmax statistics fp32: an output is off by 3e-4 to 6e-4 of its size, of which 2e-4 is
  * its own rounding (kvq_paged_decode_attn: 4.1e-4 to 4.3e-4 where this call is off by 3.5e-4
  * to 4.0e-4).  For one token per slot that call is the faster one (eight slots of 17K to 56K
- * tokens: 71 us against 139).
+ * tokens: 71 us against 139).  KVQ_MODE_E4M3, KVQ_MODE_INT8: codes are exact operands, as in
+ * kvq_paged_decode_attn, and an output is off by 2.4e-4 to 2.9e-4 of its size.
  * Infinite and NaN values reach the rows that see them and no others.  A packed key or value
  * that rounds beyond fp16's largest when dequantized counts as one of them: the rows of its
  * slot become infinite or NaN.  A page-table entry that is no page is reported
