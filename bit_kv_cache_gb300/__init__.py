@@ -163,9 +163,14 @@ def _stream_of(index):
     return torch._C._cuda_getCurrentRawStream(index)
 
 
+def _index(device):
+    """A device as Tensor.get_device() names it."""
+    return -1 if device.index is None else device.index
+
+
 def _rows(t, heads, D, n, device, what):
     """(address, row stride) of token-major rows [>= n][heads][D], float16, heads adjacent."""
-    if t.get_device() != device.index or t.dtype is not _float16():
+    if t.get_device() != _index(device) or t.dtype is not _float16():
         raise ValueError("%s must be a float16 tensor on %s" % (what, device))
     if t.dim() != 3:
         raise ValueError("%s has shape %s, expected at least [%d, %d, %d]" % (what, tuple(t.shape), n, heads, D))
@@ -181,7 +186,7 @@ def _weight(w, D, device, what):
     """Address of a norm's weights (None: no norm)."""
     if w is None:
         return None
-    if w.get_device() != device.index or w.dtype is not _float16() or w.dim() != 1 or w.numel() != D or not w.is_contiguous():
+    if w.get_device() != _index(device) or w.dtype is not _float16() or w.dim() != 1 or w.numel() != D or not w.is_contiguous():
         raise ValueError("%s must be a contiguous float16 tensor [%d] on %s" % (what, D, device))
     return w.data_ptr()
 
@@ -886,7 +891,7 @@ class KVQPagedCache:
         if out is None:
             out = self.torch.zeros_like(q)
         for t, what in ((q, "q"), (out, "out")):
-            if t.get_device() != dev.index or t.dtype is not _float16() or not t.is_contiguous():
+            if t.get_device() != _index(dev) or t.dtype is not _float16() or not t.is_contiguous():
                 raise ValueError("%s must be a contiguous float16 tensor on %s" % (what, dev))
             if t.shape != shape:
                 raise ValueError("%s has shape %s, expected %s" % (what, tuple(t.shape), shape))
