@@ -33,10 +33,12 @@ __device__ __forceinline__ int64_t page_of(const PackParams &p, int entry, int h
 template <int G>
 constexpr int kCtas = G == 64 ? 8 : G == 128 ? 5 : 3;
 
-// Page blockIdx.x of a planned chunk, or, behind them, a slot's fp16 rows.
+// Pages of a planned chunk, then the slots' fp16 rows.  CTA i: head i % H of one side of page (slot)
+// i / (2 H): the heads of a token are neighbours in memory, and are read at about the same time
+// (pages next to each other first: four long prompts 55 us against 53).
 template <bool E4M3, int G>
 __global__ void __launch_bounds__(256, kCtas<G>) block_extend_kernel(const __grid_constant__ BlockExtendParams p) {
-    const int h = blockIdx.y, side = blockIdx.z, i = blockIdx.x;
+    const int x = blockIdx.x / p.H_kv, h = blockIdx.x - x * p.H_kv, side = x & 1, i = x >> 1;
     griddep_wait();
     if (i >= p.n_pack) {
         extend_slot(p, i - p.n_pack, h, side, 0, 1);
@@ -97,7 +99,9 @@ cudaError_t launch_block_extend(const ExtendParams &x, const ChunkSlot *slots, b
         p.row0[b] = slots[b].cu + slots[b].to_sink - slots[b].nr;
         p.lp0[b] = slots[b].T / x.G;
     }
-    const dim3 grid((unsigned)(p.n_pack + p.B), (unsigned)p.H_kv, 2);
+    const int64_t ctas = ((int64_t)p.n_pack + p.B) * 2 * p.H_kv;
+    if (ctas > INT32_MAX) return cudaErrorInvalidConfiguration;
+    const dim3 grid((unsigned)ctas);
     return by_form(p.G, e4m3, [&](auto form, auto g) {
         return launch_dependent(block_extend_kernel<decltype(form)::value, decltype(g)::value>, grid, 256, 0, st, p);
     });
