@@ -56,6 +56,9 @@ __device__ __forceinline__ __half2 max_abs2(__half2 m, uint32_t x) { return __hm
 // all there, the common case, which has loads of its own: one addition for an address); page(): the
 // page's index, asked for once the rows are in registers (-1: nothing is stored).  A page that holds
 // an infinity or NaN gets an infinite or NaN scale, so that all its values count as NaN.
+// Bound by the latency of its loads: half the stalls of a warp wait for them at 50% of the memory's
+// rate, with every register of the SM in use.  Tried and dropped: persistent CTAs that load a page
+// while they pack the one before (72 us against 55 on four long prompts: fewer loads on their way).
 // Keys: thread (tid / 16, tid % 16) holds 8 channels of every 16th row, so that loads and stores
 // are whole rows.  Values are stored with tokens contiguous: a thread holds four neighbouring
 // tokens of 8 channels and turns their bytes in registers (16 lanes store 64 contiguous bytes; no
