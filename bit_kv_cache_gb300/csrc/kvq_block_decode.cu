@@ -350,6 +350,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) block_decode_kernel
     const int tiles = begin + w < min(end, np) ? (min(end, np) - begin - w + kWarps - 1) / kWarps : 0;
     unsigned char *ring = sm + w * kStages * kPiece;
     uint64_t *full = bar->full[w];
+    int brought = 0;  // pieces
     for (int t0 = 0; t0 == 0 || t0 < tiles; t0 += 32) {
         const int m = min(32, tiles - t0);
         size_t at = 0;
@@ -368,6 +369,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) block_decode_kernel
         }
         auto bring = [&](int i) {  // piece i of these tiles
             const size_t from = __shfl_sync(0xffffffffu, at, i >> 1);
+            if (*(volatile int *)&bar->stop) return;  // a wait ran out: nothing more is asked for
+            brought = 2 * t0 + i + 1;
             if (lane) return;
             const int stage = (2 * t0 + i) % kStages;
             mbar_arrive_expect_tx(&full[stage], kPiece);
@@ -403,6 +406,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) block_decode_kernel
             if (i + 1 + kStages < 2 * m) bring(i + 1 + kStages);
         }
     }
+    // where a wait ran out, the copies on their way land (or are waited for once more) before the block ends
+    if (*(volatile int *)&bar->stop)
+        for (int k = max(brought - kStages, 0); k < brought; k++) mbar_wait(&full[k % kStages], (k / kStages) & 1, p.status);
     // the warps' states, joined in warp order: 8 NT rows of 128 channels each, in the rings
     constexpr int kRows = 8 * NT;
     float(*s_o)[kRows][128] = reinterpret_cast<float(*)[kRows][128]>(sm);

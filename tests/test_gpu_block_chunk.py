@@ -306,3 +306,87 @@ def test_captured_calls_and_streams():
     with torch.cuda.stream(s):
         assert torch.equal(c.decode_attn(qd), wantd)
     assert c.read_status() == 0
+
+
+@pytest.mark.parametrize("mode", MODES)
+def test_replay_after_growth(mode):
+    """A captured decode attends over the lengths of its replay, also behind a page boundary and
+    with a slot that has become empty."""
+    rng = np.random.default_rng(15)
+    c = make_cache(rng, [3000, 60, 200, 1], mode, H_kv=1, H_q=4, S=2)
+    q, out = randn(rng, 4, 4, D), torch.zeros(4, 4, D, dtype=torch.float16, device=DEV)
+    c.decode_attn(q, out=out)
+    torch.cuda.synchronize()
+    s, g = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        c.decode_attn(q, out=out)
+    for n in (1, 70, 130):
+        new = [n, n, 0, n]
+        x = randn(rng, 3 * n, 2, D)
+        c.extend(c.plan(new), x[:, :1], x[:, 1:])
+        if n == 70:
+            c.release(2)
+        out.fill_(7.0)
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        for b in (0, 1, 2, 3):
+            if not c.lengths(b)["active"]:
+                assert torch.all(out[b] == 7.0)
+                continue
+            K, V = cached_rows(c, b)
+            ref, size, mag = softmax_rows(q[b].cpu().double().numpy(), K[0], V[0])
+            assert np.all(np.abs(out[b].cpu().double().numpy() - ref) <= bound_of(ref, size, mag)), (n, b)
+    assert c.read_status() == 0
+
+
+def test_pages_beyond_4_gb():
+    """Pages whose codes lie more than 2^32 bytes behind the pool's start, in every call."""
+    import bit_kv_cache_gb300 as kvq
+    rng = np.random.default_rng(16)
+    n_pages = 36000  # 131072 bytes a side each
+    c = kvq.KVQPagedCache(2, 16, 8, D, 128, 8, n_pages=n_pages, max_T=4096, device=DEV, mode="e4m3")
+    c.free = list(range(n_pages - 40, n_pages))
+    k, v = randn(rng, 8, 700, D), randn(rng, 8, 700, D)
+    c.prefill(0, k, v)
+    x = randn(rng, 380, 32, D)
+    ch = c.plan([300, 80])
+    out = c.chunk_attn(ch, x[:, :16], x[:, 16:24], x[:, 24:])
+    attn_check(c, [300, 80], x[:, :16], x[:, 16:24], x[:, 24:], out)
+    c.extend(ch, x[:, 16:24], x[:, 24:])
+    for _ in range(30):
+        y = randn(rng, 2, 32, D)
+        q = c.append_rope(y[:, :16], y[:, 16:24], y[:, 24:])
+    assert int(c.table[0, : c.lengths(0)["T"] // 128].min()) >= n_pages - 40
+    ch = c.plan([2, 1])
+    few = c.chunk_attn(ch, x[:3, :16], x[:3, 16:24], x[:3, 24:])
+    attn_check(c, [2, 1], x[:3, :16], x[:3, 16:24], x[:3, 24:], few)
+    out = c.decode_attn(q)
+    for b in range(2):
+        K, V = cached_rows(c, b)
+        for h in range(8):
+            ref, size, mag = softmax_rows(q[b, 2 * h: 2 * h + 2].cpu().double().numpy(), K[h], V[h])
+            assert np.all(np.abs(out[b, 2 * h: 2 * h + 2].cpu().double().numpy() - ref) <= bound_of(ref, size, mag))
+    assert c.read_status() == 0
+
+
+def test_calls_on_a_stream_of_their_own():
+    """Every call on a side stream, ordered by events alone."""
+    import bit_kv_cache_gb300 as kvq
+    rng = np.random.default_rng(17)
+    a, b = (make_cache(np.random.default_rng(18), [300, 64], "int8") for _ in range(2))
+    x = randn(rng, 70, 12, D)
+    y = randn(rng, 2, 12, D)
+    s = torch.cuda.Stream()
+    res = []
+    for c, st in ((a, torch.cuda.current_stream()), (b, s)):
+        st.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(st):
+            out, _ = c.chunk_step([65, 5], x[:, :8], x[:, 8:10], x[:, 10:])
+            q = c.append_rope(y[:, :8], y[:, 8:10], y[:, 10:])
+            res.append((out, q, c.decode_attn(q)))
+            c.flush()
+    torch.cuda.synchronize()
+    assert all(torch.equal(i, j) for i, j in zip(*res)) and torch.equal(a.lens, b.lens)
+    for name in a.buf:
+        assert torch.equal(a.buf[name], b.buf[name]), name
