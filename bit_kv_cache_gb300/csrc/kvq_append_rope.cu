@@ -4,12 +4,12 @@
 // One launch does what kvq_paged_flush, kvq_qk_norm_rope and kvq_paged_append do.  The CTAs of a
 // page come first: each packs one side of a page of a full residual; the one that holds the
 // residual's first row then writes the new token's row there, which no other CTA reads.  Behind
-// them come the slots' own CTAs, with 16 heads each: 16 lanes hold a head's row, both channels of a
+// them come the slots' own CTAs: 16 lanes hold a head's row, both channels of a
 // pair in one thread, so that a row needs one reduction and no exchange; sines and cosines are
 // formed once per CTA, while the rows arrive.  Positions and destinations come as a parameter, from
 // the host's lengths: no CTA reads the lengths that another one advances.
 // What bounds it.  Few slots: the host call (8 slots: 9.6 us through the binding, 4.6 of them in the
-// C call; the kernel takes 4.4).  256 slots whose residuals are all full (208 MB): 44 us, 4.7 TB/s;
+// C call; the kernel takes 4.4).  256 slots whose residuals are all full (208 MB): 43 us, 4.8 TB/s;
 // the CTAs of the pages spend most of their time in the latency of their loads (kvq_block.cuh).
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -29,7 +29,8 @@ namespace kvq {
 namespace {
 
 constexpr int kMaxPages = 1024;          // packed by one launch
-constexpr int kThreads = 256, kRowsPerPass = kThreads / 16;
+template <int FORM, int G>
+constexpr int kThreads = FORM ? 4 * G : 256;  // a page's CTA; slots' rows by as many
 constexpr int32_t kToSink = 1 << 30, kFull = 1 << 29, kNone = -1;
 
 struct AppendRopeParams : PackParams {
@@ -53,7 +54,7 @@ struct AppendRopeParams : PackParams {
 
 // Cosine and sine of every pair at a position, times amp.
 __device__ __forceinline__ void angles(const AppendRopeParams &p, int64_t pos, float2 *cs) {
-    for (int j = threadIdx.x; j < p.rotary >> 1; j += kThreads) {
+    for (int j = threadIdx.x; j < p.rotary >> 1; j += blockDim.x) {
         const uint64_t a = (uint64_t)pos * p.turn[j];
         float s, c;
         sincospif((float)(int32_t)(a >> 32) * 0x1p-31f, &s, &c);
@@ -128,10 +129,10 @@ __device__ __forceinline__ void copy_row(const uint16_t *src, uint16_t *dst) {
     reinterpret_cast<uint4 *>(dst)[threadIdx.x & 15] = reinterpret_cast<const uint4 *>(src)[threadIdx.x & 15];
 }
 
-// Sixteen of a slot's heads: queries, keys, values.
+// Part `part` of a slot's heads, queries, keys, values, by 16 threads each.
 __device__ __forceinline__ void slot_rows(const AppendRopeParams &p, int b, int part, float2 *cs) {
     const int dst = p.dst[b], row = dst & (kFull - 1), heads = p.H_q + 2 * p.H_kv;
-    const int i = part * kRowsPerPass + (threadIdx.x >> 4), kind = i < p.H_q ? 0 : i < p.H_q + p.H_kv ? 1 : 2, h = kind ? i - p.H_q - (kind - 1) * p.H_kv : i;
+    const int i = part * (blockDim.x >> 4) + (threadIdx.x >> 4), kind = i < p.H_q ? 0 : i < p.H_q + p.H_kv ? 1 : 2, h = kind ? i - p.H_q - (kind - 1) * p.H_kv : i;
     const uint16_t *src = nullptr;
     uint16_t *to = nullptr;
     if (kind == 0) {
@@ -162,7 +163,7 @@ __device__ __forceinline__ void slot_rows(const AppendRopeParams &p, int b, int 
 
 // FORM: 0 min-max codes, 1 e4m3, 2 int8; G tokens a page.
 template <int FORM, int G>
-__global__ void __launch_bounds__(kThreads, FORM == 0 ? (G == 256 ? 2 : 4) : G == 64 ? 8 : G == 128 ? 5 : 3) append_rope_kernel(const __grid_constant__ AppendRopeParams p) {
+__global__ void __launch_bounds__(kThreads<FORM, G>, FORM == 0 ? (G == 256 ? 2 : 4) : kPackCtas<G>) append_rope_kernel(const __grid_constant__ AppendRopeParams p) {
     __shared__ __align__(16) unsigned char smem[FORM ? 16 : 32 * 512 + 512];
     __shared__ float2 s_cs[64];
     griddep_wait();
@@ -209,15 +210,20 @@ __global__ void __launch_bounds__(kThreads, FORM == 0 ? (G == 256 ? 2 : 4) : G =
         copy_row(p.v_new + b * p.v_stride + h * 128, p.v_res + u * p.R * 128);
 }
 
-cudaError_t launch_append_rope(const AppendRopeParams &p, int form, cudaStream_t st) {
-    const dim3 grid((unsigned)((int64_t)p.n_pack * p.H_kv * p.sides + (int64_t)p.n_slots * p.parts));
-    auto go = [&](auto kernel) { return launch_dependent(kernel, grid, kThreads, 0, st, p); };
-    if (form == 0) return p.G == 128 ? go(append_rope_kernel<0, 128>) : go(append_rope_kernel<0, 256>);
-    auto pages = [&](auto f) {
-        constexpr int F = decltype(f)::value;
-        return p.G == 64 ? go(append_rope_kernel<F, 64>) : p.G == 128 ? go(append_rope_kernel<F, 128>) : go(append_rope_kernel<F, 256>);
+cudaError_t launch_append_rope(AppendRopeParams &p, int form, cudaStream_t st) {
+    using std::integral_constant;
+    auto go = [&](auto f, auto g) {
+        constexpr int F = decltype(f)::value, G = decltype(g)::value, T = kThreads<F, G>;
+        p.parts = (16 * (p.H_q + 2 * p.H_kv) + T - 1) / T;
+        const dim3 grid((unsigned)((int64_t)p.n_pack * p.H_kv * p.sides + (int64_t)p.n_slots * p.parts));
+        return launch_dependent(append_rope_kernel<F, G>, grid, T, 0, st, p);
     };
-    return form == 1 ? pages(std::integral_constant<int, 1>()) : pages(std::integral_constant<int, 2>());
+    auto pages = [&](auto f) {
+        return p.G == 64 ? go(f, integral_constant<int, 64>()) : p.G == 128 ? go(f, integral_constant<int, 128>()) : go(f, integral_constant<int, 256>());
+    };
+    if (form) return form == 1 ? pages(integral_constant<int, 1>()) : pages(integral_constant<int, 2>());
+    const integral_constant<int, 0> f;
+    return p.G == 128 ? go(f, integral_constant<int, 128>()) : go(f, integral_constant<int, 256>());
 }
 
 }  // namespace
@@ -305,7 +311,6 @@ extern "C" int kvq_paged_append_rope(const kvq_config *c, kvq_paged *pc, const k
     p.per = per;
     p.sides = block8(c) ? 2 : 1 + c->G / 128;
     p.map = new_pages != nullptr;
-    p.parts = (c->H_q + 2 * c->H_kv + kRowsPerPass - 1) / kRowsPerPass;
     if (qk->rotary_dim && freq) turns_of_freq(freq, qk->rotary_dim, p.turn);
     else if (qk->rotary_dim) turns_of_base(qk->rope_base, qk->rotary_dim, p.turn);
     const int form = c->mode == KVQ_MODE_E4M3 ? 1 : c->mode == KVQ_MODE_INT8 ? 2 : 0;

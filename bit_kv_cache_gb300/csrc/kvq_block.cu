@@ -28,16 +28,11 @@ __device__ __forceinline__ int64_t page_of(const PackParams &p, int entry, int h
     return -1;
 }
 
-// CTAs per SM: as many as the registers of G / 16 loads per thread leave room for (four prompts of
-// 2K to 12K tokens in pages of 64: 62 us with four CTAs, 55 with eight).
-template <int G>
-constexpr int kCtas = G == 64 ? 8 : G == 128 ? 5 : 3;
-
 // Pages of a planned chunk, then the slots' fp16 rows.  CTA i: head i % H of one side of page (slot)
 // i / (2 H): the heads of a token are neighbours in memory, and are read at about the same time
-// (pages next to each other first: four long prompts 55 us against 53).
+// (pages next to each other first: four long prompts 55 us against 53 at 256 threads a CTA).
 template <bool E4M3, int G>
-__global__ void __launch_bounds__(256, kCtas<G>) block_extend_kernel(const __grid_constant__ BlockExtendParams p) {
+__global__ void __launch_bounds__(4 * G, kPackCtas<G>) block_extend_kernel(const __grid_constant__ BlockExtendParams p) {
     const int x = blockIdx.x / p.H_kv, h = blockIdx.x - x * p.H_kv, side = x & 1, i = x >> 1;
     griddep_wait();
     if (i >= p.n_pack) {
@@ -60,12 +55,12 @@ __global__ void __launch_bounds__(256, kCtas<G>) block_extend_kernel(const __gri
     // (the barrier inside the packing) writes the new ones
     if (t0 < p.R) {
         const int4 *d = reinterpret_cast<const int4 *>(p.desc) + 2 * b;
-        keep_rows(p, d[0], d[1], b, h, side, false, true, threadIdx.x, 256, t0, t0 + G);
+        keep_rows(p, d[0], d[1], b, h, side, false, true, threadIdx.x, 4 * G, t0, t0 + G);
     }
 }
 
 template <bool E4M3, int G>
-__global__ void __launch_bounds__(256, kCtas<G>) block_list_kernel(const __grid_constant__ BlockListParams p) {
+__global__ void __launch_bounds__(4 * G, kPackCtas<G>) block_list_kernel(const __grid_constant__ BlockListParams p) {
     const int h = blockIdx.y, side = blockIdx.z, k = blockIdx.x / p.per, j = blockIdx.x - k * p.per, b = p.seq[k];
     griddep_wait();
     const Sides s = sides(p, side);
@@ -103,14 +98,14 @@ cudaError_t launch_block_extend(const ExtendParams &x, const ChunkSlot *slots, b
     if (ctas > INT32_MAX) return cudaErrorInvalidConfiguration;
     const dim3 grid((unsigned)ctas);
     return by_form(p.G, e4m3, [&](auto form, auto g) {
-        return launch_dependent(block_extend_kernel<decltype(form)::value, decltype(g)::value>, grid, 256, 0, st, p);
+        return launch_dependent(block_extend_kernel<decltype(form)::value, decltype(g)::value>, grid, 4 * decltype(g)::value, 0, st, p);
     });
 }
 
 cudaError_t launch_block_list(const BlockListParams &p, bool e4m3, cudaStream_t st) {
     const dim3 grid((unsigned)p.n_pack, (unsigned)p.H_kv, 2);
     return by_form(p.G, e4m3, [&](auto form, auto g) {
-        return launch_dependent(block_list_kernel<decltype(form)::value, decltype(g)::value>, grid, 256, 0, st, p);
+        return launch_dependent(block_list_kernel<decltype(form)::value, decltype(g)::value>, grid, 4 * decltype(g)::value, 0, st, p);
     });
 }
 

@@ -50,37 +50,38 @@ __device__ __forceinline__ uint32_t to_codes(uint32_t x, uint32_t y, uint64_t in
 // The larger magnitudes of two pairs, NaN if one is.
 __device__ __forceinline__ __half2 max_abs2(__half2 m, uint32_t x) { return __hmax2_nan(m, __habs2(*reinterpret_cast<const __half2 *>(&x))); }
 
-// One side of a page of G tokens by a CTA of 256 threads:
+// One side of a page of G tokens by a CTA of 4 G threads:
 //   scale = amax / M, code = rn(x (M / amax)),  M = 448 (e4m3) or 127 (int8); 1 and 0 of zeros.
 // Token t's 128 fp16 channels lie at res + 128 t for t < nr, behind that at src + t stride (nr <= 0:
 // all there, the common case, which has loads of its own: one addition for an address); page(): the
 // page's index, asked for once the rows are in registers (-1: nothing is stored).  A page that holds
 // an infinity or NaN gets an infinite or NaN scale, so that all its values count as NaN.
-// Bound by the latency of its loads: half the stalls of a warp wait for them at 50% of the memory's
-// rate, with every register of the SM in use.  Tried and dropped: persistent CTAs that load a page
-// while they pack the one before (72 us against 55 on four long prompts: fewer loads on their way).
-// Keys: thread (tid / 16, tid % 16) holds 8 channels of every 16th row, so that loads and stores
+// Bound by the latency of its loads: half the stalls of a warp wait for them.  So a thread holds no
+// more than four rows of 8 channels, in 32 registers, and an SM's 2048 threads 128 KB (256 residuals
+// of 128 tokens: 44 us with 256 threads of eight rows, 43 with 512 of four; four long prompts 52.7
+// and 51.8, one short prompt 14.8 and 15.2).  Tried and dropped: persistent CTAs that load a page
+// while they pack the one before (four long prompts 72 us against 55: fewer loads on their way).
+// Keys: thread (tid / 16, tid % 16) holds 8 channels of every G/4-th row, so that loads and stores
 // are whole rows.  Values are stored with tokens contiguous: a thread holds four neighbouring
 // tokens of 8 channels and turns their bytes in registers (16 lanes store 64 contiguous bytes; no
 // staging in shared memory, no second barrier).
 template <bool E4M3, int G, typename Page>
 __device__ __forceinline__ void pack_block(const uint16_t *res, int nr, const uint16_t *src, int64_t stride, Page page, bool value,
                                            uint8_t *codes, float4 *scales) {
-    constexpr int N = G / 16;
-    __shared__ uint32_t s_max[8];
-    const int tid = threadIdx.x, lo = tid & 15, hi = tid >> 4;
-    const int cg = value ? hi : lo;  // eight channels
+    constexpr int N = 4, Q = G / 4, kWarps = G / 8;  // rows of a thread, threads along the tokens
+    __shared__ uint32_t s_max[kWarps];
+    const int tid = threadIdx.x;
+    const int cg = value ? tid / Q : tid & 15;        // eight channels
+    const int first = value ? 4 * (tid % Q) : tid >> 4, step = value ? 1 : Q;
     uint4 x[N];
-    const int first = value ? 4 * lo : hi;  // the thread's rows: first, and from there
-    auto row = [&](int i) { return value ? 64 * (i >> 2) + (i & 3) : 16 * i; };
     if (nr <= 0) {
         const uint16_t *at = src + first * stride + 8 * cg;
 #pragma unroll
-        for (int i = 0; i < N; i++) x[i] = *reinterpret_cast<const uint4 *>(at + row(i) * stride);
+        for (int i = 0; i < N; i++) x[i] = *reinterpret_cast<const uint4 *>(at + i * step * stride);
     } else {
 #pragma unroll
         for (int i = 0; i < N; i++) {
-            const int t = first + row(i);
+            const int t = first + i * step;
             x[i] = *reinterpret_cast<const uint4 *>((t < nr ? res + t * 128 : src + t * stride) + 8 * cg);
         }
     }
@@ -94,8 +95,7 @@ __device__ __forceinline__ void pack_block(const uint16_t *res, int nr, const ui
     __syncthreads();
     const int64_t pg = page();
     if (pg < 0) return;
-#pragma unroll
-    for (int i = 0; i < 8; i++) m = max(m, s_max[i]);
+    m = __reduce_max_sync(0xffffffffu, s_max[tid & (kWarps - 1)]);
     const float amax = h2f((uint16_t)m), top = E4M3 ? 448.f : 127.f;
     const float inv = m ? __fdiv_rn(top, amax) : 0.f;
     const uint64_t inv2 = pk2(inv, inv);
@@ -110,24 +110,24 @@ __device__ __forceinline__ void pack_block(const uint16_t *res, int nr, const ui
     if (!value) {
 #pragma unroll
         for (int i = 0; i < N; i++) {
-            const int t = 16 * i + hi, pos = (cg >> 1) ^ ((t & 1) << 2);
+            const int t = first + i * Q, pos = (cg >> 1) ^ ((t & 1) << 2);
             *reinterpret_cast<uint2 *>(dst + t * 128 + pos * 16 + (cg & 1) * 8) = make_uint2(c[i][0], c[i][1]);
         }
         return;
     }
+    uint8_t *at = dst + (first >> 6) * 8192 + cg * 512 + (first & 63);
 #pragma unroll
-    for (int i = 0; i < N; i += 4) {
-        uint8_t *at = dst + (i >> 2) * 8192 + cg * 512 + 4 * lo;
-#pragma unroll
-        for (int k = 0; k < 2; k++) {  // the bytes of four tokens by four channels, transposed
-            const uint32_t a = prmt(c[i][k], c[i + 1][k], 0x5140), b = prmt(c[i + 2][k], c[i + 3][k], 0x5140);
-            const uint32_t e = prmt(c[i][k], c[i + 1][k], 0x7362), f = prmt(c[i + 2][k], c[i + 3][k], 0x7362);
-            *reinterpret_cast<uint32_t *>(at + (4 * k) * 64) = prmt(a, b, 0x5410);
-            *reinterpret_cast<uint32_t *>(at + (4 * k + 1) * 64) = prmt(a, b, 0x7632);
-            *reinterpret_cast<uint32_t *>(at + (4 * k + 2) * 64) = prmt(e, f, 0x5410);
-            *reinterpret_cast<uint32_t *>(at + (4 * k + 3) * 64) = prmt(e, f, 0x7632);
-        }
+    for (int k = 0; k < 2; k++) {  // the bytes of four tokens by four channels, transposed
+        const uint32_t a = prmt(c[0][k], c[1][k], 0x5140), b = prmt(c[2][k], c[3][k], 0x5140);
+        const uint32_t e = prmt(c[0][k], c[1][k], 0x7362), f = prmt(c[2][k], c[3][k], 0x7362);
+        *reinterpret_cast<uint32_t *>(at + (4 * k) * 64) = prmt(a, b, 0x5410);
+        *reinterpret_cast<uint32_t *>(at + (4 * k + 1) * 64) = prmt(a, b, 0x7632);
+        *reinterpret_cast<uint32_t *>(at + (4 * k + 2) * 64) = prmt(e, f, 0x5410);
+        *reinterpret_cast<uint32_t *>(at + (4 * k + 3) * 64) = prmt(e, f, 0x7632);
     }
 }
+// CTAs per SM: all its threads.
+template <int G>
+constexpr int kPackCtas = 2048 / (4 * G);
 
 }  // namespace kvq

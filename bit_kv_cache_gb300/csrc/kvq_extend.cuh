@@ -259,7 +259,7 @@ __device__ __forceinline__ void extend_slot(const ExtendParams &p, int b, int h,
     const int4 *d = reinterpret_cast<const int4 *>(p.desc);
     const int4 x = d[2 * b], y = d[2 * b + 1];
     if (!x.w) return;
-    keep_rows(p, x, y, b, h, side, true, !(p.once && y.z), z * 256 + threadIdx.x, nz * 256);
+    keep_rows(p, x, y, b, h, side, true, !(p.once && y.z), z * blockDim.x + threadIdx.x, nz * blockDim.x);
     if (h == 0 && side == 0 && z == 0 && threadIdx.x == 0)
         reinterpret_cast<int4 *>(p.lens)[b] = make_int4(x.x + y.y, x.y + y.z, x.z + x.w - y.y - y.z, 1);
 }
