@@ -869,9 +869,9 @@ class KVQPagedCache:
         """One step of n_new[b] new tokens per slot: plan, norm and rotation of q and k at
         their positions, attention, and the tokens' entry into the cache.  q: float16
         [n, H_q, D], k, v: float16 [n, H_kv, D], n >= sum(n_new); rows behind that sum are left
-        alone.  rope: a Rope, instead of rope_base, rotary_dim and halves.  Returns (out, chunk), out with sum(n_new) rows if it is not the caller's.  A
-        chunk made here (chunk=None) costs its arrays and a workspace in every call; a loop
-        keeps one."""
+        alone.  rope: a Rope, instead of rope_base, rotary_dim and halves.  Returns (out, chunk),
+        out with sum(n_new) rows if it is not the caller's.  A chunk made here (chunk=None) costs
+        its arrays and a workspace in every call; a loop keeps one."""
         chunk = self.plan(n_new, chunk)
         n = chunk.n_tokens
         if n == 0:

@@ -263,7 +263,7 @@ extern "C" int kvq_paged_append_rope(const kvq_config *c, kvq_paged *pc, const k
     const size_t no = (size_t)B * c->H_q * c->D * 2;
     const bool own = q_out == q && (qk->q_stride == (int64_t)c->H_q * c->D || B == 1);
     if ((!own && overlap(q_out, no, q, span(qk->q_stride, c->H_q))) || overlap(q_out, no, k, span(qk->k_stride, c->H_kv)) ||
-        overlap(q_out, no, v, span(v_stride, c->H_kv)))
+        overlap(q_out, no, v, span(v_stride, c->H_kv)) || (w_q && overlap(q_out, no, w_q, c->D * 2)) || (w_k && overlap(q_out, no, w_k, c->D * 2)))
         return KVQ_ERR_INVALID_ARG;
     if (full && per > kMaxPages) return KVQ_ERR_UNSUPPORTED;
     cudaStream_t st = (cudaStream_t)stream;

@@ -624,6 +624,8 @@ size_t block_decode_ws_bytes(const kvq_config *c) { return 256 + ml_bytes(c) + (
 
 int block_decode(const kvq_config *c, const kvq_paged *pc, const uint16_t *q, uint16_t *out, void *ws, size_t ws_bytes,
                  cudaStream_t st) {
+    const size_t rows = (size_t)c->B * c->H_q * c->D * 2;
+    if (out != q && host::overlap(out, rows, q, rows)) return KVQ_ERR_INVALID_ARG;  // a row's own place: read before it is written
     if (!ws || !host::aligned16(ws) || ws_bytes < block_decode_ws_bytes(c)) return KVQ_ERR_WORKSPACE;
     BlockDecodeParams p;
     fill(c, pc, p);

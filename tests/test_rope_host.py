@@ -104,7 +104,8 @@ def test_append_rope_refusals(kvq):
     assert f.append(pages=[1, 9]) == INVALID and f.append(pages=[-1, 2]) == INVALID
     ok = dict(pages=[1, 2])
     for kw in (dict(q=None), dict(q=0x1000008), dict(k=None), dict(v=None), dict(vs=H_kv * D - 8), dict(vs=H_kv * D + 4), dict(w=0x5000002),
-               dict(out=None), dict(out=0x4000004), dict(out=0x1000000 + 256), dict(out=0x2000000), dict(out=0x3000000 + 512),
+               dict(out=None), dict(out=0x4000004), dict(out=0x1000000 + 256), dict(out=0x2000000), dict(out=0x3000000 + 512), dict(out=0x5000000, w=0x5000010),
+               dict(w=0x4000010),
                dict(amp=float("inf")), dict(freq=[-1.0] * 64), dict(freq=[float("nan")] * 64), dict(freq=[3e9] * 64)):
         assert f.append(**{**ok, **kw}) == INVALID, kw
     for name, bad, code in (("H_q", 8, INVALID), ("H_kv", 4, INVALID), ("D", 64, INVALID), ("rotary_dim", 136, INVALID),
@@ -158,6 +159,7 @@ def test_block_decode_refusals(kvq):
         return L.kvq_paged_decode_attn(ctypes.byref(f.cfg), ctypes.byref(f.p), q, out, ws, n, None)
 
     assert decode(q=None) == INVALID and decode(out=0x2000008) == INVALID and decode(q=0x1000002) == INVALID
+    assert decode(out=0x1000000 + 256) == INVALID and decode(q=0x2000000 + 4 * H_q * D * 2 - 16) == INVALID
     assert decode(ws=None) == -4 and decode(n=size - 1) == -4 and decode(ws=0x3000004) == -4
     f.p.n_pages = 0
     assert decode() == INVALID  # packed tokens, and no page
