@@ -15,7 +15,8 @@
 // (two CTAs of three pieces: 90.8 and 41; six CTAs of two warps: 90 and 56, the longest slots end
 // last; plain loads into registers: 119 and 70).  One slot of 131K tokens takes 47 us, of which joining
 // its 57 parts takes 5.  Long slots first: 128 slots 51 -> 41 us.  More parts than run at once: 46 to
-// 52 us there, as joining costs a launch.  Letting the kernel behind start early: 44 us there.
+// 52 us there, as joining costs a launch.  Letting the kernel behind start early: 44 us there
+// (from the end of the loop on: no change, nor in joining).
 // Rows of a chunk: up to 8 (16, 32) in one (two, four) operand tiles of 8.  8 slots as above with 4
 // tokens and heads each take 89 us; with 8 of them 121, bound by the tensor core's issue at two
 // CTAs per SM (255 registers; 340 to 380 bytes of a thread spilled, of tiles between products).
