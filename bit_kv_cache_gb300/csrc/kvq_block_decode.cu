@@ -19,7 +19,7 @@
 // (from the end of the loop on: no change, nor in joining).
 // Rows of a chunk: up to 8 (16, 32) in one (two, four) operand tiles of 8.  8 slots as above with 4
 // tokens and heads each take 89 us; with 8 of them 121, bound by the tensor core's issue at two
-// CTAs per SM (255 registers; 340 to 380 bytes of a thread spilled, of tiles between products).
+// CTAs per SM (255 registers; 340 to 400 bytes of a thread spilled, of tiles between products).
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
