@@ -90,7 +90,7 @@ __device__ __forceinline__ void weights(State<NT> &st, int n, float (&x)[N][4], 
 #pragma unroll
         for (int s = 1; s < N; s++) top[e] = fmaxf(top[e], fmaxf(x[s][e], x[s][2 + e]));
     }
-    if (__any_sync(0xffffffffu, top[0] > st.m[n][0] + kSlack || top[1] > st.m[n][1] + kSlack)) {
+    if (__any_sync(0xffffffffu, top[0] - st.m[n][0] > kSlack || top[1] - st.m[n][1] > kSlack)) {
 #pragma unroll
         for (int e = 0; e < 2; e++) {
 #pragma unroll
@@ -105,13 +105,15 @@ __device__ __forceinline__ void weights(State<NT> &st, int n, float (&x)[N][4], 
             }
         }
     }
-    const float off[2] = {st.m[n][0] == -INFINITY ? 0.f : kUp - st.m[n][0], st.m[n][1] == -INFINITY ? 0.f : kUp - st.m[n][1]};
+    // differences first, which are exact where it matters: beyond 2^25, where exponents are 4 and more
+    // apart, kUp - m would be rounded to more than fp16 has room for
+    const float ref[2] = {st.m[n][0] == -INFINITY ? 0.f : st.m[n][0], st.m[n][1] == -INFINITY ? 0.f : st.m[n][1]};
     float sum[2] = {0.f, 0.f};
 #pragma unroll
     for (int s = 0; s < N; s++) {
 #pragma unroll
         for (int e = 0; e < 4; e++) {
-            x[s][e] = ex2(x[s][e] + off[e & 1]);
+            x[s][e] = ex2((x[s][e] - ref[e & 1]) + kUp);
             sum[e & 1] += x[s][e];
         }
         b[s][0] = transpose8(pack_half2(x[s][0], x[s][1]));
