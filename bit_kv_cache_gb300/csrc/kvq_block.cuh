@@ -27,6 +27,10 @@ __device__ __forceinline__ void code_pairs(uint32_t w, uint32_t &lo, uint32_t &h
     }
 }
 
+// A page's scale as attention reads it: an infinite one, of a page with an infinite value, is NaN, as
+// int8 codes hold no NaN: keys of one would be infinite scores, of either sign.
+__device__ __forceinline__ float page_scale(float s) { return fmaf(s, 0.f, s); }
+
 // Four fp16 values to codes (the low half of x in the low byte): the fp32 product with inv, rounded
 // to nearest even.
 template <bool E4M3>

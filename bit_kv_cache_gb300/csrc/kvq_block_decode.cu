@@ -367,8 +367,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) block_decode_kernel
             }
             const size_t pg = (size_t)page * p.H_kv + h;
             at = ((pg << p.g_shift) + (tok & ((1 << p.g_shift) - 1))) * 128;
-            sk = p.k_scale[pg].x;
-            sv = p.v_scale[pg].x;
+            sk = page_scale(p.k_scale[pg].x);
+            sv = page_scale(p.v_scale[pg].x);
         }
         auto bring = [&](int i) {  // piece i of these tiles
             const size_t from = __shfl_sync(0xffffffffu, at, i >> 1);

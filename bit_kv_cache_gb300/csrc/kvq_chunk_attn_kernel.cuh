@@ -422,8 +422,8 @@ __device__ __forceinline__ void produce(const ChunkAttnParams &p, unsigned char 
             if (2 * kt + h >= pieces) return nullptr;
             const int64_t page = page_index(p, s.it, ent[h]);
             if (!value && tid == h) {
-                sk = __ldcg(reinterpret_cast<const float *>(p.k_meta) + 4 * page);
-                sv = __ldcg(reinterpret_cast<const float *>(p.v_meta) + 4 * page);
+                sk = page_scale(__ldcg(reinterpret_cast<const float *>(p.k_meta) + 4 * page));
+                sv = page_scale(__ldcg(reinterpret_cast<const float *>(p.v_meta) + 4 * page));
             }
             return codes + ((size_t)page * p.G + ((2 * kt + h) * 64 & (p.G - 1))) * kD;
         };
