@@ -1,13 +1,18 @@
 // kvq_block_decode.cu -- attention of one token per slot over an 8-bit cache with one scale per
 // page and head (kvq_paged_decode_attn), and of a few new tokens per slot (kvq_paged_chunk_attn).
 //
-// For a row (query head of a key head's group, token) and cached token t, with the page's scales
-// s_K and s_V,
-//   y_t = (q . code_t) s_K log2(e) / sqrt(D) + log2(s_V),   w_t = 2^(y_t - m),
-//   O = sum w_t code_t,   l = sum w_t / s_V,   out = O / l:
-// the value scale is part of the exponent, so both products have exact operands (codes in fp16)
-// and only w is rounded to fp16, once.  Sums, m and l are fp32; m follows the running maximum with
-// up to kSlack of lag, which keeps w below fp16's largest value and O unscaled in most steps.
+// For a row (query head of a key head's group, token) and cached token x of tile i, with the page's
+// scales s_K and s_V,
+//   y_x = (q . code_x) s_K log2(e) / sqrt(D),   w_x = 2^(y_x - t_i),   t_i near the tile's largest y,
+//   O = sum_i 2^(t_i - m) s_V sum_x w_x code_x,   l = sum_i 2^(t_i - m) sum_x w_x,   out = O / l:
+// both products have exact operands (codes in fp16) but for w, which is rounded to fp16 once.  A tile's
+// product is counted into the state by an fp32 factor that holds the value scale and the distance of
+// the tile's reference from the state's, so that a weight's bits do not depend on other tiles: beside a
+// token that takes most of the attention (an fp16 sink, a page of zeros, whose scale is 1), and beside
+// pages of other scales, a weight has fp16's 11 bits as long as it is 2^-29 of its tile's largest.
+// (With the scale in the exponent and one reference for all tiles, which cost 1 us less of
+// chunk_verify's 31 and nothing elsewhere, weights of pages of small values fell below fp16's normal
+// numbers: outputs off by up to 20 times what roundings make.)  Sums, m and l are fp32.
 //
 // Bound by memory: 8 slots of 17K to 56K tokens (561 MB) take 87 us, 6.4 TB/s, 0.95 of a plain copy's
 // rate.  Each warp has a ring of its own and works alone until its part ends: no barriers, 192 KB on
@@ -41,7 +46,7 @@ constexpr int kWarps = 4, kThreads = 32 * kWarps;
 constexpr int kStages = 2, kPiece = 8192;                // of a warp's ring: keys or values of a packed tile
 constexpr int kTokens = 64, kTailTokens = 16;            // of an item: packed, fp16
 constexpr int kLeast = 16;                               // items of a part, if the slot has as many
-constexpr float kUp = 6.f, kSlack = 8.f;                 // w <= 2^(kUp + kSlack); small weights stay normal numbers
+constexpr float kUp = 15.f, kLag = 16.f;                 // a tile's weights are 2^kUp at most, their factor 2^kLag
 static_assert(kFewRows == 32, "row tiles of the largest form");
 
 // A warp's state for NT tiles of 8 rows: lane (r, c) = (lane / 4, lane % 4) has rows 2 c, 2 c + 1 of
@@ -49,8 +54,8 @@ static_assert(kFewRows == 32, "row tiles of the largest form");
 // tiles.
 template <int NT>
 struct State {
-    float m[NT][2], l[NT][2];   // l: the lane's own share
-    float o[NT][8][4];
+    float m[NT][2], l[NT][2];   // reference (-inf: none yet), sum in units of 2^m, the lane's own share
+    float o[NT][8][4];          // in the same units
 };
 
 // Query operands: rows of tile n, step i, of a lane.  One tile stays in registers, more in shared
@@ -76,25 +81,26 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
 }
 
 // Scores of 16 N tokens (x[s]: tokens r and r + 8 of group s, rows 2 c, 2 c + 1 of row tile n) to
-// weights, as B operands of the value product.  a, lsv: y = x a + lsv; inv: 1 / s_V.
+// weights 2^(y - t), y = x a, as B operands of the value product; t is kUp below the tile's largest y
+// of a row.  u: 2^(t - m), what the product counts in the state.
 template <int N, int NT>
-__device__ __forceinline__ void weights(State<NT> &st, int n, float (&x)[N][4], float a, float lsv, float inv, uint32_t (*b)[2]) {
+__device__ __forceinline__ void weights(State<NT> &st, int n, float (&x)[N][4], float a, float (&u)[2], uint32_t (*b)[2]) {
 #pragma unroll
     for (int s = 0; s < N; s++)
 #pragma unroll
-        for (int e = 0; e < 4; e++) x[s][e] = fmaf(x[s][e], a, lsv);
+        for (int e = 0; e < 4; e++) x[s][e] = __fmul_rn(x[s][e], a);  // (not joined with the difference to t, which has its rounding)
     float top[2];
 #pragma unroll
     for (int e = 0; e < 2; e++) {
         top[e] = fmaxf(x[0][e], x[0][2 + e]);
 #pragma unroll
         for (int s = 1; s < N; s++) top[e] = fmaxf(top[e], fmaxf(x[s][e], x[s][2 + e]));
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], o));
     }
-    if (__any_sync(0xffffffffu, top[0] - st.m[n][0] > kSlack || top[1] - st.m[n][1] > kSlack)) {
+    if (__any_sync(0xffffffffu, top[0] - st.m[n][0] > kLag || top[1] - st.m[n][1] > kLag)) {
 #pragma unroll
         for (int e = 0; e < 2; e++) {
-#pragma unroll
-            for (int o = 4; o < 32; o <<= 1) top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], o));
             const float m = fmaxf(st.m[n][e], top[e]), f = m == st.m[n][e] ? 1.f : ex2(st.m[n][e] - m);
             st.m[n][e] = m;
             st.l[n][e] *= f;
@@ -105,22 +111,38 @@ __device__ __forceinline__ void weights(State<NT> &st, int n, float (&x)[N][4], 
             }
         }
     }
-    // differences first, which are exact where it matters: beyond 2^25, where exponents are 4 and more
-    // apart, kUp - m would be rounded to more than fp16 has room for
-    const float ref[2] = {st.m[n][0] == -INFINITY ? 0.f : st.m[n][0], st.m[n][1] == -INFINITY ? 0.f : st.m[n][1]};
-    float sum[2] = {0.f, 0.f};
 #pragma unroll
-    for (int s = 0; s < N; s++) {
-#pragma unroll
-        for (int e = 0; e < 4; e++) {
-            x[s][e] = ex2((x[s][e] - ref[e & 1]) + kUp);
-            sum[e & 1] += x[s][e];
-        }
-        b[s][0] = transpose8(pack_half2(x[s][0], x[s][1]));
-        b[s][1] = transpose8(pack_half2(x[s][2], x[s][3]));
+    for (int e = 0; e < 2; e++) {
+        // t itself beyond 2^22, where exponents are 0.5 and more apart and kUp less would be rounded
+        if (fabsf(top[e]) < 0x1p22f) top[e] -= kUp;
+        u[e] = top[e] == -INFINITY ? 0.f : ex2(top[e] - st.m[n][e]);
+        if (top[e] == -INFINITY) top[e] = 0.f;
     }
-    st.l[n][0] = fmaf(sum[0], inv, st.l[n][0]);
-    st.l[n][1] = fmaf(sum[1], inv, st.l[n][1]);
+    const uint64_t less = pk2(-top[0], -top[1]);
+    uint64_t sum = 0;
+#pragma unroll
+    for (int s = 0; s < N; s++)
+#pragma unroll
+        for (int e = 0; e < 2; e++) {
+            float2 w = up2(add_x2(pk2(x[s][2 * e], x[s][2 * e + 1]), less));
+            w.x = ex2(w.x);
+            w.y = ex2(w.y);
+            sum = add_x2(sum, pk2(w.x, w.y));
+            b[s][e] = transpose8(pack_half2(w.x, w.y));
+        }
+    const float2 add = up2(sum);
+    st.l[n][0] = fmaf(add.x, u[0], st.l[n][0]);
+    st.l[n][1] = fmaf(add.y, u[1], st.l[n][1]);
+}
+
+// o += p u, of rows 2 c and 2 c + 1 for two channels.
+__device__ __forceinline__ void count(float (&o)[4], const float (&p)[4], uint64_t u) {
+#pragma unroll
+    for (int e = 0; e < 4; e += 2) {
+        const float2 y = up2(fma_x2(pk2(p[e], p[e + 1]), u, pk2(o[e], o[e + 1])));
+        o[e] = y.x;
+        o[e + 1] = y.y;
+    }
 }
 
 // A packed tile.  The order of the contracted dimension is free as long as both operands share
@@ -158,20 +180,27 @@ __device__ __forceinline__ void key_tile(const Queries<NT> &q, const uint8_t *k,
     }
 }
 template <bool E4M3, int NT>
-__device__ __forceinline__ void value_tile(State<NT> &st, const uint8_t *v, const uint32_t (&b)[NT][4][2], int lane) {
+__device__ __forceinline__ void value_tile(State<NT> &st, const uint8_t *v, const uint32_t (&b)[NT][4][2], const float (&u)[NT][2], float scale, int lane) {
     const int r = lane >> 2, c = lane & 3;
 #pragma unroll
     for (int i = 0; i < 8; i++) {
         const uint4 lo = *reinterpret_cast<const uint4 *>(v + out_channel(i, r, 0) * 64 + c * 16);
         const uint4 hi = *reinterpret_cast<const uint4 *>(v + out_channel(i, r, 1) * 64 + c * 16);
+        float o[NT][4];
+#pragma unroll
+        for (int n = 0; n < NT; n++)
+#pragma unroll
+            for (int e = 0; e < 4; e++) o[n][e] = 0.f;
 #pragma unroll
         for (int s = 0; s < 4; s++) {
             uint32_t a[4];
             code_pairs<E4M3>((&lo.x)[s], a[0], a[2]);
             code_pairs<E4M3>((&hi.x)[s], a[1], a[3]);
 #pragma unroll
-            for (int n = 0; n < NT; n++) mma_16816(st.o[n][i], a[0], a[1], a[2], a[3], b[n][s][0], b[n][s][1]);
+            for (int n = 0; n < NT; n++) mma_16816(o[n], a[0], a[1], a[2], a[3], b[n][s][0], b[n][s][1]);
         }
+#pragma unroll
+        for (int n = 0; n < NT; n++) count(st.o[n][i], o[n], pk2(u[n][0] * scale, u[n][1] * scale));
     }
 }
 
@@ -213,6 +242,7 @@ __device__ __forceinline__ bool tail_tile(State<NT> &st, const Queries<NT> &q, c
     };
     if (NT < 4) load_values();  // before the first use of the keys, if there are registers for both
     uint32_t b[NT][1][2];
+    float u[NT][2];
 #pragma unroll
     for (int n = 0; n < NT; n++) {
         float x[1][4] = {{0.f, 0.f, 0.f, 0.f}};
@@ -227,7 +257,7 @@ __device__ __forceinline__ bool tail_tile(State<NT> &st, const Queries<NT> &q, c
             if (x0 + r >= lim[n][e]) x[0][e] = -INFINITY;
             if (x0 + r + 8 >= lim[n][e]) x[0][2 + e] = -INFINITY;
         }
-        weights<1, NT>(st, n, x, kScale, 0.f, 1.f, b[n]);
+        weights<1, NT>(st, n, x, kScale, u[n], b[n]);
     }
     if (NT == 4) load_values();
     bool odd = false;
@@ -239,8 +269,11 @@ __device__ __forceinline__ bool tail_tile(State<NT> &st, const Queries<NT> &q, c
                                transpose8(v[j][0].z), transpose8(v[j][0].w), transpose8(v[j][1].z), transpose8(v[j][1].w)};
 #pragma unroll
         for (int n = 0; n < NT; n++) {
-            mma_16816(st.o[n][2 * j], a[0], a[1], a[2], a[3], b[n][0][0], b[n][0][1]);
-            mma_16816(st.o[n][2 * j + 1], a[4], a[5], a[6], a[7], b[n][0][0], b[n][0][1]);
+            float o[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+            mma_16816(o[0], a[0], a[1], a[2], a[3], b[n][0][0], b[n][0][1]);
+            mma_16816(o[1], a[4], a[5], a[6], a[7], b[n][0][0], b[n][0][1]);
+            count(st.o[n][2 * j], o[0], pk2(u[n][0], u[n][1]));
+            count(st.o[n][2 * j + 1], o[1], pk2(u[n][0], u[n][1]));
         }
     }
     return odd;
@@ -394,17 +427,18 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) block_decode_kernel
         }
         for (int t = 0; t < m; t++) {
             uint32_t bp[NT][4][2];
+            float u[NT][2];
             const int i = 2 * t, k = 2 * t0 + i;  // pieces: of these tiles, of all
             warp_await(&full[k % kStages], (k / kStages) & 1, &bar->stop, p.status);
-            const float tk = kScale * __shfl_sync(0xffffffffu, sk, t), tv = __shfl_sync(0xffffffffu, sv, t), lsv = log2f(tv), inv = 1.f / tv;
+            const float tk = kScale * __shfl_sync(0xffffffffu, sk, t), tv = __shfl_sync(0xffffffffu, sv, t);
             float x[NT][4][4];
             key_tile<E4M3, NT>(q, ring + k % kStages * kPiece, x, lane);
             __syncwarp();
             if (i + kStages < 2 * m) bring(i + kStages);
 #pragma unroll
-            for (int y = 0; y < NT; y++) weights<4, NT>(st, y, x[y], tk, lsv, inv, bp[y]);
+            for (int y = 0; y < NT; y++) weights<4, NT>(st, y, x[y], tk, u[y], bp[y]);
             warp_await(&full[(k + 1) % kStages], ((k + 1) / kStages) & 1, &bar->stop, p.status);
-            value_tile<E4M3, NT>(st, ring + (k + 1) % kStages * kPiece, bp, lane);
+            value_tile<E4M3, NT>(st, ring + (k + 1) % kStages * kPiece, bp, u, tv, lane);
             __syncwarp();
             if (i + 1 + kStages < 2 * m) bring(i + 1 + kStages);
         }

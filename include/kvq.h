@@ -447,9 +447,10 @@ size_t kvq_paged_workspace_bytes(const kvq_config *cfg);
 /* Decode attention, as kvq_decode_attn, for every active sequence over its own
  * length: q, out device fp16 [B][H_q][D]; rows of empty slots are not written.
  * KVQ_MODE_E4M3, KVQ_MODE_INT8: out may be q, but may not overlap it in another way
- * (KVQ_ERR_INVALID_ARG); codes are exact fp16 operands, the scales enter the softmax;
- * only its weights (fp16) and the output are rounded, sums are fp32: an output is off by 2.3e-4
- * to 2.9e-4 of its size, of which 2e-4 is its own rounding.  Infinite and NaN values of fp16
+ * (KVQ_ERR_INVALID_ARG); codes are exact fp16 operands, scales and sums are fp32;
+ * only the softmax's weights (fp16, each beside the largest one of its 64 tokens) and the output
+ * are rounded: an output of values of either sign is off by 2.3e-4 to 2.9e-4 of its size, of which
+ * 2e-4 is its own rounding, whatever the pages' scales and beside sink tokens of any weight.  Infinite and NaN values of fp16
  * tokens reach the output as they are.  The call may be captured: a replay attends over the
  * lengths that the cache then has, for the slots that held tokens at the capture. */
 int kvq_paged_decode_attn(const kvq_config *cfg, const kvq_paged *pc, const uint16_t *q,
