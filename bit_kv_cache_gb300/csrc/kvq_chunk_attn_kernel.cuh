@@ -57,12 +57,13 @@
 // 8-bit codes with a scale per page: the operands are the codes, which fp16 holds exactly, and the
 // scales of a tile's halves (a page has 64 tokens at least) go into the softmax,
 //   w_t = 2^(s_t s_K kScale + log2(s_V) + kUp - r),   out = sum w_t code_t / sum (w_t / s_V),
-// with a reference r that counts log2(s_V) in.  So a block of small values keeps its weights, and
-// only the weights and the output are rounded.  Their tiles are made from registers that the
-// producers load a tile ahead, with 56 registers a thread instead of 48: a packed tile has 16 KB, and
-// shared memory has room for one a side.  1025 tokens of 32 heads over 49252 cached ones (836 GFLOP):
-// 620 to 660 us, 1.26 to 1.35 PFLOP/s (849 with whole packed tiles through that one slot, 702 with
-// slots for each half).
+// with a reference r that counts log2(s_V) in: of the block whose scores gave it, or of one of smaller
+// values behind.  So a weight has fp16's 11 bits, beside blocks of any scale, as long as it is 2^-18 of
+// the row's largest (both without the scales), and only the weights and the output are rounded.  Their
+// tiles are made from registers that the producers load a tile ahead, with 56 registers a thread
+// instead of 48: a packed tile has 16 KB, and shared memory has room for one a side.  1025 tokens of 32
+// heads over 49252 cached ones (836 GFLOP): 620 to 660 us, 1.26 to 1.35 PFLOP/s (849 with whole packed
+// tiles through that one slot, 702 with slots for each half).
 #pragma once
 
 #include <cuda_fp16.h>
@@ -96,6 +97,10 @@ constexpr int kOffQ = 0, kOffK = 2 * kTileBytes, kOffV = kOffK + kRing * kTileBy
 constexpr float kUp = 6.f, kMostSum = 16384.f, kNear = 4096.f;
 // With scales the reference is an exponent: near is 512, where it is off by 2^-15 as well.
 constexpr float kNearExp = 512.f;
+// It goes down with the values' scale, if that is lower by more than kScaleDrop bits, as a pass over O
+// is what a moved reference costs.  (What is compared in every step is that bound: formed there from
+// the scale that the reference counts in, the chunk of 1025 tokens above took 664 us against 637.)
+constexpr float kScaleDrop = 2.f;
 enum { kMinMax = 0, kE4m3 = 1, kInt8 = 2 };
 constexpr int kScaleRing = 8;  // tiles whose scales are held; producers are at most five tiles ahead of a softmax group
 // registers of a thread after the split; 64 at launch, times 1024 threads
@@ -644,15 +649,32 @@ struct RowState {
     uint32_t ns, given, no1;  // per buffer h: parity of the weights given, any given; narrow units joined
     float r, l;               // reference (-inf: none yet), sum of the weights
 };
-// Whether weights of this sum, formed with a near reference, stand; the reference that weights
-// are formed with in any case.
+// Whether weights of this sum, formed with a near reference, stand.  low: kScaleDrop below the
+// log2 s_V that the reference counts in.
 template <int FMT>
-__device__ __forceinline__ bool stands(float sum, float r) { return sum <= kMostSum && fabsf(r) <= (FMT ? kNearExp : kNear); }
+__device__ __forceinline__ bool stands(float sum, float r, float low, const float4 &sc) {
+    return sum <= kMostSum && fabsf(r) <= (FMT ? kNearExp : kNear) && !(FMT && sc.y < low);
+}
 // The factor between references, and the reference of a largest score.
 template <int FMT>
 __device__ __forceinline__ float lower(float from, float to) { return ex2(FMT ? from - to : (from - to) * kScale); }
 template <int FMT>
 __device__ __forceinline__ float ref_of(float score, const float4 &sc) { return FMT ? __fmaf_rn(score, sc.x, sc.y) : score; }
+// The reference for a step of this largest score: a larger one, and where the scale is below `low` one
+// for blocks of smaller values.  Returns the factor of what has been summed.
+template <int FMT>
+__device__ __forceinline__ float move_ref(float &r, float &low, float score, const float4 &sc) {
+    float to = ref_of<FMT>(score, sc);
+    if (!(to > r || (FMT && sc.y < low))) return 1.f;
+    if (FMT) {
+        to = fmaxf(to, (r - low) + (sc.y - kScaleDrop));
+        low = sc.y - kScaleDrop;
+        if (to == r) return 1.f;  // (-inf)
+    }
+    const float f = lower<FMT>(r, to);
+    r = to;
+    return f;
+}
 // Scales of half h of packed key tile number n; fp16 tokens have none.
 template <int FMT>
 __device__ __forceinline__ float4 scales_of(const Bars *bar, bool packed, int n, int h) {
@@ -686,7 +708,7 @@ template <int FMT, bool NARROW>
 __device__ __forceinline__ void softmax_steps(const ChunkAttnParams &p, Bars *bar, const Seg &s, RowState &st, uint32_t ts, uint32_t to,
                                               int m, int lim, bool any, int n) {
     const int steps = NARROW ? 2 * ((s.k1 - s.k0 - m + 1) >> 1) : s.steps;
-    float r = -INFINITY, l = 0.f;
+    float r = -INFINITY, low = -kScaleDrop, l = 0.f;
     for (int i = 0; i < steps; i++) {
         const int h = i & 1, kt = s.k0 + (NARROW ? 2 * (i >> 1) + m : i >> 1);
         warp_await(&bar->s_full[m][h], (st.ns >> h) & 1, &bar->stop, p.status);
@@ -697,12 +719,9 @@ __device__ __forceinline__ void softmax_steps(const ChunkAttnParams &p, Bars *ba
             uint32_t x[64];
             load_scores<64>(x, ts + 64 * h, y);
             float add = weights<FMT, 64, false>(x, r, sc);  // infinite or NaN without a reference
-            if (__any_sync(0xffffffffu, !stands<FMT>(add, r))) {
+            if (__any_sync(0xffffffffu, !stands<FMT>(add, r, low, sc))) {
                 load_scores<64>(x, ts + 64 * h, y);
-                const float cand = ref_of<FMT>(max_of<64>(reinterpret_cast<const float *>(x)), sc);
-                const bool grow = cand > r;
-                const float corr = grow ? lower<FMT>(r, cand) : 1.f;
-                if (grow) r = cand;
+                const float corr = move_ref<FMT>(r, low, max_of<64>(reinterpret_cast<const float *>(x)), sc);
                 l *= corr;
                 if (i > 0) {
                     // the step before was the last to write O
@@ -742,7 +761,7 @@ template <int FMT, int REP>
 __device__ __forceinline__ void softmax_tiles(const ChunkAttnParams &p, Bars *bar, const Seg &s, RowState &st, uint32_t ts, uint32_t to,
                                               int m, int lim, int c, int n) {
     constexpr int KEYS = 128 / REP;
-    float r = -INFINITY, l = 0.f;
+    float r = -INFINITY, low = -kScaleDrop, l = 0.f;
     for (int kt = s.k0 + m; kt < s.k1; kt += 2) {
         warp_await(&bar->s_full[m][0], st.ns & 1, &bar->stop, p.status);
         warp_await(&bar->s_full[m][1], (st.ns >> 1) & 1, &bar->stop, p.status);
@@ -752,12 +771,9 @@ __device__ __forceinline__ void softmax_tiles(const ChunkAttnParams &p, Bars *ba
         uint32_t x[KEYS];
         load_scores<KEYS>(x, ts + KEYS * c, y);
         float add = weights<FMT, KEYS, false>(x, r, sc);  // infinite or NaN without a reference
-        if (__any_sync(0xffffffffu, !stands<FMT>(add, r))) {
+        if (__any_sync(0xffffffffu, !stands<FMT>(add, r, low, sc))) {
             load_scores<KEYS>(x, ts + KEYS * c, y);
-            const float cand = ref_of<FMT>(max_of<KEYS>(reinterpret_cast<const float *>(x)), sc);
-            const bool grow = cand > r;
-            const float corr = grow ? lower<FMT>(r, cand) : 1.f;
-            if (grow) r = cand;
+            const float corr = move_ref<FMT>(r, low, max_of<KEYS>(reinterpret_cast<const float *>(x)), sc);
             l *= corr;
             if (kt > s.k0 + m) {  // the products before these scores have ended
 #pragma unroll 1

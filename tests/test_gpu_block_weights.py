@@ -115,7 +115,7 @@ def test_decode_beside_a_page_of_zeros(size, mode):
 
 
 @pytest.mark.parametrize("mode", MODES)
-@pytest.mark.parametrize("new", [[3, 1], [8, 5]], ids=str)
+@pytest.mark.parametrize("new", [[3, 1], [8, 5], [80, 20], [10, 30]], ids=str)
 @pytest.mark.parametrize("size", SIZES)
 def test_chunk_beside_a_page_of_zeros(size, new, mode):
     rng = np.random.default_rng(24)
