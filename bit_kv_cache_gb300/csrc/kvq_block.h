@@ -29,11 +29,16 @@ struct BlockListParams : PackParams {
 // Attention of at most kFewRows rows (new tokens times query heads) per key head of a slot.  A CTA
 // is (key head, part of a slot): the slot's items, packed tiles of 64 tokens and then 16-token tiles
 // of the fp16 tokens [sink | residual | new ones], are cut into equal parts.  8 slots of 17K to 56K
-// tokens with 32 rows each take 121 us, with 36 rows, which go to the tensor-memory kernel, 175.
-// Beside slots of more rows it runs as a launch of its own, if it has kFewTiles tiles of 128 tokens
-// and heads at least: two slots with 5600 of them beside a 517-token chunk 106 us against 112, one
-// with 2290 95 against 86.
-constexpr int kFewRows = 32, kFewTiles = 4096;
+// tokens with 32 rows each take 126 us, with 36 rows, which go to the tensor-memory kernel, 188.
+// Beside slots of more rows it runs as a launch of its own from a number of tiles, of 128 tokens and
+// heads, on.  Us, with a launch of its own against one kernel for all, beside a slot of 40, of 517 and
+// of 2000 new tokens (4 heads a key head):
+//   slots of 4 rows:  2288 tiles (517 new tokens) 88 and 87; 5584 tiles 75 and 74, 107 and 114, 504 and
+//                     500; 6632 tiles 78 and 86, 112 and 126, 236 and 261; 15984 tiles 122 and 170, 158
+//                     and 215, 283 and 357 (16 rows: 4056 tiles, 517 tokens 101 and 89, else the same);
+//   slots of 32 rows: 6632 tiles 97 and 88, 131 and 130, 256 and 268; 8688 tiles 108 and 110, 140 and
+//                     154, 266 and 296; 15984 tiles 154 and 179, 186 and 224, 312 and 364.
+constexpr int kFewRows = 32, kFewTiles = 5120, kFewTiles32 = 8192;  // kFewTiles32: of more than 16 rows
 struct BlockDecodeParams {
     const uint16_t *q, *k_new, *v_new;   // new rows of a chunk (decode: none, the cache holds the token)
     int64_t q_stride, k_stride, v_stride;

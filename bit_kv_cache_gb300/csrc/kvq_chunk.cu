@@ -606,15 +606,18 @@ int kvq_paged_chunk_attn(const kvq_config *c, const kvq_paged *pc, kvq_chunk *ch
     const ChunkSlot *slots = slots_of(ch);
     if (block8(c)) {
         int64_t tiles = 0;
+        int most = 0;  // rows of such a slot
         for (int b = 0; b < c->B; b++) {
             const ChunkSlot &s = slots[b];
             if (s.n_new && s.T && pc->n_pages < 1) return KVQ_ERR_INVALID_ARG;
             few[b] = s.n_new && (int64_t)s.n_new * p.g <= kFewRows;
             any_few |= few[b];
             all_few &= few[b] || !s.n_new;
-            if (few[b]) tiles += (int64_t)p.H_kv * (s.T / kChunkKeys);
+            if (!few[b]) continue;
+            tiles += (int64_t)p.H_kv * (s.T / kChunkKeys);
+            most = std::max(most, s.n_new * p.g);
         }
-        any_few &= all_few || tiles >= kFewTiles;
+        any_few &= all_few || tiles >= (most > 16 ? kFewTiles32 : kFewTiles);
         for (int b = 0; any_few && b < c->B; b++) {
             rest[b] = slots[b];
             if (few[b]) rest[b].n_new = 0;
