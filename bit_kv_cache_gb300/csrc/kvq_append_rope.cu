@@ -8,8 +8,9 @@
 // pair in one thread, so that a row needs one reduction and no exchange; sines and cosines are
 // formed once per CTA, while the rows arrive.  Positions and destinations come as a parameter, from
 // the host's lengths: no CTA reads the lengths that another one advances.
-// What bounds it.  Few slots: the host call (8 slots: 9.6 us through the binding, 4.6 of them in the
-// C call; the kernel takes 4.4).  256 slots whose residuals are all full (208 MB): 43 us, 4.8 TB/s;
+// What bounds it.  Few slots: the host call (8 slots: 11.6 us through the binding, 5.3 of them in the
+// C call; the kernel takes 4).  256 slots whose residuals are all full (208 MB): 43 us, 4.8 TB/s (in
+// another loop 44, and 53 over min-max codes of 4 bits);
 // the CTAs of the pages spend most of their time in the latency of their loads (kvq_block.cuh).
 #include <cuda_runtime.h>
 #include <stdint.h>

@@ -59,6 +59,9 @@ __global__ void __launch_bounds__(4 * G, kPackCtas<G>) block_extend_kernel(const
     }
 }
 
+// Pages of listed slots.  A prefill of 12345 tokens of 8 heads (76 MB), with the copies of its last
+// rows, takes 26 us (e4m3; int8 27, min-max codes of 4 bits 36); a flush of 256 full residuals (201 MB),
+// with setting the lengths back, 38 (39, 53).
 template <bool E4M3, int G>
 __global__ void __launch_bounds__(4 * G, kPackCtas<G>) block_list_kernel(const __grid_constant__ BlockListParams p) {
     const int h = blockIdx.y, side = blockIdx.z, k = blockIdx.x / p.per, j = blockIdx.x - k * p.per, b = p.seq[k];

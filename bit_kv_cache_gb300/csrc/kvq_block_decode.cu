@@ -14,17 +14,17 @@
 // chunk_verify's 31 and nothing elsewhere, weights of pages of small values fell below fp16's normal
 // numbers: outputs off by up to 20 times what roundings make.)  Sums, m and l are fp32.
 //
-// Bound by memory: 8 slots of 17K to 56K tokens (561 MB) take 87 us, 6.4 TB/s, 0.95 of a plain copy's
+// Bound by memory: 8 slots of 17K to 56K tokens (561 MB) take 88 us, 6.4 TB/s, 0.94 of a plain copy's
 // rate.  Each warp has a ring of its own and works alone until its part ends: no barriers, 192 KB on
-// their way per SM.  Three CTAs of two 8 KB pieces a warp: 87.5 us, 128 slots of 8 to 4001 tokens 39
+// their way per SM.  Three CTAs of two 8 KB pieces a warp: 88 us, 128 slots of 8 to 4001 tokens 40
 // (two CTAs of three pieces: 90.8 and 41; six CTAs of two warps: 90 and 56, the longest slots end
 // last; plain loads into registers: 119 and 70).  One slot of 131K tokens takes 47 us, of which joining
 // its 57 parts takes 5.  Long slots first: 128 slots 51 -> 41 us.  More parts than run at once: 46 to
 // 52 us there, as joining costs a launch.  Letting the kernel behind start early: 44 us there
 // (from the end of the loop on: no change, nor in joining).
 // Rows of a chunk: up to 8 (16, 32) in one (two, four) operand tiles of 8.  8 slots as above with 4
-// tokens and heads each take 89 us; with 8 of them 121, bound by the tensor core's issue at two
-// CTAs per SM (255 registers; 340 to 400 bytes of a thread spilled, of tiles between products).
+// tokens and heads each take 90 us; with 8 tokens 126 (int8 132), bound by the tensor core's issue at
+// two CTAs per SM (255 registers; 520 to 640 bytes of a thread spilled, of tiles between products).
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>

@@ -528,8 +528,8 @@ size_t kvq_paged_chunk_workspace_bytes(const kvq_config *cfg);
  * tokens: 71 us against 139).  KVQ_MODE_E4M3, KVQ_MODE_INT8: codes are exact operands, as in
  * kvq_paged_decode_attn, and an output of values of either sign is off by 2.4e-4 to 2.9e-4 of its
  * size, whatever the pages' scales (slots of more than 32 rows, new tokens times query heads of a
- * key head: as long as it does not rest on tokens of less than 2^-18 of the row's largest weight,
- * where a weight loses bits).
+ * key head, and slots of fewer in one call with such: as long as it does not rest on tokens of less
+ * than 2^-18 of the row's largest weight, where a weight loses bits).
  * Infinite and NaN values reach the rows that see them and no others.  A packed key or value
  * that rounds beyond fp16's largest when dequantized counts as one of them: the rows of its
  * slot become infinite or NaN.  A page-table entry that is no page is reported
