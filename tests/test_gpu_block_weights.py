@@ -144,3 +144,26 @@ def test_a_block_of_small_values_that_counts(new, mode):
         p, ref, mag = rows_of(q[b].cpu().double().numpy(), K[0], V[0])
         assert p[:, 130].min() > 0.99 and np.median(np.abs(ref) / worst(p, V[0], ref, mag)) > 100
     (decode_errors(c, q) if new is None else chunk_errors(c, rng, new, q, 1.0)).check()
+
+
+@pytest.mark.parametrize("mode", MODES)
+@pytest.mark.parametrize("new", [None, [7, 2], [70, 25], [1, 200]], ids=str)
+@pytest.mark.parametrize("seed", range(3))
+def test_pages_of_any_sizes(seed, new, mode):
+    """Every page with sizes of its own, keys by 16 times, values from 1e-4 to 300, some pages of
+    zeros, and sink tokens of any weight and size."""
+    rng = np.random.default_rng(100 + seed)
+    G, S = ((64, 3), (128, 0), (256, 20))[seed]
+    q, keys = aimed(rng, 2, 2, 4, 5.0)
+    c = make_cache(rng, [0, 0], mode, G=G, S=S)
+    for b, n in enumerate((S + 2500, S + 7 * G + 13)):
+        k, v = randn(rng, 2, n, D), randn(rng, 2, n, D)
+        for t in range(0, n, G):
+            k[:, S + t: S + t + G] *= float(2.0 ** rng.uniform(-3, 1))
+            v[:, S + t: S + t + G] *= float(rng.choice([0.0, 10.0 ** rng.uniform(-4, 2.5)], p=[0.15, 0.85]))
+        if S:
+            k[:, 1] = keys[b]
+            v[:, :S] *= float(10.0 ** rng.uniform(-4, 1))
+        k[:, S + 2 * G + 5] = keys[b]
+        c.prefill(b, k, v)
+    (decode_errors(c, q) if new is None else chunk_errors(c, rng, new, q, float(10.0 ** rng.uniform(-4, 1)))).check()
