@@ -653,8 +653,9 @@ class KVQPagedCache:
         q: float16 [B, H_q, D], k, v: float16 [B, H_kv, D], row b for slot b; rows may be strided
         (views of a fused projection), those of empty slots are ignored.  rope: a Rope; by
         default all channels, interleaved, base 10000.  pages: ids of physical pages that the
-        caller hands out to the full residuals (host integers, or an int32 CPU tensor), here and
-        in every later call that needs pages, until clear(); by default they come from the
+        caller hands out to the full residuals (host integers, or an int32 CPU tensor; pages that
+        no slot holds, each once), here and in every later call that needs pages, until clear(); by
+        default they come from the
         cache's own free list.  Returns the queries for decode_attn, out if it is given
         (contiguous [B, H_q, D]; it may be q)."""
         dev = self._dev

@@ -46,7 +46,7 @@ constexpr int kWarps = 4, kThreads = 32 * kWarps;
 constexpr int kStages = 2, kPiece = 8192;                // of a warp's ring: keys or values of a packed tile
 constexpr int kTokens = 64, kTailTokens = 16;            // of an item: packed, fp16
 constexpr int kLeast = 16;                               // items of a part, if the slot has as many
-constexpr float kUp = 15.f, kLag = 16.f;                 // a tile's weights are 2^kUp at most, their factor 2^kLag
+constexpr float kUp = 15.f, kLag = 16.f;                 // log2: a tile's largest weight; the state's reference lags by so much at most
 static_assert(kFewRows == 32, "row tiles of the largest form");
 
 // A warp's state for NT tiles of 8 rows: lane (r, c) = (lane / 4, lane % 4) has rows 2 c, 2 c + 1 of

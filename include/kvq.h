@@ -598,7 +598,8 @@ int kvq_qk_norm_rope_freq(const kvq_qk_config *c, const double *freq, float amp,
  * for bit, in this order.
  *   - Residuals that are full (kvq_paged_flush_plan) are packed into their next R/G pages.  If
  *     new_pages (host int32 [n_new_pages], read before the call returns) is given, the page table
- *     gets its ids, slot after slot in ascending order; if it is NULL the caller has mapped them.
+ *     gets its ids, slot after slot in ascending order (pages that no slot holds, each once,
+ *     which is not checked); if it is NULL the caller has mapped them.
  *   - Row b of q, k and v (device fp16 rows of H_q, H_kv and H_kv heads; strides qk->q_stride,
  *     qk->k_stride and v_stride in elements, as in a chunk) is slot b's new token.  Its query and
  *     key are normalized and rotated at its position (qk, freq, amp, w_q, w_k as in
